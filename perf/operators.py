@@ -79,8 +79,8 @@ def draw(rng):
     B = rng.choice([16, 32])
     dt = rng.choice(["bf16", "fp16"])
     if op == "prompt":
-        hi = _log(rng, 2, 8192)
-        S = _log(rng, 1, max(1, min(64, 25 * 10 ** 8 // (G * Hk * hi * hi))))
+        hi = _log(rng, 2, min(8192, math.isqrt(25 * 10 ** 8 // (G * Hk))))
+        S = _log(rng, 1, min(64, 25 * 10 ** 8 // (G * Hk * hi * hi)))
         return dict(op=op, S=S, H=G * Hk, Hk=Hk, D=D, lo=_log(rng, 1, hi), hi=hi, dtype=dt,
                     out=rng.choice([dt, dt, "fp32"]))
     if op == "shared":
