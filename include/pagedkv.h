@@ -433,6 +433,79 @@ PKV_API pkv_status paged_attn_multi_query(void* out, pkv_dtype out_dtype, const 
                                           float scale, int max_context_len, void* stream);
 
 /*
+ * paged_attn_decode_weights -- paged_attn_decode that also adds up how much
+ * attention every cached token gets, for an eviction that keeps the heavy
+ * ones (kv_evict):
+ *
+ *     out[s,h,:]    = sum_t p[s,h,t] V_t,   p[s,h,:] = softmax_t(scale q[s,h] . K_t)
+ *     weights[s,t] += sum_h p[s,h,t]        for t < context_lens[s]
+ *
+ *   weights       device float, row s at weights + s * weight_stride (elements),
+ *                 weight_stride >= max_context_len; entries at and behind a
+ *                 sequence's context are neither read nor written.  The caller
+ *                 zeroes an entry before its token's first decode.  The heads of
+ *                 a token are added in order, so results repeat bit for bit.
+ *   workspace     device, >= pkv_decode_weights_workspace_bytes(...) bytes,
+ *                 256-byte aligned; contents on entry are ignored.  Calls that
+ *                 may overlap on the GPU need a workspace each.
+ *   other arguments as paged_attn_decode (the split is automatic).
+ * Supported shapes as paged_attn_decode; at most 65535 sequences, 4096 query
+ * heads.  A token in a block outside the pool is left out (weight 0) and
+ * flagged PKV_DEVERR_BLOCK_ID.  Two launches.
+ */
+PKV_API size_t pkv_decode_weights_workspace_bytes(int num_seqs, int n_heads, int n_kv_heads,
+                                                  int head_dim, int block_size,
+                                                  int max_context_len);
+
+PKV_API pkv_status paged_attn_decode_weights(
+    void* out, pkv_dtype out_dtype, const void* q, const void* k_pool, const void* v_pool,
+    pkv_dtype kv_dtype, const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* context_lens, float* weights, int64_t weight_stride, int num_seqs, int n_heads,
+    int n_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
+    int max_context_len, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * kv_evict -- cut every sequence of more than `keep` tokens to `keep`: its
+ * last `recent` tokens stay and, of the others, the keep - recent with the
+ * largest weights (of equal ones the lower index; NaN counts below every
+ * number).  They stay in their order: token kept[s][j] becomes token j, and
+ * its K and V rows are copied into the pages of new_tables[s].  Sources are
+ * only read, so pages that other sequences share are untouched; the caller
+ * drops the old pages' references once the call is enqueued
+ * (pkv_evict_tables gives new tables and the old ids).
+ *
+ *   k_pool, v_pool device [num_blocks, block_size, n_kv_heads, head_dim] of
+ *                 dtype F16, BF16 or F32, 16-byte aligned, token rows a
+ *                 multiple of 16 bytes; any block_size
+ *   block_tables, context_lens  as paged_attn_decode: before the cut
+ *   weights       device float, row s at weights + s * weight_stride,
+ *                 weight_cols columns (context lengths up to weight_cols)
+ *   new_tables    device int32 [num_seqs, new_blocks_per_seq]; of a sequence
+ *                 that is cut, the first ceil(keep / block_size) entries are
+ *                 read: distinct pages that no sequence of the call reads.
+ *                 Rows of other sequences are not read.
+ *   new_lens      device int32 [num_seqs], written: min(context, keep)
+ *   new_weights   device float, row s at new_weights + s * new_weight_stride,
+ *                 new_weight_cols >= keep columns: the staying tokens' weights,
+ *                 then zeros to the end of the row
+ *   kept          device int32 [num_seqs, keep], written: the staying tokens'
+ *                 indexes (0 .. n - 1 of a sequence of n <= keep tokens), then -1
+ * A sequence of at most `keep` tokens keeps its pages and nothing of it is
+ * copied.  A context below 0 or beyond the table or weight_cols is flagged
+ * PKV_DEVERR_CONTEXT and treated as empty; a row whose source or destination
+ * block lies outside the pool is not copied and flagged PKV_DEVERR_BLOCK_ID.
+ * new_lens, new_weights and kept may not overlap the inputs.  Two launches.
+ */
+PKV_API pkv_status kv_evict(void* k_pool, void* v_pool, pkv_dtype dtype,
+                            const int32_t* block_tables, int max_blocks_per_seq,
+                            const int32_t* context_lens, const float* weights,
+                            int64_t weight_stride, int weight_cols, const int32_t* new_tables,
+                            int new_blocks_per_seq, int32_t* new_lens, float* new_weights,
+                            int64_t new_weight_stride, int new_weight_cols, int32_t* kept,
+                            int num_seqs, int keep, int recent, int n_kv_heads, int head_dim,
+                            int block_size, int num_blocks, void* stream);
+
+/*
  * kv_append -- write one new token per sequence into its page
  * (reshape-and-cache; [LAYOUT] section 三 append_token):
  *
@@ -553,6 +626,28 @@ PKV_API pkv_status pkv_append_slots_cow(pkv_block_manager* mgr, int32_t* block_t
                                         int max_blocks_per_seq, int32_t* context_lens,
                                         int num_seqs, int64_t* slot_mapping,
                                         int64_t* copy_pairs, int* n_copy_pairs);
+
+/*
+ * pkv_evict_tables -- the host bookkeeping of kv_evict: for every sequence
+ * of more than `keep` tokens, ceil(keep / block_size) blocks are allocated
+ * into its row of new_tables and the ids of its old blocks are listed in
+ * old_ids; the row of any other sequence is copied.  Unused entries of
+ * new_tables become -1, and context_lens[s] = min(context_lens[s], keep).
+ * The old blocks stay held: after kv_evict is enqueued the caller frees each
+ * listed id (pkv_block_free), shared ones included (their other holders keep
+ * them).
+ *   block_tables host int32 [num_seqs, max_blocks_per_seq], read
+ *   context_lens host int32 [num_seqs], updated in place
+ *   new_tables   host int32 [num_seqs, new_blocks_per_seq], written
+ *   old_ids      host int32 [cap], written (*n_old ids used)
+ * PKV_ERR_NO_BLOCKS when the pool has too few free blocks for all of them,
+ * PKV_ERR_INVALID for a bad length or table entry, a row that does not fit
+ * new_tables, or cap too small; nothing is changed then (*n_old = 0).
+ */
+PKV_API pkv_status pkv_evict_tables(pkv_block_manager* mgr, const int32_t* block_tables,
+                                    int max_blocks_per_seq, int32_t* context_lens, int num_seqs,
+                                    int keep, int32_t* new_tables, int new_blocks_per_seq,
+                                    int32_t* old_ids, int cap, int* n_old);
 
 /*
  * pkv_defrag -- plan a compaction of the pool ([SWAP]: swap_blocks also

@@ -56,6 +56,12 @@ SIGNATURES = {
                                        _i, _f, _i, _i, _p]),
     "paged_attn_multi_query": (_i, [_p, _i, _p, _p, _i, _i, _p, _p, _i, _p, _i, _p, _i, _i, _i,
                                     _i, _i, _i, _f, _i, _p]),
+    "pkv_decode_weights_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "paged_attn_decode_weights": (_i, [_p, _i, _p, _p, _p, _i, _p, _i, _p, _p, _i64, _i, _i, _i,
+                                       _i, _i, _i, _f, _i, _p, _sz, _p]),
+    "kv_evict": (_i, [_p, _p, _i, _p, _i, _p, _p, _i64, _i, _p, _i, _p, _p, _i64, _i, _p, _i, _i,
+                      _i, _i, _i, _i, _i, _p]),
+    "pkv_evict_tables": (_i, [_p, _p, _i, _p, _i, _i, _p, _i, _p, _i, C.POINTER(_i)]),
     "kv_append": (_i, [_p, _p, _p, _p, _i, _p, _i, _i, _i, _i, _i, _p]),
     "swap_blocks": (_i, [_p, _p, _sz, _p, _i, _i64, _i64, _p]),
     "swap_blocks_kv": (_i, [_p, _p, _p, _p, _sz, _p, _i, _i64, _i64, _p]),

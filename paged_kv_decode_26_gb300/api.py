@@ -63,6 +63,16 @@ def _addr(t: Optional[torch.Tensor]) -> int:
     return t.data_ptr() if t is not None and t.numel() else 0
 
 
+def _stream_buffer(nbytes: int, device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """A call's own workspace, from the allocator's pool of the stream that
+    the call runs on, so that it is not handed out again before that stream
+    is done with it."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+
+
 _DECODE_NAMES = ("out", "q", "k_pool", "v_pool", "block_tables", "context_lens")
 _APPEND_NAMES = _DECODE_NAMES + ("k_new", "v_new", "slot_mapping")
 
@@ -399,6 +409,106 @@ def paged_attn_multi_query(out: torch.Tensor, q: torch.Tensor, q_start: torch.Te
     return out
 
 
+def decode_weights_workspace_bytes(num_seqs: int, n_heads: int, n_kv_heads: int, head_dim: int,
+                                   block_size: int, max_context_len: int) -> int:
+    return int(lib().pkv_decode_weights_workspace_bytes(num_seqs, n_heads, n_kv_heads, head_dim,
+                                                        block_size, max_context_len))
+
+
+def _need_rows(name: str, t: torch.Tensor, dtype: torch.dtype, rows: int) -> int:
+    """Checks a CUDA matrix of `rows` rows whose rows are contiguous; its row
+    stride in elements."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows:
+        raise ValueError(f"{name} must be {dtype} with a row per sequence")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    if rows > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}: rows must not overlap")
+    return t.stride(0) if rows > 1 else t.shape[1]
+
+
+def _need_one_device(tensors) -> None:
+    """The library launches on the current device."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != cur:
+            raise ValueError("tensors must be on the current CUDA device")
+
+
+def paged_attn_decode_weights(out: torch.Tensor, q: torch.Tensor, k_pool: torch.Tensor,
+                              v_pool: torch.Tensor, block_tables: torch.Tensor,
+                              context_lens: torch.Tensor, weights: torch.Tensor, scale: float,
+                              max_context_len: int, workspace: Optional[torch.Tensor] = None,
+                              stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """paged_attn_decode, and weights[s, t] += sum over heads of token t's
+    softmax weight (fp32 [S, >= max_context_len], rows contiguous) -- what
+    kv_evict goes by."""
+    _need_all_cuda(_DECODE_NAMES, (out, q, k_pool, v_pool, block_tables, context_lens))
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise ValueError("block_tables and context_lens must be int32")
+    S, H, D = q.shape
+    nb, B, Hk, D2 = k_pool.shape
+    if (D2 != D or v_pool.shape != k_pool.shape or out.shape != q.shape
+            or q.dtype != k_pool.dtype or v_pool.dtype != k_pool.dtype
+            or block_tables.dim() != 2 or block_tables.shape[0] != S
+            or context_lens.shape != (S,)):
+        raise ValueError("inconsistent shapes or dtypes")
+    w_stride = _need_rows("weights", weights, torch.float32, S)
+    if weights.shape[1] < max_context_len:
+        raise ValueError("weights has fewer columns than max_context_len")
+    _need_one_device((out, q, k_pool, v_pool, block_tables, context_lens, weights, workspace))
+    if workspace is None:
+        n = decode_weights_workspace_bytes(S, H, Hk, D, B, max_context_len)
+        workspace = _stream_buffer(n, q.device, stream)
+    st = lib().paged_attn_decode_weights(
+        _addr(out), _DT[out.dtype], _addr(q), _addr(k_pool), _addr(v_pool), _DT[k_pool.dtype],
+        _addr(block_tables), block_tables.shape[1], _addr(context_lens), _addr(weights), w_stride,
+        S, H, Hk, D, B, nb, float(scale), int(max_context_len), _addr(workspace),
+        workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    check(st, "paged_attn_decode_weights")
+    return out
+
+
+def kv_evict(k_pool: torch.Tensor, v_pool: torch.Tensor, block_tables: torch.Tensor,
+             context_lens: torch.Tensor, weights: torch.Tensor, new_tables: torch.Tensor,
+             new_lens: torch.Tensor, new_weights: torch.Tensor, kept: torch.Tensor, keep: int,
+             recent: int, stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Cut every sequence of more than `keep` tokens to its last `recent` and
+    the keep - recent heaviest earlier ones (the lower index of equal
+    weights), copied in order into the pages of new_tables.  Written: new_lens
+    int32 [S], new_weights fp32 [S, >= keep] (zeros behind the staying
+    tokens), kept int32 [S, keep] (their indexes, then -1).  Free the old
+    pages afterwards (BlockManager.evict_tables gives both)."""
+    for name, t in (("k_pool", k_pool), ("v_pool", v_pool), ("block_tables", block_tables),
+                    ("context_lens", context_lens), ("new_tables", new_tables),
+                    ("new_lens", new_lens), ("kept", kept)):
+        _need_cuda(name, t)
+    S = context_lens.shape[0]
+    for name, t in (("block_tables", block_tables), ("context_lens", context_lens),
+                    ("new_tables", new_tables), ("new_lens", new_lens), ("kept", kept)):
+        if t.dtype != torch.int32:
+            raise ValueError(f"{name} must be int32")
+    nb, B, Hk, D = k_pool.shape
+    if (v_pool.shape != k_pool.shape or v_pool.dtype != k_pool.dtype
+            or context_lens.dim() != 1 or new_lens.shape != (S,)
+            or block_tables.dim() != 2 or block_tables.shape[0] != S
+            or new_tables.dim() != 2 or new_tables.shape[0] != S
+            or tuple(kept.shape) != (S, keep)):
+        raise ValueError("inconsistent shapes or dtypes")
+    w_stride = _need_rows("weights", weights, torch.float32, S)
+    nw_stride = _need_rows("new_weights", new_weights, torch.float32, S)
+    _need_one_device((k_pool, v_pool, block_tables, context_lens, weights, new_tables, new_lens,
+                      new_weights, kept))
+    st = lib().kv_evict(_addr(k_pool), _addr(v_pool), _DT[k_pool.dtype], _addr(block_tables),
+                        block_tables.shape[1], _addr(context_lens), _addr(weights), w_stride,
+                        weights.shape[1], _addr(new_tables), new_tables.shape[1], _addr(new_lens),
+                        _addr(new_weights), nw_stride, new_weights.shape[1], _addr(kept), S,
+                        int(keep), int(recent), Hk, D, B, nb, _stream_handle(stream))
+    check(st, "kv_evict")
+
+
 def kv_append(k_pool: torch.Tensor, v_pool: torch.Tensor, k_new: torch.Tensor,
               v_new: torch.Tensor, slot_mapping: torch.Tensor,
               stream: Optional[torch.cuda.Stream] = None) -> None:
@@ -549,6 +659,33 @@ class BlockManager:
         if st not in (_lib.PKV_OK, _lib.PKV_ERR_NO_BLOCKS):
             check(st, "pkv_append_slots_cow")
         return int(st), pairs[:n.value].clone()
+
+
+def _evict_tables(self, block_tables: torch.Tensor, context_lens: torch.Tensor, keep: int,
+                  new_blocks_per_seq: Optional[int] = None):
+    """Host bookkeeping of kv_evict: allocates the pages of every sequence
+    cut to `keep` tokens and updates the CPU int32 context_lens in place.
+    Returns (new_tables int32 [S, new_blocks_per_seq], old_ids int32 [n]);
+    new_blocks_per_seq defaults to the tables' width.  Free each old id
+    (free()) once kv_evict is enqueued.  Raises without changing anything if
+    the pool has too few free blocks."""
+    for t in (block_tables, context_lens):
+        if t.device.type != "cpu" or not t.is_contiguous() or t.dtype != torch.int32:
+            raise ValueError("evict_tables takes contiguous CPU int32 tensors")
+    S = context_lens.shape[0]
+    if block_tables.dim() != 2 or context_lens.dim() != 1 or block_tables.shape[0] != S:
+        raise ValueError("inconsistent shapes")
+    width = block_tables.shape[1] if new_blocks_per_seq is None else int(new_blocks_per_seq)
+    new_tables = torch.empty(S, max(width, 0), dtype=torch.int32)
+    old = torch.empty(max(block_tables.numel(), 1), dtype=torch.int32)
+    n = C.c_int(0)
+    check(lib().pkv_evict_tables(self._h, _ptr(block_tables), block_tables.shape[1],
+                                 _ptr(context_lens), S, int(keep), _ptr(new_tables), width,
+                                 _ptr(old), old.numel(), C.byref(n)), "pkv_evict_tables")
+    return new_tables, old[:n.value].clone()
+
+
+BlockManager.evict_tables = _evict_tables
 
 
 def _defrag(self, block_tables: torch.Tensor):

@@ -15,6 +15,8 @@
 // used blocks move to [0, n_used).
 // Copy-on-write (section 四.2): a request that writes its next token into a
 // block other requests still reference gets a private copy of that block.
+// Eviction: new tables for sequences cut to a budget (their old blocks stay
+// held until the rows that stay have been copied out of them).
 // The free set is a bitmap with a "lowest possibly free word" hint, so
 // allocate/free cost O(1) amortised instead of the page's list sort.
 #include <stdint.h>
@@ -245,6 +247,59 @@ PKV_API pkv_status pkv_append_slots_cow(pkv_block_manager* mgr, int32_t* block_t
     }
     *n_copy_pairs = n_pairs;
     return result;
+}
+
+PKV_API pkv_status pkv_evict_tables(pkv_block_manager* mgr, const int32_t* block_tables,
+                                    int max_blocks_per_seq, int32_t* context_lens, int num_seqs,
+                                    int keep, int32_t* new_tables, int new_blocks_per_seq,
+                                    int32_t* old_ids, int cap, int* n_old) {
+    if (!n_old) return PKV_ERR_INVALID;
+    *n_old = 0;
+    if (!mgr || num_seqs < 0 || max_blocks_per_seq < 0 || new_blocks_per_seq < 0 || cap < 0 ||
+        keep < 1)
+        return PKV_ERR_INVALID;
+    if (num_seqs > 0 && (!block_tables || !context_lens || !new_tables)) return PKV_ERR_INVALID;
+    if (cap > 0 && !old_ids) return PKV_ERR_INVALID;
+    const long long B = mgr->block_size;
+    const long long new_pages = (keep + B - 1) / B;
+    // check everything first: a failing call changes nothing
+    long long need = 0, old = 0;
+    for (int s = 0; s < num_seqs; ++s) {
+        const long long n = context_lens[s], pages = (n + B - 1) / B;
+        if (n < 0 || pages > max_blocks_per_seq) return PKV_ERR_INVALID;
+        const int32_t* row = block_tables + (size_t)s * max_blocks_per_seq;
+        for (long long j = 0; j < pages; ++j)
+            if (row[j] < 0 || row[j] >= mgr->num_blocks || mgr->ref[row[j]] == 0)
+                return PKV_ERR_INVALID;
+        if ((n > keep ? new_pages : pages) > new_blocks_per_seq) return PKV_ERR_INVALID;
+        if (n > keep) {
+            need += new_pages;
+            old += pages;
+        }
+    }
+    if (old > cap) return PKV_ERR_INVALID;
+    if (need > mgr->free_count) return PKV_ERR_NO_BLOCKS;
+    int k = 0;
+    for (int s = 0; s < num_seqs; ++s) {
+        const long long n = context_lens[s], pages = (n + B - 1) / B;
+        const int32_t* row = block_tables + (size_t)s * max_blocks_per_seq;
+        int32_t* dst = new_tables + (size_t)s * new_blocks_per_seq;
+        const bool cut = n > keep;
+        const long long used = cut ? new_pages : pages;
+        for (long long j = 0; j < new_blocks_per_seq; ++j) {
+            dst[j] = -1;
+            if (j >= used) continue;
+            if (cut)
+                pkv_block_allocate(mgr, &dst[j]);
+            else
+                dst[j] = row[j];
+        }
+        if (!cut) continue;
+        for (long long j = 0; j < pages; ++j) old_ids[k++] = row[j];
+        context_lens[s] = keep;
+    }
+    *n_old = k;
+    return PKV_OK;
 }
 
 PKV_API pkv_status pkv_defrag(pkv_block_manager* mgr, int32_t* block_tables,

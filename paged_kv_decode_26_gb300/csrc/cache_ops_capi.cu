@@ -1,0 +1,341 @@
+// cache_ops_capi.cu -- the C ABI's cache-budget calls: the decode that
+// accumulates attention weights (paged_attn_decode_weights) and the eviction
+// that goes by them (kv_evict): validation, workspace layout and launches.
+// Declarations and contracts: pagedkv.h.
+#include <cudaTypedefs.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "capi_host.h"
+#include "decode_pieces_launch.h"
+#include "evict_kernels.cuh"
+#include "pieces_host.h"
+
+using namespace pkv::host;
+
+namespace {
+
+bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + bn && y < x + an;
+}
+
+// A kernel that starts while the one ahead of it on the stream drains (it
+// waits for that one's results before it reads them).
+template <class Kernel, class Params>
+cudaError_t launch_dependent(Kernel kernel, dim3 grid, int threads, size_t smem,
+                             cudaStream_t stream, const Params& p) {
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace
+
+namespace pkv {
+namespace host {
+
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+int pieces_stream_heads(int n_kv_heads) {
+    int hw = kPieceWarps;
+    while (n_kv_heads % hw) hw /= 2;
+    return hw;
+}
+
+int pieces_ctas(int num_seqs, int n_kv_heads, int max_context_len, int sm_count) {
+    const int hw = pieces_stream_heads(n_kv_heads);
+    const long long chunks = (long long)num_seqs * (n_kv_heads / hw) *
+                             (((long long)max_context_len + kPieceTokens - 1) / kPieceTokens);
+    const long long streams = (chunks + kPieceMinRun - 1) / kPieceMinRun;
+    const int per_cta = kPieceWarps / hw;
+    const long long ctas = (streams + per_cta - 1) / per_cta;
+    return (int)(ctas < 1 ? 1 : (ctas < sm_count ? ctas : sm_count));
+}
+
+PiecesWorkspace pieces_workspace(int num_seqs, int n_heads, int n_kv_heads, int head_dim,
+                                 int max_context_len, int sm_count) {
+    PiecesWorkspace w;
+    const int ctas = pieces_ctas(num_seqs, n_kv_heads, max_context_len, sm_count);
+    const size_t rows = (size_t)num_seqs * n_heads +
+                        (size_t)ctas * kPieceWarps * (n_heads / n_kv_heads);
+    const size_t pairs = (size_t)num_seqs * n_kv_heads;
+    w.o = 0;
+    w.ml = align256(w.o + rows * head_dim * sizeof(float));
+    w.seg_first = align256(w.ml + rows * 2 * sizeof(float));
+    w.seg_last = align256(w.seg_first + pairs * sizeof(int));
+    w.end = align256(w.seg_last + pairs * sizeof(int));
+    return w;
+}
+
+pkv_status check_paged_decode(const void* out, pkv_dtype out_dtype, const void* q,
+                              const void* k_pool, const void* v_pool, pkv_dtype kv_dtype,
+                              const int32_t* block_tables, int max_blocks_per_seq,
+                              const int32_t* context_lens, int num_seqs, int n_heads,
+                              int n_kv_heads, int head_dim, int block_size, int num_blocks,
+                              float scale, int max_context_len) {
+    if (num_seqs < 0 || max_context_len < 0) return invalid("sizes");
+    if (num_seqs > 65535) return unsupported("more than 65535 sequences per call");
+    if (n_heads <= 0 || n_kv_heads <= 0 || n_heads % n_kv_heads)
+        return invalid("n_heads must be a positive multiple of n_kv_heads");
+    if (kv_dtype != PKV_BF16 && kv_dtype != PKV_F16)
+        return unsupported("kv_dtype must be F16 or BF16");
+    if (out_dtype != PKV_BF16 && out_dtype != PKV_F16 && out_dtype != PKV_F32)
+        return invalid("out_dtype");
+    if (!supported_shape(n_heads, n_kv_heads, head_dim, block_size))
+        return unsupported("head_dim 64/128, block_size 16/32, group 1/2/4/8");
+    if (n_heads > 4096) return unsupported("more than 4096 query heads");
+    if (num_blocks < 0 || max_blocks_per_seq <= 0) return invalid("pool / table sizes");
+    if (!table_tokens_fit(max_blocks_per_seq, block_size))
+        return unsupported("max_blocks_per_seq * block_size exceeds 2^31 - 1 tokens");
+    if (!std::isfinite(scale)) return invalid("scale is not finite");
+    if (max_context_len > 0x7fffffff - 1024) return unsupported("max_context_len");
+    if ((long long)num_seqs * (((long long)max_context_len + 15) / 16) > 0x7fffffffLL)
+        return unsupported("num_seqs * max_context_len exceeds 2^35 tokens");
+    if (num_seqs == 0) return PKV_OK;
+    if (!out || !q || !block_tables || !context_lens) return invalid("NULL pointer");
+    if (num_blocks > 0 && (!k_pool || !v_pool)) return invalid("k_pool or v_pool is NULL");
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool))
+        return invalid("out, q, k_pool and v_pool must be 16-byte aligned");
+    return PKV_OK;
+}
+
+pkv_status fill_pieces(pkv::PiecesLaunch* L, void* out, pkv_dtype out_dtype, const void* q,
+                       const void* k_pool, const void* v_pool, pkv_dtype kv_dtype,
+                       const int32_t* block_tables, int max_blocks_per_seq,
+                       const int32_t* context_lens, int num_seqs, int n_heads, int n_kv_heads,
+                       int head_dim, int block_size, int num_blocks, float scale,
+                       int max_context_len, const PiecesWorkspace& w, void* workspace,
+                       const DeviceInfo& dev, void* stream) {
+    std::memset(L, 0, sizeof(*L));
+    const int map_blocks = num_blocks > 0 ? num_blocks : 1;
+    cudaError_t e;
+    if ((e = encode_pool_map(&L->tm_k, num_blocks > 0 ? k_pool : q, kv_dtype, map_blocks,
+                             block_size, n_kv_heads, head_dim, 1, true, kPieceTokens)) ||
+        (e = encode_pool_map(&L->tm_v, num_blocks > 0 ? v_pool : q, kv_dtype, map_blocks,
+                             block_size, n_kv_heads, head_dim, 1, true, kPieceTokens)))
+        return cuda_fail(e);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    pkv::PieceParams& p = L->p;
+    p.out = out;
+    p.out_dtype = out_dtype;
+    p.q = q;
+    p.block_tables = block_tables;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.context_lens = context_lens;
+    p.num_seqs = num_seqs;
+    p.n_heads = n_heads;
+    p.n_kv_heads = n_kv_heads;
+    p.group = n_heads / n_kv_heads;
+    p.block_size = block_size;
+    p.num_blocks = num_blocks;
+    const long long table = (long long)max_blocks_per_seq * block_size;
+    p.cap_tokens = (int)(table < max_context_len ? table : max_context_len);
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.stream_heads = pieces_stream_heads(n_kv_heads);
+    L->ctas = pieces_ctas(num_seqs, n_kv_heads, max_context_len, dev.sm_count);
+    p.streams = L->ctas * (pkv::kPieceWarps / p.stream_heads);
+    p.min_run = kPieceMinRun;
+    p.ws_o = reinterpret_cast<float*>(ws + w.o);
+    p.ws_ml = reinterpret_cast<float*>(ws + w.ml);
+    p.seg_first = reinterpret_cast<int*>(ws + w.seg_first);
+    p.seg_last = reinterpret_cast<int*>(ws + w.seg_last);
+    p.errors = dev.errors;
+    L->stream = static_cast<cudaStream_t>(stream);
+    return PKV_OK;
+}
+
+pkv_status check_workspace(const void* workspace, size_t bytes, size_t need) {
+    if (!workspace || bytes < need) {
+        invalid("workspace smaller than the call's workspace_bytes()");
+        return PKV_ERR_WORKSPACE;
+    }
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return invalid("workspace must be 256-byte aligned");
+    return PKV_OK;
+}
+
+}  // namespace host
+}  // namespace pkv
+
+namespace {
+
+// Scores of every head: rows of whole chunks.
+size_t score_row(int max_context_len) { return ((size_t)max_context_len + 15) / 16 * 16; }
+
+size_t weights_bytes(int num_seqs, int n_heads, int n_kv_heads, int head_dim, int max_context_len,
+                     int sm_count, PiecesWorkspace* w) {
+    *w = pieces_workspace(num_seqs, n_heads, n_kv_heads, head_dim, max_context_len, sm_count);
+    return w->end + align256((size_t)num_seqs * n_heads * score_row(max_context_len) *
+                             sizeof(float));
+}
+
+}  // namespace
+
+extern "C" {
+
+PKV_API size_t pkv_decode_weights_workspace_bytes(int num_seqs, int n_heads, int n_kv_heads,
+                                                  int head_dim, int block_size,
+                                                  int max_context_len) {
+    if (!supported_shape(n_heads, n_kv_heads, head_dim, block_size) || num_seqs <= 0 ||
+        max_context_len < 0)
+        return 0;
+    DeviceInfo* dev = nullptr;
+    const int sms = device_info(&dev) == cudaSuccess ? dev->sm_count : kDefaultSms;
+    PiecesWorkspace w;
+    return weights_bytes(num_seqs, n_heads, n_kv_heads, head_dim, max_context_len, sms, &w);
+}
+
+PKV_API pkv_status paged_attn_decode_weights(
+    void* out, pkv_dtype out_dtype, const void* q, const void* k_pool, const void* v_pool,
+    pkv_dtype kv_dtype, const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* context_lens, float* weights, int64_t weight_stride, int num_seqs, int n_heads,
+    int n_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
+    int max_context_len, void* workspace, size_t workspace_bytes, void* stream) {
+    pkv_status st = check_paged_decode(out, out_dtype, q, k_pool, v_pool, kv_dtype, block_tables,
+                                       max_blocks_per_seq, context_lens, num_seqs, n_heads,
+                                       n_kv_heads, head_dim, block_size, num_blocks, scale,
+                                       max_context_len);
+    if (st != PKV_OK) return st;
+    if (weight_stride < max_context_len) return invalid("weight_stride below max_context_len");
+    if (num_seqs == 0) return PKV_OK;
+    if (!weights) return invalid("weights is NULL");
+    if ((reinterpret_cast<uintptr_t>(weights) & 3u) != 0) return invalid("weights must be 4-byte aligned");
+    DeviceInfo* dev = nullptr;
+    cudaError_t e = device_info(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    PiecesWorkspace w;
+    const size_t need = weights_bytes(num_seqs, n_heads, n_kv_heads, head_dim, max_context_len,
+                                      dev->sm_count, &w);
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != PKV_OK) return st;
+    pkv::PiecesLaunch L;
+    st = fill_pieces(&L, out, out_dtype, q, k_pool, v_pool, kv_dtype, block_tables,
+                     max_blocks_per_seq, context_lens, num_seqs, n_heads, n_kv_heads, head_dim,
+                     block_size, num_blocks, scale, max_context_len, w, workspace, *dev, stream);
+    if (st != PKV_OK) return st;
+    pkv::PieceParams& p = L.p;
+    p.scores = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + w.end);
+    p.score_stride = (long long)score_row(max_context_len);
+    p.weights = weights;
+    p.weight_stride = weight_stride;
+    e = kv_dtype == PKV_BF16 ? pkv::launch_pieces_bf16(head_dim, true, L)
+                             : pkv::launch_pieces_f16(head_dim, true, L);
+    if (e != cudaSuccess) return cuda_fail(e);
+    const int tiles = (p.cap_tokens + pkv::kWeightTokens - 1) / pkv::kWeightTokens;
+    const dim3 grid((unsigned)(tiles < 1 ? 1 : tiles), (unsigned)num_seqs);
+    const size_t smem = (size_t)n_heads * sizeof(float2);
+    e = head_dim == 128
+            ? launch_dependent(pkv::decode_weights_finish_kernel<128>, grid, pkv::kWeightThreads,
+                               smem, L.stream, p)
+            : launch_dependent(pkv::decode_weights_finish_kernel<64>, grid, pkv::kWeightThreads,
+                               smem, L.stream, p);
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e);
+}
+
+PKV_API pkv_status kv_evict(void* k_pool, void* v_pool, pkv_dtype dtype,
+                            const int32_t* block_tables, int max_blocks_per_seq,
+                            const int32_t* context_lens, const float* weights,
+                            int64_t weight_stride, int weight_cols, const int32_t* new_tables,
+                            int new_blocks_per_seq, int32_t* new_lens, float* new_weights,
+                            int64_t new_weight_stride, int new_weight_cols, int32_t* kept,
+                            int num_seqs, int keep, int recent, int n_kv_heads, int head_dim,
+                            int block_size, int num_blocks, void* stream) {
+    if (num_seqs < 0 || n_kv_heads <= 0 || head_dim <= 0 || block_size <= 0 || num_blocks < 0 ||
+        max_blocks_per_seq <= 0 || new_blocks_per_seq <= 0 || weight_cols < 0)
+        return invalid("sizes");
+    if (num_seqs > 65535) return unsupported("more than 65535 sequences per call");
+    if (keep < 1 || recent < 0 || recent > keep) return invalid("keep >= 1 and 0 <= recent <= keep");
+    if (!table_tokens_fit(max_blocks_per_seq, block_size))
+        return unsupported("max_blocks_per_seq * block_size exceeds 2^31 - 1 tokens");
+    if ((long long)new_blocks_per_seq * block_size < keep)
+        return invalid("new_tables cannot hold keep tokens");
+    if (weight_stride < weight_cols || new_weight_stride < new_weight_cols || new_weight_cols < keep)
+        return invalid("weight rows: strides below the columns, or new_weights below keep columns");
+    int es = 0;
+    switch (dtype) {
+        case PKV_F16:
+        case PKV_BF16: es = 2; break;
+        case PKV_F32: es = 4; break;
+        default: return invalid("dtype");
+    }
+    const long long row_bytes = (long long)n_kv_heads * head_dim * es;
+    if (row_bytes % 16)
+        return unsupported("n_kv_heads * head_dim * element size must be a multiple of 16 bytes");
+    if (row_bytes / 16 > 0x7fffffffLL) return unsupported("row too large");
+    if (num_seqs == 0) return PKV_OK;
+    if (!block_tables || !context_lens || !weights || !new_tables || !new_lens || !new_weights ||
+        !kept)
+        return invalid("NULL pointer");
+    if (num_blocks > 0 && (!k_pool || !v_pool)) return invalid("k_pool or v_pool is NULL");
+    if (!aligned16(k_pool) || !aligned16(v_pool)) return invalid("pools must be 16-byte aligned");
+    // the second kernel reads what the first one read: outputs may not lie on inputs
+    const size_t n = (size_t)num_seqs;
+    const struct {
+        const void* p;
+        size_t bytes;
+    } in[] = {{block_tables, n * max_blocks_per_seq * 4},
+              {context_lens, n * 4},
+              {weights, ((n - 1) * (size_t)weight_stride + (size_t)weight_cols) * 4},
+              {new_tables, n * new_blocks_per_seq * 4}},
+      outs[] = {{new_lens, n * 4},
+                {new_weights, ((n - 1) * (size_t)new_weight_stride + (size_t)new_weight_cols) * 4},
+                {kept, n * (size_t)keep * 4}};
+    for (const auto& o : outs)
+        for (const auto& i : in)
+            if (overlap(o.p, o.bytes, i.p, i.bytes))
+                return invalid("new_lens, new_weights and kept may not overlap the inputs");
+    DeviceInfo* dev = nullptr;
+    cudaError_t e = device_info(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+
+    pkv::EvictParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.block_tables = block_tables;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.context_lens = context_lens;
+    p.weights = weights;
+    p.weight_stride = weight_stride;
+    const long long table = (long long)max_blocks_per_seq * block_size;
+    p.cap_tokens = (int)(table < weight_cols ? table : weight_cols);
+    p.new_tables = new_tables;
+    p.new_blocks_per_seq = new_blocks_per_seq;
+    p.new_lens = new_lens;
+    p.new_weights = new_weights;
+    p.new_weight_stride = new_weight_stride;
+    p.new_weight_cols = new_weight_cols;
+    p.kept = kept;
+    p.num_seqs = num_seqs;
+    p.keep = keep;
+    p.recent = recent;
+    p.block_size = block_size;
+    p.num_blocks = num_blocks;
+    p.pool[0] = static_cast<uint4*>(k_pool);
+    p.pool[1] = static_cast<uint4*>(v_pool);
+    p.row_vec = (int)(row_bytes / 16);
+    p.part_vec = p.row_vec < 128 ? p.row_vec : 128;     // 2 KB of a row per warp
+    p.parts = (p.row_vec + p.part_vec - 1) / p.part_vec;
+    p.errors = dev->errors;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    pkv::evict_select_kernel<<<(unsigned)num_seqs, pkv::kEvictThreads, 0, cs>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e);
+    const long long units = (long long)num_seqs * ((keep + 31) / 32) * 2 * p.parts;
+    const int warps = pkv::kEvictCopyThreads / 32;
+    long long ctas = (units + warps - 1) / warps;
+    const long long cap = 8LL * dev->sm_count;
+    if (ctas > cap) ctas = cap;
+    e = launch_dependent(pkv::evict_copy_kernel, dim3((unsigned)ctas), pkv::kEvictCopyThreads, 0,
+                         cs, p);
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,50 @@
+// pieces_host.h -- host side shared by the calls built on the piece decode
+// (cache_ops_capi.cu, shared_capi.cu): argument checks, workspace layout,
+// launch parameters.
+#pragma once
+
+#include "capi_host.h"
+#include "decode_pieces_launch.h"
+
+namespace pkv {
+namespace host {
+
+constexpr int kDefaultSms = 152;      // workspace sizes asked for without a device
+constexpr int kPieceMinRun = 4;       // chunks a stream takes at least
+
+struct PiecesWorkspace {
+    size_t o, ml, seg_first, seg_last, end;   // byte offsets; end: first free byte
+};
+
+size_t align256(size_t n);
+
+// kv heads per stream: the largest of 8, 4, 2, 1 that divides n_kv_heads.
+int pieces_stream_heads(int n_kv_heads);
+
+// CTAs of the piece decode: one per SM, fewer where the longest contexts
+// allowed could not give every stream its least run.
+int pieces_ctas(int num_seqs, int n_kv_heads, int max_context_len, int sm_count);
+
+PiecesWorkspace pieces_workspace(int num_seqs, int n_heads, int n_kv_heads, int head_dim,
+                                 int max_context_len, int sm_count);
+
+// Argument checks that the calls share with paged_attn_decode.
+pkv_status check_paged_decode(const void* out, pkv_dtype out_dtype, const void* q,
+                              const void* k_pool, const void* v_pool, pkv_dtype kv_dtype,
+                              const int32_t* block_tables, int max_blocks_per_seq,
+                              const int32_t* context_lens, int num_seqs, int n_heads,
+                              int n_kv_heads, int head_dim, int block_size, int num_blocks,
+                              float scale, int max_context_len);
+
+pkv_status check_workspace(const void* workspace, size_t bytes, size_t need);
+
+pkv_status fill_pieces(pkv::PiecesLaunch* L, void* out, pkv_dtype out_dtype, const void* q,
+                       const void* k_pool, const void* v_pool, pkv_dtype kv_dtype,
+                       const int32_t* block_tables, int max_blocks_per_seq,
+                       const int32_t* context_lens, int num_seqs, int n_heads, int n_kv_heads,
+                       int head_dim, int block_size, int num_blocks, float scale,
+                       int max_context_len, const PiecesWorkspace& w, void* workspace,
+                       const DeviceInfo& dev, void* stream);
+
+}  // namespace host
+}  // namespace pkv
