@@ -506,6 +506,37 @@ PKV_API pkv_status kv_evict(void* k_pool, void* v_pool, pkv_dtype dtype,
                             int block_size, int num_blocks, void* stream);
 
 /*
+ * pkv_attn_prompt -- causal attention over whole prompts, straight from the
+ * projections' output, before anything is in pages ([SWAP] serving loop: the
+ * prefill step; kv_append with one slot per token then writes the rows into
+ * their pages).  The sequences are packed one after the other: sequence s owns
+ * tokens q_start[s] .. q_start[s+1]-1, and token i of it sees its tokens t <= i:
+ *
+ *     out[i, h, :] = sum_{t <= i} softmax_t(scale * q[i, h, :] . k[t, h / G]) v[t, h / G]
+ *
+ * with G = n_heads / n_kv_heads.
+ *   out          device [total_q, n_heads, head_dim] of out_dtype (F16, BF16 or
+ *                F32), contiguous; rows of no sequence are not written
+ *   q, k, v      device, token i at q + i * q_stride (elements of dtype, F16 or
+ *                BF16): [n_heads, head_dim] and [n_kv_heads, head_dim] contiguous
+ *                per token, so the three may be views of one fused tensor;
+ *                strides multiples of 8 elements; out may not overlap them
+ *   q_start      device int32 [num_seqs + 1], non-decreasing, within total_q
+ *   max_len      host-side bound of a sequence's length
+ * out, q, k and v 16-byte aligned.  head_dim 64 or 128, G 1, 2, 4 or 8.
+ * A sequence whose bounds lie outside the tokens or whose length exceeds
+ * max_len is left out (its rows are not written) and flagged
+ * PKV_DEVERR_CONTEXT.  The softmax weights enter the second product rounded to
+ * dtype, except for F32 outputs (hi + lo parts, as in the other calls).  One
+ * launch, no workspace.
+ */
+PKV_API pkv_status pkv_attn_prompt(void* out, pkv_dtype out_dtype, const void* q, int64_t q_stride,
+                               const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                               pkv_dtype dtype, const int32_t* q_start, int num_seqs, int total_q,
+                               int max_len, int n_heads, int n_kv_heads, int head_dim, float scale,
+                               void* stream);
+
+/*
  * kv_append -- write one new token per sequence into its page
  * (reshape-and-cache; [LAYOUT] section 三 append_token):
  *

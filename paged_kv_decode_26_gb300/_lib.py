@@ -62,6 +62,8 @@ SIGNATURES = {
     "kv_evict": (_i, [_p, _p, _i, _p, _i, _p, _p, _i64, _i, _p, _i, _p, _p, _i64, _i, _p, _i, _i,
                       _i, _i, _i, _i, _i, _p]),
     "pkv_evict_tables": (_i, [_p, _p, _i, _p, _i, _i, _p, _i, _p, _i, C.POINTER(_i)]),
+    "pkv_attn_prompt": (_i, [_p, _i, _p, _i64, _p, _i64, _p, _i64, _i, _p, _i, _i, _i, _i, _i, _i,
+                         _f, _p]),
     "kv_append": (_i, [_p, _p, _p, _p, _i, _p, _i, _i, _i, _i, _i, _p]),
     "swap_blocks": (_i, [_p, _p, _sz, _p, _i, _i64, _i64, _p]),
     "swap_blocks_kv": (_i, [_p, _p, _p, _p, _sz, _p, _i, _i64, _i64, _p]),

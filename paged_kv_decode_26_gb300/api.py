@@ -509,6 +509,44 @@ def kv_evict(k_pool: torch.Tensor, v_pool: torch.Tensor, block_tables: torch.Ten
     check(st, "kv_evict")
 
 
+def _token_stride(name: str, t: torch.Tensor) -> int:
+    """Checks packed rows [T, heads, head_dim] whose heads are contiguous; the
+    token stride in elements."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or (t.numel() and (t.stride(2) != 1 or
+                                       (t.shape[1] > 1 and t.stride(1) != t.shape[2]))):
+        raise ValueError(f"{name} must be [tokens, heads, head_dim], each token contiguous")
+    row = t.shape[1] * t.shape[2]
+    return t.stride(0) if t.shape[0] > 1 else row
+
+
+def attn_prompt(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                q_start: torch.Tensor, scale: float, max_len: int,
+                stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Causal attention over whole packed prompts: tokens q_start[s] ..
+    q_start[s+1]-1 are sequence s.  q [T, H, D], k and v [T, Hk, D] (each
+    token contiguous: views of one fused projection will do), out [T, H, D]
+    contiguous, q_start int32 [S + 1], max_len a bound of the lengths."""
+    _need_cuda("out", out)
+    _need_cuda("q_start", q_start)
+    strides = [_token_stride(n, t) for n, t in (("q", q), ("k", k), ("v", v))]
+    if q_start.dtype != torch.int32 or q_start.dim() != 1 or q_start.shape[0] < 1:
+        raise ValueError("q_start must be int32 [S + 1]")
+    T, H, D = q.shape
+    Hk = k.shape[1]
+    if (out.shape != q.shape or tuple(k.shape) != (T, Hk, D) or v.shape != k.shape
+            or k.dtype != q.dtype or v.dtype != q.dtype):
+        raise ValueError("inconsistent shapes or dtypes")
+    _need_one_device((out, q, k, v, q_start))
+    st = lib().pkv_attn_prompt(_addr(out), _DT[out.dtype], _addr(q), strides[0], _addr(k), strides[1],
+                           _addr(v), strides[2], _DT[q.dtype], _addr(q_start),
+                           q_start.shape[0] - 1, T, int(max_len), H, Hk, D, float(scale),
+                           _stream_handle(stream))
+    check(st, "attn_prompt")
+    return out
+
+
 def kv_append(k_pool: torch.Tensor, v_pool: torch.Tensor, k_new: torch.Tensor,
               v_new: torch.Tensor, slot_mapping: torch.Tensor,
               stream: Optional[torch.cuda.Stream] = None) -> None:

@@ -1,0 +1,116 @@
+// attn_capi.cu -- pkv_attn_prompt of the C ABI: validation, tensor maps, launch.
+// Declarations and contracts: pagedkv.h.
+#include <cudaTypedefs.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "attn_host.h"
+#include "attn_tc_launch.h"
+#include "capi_host.h"
+
+using namespace pkv::host;
+
+namespace pkv {
+namespace host {
+
+cudaError_t encode_rows_map(CUtensorMap* map, const void* x, pkv_dtype dt, int rows, int heads,
+                            int head_dim, long long row_stride, int box_heads, int box_rows) {
+    auto encode = tensor_map_encoder();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint64_t es = 2;
+    cuuint64_t dims[4] = {64, (cuuint64_t)head_dim / 64, (cuuint64_t)heads, (cuuint64_t)rows};
+    cuuint64_t strides[3] = {64 * es, (cuuint64_t)head_dim * es, (cuuint64_t)row_stride * es};
+    cuuint32_t box[4] = {64, 1, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = encode(map, dt == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                             : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                        4, const_cast<void*>(x), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+int attn_stages(int head_dim, int smem_optin) {
+    int stages = 8;
+    while (stages > 2 && pkv::attn_tc_smem_bytes(head_dim, stages) > (size_t)smem_optin) --stages;
+    return stages;
+}
+
+}  // namespace host
+}  // namespace pkv
+
+extern "C" {
+
+PKV_API pkv_status pkv_attn_prompt(void* out, pkv_dtype out_dtype, const void* q, int64_t q_stride,
+                               const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                               pkv_dtype dtype, const int32_t* q_start, int num_seqs, int total_q,
+                               int max_len, int n_heads, int n_kv_heads, int head_dim, float scale,
+                               void* stream) {
+    if (num_seqs < 0 || total_q < 0 || max_len < 0) return invalid("sizes");
+    if (n_heads <= 0 || n_kv_heads <= 0 || n_heads % n_kv_heads)
+        return invalid("n_heads must be a positive multiple of n_kv_heads");
+    if (dtype != PKV_BF16 && dtype != PKV_F16) return unsupported("dtype must be F16 or BF16");
+    if (out_dtype != PKV_BF16 && out_dtype != PKV_F16 && out_dtype != PKV_F32)
+        return invalid("out_dtype");
+    if (!supported_shape(n_heads, n_kv_heads, head_dim, 16))
+        return unsupported("head_dim 64/128, group 1/2/4/8");
+    if (!std::isfinite(scale)) return invalid("scale is not finite");
+    // a larger max_len than there are tokens only adds empty work items
+    if (max_len > total_q) max_len = total_q;
+    if (max_len > 0x7fffffff - 1024) return unsupported("max_len");
+    const int64_t q_row = (int64_t)n_heads * head_dim, kv_row = (int64_t)n_kv_heads * head_dim;
+    if (q_stride < q_row || k_stride < kv_row || v_stride < kv_row)
+        return invalid("token strides below the rows' elements");
+    if (q_stride % 8 || k_stride % 8 || v_stride % 8)
+        return invalid("token strides must be multiples of 8 elements");
+    if (q_stride >= 1ll << 38 || k_stride >= 1ll << 38 || v_stride >= 1ll << 38)
+        return unsupported("token stride");
+    if (num_seqs == 0 || total_q == 0 || max_len == 0) return PKV_OK;
+    if (!out || !q || !k || !v || !q_start) return invalid("NULL pointer");
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k) || !aligned16(v))
+        return invalid("out, q, k and v must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(q_start) & 3u) != 0)
+        return invalid("q_start must be 4-byte aligned");
+    const int G = n_heads / n_kv_heads;
+    const int pair_tokens = 2 * pkv::kAtRows / G;
+    const int tiles = (max_len + pair_tokens - 1) / pair_tokens;
+    const long long per_tile = (long long)n_kv_heads * num_seqs;
+    if (per_tile > 0x7fffffffLL) return unsupported("n_kv_heads * num_seqs exceeds 2^31 - 1");
+    DeviceInfo* dev = nullptr;
+    cudaError_t e = device_info(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    pkv::AttnLaunch L;
+    std::memset(&L, 0, sizeof(L));
+    if ((e = encode_rows_map(&L.tm_q, q, dtype, total_q, n_heads, head_dim, q_stride, G,
+                             pkv::kAtRows / G)) ||
+        (e = encode_rows_map(&L.tm_k, k, dtype, total_q, n_kv_heads, head_dim, k_stride, 1,
+                             pkv::kAtKeys)) ||
+        (e = encode_rows_map(&L.tm_v, v, dtype, total_q, n_kv_heads, head_dim, v_stride, 1,
+                             pkv::kAtKeys)))
+        return cuda_fail(e);
+    pkv::AttnParams& p = L.p;
+    p.out = out;
+    p.out_dtype = out_dtype;
+    p.num_seqs = num_seqs;
+    p.n_heads = n_heads;
+    p.n_kv_heads = n_kv_heads;
+    p.group = G;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.stages = attn_stages(head_dim, dev->smem_optin);
+    p.tiles = tiles;
+    p.n_items = per_tile * tiles;
+    p.q_start = q_start;
+    p.total_q = total_q;
+    p.max_len = max_len;
+    p.errors = dev->errors;
+    L.ctas = (int)(p.n_items < dev->sm_count ? p.n_items : dev->sm_count);
+    L.smem_bytes = pkv::attn_tc_smem_bytes(head_dim, p.stages);
+    L.stream = static_cast<cudaStream_t>(stream);
+    const bool precise = out_dtype == PKV_F32;
+    e = dtype == PKV_BF16 ? pkv::launch_attn_prompt_bf16(head_dim, precise, L)
+                          : pkv::launch_attn_prompt_f16(head_dim, precise, L);
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,20 @@
+// attn_host.h -- host side shared by the calls built on attn_tc_kernel.cuh.
+#pragma once
+
+#include "capi_host.h"
+
+namespace pkv {
+namespace host {
+
+// Rows [rows, heads, head_dim] (row stride in elements) as a 4-D tensor for
+// TMA: dims (64, head_dim / 64, heads, rows), box (64, 1, box_heads,
+// box_rows), 128-byte swizzle: one load per 64-element half brings box_rows x
+// box_heads rows of 128 bytes.  Rows past the tensor read as zeros.
+cudaError_t encode_rows_map(CUtensorMap* map, const void* x, pkv_dtype dt, int rows, int heads,
+                            int head_dim, long long row_stride, int box_heads, int box_rows);
+
+// Slots of the K/V ring that fit beside the queries.
+int attn_stages(int head_dim, int smem_optin);
+
+}  // namespace host
+}  // namespace pkv

@@ -1,0 +1,24 @@
+// attn_tc_launch.h -- host-side launch interface of attn_tc_kernel.cuh.
+#pragma once
+
+#include "attn_tc_kernel.cuh"
+
+namespace pkv {
+
+struct AttnLaunch {
+    CUtensorMap tm_q;
+    CUtensorMap tm_k;
+    CUtensorMap tm_v;
+    AttnParams p;
+    int ctas;
+    size_t smem_bytes;
+    cudaStream_t stream;
+};
+
+// Launch attn_tc_kernel<D, T, paged, precise>.
+cudaError_t launch_attn_prompt_bf16(int D, bool precise, const AttnLaunch& L);
+cudaError_t launch_attn_prompt_f16(int D, bool precise, const AttnLaunch& L);
+cudaError_t launch_attn_prefix_bf16(int D, bool precise, const AttnLaunch& L);
+cudaError_t launch_attn_prefix_f16(int D, bool precise, const AttnLaunch& L);
+
+}  // namespace pkv

@@ -132,3 +132,29 @@ def test_evict_tables_refuses_unheld_pages(L):
         bm.evict_tables(_ints([[0, -1, 2]]), _ints([9]), 5)
     with pytest.raises(ValueError):
         bm.evict_tables(_ints([[0, 2]]).long(), _ints([9]), 5)
+
+
+def _prompt(L, **kw):
+    a = dict(out=FAKE(1), od=1, q=FAKE(2), qs=1024, k=FAKE(3), ks=256, v=FAKE(4), vs=256, dt=1,
+             st=FAKE(5), S=2, T=100, ml=60, H=8, Hk=2, D=128, scale=0.1)
+    a.update(kw)
+    return L.pkv_attn_prompt(a["out"], a["od"], a["q"], a["qs"], a["k"], a["ks"], a["v"], a["vs"],
+                         a["dt"], a["st"], a["S"], a["T"], a["ml"], a["H"], a["Hk"], a["D"],
+                         a["scale"], NULL)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(S=-1), 1), (dict(T=-1), 1), (dict(ml=-1), 1), (dict(H=6, Hk=4), 1), (dict(D=96), 2),
+    (dict(H=6), 2), (dict(dt=2), 2), (dict(od=9), 1), (dict(scale=float("nan")), 1),
+    (dict(qs=1016), 1), (dict(ks=255), 1), (dict(vs=260), 1), (dict(vs=1 << 40), 2),
+    (dict(q=NULL), 1), (dict(out=NULL), 1), (dict(st=NULL), 1), (dict(k=C.c_void_p(4104)), 1),
+    (dict(st=C.c_void_p(4097)), 1), (dict(S=1 << 30, H=8, Hk=8, ks=1024, vs=1024), 2),
+])
+def test_prompt_refusals(L, kw, code):
+    assert _prompt(L, **kw) == code
+    assert L.pkv_last_error_detail()
+
+
+@pytest.mark.parametrize("kw", [dict(S=0, st=NULL), dict(T=0, q=NULL), dict(ml=0)])
+def test_prompt_of_nothing_is_a_no_op(L, kw):
+    assert _prompt(L, **kw) == 0
