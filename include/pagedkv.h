@@ -506,6 +506,50 @@ PKV_API pkv_status kv_evict(void* k_pool, void* v_pool, pkv_dtype dtype,
                             int block_size, int num_blocks, void* stream);
 
 /*
+ * paged_attn_decode_shared -- paged_attn_decode for a batch whose sequences
+ * share long prefixes ([LAYOUT] section 四.2: several requests point at the
+ * same physical blocks of a common prompt): each shared prefix is read and
+ * multiplied once for its whole group, on the tensor cores, the rest of every
+ * context as in paged_attn_decode, and the two parts are merged by the
+ * OnlineSoftmax recurrence.  The result is paged_attn_decode's.
+ *
+ *   group_start   device int32 [num_groups + 1], non-decreasing: sequences
+ *                 group_start[g] .. group_start[g+1]-1 are group g.  Sequences in
+ *                 no group are decoded alone.
+ *   prefix_lens   device int32 [num_groups], multiples of block_size: the first
+ *                 prefix_lens[g] tokens of group g's sequences lie in the same
+ *                 blocks (the caller's promise: only one member's table is read
+ *                 for them).  A member whose context is shorter than the prefix
+ *                 is decoded alone.
+ *   max_group, max_prefix  host-side bounds of a group's size (at most num_seqs)
+ *                 and of prefix_lens (at most max_context_len)
+ *   workspace     device, >= pkv_decode_shared_workspace_bytes(...) bytes,
+ *                 256-byte aligned; contents on entry are ignored.  Calls that
+ *                 may overlap on the GPU need a workspace each.
+ *   other arguments as paged_attn_decode (the split is automatic).
+ * A group with bounds outside the batch, more than max_group members, or a
+ * prefix that is negative, beyond max_prefix or no multiple of block_size is
+ * flagged PKV_DEVERR_CONTEXT and its members are decoded alone.  A split of a
+ * prefix with a block outside the pool is left out and flagged
+ * PKV_DEVERR_BLOCK_ID.  Softmax weights of the prefix enter the second product
+ * rounded to kv_dtype, except for F32 outputs.  Supported shapes as
+ * paged_attn_decode; at most 65535 sequences, 65535 groups, 4096 query heads.
+ * Three launches.
+ */
+PKV_API size_t pkv_decode_shared_workspace_bytes(int num_seqs, int num_groups, int max_group,
+                                                 int max_prefix, int n_heads, int n_kv_heads,
+                                                 int head_dim, int block_size,
+                                                 int max_context_len);
+
+PKV_API pkv_status paged_attn_decode_shared(
+    void* out, pkv_dtype out_dtype, const void* q, const void* k_pool, const void* v_pool,
+    pkv_dtype kv_dtype, const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* context_lens, const int32_t* group_start, const int32_t* prefix_lens,
+    int num_groups, int max_group, int max_prefix, int num_seqs, int n_heads, int n_kv_heads,
+    int head_dim, int block_size, int num_blocks, float scale, int max_context_len,
+    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * pkv_attn_prompt -- causal attention over whole prompts, straight from the
  * projections' output, before anything is in pages ([SWAP] serving loop: the
  * prefill step; kv_append with one slot per token then writes the rows into

@@ -62,6 +62,9 @@ SIGNATURES = {
     "kv_evict": (_i, [_p, _p, _i, _p, _i, _p, _p, _i64, _i, _p, _i, _p, _p, _i64, _i, _p, _i, _i,
                       _i, _i, _i, _i, _i, _p]),
     "pkv_evict_tables": (_i, [_p, _p, _i, _p, _i, _i, _p, _i, _p, _i, C.POINTER(_i)]),
+    "pkv_decode_shared_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i, _i]),
+    "paged_attn_decode_shared": (_i, [_p, _i, _p, _p, _p, _i, _p, _i, _p, _p, _p, _i, _i, _i, _i,
+                                      _i, _i, _i, _i, _i, _f, _i, _p, _sz, _p]),
     "pkv_attn_prompt": (_i, [_p, _i, _p, _i64, _p, _i64, _p, _i64, _i, _p, _i, _i, _i, _i, _i, _i,
                          _f, _p]),
     "kv_append": (_i, [_p, _p, _p, _p, _i, _p, _i, _i, _i, _i, _i, _p]),

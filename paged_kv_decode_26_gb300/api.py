@@ -509,6 +509,56 @@ def kv_evict(k_pool: torch.Tensor, v_pool: torch.Tensor, block_tables: torch.Ten
     check(st, "kv_evict")
 
 
+def decode_shared_workspace_bytes(num_seqs: int, num_groups: int, max_group: int,
+                                  max_prefix: int, n_heads: int, n_kv_heads: int, head_dim: int,
+                                  block_size: int, max_context_len: int) -> int:
+    return int(lib().pkv_decode_shared_workspace_bytes(num_seqs, num_groups, max_group,
+                                                       max_prefix, n_heads, n_kv_heads, head_dim,
+                                                       block_size, max_context_len))
+
+
+def paged_attn_decode_shared(out: torch.Tensor, q: torch.Tensor, k_pool: torch.Tensor,
+                             v_pool: torch.Tensor, block_tables: torch.Tensor,
+                             context_lens: torch.Tensor, group_start: torch.Tensor,
+                             prefix_lens: torch.Tensor, scale: float, max_context_len: int,
+                             max_group: int, max_prefix: int,
+                             workspace: Optional[torch.Tensor] = None,
+                             stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """paged_attn_decode where sequences group_start[g] .. group_start[g+1]-1
+    (int32 [groups + 1]) share the blocks of their first prefix_lens[g] tokens
+    (int32 [groups], whole blocks): each prefix is attended once for its
+    group.  max_group and max_prefix bound the groups' sizes and prefixes."""
+    _need_all_cuda(_DECODE_NAMES + ("group_start", "prefix_lens"),
+                   (out, q, k_pool, v_pool, block_tables, context_lens, group_start, prefix_lens))
+    for name, t in (("block_tables", block_tables), ("context_lens", context_lens),
+                    ("group_start", group_start), ("prefix_lens", prefix_lens)):
+        if t.dtype != torch.int32:
+            raise ValueError(f"{name} must be int32")
+    S, H, D = q.shape
+    nb, B, Hk, D2 = k_pool.shape
+    if (D2 != D or v_pool.shape != k_pool.shape or out.shape != q.shape
+            or q.dtype != k_pool.dtype or v_pool.dtype != k_pool.dtype
+            or block_tables.dim() != 2 or block_tables.shape[0] != S
+            or context_lens.shape != (S,) or prefix_lens.dim() != 1
+            or group_start.shape != (prefix_lens.shape[0] + 1,)):
+        raise ValueError("inconsistent shapes or dtypes")
+    _need_one_device((out, q, k_pool, v_pool, block_tables, context_lens, group_start,
+                      prefix_lens, workspace))
+    groups = prefix_lens.shape[0]
+    if workspace is None:
+        n = decode_shared_workspace_bytes(S, groups, int(max_group), int(max_prefix), H, Hk, D, B,
+                                          int(max_context_len))
+        workspace = _stream_buffer(n, q.device, stream)
+    st = lib().paged_attn_decode_shared(
+        _addr(out), _DT[out.dtype], _addr(q), _addr(k_pool), _addr(v_pool), _DT[k_pool.dtype],
+        _addr(block_tables), block_tables.shape[1], _addr(context_lens), _addr(group_start),
+        _addr(prefix_lens), groups, int(max_group), int(max_prefix), S, H, Hk, D, B, nb,
+        float(scale), int(max_context_len), _addr(workspace),
+        workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    check(st, "paged_attn_decode_shared")
+    return out
+
+
 def _token_stride(name: str, t: torch.Tensor) -> int:
     """Checks packed rows [T, heads, head_dim] whose heads are contiguous; the
     token stride in elements."""

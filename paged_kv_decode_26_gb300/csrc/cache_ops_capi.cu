@@ -21,25 +21,6 @@ bool overlap(const void* a, size_t an, const void* b, size_t bn) {
     return x < y + bn && y < x + an;
 }
 
-// A kernel that starts while the one ahead of it on the stream drains (it
-// waits for that one's results before it reads them).
-template <class Kernel, class Params>
-cudaError_t launch_dependent(Kernel kernel, dim3 grid, int threads, size_t smem,
-                             cudaStream_t stream, const Params& p) {
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof(cfg));
-    cudaLaunchAttribute attr[1];
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
 }  // namespace
 
 namespace pkv {

@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kPieceThreads, 1)
         fence_barrier_init();
     }
     const int* gs = p.group_start;
-    if (!WEIGHTS && p.num_groups <= kPieceGroupsMax) {
+    if (!WEIGHTS && p.num_groups > 0 && p.num_groups <= kPieceGroupsMax) {
         for (int i = threadIdx.x; i <= p.num_groups; i += kPieceThreads) s_gs[i] = p.group_start[i];
         gs = s_gs;
         __syncthreads();

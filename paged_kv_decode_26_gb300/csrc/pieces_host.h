@@ -3,6 +3,8 @@
 // launch parameters.
 #pragma once
 
+#include <cstring>
+
 #include "capi_host.h"
 #include "decode_pieces_launch.h"
 
@@ -45,6 +47,25 @@ pkv_status fill_pieces(pkv::PiecesLaunch* L, void* out, pkv_dtype out_dtype, con
                        int head_dim, int block_size, int num_blocks, float scale,
                        int max_context_len, const PiecesWorkspace& w, void* workspace,
                        const DeviceInfo& dev, void* stream);
+
+// A kernel that starts while the one ahead of it on the stream drains (it
+// waits for that one's results before it reads them).
+template <class Kernel, class Params>
+cudaError_t launch_dependent(Kernel kernel, dim3 grid, int threads, size_t smem,
+                             cudaStream_t stream, const Params& p) {
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
 
 }  // namespace host
 }  // namespace pkv

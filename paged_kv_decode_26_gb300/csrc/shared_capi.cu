@@ -1,0 +1,193 @@
+// shared_capi.cu -- paged_attn_decode_shared of the C ABI: the shared
+// prefixes on tcgen05 (attn_tc_kernel.cuh), the rest of every context as
+// equal pieces (decode_pieces_kernel.cuh), and their merge.  Declarations and
+// contracts: pagedkv.h.
+#include <cudaTypedefs.h>
+
+#include <cstring>
+
+#include "attn_host.h"
+#include "attn_tc_launch.h"
+#include "capi_host.h"
+#include "decode_pieces_launch.h"
+#include "pieces_host.h"
+
+using namespace pkv::host;
+
+namespace {
+
+// Splits of the longest prefix: enough work items (split x kv head x pair of
+// row tiles x group) for every SM to take `kItemsPerSm` of them, but at least
+// kMinSplit tokens each, so that a split's fixed cost stays small.
+constexpr int kItemsPerSm = 2;
+constexpr int kMinSplit = 512;
+
+struct SharedShape {
+    int tiles;
+    int split_tokens;
+    int max_splits;
+    PiecesWorkspace pieces;
+    size_t start, pre_o, pre_ml, end;
+};
+
+SharedShape shared_shape(int num_seqs, int num_groups, int max_group, int max_prefix, int n_heads,
+                         int n_kv_heads, int head_dim, int max_context_len, int sm_count) {
+    SharedShape c;
+    const int G = n_heads / n_kv_heads;
+    const int pair_rows = 2 * pkv::kAtRows / G;
+    c.tiles = max_group > 0 ? (max_group + pair_rows - 1) / pair_rows : 0;
+    const long long units = (long long)num_groups * n_kv_heads * c.tiles;
+    c.max_splits = 0;
+    c.split_tokens = pkv::kAtKeys;
+    if (units > 0 && max_prefix > 0) {
+        long long splits = ((long long)kItemsPerSm * sm_count + units - 1) / units;
+        const long long most = ((long long)max_prefix + kMinSplit - 1) / kMinSplit;
+        if (splits > most) splits = most;
+        const long long tokens = (max_prefix + splits - 1) / splits;
+        c.split_tokens = (int)((tokens + pkv::kAtKeys - 1) / pkv::kAtKeys * pkv::kAtKeys);
+        c.max_splits = (int)(((long long)max_prefix + c.split_tokens - 1) / c.split_tokens);
+    }
+    c.pieces = pieces_workspace(num_seqs, n_heads, n_kv_heads, head_dim, max_context_len, sm_count);
+    const size_t rows = (size_t)num_seqs * n_heads * c.max_splits;
+    c.start = c.pieces.end;
+    c.pre_o = align256(c.start + (size_t)num_seqs * sizeof(int));
+    c.pre_ml = align256(c.pre_o + rows * head_dim * sizeof(float));
+    c.end = align256(c.pre_ml + rows * 2 * sizeof(float));
+    return c;
+}
+
+bool groups_ok(int num_seqs, int num_groups, int max_group, int max_prefix, int max_context_len) {
+    return num_groups >= 0 && max_group >= 0 && max_group <= num_seqs && max_prefix >= 0 &&
+           max_prefix <= max_context_len;
+}
+
+}  // namespace
+
+extern "C" {
+
+PKV_API size_t pkv_decode_shared_workspace_bytes(int num_seqs, int num_groups, int max_group,
+                                                 int max_prefix, int n_heads, int n_kv_heads,
+                                                 int head_dim, int block_size,
+                                                 int max_context_len) {
+    if (!supported_shape(n_heads, n_kv_heads, head_dim, block_size) || num_seqs <= 0 ||
+        max_context_len < 0 ||
+        !groups_ok(num_seqs, num_groups, max_group, max_prefix, max_context_len))
+        return 0;
+    DeviceInfo* dev = nullptr;
+    const int sms = device_info(&dev) == cudaSuccess ? dev->sm_count : kDefaultSms;
+    return shared_shape(num_seqs, num_groups, max_group, max_prefix, n_heads, n_kv_heads, head_dim,
+                        max_context_len, sms)
+        .end;
+}
+
+PKV_API pkv_status paged_attn_decode_shared(
+    void* out, pkv_dtype out_dtype, const void* q, const void* k_pool, const void* v_pool,
+    pkv_dtype kv_dtype, const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* context_lens, const int32_t* group_start, const int32_t* prefix_lens,
+    int num_groups, int max_group, int max_prefix, int num_seqs, int n_heads, int n_kv_heads,
+    int head_dim, int block_size, int num_blocks, float scale, int max_context_len,
+    void* workspace, size_t workspace_bytes, void* stream) {
+    pkv_status st = check_paged_decode(out, out_dtype, q, k_pool, v_pool, kv_dtype, block_tables,
+                                       max_blocks_per_seq, context_lens, num_seqs, n_heads,
+                                       n_kv_heads, head_dim, block_size, num_blocks, scale,
+                                       max_context_len);
+    if (st != PKV_OK) return st;
+    if (num_groups < 0 || max_group < 0 || max_prefix < 0) return invalid("group sizes");
+    if (num_groups > 65535) return unsupported("more than 65535 groups");
+    if (num_seqs == 0) return PKV_OK;
+    if (num_groups > 0 && (!group_start || !prefix_lens))
+        return invalid("group_start or prefix_lens is NULL");
+    if (((reinterpret_cast<uintptr_t>(group_start) | reinterpret_cast<uintptr_t>(prefix_lens)) &
+         3u) != 0)
+        return invalid("group_start and prefix_lens must be 4-byte aligned");
+    if (!groups_ok(num_seqs, num_groups, max_group, max_prefix, max_context_len))
+        return invalid("max_group beyond num_seqs, or max_prefix beyond max_context_len");
+    DeviceInfo* dev = nullptr;
+    cudaError_t e = device_info(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    const SharedShape c = shared_shape(num_seqs, num_groups, max_group, max_prefix, n_heads,
+                                       n_kv_heads, head_dim, max_context_len, dev->sm_count);
+    if ((st = check_workspace(workspace, workspace_bytes, c.end)) != PKV_OK) return st;
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    pkv::PiecesLaunch L;
+    st = fill_pieces(&L, out, out_dtype, q, k_pool, v_pool, kv_dtype, block_tables,
+                     max_blocks_per_seq, context_lens, num_seqs, n_heads, n_kv_heads, head_dim,
+                     block_size, num_blocks, scale, max_context_len, c.pieces, workspace, *dev,
+                     stream);
+    if (st != PKV_OK) return st;
+    pkv::PieceParams& p = L.p;
+    p.group_start = group_start;
+    p.prefix_lens = prefix_lens;
+    p.num_groups = num_groups;
+    p.max_group = max_group;
+    p.max_prefix = max_prefix;
+    p.start = reinterpret_cast<int*>(ws + c.start);
+    p.pre_o = reinterpret_cast<float*>(ws + c.pre_o);
+    p.pre_ml = reinterpret_cast<float*>(ws + c.pre_ml);
+    p.split_tokens = c.split_tokens;
+    p.max_splits = c.max_splits;
+
+    // ---- the prefixes
+    if (c.max_splits > 0 && num_blocks > 0) {
+        pkv::AttnLaunch A;
+        std::memset(&A, 0, sizeof(A));
+        const int G = n_heads / n_kv_heads;
+        if ((e = encode_rows_map(&A.tm_q, q, kv_dtype, num_seqs, n_heads, head_dim,
+                                 (long long)n_heads * head_dim, G, pkv::kAtRows / G)) ||
+            (e = encode_pool_map(&A.tm_k, k_pool, kv_dtype, num_blocks, block_size, n_kv_heads,
+                                 head_dim, 1, true)) ||
+            (e = encode_pool_map(&A.tm_v, v_pool, kv_dtype, num_blocks, block_size, n_kv_heads,
+                                 head_dim, 1, true)))
+            return cuda_fail(e);
+        pkv::AttnParams& a = A.p;
+        a.out_dtype = out_dtype;
+        a.num_seqs = num_seqs;
+        a.n_heads = n_heads;
+        a.n_kv_heads = n_kv_heads;
+        a.group = G;
+        a.scale_log2 = p.scale_log2;
+        a.stages = attn_stages(head_dim, dev->smem_optin);
+        a.tiles = c.tiles;
+        a.n_items = (long long)num_groups * n_kv_heads * c.tiles * c.max_splits;
+        a.group_start = group_start;
+        a.prefix_lens = prefix_lens;
+        a.num_groups = num_groups;
+        a.max_group = max_group;
+        a.max_prefix = max_prefix;
+        a.block_tables = block_tables;
+        a.max_blocks_per_seq = max_blocks_per_seq;
+        a.context_lens = context_lens;
+        a.cap_tokens = p.cap_tokens;
+        a.block_size = block_size;
+        a.num_blocks = num_blocks;
+        a.split_tokens = c.split_tokens;
+        a.max_splits = c.max_splits;
+        a.pre_o = reinterpret_cast<float*>(ws + c.pre_o);
+        a.pre_ml = reinterpret_cast<float*>(ws + c.pre_ml);
+        a.errors = dev->errors;
+        A.ctas = (int)(a.n_items < dev->sm_count ? a.n_items : dev->sm_count);
+        A.smem_bytes = pkv::attn_tc_smem_bytes(head_dim, a.stages);
+        A.stream = L.stream;
+        const bool precise = out_dtype == PKV_F32;
+        e = kv_dtype == PKV_BF16 ? pkv::launch_attn_prefix_bf16(head_dim, precise, A)
+                                 : pkv::launch_attn_prefix_f16(head_dim, precise, A);
+        if (e != cudaSuccess) return cuda_fail(e);
+        L.after_prefix = true;
+    } else {
+        p.num_groups = 0;      // whole contexts, nothing to join
+    }
+    // ---- the rest of every context, and the merge
+    e = kv_dtype == PKV_BF16 ? pkv::launch_pieces_bf16(head_dim, false, L)
+                             : pkv::launch_pieces_f16(head_dim, false, L);
+    if (e != cudaSuccess) return cuda_fail(e);
+    const long long units = (long long)num_seqs * n_heads;
+    const dim3 grid((unsigned)((units + pkv::kFinishWarps - 1) / pkv::kFinishWarps));
+    e = head_dim == 128
+            ? launch_dependent(pkv::decode_shared_finish_kernel<128>, grid, 32 * pkv::kFinishWarps,
+                               0, L.stream, p)
+            : launch_dependent(pkv::decode_shared_finish_kernel<64>, grid, 32 * pkv::kFinishWarps,
+                               0, L.stream, p);
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e);
+}
+
+}  // extern "C"

@@ -158,3 +158,38 @@ def test_prompt_refusals(L, kw, code):
 @pytest.mark.parametrize("kw", [dict(S=0, st=NULL), dict(T=0, q=NULL), dict(ml=0)])
 def test_prompt_of_nothing_is_a_no_op(L, kw):
     assert _prompt(L, **kw) == 0
+
+
+def _shared(L, **kw):
+    a = dict(out=FAKE(1), od=1, q=FAKE(2), k=FAKE(3), v=FAKE(4), kd=1, bt=FAKE(5), mb=4,
+             cl=FAKE(6), gs=FAKE(7), pl=FAKE(8), ng=1, mg=2, mp=32, S=2, H=8, Hk=8, D=128, B=16,
+             nb=10, scale=0.1, maxc=64, ws=FAKE(9), wsb=0)
+    a.update(kw)
+    return L.paged_attn_decode_shared(
+        a["out"], a["od"], a["q"], a["k"], a["v"], a["kd"], a["bt"], a["mb"], a["cl"], a["gs"],
+        a["pl"], a["ng"], a["mg"], a["mp"], a["S"], a["H"], a["Hk"], a["D"], a["B"], a["nb"],
+        a["scale"], a["maxc"], a["ws"], a["wsb"], NULL)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(S=-1), 1), (dict(S=65536), 2), (dict(ng=-1), 1), (dict(ng=65536), 2), (dict(mg=-1), 1),
+    (dict(mg=3), 1), (dict(mp=-1), 1), (dict(mp=65), 1), (dict(gs=NULL), 1), (dict(pl=NULL), 1),
+    (dict(gs=C.c_void_p(4098)), 1), (dict(H=6, Hk=4), 1), (dict(D=96), 2), (dict(B=8), 2),
+    (dict(kd=2), 2), (dict(od=7), 1), (dict(k=NULL), 1), (dict(scale=float("nan")), 1),
+    (dict(q=NULL), 1), (dict(out=C.c_void_p(4104)), 1),
+])
+def test_shared_refusals(L, kw, code):
+    assert _shared(L, **kw) == code
+    assert L.pkv_last_error_detail()
+
+
+def test_shared_of_no_sequences_is_a_no_op(L):
+    assert _shared(L, S=0, mg=0, q=NULL) == 0
+
+
+def test_shared_workspace_bytes(L):
+    f = L.pkv_decode_shared_workspace_bytes
+    assert f(4, 1, 5, 64, 8, 8, 128, 16, 100) == 0          # a group beyond the batch
+    assert f(4, 1, 4, 101, 8, 8, 128, 16, 100) == 0         # a prefix beyond the context
+    assert f(4, 0, 0, 0, 8, 8, 128, 16, 100) > 0
+    assert f(64, 1, 64, 4096, 8, 8, 128, 16, 5000) > f(64, 0, 0, 0, 8, 8, 128, 16, 5000)
