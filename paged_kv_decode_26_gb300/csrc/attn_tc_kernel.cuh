@@ -109,6 +109,31 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+// MMAs issued by the lane with `lead` set; every lane of the warp runs the
+// instruction, so descriptors stay in uniform registers.
+__device__ __forceinline__ void at_mma(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                       uint32_t idesc, uint32_t accumulate, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead));
+}
+__device__ __forceinline__ void at_mma_tmem_a(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
+                                              uint32_t idesc, uint32_t accumulate, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead));
+}
+__device__ __forceinline__ void at_commit(uint64_t* bar, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::
+            "r"(smem_addr(bar)),
+        "r"(lead)
+        : "memory");
+}
+
 template <int D, typename T, bool PAGED, bool PRECISE>
 __global__ void __launch_bounds__(kAtThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -428,6 +453,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         const uint64_t dq0 = tc_desc_sw128(smem_addr(sQ), 16, 1024);
         const uint64_t dk0 = tc_desc_sw128(smem_addr(sKV), 16, 1024);
         const uint64_t dv0 = tc_desc_sw128(smem_addr(sKV), KV_HALF, 1024);
+        const uint32_t lead = elect_one() ? 1u : 0u;
         int slot = 0, sph = 0;
         int st = 0;                         // ring slot of the next tile to use
         uint32_t ph = 0;
@@ -444,16 +470,16 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             }
             if (!ok) return;
             tc_fence_after();
-            if (elect_one()) {
+            {
                 const uint64_t q = dq0 + (uint64_t)((t * Q_BYTES) >> 4);
                 const uint64_t k = dk0 + (uint64_t)(ks * (KV_BYTES >> 4));
                 const uint32_t d = tmem + t * TILE_COLS + S_COL;
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i)
-                    tc_mma(d, q + (((i / 4) * Q_HALF + (i % 4) * 32) >> 4),
-                           k + (((i / 4) * KV_HALF + (i % 4) * 32) >> 4), id_s, i > 0 ? 1u : 0u);
-                tc_commit(&s_full[t]);
-                if (last) tc_commit(&q_free[t]);
+                    at_mma(d, q + (((i / 4) * Q_HALF + (i % 4) * 32) >> 4),
+                           k + (((i / 4) * KV_HALF + (i % 4) * 32) >> 4), id_s, i > 0 ? 1u : 0u, lead);
+                at_commit(&s_full[t], lead);
+                if (last) at_commit(&q_free[t], lead);
             }
             __syncwarp();
         };
@@ -477,7 +503,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             wait(&kv_full[st], ph);
             for (int t = 0; t < 2; ++t)
                 if (ok && cur.nt[t]) issue_s(t, st, true, cur.nt[t] == 1);
-            if (ok && elect_one()) tc_commit(&kv_free[st]);
+            if (ok) at_commit(&kv_free[st], lead);
             __syncwarp();
             if (++st == NS) {
                 st = 0;
@@ -523,18 +549,18 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                             wait(&p_full[2 * t + half], n_p[t]);
                             if (!ok) break;
                             tc_fence_after();
-                            if (elect_one()) {
+                            {
                                 const uint32_t o = tmem + t * TILE_COLS;
                                 const uint64_t v = dv0 + (uint64_t)(vs * (KV_BYTES >> 4));
 #pragma unroll
                                 for (int part = 0; part < (PRECISE ? 2 : 1); ++part)
 #pragma unroll
                                     for (int i = half * 4; i < half * 4 + 4; ++i)
-                                        tc_mma_tmem_a(
+                                        at_mma_tmem_a(
                                             o, o + S_COL + part * (kAtKeys / 2) + i * 8,
                                             v + (uint64_t)((i * 16 * 128) >> 4), id_o,
-                                            (j > 0 || part > 0 || i > 0) ? 1u : 0u);
-                                if (half && j + 1 == nt) tc_commit(&o_full[t]);
+                                            (j > 0 || part > 0 || i > 0) ? 1u : 0u, lead);
+                                if (half && j + 1 == nt) at_commit(&o_full[t], lead);
                             }
                             __syncwarp();
                         }
@@ -552,10 +578,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     }
                 }
                 if (!ok) break;
-                if (elect_one()) {
-                    tc_commit(&kv_free[vs]);
-                    if (have_k) tc_commit(&kv_free[ks]);
-                }
+                at_commit(&kv_free[vs], lead);
+                if (have_k) at_commit(&kv_free[ks], lead);
                 __syncwarp();
                 if (have_k && ++st == NS) {
                     st = 0;
@@ -564,7 +588,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             }
         }
         // every MMA complete before the tensor memory is released
-        if (elect_one()) tc_commit(fin);
+        at_commit(fin, lead);
         __syncwarp();
         mbar_wait(fin, 0, p.errors);
         __syncwarp();
