@@ -45,7 +45,7 @@ constexpr int kAtThreads = 384;     // 8 softmax warps, MMA, loader, scheduler, 
 // softmax warps (which hold a row of S) have taken over the others' share.
 constexpr int kAtSoftmaxRegs = 200, kAtOtherRegs = 104;
 static_assert(256 * kAtSoftmaxRegs + 128 * kAtOtherRegs <= kAtThreads * 168, "registers");
-constexpr int kAtItems = 4;         // work items the scheduler is ahead
+constexpr int kAtItems = 2;         // the item in work and the next one
 
 struct AttnParams {
     void* out;
@@ -58,6 +58,7 @@ struct AttnParams {
     int stages;                // slots of the K/V ring
     int tiles;                 // pairs of row tiles of the longest sequence / largest group
     long long n_items;
+    int dynamic;               // prompts: one CTA per item, running CTAs take over waiting ones
     // whole prompts
     const int* q_start;        // [num_seqs + 1]
     int total_q;
@@ -97,8 +98,15 @@ struct AttnItem {
 
 inline size_t attn_tc_smem_bytes(int D, int stages) {
     return 1024 + (size_t)2 * kAtRows * D * 2 + (size_t)stages * kAtKeys * D * 2 +
-           (size_t)(2 * stages + 1 + 4 + 2 + 4 + 2 + 2 + 2 * kAtItems + 1) * sizeof(uint64_t) +
-           kAtItems * sizeof(AttnItem) + 16;
+           (size_t)(2 * stages + 1 + 4 + 2 + 4 + 2 + 2 + 2 * kAtItems + 2) * sizeof(uint64_t) +
+           kAtItems * sizeof(AttnItem) + 32;
+}
+
+// The largest of three in one instruction (fmaxf's treatment of NaN).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -107,6 +115,35 @@ __device__ __forceinline__ bool elect_one() {
         "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(p));
     return p != 0;
+}
+
+// Asks for a CTA of this grid that has not started; the answer (16 bytes)
+// completes on `bar`.  If there was one it will not start: the caller does its
+// work.  No request may follow one that found none.
+__device__ __forceinline__ void steal_cta(uint4* answer, uint64_t* bar) {
+    mbar_arrive_expect_tx(bar, 16);
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+        "[%0], [%1];" ::"r"(smem_addr(answer)),
+        "r"(smem_addr(bar))
+        : "memory");
+}
+// Index of the CTA taken over, -1 if there was none left.
+__device__ __forceinline__ int stolen_cta(const uint4* answer) {
+    int id;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t.reg .b32 x;\n\t"
+        "ld.shared.b128 h, [%1];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "mov.b32 x, -1;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 x, h;\n\t"
+        "mov.b32 %0, x;\n\t}"
+        : "=r"(id)
+        : "r"(smem_addr(answer))
+        : "memory");
+    // the next answer is written by the async proxy after this read
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    return id;
 }
 
 // MMAs issued by the lane with `lead` set; every lane of the warp runs the
@@ -157,7 +194,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     unsigned char* sQ = sm;
     unsigned char* sKV = sQ + 2 * Q_BYTES;
     const int NS = p.stages;
-    uint64_t* kv_full = reinterpret_cast<uint64_t*>(sKV + (size_t)NS * KV_BYTES);
+    uint64_t* kv_full = reinterpret_cast<uint64_t*>(sKV + (size_t)NS * KV_BYTES + 16);
     uint64_t* kv_free = kv_full + NS;
     uint64_t* land = kv_free + NS;           // a V tile to clear rows of has landed
     uint64_t* q_full = land + 1;             // [tile]
@@ -169,8 +206,10 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     uint64_t* it_full = o_free + 2;          // [kAtItems]
     uint64_t* it_free = it_full + kAtItems;
     uint64_t* fin = it_free + kAtItems;
-    AttnItem* items = reinterpret_cast<AttnItem*>(fin + 1);
+    uint64_t* steal_bar = fin + 1;           // a request for another CTA's item
+    AttnItem* items = reinterpret_cast<AttnItem*>(steal_bar + 1);
     int* s_tmem = reinterpret_cast<int*>(items + kAtItems);
+    uint4* steal = reinterpret_cast<uint4*>(sm + 2 * Q_BYTES + (size_t)NS * KV_BYTES);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.group;
     const int QT = kAtRows / G;              // tokens per row tile
@@ -202,6 +241,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             mbar_init(&it_free[i], 10);
         }
         mbar_init(fin, 1);
+        mbar_init(steal_bar, 1);
         fence_barrier_init();
     }
     tc_fence_before();
@@ -213,28 +253,35 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtOtherRegs));
     if (warp == 10) {
         // ================= scheduler: the items of this CTA =================
-        // Item i: the pair of row tiles that sees the most keys first.  CTA c
-        // takes items c, c + grid, ...; lanes look at 32 of them at once.
-        const long long per_tile = (long long)p.n_kv_heads * (PAGED ? p.num_groups * (long long)p.max_splits : p.num_seqs);
+        // CTA c takes items c, c + grid, ...; lanes look at 32 of them at once.
+        // With `dynamic` there is a CTA for every item: this one takes its own,
+        // then, one after the other, those of CTAs that have not started yet.
+        const long long per_tile =
+            (long long)p.n_kv_heads *
+            (PAGED ? p.num_groups * (long long)p.max_splits : p.num_seqs);
+        const bool dynamic = !PAGED && p.dynamic != 0;
+        const long long stride = dynamic ? p.n_items : gridDim.x;
+        uint32_t steal_ph = 0;
         int slot = 0, round = 0;
         bool ok = true;
-        for (long long base = blockIdx.x; ok; base += 32ll * gridDim.x) {
-            const long long i = base + (long long)lane * gridDim.x;
+        for (long long base = blockIdx.x; ok;) {
+            const long long i = base + (long long)lane * stride;
             AttnItem it;
             bool have = false;
             it.done = 0;
             if (i < p.n_items) {
                 if (!PAGED) {
-                    const int tile = p.tiles - 1 - (int)(i / per_tile);
+                    // the last pair of tiles of every sequence comes first
+                    const int back = (int)(i / per_tile);
                     const int x = (int)(i % per_tile);
                     const int s = x / p.n_kv_heads;
                     it.kvh = x % p.n_kv_heads;
                     const int q0 = p.q_start[s], q1 = p.q_start[s + 1];
                     const int len = q1 - q0;
-                    const int lo = tile * 2 * QT;
+                    const int lo = ((len + 2 * QT - 1) / (2 * QT) - 1 - back) * 2 * QT;
                     if (q0 < 0 || len < 0 || q1 > p.total_q || len > p.max_len) {
-                        if (tile == 0 && it.kvh == 0) raise_error(p.errors, PKV_DEVERR_CONTEXT);
-                    } else if (lo < len) {
+                        if (back == 0 && it.kvh == 0) raise_error(p.errors, PKV_DEVERR_CONTEXT);
+                    } else if (lo >= 0 && len > 0) {
                         have = true;
                         it.row0 = q0 + lo;
                         it.rows = len - lo;
@@ -298,7 +345,39 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 }
             }
             unsigned todo = __ballot_sync(0xffffffffu, have);
-            const bool more = __any_sync(0xffffffffu, base + 32ll * gridDim.x < p.n_items);
+            bool more;
+            if (dynamic) {
+                // place the item, and ask for another one only when there is
+                // a slot for it: what waits here cannot go to an idle SM
+                if (todo) {
+                    ok = round == 0 ||
+                         __all_sync(0xffffffffu, mbar_wait(&it_free[slot], (round - 1) & 1, p.errors));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        items[slot] = it;
+                        mbar_arrive(&it_full[slot]);
+                    }
+                    if (++slot == kAtItems) {
+                        slot = 0;
+                        ++round;
+                    }
+                    todo = 0;
+                }
+                ok = round == 0 ||
+                     __all_sync(0xffffffffu, mbar_wait(&it_free[slot], (round - 1) & 1, p.errors));
+                if (!ok) break;
+                if (lane == 0) steal_cta(steal, steal_bar);
+                ok = __all_sync(0xffffffffu, mbar_wait(steal_bar, steal_ph, p.errors));
+                steal_ph ^= 1u;
+                if (!ok) break;
+                const int next = stolen_cta(steal);
+                __syncwarp();
+                more = next >= 0;
+                if (more) base = next;
+            } else {
+                base += 32ll * stride;
+                more = base < p.n_items;
+            }
             while (ok && (todo || !more)) {
                 const bool w = round == 0 || mbar_wait(&it_free[slot], (round - 1) & 1, p.errors);
                 ok = __all_sync(0xffffffffu, w);
@@ -652,16 +731,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     }
                     float m8[8];
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) m8[c] = y[c];
+                    for (int e = 0; e < 8; ++e) m8[e] = fmaxf(y[e], y[8 + e]);
 #pragma unroll
-                    for (int c = 8; c < kAtKeys; c += 16)
+                    for (int c = 16; c < kAtKeys; c += 16)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            m8[e] = c + 8 + e < kAtKeys
-                                        ? fmaxf(fmaxf(m8[e], y[c + e]), y[(c + 8 + e) % kAtKeys])
-                                        : fmaxf(m8[e], y[c + e]);
-                    const float mx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                                           fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
+                        for (int e = 0; e < 8; ++e) m8[e] = max3(m8[e], y[c + e], y[c + 8 + e]);
+                    const float mx = max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]),
+                                          fmaxf(m8[6], m8[7]));
                     const float tmax = mx * a;
                     const bool first = m_used == -INFINITY;
                     const bool grow = tmax > m_used + kTcRescale;
