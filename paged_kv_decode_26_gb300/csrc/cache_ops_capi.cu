@@ -8,6 +8,7 @@
 #include <cstring>
 
 #include "capi_host.h"
+#include "decode_launch.h"
 #include "decode_pieces_launch.h"
 #include "evict_kernels.cuh"
 #include "pieces_host.h"
@@ -213,12 +214,14 @@ PKV_API pkv_status paged_attn_decode_weights(
                              : pkv::launch_pieces_f16(head_dim, true, L);
     if (e != cudaSuccess) return cuda_fail(e);
     const int tiles = (p.cap_tokens + pkv::kWeightTokens - 1) / pkv::kWeightTokens;
-    const dim3 grid((unsigned)(tiles < 1 ? 1 : tiles), (unsigned)num_seqs);
-    const size_t smem = (size_t)n_heads * sizeof(float2);
+    const dim3 grid((unsigned)(n_heads + tiles), (unsigned)num_seqs);
+    const size_t merge = (size_t)pkv::kFinishWarps * head_dim * sizeof(float);
+    const size_t sums = (size_t)n_heads * sizeof(float2);
+    const size_t smem = merge > sums ? merge : sums;
     e = head_dim == 128
-            ? launch_dependent(pkv::decode_weights_finish_kernel<128>, grid, pkv::kWeightThreads,
+            ? launch_dependent(pkv::decode_weights_finish_kernel<128>, grid, pkv::kFinishThreads,
                                smem, L.stream, p)
-            : launch_dependent(pkv::decode_weights_finish_kernel<64>, grid, pkv::kWeightThreads,
+            : launch_dependent(pkv::decode_weights_finish_kernel<64>, grid, pkv::kFinishThreads,
                                smem, L.stream, p);
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
 }
@@ -307,12 +310,25 @@ PKV_API pkv_status kv_evict(void* k_pool, void* v_pool, pkv_dtype dtype,
     p.parts = (p.row_vec + p.part_vec - 1) / p.part_vec;
     p.errors = dev->errors;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    pkv::evict_select_kernel<<<(unsigned)num_seqs, pkv::kEvictThreads, 0, cs>>>(p);
+    static unsigned long long select_mask = 0;
+    p.staged = p.cap_tokens < pkv::kEvictStaged ? p.cap_tokens : pkv::kEvictStaged;
+    const size_t smem = (size_t)p.staged * sizeof(uint32_t);
+    e = pkv::ensure_smem_limit(reinterpret_cast<const void*>(&pkv::evict_select_kernel),
+                               &select_mask, smem);
+    if (e != cudaSuccess) return cuda_fail(e);
+    pkv::evict_select_kernel<<<(unsigned)num_seqs, pkv::kEvictThreads, smem, cs>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e);
-    const long long units = (long long)num_seqs * ((keep + 31) / 32) * 2 * p.parts;
+    // 32 tokens per warp where that gives every SM 16 warps, fewer otherwise:
+    // a warp's tokens are copied one batch of loads after the other (64
+    // tokens of 1 KB rows on 16 warps took 23 us)
     const int warps = pkv::kEvictCopyThreads / 32;
-    long long ctas = (units + warps - 1) / warps;
     const long long cap = 8LL * dev->sm_count;
+    p.batch = 32;
+    auto count = [&] {
+        return (long long)num_seqs * ((keep + p.batch - 1) / p.batch) * 2 * p.parts;
+    };
+    while (p.batch > 1 && count() < 16LL * dev->sm_count) p.batch /= 2;
+    long long ctas = (count() + warps - 1) / warps;
     if (ctas > cap) ctas = cap;
     e = launch_dependent(pkv::evict_copy_kernel, dim3((unsigned)ctas), pkv::kEvictCopyThreads, 0,
                          cs, p);

@@ -475,118 +475,137 @@ __device__ __forceinline__ PieceSet piece_set(const PieceParams& p, int s, int h
     return c;
 }
 
-// Merged (M, L) of the pieces, by one warp: lanes take pieces in turn.
-__device__ __forceinline__ float2 merge_ml(const PieceParams& p, const PieceSet& c, int lane) {
-    const int k = c.n_pre + c.first + c.extra;
-    float m = -INFINITY;
-    for (int i = lane; i < k; i += 32) m = fmaxf(m, piece_ml(p, c, i).x);
-#pragma unroll
-    for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    float l = 0.f;
-    for (int i = lane; i < k; i += 32) {
-        const float2 ml = piece_ml(p, c, i);
-        if (ml.y != 0.f) l += ml.y * exp2f(ml.x - m);      // NaN stays NaN
-    }
-#pragma unroll
-    for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-    return make_float2(m, l);
+// (M, L) of two states joined.
+__device__ __forceinline__ float2 join_ml(float2 a, float2 b) {
+    const float m = fmaxf(a.x, b.x);
+    // (an empty state has L = 0; NaN stays NaN)
+    const float la = a.y != 0.f ? a.y * exp2f(a.x - m) : 0.f;
+    const float lb = b.y != 0.f ? b.y * exp2f(b.x - m) : 0.f;
+    return make_float2(m, la + lb);
 }
 
-// The merged output row of (s, h), by one warp.
-template <int D>
-__device__ __forceinline__ void merge_row(const PieceParams& p, const PieceSet& c, float2 ml, int s,
-                                          int h, int lane) {
-    constexpr int V = D / 32;
+// Merged (M, L) of the pieces, by `lanes` neighbouring lanes of a warp (a
+// power of two), lane `sub` of them taking pieces sub, sub + lanes, ...
+__device__ __forceinline__ float2 merge_ml(const PieceParams& p, const PieceSet& c, int sub,
+                                           int lanes) {
     const int k = c.n_pre + c.first + c.extra;
+    float2 ml = make_float2(-INFINITY, 0.f);
+#pragma unroll 4
+    for (int i = sub; i < k; i += lanes) ml = join_ml(ml, piece_ml(p, c, i));
+    for (int off = lanes / 2; off; off >>= 1)
+        ml = join_ml(ml, make_float2(__shfl_xor_sync(0xffffffffu, ml.x, off),
+                                     __shfl_xor_sync(0xffffffffu, ml.y, off)));
+    return ml;
+}
+
+constexpr int kFinishThreads = 128;
+constexpr int kFinishWarps = kFinishThreads / 32;
+
+// The merged output row of (s, h), by one CTA: its warps take the pieces in
+// turn, so that many pieces (a long context on many streams) are read at
+// once.  s_o: [kFinishWarps, D].
+template <int D>
+__device__ __forceinline__ void merge_row(const PieceParams& p, const PieceSet& c, int s, int h,
+                                          float* s_o) {
+    constexpr int V = D / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int k = c.n_pre + c.first + c.extra;
+    const float2 ml = merge_ml(p, c, lane, 32);
+    const float inv = ml.y != 0.f ? 1.f / ml.y : 0.f;
     float o[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) o[e] = 0.f;
-    const float inv = ml.y != 0.f ? 1.f / ml.y : 0.f;
 #pragma unroll 4
-    for (int i = 0; i < k; ++i) {
+    for (int i = warp; i < k; i += kFinishWarps) {
         const float2 a = piece_ml(p, c, i);
         const float w = a.y != 0.f ? a.y * exp2f(a.x - ml.x) * inv : 0.f;
         const float* row = piece_o(p, c, i, D) + lane * V;
-        float x[V];
-        if (V == 4) {
-            const float4 r = *reinterpret_cast<const float4*>(row);
-            x[0] = r.x, x[1] = r.y, x[2 % V] = r.z, x[3 % V] = r.w;
-        } else {
-            const float2 r = *reinterpret_cast<const float2*>(row);
-            x[0] = r.x, x[1] = r.y;
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+            const float2 x = *reinterpret_cast<const float2*>(row + e);
+            o[e] += w * x.x;
+            o[e + 1] += w * x.y;
         }
-#pragma unroll
-        for (int e = 0; e < V; ++e) o[e] += w * x[e];
     }
-    const size_t d = ((size_t)s * p.n_heads + h) * D + lane * V;
-    if (p.out_dtype == PKV_F32) {
-        float* out = reinterpret_cast<float*>(p.out) + d;
 #pragma unroll
-        for (int e = 0; e < V; e += 2)
-            *reinterpret_cast<float2*>(out + e) = make_float2(o[e], o[e + 1]);
-    } else {
-        uint16_t* out = reinterpret_cast<uint16_t*>(p.out) + d;
+    for (int e = 0; e < V; e += 2)
+        *reinterpret_cast<float2*>(s_o + warp * D + lane * V + e) = make_float2(o[e], o[e + 1]);
+    __syncthreads();
+    const int d = 2 * threadIdx.x;
+    if (d >= D) return;
+    float2 x = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < V; e += 2)
-            *reinterpret_cast<uint32_t*>(out + e) = pack_out(o[e], o[e + 1], p.out_dtype);
+    for (int w = 0; w < kFinishWarps; ++w) {
+        const float2 y = *reinterpret_cast<const float2*>(s_o + w * D + d);
+        x.x += y.x;
+        x.y += y.y;
     }
+    const size_t at = ((size_t)s * p.n_heads + h) * D + d;
+    if (p.out_dtype == PKV_F32)
+        *reinterpret_cast<float2*>(reinterpret_cast<float*>(p.out) + at) = x;
+    else
+        *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.out) + at) =
+            pack_out(x.x, x.y, p.out_dtype);
 }
 
-// Merges every (sequence, head): one warp each.
-constexpr int kFinishWarps = 4;
+// One CTA per (head, sequence).
 template <int D>
-__global__ void __launch_bounds__(32 * kFinishWarps)
+__global__ void __launch_bounds__(kFinishThreads)
     decode_shared_finish_kernel(const __grid_constant__ PieceParams p) {
+    __shared__ __align__(16) float s_o[kFinishWarps * D];
     dependency_wait();
-    const int lane = threadIdx.x & 31;
-    const long long u = (long long)blockIdx.x * kFinishWarps + (threadIdx.x >> 5);
-    if (u >= (long long)p.num_seqs * p.n_heads) return;
-    const int s = (int)(u / p.n_heads), h = (int)(u % p.n_heads);
-    const int n = piece_length(p, s), start = p.start[s];
-    const PieceSet c = piece_set(p, s, h, n, start);
-    merge_row<D>(p, c, merge_ml(p, c, lane), s, h, lane);
+    const int s = blockIdx.y, h = blockIdx.x;
+    merge_row<D>(p, piece_set(p, s, h, piece_length(p, s), p.start[s]), s, h, s_o);
 }
 
-// Adds the weights of kWeightTokens tokens of one sequence per CTA (grid x:
-// token tiles, y: sequences) and merges the sequence's cut heads, dealt over
-// its CTAs.  The heads of a token are summed in order: the result does not
-// depend on the launch.
-constexpr int kWeightThreads = 256;
-constexpr int kWeightTokens = 4 * kWeightThreads;
+// grid x: n_heads CTAs that merge a head cut into pieces (or empty), then a
+// CTA per kWeightTokens tokens that adds their weights; y: sequences.  A
+// thread owns four neighbouring tokens and sums their weights over the heads
+// in order, so the result does not depend on the launch.
+constexpr int kWeightTokens = 4 * kFinishThreads;
 template <int D>
-__global__ void __launch_bounds__(kWeightThreads)
+__global__ void __launch_bounds__(kFinishThreads)
     decode_weights_finish_kernel(const __grid_constant__ PieceParams p) {
-    extern __shared__ float2 s_ml[];     // (M, 1 / L) per head
+    extern __shared__ __align__(16) float s_mem[];
     dependency_wait();
     const int s = blockIdx.y;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n = piece_length(p, s);
-    for (int h = warp; h < p.n_heads; h += kWeightThreads / 32) {
-        const PieceSet c = piece_set(p, s, h, n, 0);
-        float2 ml;
-        if (c.extra == 0 && c.first) {
-            ml = piece_ml(p, c, 0);
-        } else {
-            ml = merge_ml(p, c, lane);
-            if (h % gridDim.x == blockIdx.x) merge_row<D>(p, c, ml, s, h, lane);
-        }
-        if (lane == 0)
+    if ((int)blockIdx.x < p.n_heads) {
+        const PieceSet c = piece_set(p, s, blockIdx.x, n, 0);
+        if (c.extra || !c.first) merge_row<D>(p, c, s, blockIdx.x, s_mem);
+        return;
+    }
+    const int t0 = (blockIdx.x - p.n_heads) * kWeightTokens;
+    if (t0 >= n) return;
+    // (M, 1 / L) of every head, four lanes each
+    float2* s_ml = reinterpret_cast<float2*>(s_mem);
+    for (int h0 = 0; h0 < p.n_heads; h0 += kFinishThreads / 4) {
+        const int h = h0 + threadIdx.x / 4;
+        PieceSet c = piece_set(p, s, min(h, p.n_heads - 1), n, 0);
+        const float2 ml = merge_ml(p, c, threadIdx.x & 3, 4);
+        if (h < p.n_heads && (threadIdx.x & 3) == 0)
             s_ml[h] = make_float2(ml.x == -INFINITY ? 0.f : ml.x, ml.y != 0.f ? 1.f / ml.y : 0.f);
     }
     __syncthreads();
-    for (int k = 0; k < 4; ++k) {
-        const int t = blockIdx.x * kWeightTokens + k * kWeightThreads + threadIdx.x;
-        if (t >= n) break;
-        const float* x = p.scores + (size_t)s * p.n_heads * p.score_stride + t;
-        float w = 0.f;
+    const int t = t0 + 4 * threadIdx.x;
+    if (t >= n) return;
+    const float* x = p.scores + (size_t)s * p.n_heads * p.score_stride + t;
+    float w[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-        for (int h = 0; h < p.n_heads; ++h) {
-            const float2 ml = s_ml[h];
-            w += exp2f(x[(size_t)h * p.score_stride] - ml.x) * ml.y;
-        }
-        float* acc = p.weights + (size_t)s * p.weight_stride + t;
-        *acc += w;
+    for (int h = 0; h < p.n_heads; ++h) {
+        const float2 ml = s_ml[h];
+        // (rows hold whole chunks of 16: the last ones past the context are
+        // read, whatever they hold, and not used)
+        const float4 y = __ldcs(reinterpret_cast<const float4*>(x + (size_t)h * p.score_stride));
+        w[0] += exp2f(y.x - ml.x) * ml.y;
+        w[1] += exp2f(y.y - ml.x) * ml.y;
+        w[2] += exp2f(y.z - ml.x) * ml.y;
+        w[3] += exp2f(y.w - ml.x) * ml.y;
     }
+    float* acc = p.weights + (size_t)s * p.weight_stride + t;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (t + e < n) acc[e] += w[e];
 }
 
 }  // namespace pkv

@@ -10,7 +10,7 @@
 //     pass.  It reads 4 bytes per token a pass, from L2 after the first.
 //   evict_copy_kernel    moves the listed tokens' K and V rows into the new
 //     pages: bound by HBM, each kept row read and written once.  A warp takes
-//     32 listed tokens, so the page-table lookups of a batch are one
+//     up to 32 listed tokens, so the page-table lookups of a batch are one
 //     coalesced round, and keeps 8 16-byte loads in flight per lane.
 // The rows move to other pages, so no copy can overwrite a row that another
 // still has to read, and pages that other sequences share stay as they are.
@@ -23,6 +23,7 @@ namespace pkv {
 constexpr int kEvictThreads = 1024;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictBins = 2048;
+constexpr int kEvictStaged = 48 * 1024;   // keys of a sequence kept in shared memory
 
 struct EvictParams {
     const int* block_tables;
@@ -41,12 +42,14 @@ struct EvictParams {
     int num_seqs;
     int keep;
     int recent;
+    int staged;                 // keys that fit the launch's shared memory
     int block_size;
     int num_blocks;
     uint4* pool[2];
     int row_vec;                // 16-byte vectors per token row
     int parts;                  // column parts per row
     int part_vec;               // vectors per part
+    int batch;                  // kept tokens per unit, at most 32
     unsigned int* errors;
 };
 
@@ -87,6 +90,16 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
 
     const int older = n - p.recent;          // candidates
     int want = p.keep - p.recent;            // of them stay (want < older)
+    // the passes below read the keys from shared memory where they fit
+    // (a pass over 32768 weights from L2 took 12 us, from there 3)
+    extern __shared__ uint32_t s_keys[];
+    const bool staged = older <= p.staged;
+    if (staged) {
+#pragma unroll 8
+        for (int t = tid; t < older; t += kEvictThreads) s_keys[t] = weight_key(w[t]);
+        __syncthreads();
+    }
+    auto key_of = [&](int t) -> uint32_t { return staged ? s_keys[t] : weight_key(w[t]); };
     // ---- the smallest key that stays, and how many of its equals do
     uint32_t prefix = 0xffffffffu;           // want == 0: no key reaches it
     if (want > 0) {
@@ -100,7 +113,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
             __syncthreads();
 #pragma unroll 4
             for (int t = tid; t < (older + 31) / 32 * 32; t += kEvictThreads) {
-                const uint32_t key = t < older ? weight_key(w[t]) : 0u;
+                const uint32_t key = t < older ? key_of(t) : 0u;
                 const bool in = t < older && (key & mask) == prefix;
                 const int bin = in ? (int)((key >> shift) & digits) : -1;
                 // many equal keys in a warp: one addition
@@ -144,8 +157,9 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
     const int seg = ((n + kEvictWarps - 1) / kEvictWarps + 31) / 32 * 32;
     const int t0 = warp * seg, t1 = min(n, t0 + seg);
     int above = 0, equal = 0;
+#pragma unroll 4
     for (int t = t0 + lane; t - lane < t1; t += 32) {
-        const uint32_t key = t < older ? weight_key(w[t]) : 0u;
+        const uint32_t key = t < older ? key_of(t) : 0u;
         above += __popc(__ballot_sync(0xffffffffu, (t < older && key > prefix) ||
                                                        (t >= older && t < n)));
         equal += __popc(__ballot_sync(0xffffffffu, t < older && key == prefix));
@@ -162,9 +176,10 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
     }
     at += min(eq, want);
     const unsigned below = (1u << lane) - 1u;
+#pragma unroll 4
     for (int t = t0 + lane; t - lane < t1; t += 32) {
         const float x = t < n ? w[t] : 0.f;
-        const uint32_t key = weight_key(x);
+        const uint32_t key = t < older ? key_of(t) : 0u;
         const bool is_eq = t < older && key == prefix;
         const unsigned eq_mask = __ballot_sync(0xffffffffu, is_eq);
         const bool take = (t < older ? key > prefix : t < n) ||
@@ -183,12 +198,12 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
 constexpr int kEvictCopyThreads = 256;
 constexpr int kEvictUnroll = 8;
 
-// Units: (sequence, 32 kept tokens, pool, part), the part fastest so that a
+// Units: (sequence, `batch` kept tokens, pool, part), the part fastest so that a
 // token's row is read by neighbouring warps.
 __global__ void __launch_bounds__(kEvictCopyThreads) evict_copy_kernel(const EvictParams p) {
     dependency_wait();
     const int lane = threadIdx.x & 31;
-    const int batches = (p.keep + 31) / 32;
+    const int batches = (p.keep + p.batch - 1) / p.batch;
     const long long units = (long long)p.num_seqs * batches * 2 * p.parts;
     const long long stride = (long long)gridDim.x * (kEvictCopyThreads / 32);
     for (long long u = (long long)blockIdx.x * (kEvictCopyThreads / 32) + (threadIdx.x >> 5);
@@ -196,11 +211,11 @@ __global__ void __launch_bounds__(kEvictCopyThreads) evict_copy_kernel(const Evi
         const int part = (int)(u % p.parts);
         const int which = (int)(u / p.parts % 2);
         const long long sb = u / p.parts / 2;
-        const int s = (int)(sb / batches), j = (int)(sb % batches) * 32 + lane;
+        const int s = (int)(sb / batches), j0 = (int)(sb % batches) * p.batch, j = j0 + lane;
         if (evict_length(p, s) <= p.keep) continue;
         // source and destination row of this lane's token (-1: none)
         long long src = -1, dst = -1;
-        if (j < p.keep) {
+        if (lane < p.batch && j < p.keep) {
             const int t = p.kept[(size_t)s * p.keep + j];
             const int sb_id = p.block_tables[(size_t)s * p.max_blocks_per_seq + t / p.block_size];
             const int db_id = p.new_tables[(size_t)s * p.new_blocks_per_seq + j / p.block_size];
@@ -213,8 +228,8 @@ __global__ void __launch_bounds__(kEvictCopyThreads) evict_copy_kernel(const Evi
         }
         uint4* pool = p.pool[which];
         const int col0 = part * p.part_vec, cols = min(p.part_vec, p.row_vec - col0);
-        const int rows = min(32, p.keep - (j - lane));
-        // lanes walk the 32 x cols vectors of the batch; (row, col) of lane
+        const int rows = min(p.batch, p.keep - j0);
+        // lanes walk the rows x cols vectors of the batch; (row, col) of lane
         int row = lane / cols, col = lane % cols;
         const int dr = 32 / cols, dc = 32 % cols;
         while (__any_sync(0xffffffffu, row < rows)) {

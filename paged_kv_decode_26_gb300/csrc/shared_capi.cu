@@ -16,11 +16,9 @@ using namespace pkv::host;
 
 namespace {
 
-// Splits of the longest prefix: enough work items (split x kv head x pair of
-// row tiles x group) for every SM to take `kItemsPerSm` of them, but at least
-// kMinSplit tokens each, so that a split's fixed cost stays small.
-constexpr int kItemsPerSm = 2;
-constexpr int kMinSplit = 512;
+// A split costs its key tiles and about this many more (queries, first and
+// last products, output of the partial states).
+constexpr int kSplitCost = 4;
 
 struct SharedShape {
     int tiles;
@@ -40,11 +38,19 @@ SharedShape shared_shape(int num_seqs, int num_groups, int max_group, int max_pr
     c.max_splits = 0;
     c.split_tokens = pkv::kAtKeys;
     if (units > 0 && max_prefix > 0) {
-        long long splits = ((long long)kItemsPerSm * sm_count + units - 1) / units;
-        const long long most = ((long long)max_prefix + kMinSplit - 1) / kMinSplit;
-        if (splits > most) splits = most;
-        const long long tokens = (max_prefix + splits - 1) / splits;
-        c.split_tokens = (int)((tokens + pkv::kAtKeys - 1) / pkv::kAtKeys * pkv::kAtKeys);
+        // Work items (split x kv head x pair of row tiles x group) are dealt
+        // out to the SMs in turn: the split length with the smallest sum of
+        // key tiles over the busiest SM's items, the longer one of equals.
+        const int key_tiles = (max_prefix + pkv::kAtKeys - 1) / pkv::kAtKeys;
+        long long best = 0;
+        for (int n = key_tiles; n >= 1; --n) {
+            const long long items = units * ((key_tiles + n - 1) / n);
+            const long long cost = (items + sm_count - 1) / sm_count * (n + kSplitCost);
+            if (best == 0 || cost < best) {
+                best = cost;
+                c.split_tokens = n * pkv::kAtKeys;
+            }
+        }
         c.max_splits = (int)(((long long)max_prefix + c.split_tokens - 1) / c.split_tokens);
     }
     c.pieces = pieces_workspace(num_seqs, n_heads, n_kv_heads, head_dim, max_context_len, sm_count);
@@ -180,13 +186,11 @@ PKV_API pkv_status paged_attn_decode_shared(
     e = kv_dtype == PKV_BF16 ? pkv::launch_pieces_bf16(head_dim, false, L)
                              : pkv::launch_pieces_f16(head_dim, false, L);
     if (e != cudaSuccess) return cuda_fail(e);
-    const long long units = (long long)num_seqs * n_heads;
-    const dim3 grid((unsigned)((units + pkv::kFinishWarps - 1) / pkv::kFinishWarps));
-    e = head_dim == 128
-            ? launch_dependent(pkv::decode_shared_finish_kernel<128>, grid, 32 * pkv::kFinishWarps,
-                               0, L.stream, p)
-            : launch_dependent(pkv::decode_shared_finish_kernel<64>, grid, 32 * pkv::kFinishWarps,
-                               0, L.stream, p);
+    const dim3 grid((unsigned)n_heads, (unsigned)num_seqs);
+    e = head_dim == 128 ? launch_dependent(pkv::decode_shared_finish_kernel<128>, grid,
+                                           pkv::kFinishThreads, 0, L.stream, p)
+                        : launch_dependent(pkv::decode_shared_finish_kernel<64>, grid,
+                                           pkv::kFinishThreads, 0, L.stream, p);
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
 }
 
