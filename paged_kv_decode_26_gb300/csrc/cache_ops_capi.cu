@@ -306,32 +306,61 @@ PKV_API pkv_status kv_evict(void* k_pool, void* v_pool, pkv_dtype dtype,
     p.pool[0] = static_cast<uint4*>(k_pool);
     p.pool[1] = static_cast<uint4*>(v_pool);
     p.row_vec = (int)(row_bytes / 16);
-    p.part_vec = p.row_vec < 128 ? p.row_vec : 128;     // 2 KB of a row per warp
-    p.parts = (p.row_vec + p.part_vec - 1) / p.part_vec;
+    // K and V of a part of a row: 2 KB of each per warp and token, or the row
+    p.row_lanes = 32;
+    while (p.row_lanes > 1 && p.row_lanes / 2 >= p.row_vec) p.row_lanes /= 2;
+    const int vec = p.row_vec > 64 ? 4 : (p.row_vec > 32 ? 2 : 1);
+    p.parts = (p.row_vec + p.row_lanes * vec - 1) / (p.row_lanes * vec);
     p.errors = dev->errors;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    // More CTAs per sequence while they find idle SMs and 4096 tokens each
+    // (GB300, 4 sequences of 32768 tokens: 45 us with one CTA each).
+    p.select_ctas = 1;
+    while (p.select_ctas < pkv::kEvictCluster &&
+           2LL * p.select_ctas * num_seqs <= dev->sm_count &&
+           p.cap_tokens >= 8192LL * p.select_ctas)
+        p.select_ctas *= 2;
     static unsigned long long select_mask = 0;
-    p.staged = p.cap_tokens < pkv::kEvictStaged ? p.cap_tokens : pkv::kEvictStaged;
+    const long long own = ((long long)p.cap_tokens + p.select_ctas - 1) / p.select_ctas + 1024;
+    p.staged = own < pkv::kEvictStaged ? (int)own : pkv::kEvictStaged;
     const size_t smem = (size_t)p.staged * sizeof(uint32_t);
     e = pkv::ensure_smem_limit(reinterpret_cast<const void*>(&pkv::evict_select_kernel),
                                &select_mask, smem);
     if (e != cudaSuccess) return cuda_fail(e);
-    pkv::evict_select_kernel<<<(unsigned)num_seqs, pkv::kEvictThreads, smem, cs>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e);
-    // 32 tokens per warp where that gives every SM 16 warps, fewer otherwise:
-    // a warp's tokens are copied one batch of loads after the other (64
-    // tokens of 1 KB rows on 16 warps took 23 us)
+    {
+        cudaLaunchConfig_t cfg;
+        std::memset(&cfg, 0, sizeof(cfg));
+        cudaLaunchAttribute attr[1];
+        cfg.gridDim = dim3((unsigned)(num_seqs * p.select_ctas));
+        cfg.blockDim = dim3(pkv::kEvictThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = cs;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)p.select_ctas;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = p.select_ctas > 1 ? 1 : 0;
+        if ((e = cudaLaunchKernelEx(&cfg, pkv::evict_select_kernel, p)) != cudaSuccess)
+            return cuda_fail(e);
+    }
+    // 32 tokens per warp, fewer while the warps that stay resident (3 CTAs
+    // per SM) get less than two units each: in a small batch short units
+    // spread over the SMs (64 tokens of 1 KB rows on 16 warps took 23 us, on
+    // 256 5 us) and even out the end of the launch (32768 rows of 2 KB: 46 us
+    // at 32, 40 at 4).
     const int warps = pkv::kEvictCopyThreads / 32;
-    const long long cap = 8LL * dev->sm_count;
+    const long long cap = 3LL * dev->sm_count;
     p.batch = 32;
-    auto count = [&] {
-        return (long long)num_seqs * ((keep + p.batch - 1) / p.batch) * 2 * p.parts;
-    };
-    while (p.batch > 1 && count() < 16LL * dev->sm_count) p.batch /= 2;
+    auto count = [&] { return (long long)num_seqs * ((keep + p.batch - 1) / p.batch) * p.parts; };
+    while (p.batch > 1 && count() < 2 * warps * cap) p.batch /= 2;
     long long ctas = (count() + warps - 1) / warps;
     if (ctas > cap) ctas = cap;
-    e = launch_dependent(pkv::evict_copy_kernel, dim3((unsigned)ctas), pkv::kEvictCopyThreads, 0,
-                         cs, p);
+    const dim3 grid((unsigned)ctas);
+    const int threads = pkv::kEvictCopyThreads;
+    e = vec == 4   ? launch_dependent(pkv::evict_copy_kernel<4>, grid, threads, 0, cs, p)
+        : vec == 2 ? launch_dependent(pkv::evict_copy_kernel<2>, grid, threads, 0, cs, p)
+                   : launch_dependent(pkv::evict_copy_kernel<1>, grid, threads, 0, cs, p);
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
 }
 
