@@ -6,7 +6,7 @@
 #include <cstring>
 
 #include "attn_host.h"
-#include "attn_tc_launch.h"
+#include "attn_prompt_launch.h"
 #include "capi_host.h"
 
 using namespace pkv::host;

@@ -1,5 +1,4 @@
 // attn_prompt_bf16.cu -- tcgen05 attention kernels of whole prompts for bf16.
 #define PKV_ELEM __nv_bfloat16
-#define PKV_PAGED false
 #define PKV_FN launch_attn_prompt_bf16
-#include "attn_tc_inst.inc"
+#include "attn_prompt_inst.inc"

@@ -1,5 +1,4 @@
 // attn_prompt_f16.cu -- tcgen05 attention kernels of whole prompts for f16.
 #define PKV_ELEM __half
-#define PKV_PAGED false
 #define PKV_FN launch_attn_prompt_f16
-#include "attn_tc_inst.inc"
+#include "attn_prompt_inst.inc"

@@ -1,4 +1,5 @@
-// attn_tc_launch.h -- host-side launch interface of attn_tc_kernel.cuh.
+// attn_prompt_launch.h -- host-side launch interface of attn_prompt_kernel
+// (attn_tc_kernel.cuh).
 #pragma once
 
 #include "attn_tc_kernel.cuh"
@@ -15,10 +16,8 @@ struct AttnLaunch {
     cudaStream_t stream;
 };
 
-// Launch attn_tc_kernel<D, T, paged, precise>.
+// Launch attn_prompt_kernel<D, T, precise>.
 cudaError_t launch_attn_prompt_bf16(int D, bool precise, const AttnLaunch& L);
 cudaError_t launch_attn_prompt_f16(int D, bool precise, const AttnLaunch& L);
-cudaError_t launch_attn_prefix_bf16(int D, bool precise, const AttnLaunch& L);
-cudaError_t launch_attn_prefix_f16(int D, bool precise, const AttnLaunch& L);
 
 }  // namespace pkv

@@ -96,10 +96,123 @@ struct AttnItem {
     int done;
 };
 
+// Sizes in shared and tensor memory.
+template <int D>
+struct AttnSizes {
+    static constexpr int HALVES = D / 64;
+    static constexpr uint32_t KV_HALF = kAtKeys * 128;        // [128 keys x 64 elements]
+    static constexpr uint32_t KV_BYTES = HALVES * KV_HALF;    // one slot: a K or a V tile
+    static constexpr uint32_t Q_HALF = kAtRows * 128;
+    static constexpr uint32_t Q_BYTES = HALVES * Q_HALF;
+    static constexpr uint32_t TMEM_COLS = 512;
+    static constexpr uint32_t TILE_COLS = 256;                // per row tile: O, then S / P
+    static constexpr uint32_t S_COL = D;
+    static_assert(D % 64 == 0 && D + kAtKeys <= TILE_COLS, "shape");
+};
+#define PKV_ATTN_SIZES(D)                                                                     \
+    [[maybe_unused]] constexpr int HALVES = AttnSizes<D>::HALVES;                             \
+    [[maybe_unused]] constexpr uint32_t KV_HALF = AttnSizes<D>::KV_HALF;                      \
+    [[maybe_unused]] constexpr uint32_t KV_BYTES = AttnSizes<D>::KV_BYTES;                    \
+    [[maybe_unused]] constexpr uint32_t Q_HALF = AttnSizes<D>::Q_HALF;                        \
+    [[maybe_unused]] constexpr uint32_t Q_BYTES = AttnSizes<D>::Q_BYTES;                      \
+    [[maybe_unused]] constexpr uint32_t TILE_COLS = AttnSizes<D>::TILE_COLS;                  \
+    [[maybe_unused]] constexpr uint32_t S_COL = AttnSizes<D>::S_COL;
+
+// Barriers and item slots of one CTA, behind the tiles in shared memory.
+struct AttnControl {
+    uint64_t* bars;
+    uint64_t* kv_full;      // [stages]
+    uint64_t* kv_free;      // [stages]
+    uint64_t* land;         // a V tile to clear rows of has landed
+    uint64_t* q_full;       // [tile]
+    uint64_t* q_free;
+    uint64_t* s_full;
+    uint64_t* p_full;       // [tile][half of the keys]
+    uint64_t* o_full;
+    uint64_t* o_free;
+    uint64_t* it_full;      // [kAtItems]
+    uint64_t* it_free;
+    uint64_t* fin;
+    AttnItem* items;
+    unsigned char* sQ;
+    unsigned char* sKV;
+    uint32_t tmem;
+    int stages;
+};
+
+__host__ __device__ constexpr int attn_bars(int stages) { return 2 * stages + 1 + 4 + 2 + 4 + 4 + 2 * kAtItems + 1; }
+
+// Bytes behind the tiles: barriers, then item slots.
+inline __host__ __device__ size_t attn_control_bytes(int stages) {
+    return (size_t)attn_bars(stages) * sizeof(uint64_t) + kAtItems * sizeof(AttnItem);
+}
+
+template <int D>
+__device__ __forceinline__ AttnControl attn_control(unsigned char* tiles, unsigned char* control,
+                                                    int stages) {
+    AttnControl c;
+    c.stages = stages;
+    c.sQ = tiles;
+    c.sKV = tiles + 2 * AttnSizes<D>::Q_BYTES;
+    c.bars = reinterpret_cast<uint64_t*>(control);
+    c.kv_full = c.bars;
+    c.kv_free = c.kv_full + stages;
+    c.land = c.kv_free + stages;
+    c.q_full = c.land + 1;
+    c.q_free = c.q_full + 2;
+    c.s_full = c.q_free + 2;
+    c.p_full = c.s_full + 2;
+    c.o_full = c.p_full + 4;
+    c.o_free = c.o_full + 2;
+    c.it_full = c.o_free + 2;
+    c.it_free = c.it_full + kAtItems;
+    c.fin = c.it_free + kAtItems;
+    c.items = reinterpret_cast<AttnItem*>(c.fin + 1);
+    c.tmem = 0;
+    return c;
+}
+
+// By one thread; the CTA's barrier orders it before the first use.
+__device__ __forceinline__ void attn_init_barriers(const AttnControl& c) {
+    for (int i = 0; i < c.stages; ++i) {
+        mbar_init(&c.kv_full[i], 1);
+        mbar_init(&c.kv_free[i], 1);
+    }
+    mbar_init(c.land, 1);
+    for (int t = 0; t < 2; ++t) {
+        mbar_init(&c.q_full[t], 1);
+        mbar_init(&c.q_free[t], 1);
+        mbar_init(&c.s_full[t], 1);
+        mbar_init(&c.p_full[2 * t], 4);
+        mbar_init(&c.p_full[2 * t + 1], 4);
+        mbar_init(&c.o_full[t], 1);
+        mbar_init(&c.o_free[t], 4);
+    }
+    for (int i = 0; i < kAtItems; ++i) {
+        mbar_init(&c.it_full[i], 1);
+        mbar_init(&c.it_free[i], 10);
+    }
+    mbar_init(c.fin, 1);
+    fence_barrier_init();
+}
+
+__device__ __forceinline__ void attn_tmem_alloc(int* s_tmem) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(s_tmem)),
+                 "r"(AttnSizes<64>::TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void attn_tmem_free(uint32_t tmem) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(AttnSizes<64>::TMEM_COLS)
+                 : "memory");
+}
+
+// Dynamic shared memory of attn_prompt_kernel.
 inline size_t attn_tc_smem_bytes(int D, int stages) {
-    return 1024 + (size_t)2 * kAtRows * D * 2 + (size_t)stages * kAtKeys * D * 2 +
-           (size_t)(2 * stages + 1 + 4 + 2 + 4 + 2 + 2 + 2 * kAtItems + 2) * sizeof(uint64_t) +
-           kAtItems * sizeof(AttnItem) + 32;
+    return 1024 + (size_t)2 * kAtRows * D * 2 + (size_t)stages * kAtKeys * D * 2 + 32 +
+           attn_control_bytes(stages);
 }
 
 // The largest of three in one instruction (fmaxf's treatment of NaN).
@@ -171,697 +284,612 @@ __device__ __forceinline__ void at_commit(uint64_t* bar, uint32_t lead) {
         : "memory");
 }
 
-template <int D, typename T, bool PAGED, bool PRECISE>
-__global__ void __launch_bounds__(kAtThreads, 1)
-    attn_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
-                   const __grid_constant__ CUtensorMap tm_k,
-                   const __grid_constant__ CUtensorMap tm_v,
-                   const __grid_constant__ AttnParams p) {
-    constexpr int HALVES = D / 64;
-    constexpr uint32_t KV_HALF = kAtKeys * 128;         // [128 keys x 64 elements]
-    constexpr uint32_t KV_BYTES = HALVES * KV_HALF;     // one slot: a K or a V tile
-    constexpr uint32_t Q_HALF = kAtRows * 128;
-    constexpr uint32_t Q_BYTES = HALVES * Q_HALF;
-    constexpr uint32_t TMEM_COLS = 512;
-    constexpr uint32_t TILE_COLS = 256;                 // per row tile: O, then S / P
-    constexpr uint32_t S_COL = D;
-    static_assert(D % 64 == 0 && D + kAtKeys <= TILE_COLS, "shape");
+// Warp 9: queries, K and V by TMA.
+template <int D, bool PAGED>
+__device__ __forceinline__ void attn_loader(const AttnControl& ctl, const AttnParams& p,
+                                            const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                                            const CUtensorMap& tm_v, int lane) {
+    PKV_ATTN_SIZES(D)
+    const int G = p.group;
+    const int QT = kAtRows / G;
+    if (lane == 0) {
+        prefetch_tensormap(&tm_q);
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
+    }
+    const uint64_t keep = l2_policy_evict_normal();   // other row tiles re-read K and V
+    const uint64_t once = l2_policy_evict_first();
+    int slot = 0, sph = 0;          // item ring
+    int st = 0, round = 0;          // K/V ring
+    uint32_t q_uses[2] = {0, 0};
+    uint32_t land_ph = 0;
+    bool ok = true;
+    const int per_tile = PAGED ? kAtKeys / p.block_size : 0;
 
-    if (PAGED) launch_dependents();
+    auto next_slot = [&]() {
+        if (++st == ctl.stages) {
+            st = 0;
+            ++round;
+        }
+    };
+    while (ok) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&ctl.it_full[slot], sph, p.errors));
+        if (!ok) break;
+        const AttnItem it = ctl.items[slot];
+        if (it.done) break;
+        const bool bad = PAGED && it.split < 0;
+        const int n_tiles = bad ? 0 : max(it.nt[0], it.nt[1]);
+        const int* table = PAGED ? p.block_tables + (size_t)it.key_row * p.max_blocks_per_seq +
+                                       it.key0 / p.block_size
+                                 : nullptr;
+        // pages of key tile j (lane k: page k of the tile)
+        auto page_id = [&](int j) -> int {
+            const int page = j * per_tile + lane;
+            return lane < per_tile && page * p.block_size < it.n_keys ? table[page] : -1;
+        };
+        int id = PAGED && n_tiles ? page_id(0) : 0;
+        for (int j = 0; ok && j < n_tiles; ++j) {
+            const int id_next = PAGED && j + 1 < n_tiles ? page_id(j + 1) : 0;
+#pragma unroll 1
+            for (int kv = 0; ok && kv < 2; ++kv) {
+                // K_0, then the queries, then V_0: the order of their use
+                if (kv == 1 && j == 0) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (it.nt[t] == 0) continue;
+                        if (q_uses[t] > 0)
+                            ok = ok && __all_sync(0xffffffffu,
+                                                  mbar_wait(&ctl.q_free[t], (q_uses[t] - 1) & 1,
+                                                            p.errors));
+                        ++q_uses[t];
+                        if (ok && lane == 0) {
+                            mbar_arrive_expect_tx(&ctl.q_full[t], Q_BYTES);
+#pragma unroll
+                            for (int h = 0; h < HALVES; ++h)
+                                tma_load_4d(ctl.sQ + t * Q_BYTES + h * Q_HALF, &tm_q, &ctl.q_full[t],
+                                            0, h, it.kvh * G, it.row0 + t * QT, once);
+                        }
+                    }
+                    if (!ok) break;
+                }
+                const bool w = round == 0 ||
+                               mbar_wait(&ctl.kv_free[st], (round - 1) & 1, p.errors);
+                ok = __all_sync(0xffffffffu, w);
+                if (!ok) break;
+                const bool clear = kv == 1 && (j + 1) * kAtKeys > it.n_keys;
+                uint64_t* bar = clear ? ctl.land : &ctl.kv_full[st];
+                unsigned char* dst = ctl.sKV + (size_t)st * KV_BYTES;
+                const CUtensorMap* tm = kv ? &tm_v : &tm_k;
+                if (!PAGED) {
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar, KV_BYTES);
+#pragma unroll
+                        for (int h = 0; h < HALVES; ++h)
+                            tma_load_4d(dst + h * KV_HALF, tm, bar, 0, h, it.kvh,
+                                        it.key_row + j * kAtKeys, keep);
+                    }
+                } else {
+                    const unsigned pages = __ballot_sync(0xffffffffu, id >= 0);
+                    const uint32_t page_bytes = HALVES * p.block_size * 128;
+                    if (lane == 0) mbar_arrive_expect_tx(bar, __popc(pages) * page_bytes);
+                    __syncwarp();
+                    if (id >= 0) {
+#pragma unroll
+                        for (int h = 0; h < HALVES; ++h)
+                            tma_load_4d(dst + h * KV_HALF + lane * p.block_size * 128, tm, bar,
+                                        0, it.kvh * HALVES + h, 0, id, keep);
+                    }
+                }
+                if (clear) {
+                    // rows past the last key: another sequence's, never
+                    // loaded, or past the tensor
+                    ok = __all_sync(0xffffffffu, mbar_wait(ctl.land, land_ph, p.errors));
+                    land_ph ^= 1u;
+                    if (!ok) break;
+                    const int from = it.n_keys - j * kAtKeys;
+                    for (int idx = from * 8 + lane; idx < kAtKeys * 8; idx += 32)
+#pragma unroll
+                        for (int h = 0; h < HALVES; ++h)
+                            *reinterpret_cast<uint4*>(dst + h * KV_HALF + idx * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl.kv_full[st]);
+                }
+                next_slot();
+            }
+            id = id_next;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.it_free[slot]);
+        if (++slot == kAtItems) {
+            slot = 0;
+            sph ^= 1;
+        }
+    }
+    if (!ok) {
+        // loads in flight land before the CTA may exit
+        const int issued = round * ctl.stages + st;
+        for (int k = max(0, issued - ctl.stages); k < issued; ++k)
+            mbar_wait(&ctl.kv_full[k % ctl.stages], (k / ctl.stages) & 1, p.errors);
+        for (int t = 0; t < 2; ++t)
+            if (q_uses[t]) mbar_wait(&ctl.q_full[t], (q_uses[t] - 1) & 1, p.errors);
+    }
+    __syncwarp();
+}
+
+// Warp 8: every MMA.
+template <int D, typename T, bool PAGED, bool PRECISE>
+__device__ __forceinline__ void attn_mma(const AttnControl& ctl, const AttnParams& p, int lane) {
+    PKV_ATTN_SIZES(D)
+    const uint32_t id_s = tc_idesc<T>(kAtRows, kAtKeys, 0);
+    const uint32_t id_o = tc_idesc<T>(kAtRows, D, 1);
+    const uint64_t dq0 = tc_desc_sw128(smem_addr(ctl.sQ), 16, 1024);
+    const uint64_t dk0 = tc_desc_sw128(smem_addr(ctl.sKV), 16, 1024);
+    const uint64_t dv0 = tc_desc_sw128(smem_addr(ctl.sKV), KV_HALF, 1024);
+    const uint32_t lead = elect_one() ? 1u : 0u;
+    int slot = 0, sph = 0;
+    int st = 0;                         // ring slot of the next tile to use
+    uint32_t ph = 0;
+    uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_o[2] = {0, 0};
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u, p.errors));
+    };
+    // S_t = Q_t K^T with K in slot ks; last: the item's last use of Q_t
+    auto issue_s = [&](int t, int ks, bool first, bool last) {
+        if (first) {
+            wait(&ctl.q_full[t], n_q[t]);
+            ++n_q[t];
+        }
+        if (!ok) return;
+        tc_fence_after();
+        {
+            const uint64_t q = dq0 + (uint64_t)((t * Q_BYTES) >> 4);
+            const uint64_t k = dk0 + (uint64_t)(ks * (KV_BYTES >> 4));
+            const uint32_t d = ctl.tmem + t * TILE_COLS + S_COL;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+                at_mma(d, q + (((i / 4) * Q_HALF + (i % 4) * 32) >> 4),
+                       k + (((i / 4) * KV_HALF + (i % 4) * 32) >> 4), id_s, i > 0 ? 1u : 0u, lead);
+            at_commit(&ctl.s_full[t], lead);
+            if (last) at_commit(&ctl.q_free[t], lead);
+        }
+        __syncwarp();
+    };
+    wait(&ctl.it_full[slot], sph);
+    AttnItem cur;
+    if (ok) cur = ctl.items[slot];
+    // ctl.items with a missing page have no products
+    auto skip_bad = [&]() {
+        while (PAGED && ok && !cur.done && cur.split < 0) {
+            if (lane == 0) mbar_arrive(&ctl.it_free[slot]);
+            if (++slot == kAtItems) {
+                slot = 0;
+                sph ^= 1;
+            }
+            wait(&ctl.it_full[slot], sph);
+            if (ok) cur = ctl.items[slot];
+        }
+    };
+    if (ok) skip_bad();
+    if (ok && !cur.done) {
+        wait(&ctl.kv_full[st], ph);
+        for (int t = 0; t < 2; ++t)
+            if (ok && cur.nt[t]) issue_s(t, st, true, cur.nt[t] == 1);
+        if (ok) at_commit(&ctl.kv_free[st], lead);
+        __syncwarp();
+        if (++st == ctl.stages) {
+            st = 0;
+            ph ^= 1u;
+        }
+    }
+    while (ok && !cur.done) {
+        const int nt0 = cur.nt[0], nt1 = cur.nt[1];
+        const int n_tiles = max(nt0, nt1);
+        for (int j = 0; ok && j < n_tiles; ++j) {
+            const bool last = j + 1 == n_tiles;
+            if (last) {
+                // this item's fields are no longer needed; look at the next
+                if (lane == 0) mbar_arrive(&ctl.it_free[slot]);
+                if (++slot == kAtItems) {
+                    slot = 0;
+                    sph ^= 1;
+                }
+                wait(&ctl.it_full[slot], sph);
+                if (ok) cur = ctl.items[slot];
+                if (ok) skip_bad();
+                if (!ok) break;
+            }
+            const int vs = st;
+            wait(&ctl.kv_full[vs], ph);
+            if (++st == ctl.stages) {
+                st = 0;
+                ph ^= 1u;
+            }
+            const int ks = st;
+            const bool have_k = !last || !cur.done;
+            bool k_seen = false;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int nt = t ? nt1 : nt0;
+                if (j < nt) {
+                    if (j == 0) {
+                        if (n_o[t] > 0) wait(&ctl.o_free[t], n_o[t] - 1);
+                        ++n_o[t];
+                    }
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        wait(&ctl.p_full[2 * t + half], n_p[t]);
+                        if (!ok) break;
+                        tc_fence_after();
+                        {
+                            const uint32_t o = ctl.tmem + t * TILE_COLS;
+                            const uint64_t v = dv0 + (uint64_t)(vs * (KV_BYTES >> 4));
+#pragma unroll
+                            for (int part = 0; part < (PRECISE ? 2 : 1); ++part)
+#pragma unroll
+                                for (int i = half * 4; i < half * 4 + 4; ++i)
+                                    at_mma_tmem_a(
+                                        o, o + S_COL + part * (kAtKeys / 2) + i * 8,
+                                        v + (uint64_t)((i * 16 * 128) >> 4), id_o,
+                                        (j > 0 || part > 0 || i > 0) ? 1u : 0u, lead);
+                            if (half && j + 1 == nt) at_commit(&ctl.o_full[t], lead);
+                        }
+                        __syncwarp();
+                    }
+                    ++n_p[t];
+                }
+                if (!ok) break;
+                const bool more = last ? !cur.done && cur.nt[t] > 0 : j + 1 < nt;
+                if (more) {
+                    if (!k_seen) {
+                        wait(&ctl.kv_full[ks], ph);
+                        k_seen = true;
+                    }
+                    if (ok)
+                        issue_s(t, ks, last, last ? cur.nt[t] == 1 : j + 2 == nt);
+                }
+            }
+            if (!ok) break;
+            at_commit(&ctl.kv_free[vs], lead);
+            if (have_k) at_commit(&ctl.kv_free[ks], lead);
+            __syncwarp();
+            if (have_k && ++st == ctl.stages) {
+                st = 0;
+                ph ^= 1u;
+            }
+        }
+    }
+    // every MMA complete before the tensor memory is released
+    at_commit(ctl.fin, lead);
+    __syncwarp();
+    mbar_wait(ctl.fin, 0, p.errors);
+    __syncwarp();
+}
+
+// Warps 0-7: thread r of group t owns row r of tile t.
+template <int D, typename T, bool PAGED, bool PRECISE>
+__device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnParams& p, int warp,
+                                             int lane) {
+    PKV_ATTN_SIZES(D)
+    const int G = p.group;
+    const int QT = kAtRows / G;
+    const int t = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t t_lane = ctl.tmem + t * TILE_COLS + ((uint32_t)((warp & 3) * 32) << 16);
+    const float sc = p.scale_log2;
+    const bool pos_sc = sc > 0.f;                     // the usual case
+    const float a = pos_sc ? sc : 1.f;                // exponent = y a - m
+    int slot = 0, sph = 0;
+    uint32_t n_s = 0, n_o = 0;
+    bool ok = true;
+    while (ok) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&ctl.it_full[slot], sph, p.errors));
+        if (!ok) break;
+        const AttnItem it = ctl.items[slot];
+        if (it.done) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.it_free[slot]);
+        if (++slot == kAtItems) {
+            slot = 0;
+            sph ^= 1;
+        }
+        const int tok = t * QT + r / G;                // within the item
+        const bool real = tok < it.rows;
+        const bool bad = PAGED && it.split < 0;
+        const int nt = it.nt[t];
+        // last key this row sees; rows of no token (never written) may see more
+        const int pos = PAGED ? it.n_keys - 1 : it.pos0 + tok;
+        const int warp_pos = PAGED ? pos : it.pos0 + t * QT + ((warp & 3) * 32) / G;
+        float m_used = -INFINITY;
+        float2 l4[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l4[i] = make_float2(0.f, 0.f);
+        if (nt > 0 && !bad) {
+            for (int j = 0; j < nt; ++j) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&ctl.s_full[t], n_s & 1u, p.errors));
+                if (!ok) break;
+                ++n_s;
+                tc_fence_after();
+                float y[kAtKeys];
+                uint32_t* yr = reinterpret_cast<uint32_t*>(y);
+                tc_ld32(t_lane + S_COL, yr);
+                tc_ld32(t_lane + S_COL + 32, yr + 32);
+                tc_ld32(t_lane + S_COL + 64, yr + 64);
+                tc_ld32(t_lane + S_COL + 96, yr + 96);
+                tc_wait_ld();
+                if (!pos_sc) {
+#pragma unroll
+                    for (int c = 0; c < kAtKeys; ++c) y[c] *= sc;
+                }
+                if (j * kAtKeys + kAtKeys - 1 > warp_pos) {
+                    // keys that rows of this warp may not see
+                    const int lim = pos - j * kAtKeys;
+#pragma unroll
+                    for (int c = 0; c < kAtKeys; ++c) y[c] = c <= lim ? y[c] : -INFINITY;
+                }
+                float m8[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) m8[e] = fmaxf(y[e], y[8 + e]);
+#pragma unroll
+                for (int c = 16; c < kAtKeys; c += 16)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) m8[e] = max3(m8[e], y[c + e], y[c + 8 + e]);
+                const float mx = max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]),
+                                      fmaxf(m8[6], m8[7]));
+                const float tmax = mx * a;
+                const bool first = m_used == -INFINITY;
+                const bool grow = tmax > m_used + kTcRescale;
+                float alpha = 1.f;
+                if (grow) {
+                    alpha = first ? 1.f : exp2f(m_used - tmax);
+                    m_used = tmax;
+                }
+                if (__any_sync(0xffffffffu, grow && !first)) {
+                    // O is at rest: the products up to key tile j - 1
+                    // completed before S_j did
+                    const float2 a2 = make_float2(alpha, alpha);
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t ov[32];
+                        tc_ld32(t_lane + c0, ov);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) {
+                            const float2 v = __fmul2_rn(
+                                make_float2(__uint_as_float(ov[c]), __uint_as_float(ov[c + 1])),
+                                a2);
+                            ov[c] = __float_as_uint(v.x);
+                            ov[c + 1] = __float_as_uint(v.y);
+                        }
+                        tc_st32(t_lane + c0, ov);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) l4[i] = __fmul2_rn(l4[i], a2);
+                }
+                const float mu = m_used == -INFINITY ? 0.f : m_used;
+                const float2 aa = make_float2(a, a), nmu = make_float2(-mu, -mu);
+                const float2 neg1 = make_float2(-1.f, -1.f);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t hi[32], lo[PRECISE ? 32 : 1];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const int c = half * 64 + 2 * i;
+                        const float2 e = __ffma2_rn(make_float2(y[c], y[c + 1]), aa, nmu);
+                        const float2 pv = make_float2(exp2f(e.x), exp2f(e.y));
+                        l4[i & 3] = __fadd2_rn(l4[i & 3], pv);
+                        hi[i] = pack2<T>(pv.x, pv.y);
+                        if (PRECISE) {
+                            const float2 rest = __ffma2_rn(unpack2<T>(hi[i]), neg1, pv);
+                            lo[PRECISE ? i : 0] = pack2<T>(rest.x, rest.y);
+                        }
+                    }
+                    tc_st32(t_lane + S_COL + half * 32, hi);
+                    if (PRECISE) tc_st32(t_lane + S_COL + 64 + half * 32, lo);
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl.p_full[2 * t + half]);
+                }
+            }
+            if (!ok) break;
+            ok = __all_sync(0xffffffffu, mbar_wait(&ctl.o_full[t], n_o & 1u, p.errors));
+            if (!ok) break;
+            ++n_o;
+            tc_fence_after();
+        }
+        if (nt > 0) {
+            const float2 la = __fadd2_rn(l4[0], l4[1]), lb = __fadd2_rn(l4[2], l4[3]);
+            const float l = (la.x + lb.x) + (la.y + lb.y);
+            const float inv = l != 0.f ? 1.f / l : 0.f;
+            const int qh = it.kvh * G + r % G;
+            const size_t row = (size_t)(it.row0 + tok) * p.n_heads + qh;
+            const size_t unit = PAGED ? row * p.max_splits + (bad ? -1 - it.split : it.split)
+                                      : row;
+            if (PAGED && real) 
+                *reinterpret_cast<float2*>(p.pre_ml + unit * 2) = make_float2(m_used, l);
+            if (!bad) {
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t ov[32];
+                    tc_ld32(t_lane + c0, ov);
+                    tc_wait_ld();
+                    if (!real) continue;
+                    const size_t e = unit * D + c0;
+                    if (PAGED || p.out_dtype == PKV_F32) {
+                        float4* o4 = reinterpret_cast<float4*>(
+                            (PAGED ? p.pre_o : reinterpret_cast<float*>(p.out)) + e);
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4)
+                            o4[c / 4] = make_float4(__uint_as_float(ov[c]) * inv,
+                                                    __uint_as_float(ov[c + 1]) * inv,
+                                                    __uint_as_float(ov[c + 2]) * inv,
+                                                    __uint_as_float(ov[c + 3]) * inv);
+                    } else {
+                        uint4* o4 =
+                            reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + e);
+#pragma unroll
+                        for (int c = 0; c < 32; c += 8)
+                            o4[c / 8] = make_uint4(
+                                pack_out(__uint_as_float(ov[c]) * inv,
+                                         __uint_as_float(ov[c + 1]) * inv, p.out_dtype),
+                                pack_out(__uint_as_float(ov[c + 2]) * inv,
+                                         __uint_as_float(ov[c + 3]) * inv, p.out_dtype),
+                                pack_out(__uint_as_float(ov[c + 4]) * inv,
+                                         __uint_as_float(ov[c + 5]) * inv, p.out_dtype),
+                                pack_out(__uint_as_float(ov[c + 6]) * inv,
+                                         __uint_as_float(ov[c + 7]) * inv, p.out_dtype));
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.o_free[t]);
+            } else if (real) {
+                float4* o4 = reinterpret_cast<float4*>(p.pre_o + unit * D);
+                for (int c = 0; c < D / 4; ++c) o4[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        }
+    }
+
+}
+
+// The work item i of a launch over whole prompts; false: it is empty.  The
+// last pair of tiles of every sequence comes first.
+__device__ __forceinline__ bool attn_prompt_item(const AttnParams& p, long long i, AttnItem& it) {
+    const int G = p.group, QT = kAtRows / G;
+    const long long per_tile = (long long)p.n_kv_heads * p.num_seqs;
+    const int back = (int)(i / per_tile);
+    const int x = (int)(i % per_tile);
+    const int s = x / p.n_kv_heads;
+    it.done = 0;
+    it.kvh = x % p.n_kv_heads;
+    const int q0 = p.q_start[s], q1 = p.q_start[s + 1];
+    const int len = q1 - q0;
+    if (q0 < 0 || len < 0 || q1 > p.total_q || len > p.max_len) {
+        if (back == 0 && it.kvh == 0) raise_error(p.errors, PKV_DEVERR_CONTEXT);
+        return false;
+    }
+    const int lo = ((len + 2 * QT - 1) / (2 * QT) - 1 - back) * 2 * QT;
+    if (lo < 0 || len == 0) return false;
+    it.row0 = q0 + lo;
+    it.rows = len - lo;
+    it.pos0 = lo;
+    it.key_row = q0;
+    it.key0 = 0;
+    it.n_keys = len;
+    it.split = 0;
+    it.nt[0] = (min(len, lo + QT) + kAtKeys - 1) / kAtKeys;
+    it.nt[1] = lo + QT < len ? (min(len, lo + 2 * QT) + kAtKeys - 1) / kAtKeys : 0;
+    return true;
+}
+
+// Whole prompts.  With `dynamic` there is a CTA for every item: a running one
+// takes its own item, then, one after the other, those of CTAs that have not
+// started yet.  Otherwise CTA c takes items c, c + grid, ...
+template <int D, typename T, bool PRECISE>
+__global__ void __launch_bounds__(kAtThreads, 1)
+    attn_prompt_kernel(const __grid_constant__ CUtensorMap tm_q,
+                       const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v,
+                       const __grid_constant__ AttnParams p) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     unsigned char* sm = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
-    unsigned char* sQ = sm;
-    unsigned char* sKV = sQ + 2 * Q_BYTES;
-    const int NS = p.stages;
-    uint64_t* kv_full = reinterpret_cast<uint64_t*>(sKV + (size_t)NS * KV_BYTES + 16);
-    uint64_t* kv_free = kv_full + NS;
-    uint64_t* land = kv_free + NS;           // a V tile to clear rows of has landed
-    uint64_t* q_full = land + 1;             // [tile]
-    uint64_t* q_free = q_full + 2;
-    uint64_t* s_full = q_free + 2;
-    uint64_t* p_full = s_full + 2;           // [tile][half of the keys]
-    uint64_t* o_full = p_full + 4;
-    uint64_t* o_free = o_full + 2;
-    uint64_t* it_full = o_free + 2;          // [kAtItems]
-    uint64_t* it_free = it_full + kAtItems;
-    uint64_t* fin = it_free + kAtItems;
-    uint64_t* steal_bar = fin + 1;           // a request for another CTA's item
-    AttnItem* items = reinterpret_cast<AttnItem*>(steal_bar + 1);
-    int* s_tmem = reinterpret_cast<int*>(items + kAtItems);
-    uint4* steal = reinterpret_cast<uint4*>(sm + 2 * Q_BYTES + (size_t)NS * KV_BYTES);
+    unsigned char* control =
+        sm + 2 * AttnSizes<D>::Q_BYTES + (size_t)p.stages * AttnSizes<D>::KV_BYTES;
+    uint4* steal = reinterpret_cast<uint4*>(control);
+    uint64_t* steal_bar = reinterpret_cast<uint64_t*>(control + 16);
+    int* s_tmem = reinterpret_cast<int*>(control + 24);
+    AttnControl c = attn_control<D>(sm, control + 32, p.stages);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int G = p.group;
-    const int QT = kAtRows / G;              // tokens per row tile
 
-    if (warp == 8) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_addr(s_tmem)),
-                     "r"(TMEM_COLS)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
+    if (warp == 8) attn_tmem_alloc(s_tmem);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(&kv_full[i], 1);
-            mbar_init(&kv_free[i], 1);
-        }
-        mbar_init(land, 1);
-        for (int t = 0; t < 2; ++t) {
-            mbar_init(&q_full[t], 1);
-            mbar_init(&q_free[t], 1);
-            mbar_init(&s_full[t], 1);
-            mbar_init(&p_full[2 * t], 4);
-            mbar_init(&p_full[2 * t + 1], 4);
-            mbar_init(&o_full[t], 1);
-            mbar_init(&o_free[t], 4);
-        }
-        for (int i = 0; i < kAtItems; ++i) {
-            mbar_init(&it_full[i], 1);
-            mbar_init(&it_free[i], 10);
-        }
-        mbar_init(fin, 1);
+        attn_init_barriers(c);
         mbar_init(steal_bar, 1);
         fence_barrier_init();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = (uint32_t)*s_tmem;
+    c.tmem = (uint32_t)*s_tmem;
 
     if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtOtherRegs));
-    if (warp == 10) {
-        // ================= scheduler: the items of this CTA =================
-        // CTA c takes items c, c + grid, ...; lanes look at 32 of them at once.
-        // With `dynamic` there is a CTA for every item: this one takes its own,
-        // then, one after the other, those of CTAs that have not started yet.
-        const long long per_tile =
-            (long long)p.n_kv_heads *
-            (PAGED ? p.num_groups * (long long)p.max_splits : p.num_seqs);
-        const bool dynamic = !PAGED && p.dynamic != 0;
-        const long long stride = dynamic ? p.n_items : gridDim.x;
-        uint32_t steal_ph = 0;
-        int slot = 0, round = 0;
-        bool ok = true;
-        for (long long base = blockIdx.x; ok;) {
-            const long long i = base + (long long)lane * stride;
-            AttnItem it;
-            bool have = false;
-            it.done = 0;
-            if (i < p.n_items) {
-                if (!PAGED) {
-                    // the last pair of tiles of every sequence comes first
-                    const int back = (int)(i / per_tile);
-                    const int x = (int)(i % per_tile);
-                    const int s = x / p.n_kv_heads;
-                    it.kvh = x % p.n_kv_heads;
-                    const int q0 = p.q_start[s], q1 = p.q_start[s + 1];
-                    const int len = q1 - q0;
-                    const int lo = ((len + 2 * QT - 1) / (2 * QT) - 1 - back) * 2 * QT;
-                    if (q0 < 0 || len < 0 || q1 > p.total_q || len > p.max_len) {
-                        if (back == 0 && it.kvh == 0) raise_error(p.errors, PKV_DEVERR_CONTEXT);
-                    } else if (lo >= 0 && len > 0) {
-                        have = true;
-                        it.row0 = q0 + lo;
-                        it.rows = len - lo;
-                        it.pos0 = lo;
-                        it.key_row = q0;
-                        it.key0 = 0;
-                        it.n_keys = len;
-                        it.split = 0;
-                        it.nt[0] = (min(len, lo + QT) + kAtKeys - 1) / kAtKeys;
-                        it.nt[1] = lo + QT < len
-                                       ? (min(len, lo + 2 * QT) + kAtKeys - 1) / kAtKeys
-                                       : 0;
-                    }
-                } else {
-                    // (the row tiles of a split fastest: they share its keys)
-                    const int tile = (int)(i % p.tiles);
-                    long long x = i / p.tiles;
-                    const int split = (int)(x % p.max_splits);
-                    x /= p.max_splits;
-                    it.kvh = (int)(x % p.n_kv_heads);
-                    const int g = (int)(x / p.n_kv_heads);
-                    const int g0 = p.group_start[g], g1 = p.group_start[g + 1];
-                    const int pl = p.prefix_lens[g];
-                    const bool valid = g0 >= 0 && g1 >= g0 && g1 <= p.num_seqs &&
-                                       g1 - g0 <= p.max_group && pl >= 0 &&
-                                       pl <= p.max_prefix && pl % p.block_size == 0;
-                    const int lo = tile * 2 * QT;
-                    if (!valid) {
-                        if (tile == 0 && split == 0 && it.kvh == 0)
-                            raise_error(p.errors, PKV_DEVERR_CONTEXT);
-                    } else if (g0 + lo < g1 && split * p.split_tokens < pl) {
-                        // the prefix is read through the table of the first
-                        // member that holds all of it
-                        int m = g0;
-                        while (m < g1 && min(p.context_lens[m], p.cap_tokens) < pl) ++m;
-                        if (m < g1) {
-                            have = true;
-                            it.row0 = g0 + lo;
-                            it.rows = g1 - g0 - lo;
-                            it.pos0 = 0;
-                            it.key_row = m;
-                            it.key0 = split * p.split_tokens;
-                            it.n_keys = min(p.split_tokens, pl - it.key0);
-                            it.split = split;
-                            const int nt = (it.n_keys + kAtKeys - 1) / kAtKeys;
-                            it.nt[0] = nt;
-                            it.nt[1] = lo + QT < g1 - g0 ? nt : 0;
-                            const int* row = p.block_tables + (size_t)m * p.max_blocks_per_seq +
-                                             it.key0 / p.block_size;
-                            const int pages = (it.n_keys + p.block_size - 1) / p.block_size;
-                            bool bad = false;
-#pragma unroll 8
-                            for (int k = 0; k < pages; ++k)
-                                bad |= (unsigned)row[k] >= (unsigned)p.num_blocks;
-                            if (bad) {
-                                raise_error(p.errors, PKV_DEVERR_BLOCK_ID);
-                                it.split = -1 - split;
-                            }
-                        }
-                    }
-                }
-            }
-            unsigned todo = __ballot_sync(0xffffffffu, have);
-            bool more;
-            if (dynamic) {
-                // place the item, and ask for another one only when there is
-                // a slot for it: what waits here cannot go to an idle SM
-                if (todo) {
-                    ok = round == 0 ||
-                         __all_sync(0xffffffffu, mbar_wait(&it_free[slot], (round - 1) & 1, p.errors));
-                    if (!ok) break;
-                    if (lane == 0) {
-                        items[slot] = it;
-                        mbar_arrive(&it_full[slot]);
-                    }
-                    if (++slot == kAtItems) {
-                        slot = 0;
-                        ++round;
-                    }
-                    todo = 0;
-                }
-                ok = round == 0 ||
-                     __all_sync(0xffffffffu, mbar_wait(&it_free[slot], (round - 1) & 1, p.errors));
-                if (!ok) break;
-                if (lane == 0) steal_cta(steal, steal_bar);
-                ok = __all_sync(0xffffffffu, mbar_wait(steal_bar, steal_ph, p.errors));
-                steal_ph ^= 1u;
-                if (!ok) break;
-                const int next = stolen_cta(steal);
-                __syncwarp();
-                more = next >= 0;
-                if (more) base = next;
-            } else {
-                base += 32ll * stride;
-                more = base < p.n_items;
-            }
-            while (ok && (todo || !more)) {
-                const bool w = round == 0 || mbar_wait(&it_free[slot], (round - 1) & 1, p.errors);
-                ok = __all_sync(0xffffffffu, w);
-                if (!ok) break;
-                const int src = todo ? __ffs(todo) - 1 : 0;
-                if (lane == src) {
-                    if (!todo) it.done = 1;
-                    items[slot] = it;
-                    mbar_arrive(&it_full[slot]);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtOtherRegs));
+        if (warp == 8) {
+            attn_mma<D, T, false, PRECISE>(c, p, lane);
+        } else if (warp == 9) {
+            attn_loader<D, false>(c, p, tm_q, tm_k, tm_v, lane);
+        } else if (warp == 10) {
+            // ---- scheduler; lanes look at 32 items at once
+            const bool dynamic = p.dynamic != 0;
+            const long long stride = dynamic ? p.n_items : gridDim.x;
+            uint32_t steal_ph = 0;
+            int slot = 0, round = 0;
+            bool ok = true;
+            auto slot_free = [&]() {
+                return round == 0 ||
+                       __all_sync(0xffffffffu,
+                                  mbar_wait(&c.it_free[slot], (round - 1) & 1, p.errors));
+            };
+            auto put = [&](const AttnItem& it, bool mine) {
+                if (mine) {
+                    c.items[slot] = it;
+                    mbar_arrive(&c.it_full[slot]);
                 }
                 if (++slot == kAtItems) {
                     slot = 0;
                     ++round;
                 }
-                if (!todo) {
-                    ok = false;          // the end mark is out
+            };
+            for (long long base = blockIdx.x; ok;) {
+                const long long i = base + (long long)lane * stride;
+                AttnItem it;
+                const bool have = i < p.n_items && attn_prompt_item(p, i, it);
+                unsigned todo = __ballot_sync(0xffffffffu, have);
+                while (todo && (ok = slot_free())) {
+                    put(it, lane == __ffs(todo) - 1);
+                    todo &= todo - 1;
+                }
+                if (!ok) break;
+                bool more;
+                if (dynamic) {
+                    // ask for another item only when there is a slot for it:
+                    // what waits here cannot go to an idle SM
+                    if (!(ok = slot_free())) break;
+                    if (lane == 0) steal_cta(steal, steal_bar);
+                    ok = __all_sync(0xffffffffu, mbar_wait(steal_bar, steal_ph, p.errors));
+                    steal_ph ^= 1u;
+                    if (!ok) break;
+                    const int next = stolen_cta(steal);
+                    __syncwarp();
+                    more = next >= 0;
+                    if (more) base = next;
+                } else {
+                    base += 32ll * stride;
+                    more = __any_sync(0xffffffffu, base < p.n_items);
+                }
+                if (!more) {
+                    if (slot_free()) {
+                        it.done = 1;
+                        put(it, lane == 0);
+                    }
                     break;
                 }
-                todo &= todo - 1;
             }
         }
-    } else if (warp == 9) {
-        // ================= loader =================
-        if (lane == 0) {
-            prefetch_tensormap(&tm_q);
-            prefetch_tensormap(&tm_k);
-            prefetch_tensormap(&tm_v);
-        }
-        const uint64_t keep = l2_policy_evict_normal();   // other row tiles re-read K and V
-        const uint64_t once = l2_policy_evict_first();
-        int slot = 0, sph = 0;          // item ring
-        int st = 0, round = 0;          // K/V ring
-        uint32_t q_uses[2] = {0, 0};
-        uint32_t land_ph = 0;
-        bool ok = true;
-        const int per_tile = PAGED ? kAtKeys / p.block_size : 0;
-
-        auto next_slot = [&]() {
-            if (++st == NS) {
-                st = 0;
-                ++round;
-            }
-        };
-        while (ok) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&it_full[slot], sph, p.errors));
-            if (!ok) break;
-            const AttnItem it = items[slot];
-            if (it.done) break;
-            const bool bad = PAGED && it.split < 0;
-            const int n_tiles = bad ? 0 : max(it.nt[0], it.nt[1]);
-            const int* table = PAGED ? p.block_tables + (size_t)it.key_row * p.max_blocks_per_seq +
-                                           it.key0 / p.block_size
-                                     : nullptr;
-            // pages of key tile j (lane k: page k of the tile)
-            auto page_id = [&](int j) -> int {
-                const int page = j * per_tile + lane;
-                return lane < per_tile && page * p.block_size < it.n_keys ? table[page] : -1;
-            };
-            int id = PAGED && n_tiles ? page_id(0) : 0;
-            for (int j = 0; ok && j < n_tiles; ++j) {
-                const int id_next = PAGED && j + 1 < n_tiles ? page_id(j + 1) : 0;
-#pragma unroll 1
-                for (int kv = 0; ok && kv < 2; ++kv) {
-                    // K_0, then the queries, then V_0: the order of their use
-                    if (kv == 1 && j == 0) {
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            if (it.nt[t] == 0) continue;
-                            if (q_uses[t] > 0)
-                                ok = ok && __all_sync(0xffffffffu,
-                                                      mbar_wait(&q_free[t], (q_uses[t] - 1) & 1,
-                                                                p.errors));
-                            ++q_uses[t];
-                            if (ok && lane == 0) {
-                                mbar_arrive_expect_tx(&q_full[t], Q_BYTES);
-#pragma unroll
-                                for (int h = 0; h < HALVES; ++h)
-                                    tma_load_4d(sQ + t * Q_BYTES + h * Q_HALF, &tm_q, &q_full[t],
-                                                0, h, it.kvh * G, it.row0 + t * QT, once);
-                            }
-                        }
-                        if (!ok) break;
-                    }
-                    const bool w = round == 0 ||
-                                   mbar_wait(&kv_free[st], (round - 1) & 1, p.errors);
-                    ok = __all_sync(0xffffffffu, w);
-                    if (!ok) break;
-                    const bool clear = kv == 1 && (j + 1) * kAtKeys > it.n_keys;
-                    uint64_t* bar = clear ? land : &kv_full[st];
-                    unsigned char* dst = sKV + (size_t)st * KV_BYTES;
-                    const CUtensorMap* tm = kv ? &tm_v : &tm_k;
-                    if (!PAGED) {
-                        if (lane == 0) {
-                            mbar_arrive_expect_tx(bar, KV_BYTES);
-#pragma unroll
-                            for (int h = 0; h < HALVES; ++h)
-                                tma_load_4d(dst + h * KV_HALF, tm, bar, 0, h, it.kvh,
-                                            it.key_row + j * kAtKeys, keep);
-                        }
-                    } else {
-                        const unsigned pages = __ballot_sync(0xffffffffu, id >= 0);
-                        const uint32_t page_bytes = HALVES * p.block_size * 128;
-                        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(pages) * page_bytes);
-                        __syncwarp();
-                        if (id >= 0) {
-#pragma unroll
-                            for (int h = 0; h < HALVES; ++h)
-                                tma_load_4d(dst + h * KV_HALF + lane * p.block_size * 128, tm, bar,
-                                            0, it.kvh * HALVES + h, 0, id, keep);
-                        }
-                    }
-                    if (clear) {
-                        // rows past the last key: another sequence's, never
-                        // loaded, or past the tensor
-                        ok = __all_sync(0xffffffffu, mbar_wait(land, land_ph, p.errors));
-                        land_ph ^= 1u;
-                        if (!ok) break;
-                        const int from = it.n_keys - j * kAtKeys;
-                        for (int idx = from * 8 + lane; idx < kAtKeys * 8; idx += 32)
-#pragma unroll
-                            for (int h = 0; h < HALVES; ++h)
-                                *reinterpret_cast<uint4*>(dst + h * KV_HALF + idx * 16) =
-                                    make_uint4(0u, 0u, 0u, 0u);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&kv_full[st]);
-                    }
-                    next_slot();
-                }
-                id = id_next;
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&it_free[slot]);
-            if (++slot == kAtItems) {
-                slot = 0;
-                sph ^= 1;
-            }
-        }
-        if (!ok) {
-            // loads in flight land before the CTA may exit
-            const int issued = round * NS + st;
-            for (int k = max(0, issued - NS); k < issued; ++k)
-                mbar_wait(&kv_full[k % NS], (k / NS) & 1, p.errors);
-            for (int t = 0; t < 2; ++t)
-                if (q_uses[t]) mbar_wait(&q_full[t], (q_uses[t] - 1) & 1, p.errors);
-        }
-        __syncwarp();
-    } else if (warp == 8) {
-        // ================= MMA issuer =================
-        const uint32_t id_s = tc_idesc<T>(kAtRows, kAtKeys, 0);
-        const uint32_t id_o = tc_idesc<T>(kAtRows, D, 1);
-        const uint64_t dq0 = tc_desc_sw128(smem_addr(sQ), 16, 1024);
-        const uint64_t dk0 = tc_desc_sw128(smem_addr(sKV), 16, 1024);
-        const uint64_t dv0 = tc_desc_sw128(smem_addr(sKV), KV_HALF, 1024);
-        const uint32_t lead = elect_one() ? 1u : 0u;
-        int slot = 0, sph = 0;
-        int st = 0;                         // ring slot of the next tile to use
-        uint32_t ph = 0;
-        uint32_t n_q[2] = {0, 0}, n_p[2] = {0, 0}, n_o[2] = {0, 0};
-        bool ok = true;
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u, p.errors));
-        };
-        // S_t = Q_t K^T with K in slot ks; last: the item's last use of Q_t
-        auto issue_s = [&](int t, int ks, bool first, bool last) {
-            if (first) {
-                wait(&q_full[t], n_q[t]);
-                ++n_q[t];
-            }
-            if (!ok) return;
-            tc_fence_after();
-            {
-                const uint64_t q = dq0 + (uint64_t)((t * Q_BYTES) >> 4);
-                const uint64_t k = dk0 + (uint64_t)(ks * (KV_BYTES >> 4));
-                const uint32_t d = tmem + t * TILE_COLS + S_COL;
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-                    at_mma(d, q + (((i / 4) * Q_HALF + (i % 4) * 32) >> 4),
-                           k + (((i / 4) * KV_HALF + (i % 4) * 32) >> 4), id_s, i > 0 ? 1u : 0u, lead);
-                at_commit(&s_full[t], lead);
-                if (last) at_commit(&q_free[t], lead);
-            }
-            __syncwarp();
-        };
-        wait(&it_full[slot], sph);
-        AttnItem cur;
-        if (ok) cur = items[slot];
-        // items with a missing page have no products
-        auto skip_bad = [&]() {
-            while (PAGED && ok && !cur.done && cur.split < 0) {
-                if (lane == 0) mbar_arrive(&it_free[slot]);
-                if (++slot == kAtItems) {
-                    slot = 0;
-                    sph ^= 1;
-                }
-                wait(&it_full[slot], sph);
-                if (ok) cur = items[slot];
-            }
-        };
-        if (ok) skip_bad();
-        if (ok && !cur.done) {
-            wait(&kv_full[st], ph);
-            for (int t = 0; t < 2; ++t)
-                if (ok && cur.nt[t]) issue_s(t, st, true, cur.nt[t] == 1);
-            if (ok) at_commit(&kv_free[st], lead);
-            __syncwarp();
-            if (++st == NS) {
-                st = 0;
-                ph ^= 1u;
-            }
-        }
-        while (ok && !cur.done) {
-            const int nt0 = cur.nt[0], nt1 = cur.nt[1];
-            const int n_tiles = max(nt0, nt1);
-            for (int j = 0; ok && j < n_tiles; ++j) {
-                const bool last = j + 1 == n_tiles;
-                if (last) {
-                    // this item's fields are no longer needed; look at the next
-                    if (lane == 0) mbar_arrive(&it_free[slot]);
-                    if (++slot == kAtItems) {
-                        slot = 0;
-                        sph ^= 1;
-                    }
-                    wait(&it_full[slot], sph);
-                    if (ok) cur = items[slot];
-                    if (ok) skip_bad();
-                    if (!ok) break;
-                }
-                const int vs = st;
-                wait(&kv_full[vs], ph);
-                if (++st == NS) {
-                    st = 0;
-                    ph ^= 1u;
-                }
-                const int ks = st;
-                const bool have_k = !last || !cur.done;
-                bool k_seen = false;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const int nt = t ? nt1 : nt0;
-                    if (j < nt) {
-                        if (j == 0) {
-                            if (n_o[t] > 0) wait(&o_free[t], n_o[t] - 1);
-                            ++n_o[t];
-                        }
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            wait(&p_full[2 * t + half], n_p[t]);
-                            if (!ok) break;
-                            tc_fence_after();
-                            {
-                                const uint32_t o = tmem + t * TILE_COLS;
-                                const uint64_t v = dv0 + (uint64_t)(vs * (KV_BYTES >> 4));
-#pragma unroll
-                                for (int part = 0; part < (PRECISE ? 2 : 1); ++part)
-#pragma unroll
-                                    for (int i = half * 4; i < half * 4 + 4; ++i)
-                                        at_mma_tmem_a(
-                                            o, o + S_COL + part * (kAtKeys / 2) + i * 8,
-                                            v + (uint64_t)((i * 16 * 128) >> 4), id_o,
-                                            (j > 0 || part > 0 || i > 0) ? 1u : 0u, lead);
-                                if (half && j + 1 == nt) at_commit(&o_full[t], lead);
-                            }
-                            __syncwarp();
-                        }
-                        ++n_p[t];
-                    }
-                    if (!ok) break;
-                    const bool more = last ? !cur.done && cur.nt[t] > 0 : j + 1 < nt;
-                    if (more) {
-                        if (!k_seen) {
-                            wait(&kv_full[ks], ph);
-                            k_seen = true;
-                        }
-                        if (ok)
-                            issue_s(t, ks, last, last ? cur.nt[t] == 1 : j + 2 == nt);
-                    }
-                }
-                if (!ok) break;
-                at_commit(&kv_free[vs], lead);
-                if (have_k) at_commit(&kv_free[ks], lead);
-                __syncwarp();
-                if (have_k && ++st == NS) {
-                    st = 0;
-                    ph ^= 1u;
-                }
-            }
-        }
-        // every MMA complete before the tensor memory is released
-        at_commit(fin, lead);
-        __syncwarp();
-        mbar_wait(fin, 0, p.errors);
-        __syncwarp();
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAtSoftmaxRegs));
-        // ================= softmax: thread r of group t owns row r =================
-        const int t = warp >> 2;
-        const int r = (warp & 3) * 32 + lane;
-        const uint32_t t_lane = tmem + t * TILE_COLS + ((uint32_t)((warp & 3) * 32) << 16);
-        const float sc = p.scale_log2;
-        const bool pos_sc = sc > 0.f;                     // the usual case
-        const float a = pos_sc ? sc : 1.f;                // exponent = y a - m
-        int slot = 0, sph = 0;
-        uint32_t n_s = 0, n_o = 0;
-        bool ok = true;
-        while (ok) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&it_full[slot], sph, p.errors));
-            if (!ok) break;
-            const AttnItem it = items[slot];
-            if (it.done) break;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&it_free[slot]);
-            if (++slot == kAtItems) {
-                slot = 0;
-                sph ^= 1;
-            }
-            const int tok = t * QT + r / G;                // within the item
-            const bool real = tok < it.rows;
-            const bool bad = PAGED && it.split < 0;
-            const int nt = it.nt[t];
-            // last key this row sees; rows of no token (never written) may see more
-            const int pos = PAGED ? it.n_keys - 1 : it.pos0 + tok;
-            const int warp_pos = PAGED ? pos : it.pos0 + t * QT + ((warp & 3) * 32) / G;
-            float m_used = -INFINITY;
-            float2 l4[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) l4[i] = make_float2(0.f, 0.f);
-            if (nt > 0 && !bad) {
-                for (int j = 0; j < nt; ++j) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], n_s & 1u, p.errors));
-                    if (!ok) break;
-                    ++n_s;
-                    tc_fence_after();
-                    float y[kAtKeys];
-                    uint32_t* yr = reinterpret_cast<uint32_t*>(y);
-                    tc_ld32(t_lane + S_COL, yr);
-                    tc_ld32(t_lane + S_COL + 32, yr + 32);
-                    tc_ld32(t_lane + S_COL + 64, yr + 64);
-                    tc_ld32(t_lane + S_COL + 96, yr + 96);
-                    tc_wait_ld();
-                    if (!pos_sc) {
-#pragma unroll
-                        for (int c = 0; c < kAtKeys; ++c) y[c] *= sc;
-                    }
-                    if (j * kAtKeys + kAtKeys - 1 > warp_pos) {
-                        // keys that rows of this warp may not see
-                        const int lim = pos - j * kAtKeys;
-#pragma unroll
-                        for (int c = 0; c < kAtKeys; ++c) y[c] = c <= lim ? y[c] : -INFINITY;
-                    }
-                    float m8[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) m8[e] = fmaxf(y[e], y[8 + e]);
-#pragma unroll
-                    for (int c = 16; c < kAtKeys; c += 16)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) m8[e] = max3(m8[e], y[c + e], y[c + 8 + e]);
-                    const float mx = max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]),
-                                          fmaxf(m8[6], m8[7]));
-                    const float tmax = mx * a;
-                    const bool first = m_used == -INFINITY;
-                    const bool grow = tmax > m_used + kTcRescale;
-                    float alpha = 1.f;
-                    if (grow) {
-                        alpha = first ? 1.f : exp2f(m_used - tmax);
-                        m_used = tmax;
-                    }
-                    if (__any_sync(0xffffffffu, grow && !first)) {
-                        // O is at rest: the products up to key tile j - 1
-                        // completed before S_j did
-                        const float2 a2 = make_float2(alpha, alpha);
-#pragma unroll 1
-                        for (int c0 = 0; c0 < D; c0 += 32) {
-                            uint32_t ov[32];
-                            tc_ld32(t_lane + c0, ov);
-                            tc_wait_ld();
-#pragma unroll
-                            for (int c = 0; c < 32; c += 2) {
-                                const float2 v = __fmul2_rn(
-                                    make_float2(__uint_as_float(ov[c]), __uint_as_float(ov[c + 1])),
-                                    a2);
-                                ov[c] = __float_as_uint(v.x);
-                                ov[c + 1] = __float_as_uint(v.y);
-                            }
-                            tc_st32(t_lane + c0, ov);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) l4[i] = __fmul2_rn(l4[i], a2);
-                    }
-                    const float mu = m_used == -INFINITY ? 0.f : m_used;
-                    const float2 aa = make_float2(a, a), nmu = make_float2(-mu, -mu);
-                    const float2 neg1 = make_float2(-1.f, -1.f);
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t hi[32], lo[PRECISE ? 32 : 1];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int c = half * 64 + 2 * i;
-                            const float2 e = __ffma2_rn(make_float2(y[c], y[c + 1]), aa, nmu);
-                            const float2 pv = make_float2(exp2f(e.x), exp2f(e.y));
-                            l4[i & 3] = __fadd2_rn(l4[i & 3], pv);
-                            hi[i] = pack2<T>(pv.x, pv.y);
-                            if (PRECISE) {
-                                const float2 rest = __ffma2_rn(unpack2<T>(hi[i]), neg1, pv);
-                                lo[PRECISE ? i : 0] = pack2<T>(rest.x, rest.y);
-                            }
-                        }
-                        tc_st32(t_lane + S_COL + half * 32, hi);
-                        if (PRECISE) tc_st32(t_lane + S_COL + 64 + half * 32, lo);
-                        tc_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
-                    }
-                }
-                if (!ok) break;
-                ok = __all_sync(0xffffffffu, mbar_wait(&o_full[t], n_o & 1u, p.errors));
-                if (!ok) break;
-                ++n_o;
-                tc_fence_after();
-            }
-            if (nt > 0) {
-                const float2 la = __fadd2_rn(l4[0], l4[1]), lb = __fadd2_rn(l4[2], l4[3]);
-                const float l = (la.x + lb.x) + (la.y + lb.y);
-                const float inv = l != 0.f ? 1.f / l : 0.f;
-                const int qh = it.kvh * G + r % G;
-                const size_t row = (size_t)(it.row0 + tok) * p.n_heads + qh;
-                const size_t unit = PAGED ? row * p.max_splits + (bad ? -1 - it.split : it.split)
-                                          : row;
-                if (PAGED && real) 
-                    *reinterpret_cast<float2*>(p.pre_ml + unit * 2) = make_float2(m_used, l);
-                if (!bad) {
-#pragma unroll 1
-                    for (int c0 = 0; c0 < D; c0 += 32) {
-                        uint32_t ov[32];
-                        tc_ld32(t_lane + c0, ov);
-                        tc_wait_ld();
-                        if (!real) continue;
-                        const size_t e = unit * D + c0;
-                        if (PAGED || p.out_dtype == PKV_F32) {
-                            float4* o4 = reinterpret_cast<float4*>(
-                                (PAGED ? p.pre_o : reinterpret_cast<float*>(p.out)) + e);
-#pragma unroll
-                            for (int c = 0; c < 32; c += 4)
-                                o4[c / 4] = make_float4(__uint_as_float(ov[c]) * inv,
-                                                        __uint_as_float(ov[c + 1]) * inv,
-                                                        __uint_as_float(ov[c + 2]) * inv,
-                                                        __uint_as_float(ov[c + 3]) * inv);
-                        } else {
-                            uint4* o4 =
-                                reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + e);
-#pragma unroll
-                            for (int c = 0; c < 32; c += 8)
-                                o4[c / 8] = make_uint4(
-                                    pack_out(__uint_as_float(ov[c]) * inv,
-                                             __uint_as_float(ov[c + 1]) * inv, p.out_dtype),
-                                    pack_out(__uint_as_float(ov[c + 2]) * inv,
-                                             __uint_as_float(ov[c + 3]) * inv, p.out_dtype),
-                                    pack_out(__uint_as_float(ov[c + 4]) * inv,
-                                             __uint_as_float(ov[c + 5]) * inv, p.out_dtype),
-                                    pack_out(__uint_as_float(ov[c + 6]) * inv,
-                                             __uint_as_float(ov[c + 7]) * inv, p.out_dtype));
-                        }
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&o_free[t]);
-                } else if (real) {
-                    float4* o4 = reinterpret_cast<float4*>(p.pre_o + unit * D);
-                    for (int c = 0; c < D / 4; ++c) o4[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-                }
-            }
-        }
+        attn_softmax<D, T, false, PRECISE>(c, p, warp, lane);
     }
 
     // ---- tensor memory is released after every thread is done with it
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 8)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                     "r"(TMEM_COLS)
-                     : "memory");
+    if (warp == 8) attn_tmem_free(c.tmem);
 }
 
 }  // namespace pkv

@@ -9,7 +9,7 @@
 
 #include "capi_host.h"
 #include "decode_launch.h"
-#include "decode_pieces_launch.h"
+#include "decode_weights_launch.h"
 #include "evict_kernels.cuh"
 #include "pieces_host.h"
 
@@ -35,20 +35,19 @@ int pieces_stream_heads(int n_kv_heads) {
     return hw;
 }
 
-int pieces_ctas(int num_seqs, int n_kv_heads, int max_context_len, int sm_count) {
+int pieces_ctas(int num_seqs, int n_kv_heads, int max_context_len, int most) {
     const int hw = pieces_stream_heads(n_kv_heads);
     const long long chunks = (long long)num_seqs * (n_kv_heads / hw) *
                              (((long long)max_context_len + kPieceTokens - 1) / kPieceTokens);
     const long long streams = (chunks + kPieceMinRun - 1) / kPieceMinRun;
     const int per_cta = kPieceWarps / hw;
     const long long ctas = (streams + per_cta - 1) / per_cta;
-    return (int)(ctas < 1 ? 1 : (ctas < sm_count ? ctas : sm_count));
+    return (int)(ctas < 1 ? 1 : (ctas < most ? ctas : most));
 }
 
 PiecesWorkspace pieces_workspace(int num_seqs, int n_heads, int n_kv_heads, int head_dim,
-                                 int max_context_len, int sm_count) {
+                                 int ctas) {
     PiecesWorkspace w;
-    const int ctas = pieces_ctas(num_seqs, n_kv_heads, max_context_len, sm_count);
     const size_t rows = (size_t)num_seqs * n_heads +
                         (size_t)ctas * kPieceWarps * (n_heads / n_kv_heads);
     const size_t pairs = (size_t)num_seqs * n_kv_heads;
@@ -92,23 +91,43 @@ pkv_status check_paged_decode(const void* out, pkv_dtype out_dtype, const void* 
     return PKV_OK;
 }
 
-pkv_status fill_pieces(pkv::PiecesLaunch* L, void* out, pkv_dtype out_dtype, const void* q,
-                       const void* k_pool, const void* v_pool, pkv_dtype kv_dtype,
-                       const int32_t* block_tables, int max_blocks_per_seq,
+// The pool [num_blocks, B, Hk, D] as a 4-D tensor for the piece decode: dims
+// (64, B, Hk D / 64, blocks), box (64, 16, D / 64, 1), 128-byte swizzle: one
+// load brings 16 tokens of one kv head as [D / 64][16][64].
+static cudaError_t encode_chunk_map(CUtensorMap* map, const void* pool, pkv_dtype dt,
+                                    int num_blocks, int block_size, int n_kv_heads,
+                                    int head_dim) {
+    auto encode = tensor_map_encoder();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint64_t es = 2, row = (cuuint64_t)n_kv_heads * head_dim;
+    cuuint64_t dims[4] = {64, (cuuint64_t)block_size, row / 64, (cuuint64_t)num_blocks};
+    cuuint64_t strides[3] = {row * es, 64 * es, (cuuint64_t)block_size * row * es};
+    cuuint32_t box[4] = {64, (cuuint32_t)kPieceTokens, (cuuint32_t)(head_dim / 64), 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = encode(map, dt == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                             : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                        4, const_cast<void*>(pool), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+pkv_status fill_pieces(PieceParams* pp, CUtensorMap* tm_k, CUtensorMap* tm_v, int ctas, void* out,
+                       pkv_dtype out_dtype, const void* q, const void* k_pool, const void* v_pool,
+                       pkv_dtype kv_dtype, const int32_t* block_tables, int max_blocks_per_seq,
                        const int32_t* context_lens, int num_seqs, int n_heads, int n_kv_heads,
                        int head_dim, int block_size, int num_blocks, float scale,
                        int max_context_len, const PiecesWorkspace& w, void* workspace,
-                       const DeviceInfo& dev, void* stream) {
-    std::memset(L, 0, sizeof(*L));
+                       const DeviceInfo& dev) {
     const int map_blocks = num_blocks > 0 ? num_blocks : 1;
     cudaError_t e;
-    if ((e = encode_pool_map(&L->tm_k, num_blocks > 0 ? k_pool : q, kv_dtype, map_blocks,
-                             block_size, n_kv_heads, head_dim, 1, true, kPieceTokens)) ||
-        (e = encode_pool_map(&L->tm_v, num_blocks > 0 ? v_pool : q, kv_dtype, map_blocks,
-                             block_size, n_kv_heads, head_dim, 1, true, kPieceTokens)))
+    if ((e = encode_chunk_map(tm_k, num_blocks > 0 ? k_pool : q, kv_dtype, map_blocks, block_size,
+                              n_kv_heads, head_dim)) ||
+        (e = encode_chunk_map(tm_v, num_blocks > 0 ? v_pool : q, kv_dtype, map_blocks, block_size,
+                              n_kv_heads, head_dim)))
         return cuda_fail(e);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
-    pkv::PieceParams& p = L->p;
+    PieceParams& p = *pp;
     p.out = out;
     p.out_dtype = out_dtype;
     p.q = q;
@@ -125,15 +144,13 @@ pkv_status fill_pieces(pkv::PiecesLaunch* L, void* out, pkv_dtype out_dtype, con
     p.cap_tokens = (int)(table < max_context_len ? table : max_context_len);
     p.scale_log2 = scale * 1.4426950408889634f;
     p.stream_heads = pieces_stream_heads(n_kv_heads);
-    L->ctas = pieces_ctas(num_seqs, n_kv_heads, max_context_len, dev.sm_count);
-    p.streams = L->ctas * (pkv::kPieceWarps / p.stream_heads);
+    p.streams = ctas * (pkv::kPieceWarps / p.stream_heads);
     p.min_run = kPieceMinRun;
     p.ws_o = reinterpret_cast<float*>(ws + w.o);
     p.ws_ml = reinterpret_cast<float*>(ws + w.ml);
     p.seg_first = reinterpret_cast<int*>(ws + w.seg_first);
     p.seg_last = reinterpret_cast<int*>(ws + w.seg_last);
     p.errors = dev.errors;
-    L->stream = static_cast<cudaStream_t>(stream);
     return PKV_OK;
 }
 
@@ -157,7 +174,8 @@ size_t score_row(int max_context_len) { return ((size_t)max_context_len + 15) / 
 
 size_t weights_bytes(int num_seqs, int n_heads, int n_kv_heads, int head_dim, int max_context_len,
                      int sm_count, PiecesWorkspace* w) {
-    *w = pieces_workspace(num_seqs, n_heads, n_kv_heads, head_dim, max_context_len, sm_count);
+    *w = pieces_workspace(num_seqs, n_heads, n_kv_heads, head_dim,
+                          pieces_ctas(num_seqs, n_kv_heads, max_context_len, sm_count));
     return w->end + align256((size_t)num_seqs * n_heads * score_row(max_context_len) *
                              sizeof(float));
 }
@@ -201,17 +219,21 @@ PKV_API pkv_status paged_attn_decode_weights(
                                       dev->sm_count, &w);
     if ((st = check_workspace(workspace, workspace_bytes, need)) != PKV_OK) return st;
     pkv::PiecesLaunch L;
-    st = fill_pieces(&L, out, out_dtype, q, k_pool, v_pool, kv_dtype, block_tables,
-                     max_blocks_per_seq, context_lens, num_seqs, n_heads, n_kv_heads, head_dim,
-                     block_size, num_blocks, scale, max_context_len, w, workspace, *dev, stream);
-    if (st != PKV_OK) return st;
+    std::memset(&L, 0, sizeof(L));
+    L.ctas = pieces_ctas(num_seqs, n_kv_heads, max_context_len, dev->sm_count);
+    L.stream = static_cast<cudaStream_t>(stream);
     pkv::PieceParams& p = L.p;
+    st = fill_pieces(&p, &L.tm_k, &L.tm_v, L.ctas, out, out_dtype, q, k_pool, v_pool, kv_dtype,
+                     block_tables, max_blocks_per_seq, context_lens, num_seqs, n_heads,
+                     n_kv_heads, head_dim, block_size, num_blocks, scale, max_context_len, w,
+                     workspace, *dev);
+    if (st != PKV_OK) return st;
     p.scores = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + w.end);
     p.score_stride = (long long)score_row(max_context_len);
     p.weights = weights;
     p.weight_stride = weight_stride;
-    e = kv_dtype == PKV_BF16 ? pkv::launch_pieces_bf16(head_dim, true, L)
-                             : pkv::launch_pieces_f16(head_dim, true, L);
+    e = kv_dtype == PKV_BF16 ? pkv::launch_weights_bf16(head_dim, L)
+                             : pkv::launch_weights_f16(head_dim, L);
     if (e != cudaSuccess) return cuda_fail(e);
     const int tiles = (p.cap_tokens + pkv::kWeightTokens - 1) / pkv::kWeightTokens;
     const dim3 grid((unsigned)(n_heads + tiles), (unsigned)num_seqs);
@@ -350,10 +372,10 @@ PKV_API pkv_status kv_evict(void* k_pool, void* v_pool, pkv_dtype dtype,
     // 256 5 us) and even out the end of the launch (32768 rows of 2 KB: 46 us
     // at 32, 40 at 4).
     const int warps = pkv::kEvictCopyThreads / 32;
-    const long long cap = 3LL * dev->sm_count;
+    const long long resident = 3LL * dev->sm_count, cap = 8LL * dev->sm_count;
     p.batch = 32;
     auto count = [&] { return (long long)num_seqs * ((keep + p.batch - 1) / p.batch) * p.parts; };
-    while (p.batch > 1 && count() < 2 * warps * cap) p.batch /= 2;
+    while (p.batch > 1 && count() < 2 * warps * resident) p.batch /= 2;
     long long ctas = (count() + warps - 1) / warps;
     if (ctas > cap) ctas = cap;
     const dim3 grid((unsigned)ctas);

@@ -138,21 +138,13 @@ __device__ __forceinline__ void mma_heads_start(MmaHeads<D>& st, const T* qrow0,
     st.l[0] = st.l[1] = 0.f;
 }
 
-// What mma_heads_chunk does with a chunk's scaled scores beside the softmax
-// (log2 domain; this lane's: tokens gid and gid + 8 of heads 2 tig, 2 tig + 1;
-// -inf past the context): nothing.
-struct NoScores {
-    __device__ __forceinline__ void operator()(float, float, float, float) const {}
-};
-
 // One 16-token chunk (`valid` of its tokens inside the context, 1..16) of
 // one kv head's K and V, swizzled [rows x 128 B] boxes at kbase / vbase,
 // token rows t0 .. t0 + 15 of the boxes.
-template <int D, typename T, class Scores = NoScores>
+template <int D, typename T>
 __device__ __forceinline__ void mma_heads_chunk(MmaHeads<D>& st, uint32_t kbase, uint32_t vbase,
                                                 uint32_t box_bytes, int t0, int valid,
-                                                float scale_log2, int lane,
-                                                const Scores& scores = Scores()) {
+                                                float scale_log2, int lane) {
     constexpr int KSTEPS = D / 16;
     const int gid = lane >> 2, tig = lane & 3;
     const int mat = lane >> 3, mrow = lane & 7;
@@ -178,7 +170,6 @@ __device__ __forceinline__ void mma_heads_chunk(MmaHeads<D>& st, uint32_t kbase,
     const float x1 = v0 ? s[1] * scale_log2 : -INFINITY;
     const float x2 = v1 ? s[2] * scale_log2 : -INFINITY;
     const float x3 = v1 ? s[3] * scale_log2 : -INFINITY;
-    scores(x0, x1, x2, x3);
     float c0 = fmaxf(x0, x2), c1 = fmaxf(x1, x3);
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {

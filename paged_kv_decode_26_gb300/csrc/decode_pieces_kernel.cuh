@@ -83,10 +83,8 @@ struct PieceParams {
     unsigned int* errors;
 };
 
-inline size_t decode_pieces_smem_bytes(int D) {
-    return 1024 + (size_t)kPieceWarps * kPieceStages * (2 * kPieceTokens * D * 2) +
-           (size_t)kPieceWarps * kPieceStages * sizeof(uint64_t) +
-           (256 + 8 + kPieceGroupsMax + 2) * sizeof(int);
+__host__ __device__ constexpr size_t decode_pieces_ring_bytes(int D) {
+    return (size_t)kPieceWarps * kPieceStages * (2 * kPieceTokens * D * 2);
 }
 
 // Length of sequence s, clamped to what the call allows.
@@ -139,6 +137,111 @@ struct StoreScores {
     }
 };
 
+struct NoScores {
+    __device__ __forceinline__ void operator()(float, float, float, float) const {}
+};
+
+// One 16-token chunk (`valid` of its tokens inside the context, 1..16) of one
+// kv head's K and V, swizzled [16 x 128 B] boxes at kbase / vbase, into the
+// state of its query heads: mma_heads_chunk with two differences that shorten
+// the chain of a chunk (a warp waits for nothing else): the score products
+// run in two accumulators, and the running maximum is an older one until a
+// score exceeds it by more than 2^8 -- the common chunk then needs one vote
+// instead of the maximum over the lanes, and no rescaling of O.
+constexpr float kPieceGrow = 8.0f;
+template <int D, typename T, class Scores>
+__device__ __forceinline__ void piece_chunk(MmaHeads<D>& st, uint32_t kbase, uint32_t vbase,
+                                            int valid, float scale_log2, int lane,
+                                            const Scores& scores) {
+    constexpr int KSTEPS = D / 16;
+    constexpr uint32_t BOX = kPieceTokens * 128;
+    const int gid = lane >> 2, tig = lane & 3;
+    const int mat = lane >> 3, mrow = lane & 7;
+    // ldmatrix matrices: K (tokens 0-7, c), (0-7, c+1), (8-15, c), (8-15, c+1);
+    // V transposed: (tokens 0-7, c), (8-15, c), (0-7, c+1), (8-15, c+1)
+    const int k_tok = (mat >> 1) * 8 + mrow, k_dc = mat & 1;
+    const int v_tok = (mat & 1) * 8 + mrow, v_dc = mat >> 1;
+
+    // ---- S^T = K Q^T: rows = tokens, columns = query heads
+    float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ks = 0; ks < KSTEPS; ++ks) {
+        uint32_t b0, b1, b2, b3;
+        ldsm_x4(kbase + (ks / 4) * BOX + swz(k_tok, (ks % 4) * 2 + k_dc), b0, b1, b2, b3);
+        const uint32_t a[4] = {b0, b2, b1, b3};
+        mma16816<T>(ks & 1 ? s1 : s0, a, st.qb[ks][0], st.qb[ks][1]);
+    }
+    // this lane: tokens gid (x0, x1) and gid + 8 (x2, x3) of heads 2 tig, 2 tig + 1
+    const bool v0 = gid < valid, v1 = gid + 8 < valid;
+    const float x0 = v0 ? (s0[0] + s1[0]) * scale_log2 : -INFINITY;
+    const float x1 = v0 ? (s0[1] + s1[1]) * scale_log2 : -INFINITY;
+    const float x2 = v1 ? (s0[2] + s1[2]) * scale_log2 : -INFINITY;
+    const float x3 = v1 ? (s0[3] + s1[3]) * scale_log2 : -INFINITY;
+    scores(x0, x1, x2, x3);
+    float c0 = fmaxf(x0, x2), c1 = fmaxf(x1, x3);
+    if (__any_sync(0xffffffffu, c0 > st.m[0] + kPieceGrow || c1 > st.m[1] + kPieceGrow)) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+            c0 = fmaxf(c0, __shfl_xor_sync(0xffffffffu, c0, off));
+            c1 = fmaxf(c1, __shfl_xor_sync(0xffffffffu, c1, off));
+        }
+        const float m0 = fmaxf(st.m[0], c0), m1 = fmaxf(st.m[1], c1);
+        const float al0 = m0 == -INFINITY ? 1.f : exp2f(st.m[0] - m0);
+        const float al1 = m1 == -INFINITY ? 1.f : exp2f(st.m[1] - m1);
+        st.m[0] = m0;
+        st.m[1] = m1;
+        st.l[0] *= al0;
+        st.l[1] *= al1;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+            st.o[j][0] *= al0;
+            st.o[j][1] *= al1;
+            st.o[j][2] *= al0;
+            st.o[j][3] *= al1;
+        }
+    }
+    const float mu0 = st.m[0] == -INFINITY ? 0.f : st.m[0];
+    const float mu1 = st.m[1] == -INFINITY ? 0.f : st.m[1];
+    const float p0 = exp2f(x0 - mu0), p1 = exp2f(x1 - mu1);
+    const float p2 = exp2f(x2 - mu0), p3 = exp2f(x3 - mu1);
+    st.l[0] += p0 + p2;
+    st.l[1] += p1 + p3;
+    // P in two 16-bit parts (hi = round(p), lo = round(p - hi)), packed by
+    // token: (head 2 tig, head 2 tig + 1) of token gid and of token gid + 8
+    const uint32_t hA = pack2<T>(p0, p1), hB = pack2<T>(p2, p3);
+    const float2 fA = unpack2<T>(hA), fB = unpack2<T>(hB);
+    const uint32_t lA = pack2<T>(p0 - fA.x, p1 - fA.y), lB = pack2<T>(p2 - fB.x, p3 - fB.y);
+    // ---- P^T as the B operand: this lane (column = head gid) needs tokens
+    // 2 tig, 2 tig + 1 (k 0-7) and 2 tig + 8, 2 tig + 9 (k 8-15), which lanes
+    // 4 (2 tig) + gid / 2 and 4 (2 tig + 1) + gid / 2 hold (half gid % 2)
+    const int srcA = 4 * (2 * tig) + (gid >> 1), srcB = srcA + 4;
+    const uint32_t sel = (gid & 1) ? 0x7632u : 0x5410u;   // the half of this lane's head
+    const uint32_t hAa = __shfl_sync(0xffffffffu, hA, srcA), hAb = __shfl_sync(0xffffffffu, hA, srcB);
+    const uint32_t hBa = __shfl_sync(0xffffffffu, hB, srcA), hBb = __shfl_sync(0xffffffffu, hB, srcB);
+    const uint32_t lAa = __shfl_sync(0xffffffffu, lA, srcA), lAb = __shfl_sync(0xffffffffu, lA, srcB);
+    const uint32_t lBa = __shfl_sync(0xffffffffu, lB, srcA), lBb = __shfl_sync(0xffffffffu, lB, srcB);
+    // (keys 2 tig, 2 tig + 1) -> low / high half of one register
+    const uint32_t bh0 = __byte_perm(hAa, hAb, sel), bh1 = __byte_perm(hBa, hBb, sel);
+    const uint32_t bl0 = __byte_perm(lAa, lAb, sel), bl1 = __byte_perm(lBa, lBb, sel);
+    // ---- O^T += V^T P^T; V rows past the context may hold anything (NaN
+    // included): P is 0 there, but 0 * NaN is not, so those rows are cleared
+    // in the A fragments (tokens 2 tig, 2 tig + 1 in a0/a1, 2 tig + 8, 2 tig +
+    // 9 in a2/a3)
+    uint32_t vm0 = 0xffffffffu, vm1 = 0xffffffffu;
+    if (valid < kPieceTokens) {
+        vm0 = (tig * 2 < valid ? 0x0000ffffu : 0u) | (tig * 2 + 1 < valid ? 0xffff0000u : 0u);
+        vm1 = (8 + tig * 2 < valid ? 0x0000ffffu : 0u) | (8 + tig * 2 + 1 < valid ? 0xffff0000u : 0u);
+    }
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+        uint32_t b0, b1, b2, b3;
+        ldsm_x4_trans(vbase + (j / 4) * BOX + swz(v_tok, (j % 4) * 2 + v_dc), b0, b1, b2, b3);
+        const uint32_t a[4] = {b0 & vm0, b2 & vm0, b1 & vm1, b3 & vm1};
+        mma16816<T>(st.o[j], a, bh0, bh1);
+        mma16816<T>(st.o[j], a, bl0, bl1);
+    }
+}
+
 // Normalised rows of a finished (sequence, kv head) to the output.
 template <int D>
 __device__ __forceinline__ void piece_output(const MmaHeads<D>& st, const PieceParams& p, int s,
@@ -170,53 +273,64 @@ __device__ __forceinline__ void piece_output(const MmaHeads<D>& st, const PieceP
     }
 }
 
-// WEIGHTS: scores go to the workspace and whole (sequence, head)s straight to
-// the output; otherwise every piece goes to the workspace, where the prefix
-// joins it.
-template <int D, typename T, bool WEIGHTS>
-__global__ void __launch_bounds__(kPieceThreads, 1)
-    decode_pieces_kernel(const __grid_constant__ CUtensorMap tm_k,
-                         const __grid_constant__ CUtensorMap tm_v,
-                         const __grid_constant__ PieceParams p) {
-    constexpr int HALVES = D / 64;
-    constexpr uint32_t BOX = kPieceTokens * 128;       // [16 tokens x 64 elements]
-    constexpr uint32_t HALF = HALVES * BOX;            // a chunk of K (or V)
-    launch_dependents();
+// Where a CTA keeps the piece decode in shared memory.
+struct PieceShared {
+    unsigned char* ring;       // per warp: kPieceStages x (K, V) chunks
+    uint64_t* bars;            // per warp: kPieceStages
+    int* cum;                  // [257] chunks before each block of 256 sequences
+    int* red;                  // [8]
+    int* group_starts;         // [kPieceGroupsMax + 1]
+    const int* gs;             // the group starts: there, or in global memory
+};
 
-    extern __shared__ __align__(1024) unsigned char smem_raw[];
-    const uint32_t raw = smem_addr(smem_raw);
-    unsigned char* sm = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+// Bytes beside the ring.
+constexpr size_t kPieceControlBytes = (size_t)kPieceWarps * kPieceStages * sizeof(uint64_t) +
+                                      (257 + 8 + kPieceGroupsMax + 1) * sizeof(int);
+
+__device__ __forceinline__ PieceShared piece_shared(unsigned char* ring, unsigned char* control) {
+    PieceShared sh;
+    sh.ring = ring;
+    sh.bars = reinterpret_cast<uint64_t*>(control);
+    sh.cum = reinterpret_cast<int*>(sh.bars + kPieceWarps * kPieceStages);
+    sh.red = sh.cum + 257;
+    sh.group_starts = sh.red + 8;
+    sh.gs = nullptr;
+    return sh;
+}
+
+// First chunk, context length and number of chunks of sequence i.
+template <bool WEIGHTS>
+__device__ __forceinline__ int piece_span(const PieceParams& p, const int* gs, int i, int& first,
+                                          int& n) {
+    n = piece_length(p, i);
+    const int start = WEIGHTS ? 0 : piece_start(p, gs, i, n);
+    first = start / kPieceTokens;
+    return (n + kPieceTokens - 1) / kPieceTokens - first;
+}
+
+// The barrier of the piece decode's 256 threads.
+__device__ __forceinline__ void piece_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(kPieceThreads) : "memory");
+}
+
+// By threads 0 .. 255: barriers, group starts, and the chunks before each
+// block of 256 sequences.  Returns the chunks of all sequences.  `report`:
+// this CTA flags bad lengths and writes p.start.
+template <bool WEIGHTS>
+__device__ __forceinline__ int piece_plan(const PieceParams& p, PieceShared& sh, bool report) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    unsigned char* ring = sm + (size_t)warp * kPieceStages * 2 * HALF;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + (size_t)kPieceWarps * kPieceStages * 2 * HALF);
-    uint64_t* full = bars + warp * kPieceStages;
-    int* s_cum = reinterpret_cast<int*>(bars + kPieceWarps * kPieceStages);  // [256 + 1]
-    int* s_red = s_cum + 257;                                                // [8]
-    int* s_gs = s_red + 8;                                                   // group starts
-
-    const int HW = p.stream_heads;
-    const int NHG = p.n_kv_heads / HW;
     const int S = p.num_seqs;
     if (lane == 0) {
-        for (int st = 0; st < kPieceStages; ++st) mbar_init(&full[st], 1);
+        for (int st = 0; st < kPieceStages; ++st) mbar_init(&sh.bars[warp * kPieceStages + st], 1);
         fence_barrier_init();
     }
-    const int* gs = p.group_start;
+    sh.gs = p.group_start;
     if (!WEIGHTS && p.num_groups > 0 && p.num_groups <= kPieceGroupsMax) {
-        for (int i = threadIdx.x; i <= p.num_groups; i += kPieceThreads) s_gs[i] = p.group_start[i];
-        gs = s_gs;
-        __syncthreads();
+        for (int i = threadIdx.x; i <= p.num_groups; i += kPieceThreads)
+            sh.group_starts[i] = p.group_start[i];
+        sh.gs = sh.group_starts;
+        piece_sync();
     }
-
-    // first chunk and number of chunks of sequence i
-    auto span = [&](int i, int& first, int& n) -> int {
-        n = piece_length(p, i);
-        const int start = WEIGHTS ? 0 : piece_start(p, gs, i, n);
-        first = start / kPieceTokens;
-        return (n + kPieceTokens - 1) / kPieceTokens - first;
-    };
-
-    // ---- chunks before each block of 256 sequences
     const int n_blk = (S + 255) / 256;
     int run = 0;
     for (int b = 0; b < n_blk; ++b) {
@@ -224,213 +338,266 @@ __global__ void __launch_bounds__(kPieceThreads, 1)
         int c = 0;
         if (i < S) {
             int first, n;
-            c = span(i, first, n);
-            if (blockIdx.x == 0) {
+            c = piece_span<WEIGHTS>(p, sh.gs, i, first, n);
+            if (report) {
                 const int raw_n = p.context_lens[i];
                 if (raw_n < 0 || raw_n > p.cap_tokens) raise_error(p.errors, PKV_DEVERR_CONTEXT);
-                if (!WEIGHTS) p.start[i] = first * kPieceTokens;
             }
+            if (!WEIGHTS && report) p.start[i] = first * kPieceTokens;
         }
 #pragma unroll
         for (int off = 16; off; off >>= 1) c += __shfl_xor_sync(0xffffffffu, c, off);
-        if (lane == 0) s_red[warp] = c;
-        __syncthreads();
-        if (threadIdx.x == 0) s_cum[b] = run;
+        if (lane == 0) sh.red[warp] = c;
+        piece_sync();
+        if (threadIdx.x == 0) sh.cum[b] = run;
 #pragma unroll
-        for (int w = 0; w < kPieceWarps; ++w) run += s_red[w];
-        __syncthreads();
+        for (int w = 0; w < kPieceWarps; ++w) run += sh.red[w];
+        piece_sync();
     }
-    if (threadIdx.x == 0) s_cum[n_blk] = run;
-    __syncthreads();
+    if (threadIdx.x == 0) sh.cum[n_blk] = run;
+    piece_sync();
+    return run;
+}
 
-    // ---- this stream's run of units (sequence, head group, chunk)
-    const long long total = (long long)run * NHG;
-    const long long busy = min((long long)p.streams, (total + p.min_run - 1) / p.min_run);
-    const int v = blockIdx.x * (kPieceWarps / HW) + warp / HW;
-    if (v < busy) {
-        const long long u0 = total * v / busy, u1 = total * (v + 1) / busy;
-        const int hw = warp % HW;
+// A chunk's K and V: [head_dim / 64][16 tokens][64 elements] each, by one load
+// of each, from rows row .. row + 15 of block b, 64-element columns col, ...
+__device__ __forceinline__ void piece_load(uint32_t k, const CUtensorMap* tm_k, uint32_t v,
+                                           const CUtensorMap* tm_v, uint32_t bar, uint32_t bytes,
+                                           int row, int col, int b, uint64_t policy,
+                                           uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %10, 0;\n\t"
+        "@q mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%4], %5;\n\t"
+        "@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%11, %6, %7, %8}], [%4], %9;\n\t"
+        "@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%2], [%3, {%11, %6, %7, %8}], [%4], %9;\n\t}" ::"r"(k),
+        "l"(reinterpret_cast<uint64_t>(tm_k)), "r"(v), "l"(reinterpret_cast<uint64_t>(tm_v)),
+        "r"(bar), "r"(bytes), "r"(row), "r"(col), "r"(b), "l"(policy), "r"(lead), "r"(0)
+        : "memory");
+}
 
-        // ---- the sequence of unit u0
-        int s = 0, first = 0, n = 0, nch = 0;
-        long long off = u0;           // unit's offset within its sequence
-        {
-            const int x = (int)(u0 / NHG);
-            int b = 0;
-            while (b + 1 < n_blk && s_cum[b + 1] <= x) ++b;
-            int cum = s_cum[b];
-            for (int base = b * 256;; base += 32) {
-                const int i = base + lane;
-                int f = 0, len = 0;
-                const int c = i < S ? span(i, f, len) : 0;
-                int inc = c;
+// Streams that get work, of `streams`, and the units in all.
+__device__ __forceinline__ long long piece_units(const PieceParams& p, int run) {
+    return (long long)run * (p.n_kv_heads / p.stream_heads);
+}
+__device__ __forceinline__ long long piece_busy(const PieceParams& p, long long total) {
+    return min((long long)p.streams, (total + p.min_run - 1) / p.min_run);
+}
+
+// One warp's part of stream v's run of units (sequence, head group, chunk).
+// WEIGHTS: scores go to the workspace and whole (sequence, head)s straight to
+// the output; otherwise every piece goes to the workspace, where the prefix
+// joins it.
+template <int D, typename T, bool WEIGHTS>
+__device__ __forceinline__ void piece_run(const PieceParams& p, const CUtensorMap& tm_k,
+                                          const CUtensorMap& tm_v, const PieceShared& sh,
+                                          long long total, long long busy, int v) {
+    constexpr int HALVES = D / 64;
+    constexpr uint32_t HALF = HALVES * kPieceTokens * 128;      // a chunk of K (or V)
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long u0 = total * v / busy, u1 = total * (v + 1) / busy;
+    const int HW = p.stream_heads, NHG = p.n_kv_heads / HW, S = p.num_seqs;
+    const int n_blk = (S + 255) / 256;
+    const int hw = warp % HW;
+    unsigned char* ring = sh.ring + (size_t)warp * kPieceStages * 2 * HALF;
+    uint64_t* full = sh.bars + warp * kPieceStages;
+
+    // ---- the sequence of unit u0
+    int s = 0, first = 0, n = 0, nch = 0;
+    long long off = u0;           // unit's offset within its sequence
+    {
+        const int x = (int)(u0 / NHG);
+        int b = 0;
+        while (b + 1 < n_blk && sh.cum[b + 1] <= x) ++b;
+        int cum = sh.cum[b];
+        for (int base = b * 256;; base += 32) {
+            const int i = base + lane;
+            int f = 0, len = 0;
+            const int c = i < S ? piece_span<WEIGHTS>(p, sh.gs, i, f, len) : 0;
+            int inc = c;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, inc, o);
-                    if (lane >= o) inc += y;
-                }
-                const unsigned hit = __ballot_sync(0xffffffffu, cum + inc > x);
-                if (hit || base + 32 >= S) {
-                    const int l = hit ? __ffs(hit) - 1 : 31;
-                    s = base + l;
-                    nch = __shfl_sync(0xffffffffu, c, l);
-                    first = __shfl_sync(0xffffffffu, f, l);
-                    n = __shfl_sync(0xffffffffu, len, l);
-                    off = u0 - (long long)NHG * (cum + __shfl_sync(0xffffffffu, inc, l) - nch);
-                    break;
-                }
-                cum += __shfl_sync(0xffffffffu, inc, 31);
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += y;
             }
-        }
-        const int todo = (int)(u1 - u0);
-        // consumer: chunk c of (s, hg); producer: the same `stages` ahead
-        int hg = (int)(off / nch), c = first + (int)(off % nch);
-        int ps = s, phg = hg, pc = c, pfirst = first, pend = first + nch;
-        int win = -1, bid = -1;      // block ids of the producer's chunks win .. win + 31
-        const int per_block = p.block_size / kPieceTokens;
-        uint32_t bad = 0;            // bit st: the slot's chunk has no valid block
-        const uint64_t policy = l2_policy_evict_first();
-        if (lane == 0) {
-            prefetch_tensormap(&tm_k);
-            prefetch_tensormap(&tm_v);
-        }
-
-        auto issue = [&](int st) {
-            if (win < 0 || pc < win || pc >= win + 32) {
-                win = pc;
-                const int page = (win + lane) / per_block;
-                bid = (win + lane < pend && page < p.max_blocks_per_seq)
-                          ? p.block_tables[(size_t)ps * p.max_blocks_per_seq + page]
-                          : -1;
-                if (win + lane < pend && (bid < 0 || bid >= p.num_blocks)) {
-                    raise_error(p.errors, PKV_DEVERR_BLOCK_ID);
-                    bid = -1;
-                }
-            }
-            const int b = __shfl_sync(0xffffffffu, bid, pc - win);
-            if (b < 0) {
-                bad |= 1u << st;
-                if (lane == 0) mbar_arrive(&full[st]);
-            } else {
-                bad &= ~(1u << st);
-                if (lane == 0) {
-                    unsigned char* dst = ring + (size_t)st * 2 * HALF;
-                    const int row = (pc % per_block) * kPieceTokens;
-                    const int col = (phg * HW + hw) * HALVES;
-                    mbar_arrive_expect_tx(&full[st], 2 * HALF);
-#pragma unroll
-                    for (int h = 0; h < HALVES; ++h) {
-                        tma_load_4d(dst + h * BOX, &tm_k, &full[st], 0, col + h, row, b, policy);
-                        tma_load_4d(dst + HALF + h * BOX, &tm_v, &full[st], 0, col + h, row, b,
-                                    policy);
-                    }
-                }
-            }
-            if (++pc == pend) {
-                win = -1;
-                if (++phg == NHG) {
-                    phg = 0;
-                    int len, cnt = 0;
-                    while (++ps < S && (cnt = span(ps, pfirst, len)) == 0) {
-                    }
-                    pend = pfirst + cnt;
-                }
-                pc = pfirst;
-            }
-        };
-
-        const int ahead = min(todo, kPieceStages);
-        for (int st = 0; st < ahead; ++st) issue(st);
-
-        MmaHeads<D> state;
-        bool fresh = true;                 // the next chunk starts a piece
-        bool from_start = false;           // the piece holds the pair's first chunk
-        int st = 0;
-        uint32_t phase = 0;
-        const int gid = lane >> 2, tig = lane & 3;
-        for (int i = 0; i < todo; ++i) {
-            const int kvh = hg * HW + hw, qh0 = kvh * p.group;
-            if (fresh) {
-                mma_heads_start<D, T>(state,
-                                      reinterpret_cast<const T*>(p.q) +
-                                          ((size_t)s * p.n_heads + qh0) * D,
-                                      p.group, lane);
-                from_start = c == first;
-                fresh = false;
-            }
-            const bool w = mbar_wait(&full[st], phase, p.errors);
-            if (!__all_sync(0xffffffffu, w)) {
-                // the loads still in flight land before the CTA may exit
-                for (int j = i; j < todo && j < i + kPieceStages; ++j) {
-                    mbar_wait(&full[st], phase, p.errors);
-                    if (++st == kPieceStages) {
-                        st = 0;
-                        phase ^= 1u;
-                    }
-                }
+            const unsigned hit = __ballot_sync(0xffffffffu, cum + inc > x);
+            if (hit || base + 32 >= S) {
+                const int l = hit ? __ffs(hit) - 1 : 31;
+                s = base + l;
+                nch = __shfl_sync(0xffffffffu, c, l);
+                first = __shfl_sync(0xffffffffu, f, l);
+                n = __shfl_sync(0xffffffffu, len, l);
+                off = u0 - (long long)NHG * (cum + __shfl_sync(0xffffffffu, inc, l) - nch);
                 break;
             }
-            const int valid = min(kPieceTokens, n - c * kPieceTokens);
-            if (!((bad >> st) & 1u)) {
-                const uint32_t kbase = smem_addr(ring + (size_t)st * 2 * HALF);
-                if (WEIGHTS) {
-                    float* row = p.scores + ((size_t)s * p.n_heads + qh0 + 2 * tig) * p.score_stride;
-                    const StoreScores sink{2 * tig < p.group ? row : nullptr,
-                                           2 * tig + 1 < p.group ? row + p.score_stride : nullptr,
-                                           c * kPieceTokens + gid, n};
-                    mma_heads_chunk<D, T>(state, kbase, kbase + HALF, BOX, 0, valid, p.scale_log2,
-                                          lane, sink);
-                } else {
-                    mma_heads_chunk<D, T>(state, kbase, kbase + HALF, BOX, 0, valid, p.scale_log2,
-                                          lane);
-                }
-            } else if (WEIGHTS) {
-                // a missing block's tokens weigh nothing
-                for (int hh = 0; hh < p.group; ++hh)
-                    if (lane < valid)
-                        p.scores[((size_t)s * p.n_heads + qh0 + hh) * p.score_stride +
-                                 c * kPieceTokens + lane] = -INFINITY;
-            }
-            __syncwarp();
-            if (i + kPieceStages < todo) issue(st);
-            if (++st == kPieceStages) {
-                st = 0;
-                phase ^= 1u;
-            }
-            // ---- the piece ends with the pair or with the run
-            const bool pair_end = c + 1 == first + nch;
-            if (pair_end || i + 1 == todo) {
-                const size_t pair = (size_t)s * p.n_kv_heads + kvh;
-                if (WEIGHTS && from_start && pair_end) {
-                    piece_output<D>(state, p, s, qh0, lane);
-                } else {
-                    const size_t row = from_start
-                                           ? (size_t)s * p.n_heads + qh0
-                                           : (size_t)S * p.n_heads + ((size_t)v * HW + hw) * p.group;
-                    mma_heads_partial<D>(state, p.ws_o, p.ws_ml, row, 1, p.group, lane);
-                }
-                if (lane == 0) {
-                    if (from_start) p.seg_first[pair] = v;
-                    if (pair_end) p.seg_last[pair] = v;
-                }
-                fresh = true;
-            }
-            if (pair_end) {
-                if (++hg == NHG) {
-                    hg = 0;
-                    if (i + 1 < todo) {
-                        while (++s < S && (nch = span(s, first, n)) == 0) {
-                        }
-                    }
-                }
-                c = first;
-            } else {
-                ++c;
-            }
+            cum += __shfl_sync(0xffffffffu, inc, 31);
         }
     }
+    const int todo = (int)(u1 - u0);
+    // consumer: chunk c of (s, hg); producer: the same `stages` ahead
+    int hg = (int)(off / nch), c = first + (int)(off % nch);
+    int ps = s, phg = hg, pc = c, pfirst = first, pend = first + nch;
+    int win = -1, bid = -1;      // block ids of the producer's chunks win .. win + 31
+    const int per_block = p.block_size / kPieceTokens;
+    uint32_t bad = 0;            // bit st: the slot's chunk has no valid block
+    const uint64_t policy = l2_policy_evict_first();
+    const uint32_t lead = lane == 0 ? 1u : 0u;
+    if (lane == 0) {
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
+    }
+
+    auto issue = [&](int st) {
+        if (win < 0 || pc < win || pc >= win + 32) {
+            win = pc;
+            const int page = (win + lane) / per_block;
+            bid = (win + lane < pend && page < p.max_blocks_per_seq)
+                      ? p.block_tables[(size_t)ps * p.max_blocks_per_seq + page]
+                      : -1;
+            if (win + lane < pend && (bid < 0 || bid >= p.num_blocks)) {
+                raise_error(p.errors, PKV_DEVERR_BLOCK_ID);
+                bid = -1;
+            }
+        }
+        const int b = __shfl_sync(0xffffffffu, bid, pc - win);
+        if (b < 0) {
+            bad |= 1u << st;
+            if (lane == 0) mbar_arrive(&full[st]);
+        } else {
+            bad &= ~(1u << st);
+            // every lane runs the loads with one lane's predicate: a branch
+            // around them took 750 cycles a chunk
+            const uint32_t dst = smem_addr(ring) + st * 2 * HALF;
+            const int row = (pc % per_block) * kPieceTokens, col = (phg * HW + hw) * HALVES;
+            piece_load(dst, &tm_k, dst + HALF, &tm_v, smem_addr(&full[st]), 2 * HALF, row, col, b,
+                       policy, lead);
+        }
+        if (++pc == pend) {
+            win = -1;
+            if (++phg == NHG) {
+                phg = 0;
+                int len, cnt = 0;
+                while (++ps < S && (cnt = piece_span<WEIGHTS>(p, sh.gs, ps, pfirst, len)) == 0) {
+                }
+                pend = pfirst + cnt;
+            }
+            pc = pfirst;
+        }
+    };
+
+    const int ahead = min(todo, kPieceStages);
+    for (int k = 0; k < ahead; ++k) issue(k);
+
+    MmaHeads<D> state;
+    bool fresh = true;                 // the next chunk starts a piece
+    bool from_start = false;           // the piece holds the pair's first chunk
+    const int gid = lane >> 2, tig = lane & 3;
+    int st = 0;
+    uint32_t phase = 0;
+    for (int i = 0; i < todo; ++i) {
+        const int kvh = hg * HW + hw, qh0 = kvh * p.group;
+        if (fresh) {
+            mma_heads_start<D, T>(state,
+                                  reinterpret_cast<const T*>(p.q) +
+                                      ((size_t)s * p.n_heads + qh0) * D,
+                                  p.group, lane);
+            from_start = c == first;
+            fresh = false;
+        }
+        const bool w = mbar_wait(&full[st], phase, p.errors);
+        if (!__all_sync(0xffffffffu, w)) {
+            // the loads still in flight land before the CTA may exit
+            for (int j = i; j < todo && j < i + kPieceStages; ++j) {
+                mbar_wait(&full[st], phase, p.errors);
+                if (++st == kPieceStages) {
+                    st = 0;
+                    phase ^= 1u;
+                }
+            }
+            break;
+        }
+        const int valid = min(kPieceTokens, n - c * kPieceTokens);
+        if (!((bad >> st) & 1u)) {
+            const uint32_t kbase = smem_addr(ring + (size_t)st * 2 * HALF);
+            if (WEIGHTS) {
+                float* row = p.scores + ((size_t)s * p.n_heads + qh0 + 2 * tig) * p.score_stride;
+                const StoreScores sink{2 * tig < p.group ? row : nullptr,
+                                       2 * tig + 1 < p.group ? row + p.score_stride : nullptr,
+                                       c * kPieceTokens + gid, n};
+                piece_chunk<D, T>(state, kbase, kbase + HALF, valid, p.scale_log2, lane, sink);
+            } else {
+                piece_chunk<D, T>(state, kbase, kbase + HALF, valid, p.scale_log2, lane,
+                                  NoScores());
+            }
+        } else if (WEIGHTS) {
+            // a missing block's tokens weigh nothing
+            for (int hh = 0; hh < p.group; ++hh)
+                if (lane < valid)
+                    p.scores[((size_t)s * p.n_heads + qh0 + hh) * p.score_stride +
+                             c * kPieceTokens + lane] = -INFINITY;
+        }
+        __syncwarp();
+        if (i + kPieceStages < todo) issue(st);
+        if (++st == kPieceStages) {
+            st = 0;
+            phase ^= 1u;
+        }
+        // ---- the piece ends with the pair or with the run
+        const bool pair_end = c + 1 == first + nch;
+        if (pair_end || i + 1 == todo) {
+            const size_t pair = (size_t)s * p.n_kv_heads + kvh;
+            if (WEIGHTS && from_start && pair_end) {
+                piece_output<D>(state, p, s, qh0, lane);
+            } else {
+                const size_t row = from_start
+                                       ? (size_t)s * p.n_heads + qh0
+                                       : (size_t)S * p.n_heads + ((size_t)v * HW + hw) * p.group;
+                mma_heads_partial<D>(state, p.ws_o, p.ws_ml, row, 1, p.group, lane);
+            }
+            if (lane == 0) {
+                if (from_start) p.seg_first[pair] = v;
+                if (pair_end) p.seg_last[pair] = v;
+            }
+            fresh = true;
+        }
+        if (pair_end) {
+            if (++hg == NHG) {
+                hg = 0;
+                if (i + 1 < todo) {
+                    while (++s < S && (nch = piece_span<WEIGHTS>(p, sh.gs, s, first, n)) == 0) {
+                    }
+                }
+            }
+            c = first;
+        } else {
+            ++c;
+        }
+    }
+}
+
+inline size_t decode_pieces_smem_bytes(int D) {
+    return 1024 + decode_pieces_ring_bytes(D) + kPieceControlBytes;
+}
+
+// Every CTA is one run of each of its streams.
+template <int D, typename T, bool WEIGHTS>
+__global__ void __launch_bounds__(kPieceThreads, 1)
+    decode_pieces_kernel(const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v,
+                         const __grid_constant__ PieceParams p) {
+    launch_dependents();
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    unsigned char* sm = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    PieceShared sh = piece_shared(sm, sm + decode_pieces_ring_bytes(D));
+    const long long total = piece_units(p, piece_plan<WEIGHTS>(p, sh, blockIdx.x == 0));
+    const long long busy = piece_busy(p, total);
+    const int v = blockIdx.x * (kPieceWarps / p.stream_heads) +
+                  (threadIdx.x >> 5) / p.stream_heads;
+    if (v < busy) piece_run<D, T, WEIGHTS>(p, tm_k, tm_v, sh, total, busy, v);
     // the finishing kernel waits for this one only: it must not end before
-    // the prefix kernel that runs ahead of it
+    // the prefix kernel that may run ahead of it
     if (!WEIGHTS) dependency_wait();
 }
 
@@ -459,7 +626,8 @@ __device__ __forceinline__ const float* piece_o(const PieceParams& p, const Piec
     return p.ws_o + row * D;
 }
 
-__device__ __forceinline__ PieceSet piece_set(const PieceParams& p, int s, int h, int n, int start) {
+__device__ __forceinline__ PieceSet piece_set(const PieceParams& p, int s, int h, int n,
+                                              int start) {
     PieceSet c;
     const int kvh = h / p.group;
     const size_t pair = (size_t)s * p.n_kv_heads + kvh;

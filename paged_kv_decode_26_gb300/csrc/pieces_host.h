@@ -6,7 +6,7 @@
 #include <cstring>
 
 #include "capi_host.h"
-#include "decode_pieces_launch.h"
+#include "decode_pieces_kernel.cuh"
 
 namespace pkv {
 namespace host {
@@ -23,12 +23,12 @@ size_t align256(size_t n);
 // kv heads per stream: the largest of 8, 4, 2, 1 that divides n_kv_heads.
 int pieces_stream_heads(int n_kv_heads);
 
-// CTAs of the piece decode: one per SM, fewer where the longest contexts
-// allowed could not give every stream its least run.
-int pieces_ctas(int num_seqs, int n_kv_heads, int max_context_len, int sm_count);
+// CTAs of the piece decode: `most`, fewer where the longest contexts allowed
+// could not give every stream its least run.
+int pieces_ctas(int num_seqs, int n_kv_heads, int max_context_len, int most);
 
 PiecesWorkspace pieces_workspace(int num_seqs, int n_heads, int n_kv_heads, int head_dim,
-                                 int max_context_len, int sm_count);
+                                 int ctas);
 
 // Argument checks that the calls share with paged_attn_decode.
 pkv_status check_paged_decode(const void* out, pkv_dtype out_dtype, const void* q,
@@ -40,13 +40,14 @@ pkv_status check_paged_decode(const void* out, pkv_dtype out_dtype, const void* 
 
 pkv_status check_workspace(const void* workspace, size_t bytes, size_t need);
 
-pkv_status fill_pieces(pkv::PiecesLaunch* L, void* out, pkv_dtype out_dtype, const void* q,
-                       const void* k_pool, const void* v_pool, pkv_dtype kv_dtype,
-                       const int32_t* block_tables, int max_blocks_per_seq,
+// Fills p and the chunk maps for `ctas` CTAs of streams.
+pkv_status fill_pieces(PieceParams* p, CUtensorMap* tm_k, CUtensorMap* tm_v, int ctas, void* out,
+                       pkv_dtype out_dtype, const void* q, const void* k_pool, const void* v_pool,
+                       pkv_dtype kv_dtype, const int32_t* block_tables, int max_blocks_per_seq,
                        const int32_t* context_lens, int num_seqs, int n_heads, int n_kv_heads,
                        int head_dim, int block_size, int num_blocks, float scale,
                        int max_context_len, const PiecesWorkspace& w, void* workspace,
-                       const DeviceInfo& dev, void* stream);
+                       const DeviceInfo& dev);
 
 // A kernel that starts while the one ahead of it on the stream drains (it
 // waits for that one's results before it reads them).

@@ -1,15 +1,14 @@
-// shared_capi.cu -- paged_attn_decode_shared of the C ABI: the shared
-// prefixes on tcgen05 (attn_tc_kernel.cuh), the rest of every context as
-// equal pieces (decode_pieces_kernel.cuh), and their merge.  Declarations and
-// contracts: pagedkv.h.
+// shared_capi.cu -- paged_attn_decode_shared of the C ABI: validation, the
+// cut of the work into prefix items and runs, workspace layout and launches
+// (decode_shared_kernel.cuh, then the merge).  Declarations and contracts:
+// pagedkv.h.
 #include <cudaTypedefs.h>
 
 #include <cstring>
 
 #include "attn_host.h"
-#include "attn_tc_launch.h"
 #include "capi_host.h"
-#include "decode_pieces_launch.h"
+#include "decode_shared_launch.h"
 #include "pieces_host.h"
 
 using namespace pkv::host;
@@ -24,6 +23,7 @@ struct SharedShape {
     int tiles;
     int split_tokens;
     int max_splits;
+    int ctas;             // of the rest of the contexts
     PiecesWorkspace pieces;
     size_t start, pre_o, pre_ml, end;
 };
@@ -53,7 +53,8 @@ SharedShape shared_shape(int num_seqs, int num_groups, int max_group, int max_pr
         }
         c.max_splits = (int)(((long long)max_prefix + c.split_tokens - 1) / c.split_tokens);
     }
-    c.pieces = pieces_workspace(num_seqs, n_heads, n_kv_heads, head_dim, max_context_len, sm_count);
+    c.ctas = pieces_ctas(num_seqs, n_kv_heads, max_context_len, sm_count);
+    c.pieces = pieces_workspace(num_seqs, n_heads, n_kv_heads, head_dim, c.ctas);
     const size_t rows = (size_t)num_seqs * n_heads * c.max_splits;
     c.start = c.pieces.end;
     c.pre_o = align256(c.start + (size_t)num_seqs * sizeof(int));
@@ -115,16 +116,17 @@ PKV_API pkv_status paged_attn_decode_shared(
                                        n_kv_heads, head_dim, max_context_len, dev->sm_count);
     if ((st = check_workspace(workspace, workspace_bytes, c.end)) != PKV_OK) return st;
     unsigned char* ws = static_cast<unsigned char*>(workspace);
-    pkv::PiecesLaunch L;
-    st = fill_pieces(&L, out, out_dtype, q, k_pool, v_pool, kv_dtype, block_tables,
-                     max_blocks_per_seq, context_lens, num_seqs, n_heads, n_kv_heads, head_dim,
-                     block_size, num_blocks, scale, max_context_len, c.pieces, workspace, *dev,
-                     stream);
-    if (st != PKV_OK) return st;
+    pkv::SharedLaunch L;
+    std::memset(&L, 0, sizeof(L));
+    L.stream = static_cast<cudaStream_t>(stream);
     pkv::PieceParams& p = L.p;
+    st = fill_pieces(&p, &L.tm_kc, &L.tm_vc, c.ctas, out, out_dtype, q, k_pool, v_pool, kv_dtype,
+                     block_tables, max_blocks_per_seq, context_lens, num_seqs, n_heads,
+                     n_kv_heads, head_dim, block_size, num_blocks, scale, max_context_len,
+                     c.pieces, workspace, *dev);
+    if (st != PKV_OK) return st;
     p.group_start = group_start;
     p.prefix_lens = prefix_lens;
-    p.num_groups = num_groups;
     p.max_group = max_group;
     p.max_prefix = max_prefix;
     p.start = reinterpret_cast<int*>(ws + c.start);
@@ -132,59 +134,51 @@ PKV_API pkv_status paged_attn_decode_shared(
     p.pre_ml = reinterpret_cast<float*>(ws + c.pre_ml);
     p.split_tokens = c.split_tokens;
     p.max_splits = c.max_splits;
+    L.ctas = c.ctas;
 
-    // ---- the prefixes
+    // ---- the prefixes (none: whole contexts, nothing to join)
+    const int G = n_heads / n_kv_heads;
+    if ((e = encode_rows_map(&L.tm_q, q, kv_dtype, num_seqs, n_heads, head_dim,
+                             (long long)n_heads * head_dim, G, pkv::kAtRows / G)) ||
+        (e = encode_pool_map(&L.tm_k, num_blocks > 0 ? k_pool : q, kv_dtype,
+                             num_blocks > 0 ? num_blocks : 1, block_size, n_kv_heads, head_dim, 1,
+                             true)) ||
+        (e = encode_pool_map(&L.tm_v, num_blocks > 0 ? v_pool : q, kv_dtype,
+                             num_blocks > 0 ? num_blocks : 1, block_size, n_kv_heads, head_dim, 1,
+                             true)))
+        return cuda_fail(e);
+    pkv::AttnParams& a = L.a;
+    a.out_dtype = out_dtype;
+    a.num_seqs = num_seqs;
+    a.n_heads = n_heads;
+    a.n_kv_heads = n_kv_heads;
+    a.group = G;
+    a.scale_log2 = p.scale_log2;
+    a.stages = attn_stages(head_dim, dev->smem_optin);
+    a.tiles = c.tiles;
+    a.group_start = group_start;
+    a.prefix_lens = prefix_lens;
+    a.max_group = max_group;
+    a.max_prefix = max_prefix;
+    a.block_tables = block_tables;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.context_lens = context_lens;
+    a.cap_tokens = p.cap_tokens;
+    a.block_size = block_size;
+    a.num_blocks = num_blocks;
+    a.split_tokens = c.split_tokens;
+    a.max_splits = c.max_splits;
+    a.pre_o = reinterpret_cast<float*>(ws + c.pre_o);
+    a.pre_ml = reinterpret_cast<float*>(ws + c.pre_ml);
+    a.errors = dev->errors;
     if (c.max_splits > 0 && num_blocks > 0) {
-        pkv::AttnLaunch A;
-        std::memset(&A, 0, sizeof(A));
-        const int G = n_heads / n_kv_heads;
-        if ((e = encode_rows_map(&A.tm_q, q, kv_dtype, num_seqs, n_heads, head_dim,
-                                 (long long)n_heads * head_dim, G, pkv::kAtRows / G)) ||
-            (e = encode_pool_map(&A.tm_k, k_pool, kv_dtype, num_blocks, block_size, n_kv_heads,
-                                 head_dim, 1, true)) ||
-            (e = encode_pool_map(&A.tm_v, v_pool, kv_dtype, num_blocks, block_size, n_kv_heads,
-                                 head_dim, 1, true)))
-            return cuda_fail(e);
-        pkv::AttnParams& a = A.p;
-        a.out_dtype = out_dtype;
-        a.num_seqs = num_seqs;
-        a.n_heads = n_heads;
-        a.n_kv_heads = n_kv_heads;
-        a.group = G;
-        a.scale_log2 = p.scale_log2;
-        a.stages = attn_stages(head_dim, dev->smem_optin);
-        a.tiles = c.tiles;
+        a.num_groups = p.num_groups = num_groups;
         a.n_items = (long long)num_groups * n_kv_heads * c.tiles * c.max_splits;
-        a.group_start = group_start;
-        a.prefix_lens = prefix_lens;
-        a.num_groups = num_groups;
-        a.max_group = max_group;
-        a.max_prefix = max_prefix;
-        a.block_tables = block_tables;
-        a.max_blocks_per_seq = max_blocks_per_seq;
-        a.context_lens = context_lens;
-        a.cap_tokens = p.cap_tokens;
-        a.block_size = block_size;
-        a.num_blocks = num_blocks;
-        a.split_tokens = c.split_tokens;
-        a.max_splits = c.max_splits;
-        a.pre_o = reinterpret_cast<float*>(ws + c.pre_o);
-        a.pre_ml = reinterpret_cast<float*>(ws + c.pre_ml);
-        a.errors = dev->errors;
-        A.ctas = (int)(a.n_items < dev->sm_count ? a.n_items : dev->sm_count);
-        A.smem_bytes = pkv::attn_tc_smem_bytes(head_dim, a.stages);
-        A.stream = L.stream;
-        const bool precise = out_dtype == PKV_F32;
-        e = kv_dtype == PKV_BF16 ? pkv::launch_attn_prefix_bf16(head_dim, precise, A)
-                                 : pkv::launch_attn_prefix_f16(head_dim, precise, A);
-        if (e != cudaSuccess) return cuda_fail(e);
-        L.after_prefix = true;
-    } else {
-        p.num_groups = 0;      // whole contexts, nothing to join
+        L.prefix_ctas = (int)(a.n_items < dev->sm_count ? a.n_items : dev->sm_count);
     }
-    // ---- the rest of every context, and the merge
-    e = kv_dtype == PKV_BF16 ? pkv::launch_pieces_bf16(head_dim, false, L)
-                             : pkv::launch_pieces_f16(head_dim, false, L);
+    const bool precise = out_dtype == PKV_F32;
+    e = kv_dtype == PKV_BF16 ? pkv::launch_shared_bf16(head_dim, precise, L)
+                             : pkv::launch_shared_f16(head_dim, precise, L);
     if (e != cudaSuccess) return cuda_fail(e);
     const dim3 grid((unsigned)n_heads, (unsigned)num_seqs);
     e = head_dim == 128 ? launch_dependent(pkv::decode_shared_finish_kernel<128>, grid,
