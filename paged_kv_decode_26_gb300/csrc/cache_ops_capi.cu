@@ -35,21 +35,26 @@ int pieces_stream_heads(int n_kv_heads) {
     return hw;
 }
 
-int pieces_ctas(int num_seqs, int n_kv_heads, int max_context_len, int most) {
-    const int hw = pieces_stream_heads(n_kv_heads);
+PiecesGrid pieces_grid(int num_seqs, int n_kv_heads, int max_context_len, int sm_count,
+                       bool short_runs) {
+    const int hw = pieces_stream_heads(n_kv_heads), per_cta = kPieceWarps / hw;
     const long long chunks = (long long)num_seqs * (n_kv_heads / hw) *
                              (((long long)max_context_len + kPieceTokens - 1) / kPieceTokens);
     const long long streams = (chunks + kPieceMinRun - 1) / kPieceMinRun;
-    const int per_cta = kPieceWarps / hw;
     const long long ctas = (streams + per_cta - 1) / per_cta;
-    return (int)(ctas < 1 ? 1 : (ctas < most ? ctas : most));
+    PiecesGrid g;
+    g.ctas = (int)(ctas < 1 ? 1 : (ctas < sm_count ? ctas : sm_count));
+    g.extra = short_runs && chunks >= (long long)g.ctas * per_cta * kPieceDealt
+                  ? kPieceExtra * g.ctas
+                  : 0;
+    return g;
 }
 
 PiecesWorkspace pieces_workspace(int num_seqs, int n_heads, int n_kv_heads, int head_dim,
-                                 int ctas) {
+                                 const PiecesGrid& grid) {
     PiecesWorkspace w;
-    const size_t rows = (size_t)num_seqs * n_heads +
-                        (size_t)ctas * kPieceWarps * (n_heads / n_kv_heads);
+    const size_t rows = (size_t)num_seqs * n_heads + (size_t)(grid.ctas + grid.extra) *
+                                                         kPieceWarps * (n_heads / n_kv_heads);
     const size_t pairs = (size_t)num_seqs * n_kv_heads;
     w.o = 0;
     w.ml = align256(w.o + rows * head_dim * sizeof(float));
@@ -112,7 +117,8 @@ static cudaError_t encode_chunk_map(CUtensorMap* map, const void* pool, pkv_dtyp
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-pkv_status fill_pieces(PieceParams* pp, CUtensorMap* tm_k, CUtensorMap* tm_v, int ctas, void* out,
+pkv_status fill_pieces(PieceParams* pp, CUtensorMap* tm_k, CUtensorMap* tm_v,
+                       const PiecesGrid& grid, void* out,
                        pkv_dtype out_dtype, const void* q, const void* k_pool, const void* v_pool,
                        pkv_dtype kv_dtype, const int32_t* block_tables, int max_blocks_per_seq,
                        const int32_t* context_lens, int num_seqs, int n_heads, int n_kv_heads,
@@ -144,8 +150,8 @@ pkv_status fill_pieces(PieceParams* pp, CUtensorMap* tm_k, CUtensorMap* tm_v, in
     p.cap_tokens = (int)(table < max_context_len ? table : max_context_len);
     p.scale_log2 = scale * 1.4426950408889634f;
     p.stream_heads = pieces_stream_heads(n_kv_heads);
-    p.streams = ctas * (pkv::kPieceWarps / p.stream_heads);
-    p.min_run = kPieceMinRun;
+    p.ctas = grid.ctas;
+    p.extra_ctas = grid.extra;
     p.ws_o = reinterpret_cast<float*>(ws + w.o);
     p.ws_ml = reinterpret_cast<float*>(ws + w.ml);
     p.seg_first = reinterpret_cast<int*>(ws + w.seg_first);
@@ -175,7 +181,7 @@ size_t score_row(int max_context_len) { return ((size_t)max_context_len + 15) / 
 size_t weights_bytes(int num_seqs, int n_heads, int n_kv_heads, int head_dim, int max_context_len,
                      int sm_count, PiecesWorkspace* w) {
     *w = pieces_workspace(num_seqs, n_heads, n_kv_heads, head_dim,
-                          pieces_ctas(num_seqs, n_kv_heads, max_context_len, sm_count));
+                          pieces_grid(num_seqs, n_kv_heads, max_context_len, sm_count, true));
     return w->end + align256((size_t)num_seqs * n_heads * score_row(max_context_len) *
                              sizeof(float));
 }
@@ -220,10 +226,11 @@ PKV_API pkv_status paged_attn_decode_weights(
     if ((st = check_workspace(workspace, workspace_bytes, need)) != PKV_OK) return st;
     pkv::PiecesLaunch L;
     std::memset(&L, 0, sizeof(L));
-    L.ctas = pieces_ctas(num_seqs, n_kv_heads, max_context_len, dev->sm_count);
+    const PiecesGrid pieces =
+        pieces_grid(num_seqs, n_kv_heads, max_context_len, dev->sm_count, true);
     L.stream = static_cast<cudaStream_t>(stream);
     pkv::PieceParams& p = L.p;
-    st = fill_pieces(&p, &L.tm_k, &L.tm_v, L.ctas, out, out_dtype, q, k_pool, v_pool, kv_dtype,
+    st = fill_pieces(&p, &L.tm_k, &L.tm_v, pieces, out, out_dtype, q, k_pool, v_pool, kv_dtype,
                      block_tables, max_blocks_per_seq, context_lens, num_seqs, n_heads,
                      n_kv_heads, head_dim, block_size, num_blocks, scale, max_context_len, w,
                      workspace, *dev);

@@ -22,14 +22,15 @@
 // 1 kv heads (the largest that divides n_kv_heads), so the warps of a stream
 // read neighbouring rows of the same blocks at about the same time.  The 16-
 // token chunks of all (sequence, head group) pairs form one line, cut into
-// equal runs, one per stream: every warp of the GPU moves the same number of
-// bytes whatever the spread of the lengths.  A pair cut by a run boundary is
-// merged from its pieces.  Each warp has its own ring of chunks in shared
+// runs, one per stream, equal whatever the spread of the lengths (and some
+// short ones, see decode_pieces_kernel).  A pair cut by a run boundary is merged
+// from its pieces.  Each warp has its own ring of chunks in shared
 // memory, filled by TMA (its lane 0 refills a slot as soon as the warp has
 // used it), and never waits for another warp.
 #pragma once
 
 #include "decode_mma_kernel.cuh"
+#include "take_over.cuh"
 
 namespace pkv {
 
@@ -38,6 +39,12 @@ constexpr int kPieceThreads = 32 * kPieceWarps;
 constexpr int kPieceTokens = 16;      // tokens per chunk
 constexpr int kPieceStages = 3;       // chunks in a warp's ring
 constexpr int kPieceGroupsMax = 1024; // group starts kept in shared memory
+constexpr int kPieceMinRun = 4;       // chunks a stream takes at least
+constexpr int kPieceSoon = 2;         // chunks left to load when the next run is asked for
+constexpr int kPieceDealt = 128;      // chunks per stream from which short runs are set apart
+constexpr int kPieceRest = 5;         // 1 / this of the units is in short runs
+constexpr int kPieceExtra = 6;        // short runs per CTA
+constexpr int kPieceShort = 8;        // chunks of a short run at least
 
 struct PieceParams {
     void* out;
@@ -55,8 +62,8 @@ struct PieceParams {
     int cap_tokens;            // longest context the tables and the caller allow
     float scale_log2;
     int stream_heads;          // kv heads (warps) per stream
-    int streams;               // streams of the grid
-    int min_run;               // chunks a stream takes at least
+    int ctas;                  // CTAs that share most of the work
+    int extra_ctas;            // and CTAs of short runs
     // shared prefixes (group_start NULL: none)
     const int* group_start;    // [num_groups + 1]
     const int* prefix_lens;    // [num_groups]
@@ -314,10 +321,10 @@ __device__ __forceinline__ void piece_sync() {
 }
 
 // By threads 0 .. 255: barriers, group starts, and the chunks before each
-// block of 256 sequences.  Returns the chunks of all sequences.  `report`:
-// this CTA flags bad lengths and writes p.start.
+// block of 256 sequences, bad lengths flagged, p.start written.  Returns the
+// chunks of all sequences.
 template <bool WEIGHTS>
-__device__ __forceinline__ int piece_plan(const PieceParams& p, PieceShared& sh, bool report) {
+__device__ __forceinline__ int piece_plan(const PieceParams& p, PieceShared& sh) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = p.num_seqs;
     if (lane == 0) {
@@ -339,11 +346,11 @@ __device__ __forceinline__ int piece_plan(const PieceParams& p, PieceShared& sh,
         if (i < S) {
             int first, n;
             c = piece_span<WEIGHTS>(p, sh.gs, i, first, n);
-            if (report) {
-                const int raw_n = p.context_lens[i];
-                if (raw_n < 0 || raw_n > p.cap_tokens) raise_error(p.errors, PKV_DEVERR_CONTEXT);
-            }
-            if (!WEIGHTS && report) p.start[i] = first * kPieceTokens;
+            // (any CTA may be taken over before it starts, so all do this,
+            // with the same values)
+            const int raw_n = p.context_lens[i];
+            if (raw_n < 0 || raw_n > p.cap_tokens) raise_error(p.errors, PKV_DEVERR_CONTEXT);
+            if (!WEIGHTS) p.start[i] = first * kPieceTokens;
         }
 #pragma unroll
         for (int off = 16; off; off >>= 1) c += __shfl_xor_sync(0xffffffffu, c, off);
@@ -377,70 +384,146 @@ __device__ __forceinline__ void piece_load(uint32_t k, const CUtensorMap* tm_k, 
         : "memory");
 }
 
-// Streams that get work, of `streams`, and the units in all.
-__device__ __forceinline__ long long piece_units(const PieceParams& p, int run) {
-    return (long long)run * (p.n_kv_heads / p.stream_heads);
-}
-__device__ __forceinline__ long long piece_busy(const PieceParams& p, long long total) {
-    return min((long long)p.streams, (total + p.min_run - 1) / p.min_run);
+// How the units (sequence, head group, chunk) are cut into runs, one per
+// stream v: the first `first` streams share `share` of them equally (the
+// runs of the CTAs that start together), the other `more` the rest.
+struct PieceRuns {
+    long long total, share;
+    int first, more;
+    __device__ __forceinline__ long long begin(int v) const {
+        return v < first ? share * v / first
+                         : share + (more > 0 ? (total - share) * (v - first) / more : 0);
+    }
+};
+
+__device__ __forceinline__ PieceRuns piece_runs(const PieceParams& p, int chunks) {
+    PieceRuns r;
+    const int per_cta = kPieceWarps / p.stream_heads;
+    r.total = (long long)chunks * (p.n_kv_heads / p.stream_heads);
+    r.first = (int)min((long long)p.ctas * per_cta, (r.total + kPieceMinRun - 1) / kPieceMinRun);
+    r.share = r.total;
+    r.more = 0;
+    if (p.extra_ctas > 0 && r.total >= (long long)p.ctas * per_cta * kPieceDealt) {
+        r.share = r.total - r.total / kPieceRest;
+        r.more = (int)min((long long)p.extra_ctas * per_cta, (r.total - r.share) / kPieceShort);
+    }
+    return r;
 }
 
-// One warp's part of stream v's run of units (sequence, head group, chunk).
-// WEIGHTS: scores go to the workspace and whole (sequence, head)s straight to
-// the output; otherwise every piece goes to the workspace, where the prefix
-// joins it.
-template <int D, typename T, bool WEIGHTS>
-__device__ __forceinline__ void piece_run(const PieceParams& p, const CUtensorMap& tm_k,
-                                          const CUtensorMap& tm_v, const PieceShared& sh,
-                                          long long total, long long busy, int v) {
+// Stream of a CTA's warp, -1 where it has no work.
+__device__ __forceinline__ int piece_stream(const PieceParams& p, const PieceRuns& r, int cta,
+                                            int warp) {
+    const int per_cta = kPieceWarps / p.stream_heads;
+    const long long k = (long long)(cta < p.ctas ? cta : cta - p.ctas) * per_cta +
+                        warp / p.stream_heads;
+    if (cta < p.ctas) return k < r.first ? (int)k : -1;
+    return k < r.more ? r.first + (int)k : -1;
+}
+
+// A place in the line of units: chunk c of (sequence s, head group hg).
+struct PieceCursor {
+    int s, hg, c;
+    int first, end;      // the pair's chunks
+    int n;               // its context length
+    int left;            // units to the end of the run
+    int v;               // the run's stream
+};
+
+// The start of stream v's run, by a whole warp.
+template <bool WEIGHTS>
+__device__ __forceinline__ PieceCursor piece_locate(const PieceParams& p, const PieceShared& sh,
+                                                    const PieceRuns& r, int v, int lane) {
+    const long long u0 = r.begin(v);
+    const int NHG = p.n_kv_heads / p.stream_heads, S = p.num_seqs, n_blk = (S + 255) / 256;
+    PieceCursor k;
+    k.v = v;
+    k.left = (int)(r.begin(v + 1) - u0);
+    const int x = (int)(u0 / NHG);
+    int b = 0;
+    while (b + 1 < n_blk && sh.cum[b + 1] <= x) ++b;
+    int cum = sh.cum[b];
+    for (int base = b * 256;; base += 32) {
+        const int i = base + lane;
+        int f = 0, len = 0;
+        const int c = i < S ? piece_span<WEIGHTS>(p, sh.gs, i, f, len) : 0;
+        int inc = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, cum + inc > x);
+        if (hit || base + 32 >= S) {
+            const int l = hit ? __ffs(hit) - 1 : 31;
+            const int nch = __shfl_sync(0xffffffffu, c, l);
+            k.s = base + l;
+            k.first = __shfl_sync(0xffffffffu, f, l);
+            k.end = k.first + nch;
+            k.n = __shfl_sync(0xffffffffu, len, l);
+            const long long off =
+                u0 - (long long)NHG * (cum + __shfl_sync(0xffffffffu, inc, l) - nch);
+            k.hg = (int)(off / nch);
+            k.c = k.first + (int)(off % nch);
+            return k;
+        }
+        cum += __shfl_sync(0xffffffffu, inc, 31);
+    }
+}
+
+// The next unit of the run.
+template <bool WEIGHTS>
+__device__ __forceinline__ void piece_advance(const PieceParams& p, const PieceShared& sh,
+                                              PieceCursor& k) {
+    --k.left;
+    if (++k.c < k.end) return;
+    if (++k.hg == p.n_kv_heads / p.stream_heads) {
+        k.hg = 0;
+        if (k.left > 0) {
+            int count;
+            while (++k.s < p.num_seqs &&
+                   (count = piece_span<WEIGHTS>(p, sh.gs, k.s, k.first, k.n)) == 0) {
+            }
+            k.end = k.first + count;
+        }
+    }
+    k.c = k.first;
+}
+
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
+// The runs that a CTA takes after its own.
+struct PieceNext {
+    uint64_t* soon;        // [1] every warp's loads are near the end of the current run
+    uint64_t* full;        // [2] the next run is known
+    int* cta;              // [2] the CTA whose run it is, -1: none is left
+};
+
+// One warp's work on the CTA's runs: kv head warp % stream_heads of each head
+// group.  WEIGHTS: scores go to the workspace and whole (sequence, head)s
+// straight to the output; otherwise every piece goes to the workspace, where
+// the prefix joins it.  The loads run kPieceStages chunks ahead, over the end
+// of a run into the next one.
+template <int D, typename T, bool WEIGHTS, bool TAKES>
+__device__ __forceinline__ void piece_worker(const PieceParams& p, const CUtensorMap& tm_k,
+                                             const CUtensorMap& tm_v, const PieceShared& sh,
+                                             const PieceRuns& runs, const PieceNext& next) {
     constexpr int HALVES = D / 64;
     constexpr uint32_t HALF = HALVES * kPieceTokens * 128;      // a chunk of K (or V)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long u0 = total * v / busy, u1 = total * (v + 1) / busy;
-    const int HW = p.stream_heads, NHG = p.n_kv_heads / HW, S = p.num_seqs;
-    const int n_blk = (S + 255) / 256;
-    const int hw = warp % HW;
+    const int HW = p.stream_heads, hw = warp % HW;
     unsigned char* ring = sh.ring + (size_t)warp * kPieceStages * 2 * HALF;
     uint64_t* full = sh.bars + warp * kPieceStages;
-
-    // ---- the sequence of unit u0
-    int s = 0, first = 0, n = 0, nch = 0;
-    long long off = u0;           // unit's offset within its sequence
-    {
-        const int x = (int)(u0 / NHG);
-        int b = 0;
-        while (b + 1 < n_blk && sh.cum[b + 1] <= x) ++b;
-        int cum = sh.cum[b];
-        for (int base = b * 256;; base += 32) {
-            const int i = base + lane;
-            int f = 0, len = 0;
-            const int c = i < S ? piece_span<WEIGHTS>(p, sh.gs, i, f, len) : 0;
-            int inc = c;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += y;
-            }
-            const unsigned hit = __ballot_sync(0xffffffffu, cum + inc > x);
-            if (hit || base + 32 >= S) {
-                const int l = hit ? __ffs(hit) - 1 : 31;
-                s = base + l;
-                nch = __shfl_sync(0xffffffffu, c, l);
-                first = __shfl_sync(0xffffffffu, f, l);
-                n = __shfl_sync(0xffffffffu, len, l);
-                off = u0 - (long long)NHG * (cum + __shfl_sync(0xffffffffu, inc, l) - nch);
-                break;
-            }
-            cum += __shfl_sync(0xffffffffu, inc, 31);
-        }
-    }
-    const int todo = (int)(u1 - u0);
-    // consumer: chunk c of (s, hg); producer: the same `stages` ahead
-    int hg = (int)(off / nch), c = first + (int)(off % nch);
-    int ps = s, phg = hg, pc = c, pfirst = first, pend = first + nch;
-    int win = -1, bid = -1;      // block ids of the producer's chunks win .. win + 31
     const int per_block = p.block_size / kPieceTokens;
-    uint32_t bad = 0;            // bit st: the slot's chunk has no valid block
     const uint64_t policy = l2_policy_evict_first();
     const uint32_t lead = lane == 0 ? 1u : 0u;
     if (lane == 0) {
@@ -448,67 +531,124 @@ __device__ __forceinline__ void piece_run(const PieceParams& p, const CUtensorMa
         prefetch_tensormap(&tm_v);
     }
 
+    PieceCursor ld;              // the next chunk to load
+    PieceCursor at;              // the chunk to work on
+    bool ahead_run = false;      // the loads are in a run that `at` has not reached
+    PieceCursor ahead_start;     // its start
+    bool more = true;            // there may be a run after ld's (TAKES)
+    int win = -1, bid = -1;      // block ids of the pair's chunks win .. win + 31
+    uint32_t bad = 0;            // bit st: the slot's chunk has no valid block
+    int cta = blockIdx.x, taken = 0;
+    ld.left = 0;
+
+    // Moves ld to the next run that has work, if there is one.
+    auto next_run = [&](bool own) {
+        while (more) {
+            if (!TAKES && !own) more = false;
+            if (!more) return;
+            if (!own) {
+                const int slot = (taken + 1) & 1;
+                const bool w = mbar_wait(&next.full[slot], (taken >> 1) & 1, p.errors);
+                cta = __all_sync(0xffffffffu, w) ? next.cta[slot] : -1;
+                __syncwarp();
+                ++taken;
+                if (cta < 0) {
+                    more = false;
+                    return;
+                }
+            }
+            own = false;
+            const int v = piece_stream(p, runs, cta, warp);
+            if (v >= 0) {
+                ld = piece_locate<WEIGHTS>(p, sh, runs, v, lane);
+                win = -1;
+                if (TAKES && ld.left <= kPieceSoon && lane == 0) mbar_arrive(next.soon);
+                return;
+            }
+            if (TAKES && lane == 0) mbar_arrive(next.soon);
+        }
+    };
+    // Whether the next run is known.
+    auto known = [&]() -> bool {
+        return __all_sync(0xffffffffu, mbar_test(&next.full[(taken + 1) & 1], (taken >> 1) & 1));
+    };
     auto issue = [&](int st) {
-        if (win < 0 || pc < win || pc >= win + 32) {
-            win = pc;
+        if (win < 0 || ld.c < win || ld.c >= win + 32) {
+            win = ld.c;
             const int page = (win + lane) / per_block;
-            bid = (win + lane < pend && page < p.max_blocks_per_seq)
-                      ? p.block_tables[(size_t)ps * p.max_blocks_per_seq + page]
+            bid = (win + lane < ld.end && page < p.max_blocks_per_seq)
+                      ? p.block_tables[(size_t)ld.s * p.max_blocks_per_seq + page]
                       : -1;
-            if (win + lane < pend && (bid < 0 || bid >= p.num_blocks)) {
+            if (win + lane < ld.end && (bid < 0 || bid >= p.num_blocks)) {
                 raise_error(p.errors, PKV_DEVERR_BLOCK_ID);
                 bid = -1;
             }
         }
-        const int b = __shfl_sync(0xffffffffu, bid, pc - win);
+        const int b = __shfl_sync(0xffffffffu, bid, ld.c - win);
         if (b < 0) {
             bad |= 1u << st;
             if (lane == 0) mbar_arrive(&full[st]);
         } else {
             bad &= ~(1u << st);
             // every lane runs the loads with one lane's predicate: a branch
-            // around them took 750 cycles a chunk
+            // around them cost 150 cycles a chunk
             const uint32_t dst = smem_addr(ring) + st * 2 * HALF;
-            const int row = (pc % per_block) * kPieceTokens, col = (phg * HW + hw) * HALVES;
+            const int row = (ld.c % per_block) * kPieceTokens;
+            const int col = (ld.hg * HW + hw) * HALVES;
             piece_load(dst, &tm_k, dst + HALF, &tm_v, smem_addr(&full[st]), 2 * HALF, row, col, b,
                        policy, lead);
         }
-        if (++pc == pend) {
-            win = -1;
-            if (++phg == NHG) {
-                phg = 0;
-                int len, cnt = 0;
-                while (++ps < S && (cnt = piece_span<WEIGHTS>(p, sh.gs, ps, pfirst, len)) == 0) {
-                }
-                pend = pfirst + cnt;
-            }
-            pc = pfirst;
-        }
+        const int s = ld.s, hg = ld.hg;
+        piece_advance<WEIGHTS>(p, sh, ld);
+        if (ld.s != s || ld.hg != hg) win = -1;
+        if (TAKES && ld.left == kPieceSoon && lane == 0) mbar_arrive(next.soon);
     };
 
-    const int ahead = min(todo, kPieceStages);
-    for (int k = 0; k < ahead; ++k) issue(k);
-
+    next_run(true);
+    if (ld.left == 0) return;
+    if (!TAKES) more = false;
+    at = ld;
     MmaHeads<D> state;
     bool fresh = true;                 // the next chunk starts a piece
     bool from_start = false;           // the piece holds the pair's first chunk
     const int gid = lane >> 2, tig = lane & 3;
-    int st = 0;
+    int st = 0, put = 0, in_flight = 0;
     uint32_t phase = 0;
-    for (int i = 0; i < todo; ++i) {
-        const int kvh = hg * HW + hw, qh0 = kvh * p.group;
+    for (;;) {
+        // ---- keep the ring full
+        while (in_flight < kPieceStages) {
+            if (ld.left == 0) {
+                // (with chunks in flight the warp works on them until the next
+                // run is known)
+                if (!TAKES || !more || ahead_run || (in_flight > 0 && !known())) break;
+                next_run(false);
+                if (!more) break;
+                if (at.left == 0) {
+                    at = ld;
+                } else {
+                    ahead_run = true;
+                    ahead_start = ld;
+                }
+            }
+            issue(put);
+            if (++put == kPieceStages) put = 0;
+            ++in_flight;
+        }
+        if (in_flight == 0) break;
+        // ---- one chunk
+        const int kvh = at.hg * HW + hw, qh0 = kvh * p.group;
         if (fresh) {
             mma_heads_start<D, T>(state,
                                   reinterpret_cast<const T*>(p.q) +
-                                      ((size_t)s * p.n_heads + qh0) * D,
+                                      ((size_t)at.s * p.n_heads + qh0) * D,
                                   p.group, lane);
-            from_start = c == first;
+            from_start = at.c == at.first;
             fresh = false;
         }
         const bool w = mbar_wait(&full[st], phase, p.errors);
         if (!__all_sync(0xffffffffu, w)) {
             // the loads still in flight land before the CTA may exit
-            for (int j = i; j < todo && j < i + kPieceStages; ++j) {
+            for (; in_flight > 0; --in_flight) {
                 mbar_wait(&full[st], phase, p.errors);
                 if (++st == kPieceStages) {
                     st = 0;
@@ -517,14 +657,14 @@ __device__ __forceinline__ void piece_run(const PieceParams& p, const CUtensorMa
             }
             break;
         }
-        const int valid = min(kPieceTokens, n - c * kPieceTokens);
+        const int valid = min(kPieceTokens, at.n - at.c * kPieceTokens);
         if (!((bad >> st) & 1u)) {
-            const uint32_t kbase = smem_addr(ring + (size_t)st * 2 * HALF);
+            const uint32_t kbase = smem_addr(ring) + st * 2 * HALF;
             if (WEIGHTS) {
-                float* row = p.scores + ((size_t)s * p.n_heads + qh0 + 2 * tig) * p.score_stride;
+                float* row = p.scores + ((size_t)at.s * p.n_heads + qh0 + 2 * tig) * p.score_stride;
                 const StoreScores sink{2 * tig < p.group ? row : nullptr,
                                        2 * tig + 1 < p.group ? row + p.score_stride : nullptr,
-                                       c * kPieceTokens + gid, n};
+                                       at.c * kPieceTokens + gid, at.n};
                 piece_chunk<D, T>(state, kbase, kbase + HALF, valid, p.scale_log2, lane, sink);
             } else {
                 piece_chunk<D, T>(state, kbase, kbase + HALF, valid, p.scale_log2, lane,
@@ -534,55 +674,65 @@ __device__ __forceinline__ void piece_run(const PieceParams& p, const CUtensorMa
             // a missing block's tokens weigh nothing
             for (int hh = 0; hh < p.group; ++hh)
                 if (lane < valid)
-                    p.scores[((size_t)s * p.n_heads + qh0 + hh) * p.score_stride +
-                             c * kPieceTokens + lane] = -INFINITY;
+                    p.scores[((size_t)at.s * p.n_heads + qh0 + hh) * p.score_stride +
+                             at.c * kPieceTokens + lane] = -INFINITY;
         }
         __syncwarp();
-        if (i + kPieceStages < todo) issue(st);
+        --in_flight;
         if (++st == kPieceStages) {
             st = 0;
             phase ^= 1u;
         }
         // ---- the piece ends with the pair or with the run
-        const bool pair_end = c + 1 == first + nch;
-        if (pair_end || i + 1 == todo) {
-            const size_t pair = (size_t)s * p.n_kv_heads + kvh;
+        const bool pair_end = at.c + 1 == at.end;
+        if (pair_end || at.left == 1) {
+            const size_t pair = (size_t)at.s * p.n_kv_heads + kvh;
             if (WEIGHTS && from_start && pair_end) {
-                piece_output<D>(state, p, s, qh0, lane);
+                piece_output<D>(state, p, at.s, qh0, lane);
             } else {
-                const size_t row = from_start
-                                       ? (size_t)s * p.n_heads + qh0
-                                       : (size_t)S * p.n_heads + ((size_t)v * HW + hw) * p.group;
+                const size_t row = from_start ? (size_t)at.s * p.n_heads + qh0
+                                              : (size_t)p.num_seqs * p.n_heads +
+                                                    ((size_t)at.v * HW + hw) * p.group;
                 mma_heads_partial<D>(state, p.ws_o, p.ws_ml, row, 1, p.group, lane);
             }
             if (lane == 0) {
-                if (from_start) p.seg_first[pair] = v;
-                if (pair_end) p.seg_last[pair] = v;
+                if (from_start) p.seg_first[pair] = at.v;
+                if (pair_end) p.seg_last[pair] = at.v;
             }
             fresh = true;
         }
-        if (pair_end) {
-            if (++hg == NHG) {
-                hg = 0;
-                if (i + 1 < todo) {
-                    while (++s < S && (nch = piece_span<WEIGHTS>(p, sh.gs, s, first, n)) == 0) {
-                    }
-                }
+        if (at.left == 1) {
+            if (ahead_run) {
+                at = ahead_start;
+                ahead_run = false;
             }
-            c = first;
+            // (no run ahead: the ring is empty, the loads take the next run
+            // above, and `at` follows)
+            else
+                at.left = 0;
         } else {
-            ++c;
+            piece_advance<WEIGHTS>(p, sh, at);
         }
     }
 }
 
 inline size_t decode_pieces_smem_bytes(int D) {
-    return 1024 + decode_pieces_ring_bytes(D) + kPieceControlBytes;
+    return 1024 + decode_pieces_ring_bytes(D) + 64 + kPieceControlBytes;
 }
 
-// Every CTA is one run of each of its streams.
-template <int D, typename T, bool WEIGHTS>
-__global__ void __launch_bounds__(kPieceThreads, 1)
+// The first `ctas` CTAs have a run of each of their streams, an equal part of
+// most of the work.  SMs stream at different rates (GB300, equal parts of a
+// whole decode: the first done after 293 us, the last after 375, 331 on
+// average), so the rest is in short runs of `extra_ctas` more CTAs: a running
+// CTA takes them over one after the other (cluster launch control), its loads
+// passing from one run to the next without a break.  Warp 8 asks for the next
+// one when every warp's loads are near the end of the current run.
+// Without TAKES there are no such runs (and no warp 8): work that a GPU is done
+// with in a tenth of a millisecond gains nothing from them -- every run adds a
+// piece to merge (8 contexts of 8K-32K tokens, grouped heads: 124 us without,
+// 138 us with).
+template <int D, typename T, bool WEIGHTS, bool TAKES>
+__global__ void __launch_bounds__(kPieceThreads + (TAKES ? 32 : 0), 1)
     decode_pieces_kernel(const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v,
                          const __grid_constant__ PieceParams p) {
@@ -590,12 +740,44 @@ __global__ void __launch_bounds__(kPieceThreads, 1)
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     unsigned char* sm = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
-    PieceShared sh = piece_shared(sm, sm + decode_pieces_ring_bytes(D));
-    const long long total = piece_units(p, piece_plan<WEIGHTS>(p, sh, blockIdx.x == 0));
-    const long long busy = piece_busy(p, total);
-    const int v = blockIdx.x * (kPieceWarps / p.stream_heads) +
-                  (threadIdx.x >> 5) / p.stream_heads;
-    if (v < busy) piece_run<D, T, WEIGHTS>(p, tm_k, tm_v, sh, total, busy, v);
+    unsigned char* control = sm + decode_pieces_ring_bytes(D);
+    uint4* steal = reinterpret_cast<uint4*>(control);
+    uint64_t* steal_bar = reinterpret_cast<uint64_t*>(control + 16);
+    PieceNext next;
+    next.soon = steal_bar + 1;
+    next.full = next.soon + 1;
+    next.cta = reinterpret_cast<int*>(next.full + 2);
+    PieceShared sh = piece_shared(sm, control + 64);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (TAKES && threadIdx.x == kPieceThreads) {
+        mbar_init(steal_bar, 1);
+        mbar_init(next.soon, kPieceWarps);
+        mbar_init(&next.full[0], 1);
+        mbar_init(&next.full[1], 1);
+        fence_barrier_init();
+    }
+    int chunks = 0;
+    if (warp < kPieceWarps) chunks = piece_plan<WEIGHTS>(p, sh);
+    if (TAKES) __syncthreads();
+    if (warp < kPieceWarps) {
+        piece_worker<D, T, WEIGHTS, TAKES>(p, tm_k, tm_v, sh, piece_runs(p, chunks), next);
+    } else {
+        for (int k = 0;; ++k) {
+            int cta = -1;
+            bool ok = __all_sync(0xffffffffu, mbar_wait(next.soon, k & 1, p.errors));
+            if (ok) {
+                if (lane == 0) steal_cta(steal, steal_bar);
+                ok = __all_sync(0xffffffffu, mbar_wait(steal_bar, k & 1, p.errors));
+                if (ok) cta = stolen_cta(steal);
+                __syncwarp();
+            }
+            if (lane == 0) {
+                next.cta[(k + 1) & 1] = cta;
+                mbar_arrive(&next.full[(k + 1) & 1]);
+            }
+            if (cta < 0) break;
+        }
+    }
     // the finishing kernel waits for this one only: it must not end before
     // the prefix kernel that may run ahead of it
     if (!WEIGHTS) dependency_wait();

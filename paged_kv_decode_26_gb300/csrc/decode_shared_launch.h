@@ -16,7 +16,6 @@ struct SharedLaunch {
     AttnParams a;
     PieceParams p;
     int prefix_ctas;       // 0: no prefixes
-    int ctas;
     cudaStream_t stream;
 };
 

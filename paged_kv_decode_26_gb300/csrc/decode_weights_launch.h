@@ -11,7 +11,6 @@ struct PiecesLaunch {
     CUtensorMap tm_k;     // chunks of one kv head
     CUtensorMap tm_v;
     PieceParams p;
-    int ctas;
     cudaStream_t stream;
 };
 

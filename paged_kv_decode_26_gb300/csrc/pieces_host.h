@@ -12,7 +12,6 @@ namespace pkv {
 namespace host {
 
 constexpr int kDefaultSms = 152;      // workspace sizes asked for without a device
-constexpr int kPieceMinRun = 4;       // chunks a stream takes at least
 
 struct PiecesWorkspace {
     size_t o, ml, seg_first, seg_last, end;   // byte offsets; end: first free byte
@@ -23,12 +22,17 @@ size_t align256(size_t n);
 // kv heads per stream: the largest of 8, 4, 2, 1 that divides n_kv_heads.
 int pieces_stream_heads(int n_kv_heads);
 
-// CTAs of the piece decode: `most`, fewer where the longest contexts allowed
-// could not give every stream its least run.
-int pieces_ctas(int num_seqs, int n_kv_heads, int max_context_len, int most);
+// CTAs of the piece decode: one per SM, fewer where the longest contexts
+// allowed could not give every stream its least run; and, with short_runs, CTAs
+// of short runs, none where the longest contexts allowed are too short for them.
+struct PiecesGrid {
+    int ctas, extra;
+};
+PiecesGrid pieces_grid(int num_seqs, int n_kv_heads, int max_context_len, int sm_count,
+                       bool short_runs);
 
 PiecesWorkspace pieces_workspace(int num_seqs, int n_heads, int n_kv_heads, int head_dim,
-                                 int ctas);
+                                 const PiecesGrid& grid);
 
 // Argument checks that the calls share with paged_attn_decode.
 pkv_status check_paged_decode(const void* out, pkv_dtype out_dtype, const void* q,
@@ -40,8 +44,9 @@ pkv_status check_paged_decode(const void* out, pkv_dtype out_dtype, const void* 
 
 pkv_status check_workspace(const void* workspace, size_t bytes, size_t need);
 
-// Fills p and the chunk maps for `ctas` CTAs of streams.
-pkv_status fill_pieces(PieceParams* p, CUtensorMap* tm_k, CUtensorMap* tm_v, int ctas, void* out,
+// Fills p and the chunk maps.
+pkv_status fill_pieces(PieceParams* p, CUtensorMap* tm_k, CUtensorMap* tm_v,
+                       const PiecesGrid& grid, void* out,
                        pkv_dtype out_dtype, const void* q, const void* k_pool, const void* v_pool,
                        pkv_dtype kv_dtype, const int32_t* block_tables, int max_blocks_per_seq,
                        const int32_t* context_lens, int num_seqs, int n_heads, int n_kv_heads,
