@@ -409,32 +409,44 @@ def paged_attn_multi_query(out: torch.Tensor, q: torch.Tensor, q_start: torch.Te
     return out
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def decode_weights_workspace_bytes(num_seqs: int, n_heads: int, n_kv_heads: int, head_dim: int,
                                    block_size: int, max_context_len: int) -> int:
     return int(lib().pkv_decode_weights_workspace_bytes(num_seqs, n_heads, n_kv_heads, head_dim,
                                                         block_size, max_context_len))
 
 
-def _need_rows(name: str, t: torch.Tensor, dtype: torch.dtype, rows: int) -> int:
-    """Checks a CUDA matrix of `rows` rows whose rows are contiguous; its row
+def _rows_stride(name: str, t: torch.Tensor, rows: int) -> int:
+    """Checks an fp32 CUDA matrix of `rows` rows, each contiguous; its row
     stride in elements."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows:
-        raise ValueError(f"{name} must be {dtype} with a row per sequence")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    if t.dtype is not torch.float32 or t.dim() != 2 or t.shape[0] != rows:
+        raise ValueError(f"{name} must be float32 with a row per sequence")
+    if t.is_contiguous():
+        return t.shape[1]
+    if t.stride(1) != 1 and t.shape[1] > 1:
         raise ValueError(f"{name}: rows must be contiguous")
     if rows > 1 and t.stride(0) < t.shape[1]:
         raise ValueError(f"{name}: rows must not overlap")
     return t.stride(0) if rows > 1 else t.shape[1]
 
 
-def _need_one_device(tensors) -> None:
-    """The library launches on the current device."""
-    cur = torch.cuda.current_device()
+def _need_here(names, tensors) -> None:
+    """Every tensor contiguous and on the current CUDA device (where the
+    library launches)."""
+    cur = _current_device()
     for t in tensors:
-        if t is not None and t.device.index != cur:
+        if t.get_device() != cur or not t.is_contiguous():
+            for name, u in zip(names, tensors):
+                _need_cuda(name, u)
             raise ValueError("tensors must be on the current CUDA device")
+
+
+def _need_ints(names, tensors) -> None:
+    for t in tensors:
+        if t.dtype is not torch.int32:
+            raise ValueError(", ".join(names) + " must be int32")
 
 
 def paged_attn_decode_weights(out: torch.Tensor, q: torch.Tensor, k_pool: torch.Tensor,
@@ -445,9 +457,8 @@ def paged_attn_decode_weights(out: torch.Tensor, q: torch.Tensor, k_pool: torch.
     """paged_attn_decode, and weights[s, t] += sum over heads of token t's
     softmax weight (fp32 [S, >= max_context_len], rows contiguous) -- what
     kv_evict goes by."""
-    _need_all_cuda(_DECODE_NAMES, (out, q, k_pool, v_pool, block_tables, context_lens))
-    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
-        raise ValueError("block_tables and context_lens must be int32")
+    _need_here(_DECODE_NAMES, (out, q, k_pool, v_pool, block_tables, context_lens))
+    _need_ints(("block_tables", "context_lens"), (block_tables, context_lens))
     S, H, D = q.shape
     nb, B, Hk, D2 = k_pool.shape
     if (D2 != D or v_pool.shape != k_pool.shape or out.shape != q.shape
@@ -455,20 +466,28 @@ def paged_attn_decode_weights(out: torch.Tensor, q: torch.Tensor, k_pool: torch.
             or block_tables.dim() != 2 or block_tables.shape[0] != S
             or context_lens.shape != (S,)):
         raise ValueError("inconsistent shapes or dtypes")
-    w_stride = _need_rows("weights", weights, torch.float32, S)
+    w_stride = _rows_stride("weights", weights, S)
+    if weights.get_device() != q.get_device():
+        raise ValueError("weights must be on the current CUDA device")
     if weights.shape[1] < max_context_len:
         raise ValueError("weights has fewer columns than max_context_len")
-    _need_one_device((out, q, k_pool, v_pool, block_tables, context_lens, weights, workspace))
+    max_context_len = int(max_context_len)
     if workspace is None:
-        n = decode_weights_workspace_bytes(S, H, Hk, D, B, max_context_len)
-        workspace = _stream_buffer(n, q.device, stream)
+        workspace = _stream_buffer(
+            decode_weights_workspace_bytes(S, H, Hk, D, B, max_context_len), q.device, stream)
+    else:
+        _need_here(("workspace",), (workspace,))
     st = lib().paged_attn_decode_weights(
-        _addr(out), _DT[out.dtype], _addr(q), _addr(k_pool), _addr(v_pool), _DT[k_pool.dtype],
-        _addr(block_tables), block_tables.shape[1], _addr(context_lens), _addr(weights), w_stride,
-        S, H, Hk, D, B, nb, float(scale), int(max_context_len), _addr(workspace),
-        workspace.numel() * workspace.element_size(), _stream_handle(stream))
+        out.data_ptr(), _DT[out.dtype], q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+        _DT[k_pool.dtype], block_tables.data_ptr(), block_tables.shape[1],
+        context_lens.data_ptr(), weights.data_ptr(), w_stride, S, H, Hk, D, B, nb, float(scale),
+        max_context_len, workspace.data_ptr(), workspace.nbytes, _stream_handle(stream))
     check(st, "paged_attn_decode_weights")
     return out
+
+
+_EVICT_NAMES = ("k_pool", "v_pool", "block_tables", "context_lens", "new_tables", "new_lens",
+                "kept")
 
 
 def kv_evict(k_pool: torch.Tensor, v_pool: torch.Tensor, block_tables: torch.Tensor,
@@ -481,31 +500,26 @@ def kv_evict(k_pool: torch.Tensor, v_pool: torch.Tensor, block_tables: torch.Ten
     int32 [S], new_weights fp32 [S, >= keep] (zeros behind the staying
     tokens), kept int32 [S, keep] (their indexes, then -1).  Free the old
     pages afterwards (BlockManager.evict_tables gives both)."""
-    for name, t in (("k_pool", k_pool), ("v_pool", v_pool), ("block_tables", block_tables),
-                    ("context_lens", context_lens), ("new_tables", new_tables),
-                    ("new_lens", new_lens), ("kept", kept)):
-        _need_cuda(name, t)
+    ints = (block_tables, context_lens, new_tables, new_lens, kept)
+    _need_here(_EVICT_NAMES, (k_pool, v_pool) + ints)
+    _need_ints(_EVICT_NAMES[2:], ints)
     S = context_lens.shape[0]
-    for name, t in (("block_tables", block_tables), ("context_lens", context_lens),
-                    ("new_tables", new_tables), ("new_lens", new_lens), ("kept", kept)):
-        if t.dtype != torch.int32:
-            raise ValueError(f"{name} must be int32")
     nb, B, Hk, D = k_pool.shape
     if (v_pool.shape != k_pool.shape or v_pool.dtype != k_pool.dtype
-            or context_lens.dim() != 1 or new_lens.shape != (S,)
+            or context_lens.dim() != 1 or new_lens.shape != context_lens.shape
             or block_tables.dim() != 2 or block_tables.shape[0] != S
-            or new_tables.dim() != 2 or new_tables.shape[0] != S
-            or tuple(kept.shape) != (S, keep)):
+            or new_tables.dim() != 2 or new_tables.shape[0] != S or kept.shape != (S, keep)):
         raise ValueError("inconsistent shapes or dtypes")
-    w_stride = _need_rows("weights", weights, torch.float32, S)
-    nw_stride = _need_rows("new_weights", new_weights, torch.float32, S)
-    _need_one_device((k_pool, v_pool, block_tables, context_lens, weights, new_tables, new_lens,
-                      new_weights, kept))
-    st = lib().kv_evict(_addr(k_pool), _addr(v_pool), _DT[k_pool.dtype], _addr(block_tables),
-                        block_tables.shape[1], _addr(context_lens), _addr(weights), w_stride,
-                        weights.shape[1], _addr(new_tables), new_tables.shape[1], _addr(new_lens),
-                        _addr(new_weights), nw_stride, new_weights.shape[1], _addr(kept), S,
-                        int(keep), int(recent), Hk, D, B, nb, _stream_handle(stream))
+    w_stride = _rows_stride("weights", weights, S)
+    nw_stride = _rows_stride("new_weights", new_weights, S)
+    if not weights.get_device() == new_weights.get_device() == k_pool.get_device():
+        raise ValueError("weights must be on the current CUDA device")
+    st = lib().kv_evict(k_pool.data_ptr(), v_pool.data_ptr(), _DT[k_pool.dtype],
+                        block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
+                        weights.data_ptr(), w_stride, weights.shape[1], new_tables.data_ptr(),
+                        new_tables.shape[1], new_lens.data_ptr(), new_weights.data_ptr(),
+                        nw_stride, new_weights.shape[1], kept.data_ptr(), S, int(keep),
+                        int(recent), Hk, D, B, nb, _stream_handle(stream))
     check(st, "kv_evict")
 
 
@@ -515,6 +529,9 @@ def decode_shared_workspace_bytes(num_seqs: int, num_groups: int, max_group: int
     return int(lib().pkv_decode_shared_workspace_bytes(num_seqs, num_groups, max_group,
                                                        max_prefix, n_heads, n_kv_heads, head_dim,
                                                        block_size, max_context_len))
+
+
+_SHARED_NAMES = _DECODE_NAMES + ("group_start", "prefix_lens")
 
 
 def paged_attn_decode_shared(out: torch.Tensor, q: torch.Tensor, k_pool: torch.Tensor,
@@ -528,12 +545,9 @@ def paged_attn_decode_shared(out: torch.Tensor, q: torch.Tensor, k_pool: torch.T
     (int32 [groups + 1]) share the blocks of their first prefix_lens[g] tokens
     (int32 [groups], whole blocks): each prefix is attended once for its
     group.  max_group and max_prefix bound the groups' sizes and prefixes."""
-    _need_all_cuda(_DECODE_NAMES + ("group_start", "prefix_lens"),
-                   (out, q, k_pool, v_pool, block_tables, context_lens, group_start, prefix_lens))
-    for name, t in (("block_tables", block_tables), ("context_lens", context_lens),
-                    ("group_start", group_start), ("prefix_lens", prefix_lens)):
-        if t.dtype != torch.int32:
-            raise ValueError(f"{name} must be int32")
+    ints = (block_tables, context_lens, group_start, prefix_lens)
+    _need_here(_SHARED_NAMES, (out, q, k_pool, v_pool) + ints)
+    _need_ints(_SHARED_NAMES[4:], ints)
     S, H, D = q.shape
     nb, B, Hk, D2 = k_pool.shape
     if (D2 != D or v_pool.shape != k_pool.shape or out.shape != q.shape
@@ -542,33 +556,34 @@ def paged_attn_decode_shared(out: torch.Tensor, q: torch.Tensor, k_pool: torch.T
             or context_lens.shape != (S,) or prefix_lens.dim() != 1
             or group_start.shape != (prefix_lens.shape[0] + 1,)):
         raise ValueError("inconsistent shapes or dtypes")
-    _need_one_device((out, q, k_pool, v_pool, block_tables, context_lens, group_start,
-                      prefix_lens, workspace))
     groups = prefix_lens.shape[0]
+    max_context_len, max_group, max_prefix = int(max_context_len), int(max_group), int(max_prefix)
     if workspace is None:
-        n = decode_shared_workspace_bytes(S, groups, int(max_group), int(max_prefix), H, Hk, D, B,
-                                          int(max_context_len))
-        workspace = _stream_buffer(n, q.device, stream)
+        workspace = _stream_buffer(
+            decode_shared_workspace_bytes(S, groups, max_group, max_prefix, H, Hk, D, B,
+                                          max_context_len), q.device, stream)
+    else:
+        _need_here(("workspace",), (workspace,))
     st = lib().paged_attn_decode_shared(
-        _addr(out), _DT[out.dtype], _addr(q), _addr(k_pool), _addr(v_pool), _DT[k_pool.dtype],
-        _addr(block_tables), block_tables.shape[1], _addr(context_lens), _addr(group_start),
-        _addr(prefix_lens), groups, int(max_group), int(max_prefix), S, H, Hk, D, B, nb,
-        float(scale), int(max_context_len), _addr(workspace),
-        workspace.numel() * workspace.element_size(), _stream_handle(stream))
+        out.data_ptr(), _DT[out.dtype], q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+        _DT[k_pool.dtype], block_tables.data_ptr(), block_tables.shape[1],
+        context_lens.data_ptr(), group_start.data_ptr(), prefix_lens.data_ptr(), groups,
+        max_group, max_prefix, S, H, Hk, D, B, nb, float(scale), max_context_len,
+        workspace.data_ptr(), workspace.nbytes, _stream_handle(stream))
     check(st, "paged_attn_decode_shared")
     return out
 
 
 def _token_stride(name: str, t: torch.Tensor) -> int:
-    """Checks packed rows [T, heads, head_dim] whose heads are contiguous; the
+    """Checks packed rows [T, heads, head_dim], each token contiguous; the
     token stride in elements."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3 or (t.numel() and (t.stride(2) != 1 or
-                                       (t.shape[1] > 1 and t.stride(1) != t.shape[2]))):
+    T, heads, dim = t.shape
+    if t.is_contiguous():
+        return heads * dim
+    row, head, one = t.stride()
+    if one != 1 or (heads > 1 and head != dim):
         raise ValueError(f"{name} must be [tokens, heads, head_dim], each token contiguous")
-    row = t.shape[1] * t.shape[2]
-    return t.stride(0) if t.shape[0] > 1 else row
+    return row if T > 1 else heads * dim
 
 
 def attn_prompt(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -578,21 +593,23 @@ def attn_prompt(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Te
     q_start[s+1]-1 are sequence s.  q [T, H, D], k and v [T, Hk, D] (each
     token contiguous: views of one fused projection will do), out [T, H, D]
     contiguous, q_start int32 [S + 1], max_len a bound of the lengths."""
-    _need_cuda("out", out)
-    _need_cuda("q_start", q_start)
-    strides = [_token_stride(n, t) for n, t in (("q", q), ("k", k), ("v", v))]
-    if q_start.dtype != torch.int32 or q_start.dim() != 1 or q_start.shape[0] < 1:
+    _need_here(("out", "q_start"), (out, q_start))
+    dev = out.get_device()
+    if not q.get_device() == k.get_device() == v.get_device() == dev:
+        raise ValueError("q, k and v must be on the current CUDA device")
+    if q_start.dtype is not torch.int32 or q_start.dim() != 1 or q_start.shape[0] < 1:
         raise ValueError("q_start must be int32 [S + 1]")
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v must be [tokens, heads, head_dim]")
     T, H, D = q.shape
     Hk = k.shape[1]
-    if (out.shape != q.shape or tuple(k.shape) != (T, Hk, D) or v.shape != k.shape
+    if (out.shape != q.shape or k.shape != (T, Hk, D) or v.shape != k.shape
             or k.dtype != q.dtype or v.dtype != q.dtype):
         raise ValueError("inconsistent shapes or dtypes")
-    _need_one_device((out, q, k, v, q_start))
-    st = lib().pkv_attn_prompt(_addr(out), _DT[out.dtype], _addr(q), strides[0], _addr(k), strides[1],
-                           _addr(v), strides[2], _DT[q.dtype], _addr(q_start),
-                           q_start.shape[0] - 1, T, int(max_len), H, Hk, D, float(scale),
-                           _stream_handle(stream))
+    st = lib().pkv_attn_prompt(out.data_ptr(), _DT[out.dtype], q.data_ptr(),
+                               _token_stride("q", q), k.data_ptr(), _token_stride("k", k),
+                               v.data_ptr(), _token_stride("v", v), _DT[q.dtype],
+                               q_start.data_ptr(), q_start.shape[0] - 1, T, int(max_len), H, Hk, D, float(scale), _stream_handle(stream))
     check(st, "attn_prompt")
     return out
 

@@ -104,13 +104,14 @@ PKV_API pkv_status pkv_attn_prompt(void* out, pkv_dtype out_dtype, const void* q
     p.total_q = total_q;
     p.max_len = max_len;
     p.errors = dev->errors;
-    // A CTA per item where running CTAs can take over the waiting ones' items:
-    // the SMs then finish together (GB300, two prompts of 6.8K and 8K tokens,
-    // 32 heads: 744 us dealt out in turn, see attn_tc_kernel.cuh for the time
-    // taken over).  Where lengths differ so much that most items of the
-    // longest sequence's count are empty, the CTAs skip those 32 at a time.
+    // Where there are more items than SMs, a CTA per item, and running CTAs
+    // take over the waiting ones' items, so that the SMs finish together
+    // (GB300: packed prompts of 128-2048 tokens, grouped heads, 221 us dealt
+    // out in turn, 191 us taken over; prompts of 6.8K and 8K tokens 744 and
+    // 707 us).  Where lengths differ so much that most items of the longest
+    // sequence's count are empty, the CTAs skip those 32 at a time instead.
     const long long real = (long long)n_kv_heads * ((long long)total_q / pair_tokens + num_seqs);
-    p.dynamic = p.n_items <= 2 * real && p.n_items <= 0x7fffffffLL ? 1 : 0;
+    p.dynamic = p.n_items > dev->sm_count && p.n_items <= 2 * real && p.n_items <= 0x7fffffffLL;
     L.ctas = (int)(p.dynamic || p.n_items < dev->sm_count ? p.n_items : dev->sm_count);
     L.smem_bytes = pkv::attn_tc_smem_bytes(head_dim, p.stages);
     L.stream = static_cast<cudaStream_t>(stream);
