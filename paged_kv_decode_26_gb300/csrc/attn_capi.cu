@@ -31,6 +31,25 @@ cudaError_t encode_rows_map(CUtensorMap* map, const void* x, pkv_dtype dt, int r
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t encode_out_map(CUtensorMap* map, void* out, pkv_dtype dt, int rows, int heads,
+                           long long parts, long long head_bytes, long long row_bytes, int group) {
+    auto encode = tensor_map_encoder();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint32_t cols = dt == PKV_F32 ? 32 : 64;
+    cuuint64_t dims[4] = {cols, (cuuint64_t)parts, (cuuint64_t)heads, (cuuint64_t)rows};
+    cuuint64_t strides[3] = {128, (cuuint64_t)head_bytes, (cuuint64_t)row_bytes};
+    cuuint32_t box[4] = {cols, 1, (cuuint32_t)group, (cuuint32_t)(32 / group)};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = encode(map,
+                        dt == PKV_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                        : dt == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                        4, out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 int attn_stages(int head_dim, int smem_optin) {
     int stages = 8;
     while (stages > 2 && pkv::attn_tc_smem_bytes(head_dim, stages) > (size_t)smem_optin) --stages;
@@ -87,7 +106,11 @@ PKV_API pkv_status pkv_attn_prompt(void* out, pkv_dtype out_dtype, const void* q
         (e = encode_rows_map(&L.tm_k, k, dtype, total_q, n_kv_heads, head_dim, k_stride, 1,
                              pkv::kAtKeys)) ||
         (e = encode_rows_map(&L.tm_v, v, dtype, total_q, n_kv_heads, head_dim, v_stride, 1,
-                             pkv::kAtKeys)))
+                             pkv::kAtKeys)) ||
+        (e = encode_out_map(&L.tm_o, out, out_dtype, total_q, n_heads,
+                            head_dim * (out_dtype == PKV_F32 ? 4 : 2) / 128,
+                            q_row / n_heads * (out_dtype == PKV_F32 ? 4 : 2),
+                            q_row * (out_dtype == PKV_F32 ? 4 : 2), G)))
         return cuda_fail(e);
     pkv::AttnParams& p = L.p;
     p.out = out;

@@ -10,6 +10,7 @@ struct AttnLaunch {
     CUtensorMap tm_q;
     CUtensorMap tm_k;
     CUtensorMap tm_v;
+    CUtensorMap tm_o;
     AttnParams p;
     int ctas;
     size_t smem_bytes;

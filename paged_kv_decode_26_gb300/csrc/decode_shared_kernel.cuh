@@ -83,13 +83,13 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v,
+                       const __grid_constant__ CUtensorMap tm_o,
                        const __grid_constant__ AttnParams p) {
     launch_dependents();
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     unsigned char* sm = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
-    unsigned char* control =
-        sm + 2 * AttnSizes<D>::Q_BYTES + (size_t)p.stages * AttnSizes<D>::KV_BYTES;
+    unsigned char* control = sm + attn_tile_bytes(D, p.stages);
     int* s_tmem = reinterpret_cast<int*>(control);
     AttnControl c = attn_control<D>(sm, control + 32, p.stages);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAtSoftmaxRegs));
-        attn_softmax<D, T, true, PRECISE>(c, p, warp, lane);
+        attn_softmax<D, T, true, PRECISE>(c, p, tm_o, warp, lane);
     }
 
     // ---- tensor memory is released after every thread is done with it

@@ -11,6 +11,7 @@ struct SharedLaunch {
     CUtensorMap tm_q;
     CUtensorMap tm_k;      // whole pages of one kv head
     CUtensorMap tm_v;
+    CUtensorMap tm_o;      // the prefixes' partial outputs
     CUtensorMap tm_kc;     // chunks of one kv head
     CUtensorMap tm_vc;
     AttnParams a;

@@ -174,6 +174,10 @@ PKV_API pkv_status paged_attn_decode_shared(
     a.pre_ml = reinterpret_cast<float*>(ws + c.pre_ml);
     a.errors = dev->errors;
     if (c.max_splits > 0 && num_blocks > 0) {
+        const long long unit = (long long)head_dim * sizeof(float) * c.max_splits;
+        if ((e = encode_out_map(&L.tm_o, a.pre_o, PKV_F32, num_seqs, n_heads, unit / 128, unit,
+                                unit * n_heads, G)))
+            return cuda_fail(e);
         a.num_groups = p.num_groups = num_groups;
         a.n_items = (long long)num_groups * n_kv_heads * c.tiles * c.max_splits;
         L.prefix_ctas = (int)(a.n_items < dev->sm_count ? a.n_items : dev->sm_count);
