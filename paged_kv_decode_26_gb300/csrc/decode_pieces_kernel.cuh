@@ -851,61 +851,74 @@ __device__ __forceinline__ float2 merge_ml(const PieceParams& p, const PieceSet&
 constexpr int kFinishThreads = 128;
 constexpr int kFinishWarps = kFinishThreads / 32;
 
-// The merged output row of (s, h), by one CTA: its warps take the pieces in
-// turn, so that many pieces (a long context on many streams) are read at
-// once.  s_o: [kFinishWarps, D].
-template <int D>
-__device__ __forceinline__ void merge_row(const PieceParams& p, const PieceSet& c, int s, int h,
-                                          float* s_o) {
+// Merged output rows, by a CTA: W of its warps per row take the row's pieces in
+// turn, so that many pieces (a long context on many streams) are read at once;
+// with few pieces one warp does (W = 1, four rows per CTA).  c, s, h: this
+// warp's row (`have`: there is one).  s_o: [kFinishWarps, D].
+template <int D, int W>
+__device__ __forceinline__ void merge_rows(const PieceParams& p, const PieceSet& c, bool have,
+                                           int s, int h, float* s_o) {
     constexpr int V = D / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int k = c.n_pre + c.first + c.extra;
-    const float2 ml = merge_ml(p, c, lane, 32);
-    const float inv = ml.y != 0.f ? 1.f / ml.y : 0.f;
     float o[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) o[e] = 0.f;
+    if (have) {
+        const float2 ml = merge_ml(p, c, lane, 32);
+        const float inv = ml.y != 0.f ? 1.f / ml.y : 0.f;
 #pragma unroll 4
-    for (int i = warp; i < k; i += kFinishWarps) {
-        const float2 a = piece_ml(p, c, i);
-        const float w = a.y != 0.f ? a.y * exp2f(a.x - ml.x) * inv : 0.f;
-        const float* row = piece_o(p, c, i, D) + lane * V;
+        for (int i = warp % W; i < k; i += W) {
+            const float2 a = piece_ml(p, c, i);
+            const float w = a.y != 0.f ? a.y * exp2f(a.x - ml.x) * inv : 0.f;
+            const float* row = piece_o(p, c, i, D) + lane * V;
 #pragma unroll
-        for (int e = 0; e < V; e += 2) {
-            const float2 x = *reinterpret_cast<const float2*>(row + e);
-            o[e] += w * x.x;
-            o[e + 1] += w * x.y;
+            for (int e = 0; e < V; e += 2) {
+                const float2 x = *reinterpret_cast<const float2*>(row + e);
+                o[e] += w * x.x;
+                o[e + 1] += w * x.y;
+            }
         }
     }
+    if (W > 1) {
 #pragma unroll
-    for (int e = 0; e < V; e += 2)
-        *reinterpret_cast<float2*>(s_o + warp * D + lane * V + e) = make_float2(o[e], o[e + 1]);
-    __syncthreads();
-    const int d = 2 * threadIdx.x;
-    if (d >= D) return;
-    float2 x = make_float2(0.f, 0.f);
+        for (int e = 0; e < V; e += 2)
+            *reinterpret_cast<float2*>(s_o + warp * D + lane * V + e) = make_float2(o[e], o[e + 1]);
+        __syncthreads();
+        if (warp % W) return;
 #pragma unroll
-    for (int w = 0; w < kFinishWarps; ++w) {
-        const float2 y = *reinterpret_cast<const float2*>(s_o + w * D + d);
-        x.x += y.x;
-        x.y += y.y;
+        for (int w = 1; w < W; ++w)
+#pragma unroll
+            for (int e = 0; e < V; e += 2) {
+                const float2 x =
+                    *reinterpret_cast<const float2*>(s_o + (warp + w) * D + lane * V + e);
+                o[e] += x.x;
+                o[e + 1] += x.y;
+            }
     }
-    const size_t at = ((size_t)s * p.n_heads + h) * D + d;
-    if (p.out_dtype == PKV_F32)
-        *reinterpret_cast<float2*>(reinterpret_cast<float*>(p.out) + at) = x;
-    else
-        *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.out) + at) =
-            pack_out(x.x, x.y, p.out_dtype);
+    if (!have) return;
+    const size_t at = ((size_t)s * p.n_heads + h) * D + lane * V;
+#pragma unroll
+    for (int e = 0; e < V; e += 2) {
+        if (p.out_dtype == PKV_F32)
+            *reinterpret_cast<float2*>(reinterpret_cast<float*>(p.out) + at + e) =
+                make_float2(o[e], o[e + 1]);
+        else
+            *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.out) + at + e) =
+                pack_out(o[e], o[e + 1], p.out_dtype);
+    }
 }
 
-// One CTA per (head, sequence).
-template <int D>
+// grid x: rows of a sequence, kFinishWarps / W per CTA; y: sequences.
+template <int D, int W>
 __global__ void __launch_bounds__(kFinishThreads)
     decode_shared_finish_kernel(const __grid_constant__ PieceParams p) {
     __shared__ __align__(16) float s_o[kFinishWarps * D];
     dependency_wait();
-    const int s = blockIdx.y, h = blockIdx.x;
-    merge_row<D>(p, piece_set(p, s, h, piece_length(p, s), p.start[s]), s, h, s_o);
+    const int s = blockIdx.y, h = blockIdx.x * (kFinishWarps / W) + (threadIdx.x >> 5) / W;
+    const bool have = h < p.n_heads;
+    merge_rows<D, W>(p, piece_set(p, s, have ? h : 0, piece_length(p, s), p.start[s]), have, s, h,
+                     s_o);
 }
 
 // grid x: n_heads CTAs that merge a head cut into pieces (or empty), then a
@@ -922,7 +935,7 @@ __global__ void __launch_bounds__(kFinishThreads)
     const int n = piece_length(p, s);
     if ((int)blockIdx.x < p.n_heads) {
         const PieceSet c = piece_set(p, s, blockIdx.x, n, 0);
-        if (c.extra || !c.first) merge_row<D>(p, c, s, blockIdx.x, s_mem);
+        if (c.extra || !c.first) merge_rows<D, kFinishWarps>(p, c, true, s, blockIdx.x, s_mem);
         return;
     }
     const int t0 = (blockIdx.x - p.n_heads) * kWeightTokens;

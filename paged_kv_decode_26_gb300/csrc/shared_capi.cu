@@ -186,11 +186,19 @@ PKV_API pkv_status paged_attn_decode_shared(
     e = kv_dtype == PKV_BF16 ? pkv::launch_shared_bf16(head_dim, precise, L)
                              : pkv::launch_shared_f16(head_dim, precise, L);
     if (e != cudaSuccess) return cuda_fail(e);
-    const dim3 grid((unsigned)n_heads, (unsigned)num_seqs);
-    e = head_dim == 128 ? launch_dependent(pkv::decode_shared_finish_kernel<128>, grid,
-                                           pkv::kFinishThreads, 0, L.stream, p)
-                        : launch_dependent(pkv::decode_shared_finish_kernel<64>, grid,
-                                           pkv::kFinishThreads, 0, L.stream, p);
+    // Pieces of a row to expect: the prefix's splits, and the cuts of the rest.
+    // Up to 12 one warp merges them (GB300, 8192 rows of 6 pieces: 17 us with
+    // four warps a row, see DESIGN for one).
+    const long long streams = (long long)c.grid.ctas * (pkv::kPieceWarps / p.stream_heads);
+    const long long pairs = (long long)num_seqs * (n_kv_heads / p.stream_heads);
+    const bool few = c.max_splits + 2 + streams / pairs <= 12;
+    const int rows = few ? pkv::kFinishWarps : 1;
+    const dim3 grid((unsigned)((n_heads + rows - 1) / rows), (unsigned)num_seqs);
+    auto merge = head_dim == 128 ? (few ? pkv::decode_shared_finish_kernel<128, 1>
+                                        : pkv::decode_shared_finish_kernel<128, 4>)
+                                 : (few ? pkv::decode_shared_finish_kernel<64, 1>
+                                        : pkv::decode_shared_finish_kernel<64, 4>);
+    e = launch_dependent(merge, grid, pkv::kFinishThreads, 0, L.stream, p);
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
 }
 
