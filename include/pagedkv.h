@@ -571,8 +571,9 @@ PKV_API pkv_status paged_attn_decode_shared(
  * A sequence whose bounds lie outside the tokens or whose length exceeds
  * max_len is left out (its rows are not written) and flagged
  * PKV_DEVERR_CONTEXT.  The softmax weights enter the second product rounded to
- * dtype, except for F32 outputs (hi + lo parts, as in the other calls).  One
- * launch, no workspace.
+ * dtype, except for F32 outputs (hi + lo parts, as in the other calls).  NaN and
+ * infinities in rows of k and v reach only the tokens that see those rows (an
+ * infinity in v as an infinity or NaN).  One launch, no workspace.
  */
 PKV_API pkv_status pkv_attn_prompt(void* out, pkv_dtype out_dtype, const void* q, int64_t q_stride,
                                const void* k, int64_t k_stride, const void* v, int64_t v_stride,

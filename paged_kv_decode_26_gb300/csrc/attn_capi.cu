@@ -126,6 +126,8 @@ PKV_API pkv_status pkv_attn_prompt(void* out, pkv_dtype out_dtype, const void* q
     p.q_start = q_start;
     p.total_q = total_q;
     p.max_len = max_len;
+    p.v = v;
+    p.v_stride = v_stride;
     p.errors = dev->errors;
     // Where there are more items than SMs, a CTA per item, and running CTAs
     // take over the waiting ones' items, so that the SMs finish together

@@ -22,10 +22,10 @@
 // (128 columns), which the softmax overwrites with P as 16-bit pairs.
 //
 // Roles: warps 0-3 and 4-7 are the softmax of tile 0 and 1, a thread per row;
-// warp 8 issues every MMA; warp 9 loads by TMA and clears V rows that no row
-// may see; warp 10 picks the CTA's work items.  One CTA per SM stays for the
-// whole launch: the next item's queries, keys and first products overlap the
-// last softmax and the output of the current one.
+// warp 8 issues every MMA; warp 9 loads by TMA; warp 10 picks the CTA's work
+// items; warp 11 guards V tiles that not every row sees all of.  One CTA per SM
+// stays for the whole launch: the next item's queries, keys and first products
+// overlap the last softmax and the output of the current one.
 //
 // Precision: S, m, l and O are fp32.  P is rounded once to the 16-bit type of
 // V before the second product (at most half an eps relative to each weight,
@@ -41,7 +41,7 @@ namespace pkv {
 
 constexpr int kAtKeys = 128;        // keys per tile
 constexpr int kAtRows = 128;        // rows per row tile
-constexpr int kAtThreads = 384;     // 8 softmax warps, MMA, loader, scheduler, one idle
+constexpr int kAtThreads = 384;     // 8 softmax warps, MMA, loader, scheduler, guard
 // Registers per thread: 384 x 168 at launch = 256 x 200 + 128 x 104 after the
 // softmax warps (which hold a row of S) have taken over the others' share.
 constexpr int kAtSoftmaxRegs = 200, kAtOtherRegs = 104;
@@ -64,6 +64,8 @@ struct AttnParams {
     const int* q_start;        // [num_seqs + 1]
     int total_q;
     int max_len;
+    const void* v;             // token t's row at t * v_stride elements
+    long long v_stride;
     // shared prefixes
     const int* group_start;    // [num_groups + 1]
     const int* prefix_lens;    // [num_groups]
@@ -124,7 +126,7 @@ struct AttnControl {
     uint64_t* bars;
     uint64_t* kv_full;      // [stages]
     uint64_t* kv_free;      // [stages]
-    uint64_t* land;         // a V tile to clear rows of has landed
+    uint64_t* land;         // [stages] a V tile for the guard has landed
     uint64_t* q_full;       // [tile]
     uint64_t* q_free;
     uint64_t* s_full;
@@ -135,6 +137,7 @@ struct AttnControl {
     uint64_t* it_free;
     uint64_t* fin;
     AttnItem* items;
+    int* poison;            // [kAtItems] V of the item's last tiles held NaN or infinities
     unsigned char* sQ;
     unsigned char* sKV;
     unsigned char* sOut;    // per softmax warp 32 rows x 128 bytes of the output
@@ -142,11 +145,14 @@ struct AttnControl {
     int stages;
 };
 
-__host__ __device__ constexpr int attn_bars(int stages) { return 2 * stages + 1 + 4 + 2 + 4 + 4 + 2 * kAtItems + 1; }
+__host__ __device__ constexpr int attn_bars(int stages) {
+    return 3 * stages + 4 + 2 + 4 + 4 + 2 * kAtItems + 1;
+}
 
-// Bytes behind the tiles: barriers, then item slots.
+// Bytes behind the tiles: barriers, item slots, flags.
 inline __host__ __device__ size_t attn_control_bytes(int stages) {
-    return (size_t)attn_bars(stages) * sizeof(uint64_t) + kAtItems * sizeof(AttnItem);
+    return (size_t)attn_bars(stages) * sizeof(uint64_t) +
+           kAtItems * (sizeof(AttnItem) + sizeof(int));
 }
 
 template <int D>
@@ -161,7 +167,7 @@ __device__ __forceinline__ AttnControl attn_control(unsigned char* tiles, unsign
     c.kv_full = c.bars;
     c.kv_free = c.kv_full + stages;
     c.land = c.kv_free + stages;
-    c.q_full = c.land + 1;
+    c.q_full = c.land + stages;
     c.q_free = c.q_full + 2;
     c.s_full = c.q_free + 2;
     c.p_full = c.s_full + 2;
@@ -171,6 +177,7 @@ __device__ __forceinline__ AttnControl attn_control(unsigned char* tiles, unsign
     c.it_free = c.it_full + kAtItems;
     c.fin = c.it_free + kAtItems;
     c.items = reinterpret_cast<AttnItem*>(c.fin + 1);
+    c.poison = reinterpret_cast<int*>(c.items + kAtItems);
     c.tmem = 0;
     return c;
 }
@@ -181,7 +188,7 @@ __device__ __forceinline__ void attn_init_barriers(const AttnControl& c) {
         mbar_init(&c.kv_full[i], 1);
         mbar_init(&c.kv_free[i], 1);
     }
-    mbar_init(c.land, 1);
+    for (int i = 0; i < c.stages; ++i) mbar_init(&c.land[i], 1);
     for (int t = 0; t < 2; ++t) {
         mbar_init(&c.q_full[t], 1);
         mbar_init(&c.q_free[t], 1);
@@ -193,7 +200,7 @@ __device__ __forceinline__ void attn_init_barriers(const AttnControl& c) {
     }
     for (int i = 0; i < kAtItems; ++i) {
         mbar_init(&c.it_full[i], 1);
-        mbar_init(&c.it_free[i], 10);
+        mbar_init(&c.it_free[i], 11);
     }
     mbar_init(c.fin, 1);
     fence_barrier_init();
@@ -263,6 +270,13 @@ __device__ __forceinline__ void at_commit(uint64_t* bar, uint32_t lead) {
         : "memory");
 }
 
+// Whether V of key tile j holds rows that some query row of the item does not
+// see (they pass the guard).
+template <bool PAGED>
+__device__ __forceinline__ bool attn_guarded(const AttnItem& it, int j) {
+    return (j + 1) * kAtKeys > (PAGED ? it.n_keys : it.pos0 + 1);
+}
+
 // Warp 9: queries, K and V by TMA.
 template <int D, bool PAGED>
 __device__ __forceinline__ void attn_loader(const AttnControl& ctl, const AttnParams& p,
@@ -281,7 +295,6 @@ __device__ __forceinline__ void attn_loader(const AttnControl& ctl, const AttnPa
     int slot = 0, sph = 0;          // item ring
     int st = 0, round = 0;          // K/V ring
     uint32_t q_uses[2] = {0, 0};
-    uint32_t land_ph = 0;
     bool ok = true;
     const int per_tile = PAGED ? kAtKeys / p.block_size : 0;
 
@@ -325,8 +338,8 @@ __device__ __forceinline__ void attn_loader(const AttnControl& ctl, const AttnPa
                             mbar_arrive_expect_tx(&ctl.q_full[t], Q_BYTES);
 #pragma unroll
                             for (int h = 0; h < HALVES; ++h)
-                                tma_load_4d(ctl.sQ + t * Q_BYTES + h * Q_HALF, &tm_q, &ctl.q_full[t],
-                                            0, h, it.kvh * G, it.row0 + t * QT, once);
+                                tma_load_4d(ctl.sQ + t * Q_BYTES + h * Q_HALF, &tm_q,
+                                            &ctl.q_full[t], 0, h, it.kvh * G, it.row0 + t * QT, once);
                         }
                     }
                     if (!ok) break;
@@ -335,8 +348,8 @@ __device__ __forceinline__ void attn_loader(const AttnControl& ctl, const AttnPa
                                mbar_wait(&ctl.kv_free[st], (round - 1) & 1, p.errors);
                 ok = __all_sync(0xffffffffu, w);
                 if (!ok) break;
-                const bool clear = kv == 1 && (j + 1) * kAtKeys > it.n_keys;
-                uint64_t* bar = clear ? ctl.land : &ctl.kv_full[st];
+                uint64_t* bar = kv == 1 && attn_guarded<PAGED>(it, j) ? &ctl.land[st]
+                                                                      : &ctl.kv_full[st];
                 unsigned char* dst = ctl.sKV + (size_t)st * KV_BYTES;
                 const CUtensorMap* tm = kv ? &tm_v : &tm_k;
                 if (!PAGED) {
@@ -359,22 +372,6 @@ __device__ __forceinline__ void attn_loader(const AttnControl& ctl, const AttnPa
                                         0, it.kvh * HALVES + h, 0, id, keep);
                     }
                 }
-                if (clear) {
-                    // rows past the last key: another sequence's, never
-                    // loaded, or past the tensor
-                    ok = __all_sync(0xffffffffu, mbar_wait(ctl.land, land_ph, p.errors));
-                    land_ph ^= 1u;
-                    if (!ok) break;
-                    const int from = it.n_keys - j * kAtKeys;
-                    for (int idx = from * 8 + lane; idx < kAtKeys * 8; idx += 32)
-#pragma unroll
-                        for (int h = 0; h < HALVES; ++h)
-                            *reinterpret_cast<uint4*>(dst + h * KV_HALF + idx * 16) =
-                                make_uint4(0u, 0u, 0u, 0u);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctl.kv_full[st]);
-                }
                 next_slot();
             }
             id = id_next;
@@ -387,12 +384,94 @@ __device__ __forceinline__ void attn_loader(const AttnControl& ctl, const AttnPa
         }
     }
     if (!ok) {
-        // loads in flight land before the CTA may exit
-        const int issued = round * ctl.stages + st;
-        for (int k = max(0, issued - ctl.stages); k < issued; ++k)
-            mbar_wait(&ctl.kv_full[k % ctl.stages], (k / ctl.stages) & 1, p.errors);
-        for (int t = 0; t < 2; ++t)
-            if (q_uses[t]) mbar_wait(&ctl.q_full[t], (q_uses[t] - 1) & 1, p.errors);
+        // a wait gave up: loads in flight get a millisecond to land before the
+        // CTA may exit
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 1000000ull) __nanosleep(1000);
+    }
+    __syncwarp();
+}
+
+// x * 0 + acc of two packed elements.
+template <typename T>
+__device__ __forceinline__ uint32_t fma2_zero(uint32_t x, uint32_t acc) {
+    if (std::is_same<T, __nv_bfloat16>::value)
+        asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
+    else
+        asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
+    return acc;
+}
+
+// Warp 11: V tiles that hold rows which not every query row sees.  A hidden
+// row's weight is 0, but 0 * NaN and 0 * infinity are not, so rows past the
+// last key (another sequence's, never loaded, or past the tensor) are cleared,
+// and NaN and infinities in rows that only later queries see are taken out
+// before the product; the output adds them to the rows that see them.
+template <int D, typename T, bool PAGED>
+__device__ __forceinline__ void attn_guard(const AttnControl& ctl, const AttnParams& p, int lane) {
+    PKV_ATTN_SIZES(D)
+    constexpr uint32_t EXP = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
+    int slot = 0, sph = 0;          // item ring
+    int at = 0;                     // ring slot of the item's K_0
+    uint32_t land_ph = 0;           // bit i: phase of land[i] to wait for next
+    bool ok = true;
+    while (ok) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&ctl.it_full[slot], sph, p.errors));
+        if (!ok) break;
+        const AttnItem it = ctl.items[slot];
+        if (it.done) break;
+        const int n_tiles = PAGED && it.split < 0 ? 0 : max(it.nt[0], it.nt[1]);
+        if (lane == 0) ctl.poison[slot] = 0;
+        __syncwarp();
+        for (int j = 0; ok && j < n_tiles; ++j) {
+            if (!attn_guarded<PAGED>(it, j)) continue;
+            const int st = (at + 2 * j + 1) % ctl.stages;
+            ok = __all_sync(0xffffffffu, mbar_wait(&ctl.land[st], (land_ph >> st) & 1u, p.errors));
+            land_ph ^= 1u << st;
+            if (!ok) break;
+            unsigned char* v = ctl.sKV + (size_t)st * KV_BYTES;
+            const int keys = min(kAtKeys, it.n_keys - j * kAtKeys);
+            for (int i = keys * 8 + lane; i < kAtKeys * 8; i += 32)
+#pragma unroll
+                for (int h = 0; h < HALVES; ++h)
+                    *reinterpret_cast<uint4*>(v + h * KV_HALF + i * 16) =
+                        make_uint4(0u, 0u, 0u, 0u);
+            if (!PAGED) {
+                // x * 0 is 0 for every number, NaN for the others: one packed
+                // multiply-add per two elements
+                uint32_t seen[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 8
+                for (int i = lane; i < keys * 8; i += 32)
+#pragma unroll
+                    for (int h = 0; h < HALVES; ++h) {
+                        const uint4 x =
+                            *reinterpret_cast<const uint4*>(v + h * KV_HALF + i * 16);
+                        seen[0] = fma2_zero<T>(x.x, seen[0]);
+                        seen[1] = fma2_zero<T>(x.y, seen[1]);
+                        seen[2] = fma2_zero<T>(x.z, seen[2]);
+                        seen[3] = fma2_zero<T>(x.w, seen[3]);
+                    }
+                const bool bad = ((seen[0] | seen[1] | seen[2] | seen[3]) & 0x7fff7fffu) != 0u;
+                if (__any_sync(0xffffffffu, bad)) {
+                    if (lane == 0) ctl.poison[slot] = 1;
+                    for (int i = lane; i < keys * 64; i += 32)
+                        for (int h = 0; h < HALVES; ++h) {
+                            uint16_t* e = reinterpret_cast<uint16_t*>(v + h * KV_HALF) + i;
+                            if ((*e & EXP) == EXP) *e = 0;
+                        }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.kv_full[st]);
+        }
+        at = (at + 2 * n_tiles) % ctl.stages;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.it_free[slot]);
+        if (++slot == kAtItems) {
+            slot = 0;
+            sph ^= 1;
+        }
     }
     __syncwarp();
 }
@@ -585,12 +664,6 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
         if (!ok) break;
         const AttnItem it = ctl.items[slot];
         if (it.done) break;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.it_free[slot]);
-        if (++slot == kAtItems) {
-            slot = 0;
-            sph ^= 1;
-        }
         const int tok = t * QT + r / G;                // within the item
         const bool real = tok < it.rows;
         const bool bad = PAGED && it.split < 0;
@@ -715,6 +788,7 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
             constexpr int COLS = WIDE ? 32 : 64;
             const int warp_row = (warp & 3) * 32;
             const bool all = t * QT + (warp_row + 31) / G < it.rows;
+            const bool poison = !PAGED && ctl.poison[slot] != 0;
             unsigned char* stage = ctl.sOut + warp * 32 * 128;
             unsigned char* own = static_cast<unsigned char*>(PAGED ? p.pre_o : p.out) +
                                  unit * D * (WIDE ? 4 : 2);
@@ -739,6 +813,32 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
                     for (int c = 0; c < 32; ++c)
                         w[c] = pack_out(__uint_as_float(ov[2 * c]) * inv,
                                         __uint_as_float(ov[2 * c + 1]) * inv, p.out_dtype);
+                }
+                if (poison) {
+                    // NaN and infinities that the guard took out of V, from the
+                    // rows that this query sees
+                    const int at = g * COLS;
+#pragma unroll 1
+                    for (int key = it.pos0 / kAtKeys * kAtKeys; key <= min(pos, it.n_keys - 1);
+                         ++key) {
+                        const T* v = static_cast<const T*>(p.v) +
+                                     (size_t)(it.key_row + key) * p.v_stride + it.kvh * D + at;
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            const float x = to_float<T>(v[WIDE ? c : 2 * c]);
+                            const float y = to_float<T>(v[WIDE ? c : 2 * c + 1]);
+                            if (WIDE) {
+                                if (!(fabsf(x) <= 3.4e38f))
+                                    w[c] = __float_as_uint(__uint_as_float(w[c]) + x);
+                            } else if (!(fabsf(x) <= 3.4e38f) || !(fabsf(y) <= 3.4e38f)) {
+                                const float2 o = p.out_dtype == PKV_BF16
+                                                     ? unpack2<__nv_bfloat16>(w[c])
+                                                     : unpack2<__half>(w[c]);
+                                w[c] = pack_out(fabsf(x) <= 3.4e38f ? o.x : o.x + x,
+                                                fabsf(y) <= 3.4e38f ? o.y : o.y + y, p.out_dtype);
+                            }
+                        }
+                    }
                 }
                 if (!bad && g + 1 == D / COLS) {
                     tc_fence_before();
@@ -765,6 +865,12 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
                         o4[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
                 }
             }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.it_free[slot]);
+        if (++slot == kAtItems) {
+            slot = 0;
+            sph ^= 1;
         }
     }
     if (lane == 0) bulk_wait();
@@ -838,6 +944,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             attn_mma<D, T, false, PRECISE>(c, p, lane);
         } else if (warp == 9) {
             attn_loader<D, false>(c, p, tm_q, tm_k, tm_v, lane);
+        } else if (warp == 11) {
+            attn_guard<D, T, false>(c, p, lane);
         } else if (warp == 10) {
             // ---- scheduler; lanes look at 32 items at once
             const bool dynamic = p.dynamic != 0;

@@ -107,6 +107,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             attn_mma<D, T, true, PRECISE>(c, p, lane);
         } else if (warp == 9) {
             attn_loader<D, true>(c, p, tm_q, tm_k, tm_v, lane);
+        } else if (warp == 11) {
+            attn_guard<D, T, true>(c, p, lane);
         } else if (warp == 10) {
             // ---- scheduler; lanes look at 32 candidates at once
             int slot = 0, round = 0;

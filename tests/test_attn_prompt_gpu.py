@@ -149,6 +149,50 @@ def test_rows_of_no_sequence_stay_and_neighbours_do_not_leak():
     assert (out[:lead] == 7).all() and (out[starts[-1]:] == 7).all()
 
 
+@pytest.mark.parametrize("H,Hk,D,dtype,out_dtype", [(4, 2, 128, BF, BF), (8, 1, 64, FP, F32),
+                                                    (2, 2, 128, FP, FP)])
+def test_nan_and_infinities_reach_only_the_queries_that_see_them(H, Hk, D, dtype, out_dtype):
+    """V rows with NaN and infinities: hidden from earlier tokens, they leave
+    no trace there.  Tokens that see them get no number in those columns: NaN,
+    or the infinity -- a weight enters the product as a rounded number, or as
+    the sum of two of which the second may be 0 or negative, and infinity times
+    0, or infinity minus infinity, is NaN."""
+    _clean()
+    lens = [300, 150, 40]
+    starts = _starts(lens)
+    parts, _ = _inputs(starts[-1], H, Hk, D, dtype)
+    q, k, v = [x.clone() for x in parts]
+    inf, nan = float("inf"), float("nan")
+    v[170, 0, 3] = nan
+    v[255, 0, 5] = inf
+    v[299, Hk - 1, 7] = -inf
+    v[starts[1] + 149, 0, 1] = nan                 # the last token of a sequence
+    v[starts[2], Hk - 1, 9] = inf                  # the first one
+    v[starts[2] + 20, Hk - 1, 9] = -inf            # and the opposite: NaN from here
+    k[starts[1] + 100, 0, 2] = nan                 # a key: NaN from its token on
+    out = torch.empty(starts[-1], H, D, dtype=out_dtype, device="cuda")
+    scale = 1 / math.sqrt(D)
+    pkv.attn_prompt(out, q.cuda(), k.cuda(), v.cuda(),
+                    torch.tensor(starts, dtype=torch.int32, device="cuda"), scale, 300)
+    assert _clean() == 0
+    got = out.double().cpu()
+    ok = lambda x: torch.nan_to_num(x.double(), nan=0.0, posinf=0.0, neginf=0.0).to(dtype)  # noqa
+    want, bound = _reference((q, ok(k), ok(v)), starts, scale, out_dtype)
+    for a, b in zip(starts, starts[1:]):
+        for i in range(a, b):
+            for h in range(H):
+                g = h // (H // Hk)
+                if torch.isnan(k[a:i + 1, g]).any():
+                    assert torch.isnan(got[i, h]).all()
+                    continue
+                add = torch.where(torch.isfinite(v[a:i + 1, g]), 0.0, v[a:i + 1, g].double()).sum(0)
+                strange = ~torch.isfinite(add)
+                assert torch.equal(~torch.isfinite(got[i, h]), strange), (i, h)
+                assert torch.isnan(got[i, h][torch.isnan(add)]).all(), (i, h)
+                err = (got[i, h] - want[i, h]).abs()[~strange]
+                assert (err <= bound[i, h][~strange]).all(), (i, h)
+
+
 def test_prompt_flags_bad_bounds():
     _clean()
     _, dev = _inputs(100, 2, 2, 64, BF)
