@@ -50,6 +50,10 @@ cudaError_t encode_out_map(CUtensorMap* map, void* out, pkv_dtype dt, int rows, 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+int attn_item_tiles(int head_dim, pkv_dtype dt, pkv_dtype out_dtype) {
+    return pkv::attn_row_tiles(head_dim, pkv::attn_parts(dt == PKV_BF16, out_dtype == PKV_F32));
+}
+
 int attn_stages(int head_dim, int smem_optin) {
     int stages = 8;
     while (stages > 2 && pkv::attn_tc_smem_bytes(head_dim, stages) > (size_t)smem_optin) --stages;
@@ -92,8 +96,9 @@ PKV_API pkv_status pkv_attn_prompt(void* out, pkv_dtype out_dtype, const void* q
     if ((reinterpret_cast<uintptr_t>(q_start) & 3u) != 0)
         return invalid("q_start must be 4-byte aligned");
     const int G = n_heads / n_kv_heads;
-    const int pair_tokens = 2 * pkv::kAtRows / G;
-    const int tiles = (max_len + pair_tokens - 1) / pair_tokens;
+    const int row_tiles = attn_item_tiles(head_dim, dtype, out_dtype);
+    const int item_tokens = row_tiles * pkv::kAtRows / G;
+    const int tiles = (max_len + item_tokens - 1) / item_tokens;
     const long long per_tile = (long long)n_kv_heads * num_seqs;
     if (per_tile > 0x7fffffffLL) return unsupported("n_kv_heads * num_seqs exceeds 2^31 - 1");
     DeviceInfo* dev = nullptr;
@@ -121,6 +126,7 @@ PKV_API pkv_status pkv_attn_prompt(void* out, pkv_dtype out_dtype, const void* q
     p.group = G;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.stages = attn_stages(head_dim, dev->smem_optin);
+    p.row_tiles = row_tiles;
     p.tiles = tiles;
     p.n_items = per_tile * tiles;
     p.q_start = q_start;
@@ -135,7 +141,7 @@ PKV_API pkv_status pkv_attn_prompt(void* out, pkv_dtype out_dtype, const void* q
     // out in turn, 191 us taken over; prompts of 6.8K and 8K tokens 744 and
     // 707 us).  Where lengths differ so much that most items of the longest
     // sequence's count are empty, the CTAs skip those 32 at a time instead.
-    const long long real = (long long)n_kv_heads * ((long long)total_q / pair_tokens + num_seqs);
+    const long long real = (long long)n_kv_heads * ((long long)total_q / item_tokens + num_seqs);
     p.dynamic = p.n_items > dev->sm_count && p.n_items <= 2 * real && p.n_items <= 0x7fffffffLL;
     L.ctas = (int)(p.dynamic || p.n_items < dev->sm_count ? p.n_items : dev->sm_count);
     L.smem_bytes = pkv::attn_tc_smem_bytes(head_dim, p.stages);

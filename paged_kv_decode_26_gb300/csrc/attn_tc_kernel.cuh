@@ -30,8 +30,8 @@
 // Precision: S, m, l and O are fp32.  P is rounded once to the 16-bit type of
 // V before the second product (at most half an eps relative to each weight,
 // below the rounding of a 16-bit output) -- the rate of that product rests on
-// it -- except for fp32 outputs, where a second product adds the remainder
-// (PRECISE).  The sum l adds the unrounded weights.
+// it -- except for fp32 outputs, where further products add the remainders
+// (PRECISE, attn_parts).  The sum l adds the unrounded weights.
 #pragma once
 
 #include "multi_query_tc_kernel.cuh"
@@ -57,7 +57,8 @@ struct AttnParams {
     int group;
     float scale_log2;
     int stages;                // slots of the K/V ring
-    int tiles;                 // pairs of row tiles of the longest sequence / largest group
+    int row_tiles;             // row tiles per work item: 2, or 1
+    int tiles;                 // items of row tiles of the longest sequence / largest group
     long long n_items;
     int dynamic;               // prompts: one CTA per item, running CTAs take over waiting ones
     // whole prompts
@@ -120,6 +121,21 @@ struct AttnSizes {
     [[maybe_unused]] constexpr uint32_t Q_BYTES = AttnSizes<D>::Q_BYTES;                      \
     [[maybe_unused]] constexpr uint32_t TILE_COLS = AttnSizes<D>::TILE_COLS;                  \
     [[maybe_unused]] constexpr uint32_t S_COL = AttnSizes<D>::S_COL;
+
+// 16-bit parts whose sum stands for a softmax weight in the second product,
+// and the tensor-memory column of part k.  fp32 outputs take as many as fp32
+// needs: two of fp16 (22 bits), three of bf16 (24).  The first two fill the
+// columns of S; the third lies behind them, or, at D = 128, in the S columns of
+// row tile 1: a CTA then works on one row tile at a time.
+__host__ __device__ constexpr int attn_parts(bool bf16, bool precise) {
+    return precise ? (bf16 ? 3 : 2) : 1;
+}
+__host__ __device__ constexpr int attn_row_tiles(int D, int parts) {
+    return D == 128 && parts == 3 ? 1 : 2;
+}
+__host__ __device__ constexpr uint32_t attn_part_col(int D, int k) {
+    return k < 2 ? D + k * 64 : (D == 64 ? D + 128 : 256 + D);
+}
 
 // Barriers and item slots of one CTA, behind the tiles in shared memory.
 struct AttnControl {
@@ -235,6 +251,16 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
+}
+
+__device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15])
+        : "memory");
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -480,6 +506,7 @@ __device__ __forceinline__ void attn_guard(const AttnControl& ctl, const AttnPar
 template <int D, typename T, bool PAGED, bool PRECISE>
 __device__ __forceinline__ void attn_mma(const AttnControl& ctl, const AttnParams& p, int lane) {
     PKV_ATTN_SIZES(D)
+    constexpr int PARTS = attn_parts(std::is_same<T, __nv_bfloat16>::value, PRECISE);
     const uint32_t id_s = tc_idesc<T>(kAtRows, kAtKeys, 0);
     const uint32_t id_o = tc_idesc<T>(kAtRows, D, 1);
     const uint64_t dq0 = tc_desc_sw128(smem_addr(ctl.sQ), 16, 1024);
@@ -585,11 +612,11 @@ __device__ __forceinline__ void attn_mma(const AttnControl& ctl, const AttnParam
                             const uint32_t o = ctl.tmem + t * TILE_COLS;
                             const uint64_t v = dv0 + (uint64_t)(vs * (KV_BYTES >> 4));
 #pragma unroll
-                            for (int part = 0; part < (PRECISE ? 2 : 1); ++part)
+                            for (int part = 0; part < PARTS; ++part)
 #pragma unroll
                                 for (int i = half * 4; i < half * 4 + 4; ++i)
                                     at_mma_tmem_a(
-                                        o, o + S_COL + part * (kAtKeys / 2) + i * 8,
+                                        o, o + attn_part_col(D, part) + i * 8,
                                         v + (uint64_t)((i * 16 * 128) >> 4), id_o,
                                         (j > 0 || part > 0 || i > 0) ? 1u : 0u, lead);
                             if (half && j + 1 == nt) at_commit(&ctl.o_full[t], lead);
@@ -648,6 +675,7 @@ template <int D, typename T, bool PAGED, bool PRECISE>
 __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnParams& p,
                                              const CUtensorMap& tm_o, int warp, int lane) {
     PKV_ATTN_SIZES(D)
+    constexpr int PARTS = attn_parts(std::is_same<T, __nv_bfloat16>::value, PRECISE);
     const int G = p.group;
     const int QT = kAtRows / G;
     const int t = warp >> 2;
@@ -740,27 +768,37 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
                 const float mu = m_used == -INFINITY ? 0.f : m_used;
                 const float2 aa = make_float2(a, a), nmu = make_float2(-mu, -mu);
                 const float2 neg1 = make_float2(-1.f, -1.f);
+                // 32 keys at a time (two stores per arrival), or 64
+                constexpr int N = PARTS > 1 ? 16 : 32;
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t hi[32], lo[PRECISE ? 32 : 1];
+                for (int part = 0; part < 64 / N; ++part) {
+                    uint32_t w[PARTS][N];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int c = half * 64 + 2 * i;
+                    for (int i = 0; i < N; ++i) {
+                        const int c = 2 * (part * N + i);
                         const float2 e = __ffma2_rn(make_float2(y[c], y[c + 1]), aa, nmu);
-                        const float2 pv = make_float2(exp2f(e.x), exp2f(e.y));
+                        float2 pv = make_float2(exp2f(e.x), exp2f(e.y));
                         l4[i & 3] = __fadd2_rn(l4[i & 3], pv);
-                        hi[i] = pack2<T>(pv.x, pv.y);
-                        if (PRECISE) {
-                            const float2 rest = __ffma2_rn(unpack2<T>(hi[i]), neg1, pv);
-                            lo[PRECISE ? i : 0] = pack2<T>(rest.x, rest.y);
+#pragma unroll
+                        for (int k = 0; k < PARTS; ++k) {
+                            w[k][i] = pack2<T>(pv.x, pv.y);
+                            pv = __ffma2_rn(unpack2<T>(w[k][i]), neg1, pv);
                         }
                     }
-                    tc_st32(t_lane + S_COL + half * 32, hi);
-                    if (PRECISE) tc_st32(t_lane + S_COL + 64 + half * 32, lo);
-                    tc_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctl.p_full[2 * t + half]);
+#pragma unroll
+                    for (int k = 0; k < PARTS; ++k) {
+                        const uint32_t col = t_lane + attn_part_col(D, k) + part * N;
+                        if (N == 32)
+                            tc_st32(col, w[k]);
+                        else
+                            tc_st16(col, w[k]);
+                    }
+                    if ((part + 1) * N % 32 == 0) {
+                        tc_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ctl.p_full[2 * t + (part + 1) * N / 32 - 1]);
+                    }
                 }
             }
             if (!ok) break;
@@ -893,17 +931,18 @@ __device__ __forceinline__ bool attn_prompt_item(const AttnParams& p, long long 
         if (back == 0 && it.kvh == 0) raise_error(p.errors, PKV_DEVERR_CONTEXT);
         return false;
     }
-    const int lo = ((len + 2 * QT - 1) / (2 * QT) - 1 - back) * 2 * QT;
+    const int NT = p.row_tiles * QT;         // tokens per item
+    const int lo = ((len + NT - 1) / NT - 1 - back) * NT;
     if (lo < 0 || len == 0) return false;
     it.row0 = q0 + lo;
-    it.rows = len - lo;
+    it.rows = min(len - lo, NT);
     it.pos0 = lo;
     it.key_row = q0;
     it.key0 = 0;
     it.n_keys = len;
     it.split = 0;
     it.nt[0] = (min(len, lo + QT) + kAtKeys - 1) / kAtKeys;
-    it.nt[1] = lo + QT < len ? (min(len, lo + 2 * QT) + kAtKeys - 1) / kAtKeys : 0;
+    it.nt[1] = it.rows > QT ? (min(len, lo + 2 * QT) + kAtKeys - 1) / kAtKeys : 0;
     return true;
 }
 

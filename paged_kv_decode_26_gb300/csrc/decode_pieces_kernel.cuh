@@ -156,7 +156,7 @@ struct NoScores {
 // score exceeds it by more than 2^8 -- the common chunk then needs one vote
 // instead of the maximum over the lanes, and no rescaling of O.
 constexpr float kPieceGrow = 8.0f;
-template <int D, typename T, class Scores>
+template <int D, typename T, bool THIRD, class Scores>
 __device__ __forceinline__ void piece_chunk(MmaHeads<D>& st, uint32_t kbase, uint32_t vbase,
                                             int valid, float scale_log2, int lane,
                                             const Scores& scores) {
@@ -214,7 +214,8 @@ __device__ __forceinline__ void piece_chunk(MmaHeads<D>& st, uint32_t kbase, uin
     st.l[0] += p0 + p2;
     st.l[1] += p1 + p3;
     // P in two 16-bit parts (hi = round(p), lo = round(p - hi)), packed by
-    // token: (head 2 tig, head 2 tig + 1) of token gid and of token gid + 8
+    // token: (head 2 tig, head 2 tig + 1) of token gid and of token gid + 8;
+    // with THIRD the rest too (bf16 for an fp32 output: 24 bits)
     const uint32_t hA = pack2<T>(p0, p1), hB = pack2<T>(p2, p3);
     const float2 fA = unpack2<T>(hA), fB = unpack2<T>(hB);
     const uint32_t lA = pack2<T>(p0 - fA.x, p1 - fA.y), lB = pack2<T>(p2 - fB.x, p3 - fB.y);
@@ -230,6 +231,18 @@ __device__ __forceinline__ void piece_chunk(MmaHeads<D>& st, uint32_t kbase, uin
     // (keys 2 tig, 2 tig + 1) -> low / high half of one register
     const uint32_t bh0 = __byte_perm(hAa, hAb, sel), bh1 = __byte_perm(hBa, hBb, sel);
     const uint32_t bl0 = __byte_perm(lAa, lAb, sel), bl1 = __byte_perm(lBa, lBb, sel);
+    uint32_t bt0 = 0u, bt1 = 0u;
+    if (THIRD) {
+        const float2 gA = unpack2<T>(lA), gB = unpack2<T>(lB);
+        const uint32_t tA = pack2<T>(p0 - fA.x - gA.x, p1 - fA.y - gA.y);
+        const uint32_t tB = pack2<T>(p2 - fB.x - gB.x, p3 - fB.y - gB.y);
+        const uint32_t tAa = __shfl_sync(0xffffffffu, tA, srcA);
+        const uint32_t tAb = __shfl_sync(0xffffffffu, tA, srcB);
+        const uint32_t tBa = __shfl_sync(0xffffffffu, tB, srcA);
+        const uint32_t tBb = __shfl_sync(0xffffffffu, tB, srcB);
+        bt0 = __byte_perm(tAa, tAb, sel);
+        bt1 = __byte_perm(tBa, tBb, sel);
+    }
     // ---- O^T += V^T P^T; V rows past the context may hold anything (NaN
     // included): P is 0 there, but 0 * NaN is not, so those rows are cleared
     // in the A fragments (tokens 2 tig, 2 tig + 1 in a0/a1, 2 tig + 8, 2 tig +
@@ -246,6 +259,7 @@ __device__ __forceinline__ void piece_chunk(MmaHeads<D>& st, uint32_t kbase, uin
         const uint32_t a[4] = {b0 & vm0, b2 & vm0, b1 & vm1, b3 & vm1};
         mma16816<T>(st.o[j], a, bh0, bh1);
         mma16816<T>(st.o[j], a, bl0, bl1);
+        if (THIRD) mma16816<T>(st.o[j], a, bt0, bt1);
     }
 }
 
@@ -512,8 +526,8 @@ struct PieceNext {
 // group.  WEIGHTS: scores go to the workspace and whole (sequence, head)s
 // straight to the output; otherwise every piece goes to the workspace, where
 // the prefix joins it.  The loads run kPieceStages chunks ahead, over the end
-// of a run into the next one.
-template <int D, typename T, bool WEIGHTS, bool TAKES>
+// of a run into the next one.  THIRD: see piece_chunk.
+template <int D, typename T, bool WEIGHTS, bool TAKES, bool THIRD>
 __device__ __forceinline__ void piece_worker(const PieceParams& p, const CUtensorMap& tm_k,
                                              const CUtensorMap& tm_v, const PieceShared& sh,
                                              const PieceRuns& runs, const PieceNext& next) {
@@ -665,10 +679,11 @@ __device__ __forceinline__ void piece_worker(const PieceParams& p, const CUtenso
                 const StoreScores sink{2 * tig < p.group ? row : nullptr,
                                        2 * tig + 1 < p.group ? row + p.score_stride : nullptr,
                                        at.c * kPieceTokens + gid, at.n};
-                piece_chunk<D, T>(state, kbase, kbase + HALF, valid, p.scale_log2, lane, sink);
+                piece_chunk<D, T, THIRD>(state, kbase, kbase + HALF, valid, p.scale_log2, lane,
+                                         sink);
             } else {
-                piece_chunk<D, T>(state, kbase, kbase + HALF, valid, p.scale_log2, lane,
-                                  NoScores());
+                piece_chunk<D, T, THIRD>(state, kbase, kbase + HALF, valid, p.scale_log2, lane,
+                                         NoScores());
             }
         } else if (WEIGHTS) {
             // a missing block's tokens weigh nothing
@@ -731,7 +746,7 @@ inline size_t decode_pieces_smem_bytes(int D) {
 // with in a tenth of a millisecond gains nothing from them -- every run adds a
 // piece to merge (8 contexts of 8K-32K tokens, grouped heads: 124 us without,
 // 138 us with).
-template <int D, typename T, bool WEIGHTS, bool TAKES>
+template <int D, typename T, bool WEIGHTS, bool TAKES, bool THIRD>
 __global__ void __launch_bounds__(kPieceThreads + (TAKES ? 32 : 0), 1)
     decode_pieces_kernel(const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v,
@@ -760,7 +775,7 @@ __global__ void __launch_bounds__(kPieceThreads + (TAKES ? 32 : 0), 1)
     if (warp < kPieceWarps) chunks = piece_plan<WEIGHTS>(p, sh);
     if (TAKES) __syncthreads();
     if (warp < kPieceWarps) {
-        piece_worker<D, T, WEIGHTS, TAKES>(p, tm_k, tm_v, sh, piece_runs(p, chunks), next);
+        piece_worker<D, T, WEIGHTS, TAKES, THIRD>(p, tm_k, tm_v, sh, piece_runs(p, chunks), next);
     } else {
         for (int k = 0;; ++k) {
             int cta = -1;

@@ -26,7 +26,7 @@ __device__ __forceinline__ bool attn_prefix_candidate(const AttnParams& a, long 
     const bool valid = g0 >= 0 && g1 >= g0 && g1 <= a.num_seqs && g1 - g0 <= a.max_group &&
                        pl >= 0 && pl <= a.max_prefix && pl % a.block_size == 0;
     if (!valid && tile == 0 && split == 0 && kvh == 0) raise_error(a.errors, PKV_DEVERR_CONTEXT);
-    return valid && g0 + tile * 2 * QT < g1 && (long long)split * a.split_tokens < pl;
+    return valid && g0 + tile * a.row_tiles * QT < g1 && (long long)split * a.split_tokens < pl;
 }
 
 // The item of a candidate, by a whole warp; false: no member holds the prefix.
@@ -53,9 +53,9 @@ __device__ __forceinline__ bool attn_prefix_item(const AttnParams& a, long long 
     if (m < 0) return false;
     it.done = 0;
     it.kvh = kvh;
-    const int lo = tile * 2 * QT;
+    const int NT = a.row_tiles * QT, lo = tile * NT;
     it.row0 = g0 + lo;
-    it.rows = g1 - g0 - lo;
+    it.rows = min(g1 - g0 - lo, NT);
     it.pos0 = 0;
     it.key_row = m;
     it.key0 = split * a.split_tokens;

@@ -20,7 +20,6 @@ namespace {
 constexpr int kSplitCost = 4;
 
 struct SharedShape {
-    int tiles;
     int split_tokens;
     int max_splits;
     PiecesGrid grid;      // of the rest of the contexts
@@ -33,8 +32,8 @@ SharedShape shared_shape(int num_seqs, int num_groups, int max_group, int max_pr
     SharedShape c;
     const int G = n_heads / n_kv_heads;
     const int pair_rows = 2 * pkv::kAtRows / G;
-    c.tiles = max_group > 0 ? (max_group + pair_rows - 1) / pair_rows : 0;
-    const long long units = (long long)num_groups * n_kv_heads * c.tiles;
+    const int pairs = max_group > 0 ? (max_group + pair_rows - 1) / pair_rows : 0;
+    const long long units = (long long)num_groups * n_kv_heads * pairs;
     c.max_splits = 0;
     c.split_tokens = pkv::kAtKeys;
     if (units > 0 && max_prefix > 0) {
@@ -157,7 +156,9 @@ PKV_API pkv_status paged_attn_decode_shared(
     a.group = G;
     a.scale_log2 = p.scale_log2;
     a.stages = attn_stages(head_dim, dev->smem_optin);
-    a.tiles = c.tiles;
+    a.row_tiles = attn_item_tiles(head_dim, kv_dtype, out_dtype);
+    const int item_rows = a.row_tiles * pkv::kAtRows / G;
+    a.tiles = (max_group + item_rows - 1) / item_rows;
     a.group_start = group_start;
     a.prefix_lens = prefix_lens;
     a.max_group = max_group;
@@ -179,7 +180,7 @@ PKV_API pkv_status paged_attn_decode_shared(
                                 unit * n_heads, G)))
             return cuda_fail(e);
         a.num_groups = p.num_groups = num_groups;
-        a.n_items = (long long)num_groups * n_kv_heads * c.tiles * c.max_splits;
+        a.n_items = (long long)num_groups * n_kv_heads * a.tiles * c.max_splits;
         L.prefix_ctas = (int)(a.n_items < dev->sm_count ? a.n_items : dev->sm_count);
     }
     const bool precise = out_dtype == PKV_F32;
