@@ -532,7 +532,8 @@ PKV_API pkv_status kv_evict(void* k_pool, void* v_pool, pkv_dtype dtype,
  * flagged PKV_DEVERR_CONTEXT and its members are decoded alone.  A split of a
  * prefix with a block outside the pool is left out and flagged
  * PKV_DEVERR_BLOCK_ID.  Softmax weights of the prefix enter the second product
- * rounded to kv_dtype, except for F32 outputs.  Supported shapes as
+ * rounded to kv_dtype, except for F32 outputs (as the sum of two F16 or three
+ * BF16 parts).  Supported shapes as
  * paged_attn_decode; at most 65535 sequences, 65535 groups, 4096 query heads.
  * Three launches.
  */
@@ -571,7 +572,7 @@ PKV_API pkv_status paged_attn_decode_shared(
  * A sequence whose bounds lie outside the tokens or whose length exceeds
  * max_len is left out (its rows are not written) and flagged
  * PKV_DEVERR_CONTEXT.  The softmax weights enter the second product rounded to
- * dtype, except for F32 outputs (hi + lo parts, as in the other calls).  NaN and
+ * dtype, except for F32 outputs (as the sum of two F16 or three BF16 parts).  NaN and
  * infinities in rows of k and v reach only the tokens that see those rows (an
  * infinity in v as an infinity or NaN).  One launch, no workspace.
  */

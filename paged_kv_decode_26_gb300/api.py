@@ -435,12 +435,14 @@ def _rows_stride(name: str, t: torch.Tensor, rows: int) -> int:
 def _need_here(names, tensors) -> None:
     """Every tensor contiguous and on the current CUDA device (where the
     library launches)."""
-    cur = _current_device()
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t.get_device() != cur or not t.is_contiguous():
+        if t.get_device() != dev or dev < 0 or not t.is_contiguous():
             for name, u in zip(names, tensors):
                 _need_cuda(name, u)
             raise ValueError("tensors must be on the current CUDA device")
+    if dev != _current_device():
+        raise ValueError("tensors must be on the current CUDA device")
 
 
 def _need_ints(names, tensors) -> None:

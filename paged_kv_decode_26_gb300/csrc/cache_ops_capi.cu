@@ -215,7 +215,7 @@ PKV_API pkv_status paged_attn_decode_weights(
     if (st != PKV_OK) return st;
     if (weight_stride < max_context_len) return invalid("weight_stride below max_context_len");
     if (num_seqs == 0) return PKV_OK;
-    if (!weights) return invalid("weights is NULL");
+    if (!weights && max_context_len > 0) return invalid("weights is NULL");
     if ((reinterpret_cast<uintptr_t>(weights) & 3u) != 0) return invalid("weights must be 4-byte aligned");
     DeviceInfo* dev = nullptr;
     cudaError_t e = device_info(&dev);

@@ -299,3 +299,125 @@ def test_evict_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, outs)) and torch.equal(kp, pool)
+
+
+# ----------------------------------------------- refusals that need a device
+
+def test_workspaces_too_small_or_misaligned_are_refused():
+    c = _problem([40, 9], 4, 2, 64, 16, BF)
+    q = c["q"].cuda()
+    out = torch.full((2, 4, 64), 7.0, dtype=BF, device="cuda")
+    w = torch.zeros(2, 40, device="cuda")
+    groups = torch.tensor([0, 2], dtype=torch.int32, device="cuda")
+    prefix = torch.tensor([0], dtype=torch.int32, device="cuda")
+    n_w = pkv.decode_weights_workspace_bytes(2, 4, 2, 64, 16, 40)
+    n_s = pkv.decode_shared_workspace_bytes(2, 1, 2, 16, 4, 2, 64, 16, 40)
+    buf = torch.empty(max(n_w, n_s) + 512, dtype=torch.uint8, device="cuda")
+    for n, call in (
+            (n_w, lambda ws: pkv.paged_attn_decode_weights(
+                out, q, c["k_pool"], c["v_pool"], c["tables"], c["lens"], w, 0.1, 40,
+                workspace=ws)),
+            (n_s, lambda ws: pkv.paged_attn_decode_shared(
+                out, q, c["k_pool"], c["v_pool"], c["tables"], c["lens"], groups, prefix, 0.1, 40,
+                2, 16, workspace=ws))):
+        with pytest.raises(pkv.PagedKVError) as e:
+            call(buf[:n - 1])
+        assert e.value.status == _lib.PKV_ERR_WORKSPACE
+        with pytest.raises(pkv.PagedKVError) as e:
+            call(buf[16:])
+        assert e.value.status == _lib.PKV_ERR_INVALID
+        assert (out == 7).all()
+        call(buf[:n])
+        assert torch.isfinite(out).all() and not (out == 7).all()
+        out.fill_(7.0)
+    assert _clean() == 0
+
+
+def test_binding_refuses_bad_tensors():
+    c = _problem([40, 9], 4, 2, 64, 16, BF)
+    q = c["q"].cuda()
+    out = torch.empty(2, 4, 64, dtype=BF, device="cuda")
+    ok = dict(out=out, q=q, k_pool=c["k_pool"], v_pool=c["v_pool"], block_tables=c["tables"],
+              context_lens=c["lens"], weights=torch.zeros(2, 40, device="cuda"), scale=0.1,
+              max_context_len=40)
+    for name, bad in (("weights", torch.zeros(2, 39, device="cuda")),
+                      ("weights", torch.zeros(3, 40, device="cuda")),
+                      ("weights", torch.zeros(2, 40, dtype=torch.float64, device="cuda")),
+                      ("weights", torch.zeros(40, 2, device="cuda").t()),
+                      ("weights", torch.zeros(1, 40, device="cuda").expand(2, 40)),
+                      ("weights", torch.zeros(2, 40)),
+                      ("context_lens", c["lens"].long()), ("q", q[:, :, ::2]),
+                      ("out", out[:1]), ("v_pool", c["v_pool"].half())):
+        with pytest.raises(ValueError):
+            pkv.paged_attn_decode_weights(**{**ok, name: bad})
+
+
+def test_two_streams_at_once():
+    """The same call on two streams, a workspace each, interleaved."""
+    cases = [_problem([700, 33, 260], 8, 2, 128, 16, BF, seed=s) for s in (1, 2)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    want, got = [], []
+    for c in cases:
+        c["qd"] = c["q"].cuda()
+        out, w = torch.empty(3, 8, 128, dtype=BF, device="cuda"), torch.zeros(3, 700, device="cuda")
+        pkv.paged_attn_decode_weights(out, c["qd"], c["k_pool"], c["v_pool"], c["tables"],
+                                      c["lens"], w, c["scale"], 700)
+        want.append((out, w))
+        got.append((torch.empty_like(out), torch.zeros_like(w)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (out, w), c, s in zip(got, cases, streams):
+            with torch.cuda.stream(s):
+                w.zero_()
+                pkv.paged_attn_decode_weights(out, c["qd"], c["k_pool"], c["v_pool"], c["tables"],
+                                              c["lens"], w, c["scale"], 700)
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_no_context_at_all():
+    out = torch.full((2, 4, 64), 7.0, dtype=BF, device="cuda")
+    q = torch.randn(2, 4, 64, device="cuda").to(BF)
+    pool = torch.empty(0, 16, 2, 64, dtype=BF, device="cuda")
+    lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+    tables = torch.full((2, 1), -1, dtype=torch.int32, device="cuda")
+    pkv.paged_attn_decode_weights(out, q, pool, pool, tables, lens,
+                                  torch.zeros(2, 0, device="cuda"), 0.1, 0)
+    assert _clean() == 0 and (out == 0).all()
+    out.fill_(7.0)
+    pkv.paged_attn_decode_shared(out, q, pool, pool, tables, lens, lens[:1], lens[:0], 0.1, 0, 0, 0)
+    assert _clean() == 0 and (out == 0).all()
+
+
+def test_pools_beyond_four_gigabytes():
+    """Pages whose byte offsets pass 32 bits: a decode, an accumulation and an
+    eviction that reads and writes at both ends of the pool."""
+    B, Hk, D, blocks = 32, 16, 128, 36000          # 4.7 GB per pool
+    kp = torch.zeros(blocks, B, Hk, D, dtype=BF, device="cuda")
+    vp = torch.zeros_like(kp)
+    ids = [35999, 0, 35998, 1]
+    n = 4 * B - 5
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randn(4 * B, Hk, D, generator=g).to(BF) for _ in range(2))
+    for j, b in enumerate(ids):
+        kp[b], vp[b] = k[j * B:(j + 1) * B].cuda(), v[j * B:(j + 1) * B].cuda()
+    q = torch.randn(1, 32, D, generator=g).to(BF)
+    tables = torch.tensor([ids], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    out = torch.empty(1, 32, D, dtype=BF, device="cuda")
+    w = torch.zeros(1, n, device="cuda")
+    scale = 1 / math.sqrt(D)
+    pkv.paged_attn_decode_weights(out, q.cuda(), kp, vp, tables, lens, w, scale, n)
+    o, bound, ws = ref.decode(q, [k[:n]], [v[:n]], scale, BF)
+    ref.check(out, o, bound)
+    ref.check(w[0], ws[0][0], ws[0][1] + 1e-7)
+    new = torch.tensor([[35997, 2]], dtype=torch.int32, device="cuda")
+    nl, kept = torch.zeros_like(lens), torch.zeros(1, 50, dtype=torch.int32, device="cuda")
+    pkv.kv_evict(kp, vp, tables, lens, w, new, nl, torch.zeros(1, 50, device="cuda"), kept, 50, 7)
+    assert _clean() == 0
+    idx = ref.evict(w[0].tolist(), n, 50, 7)
+    assert kept[0].tolist() == idx
+    got = torch.cat([kp[35997], kp[2]])[:50].cpu()
+    assert torch.equal(got, k[idx])
+    assert torch.equal(torch.cat([vp[35997], vp[2]])[:50].cpu(), v[idx])

@@ -193,3 +193,24 @@ def test_shared_workspace_bytes(L):
     assert f(4, 1, 4, 101, 8, 8, 128, 16, 100) == 0         # a prefix beyond the context
     assert f(4, 0, 0, 0, 8, 8, 128, 16, 100) > 0
     assert f(64, 1, 64, 4096, 8, 8, 128, 16, 5000) > f(64, 0, 0, 0, 8, 8, 128, 16, 5000)
+
+
+def _cpu(*shape, dtype=torch.bfloat16):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+def test_binding_refuses_tensors_that_are_not_on_the_gpu(L):
+    """Checked before anything touches a device."""
+    import paged_kv_decode_26_gb300 as pkv
+    out, q = _cpu(2, 4, 64), _cpu(2, 4, 64)
+    pool, tables, lens = _cpu(4, 16, 2, 64), _ints([[0, 1], [2, 3]]), _ints([20, 30])
+    w = torch.zeros(2, 32)
+    for call in (
+            lambda: pkv.attn_prompt(out, q, q[:, :2], q[:, :2], _ints([0, 2]), 0.1, 2),
+            lambda: pkv.paged_attn_decode_weights(out, q, pool, pool, tables, lens, w, 0.1, 32),
+            lambda: pkv.paged_attn_decode_shared(out, q, pool, pool, tables, lens, _ints([0, 2]),
+                                                 _ints([16]), 0.1, 32, 2, 16),
+            lambda: pkv.kv_evict(pool, pool, tables, lens, w, tables, lens.clone(), w.clone(),
+                                 _ints([[0] * 8] * 2), 8, 2)):
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            call()
