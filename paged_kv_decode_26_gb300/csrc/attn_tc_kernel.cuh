@@ -29,13 +29,15 @@
 //
 // Precision: S, m, l and O are fp32.  P is rounded once to the 16-bit type of
 // V before the second product (at most half an eps relative to each weight,
-// below the rounding of a 16-bit output) -- the rate of that product rests on
+// below the rounding of a 16-bit output; weight_range.cuh keeps fp16 weights
+// clear of its smallest numbers) -- the rate of that product rests on
 // it -- except for fp32 outputs, where further products add the remainders
 // (PRECISE, attn_parts).  The sum l adds the unrounded weights.
 #pragma once
 
 #include "multi_query_tc_kernel.cuh"
 #include "take_over.cuh"
+#include "weight_range.cuh"
 
 namespace pkv {
 
@@ -676,6 +678,7 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
                                              const CUtensorMap& tm_o, int warp, int lane) {
     PKV_ATTN_SIZES(D)
     constexpr int PARTS = attn_parts(std::is_same<T, __nv_bfloat16>::value, PRECISE);
+    using Range = WeightRange<T>;
     const int G = p.group;
     const int QT = kAtRows / G;
     const int t = warp >> 2;
@@ -737,11 +740,12 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
                                       fmaxf(m8[6], m8[7]));
                 const float tmax = mx * a;
                 const bool first = m_used == -INFINITY;
-                const bool grow = tmax > m_used + kTcRescale;
+                const bool grow = tmax > m_used + (Range::LIFT + Range::GROW);
                 float alpha = 1.f;
                 if (grow) {
-                    alpha = first ? 1.f : exp2f(m_used - tmax);
-                    m_used = tmax;
+                    const float m_new = tmax - Range::LIFT;
+                    alpha = first ? 1.f : exp2f(m_used - m_new);
+                    m_used = m_new;
                 }
                 if (__any_sync(0xffffffffu, grow && !first)) {
                     // O is at rest: the products up to key tile j - 1

@@ -31,6 +31,7 @@
 
 #include "decode_mma_kernel.cuh"
 #include "take_over.cuh"
+#include "weight_range.cuh"
 
 namespace pkv {
 
@@ -152,10 +153,9 @@ struct NoScores {
 // kv head's K and V, swizzled [16 x 128 B] boxes at kbase / vbase, into the
 // state of its query heads: mma_heads_chunk with two differences that shorten
 // the chain of a chunk (a warp waits for nothing else): the score products
-// run in two accumulators, and the running maximum is an older one until a
-// score exceeds it by more than 2^8 -- the common chunk then needs one vote
-// instead of the maximum over the lanes, and no rescaling of O.
-constexpr float kPieceGrow = 8.0f;
+// run in two accumulators, and the state's maximum is a reference that stays
+// until a score exceeds its range (weight_range.cuh) -- the common chunk then
+// needs one vote instead of the maximum over the lanes, and no rescaling of O.
 template <int D, typename T, bool THIRD, class Scores>
 __device__ __forceinline__ void piece_chunk(MmaHeads<D>& st, uint32_t kbase, uint32_t vbase,
                                             int valid, float scale_log2, int lane,
@@ -185,14 +185,16 @@ __device__ __forceinline__ void piece_chunk(MmaHeads<D>& st, uint32_t kbase, uin
     const float x2 = v1 ? (s0[2] + s1[2]) * scale_log2 : -INFINITY;
     const float x3 = v1 ? (s0[3] + s1[3]) * scale_log2 : -INFINITY;
     scores(x0, x1, x2, x3);
+    using Range = WeightRange<T>;
+    constexpr float MOST = Range::LIFT + Range::GROW;
     float c0 = fmaxf(x0, x2), c1 = fmaxf(x1, x3);
-    if (__any_sync(0xffffffffu, c0 > st.m[0] + kPieceGrow || c1 > st.m[1] + kPieceGrow)) {
+    if (__any_sync(0xffffffffu, c0 > st.m[0] + MOST || c1 > st.m[1] + MOST)) {
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
             c0 = fmaxf(c0, __shfl_xor_sync(0xffffffffu, c0, off));
             c1 = fmaxf(c1, __shfl_xor_sync(0xffffffffu, c1, off));
         }
-        const float m0 = fmaxf(st.m[0], c0), m1 = fmaxf(st.m[1], c1);
+        const float m0 = fmaxf(st.m[0], c0 - Range::LIFT), m1 = fmaxf(st.m[1], c1 - Range::LIFT);
         const float al0 = m0 == -INFINITY ? 1.f : exp2f(st.m[0] - m0);
         const float al1 = m1 == -INFINITY ? 1.f : exp2f(st.m[1] - m1);
         st.m[0] = m0;
@@ -224,10 +226,11 @@ __device__ __forceinline__ void piece_chunk(MmaHeads<D>& st, uint32_t kbase, uin
     // 4 (2 tig) + gid / 2 and 4 (2 tig + 1) + gid / 2 hold (half gid % 2)
     const int srcA = 4 * (2 * tig) + (gid >> 1), srcB = srcA + 4;
     const uint32_t sel = (gid & 1) ? 0x7632u : 0x5410u;   // the half of this lane's head
-    const uint32_t hAa = __shfl_sync(0xffffffffu, hA, srcA), hAb = __shfl_sync(0xffffffffu, hA, srcB);
-    const uint32_t hBa = __shfl_sync(0xffffffffu, hB, srcA), hBb = __shfl_sync(0xffffffffu, hB, srcB);
-    const uint32_t lAa = __shfl_sync(0xffffffffu, lA, srcA), lAb = __shfl_sync(0xffffffffu, lA, srcB);
-    const uint32_t lBa = __shfl_sync(0xffffffffu, lB, srcA), lBb = __shfl_sync(0xffffffffu, lB, srcB);
+    auto from = [](uint32_t x, int src) { return __shfl_sync(0xffffffffu, x, src); };
+    const uint32_t hAa = from(hA, srcA), hAb = from(hA, srcB);
+    const uint32_t hBa = from(hB, srcA), hBb = from(hB, srcB);
+    const uint32_t lAa = from(lA, srcA), lAb = from(lA, srcB);
+    const uint32_t lBa = from(lB, srcA), lBb = from(lB, srcB);
     // (keys 2 tig, 2 tig + 1) -> low / high half of one register
     const uint32_t bh0 = __byte_perm(hAa, hAb, sel), bh1 = __byte_perm(hBa, hBb, sel);
     const uint32_t bl0 = __byte_perm(lAa, lAb, sel), bl1 = __byte_perm(lBa, lBb, sel);
@@ -236,12 +239,8 @@ __device__ __forceinline__ void piece_chunk(MmaHeads<D>& st, uint32_t kbase, uin
         const float2 gA = unpack2<T>(lA), gB = unpack2<T>(lB);
         const uint32_t tA = pack2<T>(p0 - fA.x - gA.x, p1 - fA.y - gA.y);
         const uint32_t tB = pack2<T>(p2 - fB.x - gB.x, p3 - fB.y - gB.y);
-        const uint32_t tAa = __shfl_sync(0xffffffffu, tA, srcA);
-        const uint32_t tAb = __shfl_sync(0xffffffffu, tA, srcB);
-        const uint32_t tBa = __shfl_sync(0xffffffffu, tB, srcA);
-        const uint32_t tBb = __shfl_sync(0xffffffffu, tB, srcB);
-        bt0 = __byte_perm(tAa, tAb, sel);
-        bt1 = __byte_perm(tBa, tBb, sel);
+        bt0 = __byte_perm(from(tA, srcA), from(tA, srcB), sel);
+        bt1 = __byte_perm(from(tB, srcA), from(tB, srcB), sel);
     }
     // ---- O^T += V^T P^T; V rows past the context may hold anything (NaN
     // included): P is 0 there, but 0 * NaN is not, so those rows are cleared
@@ -250,7 +249,7 @@ __device__ __forceinline__ void piece_chunk(MmaHeads<D>& st, uint32_t kbase, uin
     uint32_t vm0 = 0xffffffffu, vm1 = 0xffffffffu;
     if (valid < kPieceTokens) {
         vm0 = (tig * 2 < valid ? 0x0000ffffu : 0u) | (tig * 2 + 1 < valid ? 0xffff0000u : 0u);
-        vm1 = (8 + tig * 2 < valid ? 0x0000ffffu : 0u) | (8 + tig * 2 + 1 < valid ? 0xffff0000u : 0u);
+        vm1 = (tig * 2 + 8 < valid ? 0x0000ffffu : 0u) | (tig * 2 + 9 < valid ? 0xffff0000u : 0u);
     }
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) {
