@@ -50,10 +50,6 @@ cudaError_t encode_out_map(CUtensorMap* map, void* out, pkv_dtype dt, int rows, 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-int attn_item_tiles(int head_dim, pkv_dtype dt, pkv_dtype out_dtype) {
-    return pkv::attn_row_tiles(head_dim, pkv::attn_parts(dt == PKV_BF16, out_dtype == PKV_F32));
-}
-
 int attn_stages(int head_dim, int smem_optin) {
     int stages = 8;
     while (stages > 2 && pkv::attn_tc_smem_bytes(head_dim, stages) > (size_t)smem_optin) --stages;
@@ -96,7 +92,7 @@ PKV_API pkv_status pkv_attn_prompt(void* out, pkv_dtype out_dtype, const void* q
     if ((reinterpret_cast<uintptr_t>(q_start) & 3u) != 0)
         return invalid("q_start must be 4-byte aligned");
     const int G = n_heads / n_kv_heads;
-    const int row_tiles = attn_item_tiles(head_dim, dtype, out_dtype);
+    const int row_tiles = pkv::attn_row_tiles(out_dtype == PKV_F32);
     const int item_tokens = row_tiles * pkv::kAtRows / G;
     const int tiles = (max_len + item_tokens - 1) / item_tokens;
     const long long per_tile = (long long)n_kv_heads * num_seqs;

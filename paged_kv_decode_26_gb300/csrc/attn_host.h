@@ -20,9 +20,6 @@ cudaError_t encode_rows_map(CUtensorMap* map, const void* x, pkv_dtype dt, int r
 cudaError_t encode_out_map(CUtensorMap* map, void* out, pkv_dtype dt, int rows, int heads,
                            long long parts, long long head_bytes, long long row_bytes, int group);
 
-// Row tiles (of 128 rows) per work item.
-int attn_item_tiles(int head_dim, pkv_dtype dt, pkv_dtype out_dtype);
-
 // Slots of the K/V ring that fit beside the queries.
 int attn_stages(int head_dim, int smem_optin);
 

@@ -124,20 +124,25 @@ struct AttnSizes {
     [[maybe_unused]] constexpr uint32_t TILE_COLS = AttnSizes<D>::TILE_COLS;                  \
     [[maybe_unused]] constexpr uint32_t S_COL = AttnSizes<D>::S_COL;
 
-// 16-bit parts whose sum stands for a softmax weight in the second product,
-// and the tensor-memory column of part k.  fp32 outputs take as many as fp32
-// needs: two of fp16 (22 bits), three of bf16 (24).  The first two fill the
-// columns of S; the third lies behind them, or, at D = 128, in the S columns of
-// row tile 1: a CTA then works on one row tile at a time.
+// fp32 outputs (PRECISE) need more in two places.  A softmax weight enters the
+// second product as the sum of as many 16-bit parts as fp32 needs: two of fp16
+// (22 bits), three of bf16 (24).  And the tensor core drops the bits of a product
+// below its accumulator's last one, always downwards: over 32768 keys O came out
+// 2e-4 short.  So O of each key tile starts from zero, smallest parts first, and
+// is added to a sum kept beside it by fp32 additions (now 4e-7).  (16-bit
+// outputs accumulate in the tensor core: 2^-24 of O per 16 keys at most, 1e-4 at
+// 32768 keys, below half a step of fp16.)
+// Tensor-memory columns: the first two parts fill those of S, the third lies
+// behind them or in S's of row tile 1, the sum of O in O's of row tile 1: a CTA
+// works on one row tile at a time.
 __host__ __device__ constexpr int attn_parts(bool bf16, bool precise) {
     return precise ? (bf16 ? 3 : 2) : 1;
 }
-__host__ __device__ constexpr int attn_row_tiles(int D, int parts) {
-    return D == 128 && parts == 3 ? 1 : 2;
-}
+__host__ __device__ constexpr int attn_row_tiles(bool precise) { return precise ? 1 : 2; }
 __host__ __device__ constexpr uint32_t attn_part_col(int D, int k) {
     return k < 2 ? D + k * 64 : (D == 64 ? D + 128 : 256 + D);
 }
+constexpr uint32_t kAtSumCol = 256;       // the sum of O (PRECISE)
 
 // Barriers and item slots of one CTA, behind the tiles in shared memory.
 struct AttnControl {
@@ -614,13 +619,15 @@ __device__ __forceinline__ void attn_mma(const AttnControl& ctl, const AttnParam
                             const uint32_t o = ctl.tmem + t * TILE_COLS;
                             const uint64_t v = dv0 + (uint64_t)(vs * (KV_BYTES >> 4));
 #pragma unroll
-                            for (int part = 0; part < PARTS; ++part)
+                            for (int part = PARTS - 1; part >= 0; --part)
 #pragma unroll
                                 for (int i = half * 4; i < half * 4 + 4; ++i)
                                     at_mma_tmem_a(
                                         o, o + attn_part_col(D, part) + i * 8,
                                         v + (uint64_t)((i * 16 * 128) >> 4), id_o,
-                                        (j > 0 || part > 0 || i > 0) ? 1u : 0u, lead);
+                                        ((!PRECISE && j > 0) || part < PARTS - 1 || i > 0) ? 1u
+                                                                                           : 0u,
+                                        lead);
                             if (half && j + 1 == nt) at_commit(&ctl.o_full[t], lead);
                         }
                         __syncwarp();
@@ -712,6 +719,25 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
                 if (!ok) break;
                 ++n_s;
                 tc_fence_after();
+                if (PRECISE && j > 0) {
+                    // O of key tile j - 1 is complete (its products were issued
+                    // before S_j's): to the sum
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t ov[32], sum[32];
+                        tc_ld32(t_lane + c0, ov);
+                        if (j > 1) tc_ld32(t_lane + kAtSumCol + c0, sum);
+                        tc_wait_ld();
+                        if (j > 1) {
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                ov[c] = __float_as_uint(__uint_as_float(ov[c]) +
+                                                        __uint_as_float(sum[c]));
+                        }
+                        tc_st32(t_lane + kAtSumCol + c0, ov);
+                    }
+                    tc_wait_st();
+                }
                 float y[kAtKeys];
                 uint32_t* yr = reinterpret_cast<uint32_t*>(y);
                 tc_ld32(t_lane + S_COL, yr);
@@ -751,10 +777,11 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
                     // O is at rest: the products up to key tile j - 1
                     // completed before S_j did
                     const float2 a2 = make_float2(alpha, alpha);
+                    const uint32_t o_lane = t_lane + (PRECISE ? kAtSumCol : 0u);
 #pragma unroll 1
                     for (int c0 = 0; c0 < D; c0 += 32) {
                         uint32_t ov[32];
-                        tc_ld32(t_lane + c0, ov);
+                        tc_ld32(o_lane + c0, ov);
                         tc_wait_ld();
 #pragma unroll
                         for (int c = 0; c < 32; c += 2) {
@@ -764,7 +791,7 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
                             ov[c] = __float_as_uint(v.x);
                             ov[c + 1] = __float_as_uint(v.y);
                         }
-                        tc_st32(t_lane + c0, ov);
+                        tc_st32(o_lane + c0, ov);
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) l4[i] = __fmul2_rn(l4[i], a2);
@@ -842,6 +869,15 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
                     for (int c = 0; c < 32; ++c) w[c] = 0u;
                 } else if (WIDE) {
                     tc_ld32(t_lane + g * 32, w);
+                    if (PRECISE && nt > 1) {
+                        uint32_t sum[32];
+                        tc_ld32(t_lane + kAtSumCol + g * 32, sum);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            w[c] = __float_as_uint(__uint_as_float(w[c]) +
+                                                   __uint_as_float(sum[c]));
+                    }
                     tc_wait_ld();
 #pragma unroll
                     for (int c = 0; c < 32; ++c)

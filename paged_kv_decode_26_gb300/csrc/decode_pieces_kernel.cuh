@@ -156,12 +156,16 @@ struct NoScores {
 // run in two accumulators, and the state's maximum is a reference that stays
 // until a score exceeds its range (weight_range.cuh) -- the common chunk then
 // needs one vote instead of the maximum over the lanes, and no rescaling of O.
-template <int D, typename T, bool THIRD, class Scores>
+// PRECISE (fp32 outputs): a chunk's products start from zero and join O by fp32
+// additions -- the tensor core drops the bits of a product below those of its
+// accumulator, so that O came out 5e-6 short over runs of a thousand tokens.
+template <int D, typename T, bool PRECISE, class Scores>
 __device__ __forceinline__ void piece_chunk(MmaHeads<D>& st, uint32_t kbase, uint32_t vbase,
                                             int valid, float scale_log2, int lane,
                                             const Scores& scores) {
     constexpr int KSTEPS = D / 16;
     constexpr uint32_t BOX = kPieceTokens * 128;
+    constexpr bool THIRD = PRECISE && std::is_same<T, __nv_bfloat16>::value;
     const int gid = lane >> 2, tig = lane & 3;
     const int mat = lane >> 3, mrow = lane & 7;
     // ldmatrix matrices: K (tokens 0-7, c), (0-7, c+1), (8-15, c), (8-15, c+1);
@@ -217,7 +221,7 @@ __device__ __forceinline__ void piece_chunk(MmaHeads<D>& st, uint32_t kbase, uin
     st.l[1] += p1 + p3;
     // P in two 16-bit parts (hi = round(p), lo = round(p - hi)), packed by
     // token: (head 2 tig, head 2 tig + 1) of token gid and of token gid + 8;
-    // with THIRD the rest too (bf16 for an fp32 output: 24 bits)
+    // bf16 for an fp32 output the rest too (24 bits)
     const uint32_t hA = pack2<T>(p0, p1), hB = pack2<T>(p2, p3);
     const float2 fA = unpack2<T>(hA), fB = unpack2<T>(hB);
     const uint32_t lA = pack2<T>(p0 - fA.x, p1 - fA.y), lB = pack2<T>(p2 - fB.x, p3 - fB.y);
@@ -256,9 +260,17 @@ __device__ __forceinline__ void piece_chunk(MmaHeads<D>& st, uint32_t kbase, uin
         uint32_t b0, b1, b2, b3;
         ldsm_x4_trans(vbase + (j / 4) * BOX + swz(v_tok, (j % 4) * 2 + v_dc), b0, b1, b2, b3);
         const uint32_t a[4] = {b0 & vm0, b2 & vm0, b1 & vm1, b3 & vm1};
-        mma16816<T>(st.o[j], a, bh0, bh1);
-        mma16816<T>(st.o[j], a, bl0, bl1);
-        if (THIRD) mma16816<T>(st.o[j], a, bt0, bt1);
+        if (PRECISE) {
+            float o[4] = {0.f, 0.f, 0.f, 0.f};
+            if (THIRD) mma16816<T>(o, a, bt0, bt1);
+            mma16816<T>(o, a, bl0, bl1);
+            mma16816<T>(o, a, bh0, bh1);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) st.o[j][e] += o[e];
+        } else {
+            mma16816<T>(st.o[j], a, bh0, bh1);
+            mma16816<T>(st.o[j], a, bl0, bl1);
+        }
     }
 }
 
@@ -525,8 +537,8 @@ struct PieceNext {
 // group.  WEIGHTS: scores go to the workspace and whole (sequence, head)s
 // straight to the output; otherwise every piece goes to the workspace, where
 // the prefix joins it.  The loads run kPieceStages chunks ahead, over the end
-// of a run into the next one.  THIRD: see piece_chunk.
-template <int D, typename T, bool WEIGHTS, bool TAKES, bool THIRD>
+// of a run into the next one.  PRECISE: see piece_chunk.
+template <int D, typename T, bool WEIGHTS, bool TAKES, bool PRECISE>
 __device__ __forceinline__ void piece_worker(const PieceParams& p, const CUtensorMap& tm_k,
                                              const CUtensorMap& tm_v, const PieceShared& sh,
                                              const PieceRuns& runs, const PieceNext& next) {
@@ -678,10 +690,10 @@ __device__ __forceinline__ void piece_worker(const PieceParams& p, const CUtenso
                 const StoreScores sink{2 * tig < p.group ? row : nullptr,
                                        2 * tig + 1 < p.group ? row + p.score_stride : nullptr,
                                        at.c * kPieceTokens + gid, at.n};
-                piece_chunk<D, T, THIRD>(state, kbase, kbase + HALF, valid, p.scale_log2, lane,
+                piece_chunk<D, T, PRECISE>(state, kbase, kbase + HALF, valid, p.scale_log2, lane,
                                          sink);
             } else {
-                piece_chunk<D, T, THIRD>(state, kbase, kbase + HALF, valid, p.scale_log2, lane,
+                piece_chunk<D, T, PRECISE>(state, kbase, kbase + HALF, valid, p.scale_log2, lane,
                                          NoScores());
             }
         } else if (WEIGHTS) {
@@ -745,7 +757,7 @@ inline size_t decode_pieces_smem_bytes(int D) {
 // with in a tenth of a millisecond gains nothing from them -- every run adds a
 // piece to merge (8 contexts of 8K-32K tokens, grouped heads: 124 us without,
 // 138 us with).
-template <int D, typename T, bool WEIGHTS, bool TAKES, bool THIRD>
+template <int D, typename T, bool WEIGHTS, bool TAKES, bool PRECISE>
 __global__ void __launch_bounds__(kPieceThreads + (TAKES ? 32 : 0), 1)
     decode_pieces_kernel(const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v,
@@ -774,7 +786,7 @@ __global__ void __launch_bounds__(kPieceThreads + (TAKES ? 32 : 0), 1)
     if (warp < kPieceWarps) chunks = piece_plan<WEIGHTS>(p, sh);
     if (TAKES) __syncthreads();
     if (warp < kPieceWarps) {
-        piece_worker<D, T, WEIGHTS, TAKES, THIRD>(p, tm_k, tm_v, sh, piece_runs(p, chunks), next);
+        piece_worker<D, T, WEIGHTS, TAKES, PRECISE>(p, tm_k, tm_v, sh, piece_runs(p, chunks), next);
     } else {
         for (int k = 0;; ++k) {
             int cta = -1;

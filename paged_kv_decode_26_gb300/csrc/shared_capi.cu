@@ -156,7 +156,7 @@ PKV_API pkv_status paged_attn_decode_shared(
     a.group = G;
     a.scale_log2 = p.scale_log2;
     a.stages = attn_stages(head_dim, dev->smem_optin);
-    a.row_tiles = attn_item_tiles(head_dim, kv_dtype, out_dtype);
+    a.row_tiles = pkv::attn_row_tiles(out_dtype == PKV_F32);
     const int item_rows = a.row_tiles * pkv::kAtRows / G;
     a.tiles = (max_group + item_rows - 1) / item_rows;
     a.group_start = group_start;
