@@ -533,9 +533,8 @@ PKV_API pkv_status kv_evict(void* k_pool, void* v_pool, pkv_dtype dtype,
  * prefix with a block outside the pool is left out and flagged
  * PKV_DEVERR_BLOCK_ID.  Softmax weights of the prefix enter the second product
  * rounded to kv_dtype, except for F32 outputs (as the sum of two F16 or three
- * BF16 parts).  Supported shapes as
- * paged_attn_decode; at most 65535 sequences, 65535 groups, 4096 query heads.
- * Three launches.
+ * BF16 parts).  Supported shapes as paged_attn_decode; at most 65535 sequences,
+ * 65535 groups, 4096 query heads.  Three launches.
  */
 PKV_API size_t pkv_decode_shared_workspace_bytes(int num_seqs, int num_groups, int max_group,
                                                  int max_prefix, int n_heads, int n_kv_heads,
@@ -572,9 +571,9 @@ PKV_API pkv_status paged_attn_decode_shared(
  * A sequence whose bounds lie outside the tokens or whose length exceeds
  * max_len is left out (its rows are not written) and flagged
  * PKV_DEVERR_CONTEXT.  The softmax weights enter the second product rounded to
- * dtype, except for F32 outputs (as the sum of two F16 or three BF16 parts).  NaN and
- * infinities in rows of k and v reach only the tokens that see those rows (an
- * infinity in v as an infinity or NaN).  One launch, no workspace.
+ * dtype, except for F32 outputs (as the sum of two F16 or three BF16 parts).
+ * NaN and infinities in rows of k and v reach only the tokens that see those
+ * rows (an infinity in v as an infinity or NaN).  One launch, no workspace.
  */
 PKV_API pkv_status pkv_attn_prompt(void* out, pkv_dtype out_dtype, const void* q, int64_t q_stride,
                                const void* k, int64_t k_stride, const void* v, int64_t v_stride,

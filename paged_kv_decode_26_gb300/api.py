@@ -611,7 +611,8 @@ def attn_prompt(out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Te
     st = lib().pkv_attn_prompt(out.data_ptr(), _DT[out.dtype], q.data_ptr(),
                                _token_stride("q", q), k.data_ptr(), _token_stride("k", k),
                                v.data_ptr(), _token_stride("v", v), _DT[q.dtype],
-                               q_start.data_ptr(), q_start.shape[0] - 1, T, int(max_len), H, Hk, D, float(scale), _stream_handle(stream))
+                               q_start.data_ptr(), q_start.shape[0] - 1, T, int(max_len), H, Hk, D,
+                               float(scale), _stream_handle(stream))
     check(st, "attn_prompt")
     return out
 

@@ -372,7 +372,8 @@ __device__ __forceinline__ void attn_loader(const AttnControl& ctl, const AttnPa
 #pragma unroll
                             for (int h = 0; h < HALVES; ++h)
                                 tma_load_4d(ctl.sQ + t * Q_BYTES + h * Q_HALF, &tm_q,
-                                            &ctl.q_full[t], 0, h, it.kvh * G, it.row0 + t * QT, once);
+                                            &ctl.q_full[t], 0, h, it.kvh * G, it.row0 + t * QT,
+                                            once);
                         }
                     }
                     if (!ok) break;

@@ -93,6 +93,8 @@ pkv_status check_paged_decode(const void* out, pkv_dtype out_dtype, const void* 
     if (num_blocks > 0 && (!k_pool || !v_pool)) return invalid("k_pool or v_pool is NULL");
     if (!aligned16(out) || !aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool))
         return invalid("out, q, k_pool and v_pool must be 16-byte aligned");
+    if (!aligned4(block_tables) || !aligned4(context_lens))
+        return invalid("block_tables and context_lens must be 4-byte aligned");
     return PKV_OK;
 }
 
@@ -216,7 +218,7 @@ PKV_API pkv_status paged_attn_decode_weights(
     if (weight_stride < max_context_len) return invalid("weight_stride below max_context_len");
     if (num_seqs == 0) return PKV_OK;
     if (!weights && max_context_len > 0) return invalid("weights is NULL");
-    if ((reinterpret_cast<uintptr_t>(weights) & 3u) != 0) return invalid("weights must be 4-byte aligned");
+    if (!aligned4(weights)) return invalid("weights must be 4-byte aligned");
     DeviceInfo* dev = nullptr;
     cudaError_t e = device_info(&dev);
     if (e != cudaSuccess) return cuda_fail(e);
@@ -267,12 +269,14 @@ PKV_API pkv_status kv_evict(void* k_pool, void* v_pool, pkv_dtype dtype,
         max_blocks_per_seq <= 0 || new_blocks_per_seq <= 0 || weight_cols < 0)
         return invalid("sizes");
     if (num_seqs > 65535) return unsupported("more than 65535 sequences per call");
-    if (keep < 1 || recent < 0 || recent > keep) return invalid("keep >= 1 and 0 <= recent <= keep");
+    if (keep < 1 || recent < 0 || recent > keep)
+        return invalid("keep >= 1 and 0 <= recent <= keep");
     if (!table_tokens_fit(max_blocks_per_seq, block_size))
         return unsupported("max_blocks_per_seq * block_size exceeds 2^31 - 1 tokens");
     if ((long long)new_blocks_per_seq * block_size < keep)
         return invalid("new_tables cannot hold keep tokens");
-    if (weight_stride < weight_cols || new_weight_stride < new_weight_cols || new_weight_cols < keep)
+    if (weight_stride < weight_cols || new_weight_stride < new_weight_cols ||
+        new_weight_cols < keep)
         return invalid("weight rows: strides below the columns, or new_weights below keep columns");
     int es = 0;
     switch (dtype) {
@@ -291,6 +295,10 @@ PKV_API pkv_status kv_evict(void* k_pool, void* v_pool, pkv_dtype dtype,
         return invalid("NULL pointer");
     if (num_blocks > 0 && (!k_pool || !v_pool)) return invalid("k_pool or v_pool is NULL");
     if (!aligned16(k_pool) || !aligned16(v_pool)) return invalid("pools must be 16-byte aligned");
+    for (const void* x : {(const void*)block_tables, (const void*)context_lens,
+                          (const void*)weights, (const void*)new_tables, (const void*)new_lens,
+                          (const void*)new_weights, (const void*)kept})
+        if (!aligned4(x)) return invalid("tables, lengths, weights and kept must be 4-byte aligned");
     // the second kernel reads what the first one read: outputs may not lie on inputs
     const size_t n = (size_t)num_seqs;
     const struct {
@@ -303,10 +311,16 @@ PKV_API pkv_status kv_evict(void* k_pool, void* v_pool, pkv_dtype dtype,
       outs[] = {{new_lens, n * 4},
                 {new_weights, ((n - 1) * (size_t)new_weight_stride + (size_t)new_weight_cols) * 4},
                 {kept, n * (size_t)keep * 4}};
-    for (const auto& o : outs)
+    for (const auto& o : outs) {
         for (const auto& i : in)
             if (overlap(o.p, o.bytes, i.p, i.bytes))
                 return invalid("new_lens, new_weights and kept may not overlap the inputs");
+        for (const auto& i : outs)
+            if (i.p != o.p && overlap(o.p, o.bytes, i.p, i.bytes))
+                return invalid("new_lens, new_weights and kept may not overlap");
+    }
+    if (outs[0].p == outs[1].p || outs[1].p == outs[2].p || outs[0].p == outs[2].p)
+        return invalid("new_lens, new_weights and kept may not overlap");
     DeviceInfo* dev = nullptr;
     cudaError_t e = device_info(&dev);
     if (e != cudaSuccess) return cuda_fail(e);

@@ -101,13 +101,13 @@ __device__ __forceinline__ int piece_length(const PieceParams& p, int s) {
     return n < 0 ? 0 : min(n, p.cap_tokens);
 }
 
-// Prefix length of group g, 0 for a group that is not well formed (the
-// members then decode their whole contexts).  gs: group starts.
+// Prefix length of group g (sequences g0 .. g1 - 1), -1 for a group that is not
+// well formed (the members then decode their whole contexts).
 __device__ __forceinline__ int group_prefix(const PieceParams& p, int g, int g0, int g1) {
     const int pl = p.prefix_lens[g];
     const bool ok = g0 >= 0 && g1 >= g0 && g1 <= p.num_seqs && g1 - g0 <= p.max_group &&
                     pl >= 0 && pl <= p.max_prefix && pl % p.block_size == 0;
-    return ok ? pl : 0;
+    return ok ? pl : -1;
 }
 
 // Tokens of sequence s (length n) that its group's prefix covers: 0 for a
@@ -122,8 +122,8 @@ __device__ __forceinline__ int piece_start(const PieceParams& p, const int* gs, 
             hi = mid;
     }
     if (lo >= p.num_groups || gs[lo] > s) return 0;
-    const int pl = group_prefix(p, lo, gs[lo], gs[lo + 1]);
-    return n >= pl ? pl : 0;
+    const int pl = max(0, group_prefix(p, lo, gs[lo], gs[lo + 1]));
+    return n >= pl && p.num_blocks > 0 ? pl : 0;
 }
 
 // Writes the scores of one chunk to the workspace: this lane's tokens tok and
@@ -346,7 +346,7 @@ __device__ __forceinline__ void piece_sync() {
 }
 
 // By threads 0 .. 255: barriers, group starts, and the chunks before each
-// block of 256 sequences, bad lengths flagged, p.start written.  Returns the
+// block of 256 sequences, bad lengths and groups flagged, p.start written.  Returns the
 // chunks of all sequences.
 template <bool WEIGHTS>
 __device__ __forceinline__ int piece_plan(const PieceParams& p, PieceShared& sh) {
@@ -363,6 +363,10 @@ __device__ __forceinline__ int piece_plan(const PieceParams& p, PieceShared& sh)
         sh.gs = sh.group_starts;
         piece_sync();
     }
+    if (!WEIGHTS && blockIdx.x == 0)
+        for (int g = threadIdx.x; g < p.num_groups; g += kPieceThreads)
+            if (group_prefix(p, g, sh.gs[g], sh.gs[g + 1]) < 0)
+                raise_error(p.errors, PKV_DEVERR_CONTEXT);
     const int n_blk = (S + 255) / 256;
     int run = 0;
     for (int b = 0; b < n_blk; ++b) {

@@ -13,7 +13,8 @@
 namespace pkv {
 
 // Candidates (group, kv head, split, pair of row tiles), the row tiles
-// fastest (they share the keys): this one may be an item.
+// fastest (they share the keys): this one may be an item.  (Groups that are not
+// well formed have none; piece_plan flags them.)
 __device__ __forceinline__ bool attn_prefix_candidate(const AttnParams& a, long long x) {
     const int QT = kAtRows / a.group;
     const int tile = (int)(x % a.tiles);
@@ -25,7 +26,6 @@ __device__ __forceinline__ bool attn_prefix_candidate(const AttnParams& a, long 
     const int pl = a.prefix_lens[g];
     const bool valid = g0 >= 0 && g1 >= g0 && g1 <= a.num_seqs && g1 - g0 <= a.max_group &&
                        pl >= 0 && pl <= a.max_prefix && pl % a.block_size == 0;
-    if (!valid && tile == 0 && split == 0 && kvh == 0) raise_error(a.errors, PKV_DEVERR_CONTEXT);
     return valid && g0 + tile * a.row_tiles * QT < g1 && (long long)split * a.split_tokens < pl;
 }
 

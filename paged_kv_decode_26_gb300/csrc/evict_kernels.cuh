@@ -72,8 +72,9 @@ __device__ __forceinline__ int evict_length(const EvictParams& p, int s) {
 }
 
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                     : "memory");
+    asm volatile(
+        "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+            : "memory");
 }
 
 // The two ints at `local`'s place in the shared memory of CTA `rank` of the

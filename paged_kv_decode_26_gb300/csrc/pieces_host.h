@@ -19,6 +19,8 @@ struct PiecesWorkspace {
 
 size_t align256(size_t n);
 
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 // kv heads per stream: the largest of 8, 4, 2, 1 that divides n_kv_heads.
 int pieces_stream_heads(int n_kv_heads);
 

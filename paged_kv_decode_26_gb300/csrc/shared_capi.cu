@@ -106,8 +106,7 @@ PKV_API pkv_status paged_attn_decode_shared(
     if (num_seqs == 0) return PKV_OK;
     if (num_groups > 0 && (!group_start || !prefix_lens))
         return invalid("group_start or prefix_lens is NULL");
-    if (((reinterpret_cast<uintptr_t>(group_start) | reinterpret_cast<uintptr_t>(prefix_lens)) &
-         3u) != 0)
+    if (!aligned4(group_start) || !aligned4(prefix_lens))
         return invalid("group_start and prefix_lens must be 4-byte aligned");
     if (!groups_ok(num_seqs, num_groups, max_group, max_prefix, max_context_len))
         return invalid("max_group beyond num_seqs, or max_prefix beyond max_context_len");
@@ -129,6 +128,7 @@ PKV_API pkv_status paged_attn_decode_shared(
     if (st != PKV_OK) return st;
     p.group_start = group_start;
     p.prefix_lens = prefix_lens;
+    p.num_groups = num_groups;
     p.max_group = max_group;
     p.max_prefix = max_prefix;
     p.start = reinterpret_cast<int*>(ws + c.start);
@@ -179,7 +179,7 @@ PKV_API pkv_status paged_attn_decode_shared(
         if ((e = encode_out_map(&L.tm_o, a.pre_o, PKV_F32, num_seqs, n_heads, unit / 128, unit,
                                 unit * n_heads, G)))
             return cuda_fail(e);
-        a.num_groups = p.num_groups = num_groups;
+        a.num_groups = num_groups;
         a.n_items = (long long)num_groups * n_kv_heads * a.tiles * c.max_splits;
         L.prefix_ctas = (int)(a.n_items < dev->sm_count ? a.n_items : dev->sm_count);
     }
@@ -188,8 +188,8 @@ PKV_API pkv_status paged_attn_decode_shared(
                              : pkv::launch_shared_f16(head_dim, precise, L);
     if (e != cudaSuccess) return cuda_fail(e);
     // Pieces of a row to expect: the prefix's splits, and the cuts of the rest.
-    // Up to 12 one warp merges them (GB300, 8192 rows of 6 pieces: 17 us with
-    // four warps a row, see DESIGN for one).
+    // Up to 12 one warp merges them (GB300, 8192 rows of 6 pieces: 13 us, 17 us
+    // with four warps a row).
     const long long streams = (long long)c.grid.ctas * (pkv::kPieceWarps / p.stream_heads);
     const long long pairs = (long long)num_seqs * (n_kv_heads / p.stream_heads);
     const bool few = c.max_splits + 2 + streams / pairs <= 12;

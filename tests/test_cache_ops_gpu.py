@@ -421,3 +421,76 @@ def test_pools_beyond_four_gigabytes():
     got = torch.cat([kp[35997], kp[2]])[:50].cpu()
     assert torch.equal(got, k[idx])
     assert torch.equal(torch.cat([vp[35997], vp[2]])[:50].cpu(), v[idx])
+
+
+# ------------------------- batches large enough for runs that are taken over
+
+def _large(lens, Hk, D, B, dtype, blocks=400, seed=1):
+    """Contexts whose pages are drawn, with repeats, from a small pool."""
+    g = torch.Generator().manual_seed(seed)
+    width = (max(lens) + B - 1) // B
+    tables = torch.randint(blocks, (len(lens), width), generator=g, dtype=torch.int32)
+    k, v = (torch.randn(blocks, B, Hk, D, generator=g).to(dtype) for _ in range(2))
+    q = torch.randn(len(lens), Hk, D, generator=g).to(dtype)
+    return q, k, v, tables
+
+
+def _large_check(out, w, q, k, v, tables, lens, some, scale, out_dtype):
+    for s in some:
+        n = lens[s]
+        ks, vs = (x[tables[s].long()].flatten(0, 1)[:n] for x in (k, v))
+        o, bound, ws = ref.decode(q[s:s + 1], [ks], [vs], scale, out_dtype)
+        ref.check(out[s:s + 1], o, bound, f"sequence {s}")
+        ref.check(w[s, :n], ws[0][0], ws[0][1] + 2.0 ** -23 * ws[0][0], f"weights of {s}")
+        assert (w[s, n:] == 0).all()
+
+
+@pytest.mark.parametrize("Hk,D,dtype,out_dtype", [(32, 64, BF, BF), (16, 128, FP, F32)])
+def test_decode_weights_of_a_large_batch(Hk, D, dtype, out_dtype):
+    """128 chunks for every stream and more: a fifth of the work is in short
+    runs.  Also captured, and repeated with the same bits."""
+    _clean()
+    B = 16
+    g = torch.Generator().manual_seed(4)
+    lens = [1, 0, 17] + torch.randint(1, 6000, (77 * 64 // Hk // 2,), generator=g).tolist() + [6000]
+    assert sum((n + 15) // 16 for n in lens) * Hk // 8 >= 152 * 128
+    q, k, v, tables = _large(lens, Hk, D, B, dtype)
+    scale = 1 / math.sqrt(D)
+    S, L = len(lens), max(lens)
+    dev = [x.cuda() for x in (q, k, v, tables, torch.tensor(lens, dtype=torch.int32))]
+    ws = torch.empty(pkv.decode_weights_workspace_bytes(S, Hk, Hk, D, B, L), dtype=torch.uint8,
+                     device="cuda")
+    out = torch.full((S, Hk, D), float("nan"), dtype=out_dtype, device="cuda")
+    w = torch.zeros(S, L, device="cuda")
+    call = lambda: pkv.paged_attn_decode_weights(out, *dev, w, scale, L, workspace=ws)  # noqa: E731
+    call()
+    assert _clean() == 0
+    _large_check(out, w, q, k, v, tables, lens, [0, 1, 2, 3, S // 2, S - 1], scale, out_dtype)
+    first, first_w = out.clone(), w.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(3):
+        out.zero_()
+        w.zero_()
+        ws.fill_(255)
+        graph.replay()
+        assert _clean() == 0
+        assert torch.equal(out, first) and torch.equal(w, first_w)
+
+
+def test_decode_weights_short_contexts_under_a_large_bound():
+    """The bound asks for runs that can be taken over; the lengths leave them
+    empty, or leave whole CTAs without work."""
+    B, Hk, D, L = 16, 8, 64, 90000
+    for lens in ([40, 0, 1, 900], [0, 0, 0, 0], [5, 0, 0, 0]):
+        _clean()
+        q, k, v, tables = _large([1000] * 4, Hk, D, B, BF)
+        tables = torch.nn.functional.pad(tables, (0, L // B - tables.shape[1]), value=-1)
+        out = torch.full((4, Hk, D), float("nan"), dtype=BF, device="cuda")
+        w = torch.zeros(4, L, device="cuda")
+        pkv.paged_attn_decode_weights(out, q.cuda(), k.cuda(), v.cuda(), tables.cuda(),
+                                      torch.tensor(lens, dtype=torch.int32, device="cuda"), w,
+                                      0.125, L)
+        assert _clean() == 0
+        _large_check(out, w, q, k, v, tables[:, :100], lens, range(4), 0.125, BF)

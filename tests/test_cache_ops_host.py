@@ -214,3 +214,23 @@ def test_binding_refuses_tensors_that_are_not_on_the_gpu(L):
                                  _ints([[0] * 8] * 2), 8, 2)):
         with pytest.raises(ValueError, match="CUDA tensor"):
             call()
+
+
+ODD = C.c_void_p(30 * 64 * MB + 2)
+
+
+@pytest.mark.parametrize("call,name", [
+    (_weights, "bt"), (_weights, "cl"), (_shared, "bt"), (_shared, "cl"), (_shared, "pl"),
+    (_evict, "bt"), (_evict, "cl"), (_evict, "w"), (_evict, "nt"), (_evict, "nl"),
+    (_evict, "nw"), (_evict, "kept")])
+def test_refuses_misaligned_ints_and_weights(L, call, name):
+    assert call(L, **{name: ODD}) == 1
+    assert b"4-byte" in L.pkv_last_error_detail()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(kept=FAKE(8)), dict(nl=FAKE(9)), dict(nl=FAKE(8)),
+    dict(kept=C.c_void_p(8 * 64 * MB + 128)), dict(nl=C.c_void_p(9 * 64 * MB + 252))])
+def test_evict_refuses_outputs_that_overlap(L, kw):
+    assert _evict(L, **kw) == 1
+    assert b"overlap" in L.pkv_last_error_detail()

@@ -146,3 +146,40 @@ def test_decode_shared_repeats_graph_stream():
     call(stream=side)
     side.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("max_group,max_prefix", [(4, 0), (0, 64), (0, 0)])
+def test_decode_shared_flags_groups_where_no_bound_allows_any(max_group, max_prefix):
+    _clean()
+    lens, starts, prefix = [70, 80, 90, 100], [0, 4], [64]
+    c = _problem(lens, starts, prefix, 4, 2, 64, 16, BF)
+    out = _run(c, starts, prefix, BF, 100, max_group=max_group, max_prefix=max_prefix)
+    assert _clean() == _lib.DEVERR_CONTEXT
+    o, bound, _ = ref.decode(c["q"], c["k"], c["v"], c["scale"], BF)
+    ref.check(out, o, bound)
+
+
+def test_decode_shared_flags_one_group_of_many():
+    """More groups than a CTA keeps in shared memory, one of them malformed."""
+    S = 1300
+    lens = [20 + i % 30 for i in range(S)]
+    starts, prefix = list(range(S + 1)), [16] * S
+    c = _problem(lens, starts, prefix, 1, 1, 64, 16, BF)
+    prefix[1234] = 17
+    out = _run(c, starts, prefix, BF, 50, max_prefix=32)
+    assert _clean() == _lib.DEVERR_CONTEXT
+    o, bound, _ = ref.decode(c["q"], c["k"], c["v"], c["scale"], BF, once=True)
+    ref.check(out, o, bound)
+
+
+def test_decode_shared_from_an_empty_pool():
+    """No blocks at all: the tables' ids are flagged, the rows are zeros."""
+    _clean()
+    q = torch.randn(2, 4, 64, device="cuda").to(BF)
+    out = torch.full((2, 4, 64), 7.0, dtype=BF, device="cuda")
+    pool = torch.empty(0, 16, 2, 64, dtype=BF, device="cuda")
+    tables = torch.zeros(2, 4, dtype=torch.int32, device="cuda")
+    pkv.paged_attn_decode_shared(out, q, pool, pool, tables, _ints([40, 50]), _ints([0, 2]),
+                                 _ints([32]), 0.1, 64, 2, 32)
+    assert _clean() == _lib.DEVERR_BLOCK_ID
+    assert (out == 0).all()
