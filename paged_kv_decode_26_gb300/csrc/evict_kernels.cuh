@@ -264,30 +264,33 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
 constexpr int kEvictCopyThreads = 256;
 constexpr int kEvictLoads = 8;               // 16-byte loads in flight per lane
 
-// Units: (sequence, `batch` kept tokens, part of the row), the part fastest so
-// that a token's row is read by neighbouring warps.  A row's part is taken by
-// LR lanes (32, or fewer for rows below 512 bytes: then the warp's lane groups
-// take neighbouring tokens), VEC vectors each of K and of V.
-template <int VEC>
-__global__ void __launch_bounds__(kEvictCopyThreads, 3) evict_copy_kernel(const EvictParams p) {
+// Kept tokens j0 .. j1 - 1 of every sequence.  Units: (sequence, `batch` of
+// them, part of the row), the part fastest so that a token's row is read by
+// neighbouring warps.  A row's part is taken by LR lanes (32, or fewer for rows
+// below 512 bytes: then the warp's lane groups take neighbouring tokens), VEC
+// vectors each of K and of V.  RECENT: the last tokens of the context, which
+// stay whatever the weights are; otherwise those that the selection lists.
+template <int VEC, bool RECENT>
+__device__ __forceinline__ void evict_copy(const EvictParams& p, int begin, int end) {
     constexpr int T = kEvictLoads / (2 * VEC);           // tokens per lane group and round
-    dependency_wait();
     const int lane = threadIdx.x & 31;
     const int LR = p.row_lanes, groups = 32 / LR;
     const int grp = lane / LR, in_row = lane % LR;
-    const int batches = (p.keep + p.batch - 1) / p.batch;
+    const int batches = (end - begin + p.batch - 1) / p.batch;
     const long long units = (long long)p.num_seqs * batches * p.parts;
     const long long stride = (long long)gridDim.x * (kEvictCopyThreads / 32);
     for (long long u = (long long)blockIdx.x * (kEvictCopyThreads / 32) + (threadIdx.x >> 5);
          u < units; u += stride) {
         const int part = (int)(u % p.parts);
         const long long sb = u / p.parts;
-        const int s = (int)(sb / batches), j0 = (int)(sb % batches) * p.batch, j = j0 + lane;
-        if (evict_length(p, s) <= p.keep) continue;
+        const int s = (int)(sb / batches);
+        const int j0 = begin + (int)(sb % batches) * p.batch, j = j0 + lane;
+        const int n = evict_length(p, s);
+        if (n <= p.keep) continue;
         // source and destination row of this lane's token (-1: none)
         long long src = -1, dst = -1;
-        if (lane < p.batch && j < p.keep) {
-            const int t = p.kept[(size_t)s * p.keep + j];
+        if (lane < p.batch && j < end) {
+            const int t = RECENT ? n - p.keep + j : p.kept[(size_t)s * p.keep + j];
             const int from = p.block_tables[(size_t)s * p.max_blocks_per_seq + t / p.block_size];
             const int to = p.new_tables[(size_t)s * p.new_blocks_per_seq + j / p.block_size];
             if (from < 0 || from >= p.num_blocks || to < 0 || to >= p.num_blocks) {
@@ -297,7 +300,7 @@ __global__ void __launch_bounds__(kEvictCopyThreads, 3) evict_copy_kernel(const 
                 dst = ((long long)to * p.block_size + j % p.block_size) * p.row_vec;
             }
         }
-        const int rows = min(p.batch, p.keep - j0);
+        const int rows = min(p.batch, end - j0);
         const int col = part * (LR * VEC) + in_row;
 #pragma unroll 1
         for (int r0 = 0; r0 < rows; r0 += T * groups) {
@@ -326,6 +329,14 @@ __global__ void __launch_bounds__(kEvictCopyThreads, 3) evict_copy_kernel(const 
                             __stcs(p.pool[i] + to[k] + v * LR, x[k][i][v]);
         }
     }
+}
+
+// The tokens that stay in any case move while the selection runs.
+template <int VEC>
+__global__ void __launch_bounds__(kEvictCopyThreads, 3) evict_copy_kernel(const EvictParams p) {
+    if (p.recent > 0) evict_copy<VEC, true>(p, p.keep - p.recent, p.keep);
+    dependency_wait();
+    if (p.keep > p.recent) evict_copy<VEC, false>(p, 0, p.keep - p.recent);
 }
 
 }  // namespace pkv
