@@ -115,7 +115,8 @@ typedef enum pkv_tune_knob {
     PKV_TUNE_SWAP_HINT = 16,      /* bulk block copy L2 hint: 0 none, 1 evict-first */
     PKV_TUNE_DECODE_STREAM = 17,  /* 0/1: tensor-core decode by resident CTAs taking equal
                                      page shares (automatic split only) */
-    PKV_TUNE_COUNT = 18
+    PKV_TUNE_SHARED_PREFIX = 18,  /* 0/1: shared decode attends a group's prefix once off/on */
+    PKV_TUNE_COUNT = 19
 } pkv_tune_knob;
 
 /* Set one knob (value PKV_TUNE_AUTO restores the automatic choice).
@@ -508,18 +509,18 @@ PKV_API pkv_status kv_evict(void* k_pool, void* v_pool, pkv_dtype dtype,
 /*
  * paged_attn_decode_shared -- paged_attn_decode for a batch whose sequences
  * share long prefixes ([LAYOUT] section 四.2: several requests point at the
- * same physical blocks of a common prompt): each shared prefix is read and
- * multiplied once for its whole group, on the tensor cores, the rest of every
- * context as in paged_attn_decode, and the two parts are merged by the
- * OnlineSoftmax recurrence.  The result is paged_attn_decode's.
+ * same physical blocks of a common prompt): where there is enough to save,
+ * each shared prefix is read and multiplied once for its whole group, on the
+ * tensor cores, the rest of every context as in paged_attn_decode, and the two
+ * parts are merged by the OnlineSoftmax recurrence.  The result is paged_attn_decode's.
  *
  *   group_start   device int32 [num_groups + 1], non-decreasing: sequences
  *                 group_start[g] .. group_start[g+1]-1 are group g.  Sequences in
  *                 no group are decoded alone.
  *   prefix_lens   device int32 [num_groups], multiples of block_size: the first
  *                 prefix_lens[g] tokens of group g's sequences lie in the same
- *                 blocks (the caller's promise: only one member's table is read
- *                 for them).  A member whose context is shorter than the prefix
+ *                 blocks (the caller's promise: it may be that only one member's
+ *                 table is read for them).  A member whose context is shorter than the prefix
  *                 is decoded alone.
  *   max_group, max_prefix  host-side bounds of a group's size (at most num_seqs)
  *                 and of prefix_lens (at most max_context_len)
@@ -530,11 +531,12 @@ PKV_API pkv_status kv_evict(void* k_pool, void* v_pool, pkv_dtype dtype,
  * A group with bounds outside the batch, more than max_group members, or a
  * prefix that is negative, beyond max_prefix or no multiple of block_size is
  * flagged PKV_DEVERR_CONTEXT and its members are decoded alone.  A split of a
- * prefix with a block outside the pool is left out and flagged
- * PKV_DEVERR_BLOCK_ID.  Softmax weights of the prefix enter the second product
+ * prefix (or 16 tokens of a context) with a block outside the pool is left out and
+ * flagged PKV_DEVERR_BLOCK_ID.  Softmax weights of the prefix enter the second product
  * rounded to kv_dtype, except for F32 outputs (as the sum of two F16 or three
  * BF16 parts).  Supported shapes as paged_attn_decode; at most 65535 sequences,
- * 65535 groups, 4096 query heads.  Three launches.
+ * 65535 groups, 4096 query heads.  Two launches, or
+ * three where the prefixes are long enough for it to pay.
  */
 PKV_API size_t pkv_decode_shared_workspace_bytes(int num_seqs, int num_groups, int max_group,
                                                  int max_prefix, int n_heads, int n_kv_heads,

@@ -545,8 +545,8 @@ def paged_attn_decode_shared(out: torch.Tensor, q: torch.Tensor, k_pool: torch.T
                              stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """paged_attn_decode where sequences group_start[g] .. group_start[g+1]-1
     (int32 [groups + 1]) share the blocks of their first prefix_lens[g] tokens
-    (int32 [groups], whole blocks): each prefix is attended once for its
-    group.  max_group and max_prefix bound the groups' sizes and prefixes."""
+    (int32 [groups], whole blocks): where that pays, each prefix is attended
+    once for its group.  max_group and max_prefix bound the groups' sizes and prefixes."""
     ints = (block_tables, context_lens, group_start, prefix_lens)
     _need_here(_SHARED_NAMES, (out, q, k_pool, v_pool) + ints)
     _need_ints(_SHARED_NAMES[4:], ints)

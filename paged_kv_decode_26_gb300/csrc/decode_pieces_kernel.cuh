@@ -123,7 +123,7 @@ __device__ __forceinline__ int piece_start(const PieceParams& p, const int* gs, 
     }
     if (lo >= p.num_groups || gs[lo] > s) return 0;
     const int pl = max(0, group_prefix(p, lo, gs[lo], gs[lo + 1]));
-    return n >= pl && p.num_blocks > 0 ? pl : 0;
+    return n >= pl && p.max_splits > 0 ? pl : 0;
 }
 
 // Writes the scores of one chunk to the workspace: this lane's tokens tok and

@@ -4,6 +4,7 @@
 // pagedkv.h.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cstring>
 
 #include "attn_host.h"
@@ -18,6 +19,23 @@ namespace {
 // A split costs its key tiles and about this many more (queries, first and
 // last products, output of the partial states).
 constexpr int kSplitCost = 4;
+
+// Whether the prefixes are attended once per group: where they fill a key tile
+// and the other members' reads of them, at most, come to 24 MB.  Below that every
+// member reads its whole context, which saves a launch.  GB300, GPU time of a
+// call (and with the launches from Python), each member alone against once per
+// group: 0.4 MB 10.7 (21) / 11.7 us (25); 16 MB 13.2 (20) / 13.5 (25); 31 MB 17.8
+// (21) / 12.7 (24), eight groups 18.6 / 21.0; 66 MB 21.1 / 16.4, of prefixes of 64
+// tokens 25.4 / 28.2; 251 MB 39.4 / 19.0, of 64 tokens 76.4 / 72.5.
+constexpr double kSharedLeast = 24e6;
+bool prefix_once(int num_seqs, int num_groups, int max_group, int max_prefix, int n_kv_heads,
+                 int head_dim) {
+    const long long members = std::min((long long)num_seqs, (long long)num_groups * max_group);
+    const long long again = max_group > 0 ? members - (members + max_group - 1) / max_group : 0;
+    const double bytes = 4.0 * n_kv_heads * head_dim * max_prefix * again;
+    const bool pays = max_prefix >= pkv::kAtKeys && bytes >= kSharedLeast;
+    return tuning(PKV_TUNE_SHARED_PREFIX, pays ? 1 : 0) != 0;
+}
 
 struct SharedShape {
     int split_tokens;
@@ -36,7 +54,8 @@ SharedShape shared_shape(int num_seqs, int num_groups, int max_group, int max_pr
     const long long units = (long long)num_groups * n_kv_heads * pairs;
     c.max_splits = 0;
     c.split_tokens = pkv::kAtKeys;
-    if (units > 0 && max_prefix > 0) {
+    if (units > 0 && max_prefix > 0 &&
+        prefix_once(num_seqs, num_groups, max_group, max_prefix, n_kv_heads, head_dim)) {
         // Work items (split x kv head x pair of row tiles x group) are dealt
         // out to the SMs in turn: the split length with the smallest sum of
         // key tiles over the busiest SM's items, the longer one of equals.
@@ -135,51 +154,49 @@ PKV_API pkv_status paged_attn_decode_shared(
     p.pre_o = reinterpret_cast<float*>(ws + c.pre_o);
     p.pre_ml = reinterpret_cast<float*>(ws + c.pre_ml);
     p.split_tokens = c.split_tokens;
-    p.max_splits = c.max_splits;
+    const bool once = c.max_splits > 0 && num_blocks > 0;
+    p.max_splits = once ? c.max_splits : 0;
 
-    // ---- the prefixes (none: whole contexts, nothing to join)
+    // ---- the prefixes (not once: whole contexts, nothing to join)
     const int G = n_heads / n_kv_heads;
-    if ((e = encode_rows_map(&L.tm_q, q, kv_dtype, num_seqs, n_heads, head_dim,
-                             (long long)n_heads * head_dim, G, pkv::kAtRows / G)) ||
-        (e = encode_pool_map(&L.tm_k, num_blocks > 0 ? k_pool : q, kv_dtype,
-                             num_blocks > 0 ? num_blocks : 1, block_size, n_kv_heads, head_dim, 1,
-                             true)) ||
-        (e = encode_pool_map(&L.tm_v, num_blocks > 0 ? v_pool : q, kv_dtype,
-                             num_blocks > 0 ? num_blocks : 1, block_size, n_kv_heads, head_dim, 1,
-                             true)))
-        return cuda_fail(e);
     pkv::AttnParams& a = L.a;
-    a.out_dtype = out_dtype;
-    a.num_seqs = num_seqs;
-    a.n_heads = n_heads;
-    a.n_kv_heads = n_kv_heads;
-    a.group = G;
-    a.scale_log2 = p.scale_log2;
-    a.stages = attn_stages(head_dim, dev->smem_optin);
-    a.row_tiles = pkv::attn_row_tiles(out_dtype == PKV_F32);
-    const int item_rows = a.row_tiles * pkv::kAtRows / G;
-    a.tiles = (max_group + item_rows - 1) / item_rows;
-    a.group_start = group_start;
-    a.prefix_lens = prefix_lens;
-    a.max_group = max_group;
-    a.max_prefix = max_prefix;
-    a.block_tables = block_tables;
-    a.max_blocks_per_seq = max_blocks_per_seq;
-    a.context_lens = context_lens;
-    a.cap_tokens = p.cap_tokens;
-    a.block_size = block_size;
-    a.num_blocks = num_blocks;
-    a.split_tokens = c.split_tokens;
-    a.max_splits = c.max_splits;
-    a.pre_o = reinterpret_cast<float*>(ws + c.pre_o);
-    a.pre_ml = reinterpret_cast<float*>(ws + c.pre_ml);
-    a.errors = dev->errors;
-    if (c.max_splits > 0 && num_blocks > 0) {
+    if (once) {
         const long long unit = (long long)head_dim * sizeof(float) * c.max_splits;
-        if ((e = encode_out_map(&L.tm_o, a.pre_o, PKV_F32, num_seqs, n_heads, unit / 128, unit,
+        if ((e = encode_rows_map(&L.tm_q, q, kv_dtype, num_seqs, n_heads, head_dim,
+                                 (long long)n_heads * head_dim, G, pkv::kAtRows / G)) ||
+            (e = encode_pool_map(&L.tm_k, k_pool, kv_dtype, num_blocks, block_size, n_kv_heads,
+                                 head_dim, 1, true)) ||
+            (e = encode_pool_map(&L.tm_v, v_pool, kv_dtype, num_blocks, block_size, n_kv_heads,
+                                 head_dim, 1, true)) ||
+            (e = encode_out_map(&L.tm_o, ws + c.pre_o, PKV_F32, num_seqs, n_heads, unit / 128, unit,
                                 unit * n_heads, G)))
             return cuda_fail(e);
+        a.out_dtype = out_dtype;
+        a.num_seqs = num_seqs;
+        a.n_heads = n_heads;
+        a.n_kv_heads = n_kv_heads;
+        a.group = G;
+        a.scale_log2 = p.scale_log2;
+        a.stages = attn_stages(head_dim, dev->smem_optin);
+        a.row_tiles = pkv::attn_row_tiles(out_dtype == PKV_F32);
+        const int item_rows = a.row_tiles * pkv::kAtRows / G;
+        a.tiles = (max_group + item_rows - 1) / item_rows;
+        a.group_start = group_start;
+        a.prefix_lens = prefix_lens;
         a.num_groups = num_groups;
+        a.max_group = max_group;
+        a.max_prefix = max_prefix;
+        a.block_tables = block_tables;
+        a.max_blocks_per_seq = max_blocks_per_seq;
+        a.context_lens = context_lens;
+        a.cap_tokens = p.cap_tokens;
+        a.block_size = block_size;
+        a.num_blocks = num_blocks;
+        a.split_tokens = c.split_tokens;
+        a.max_splits = c.max_splits;
+        a.pre_o = reinterpret_cast<float*>(ws + c.pre_o);
+        a.pre_ml = reinterpret_cast<float*>(ws + c.pre_ml);
+        a.errors = dev->errors;
         a.n_items = (long long)num_groups * n_kv_heads * a.tiles * c.max_splits;
         L.prefix_ctas = (int)(a.n_items < dev->sm_count ? a.n_items : dev->sm_count);
     }
@@ -192,7 +209,7 @@ PKV_API pkv_status paged_attn_decode_shared(
     // with four warps a row).
     const long long streams = (long long)c.grid.ctas * (pkv::kPieceWarps / p.stream_heads);
     const long long pairs = (long long)num_seqs * (n_kv_heads / p.stream_heads);
-    const bool few = c.max_splits + 2 + streams / pairs <= 12;
+    const bool few = p.max_splits + 2 + streams / pairs <= 12;
     const int rows = few ? pkv::kFinishWarps : 1;
     const dim3 grid((unsigned)((n_heads + rows - 1) / rows), (unsigned)num_seqs);
     auto merge = head_dim == 128 ? (few ? pkv::decode_shared_finish_kernel<128, 1>
