@@ -1,8 +1,8 @@
 // attn_prompt_launch.h -- host-side launch interface of attn_prompt_kernel
-// (attn_tc_kernel.cuh).
+// (attn_prompt_kernel.cuh).
 #pragma once
 
-#include "attn_tc_kernel.cuh"
+#include "attn_prompt_kernel.cuh"
 
 namespace pkv {
 

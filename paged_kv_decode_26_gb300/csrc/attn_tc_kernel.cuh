@@ -30,9 +30,11 @@
 // Precision: S, m, l and O are fp32.  P is rounded once to the 16-bit type of
 // V before the second product (at most half an eps relative to each weight,
 // below the rounding of a 16-bit output; weight_range.cuh keeps fp16 weights
-// clear of its smallest numbers) -- the rate of that product rests on
-// it -- except for fp32 outputs, where further products add the remainders
-// (PRECISE, attn_parts).  The sum l adds the unrounded weights.
+// clear of its smallest numbers): the rate of that product rests on it.  The
+// sum l adds the unrounded weights.  O accumulates in the tensor core, which
+// drops what lies below its accumulator's last bit: 2^-24 of O per 16 keys at
+// most, 1e-4 at 32768 keys, below half a step of fp16.  fp32 outputs are formed
+// otherwise (attn_tc_precise.cuh).
 #pragma once
 
 #include "multi_query_tc_kernel.cuh"
@@ -124,25 +126,9 @@ struct AttnSizes {
     [[maybe_unused]] constexpr uint32_t TILE_COLS = AttnSizes<D>::TILE_COLS;                  \
     [[maybe_unused]] constexpr uint32_t S_COL = AttnSizes<D>::S_COL;
 
-// fp32 outputs (PRECISE) need more in two places.  A softmax weight enters the
-// second product as the sum of as many 16-bit parts as fp32 needs: two of fp16
-// (22 bits), three of bf16 (24).  And the tensor core drops the bits of a product
-// below its accumulator's last one, always downwards: over 32768 keys O came out
-// 2e-4 short.  So O of each key tile starts from zero, smallest parts first, and
-// is added to a sum kept beside it by fp32 additions (now 4e-7).  (16-bit
-// outputs accumulate in the tensor core: 2^-24 of O per 16 keys at most, 1e-4 at
-// 32768 keys, below half a step of fp16.)
-// Tensor-memory columns: the first two parts fill those of S, the third lies
-// behind them or in S's of row tile 1, the sum of O in O's of row tile 1: a CTA
-// works on one row tile at a time.
-__host__ __device__ constexpr int attn_parts(bool bf16, bool precise) {
-    return precise ? (bf16 ? 3 : 2) : 1;
-}
+// Row tiles per work item: fp32 outputs are made one at a time
+// (attn_tc_precise.cuh).
 __host__ __device__ constexpr int attn_row_tiles(bool precise) { return precise ? 1 : 2; }
-__host__ __device__ constexpr uint32_t attn_part_col(int D, int k) {
-    return k < 2 ? D + k * 64 : (D == 64 ? D + 128 : 256 + D);
-}
-constexpr uint32_t kAtSumCol = 256;       // the sum of O (PRECISE)
 
 // Barriers and item slots of one CTA, behind the tiles in shared memory.
 struct AttnControl {
@@ -159,6 +145,8 @@ struct AttnControl {
     uint64_t* it_full;      // [kAtItems]
     uint64_t* it_free;
     uint64_t* fin;
+    uint64_t* alpha_full;   // [4]           (attn_tc_precise.cuh)
+    uint64_t* row_full;     // [kAtItems]
     AttnItem* items;
     int* poison;            // [kAtItems] V of the item's last tiles held NaN or infinities
     unsigned char* sQ;
@@ -169,7 +157,7 @@ struct AttnControl {
 };
 
 __host__ __device__ constexpr int attn_bars(int stages) {
-    return 3 * stages + 4 + 2 + 4 + 4 + 2 * kAtItems + 1;
+    return 3 * stages + 4 + 2 + 4 + 4 + 2 * kAtItems + 1 + 4 + kAtItems;
 }
 
 // Bytes behind the tiles: barriers, item slots, flags.
@@ -199,7 +187,9 @@ __device__ __forceinline__ AttnControl attn_control(unsigned char* tiles, unsign
     c.it_full = c.o_free + 2;
     c.it_free = c.it_full + kAtItems;
     c.fin = c.it_free + kAtItems;
-    c.items = reinterpret_cast<AttnItem*>(c.fin + 1);
+    c.alpha_full = c.fin + 1;
+    c.row_full = c.alpha_full + 4;
+    c.items = reinterpret_cast<AttnItem*>(c.row_full + kAtItems);
     c.poison = reinterpret_cast<int*>(c.items + kAtItems);
     c.tmem = 0;
     return c;
@@ -221,9 +211,11 @@ __device__ __forceinline__ void attn_init_barriers(const AttnControl& c) {
         mbar_init(&c.o_full[t], 1);
         mbar_init(&c.o_free[t], 4);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&c.alpha_full[i], 4);
     for (int i = 0; i < kAtItems; ++i) {
         mbar_init(&c.it_full[i], 1);
         mbar_init(&c.it_free[i], 11);
+        mbar_init(&c.row_full[i], 4);
     }
     mbar_init(c.fin, 1);
     fence_barrier_init();
@@ -310,8 +302,9 @@ __device__ __forceinline__ bool attn_guarded(const AttnItem& it, int j) {
     return (j + 1) * kAtKeys > (PAGED ? it.n_keys : it.pos0 + 1);
 }
 
-// Warp 9: queries, K and V by TMA.
-template <int D, bool PAGED>
+// Warp 9: queries, K and V by TMA.  With one row tile per item (PRECISE) items
+// take turns with the two places for queries.
+template <int D, bool PAGED, bool PRECISE>
 __device__ __forceinline__ void attn_loader(const AttnControl& ctl, const AttnParams& p,
                                             const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                             const CUtensorMap& tm_v, int lane) {
@@ -327,7 +320,7 @@ __device__ __forceinline__ void attn_loader(const AttnControl& ctl, const AttnPa
     const uint64_t once = l2_policy_evict_first();
     int slot = 0, sph = 0;          // item ring
     int st = 0, round = 0;          // K/V ring
-    uint32_t q_uses[2] = {0, 0};
+    uint32_t q_uses[2] = {0, 0}, n_q = 0;
     bool ok = true;
     const int per_tile = PAGED ? kAtKeys / p.block_size : 0;
 
@@ -362,17 +355,20 @@ __device__ __forceinline__ void attn_loader(const AttnControl& ctl, const AttnPa
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         if (it.nt[t] == 0) continue;
-                        if (q_uses[t] > 0)
-                            ok = ok && __all_sync(0xffffffffu,
-                                                  mbar_wait(&ctl.q_free[t], (q_uses[t] - 1) & 1,
-                                                            p.errors));
+                        const int at = PRECISE ? (int)(n_q & 1) : t;
+                        const uint32_t uses = PRECISE ? n_q >> 1 : q_uses[t];
+                        if (uses > 0)
+                            ok = ok && __all_sync(0xffffffffu, mbar_wait(&ctl.q_free[at],
+                                                                         (uses - 1) & 1,
+                                                                         p.errors));
                         ++q_uses[t];
+                        ++n_q;
                         if (ok && lane == 0) {
-                            mbar_arrive_expect_tx(&ctl.q_full[t], Q_BYTES);
+                            mbar_arrive_expect_tx(&ctl.q_full[at], Q_BYTES);
 #pragma unroll
                             for (int h = 0; h < HALVES; ++h)
-                                tma_load_4d(ctl.sQ + t * Q_BYTES + h * Q_HALF, &tm_q,
-                                            &ctl.q_full[t], 0, h, it.kvh * G, it.row0 + t * QT,
+                                tma_load_4d(ctl.sQ + at * Q_BYTES + h * Q_HALF, &tm_q,
+                                            &ctl.q_full[at], 0, h, it.kvh * G, it.row0 + t * QT,
                                             once);
                         }
                     }
@@ -511,10 +507,9 @@ __device__ __forceinline__ void attn_guard(const AttnControl& ctl, const AttnPar
 }
 
 // Warp 8: every MMA.
-template <int D, typename T, bool PAGED, bool PRECISE>
+template <int D, typename T, bool PAGED>
 __device__ __forceinline__ void attn_mma(const AttnControl& ctl, const AttnParams& p, int lane) {
     PKV_ATTN_SIZES(D)
-    constexpr int PARTS = attn_parts(std::is_same<T, __nv_bfloat16>::value, PRECISE);
     const uint32_t id_s = tc_idesc<T>(kAtRows, kAtKeys, 0);
     const uint32_t id_o = tc_idesc<T>(kAtRows, D, 1);
     const uint64_t dq0 = tc_desc_sw128(smem_addr(ctl.sQ), 16, 1024);
@@ -620,15 +615,10 @@ __device__ __forceinline__ void attn_mma(const AttnControl& ctl, const AttnParam
                             const uint32_t o = ctl.tmem + t * TILE_COLS;
                             const uint64_t v = dv0 + (uint64_t)(vs * (KV_BYTES >> 4));
 #pragma unroll
-                            for (int part = PARTS - 1; part >= 0; --part)
-#pragma unroll
-                                for (int i = half * 4; i < half * 4 + 4; ++i)
-                                    at_mma_tmem_a(
-                                        o, o + attn_part_col(D, part) + i * 8,
-                                        v + (uint64_t)((i * 16 * 128) >> 4), id_o,
-                                        ((!PRECISE && j > 0) || part < PARTS - 1 || i > 0) ? 1u
-                                                                                           : 0u,
-                                        lead);
+                            for (int i = half * 4; i < half * 4 + 4; ++i)
+                                at_mma_tmem_a(o, o + S_COL + i * 8,
+                                              v + (uint64_t)((i * 16 * 128) >> 4), id_o,
+                                              (j > 0 || i > 0) ? 1u : 0u, lead);
                             if (half && j + 1 == nt) at_commit(&ctl.o_full[t], lead);
                         }
                         __syncwarp();
@@ -680,12 +670,38 @@ __device__ __forceinline__ void bulk_wait() {
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
+__device__ __forceinline__ bool at_finite(float x) { return fabsf(x) <= 3.4e38f; }
+
+// 128 bytes of a thread's output row.  Where the warp's 32 rows all exist they
+// go through shared memory and out by TMA in whole lines: a thread's own
+// 16-byte stores touch 32 lines an instruction and took a fifth of the time of
+// short prompts (GB300, packed prompts of 128-2048 tokens: 185 us, 166 by TMA).
+__device__ __forceinline__ void attn_store(const CUtensorMap& tm_o, unsigned char* stage,
+                                           unsigned char* own, const uint32_t* w, bool all,
+                                           bool real, int c1, int c2, int c3, int lane) {
+    if (all) {
+        if (lane == 0) bulk_read_wait();
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tma_store_4d(&tm_o, smem_addr(stage), c1, c2, c3);
+    } else if (real) {
+        uint4* o4 = reinterpret_cast<uint4*>(own);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            o4[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    }
+}
+
 // Warps 0-7: thread r of group t owns row r of tile t.
-template <int D, typename T, bool PAGED, bool PRECISE>
+template <int D, typename T, bool PAGED>
 __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnParams& p,
                                              const CUtensorMap& tm_o, int warp, int lane) {
     PKV_ATTN_SIZES(D)
-    constexpr int PARTS = attn_parts(std::is_same<T, __nv_bfloat16>::value, PRECISE);
     using Range = WeightRange<T>;
     const int G = p.group;
     const int QT = kAtRows / G;
@@ -720,25 +736,6 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
                 if (!ok) break;
                 ++n_s;
                 tc_fence_after();
-                if (PRECISE && j > 0) {
-                    // O of key tile j - 1 is complete (its products were issued
-                    // before S_j's): to the sum
-#pragma unroll 1
-                    for (int c0 = 0; c0 < D; c0 += 32) {
-                        uint32_t ov[32], sum[32];
-                        tc_ld32(t_lane + c0, ov);
-                        if (j > 1) tc_ld32(t_lane + kAtSumCol + c0, sum);
-                        tc_wait_ld();
-                        if (j > 1) {
-#pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                ov[c] = __float_as_uint(__uint_as_float(ov[c]) +
-                                                        __uint_as_float(sum[c]));
-                        }
-                        tc_st32(t_lane + kAtSumCol + c0, ov);
-                    }
-                    tc_wait_st();
-                }
                 float y[kAtKeys];
                 uint32_t* yr = reinterpret_cast<uint32_t*>(y);
                 tc_ld32(t_lane + S_COL, yr);
@@ -778,11 +775,10 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
                     // O is at rest: the products up to key tile j - 1
                     // completed before S_j did
                     const float2 a2 = make_float2(alpha, alpha);
-                    const uint32_t o_lane = t_lane + (PRECISE ? kAtSumCol : 0u);
 #pragma unroll 1
                     for (int c0 = 0; c0 < D; c0 += 32) {
                         uint32_t ov[32];
-                        tc_ld32(o_lane + c0, ov);
+                        tc_ld32(t_lane + c0, ov);
                         tc_wait_ld();
 #pragma unroll
                         for (int c = 0; c < 32; c += 2) {
@@ -792,45 +788,29 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
                             ov[c] = __float_as_uint(v.x);
                             ov[c + 1] = __float_as_uint(v.y);
                         }
-                        tc_st32(o_lane + c0, ov);
+                        tc_st32(t_lane + c0, ov);
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) l4[i] = __fmul2_rn(l4[i], a2);
                 }
                 const float mu = m_used == -INFINITY ? 0.f : m_used;
                 const float2 aa = make_float2(a, a), nmu = make_float2(-mu, -mu);
-                const float2 neg1 = make_float2(-1.f, -1.f);
-                // 32 keys at a time (two stores per arrival), or 64
-                constexpr int N = PARTS > 1 ? 16 : 32;
 #pragma unroll
-                for (int part = 0; part < 64 / N; ++part) {
-                    uint32_t w[PARTS][N];
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t w[32];
 #pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        const int c = 2 * (part * N + i);
+                    for (int i = 0; i < 32; ++i) {
+                        const int c = half * 64 + 2 * i;
                         const float2 e = __ffma2_rn(make_float2(y[c], y[c + 1]), aa, nmu);
-                        float2 pv = make_float2(exp2f(e.x), exp2f(e.y));
+                        const float2 pv = make_float2(exp2f(e.x), exp2f(e.y));
                         l4[i & 3] = __fadd2_rn(l4[i & 3], pv);
-#pragma unroll
-                        for (int k = 0; k < PARTS; ++k) {
-                            w[k][i] = pack2<T>(pv.x, pv.y);
-                            pv = __ffma2_rn(unpack2<T>(w[k][i]), neg1, pv);
-                        }
+                        w[i] = pack2<T>(pv.x, pv.y);
                     }
-#pragma unroll
-                    for (int k = 0; k < PARTS; ++k) {
-                        const uint32_t col = t_lane + attn_part_col(D, k) + part * N;
-                        if (N == 32)
-                            tc_st32(col, w[k]);
-                        else
-                            tc_st16(col, w[k]);
-                    }
-                    if ((part + 1) * N % 32 == 0) {
-                        tc_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&ctl.p_full[2 * t + (part + 1) * N / 32 - 1]);
-                    }
+                    tc_st32(t_lane + S_COL + half * 32, w);
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl.p_full[2 * t + half]);
                 }
             }
             if (!ok) break;
@@ -849,36 +829,22 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
                                       : row;
             if (PAGED && real)
                 *reinterpret_cast<float2*>(p.pre_ml + unit * 2) = make_float2(m_used, l);
-            // ---- O / l, 128 bytes of every row at a time.  Where the warp's 32
-            // rows all exist they go through shared memory and out by TMA in
-            // whole lines: a thread's own 16-byte stores touch 32 lines an
-            // instruction and took a fifth of the time of short prompts
-            // (GB300, packed prompts of 128-2048 tokens: 184 us).
-            constexpr bool WIDE = PAGED || PRECISE;            // fp32 rows
-            constexpr int COLS = WIDE ? 32 : 64;
+            // ---- O / l, 128 bytes of every row at a time (partial states are fp32)
+            constexpr int COLS = PAGED ? 32 : 64;
             const int warp_row = (warp & 3) * 32;
             const bool all = t * QT + (warp_row + 31) / G < it.rows;
             const bool poison = !PAGED && ctl.poison[slot] != 0;
             unsigned char* stage = ctl.sOut + warp * 32 * 128;
             unsigned char* own = static_cast<unsigned char*>(PAGED ? p.pre_o : p.out) +
-                                 unit * D * (WIDE ? 4 : 2);
+                                 unit * D * (PAGED ? 4 : 2);
 #pragma unroll 1
             for (int g = 0; g < D / COLS; ++g) {
                 uint32_t w[32];
                 if (bad) {
 #pragma unroll
                     for (int c = 0; c < 32; ++c) w[c] = 0u;
-                } else if (WIDE) {
+                } else if (PAGED) {
                     tc_ld32(t_lane + g * 32, w);
-                    if (PRECISE && nt > 1) {
-                        uint32_t sum[32];
-                        tc_ld32(t_lane + kAtSumCol + g * 32, sum);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            w[c] = __float_as_uint(__uint_as_float(w[c]) +
-                                                   __uint_as_float(sum[c]));
-                    }
                     tc_wait_ld();
 #pragma unroll
                     for (int c = 0; c < 32; ++c)
@@ -896,25 +862,20 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
                 if (poison) {
                     // NaN and infinities that the guard took out of V, from the
                     // rows that this query sees
-                    const int at = g * COLS;
 #pragma unroll 1
                     for (int key = it.pos0 / kAtKeys * kAtKeys; key <= min(pos, it.n_keys - 1);
                          ++key) {
                         const T* v = static_cast<const T*>(p.v) +
-                                     (size_t)(it.key_row + key) * p.v_stride + it.kvh * D + at;
+                                     (size_t)(it.key_row + key) * p.v_stride + it.kvh * D + g * 64;
 #pragma unroll
                         for (int c = 0; c < 32; ++c) {
-                            const float x = to_float<T>(v[WIDE ? c : 2 * c]);
-                            const float y = to_float<T>(v[WIDE ? c : 2 * c + 1]);
-                            if (WIDE) {
-                                if (!(fabsf(x) <= 3.4e38f))
-                                    w[c] = __float_as_uint(__uint_as_float(w[c]) + x);
-                            } else if (!(fabsf(x) <= 3.4e38f) || !(fabsf(y) <= 3.4e38f)) {
+                            const float x = to_float<T>(v[2 * c]), y = to_float<T>(v[2 * c + 1]);
+                            if (!at_finite(x) || !at_finite(y)) {
                                 const float2 o = p.out_dtype == PKV_BF16
                                                      ? unpack2<__nv_bfloat16>(w[c])
                                                      : unpack2<__half>(w[c]);
-                                w[c] = pack_out(fabsf(x) <= 3.4e38f ? o.x : o.x + x,
-                                                fabsf(y) <= 3.4e38f ? o.y : o.y + y, p.out_dtype);
+                                w[c] = pack_out(at_finite(x) ? o.x : o.x + x,
+                                                at_finite(y) ? o.y : o.y + y, p.out_dtype);
                             }
                         }
                     }
@@ -924,25 +885,9 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ctl.o_free[t]);
                 }
-                if (all) {
-                    if (lane == 0) bulk_read_wait();
-                    __syncwarp();
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        *reinterpret_cast<uint4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
-                            make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0)
-                        tma_store_4d(&tm_o, smem_addr(stage),
-                                     g + (PAGED ? (bad ? -1 - it.split : it.split) * (D / 32) : 0),
-                                     it.kvh * G, it.row0 + t * QT + warp_row / G);
-                } else if (real) {
-                    uint4* o4 = reinterpret_cast<uint4*>(own + g * 128);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        o4[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-                }
+                attn_store(tm_o, stage, own + g * 128, w, all, real,
+                           g + (PAGED ? (bad ? -1 - it.split : it.split) * (D / 32) : 0),
+                           it.kvh * G, it.row0 + t * QT + warp_row / G, lane);
             }
         }
         __syncwarp();
@@ -954,146 +899,6 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
     }
     if (lane == 0) bulk_wait();
     __syncwarp();
-}
-
-// The work item i of a launch over whole prompts; false: it is empty.  The
-// last pair of tiles of every sequence comes first.
-__device__ __forceinline__ bool attn_prompt_item(const AttnParams& p, long long i, AttnItem& it) {
-    const int G = p.group, QT = kAtRows / G;
-    const long long per_tile = (long long)p.n_kv_heads * p.num_seqs;
-    const int back = (int)(i / per_tile);
-    const int x = (int)(i % per_tile);
-    const int s = x / p.n_kv_heads;
-    it.done = 0;
-    it.kvh = x % p.n_kv_heads;
-    const int q0 = p.q_start[s], q1 = p.q_start[s + 1];
-    const int len = q1 - q0;
-    if (q0 < 0 || len < 0 || q1 > p.total_q || len > p.max_len) {
-        if (back == 0 && it.kvh == 0) raise_error(p.errors, PKV_DEVERR_CONTEXT);
-        return false;
-    }
-    const int NT = p.row_tiles * QT;         // tokens per item
-    const int lo = ((len + NT - 1) / NT - 1 - back) * NT;
-    if (lo < 0 || len == 0) return false;
-    it.row0 = q0 + lo;
-    it.rows = min(len - lo, NT);
-    it.pos0 = lo;
-    it.key_row = q0;
-    it.key0 = 0;
-    it.n_keys = len;
-    it.split = 0;
-    it.nt[0] = (min(len, lo + QT) + kAtKeys - 1) / kAtKeys;
-    it.nt[1] = it.rows > QT ? (min(len, lo + 2 * QT) + kAtKeys - 1) / kAtKeys : 0;
-    return true;
-}
-
-// Whole prompts.  With `dynamic` there is a CTA for every item: a running one
-// takes its own item, then, one after the other, those of CTAs that have not
-// started yet.  Otherwise CTA c takes items c, c + grid, ...
-template <int D, typename T, bool PRECISE>
-__global__ void __launch_bounds__(kAtThreads, 1)
-    attn_prompt_kernel(const __grid_constant__ CUtensorMap tm_q,
-                       const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v,
-                       const __grid_constant__ CUtensorMap tm_o,
-                       const __grid_constant__ AttnParams p) {
-    extern __shared__ __align__(1024) unsigned char smem_raw[];
-    const uint32_t raw = smem_addr(smem_raw);
-    unsigned char* sm = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
-    unsigned char* control = sm + attn_tile_bytes(D, p.stages);
-    uint4* steal = reinterpret_cast<uint4*>(control);
-    uint64_t* steal_bar = reinterpret_cast<uint64_t*>(control + 16);
-    int* s_tmem = reinterpret_cast<int*>(control + 24);
-    AttnControl c = attn_control<D>(sm, control + 32, p.stages);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-    if (warp == 8) attn_tmem_alloc(s_tmem);
-    if (threadIdx.x == 0) {
-        attn_init_barriers(c);
-        mbar_init(steal_bar, 1);
-        fence_barrier_init();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    c.tmem = (uint32_t)*s_tmem;
-
-    if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtOtherRegs));
-        if (warp == 8) {
-            attn_mma<D, T, false, PRECISE>(c, p, lane);
-        } else if (warp == 9) {
-            attn_loader<D, false>(c, p, tm_q, tm_k, tm_v, lane);
-        } else if (warp == 11) {
-            attn_guard<D, T, false>(c, p, lane);
-        } else if (warp == 10) {
-            // ---- scheduler; lanes look at 32 items at once
-            const bool dynamic = p.dynamic != 0;
-            const long long stride = dynamic ? p.n_items : gridDim.x;
-            uint32_t steal_ph = 0;
-            int slot = 0, round = 0;
-            bool ok = true;
-            auto slot_free = [&]() {
-                return round == 0 ||
-                       __all_sync(0xffffffffu,
-                                  mbar_wait(&c.it_free[slot], (round - 1) & 1, p.errors));
-            };
-            auto put = [&](const AttnItem& it, bool mine) {
-                if (mine) {
-                    c.items[slot] = it;
-                    mbar_arrive(&c.it_full[slot]);
-                }
-                if (++slot == kAtItems) {
-                    slot = 0;
-                    ++round;
-                }
-            };
-            for (long long base = blockIdx.x; ok;) {
-                const long long i = base + (long long)lane * stride;
-                AttnItem it;
-                const bool have = i < p.n_items && attn_prompt_item(p, i, it);
-                unsigned todo = __ballot_sync(0xffffffffu, have);
-                while (todo && (ok = slot_free())) {
-                    put(it, lane == __ffs(todo) - 1);
-                    todo &= todo - 1;
-                }
-                if (!ok) break;
-                bool more;
-                if (dynamic) {
-                    // ask for another item only when there is a slot for it:
-                    // what waits here cannot go to an idle SM
-                    if (!(ok = slot_free())) break;
-                    if (lane == 0) steal_cta(steal, steal_bar);
-                    ok = __all_sync(0xffffffffu, mbar_wait(steal_bar, steal_ph, p.errors));
-                    steal_ph ^= 1u;
-                    if (!ok) break;
-                    const int next = stolen_cta(steal);
-                    __syncwarp();
-                    more = next >= 0;
-                    if (more) base = next;
-                } else {
-                    base += 32ll * stride;
-                    more = __any_sync(0xffffffffu, base < p.n_items);
-                }
-                if (!more) {
-                    if (slot_free()) {
-                        it.done = 1;
-                        put(it, lane == 0);
-                    }
-                    break;
-                }
-            }
-        }
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAtSoftmaxRegs));
-        attn_softmax<D, T, false, PRECISE>(c, p, tm_o, warp, lane);
-    }
-
-    // ---- tensor memory is released after every thread is done with it
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    if (warp == 8) attn_tmem_free(c.tmem);
 }
 
 }  // namespace pkv

@@ -8,7 +8,7 @@
 // a group has many rows, by HBM where it has few.
 #pragma once
 
-#include "attn_tc_kernel.cuh"
+#include "attn_tc_precise.cuh"
 
 namespace pkv {
 
@@ -104,9 +104,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtOtherRegs));
         if (warp == 8) {
-            attn_mma<D, T, true, PRECISE>(c, p, lane);
+            if (PRECISE)
+                attn_mma_precise<D, T, true>(c, p, lane);
+            else
+                attn_mma<D, T, true>(c, p, lane);
         } else if (warp == 9) {
-            attn_loader<D, true>(c, p, tm_q, tm_k, tm_v, lane);
+            attn_loader<D, true, PRECISE>(c, p, tm_q, tm_k, tm_v, lane);
         } else if (warp == 11) {
             attn_guard<D, T, true>(c, p, lane);
         } else if (warp == 10) {
@@ -144,7 +147,12 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAtSoftmaxRegs));
-        attn_softmax<D, T, true, PRECISE>(c, p, tm_o, warp, lane);
+        if (!PRECISE)
+            attn_softmax<D, T, true>(c, p, tm_o, warp, lane);
+        else if (warp < 4)
+            attn_softmax_precise<D, T, true>(c, p, warp, lane);
+        else
+            attn_sum_precise<D, T, true>(c, p, tm_o, warp, lane);
     }
 
     // ---- tensor memory is released after every thread is done with it
