@@ -387,16 +387,19 @@ PKV_API pkv_status kv_evict(void* k_pool, void* v_pool, pkv_dtype dtype,
         if ((e = cudaLaunchKernelEx(&cfg, pkv::evict_select_kernel, p)) != cudaSuccess)
             return cuda_fail(e);
     }
-    // 32 tokens per warp, fewer while the warps that stay resident (3 CTAs
-    // per SM) get less than two units each: in a small batch short units
-    // spread over the SMs (64 tokens of 1 KB rows on 16 warps took 23 us, on
-    // 256 5 us) and even out the end of the launch (32768 rows of 2 KB: 46 us
-    // at 32, 40 at 4).
+    // Units of 32 tokens, shorter ones until the warps that are resident (3
+    // CTAs per SM) get sixteen each: SMs copy at different rates, and CTAs of
+    // short units start where one has ended (64 sequences cut to 1024 tokens of
+    // 8 KB rows, 310 us at two units a warp, 286 at sixteen).  Below four tokens
+    // a unit's table lookups weigh more than that (4 sequences cut to 8192
+    // tokens of 2 KB rows, 60.6 us at four, 62.2 at one), unless there are not
+    // two units for each warp (64 tokens of 1 KB rows on 16 warps took 23 us, on
+    // 256 5 us).
     const int warps = pkv::kEvictCopyThreads / 32;
-    const long long resident = 3LL * dev->sm_count, cap = 8LL * dev->sm_count;
+    const long long resident = 3LL * dev->sm_count * warps, cap = 64LL * dev->sm_count;
     p.batch = 32;
     auto count = [&] { return (long long)num_seqs * ((keep + p.batch - 1) / p.batch) * p.parts; };
-    while (p.batch > 1 && count() < 2 * warps * resident) p.batch /= 2;
+    while (p.batch > 1 && count() < (p.batch > 4 ? 16 : 2) * resident) p.batch /= 2;
     long long ctas = (count() + warps - 1) / warps;
     if (ctas > cap) ctas = cap;
     const dim3 grid((unsigned)ctas);
