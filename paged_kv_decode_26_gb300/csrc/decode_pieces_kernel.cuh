@@ -808,9 +808,6 @@ __global__ void __launch_bounds__(kPieceThreads + (TAKES ? 32 : 0), 1)
             if (cta < 0) break;
         }
     }
-    // the finishing kernel waits for this one only: it must not end before
-    // the prefix kernel that may run ahead of it
-    if (!WEIGHTS) dependency_wait();
 }
 
 // Sum of a (sequence, head)'s partial states: their merged maximum and the

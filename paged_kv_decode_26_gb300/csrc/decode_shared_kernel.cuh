@@ -1,6 +1,6 @@
 // decode_shared_kernel.cuh -- paged_attn_decode_shared's prefixes: the queries
 // of a group's sequences against the keys that they share, on tcgen05
-// (attn_tc_kernel.cuh's roles).  The rest of every context runs as pieces
+// (attn_tc_kernel.cuh's roles).  The rest of every context runs ahead as pieces
 // (decode_pieces_kernel.cuh) and decode_shared_finish_kernel merges the two.
 //
 // A work item is a split of a prefix x a kv head x a pair of row tiles (256
@@ -77,7 +77,9 @@ __device__ __forceinline__ bool attn_prefix_item(const AttnParams& a, long long 
     return true;
 }
 
-// CTA c takes candidates c, c + grid, ...
+// With `dynamic` there is a CTA for every candidate: a running one takes its
+// own, then, one after the other, those of CTAs that have not started yet.
+// Otherwise CTA c takes candidates c, c + grid, ...
 template <int D, typename T, bool PRECISE>
 __global__ void __launch_bounds__(kAtThreads, 1)
     attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -90,12 +92,18 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     const uint32_t raw = smem_addr(smem_raw);
     unsigned char* sm = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     unsigned char* control = sm + attn_tile_bytes(D, p.stages);
-    int* s_tmem = reinterpret_cast<int*>(control);
+    uint4* steal = reinterpret_cast<uint4*>(control);
+    uint64_t* steal_bar = reinterpret_cast<uint64_t*>(control + 16);
+    int* s_tmem = reinterpret_cast<int*>(control + 24);
     AttnControl c = attn_control<D>(sm, control + 32, p.stages);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (warp == 8) attn_tmem_alloc(s_tmem);
-    if (threadIdx.x == 0) attn_init_barriers(c);
+    if (threadIdx.x == 0) {
+        attn_init_barriers(c);
+        mbar_init(steal_bar, 1);
+        fence_barrier_init();
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -114,13 +122,18 @@ __global__ void __launch_bounds__(kAtThreads, 1)
             attn_guard<D, T, true>(c, p, lane);
         } else if (warp == 10) {
             // ---- scheduler; lanes look at 32 candidates at once
+            const bool dynamic = p.dynamic != 0;
+            const long long stride = dynamic ? p.n_items : gridDim.x;
+            uint32_t steal_ph = 0;
             int slot = 0, round = 0;
             bool ok = true;
+            auto slot_free = [&]() {
+                return round == 0 ||
+                       __all_sync(0xffffffffu,
+                                  mbar_wait(&c.it_free[slot], (round - 1) & 1, p.errors));
+            };
             auto put = [&](const AttnItem& it) {
-                ok = round == 0 ||
-                     __all_sync(0xffffffffu,
-                                mbar_wait(&c.it_free[slot], (round - 1) & 1, p.errors));
-                if (!ok) return;
+                if (!(ok = slot_free())) return;
                 if (lane == 0) {
                     c.items[slot] = it;
                     mbar_arrive(&c.it_full[slot]);
@@ -131,14 +144,26 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                 }
             };
             AttnItem it;
-            for (long long base = blockIdx.x; ok && base < p.n_items; base += 32ll * gridDim.x) {
-                const long long i = base + (long long)lane * gridDim.x;
+            for (long long base = blockIdx.x; ok && base < p.n_items;) {
+                const long long i = base + (long long)lane * stride;
                 unsigned todo = __ballot_sync(0xffffffffu,
                                               i < p.n_items && attn_prefix_candidate(p, i));
                 for (; ok && todo; todo &= todo - 1)
-                    if (attn_prefix_item(p, base + (long long)(__ffs(todo) - 1) * gridDim.x, lane,
+                    if (attn_prefix_item(p, base + (long long)(__ffs(todo) - 1) * stride, lane,
                                          it))
                         put(it);
+                base += 32ll * stride;
+                if (dynamic && ok) {
+                    // ask for another item only when there is a slot for it
+                    if (!(ok = slot_free())) break;
+                    if (lane == 0) steal_cta(steal, steal_bar);
+                    ok = __all_sync(0xffffffffu, mbar_wait(steal_bar, steal_ph, p.errors));
+                    steal_ph ^= 1u;
+                    if (!ok) break;
+                    const int next = stolen_cta(steal);
+                    __syncwarp();
+                    if (next >= 0) base = next;
+                }
             }
             if (ok) {
                 it.done = 1;
@@ -160,6 +185,9 @@ __global__ void __launch_bounds__(kAtThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp == 8) attn_tmem_free(c.tmem);
+    // the merging kernel waits for this one only: it must not end before the
+    // pieces that run ahead of it
+    dependency_wait();
 }
 
 }  // namespace pkv

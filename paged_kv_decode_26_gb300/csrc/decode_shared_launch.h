@@ -20,8 +20,8 @@ struct SharedLaunch {
     cudaStream_t stream;
 };
 
-// Launch attn_prefix_kernel<D, T, precise> and, as SMs get free of it,
-// decode_pieces_kernel<D, T, false>.
+// Launch decode_pieces_kernel<D, T, false> and, as SMs get free of it,
+// attn_prefix_kernel<D, T, precise>.
 cudaError_t launch_shared_bf16(int D, bool precise, const SharedLaunch& L);
 cudaError_t launch_shared_f16(int D, bool precise, const SharedLaunch& L);
 

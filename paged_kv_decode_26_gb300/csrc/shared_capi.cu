@@ -71,9 +71,7 @@ SharedShape shared_shape(int num_seqs, int num_groups, int max_group, int max_pr
         }
         c.max_splits = (int)(((long long)max_prefix + c.split_tokens - 1) / c.split_tokens);
     }
-    // (no short runs: CTAs that start late, behind the prefixes, even out
-    // little, and the further pieces cost more -- 128 contexts of 1-5K tokens:
-    // 202 us without, 206 us with)
+    // (no short runs to take over: the prefixes fill the SMs that end early)
     c.grid = pieces_grid(num_seqs, n_kv_heads, max_context_len, sm_count, false);
     c.pieces = pieces_workspace(num_seqs, n_heads, n_kv_heads, head_dim, c.grid);
     const size_t rows = (size_t)num_seqs * n_heads * c.max_splits;
@@ -198,7 +196,9 @@ PKV_API pkv_status paged_attn_decode_shared(
         a.pre_ml = reinterpret_cast<float*>(ws + c.pre_ml);
         a.errors = dev->errors;
         a.n_items = (long long)num_groups * n_kv_heads * a.tiles * c.max_splits;
-        L.prefix_ctas = (int)(a.n_items < dev->sm_count ? a.n_items : dev->sm_count);
+        // (as for prompts; beyond that many candidates most may be empty)
+        a.dynamic = a.n_items > dev->sm_count && a.n_items <= 16 * dev->sm_count;
+        L.prefix_ctas = (int)(a.dynamic || a.n_items < dev->sm_count ? a.n_items : dev->sm_count);
     }
     const bool precise = out_dtype == PKV_F32;
     e = kv_dtype == PKV_BF16 ? pkv::launch_shared_bf16(head_dim, precise, L)
