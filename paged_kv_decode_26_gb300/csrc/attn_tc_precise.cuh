@@ -14,8 +14,12 @@
 // two buffers of S and P (192 columns each: S or two parts, and the third), so
 // that S of the next key tile is there when the softmax is done with this one.
 // Warps 0-3 are the softmax, a thread per row; warps 4-7 hold the sums, a thread
-// per row, and write the output.  What bounds it: the tensor core, with 3 or 4
-// products of 128 x 128 x D per key tile (16-bit outputs: 2), and P's parts.
+// per row, and write the output.  What bounds it: the softmax, 4000 cycles a key
+// tile of which 3000 (bf16; fp16 2260) form and store P's parts, one warp per
+// scheduler; the tensor core's 3 or 4 products of 128 x 128 x D take 1536 or
+// 2048.  GB300, sixteen prompts of 128-2048 tokens, 32/8 heads of 128: 473 us
+// (fp16 417); with O summed in tensor memory by the softmax warps, in turn with
+// everything else, 672 (507).
 #pragma once
 
 #include "attn_tc_kernel.cuh"
