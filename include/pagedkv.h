@@ -575,7 +575,8 @@ PKV_API pkv_status paged_attn_decode_shared(
  * PKV_DEVERR_CONTEXT.  The softmax weights enter the second product rounded to
  * dtype, except for F32 outputs (as the sum of two F16 or three BF16 parts).
  * NaN and infinities in rows of k and v reach only the tokens that see those
- * rows (an infinity in v as an infinity or NaN).  One launch, no workspace.
+ * rows (an infinity in v as an infinity or NaN).  One launch (several where
+ * num_seqs and max_len allow more than 2^31 tiles), no workspace.
  */
 PKV_API pkv_status pkv_attn_prompt(void* out, pkv_dtype out_dtype, const void* q, int64_t q_stride,
                                const void* k, int64_t k_stride, const void* v, int64_t v_stride,

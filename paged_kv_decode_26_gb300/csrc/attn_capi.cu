@@ -2,6 +2,7 @@
 // Declarations and contracts: pagedkv.h.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -10,6 +11,15 @@
 #include "capi_host.h"
 
 using namespace pkv::host;
+
+namespace {
+
+// Prompts of this length and K and V of these bytes (what L2 holds) are worked
+// on in bands of items.
+constexpr int kBandLength = 4096;
+constexpr double kBandBytes = 128e6;
+
+}  // namespace
 
 namespace pkv {
 namespace host {
@@ -95,8 +105,9 @@ PKV_API pkv_status pkv_attn_prompt(void* out, pkv_dtype out_dtype, const void* q
     const int row_tiles = pkv::attn_row_tiles(out_dtype == PKV_F32);
     const int item_tokens = row_tiles * pkv::kAtRows / G;
     const int tiles = (max_len + item_tokens - 1) / item_tokens;
-    const long long per_tile = (long long)n_kv_heads * num_seqs;
-    if (per_tile > 0x7fffffffLL) return unsupported("n_kv_heads * num_seqs exceeds 2^31 - 1");
+    if ((long long)n_kv_heads * num_seqs > 0x7fffffffLL ||
+        (long long)n_kv_heads * ((long long)tiles + 8) > 0x7fffffffLL)
+        return unsupported("n_kv_heads * num_seqs or n_kv_heads * max_len too large");
     DeviceInfo* dev = nullptr;
     cudaError_t e = device_info(&dev);
     if (e != cudaSuccess) return cuda_fail(e);
@@ -116,7 +127,6 @@ PKV_API pkv_status pkv_attn_prompt(void* out, pkv_dtype out_dtype, const void* q
     pkv::AttnParams& p = L.p;
     p.out = out;
     p.out_dtype = out_dtype;
-    p.num_seqs = num_seqs;
     p.n_heads = n_heads;
     p.n_kv_heads = n_kv_heads;
     p.group = G;
@@ -124,28 +134,45 @@ PKV_API pkv_status pkv_attn_prompt(void* out, pkv_dtype out_dtype, const void* q
     p.stages = attn_stages(head_dim, dev->smem_optin);
     p.row_tiles = row_tiles;
     p.tiles = tiles;
-    p.n_items = per_tile * tiles;
-    p.q_start = q_start;
+    // Items are handed out longest first over all sequences and heads.  Where
+    // that would stream K and V from DRAM again for every item (more of them
+    // than L2 holds, read by many items each), eight items of a head go
+    // together (GB300: prompts of 4096-8192 tokens, 32 heads, 201 MB of K and V,
+    // 600 and 575 us, and 650 / 590 back to back, where power limits the clock;
+    // 16 of 4096, 8 kv heads, 268 MB, 1524 / 1379; but 16 of 2048, 134 MB, 450 /
+    // 467, and 6 of 4096, 101 MB, 595 / 605).
+    const double kv_bytes = 4.0 * total_q * n_kv_heads * head_dim;
+    p.band = max_len >= kBandLength && kv_bytes >= kBandBytes ? 8 : 1;
     p.total_q = total_q;
     p.max_len = max_len;
     p.v = v;
     p.v_stride = v_stride;
     p.errors = dev->errors;
-    // Where there are more items than SMs, a CTA per item, and running CTAs
-    // take over the waiting ones' items, so that the SMs finish together
-    // (GB300: packed prompts of 128-2048 tokens, grouped heads, 221 us dealt
-    // out in turn, 191 us taken over; prompts of 6.8K and 8K tokens 744 and
-    // 707 us).  Where lengths differ so much that most items of the longest
-    // sequence's count are empty, the CTAs skip those 32 at a time instead.
-    const long long real = (long long)n_kv_heads * ((long long)total_q / item_tokens + num_seqs);
-    p.dynamic = p.n_items > dev->sm_count && p.n_items <= 2 * real && p.n_items <= 0x7fffffffLL;
-    L.ctas = (int)(p.dynamic || p.n_items < dev->sm_count ? p.n_items : dev->sm_count);
     L.smem_bytes = pkv::attn_tc_smem_bytes(head_dim, p.stages);
     L.stream = static_cast<cudaStream_t>(stream);
     const bool precise = out_dtype == PKV_F32;
-    e = dtype == PKV_BF16 ? pkv::launch_attn_prompt_bf16(head_dim, precise, L)
-                          : pkv::launch_attn_prompt_f16(head_dim, precise, L);
-    return e == cudaSuccess ? PKV_OK : cuda_fail(e);
+    // one launch, unless the bounds allow 2^31 items
+    const long long per_seq = (long long)n_kv_heads * ((tiles + p.band - 1) / p.band * p.band);
+    const int step = (int)std::min((long long)num_seqs, 0x7fffffffLL / per_seq);
+    for (long long s0 = 0; s0 < num_seqs; s0 += step) {
+        p.q_start = q_start + s0;
+        p.num_seqs = (int)std::min((long long)step, num_seqs - s0);
+        p.n_items = per_seq * p.num_seqs;
+        // Where there are more items than SMs, a CTA per item, and running CTAs
+        // take over the waiting ones' items, so that the SMs finish together
+        // (GB300: packed prompts of 128-2048 tokens, grouped heads, 221 us dealt
+        // out in turn, 191 us taken over; prompts of 6.8K and 8K tokens 744 and
+        // 707 us).  Where lengths differ so much that most items of the longest
+        // sequence's count are empty, the CTAs skip those 32 at a time instead.
+        const long long real =
+            (long long)n_kv_heads * ((long long)total_q / item_tokens + p.num_seqs);
+        p.dynamic = p.n_items > dev->sm_count && p.n_items <= 2 * real;
+        L.ctas = (int)(p.dynamic || p.n_items < dev->sm_count ? p.n_items : dev->sm_count);
+        e = dtype == PKV_BF16 ? pkv::launch_attn_prompt_bf16(head_dim, precise, L)
+                              : pkv::launch_attn_prompt_f16(head_dim, precise, L);
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    return PKV_OK;
 }
 
 }  // extern "C"

@@ -7,12 +7,14 @@
 namespace pkv {
 
 // The work item i of a launch over whole prompts; false: it is empty.  The
-// last pair of tiles of every sequence comes first.
-__device__ __forceinline__ bool attn_prompt_item(const AttnParams& p, long long i, AttnItem& it) {
+// last tiles of every sequence come first: `band` items of a sequence and kv
+// head, then those of the next.
+__device__ __forceinline__ bool attn_prompt_item(const AttnParams& p, unsigned i, AttnItem& it) {
     const int G = p.group, QT = kAtRows / G;
-    const long long per_tile = (long long)p.n_kv_heads * p.num_seqs;
-    const int back = (int)(i / per_tile);
-    const int x = (int)(i % per_tile);
+    const unsigned band = (unsigned)p.n_kv_heads * p.num_seqs * p.band;
+    const unsigned in_band = i % band;
+    const int x = (int)(in_band / p.band);
+    const int back = (int)(i / band * p.band + in_band % p.band);
     const int s = x / p.n_kv_heads;
     it.done = 0;
     it.kvh = x % p.n_kv_heads;
@@ -82,7 +84,7 @@ __global__ void __launch_bounds__(kAtThreads, 1)
         } else if (warp == 10) {
             // ---- scheduler; lanes look at 32 items at once
             const bool dynamic = p.dynamic != 0;
-            const long long stride = dynamic ? p.n_items : gridDim.x;
+            const unsigned n_items = (unsigned)p.n_items;
             uint32_t steal_ph = 0;
             int slot = 0, round = 0;
             bool ok = true;
@@ -101,10 +103,11 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     ++round;
                 }
             };
-            for (long long base = blockIdx.x; ok;) {
-                const long long i = base + (long long)lane * stride;
+            for (unsigned base = blockIdx.x; ok;) {
+                const unsigned i = base + lane * gridDim.x;
                 AttnItem it;
-                const bool have = i < p.n_items && attn_prompt_item(p, i, it);
+                const bool have = i < n_items && (lane == 0 || !dynamic) &&
+                                  attn_prompt_item(p, i, it);
                 unsigned todo = __ballot_sync(0xffffffffu, have);
                 while (todo && (ok = slot_free())) {
                     put(it, lane == __ffs(todo) - 1);
@@ -125,8 +128,8 @@ __global__ void __launch_bounds__(kAtThreads, 1)
                     more = next >= 0;
                     if (more) base = next;
                 } else {
-                    base += 32ll * stride;
-                    more = __any_sync(0xffffffffu, base < p.n_items);
+                    base += 32 * gridDim.x;
+                    more = base < n_items;
                 }
                 if (!more) {
                     if (slot_free()) {

@@ -72,6 +72,7 @@ struct AttnParams {
     int stages;                // slots of the K/V ring
     int row_tiles;             // row tiles per work item: 2, or 1
     int tiles;                 // items of row tiles of the longest sequence / largest group
+    int band;                  // prompts: neighbouring items of a sequence and kv head
     long long n_items;
     int dynamic;               // prompts: one CTA per item, running CTAs take over waiting ones
     // whole prompts

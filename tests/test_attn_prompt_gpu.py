@@ -224,3 +224,52 @@ def test_prompt_repeats_and_graph_and_stream():
     pkv.attn_prompt(out, *dev, starts, 0.09, 300, stream=side)
     side.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("H,Hk,out_dtype", [(8, 8, BF), (16, 8, F32)])
+def test_long_prompts_beyond_the_cache(H, Hk, out_dtype):
+    """Long prompts whose K and V exceed L2 (items of a head go together), of
+    ragged lengths: sampled rows of every sequence and head."""
+    _clean()
+    lens, D = [9000, 4097, 1, 0, 700, 8192, 5000, 6001], 128
+    starts = _starts(lens, lead=3)
+    parts, dev = _inputs(starts[-1] + 5, H, Hk, D, BF, True)
+    out = torch.full((starts[-1] + 5, H, D), 7.0, dtype=out_dtype, device="cuda")
+    scale = 1 / math.sqrt(D)
+    pkv.attn_prompt(out, *dev, torch.tensor(starts, dtype=torch.int32, device="cuda"), scale, 9000)
+    assert _clean() == 0
+    assert (out[:3] == 7).all() and (out[-5:] == 7).all()
+    q, k, v = parts
+    g = torch.Generator().manual_seed(2)
+    for a, n in zip(starts, lens):
+        if n == 0:
+            continue
+        rows = torch.unique(torch.cat([torch.tensor([0, n - 1, n // 2]),
+                                       torch.randint(n, (12,), generator=g)]))
+        hidden = torch.arange(n)[None] > rows[:, None]
+        for h in range(H):
+            o, _, A, d = ref.attend(q[a + rows, h], k[a:a + n, h * Hk // H],
+                                    v[a:a + n, h * Hk // H], scale, hidden)
+            b = ref.out_bound(o, A, d, BF, out_dtype, once=out_dtype != F32)
+            ref.check(out[a + rows, h], o, b, f"sequence at {a}, head {h}")
+
+
+def test_bounds_that_allow_more_than_2_to_31_tiles():
+    """A hundred thousand sequences, nearly all empty, under a bound of a
+    million tokens each: several launches, each passing over empty items."""
+    _clean()
+    S, T, H, D = 100000, 1 << 20, 8, 64
+    lens = torch.zeros(S, dtype=torch.int64)
+    lens[0], lens[50000], lens[S - 1] = 100, 333, 1
+    starts = torch.cat([torch.zeros(1, dtype=torch.int64), lens.cumsum(0)])
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randn(T, H, D, generator=g, device="cuda").to(BF)
+    k, v = (torch.randn(T, 1, D, generator=g, device="cuda").to(BF) for _ in range(2))
+    out = torch.full((T, H, D), 7.0, dtype=BF, device="cuda")
+    pkv.attn_prompt(out, q, k, v, starts.int().cuda(), 0.125, T)
+    assert _clean() == 0
+    n = int(starts[-1])
+    assert (out[n:] == 7).all()
+    real = [0, 100, 433, 434]
+    o, b = _reference(tuple(x[:n].cpu() for x in (q, k, v)), real, 0.125, BF)
+    ref.check(out[:n], o, b)

@@ -89,3 +89,32 @@ def test_workspace_covers_either_way():
         assert e.value.status == _lib.PKV_ERR_WORKSPACE
     finally:
         pkv.reset_tuning()
+
+
+@pytest.mark.parametrize("groups,H", [(60, 32), (400, 8)])
+def test_items_beyond_the_sms_in_a_graph(groups, H):
+    """More prefix items than SMs, taken over by running CTAs (480), and so many
+    that they are dealt out in turn (3200); captured and replayed."""
+    Hk, D, B = 8, 64, 16
+    lens = [B * 9 + 1 + i % 40 for i in range(2 * groups)]
+    starts, prefix = list(range(0, 2 * groups + 1, 2)), [B * 8] * groups
+    c = base._problem(lens, starts, prefix, H, Hk, D, B, BF)
+    pkv.set_tuning(shared_prefix=1)
+    try:
+        want = base._run(c, starts, prefix, BF, max(lens))
+        out, q = torch.empty_like(want), c["q"].cuda()
+        gs, pl = _ints(starts), _ints(prefix)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            pkv.paged_attn_decode_shared(out, q, c["k_pool"], c["v_pool"], c["tables"], c["lens"],
+                                         gs, pl, c["scale"], max(lens), 2, B * 8)
+        for _ in range(3):
+            out.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
+    finally:
+        pkv.reset_tuning()
+    assert pkv.device_errors(clear=True) == 0
+    o, bound, _ = ref.decode(c["q"], c["k"], c["v"], c["scale"], BF, once=True)
+    ref.check(want, o, bound)
