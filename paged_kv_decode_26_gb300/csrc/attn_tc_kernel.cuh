@@ -28,9 +28,9 @@
 // overlap the last softmax and the output of the current one.
 //
 // What bounds it: the tensor core and the softmax in turn.  GB300: two prompts of
-// 4096-8192 tokens, 32 heads of 128: 600 us, 1.55 PFLOP/s (0.82 of the burst rate
-// measured for a library product; the tensor pipe is active 74 % of the time;
-// 650-700 us when calls follow one another for long, limited by power); sixteen
+// 4096-8192 tokens, 32 heads of 128: 580 us, 1.60 PFLOP/s (0.84 of the burst rate
+// measured for a library product; the tensor pipe is active 72 % of the time;
+// 610-655 us when calls follow one another for long, limited by power); sixteen
 // of 128-2048 tokens, 32 query and 8 kv heads: 175 us, 1.08 PFLOP/s (51 %: a
 // sixth of the products are hidden by the causal mask, and eight key tiles per
 // item leave its first and last steps in sight).  Pairs of SMs on one tile
