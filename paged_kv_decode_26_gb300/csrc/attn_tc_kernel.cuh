@@ -712,15 +712,12 @@ template <int D, typename T, bool PAGED>
 __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnParams& p,
                                              const CUtensorMap& tm_o, int warp, int lane) {
     PKV_ATTN_SIZES(D)
-    using Range = WeightRange<T>;
     const int G = p.group;
     const int QT = kAtRows / G;
     const int t = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t t_lane = ctl.tmem + t * TILE_COLS + ((uint32_t)((warp & 3) * 32) << 16);
     const float sc = p.scale_log2;
-    const bool pos_sc = sc > 0.f;                     // the usual case
-    const float a = pos_sc ? sc : 1.f;                // exponent = y a - m
     int slot = 0, sph = 0;
     uint32_t n_s = 0, n_o = 0;
     bool ok = true;
@@ -736,15 +733,17 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
         // last key this row sees; rows of no token (never written) may see more
         const int pos = PAGED ? it.n_keys - 1 : it.pos0 + tok;
         const int warp_pos = PAGED ? pos : it.pos0 + t * QT + ((warp & 3) * 32) / G;
-        float m_used = -INFINITY;
+        RowReference<T> ref;
+        // score = a y; scores formed ahead (a = 1) where the scale is not
+        // positive or a row's scores are large (RowReference)
+        bool formed = !(sc > 0.f);
         float2 l4[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) l4[i] = make_float2(0.f, 0.f);
         if (nt > 0 && !bad) {
-            for (int j = 0; j < nt; ++j) {
+            for (int j = 0; j < nt;) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&ctl.s_full[t], n_s & 1u, p.errors));
                 if (!ok) break;
-                ++n_s;
                 tc_fence_after();
                 float y[kAtKeys];
                 uint32_t* yr = reinterpret_cast<uint32_t*>(y);
@@ -753,10 +752,11 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
                 tc_ld32(t_lane + S_COL + 64, yr + 64);
                 tc_ld32(t_lane + S_COL + 96, yr + 96);
                 tc_wait_ld();
-                if (!pos_sc) {
+                if (formed) {
 #pragma unroll
                     for (int c = 0; c < kAtKeys; ++c) y[c] *= sc;
                 }
+                const float a = formed ? 1.f : sc;
                 if (j * kAtKeys + kAtKeys - 1 > warp_pos) {
                     // keys that rows of this warp may not see
                     const int lim = pos - j * kAtKeys;
@@ -772,46 +772,45 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
                     for (int e = 0; e < 8; ++e) m8[e] = max3(m8[e], y[c + e], y[c + 8 + e]);
                 const float mx = max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]),
                                       fmaxf(m8[6], m8[7]));
-                const float tmax = mx * a;
-                const bool first = m_used == -INFINITY;
-                const bool grow = tmax > m_used + (Range::LIFT + Range::GROW);
-                float alpha = 1.f;
-                if (grow) {
-                    const float m_new = tmax - Range::LIFT;
-                    alpha = first ? 1.f : exp2f(m_used - m_new);
-                    m_used = m_new;
-                }
-                if (__any_sync(0xffffffffu, grow && !first)) {
-                    // O is at rest: the products up to key tile j - 1
-                    // completed before S_j did
-                    const float2 a2 = make_float2(alpha, alpha);
-#pragma unroll 1
-                    for (int c0 = 0; c0 < D; c0 += 32) {
-                        uint32_t ov[32];
-                        tc_ld32(t_lane + c0, ov);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int c = 0; c < 32; c += 2) {
-                            const float2 v = __fmul2_rn(
-                                make_float2(__uint_as_float(ov[c]), __uint_as_float(ov[c + 1])),
-                                a2);
-                            ov[c] = __float_as_uint(v.x);
-                            ov[c + 1] = __float_as_uint(v.y);
-                        }
-                        tc_st32(t_lane + c0, ov);
+                const float x_max = __fmul_rn(mx, a);
+                if (__any_sync(0xffffffffu, ref.exceeded(x_max))) {
+                    if (!formed && __any_sync(0xffffffffu, ref.exceeded(x_max) &&
+                                                               ref.beyond(x_max))) {
+                        formed = true;
+                        continue;                  // this tile once more (S is still there)
                     }
+                    const float alpha = ref.take(x_max);
+                    if (__any_sync(0xffffffffu, alpha < 1.f)) {
+                        // O is at rest: the products up to key tile j - 1
+                        // completed before S_j did
+                        const float2 a2 = make_float2(alpha, alpha);
+#pragma unroll 1
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            uint32_t ov[32];
+                            tc_ld32(t_lane + c0, ov);
+                            tc_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) l4[i] = __fmul2_rn(l4[i], a2);
+                            for (int c = 0; c < 32; c += 2) {
+                                const float2 v = __fmul2_rn(
+                                    make_float2(__uint_as_float(ov[c]), __uint_as_float(ov[c + 1])),
+                                    a2);
+                                ov[c] = __float_as_uint(v.x);
+                                ov[c + 1] = __float_as_uint(v.y);
+                            }
+                            tc_st32(t_lane + c0, ov);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) l4[i] = __fmul2_rn(l4[i], a2);
+                    }
                 }
-                const float mu = m_used == -INFINITY ? 0.f : m_used;
-                const float2 aa = make_float2(a, a), nmu = make_float2(-mu, -mu);
+                const float2 mul = make_float2(a, a), add = make_float2(ref.add, ref.add);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     uint32_t w[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         const int c = half * 64 + 2 * i;
-                        const float2 e = __ffma2_rn(make_float2(y[c], y[c + 1]), aa, nmu);
+                        const float2 e = __ffma2_rn(make_float2(y[c], y[c + 1]), mul, add);
                         const float2 pv = make_float2(exp2f(e.x), exp2f(e.y));
                         l4[i & 3] = __fadd2_rn(l4[i & 3], pv);
                         w[i] = pack2<T>(pv.x, pv.y);
@@ -822,6 +821,8 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ctl.p_full[2 * t + half]);
                 }
+                ++n_s;
+                ++j;
             }
             if (!ok) break;
             ok = __all_sync(0xffffffffu, mbar_wait(&ctl.o_full[t], n_o & 1u, p.errors));
@@ -838,7 +839,8 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
             const size_t unit = PAGED ? row * p.max_splits + (bad ? -1 - it.split : it.split)
                                       : row;
             if (PAGED && real)
-                *reinterpret_cast<float2*>(p.pre_ml + unit * 2) = make_float2(m_used, l);
+                *reinterpret_cast<float2*>(p.pre_ml + unit * 2) =
+                    make_float2(ref.m, l * ref.unit(ref.m));
             // ---- O / l, 128 bytes of every row at a time (partial states are fp32)
             constexpr int COLS = PAGED ? 32 : 64;
             const int warp_row = (warp & 3) * 32;

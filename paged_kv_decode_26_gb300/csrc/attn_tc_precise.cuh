@@ -162,13 +162,10 @@ __device__ __forceinline__ void attn_softmax_precise(const AttnControl& ctl, con
                                                      int warp, int lane) {
     PKV_ATTN_SIZES(D)
     constexpr int PARTS = attn_parts<T>();
-    using Range = WeightRange<T>;
     const int G = p.group;
     const int r = warp * 32 + lane;
     const uint32_t t_lane = ctl.tmem + ((uint32_t)(warp * 32) << 16);
     const float sc = p.scale_log2;
-    const bool pos_sc = sc > 0.f;                     // the usual case
-    const float a = pos_sc ? sc : 1.f;                // exponent = y a - m
     int slot = 0, sph = 0;
     uint32_t g = 0;                                   // key tiles of the CTA so far
     bool ok = true;
@@ -181,7 +178,7 @@ __device__ __forceinline__ void attn_softmax_precise(const AttnControl& ctl, con
         // last key this row sees
         const int pos = PAGED ? it.n_keys - 1 : it.pos0 + r / G;
         const int warp_pos = PAGED ? pos : it.pos0 + (warp * 32) / G;
-        float m_used = -INFINITY;
+        RowReference<T> ref;
         float2 l4[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) l4[i] = make_float2(0.f, 0.f);
@@ -197,9 +194,14 @@ __device__ __forceinline__ void attn_softmax_precise(const AttnControl& ctl, con
             tc_ld32(buf + 64, yr + 64);
             tc_ld32(buf + 96, yr + 96);
             tc_wait_ld();
-            if (!pos_sc) {
+            // scores, rounded (the exponent from the product in one multiply-add
+            // fails for large ones, see RowReference; prompts take the same time)
+            const float2 sc2 = make_float2(sc, sc);
 #pragma unroll
-                for (int c = 0; c < kAtKeys; ++c) y[c] *= sc;
+            for (int c = 0; c < kAtKeys; c += 2) {
+                const float2 x = __fmul2_rn(make_float2(y[c], y[c + 1]), sc2);
+                y[c] = x.x;
+                y[c + 1] = x.y;
             }
             if (j * kAtKeys + kAtKeys - 1 > warp_pos) {
                 // keys that rows of this warp may not see
@@ -214,13 +216,11 @@ __device__ __forceinline__ void attn_softmax_precise(const AttnControl& ctl, con
             for (int c = 16; c < kAtKeys; c += 16)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) m8[e] = max3(m8[e], y[c + e], y[c + 8 + e]);
-            const float tmax = a * max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]),
-                                        fmaxf(m8[6], m8[7]));
+            const float mx = max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]),
+                                  fmaxf(m8[6], m8[7]));
             float alpha = 1.f;
-            if (tmax > m_used + (Range::LIFT + Range::GROW)) {
-                const float m_new = tmax - Range::LIFT;
-                alpha = m_used == -INFINITY ? 1.f : exp2f(m_used - m_new);
-                m_used = m_new;
+            if (ref.exceeded(mx)) {
+                alpha = ref.take(mx);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     l4[i] = __fmul2_rn(l4[i], make_float2(alpha, alpha));
@@ -228,8 +228,7 @@ __device__ __forceinline__ void attn_softmax_precise(const AttnControl& ctl, con
             attn_alphas(ctl)[(g % kAtAlphas) * kAtRows + r] = alpha;
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl.alpha_full[g % kAtAlphas]);
-            const float mu = m_used == -INFINITY ? 0.f : m_used;
-            const float2 aa = make_float2(a, a), nmu = make_float2(-mu, -mu);
+            const float2 add = make_float2(ref.add, ref.add);
             const float2 neg1 = make_float2(-1.f, -1.f);
 #pragma unroll
             for (int quarter = 0; quarter < 4; ++quarter) {
@@ -237,7 +236,7 @@ __device__ __forceinline__ void attn_softmax_precise(const AttnControl& ctl, con
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const int c = 2 * (quarter * 16 + i);
-                    const float2 e = __ffma2_rn(make_float2(y[c], y[c + 1]), aa, nmu);
+                    const float2 e = __fadd2_rn(make_float2(y[c], y[c + 1]), add);
                     float2 pv = make_float2(exp2f(e.x), exp2f(e.y));
                     l4[i & 3] = __fadd2_rn(l4[i & 3], pv);
 #pragma unroll
@@ -258,7 +257,7 @@ __device__ __forceinline__ void attn_softmax_precise(const AttnControl& ctl, con
         }
         if (!ok) break;
         const float2 la = __fadd2_rn(l4[0], l4[1]), lb = __fadd2_rn(l4[2], l4[3]);
-        attn_rows(ctl)[slot * kAtRows + r] = make_float2(m_used, (la.x + lb.x) + (la.y + lb.y));
+        attn_rows(ctl)[slot * kAtRows + r] = make_float2(ref.m, (la.x + lb.x) + (la.y + lb.y));
         __syncwarp();
         if (lane == 0) {
             mbar_arrive(&ctl.row_full[slot]);
@@ -325,7 +324,9 @@ __device__ __forceinline__ void attn_sum_precise(const AttnControl& ctl, const A
         const int split = bad ? -1 - it.split : it.split;
         const size_t row = (size_t)(it.row0 + tok) * p.n_heads + it.kvh * G + r % G;
         const size_t unit = PAGED ? row * p.max_splits + split : row;
-        if (PAGED && real) *reinterpret_cast<float2*>(p.pre_ml + unit * 2) = ml;
+        if (PAGED && real)
+            *reinterpret_cast<float2*>(p.pre_ml + unit * 2) =
+                make_float2(ml.x, ml.y * RowReference<T>::unit(ml.x));
         const bool poison = !PAGED && ctl.poison[slot] != 0;
         unsigned char* own = static_cast<unsigned char*>(PAGED ? p.pre_o : p.out) + unit * D * 4;
 #pragma unroll

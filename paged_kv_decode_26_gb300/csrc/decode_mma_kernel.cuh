@@ -244,11 +244,12 @@ __device__ __forceinline__ void mma_heads_sums(const MmaHeads<D>& st, float& l0,
 }
 
 // A partial state (normalised O, M, L) per real query head hh < G: row
-// row0 + hh * row_step of ws_o ([rows, D]) and ws_ml ([rows, 2]).
+// row0 + hh * row_step of ws_o ([rows, D]) and ws_ml ([rows, 2]).  L is the
+// sum kept times l_unit (weights kept at another scale than 2^(x - M)).
 template <int D>
 __device__ __forceinline__ void mma_heads_partial(const MmaHeads<D>& st, float* ws_o,
                                                   float* ws_ml, size_t row0, size_t row_step,
-                                                  int G, int lane) {
+                                                  int G, int lane, float l_unit = 1.f) {
     const int gid = lane >> 2, tig = lane & 3;
     float l0, l1;
     mma_heads_sums<D>(st, l0, l1);
@@ -264,7 +265,7 @@ __device__ __forceinline__ void mma_heads_partial(const MmaHeads<D>& st, float* 
             ws_o[unit * D + j * 16 + gid] = st.o[j][e] * inv;
             ws_o[unit * D + j * 16 + gid + 8] = st.o[j][2 + e] * inv;
         }
-        if (gid == 0) *reinterpret_cast<float2*>(ws_ml + unit * 2) = make_float2(st.m[e], l);
+        if (gid == 0) *reinterpret_cast<float2*>(ws_ml + unit * 2) = make_float2(st.m[e], l * l_unit);
     }
 }
 

@@ -186,21 +186,20 @@ __device__ __forceinline__ void piece_chunk(MmaHeads<D>& st, uint32_t kbase, uin
     }
     // this lane: tokens gid (x0, x1) and gid + 8 (x2, x3) of heads 2 tig, 2 tig + 1
     const bool v0 = gid < valid, v1 = gid + 8 < valid;
-    const float x0 = v0 ? (s0[0] + s1[0]) * scale_log2 : -INFINITY;
-    const float x1 = v0 ? (s0[1] + s1[1]) * scale_log2 : -INFINITY;
-    const float x2 = v1 ? (s0[2] + s1[2]) * scale_log2 : -INFINITY;
-    const float x3 = v1 ? (s0[3] + s1[3]) * scale_log2 : -INFINITY;
+    const float x0 = v0 ? __fmul_rn(s0[0] + s1[0], scale_log2) : -INFINITY;
+    const float x1 = v0 ? __fmul_rn(s0[1] + s1[1], scale_log2) : -INFINITY;
+    const float x2 = v1 ? __fmul_rn(s0[2] + s1[2], scale_log2) : -INFINITY;
+    const float x3 = v1 ? __fmul_rn(s0[3] + s1[3], scale_log2) : -INFINITY;
     scores(x0, x1, x2, x3);
     using Range = WeightRange<T>;
-    constexpr float MOST = Range::LIFT + Range::GROW;
     float c0 = fmaxf(x0, x2), c1 = fmaxf(x1, x3);
-    if (__any_sync(0xffffffffu, c0 > st.m[0] + MOST || c1 > st.m[1] + MOST)) {
+    if (__any_sync(0xffffffffu, c0 - st.m[0] > Range::GROW || c1 - st.m[1] > Range::GROW)) {
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
             c0 = fmaxf(c0, __shfl_xor_sync(0xffffffffu, c0, off));
             c1 = fmaxf(c1, __shfl_xor_sync(0xffffffffu, c1, off));
         }
-        const float m0 = fmaxf(st.m[0], c0 - Range::LIFT), m1 = fmaxf(st.m[1], c1 - Range::LIFT);
+        const float m0 = fmaxf(st.m[0], c0), m1 = fmaxf(st.m[1], c1);
         const float al0 = m0 == -INFINITY ? 1.f : exp2f(st.m[0] - m0);
         const float al1 = m1 == -INFINITY ? 1.f : exp2f(st.m[1] - m1);
         st.m[0] = m0;
@@ -217,8 +216,12 @@ __device__ __forceinline__ void piece_chunk(MmaHeads<D>& st, uint32_t kbase, uin
     }
     const float mu0 = st.m[0] == -INFINITY ? 0.f : st.m[0];
     const float mu1 = st.m[1] == -INFINITY ? 0.f : st.m[1];
-    const float p0 = exp2f(x0 - mu0), p1 = exp2f(x1 - mu1);
-    const float p2 = exp2f(x2 - mu0), p3 = exp2f(x3 - mu1);
+    // (the difference first: see weight_range.cuh)
+    auto weight = [](float x, float mu) {
+        return exp2f(Range::LIFT == 0.f ? x - mu : (x - mu) + Range::LIFT);
+    };
+    const float p0 = weight(x0, mu0), p1 = weight(x1, mu1);
+    const float p2 = weight(x2, mu0), p3 = weight(x3, mu1);
     st.l[0] += p0 + p2;
     st.l[1] += p1 + p3;
     // P in two 16-bit parts (hi = round(p), lo = round(p - hi)), packed by
@@ -277,7 +280,7 @@ __device__ __forceinline__ void piece_chunk(MmaHeads<D>& st, uint32_t kbase, uin
 }
 
 // Normalised rows of a finished (sequence, kv head) to the output.
-template <int D>
+template <int D, typename T>
 __device__ __forceinline__ void piece_output(const MmaHeads<D>& st, const PieceParams& p, int s,
                                              int qh0, int lane) {
     const int gid = lane >> 2, tig = lane & 3;
@@ -303,7 +306,8 @@ __device__ __forceinline__ void piece_output(const MmaHeads<D>& st, const PieceP
                 reinterpret_cast<uint16_t*>(p.out)[d1] = (uint16_t)(w >> 16);
             }
         }
-        if (gid == 0) *reinterpret_cast<float2*>(p.ws_ml + unit * 2) = make_float2(st.m[e], l);
+        if (gid == 0) *reinterpret_cast<float2*>(p.ws_ml + unit * 2) =
+                make_float2(st.m[e], l * WeightRange<T>::UNLIFT);
     }
 }
 
@@ -720,12 +724,13 @@ __device__ __forceinline__ void piece_worker(const PieceParams& p, const CUtenso
         if (pair_end || at.left == 1) {
             const size_t pair = (size_t)at.s * p.n_kv_heads + kvh;
             if (WEIGHTS && from_start && pair_end) {
-                piece_output<D>(state, p, at.s, qh0, lane);
+                piece_output<D, T>(state, p, at.s, qh0, lane);
             } else {
                 const size_t row = from_start ? (size_t)at.s * p.n_heads + qh0
                                               : (size_t)p.num_seqs * p.n_heads +
                                                     ((size_t)at.v * HW + hw) * p.group;
-                mma_heads_partial<D>(state, p.ws_o, p.ws_ml, row, 1, p.group, lane);
+                mma_heads_partial<D>(state, p.ws_o, p.ws_ml, row, 1, p.group, lane,
+                                     WeightRange<T>::UNLIFT);
             }
             if (lane == 0) {
                 if (from_start) p.seg_first[pair] = at.v;
