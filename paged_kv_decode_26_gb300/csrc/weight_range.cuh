@@ -9,7 +9,10 @@
 // m itself is a score, never shifted: where fp32 no longer resolves LIFT or
 // GROW beside it (from 2^24 on), x - m is still exact, and 0 for the key that
 // set m.
-//   bf16  has fp32's exponents: no lift.
+//   bf16  has fp32's exponents, and values up to the end of fp32's range, which
+//         their weighted sum O leaves before it is divided by l.  Lowered by
+//         2^16 O stays within it up to l = 2^16 of the largest weight; weights
+//         then vanish below 2^-110, and results below 2^-110.
 //   fp16  is spaced by 2^-24 at best.  Without a lift weights below 2^-14 lose
 //         bits one by one and those below 2^-25 vanish -- thousands of keys of
 //         small weight beside one of large weight would not add up (1500 keys
@@ -26,8 +29,8 @@ template <typename T>
 struct WeightRange;
 template <>
 struct WeightRange<__nv_bfloat16> {
-    static constexpr float LIFT = 0.f, GROW = 8.f;
-    static constexpr float UNLIFT = 1.f;                  // 2^-LIFT
+    static constexpr float LIFT = -16.f, GROW = 8.f;
+    static constexpr float UNLIFT = 65536.f;              // 2^-LIFT
 };
 template <>
 struct WeightRange<__half> {
@@ -41,23 +44,24 @@ struct WeightRange<__half> {
 // less than those of the products beside them).  The unrounded a y of the key
 // that set m may exceed m by half m's last bit, a factor of 2^8 in a weight at
 // 2^27: an item with a reference beyond() goes on with y replaced by x, rounded,
-// and a by 1.  Beyond 2^20, where fp32's steps pass 1/8, there is no lift, so that
-// add = -m is exact.
+// and a by 1.  Beyond 2^23, where fp32 holds no fractions and soon not LIFT - m,
+// there is no lift and nothing to grow by (weights stay at 1 or below).
 template <typename T>
 struct RowReference {
     using Range = WeightRange<T>;
     float m = -INFINITY;
     float add = 0.f;
+    float grow = Range::GROW;
 
     // (-inf - -inf is NaN: no key seen yet, or nothing to see)
-    __device__ __forceinline__ bool exceeded(float x) const { return x - m > Range::GROW; }
+    __device__ __forceinline__ bool exceeded(float x) const { return x - m > grow; }
     __device__ __forceinline__ static bool beyond(float x) { return fabsf(x) > 32768.f; }
     __device__ __forceinline__ static float lift(float m) {
-        return fabsf(m) <= 1048576.f ? Range::LIFT : 0.f;
+        return fabsf(m) <= 8388608.f ? Range::LIFT : 0.f;
     }
     // What the sum is to be multiplied by beside m.
     __device__ __forceinline__ static float unit(float m) {
-        return fabsf(m) <= 1048576.f ? Range::UNLIFT : 1.f;
+        return fabsf(m) <= 8388608.f ? Range::UNLIFT : 1.f;
     }
     // Takes in the largest score of a tile; the factor for what the row has
     // summed up so far.
@@ -66,6 +70,7 @@ struct RowReference {
         const float alpha = m == -INFINITY ? 1.f : exp2f((m - x) + (lift(x) - lift(m)));
         m = x;
         add = lift(x) - x;
+        grow = fabsf(x) <= 8388608.f ? Range::GROW : 0.f;
         return alpha;
     }
 };
