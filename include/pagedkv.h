@@ -492,7 +492,9 @@ PKV_API pkv_status paged_attn_decode_weights(
  *   kept          device int32 [num_seqs, keep], written: the staying tokens'
  *                 indexes (0 .. n - 1 of a sequence of n <= keep tokens), then -1
  * A sequence of at most `keep` tokens keeps its pages and nothing of it is
- * copied.  A context below 0 or beyond the table or weight_cols is flagged
+ * copied.  The longest context that the tables and weight_cols allow, and
+ * new_weight_cols, are at most 2^31 - 2^14.
+ * A context below 0 or beyond the table or weight_cols is flagged
  * PKV_DEVERR_CONTEXT and treated as empty; a row whose source or destination
  * block lies outside the pool is not copied and flagged PKV_DEVERR_BLOCK_ID.
  * new_lens, new_weights and kept may not overlap the inputs.  Two launches.

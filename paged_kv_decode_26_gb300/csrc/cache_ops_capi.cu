@@ -278,6 +278,10 @@ PKV_API pkv_status kv_evict(void* k_pool, void* v_pool, pkv_dtype dtype,
     if (weight_stride < weight_cols || new_weight_stride < new_weight_cols ||
         new_weight_cols < keep)
         return invalid("weight rows: strides below the columns, or new_weights below keep columns");
+    const long long table = (long long)max_blocks_per_seq * block_size;
+    const long long cap_tokens = table < weight_cols ? table : weight_cols;
+    if (cap_tokens > pkv::kEvictMost || new_weight_cols > pkv::kEvictMost)   // (keep is below)
+        return unsupported("contexts or new_weight_cols above 2^31 - 2^14");
     int es = 0;
     switch (dtype) {
         case PKV_F16:
@@ -332,8 +336,7 @@ PKV_API pkv_status kv_evict(void* k_pool, void* v_pool, pkv_dtype dtype,
     p.context_lens = context_lens;
     p.weights = weights;
     p.weight_stride = weight_stride;
-    const long long table = (long long)max_blocks_per_seq * block_size;
-    p.cap_tokens = (int)(table < weight_cols ? table : weight_cols);
+    p.cap_tokens = (int)cap_tokens;
     p.new_tables = new_tables;
     p.new_blocks_per_seq = new_blocks_per_seq;
     p.new_lens = new_lens;

@@ -29,6 +29,9 @@ constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictBins = 2048;
 constexpr int kEvictStaged = 48 * 1024;   // keys of a CTA's tokens kept in shared memory
 constexpr int kEvictCluster = 8;          // CTAs per sequence at most
+// Tokens and columns at most: the passes step by 8192 and round up to 1024 per
+// CTA beyond the last one, in 32 bits.
+constexpr int kEvictMost = 0x7fffffff - (1 << 14) + 1;
 
 struct EvictParams {
     const int* block_tables;
