@@ -721,9 +721,10 @@ PKV_API pkv_status pkv_append_slots_cow(pkv_block_manager* mgr, int32_t* block_t
  *   context_lens host int32 [num_seqs], updated in place
  *   new_tables   host int32 [num_seqs, new_blocks_per_seq], written
  *   old_ids      host int32 [cap], written (*n_old ids used)
+ * new_tables and old_ids may overlap neither the inputs nor each other.
  * PKV_ERR_NO_BLOCKS when the pool has too few free blocks for all of them,
  * PKV_ERR_INVALID for a bad length or table entry, a row that does not fit
- * new_tables, or cap too small; nothing is changed then (*n_old = 0).
+ * new_tables, cap too small or an overlap; nothing is changed then (*n_old = 0).
  */
 PKV_API pkv_status pkv_evict_tables(pkv_block_manager* mgr, const int32_t* block_tables,
                                     int max_blocks_per_seq, int32_t* context_lens, int num_seqs,

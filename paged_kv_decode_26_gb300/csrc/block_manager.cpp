@@ -249,6 +249,11 @@ PKV_API pkv_status pkv_append_slots_cow(pkv_block_manager* mgr, int32_t* block_t
     return result;
 }
 
+static bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return an && bn && x < y + bn && y < x + an;
+}
+
 PKV_API pkv_status pkv_evict_tables(pkv_block_manager* mgr, const int32_t* block_tables,
                                     int max_blocks_per_seq, int32_t* context_lens, int num_seqs,
                                     int keep, int32_t* new_tables, int new_blocks_per_seq,
@@ -260,6 +265,15 @@ PKV_API pkv_status pkv_evict_tables(pkv_block_manager* mgr, const int32_t* block
         return PKV_ERR_INVALID;
     if (num_seqs > 0 && (!block_tables || !context_lens || !new_tables)) return PKV_ERR_INVALID;
     if (cap > 0 && !old_ids) return PKV_ERR_INVALID;
+    const size_t seqs = (size_t)num_seqs, in_bytes = seqs * max_blocks_per_seq * sizeof(int32_t),
+                 out_bytes = seqs * new_blocks_per_seq * sizeof(int32_t);
+    // rows are read after others have been written
+    if (overlap(new_tables, out_bytes, block_tables, in_bytes) ||
+        overlap(new_tables, out_bytes, context_lens, seqs * sizeof(int32_t)) ||
+        overlap(old_ids, cap * sizeof(int32_t), block_tables, in_bytes) ||
+        overlap(old_ids, cap * sizeof(int32_t), context_lens, seqs * sizeof(int32_t)) ||
+        overlap(old_ids, cap * sizeof(int32_t), new_tables, out_bytes))
+        return PKV_ERR_INVALID;
     const long long B = mgr->block_size;
     const long long new_pages = (keep + B - 1) / B;
     // check everything first: a failing call changes nothing
