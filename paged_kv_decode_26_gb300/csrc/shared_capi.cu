@@ -59,15 +59,22 @@ SharedShape shared_shape(int num_seqs, int num_groups, int max_group, int max_pr
         // Work items (split x kv head x pair of row tiles x group) are dealt
         // out to the SMs in turn: the split length with the smallest sum of
         // key tiles over the busiest SM's items, the longer one of equals.
-        const int key_tiles = (max_prefix + pkv::kAtKeys - 1) / pkv::kAtKeys;
+        // Of the lengths that give s splits the shortest, ceil(tiles / s), is
+        // the best; a cost of s splits is at least units (tiles + kSplitCost s)
+        // / SMs, so more splits are tried only while that is below the best
+        // (a few hundred at most, whatever the bound of the prefixes).
+        const long long tiles = ((long long)max_prefix + pkv::kAtKeys - 1) / pkv::kAtKeys;
         long long best = 0;
-        for (int n = key_tiles; n >= 1; --n) {
-            const long long items = units * ((key_tiles + n - 1) / n);
-            const long long cost = (items + sm_count - 1) / sm_count * (n + kSplitCost);
+        for (long long s = 1; s <= tiles && (best == 0 || units * (tiles + kSplitCost * s) <
+                                                              best * sm_count);) {
+            const long long n = (tiles + s - 1) / s;
+            const long long cost = (units * s + sm_count - 1) / sm_count * (n + kSplitCost);
             if (best == 0 || cost < best) {
                 best = cost;
-                c.split_tokens = n * pkv::kAtKeys;
+                c.split_tokens = (int)(n * pkv::kAtKeys);
             }
+            // the next number of splits that some length gives
+            s = n > 1 ? (tiles + n - 2) / (n - 1) : tiles + 1;
         }
         c.max_splits = (int)(((long long)max_prefix + c.split_tokens - 1) / c.split_tokens);
     }
