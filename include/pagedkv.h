@@ -534,9 +534,11 @@ PKV_API pkv_status kv_evict(void* k_pool, void* v_pool, pkv_dtype dtype,
  * prefix that is negative, beyond max_prefix or no multiple of block_size is
  * flagged PKV_DEVERR_CONTEXT and its members are decoded alone.  A split of a
  * prefix (or 16 tokens of a context) with a block outside the pool is left out and
- * flagged PKV_DEVERR_BLOCK_ID.  Softmax weights of the prefix enter the second product
- * rounded to kv_dtype, except for F32 outputs (as the sum of two F16 or three
- * BF16 parts).  Supported shapes as paged_attn_decode; at most 65535 sequences,
+ * flagged PKV_DEVERR_BLOCK_ID.  Softmax weights enter the second product as the
+ * sum of two 16-bit parts, as in paged_attn_decode (three of BF16 for F32 outputs).
+ * 16-bit outputs: sums over very long contexts come out short by up to 2^-23 per 16
+ * keys of a split of the prefix or of a run of the rest.
+ * Supported shapes as paged_attn_decode; at most 65535 sequences,
  * 65535 groups, 4096 query heads.  Two launches, or
  * three where the prefixes are long enough for it to pay.
  */
@@ -576,6 +578,9 @@ PKV_API pkv_status paged_attn_decode_shared(
  * max_len is left out (its rows are not written) and flagged
  * PKV_DEVERR_CONTEXT.  The softmax weights enter the second product rounded to
  * dtype, except for F32 outputs (as the sum of two F16 or three BF16 parts).
+ * 16-bit outputs of very long prompts come out short by up to 2^-23 per 16 keys:
+ * below the outputs' own rounding up to 32768 keys (F16) and 262144 (BF16).  F32
+ * outputs do not.
  * NaN and infinities in rows of k and v reach only the tokens that see those
  * rows (an infinity in v as an infinity or NaN).  One launch (several where
  * num_seqs and max_len allow more than 2^31 tiles), no workspace.

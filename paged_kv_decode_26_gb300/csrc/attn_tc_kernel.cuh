@@ -36,14 +36,16 @@
 // item leave its first and last steps in sight).  Pairs of SMs on one tile
 // (M = 256) took 1062 us for the first, two threads per softmax row 937.
 //
-// Precision: S, m, l and O are fp32.  P is rounded once to the 16-bit type of
-// V before the second product (at most half an eps relative to each weight,
-// below the rounding of a 16-bit output; weight_range.cuh keeps fp16 weights
-// clear of its smallest numbers): the rate of that product rests on it.  The
-// sum l adds the unrounded weights.  O accumulates in the tensor core, which
-// drops what lies below its accumulator's last bit: 2^-24 of O per 16 keys at
-// most, 1e-4 at 32768 keys, below half a step of fp16.  fp32 outputs are formed
-// otherwise (attn_tc_precise.cuh).
+// Precision: S, m, l and O are fp32.  A weight of a prompt is rounded once to the
+// 16-bit type of V before the second product (half an eps relative to each
+// weight: as much as the rounding of a 16-bit output, and more of it where values
+// cancel): the rate of that product rests on it.  A prefix's weights go in two
+// parts (attn_weight_parts).  weight_range.cuh keeps fp16 weights clear of its
+// smallest numbers; the sum l adds the unrounded weights.  O accumulates in the
+// tensor core, which drops what lies below its accumulator's last bit, always
+// downwards: up to 2^-23 of O per 16 keys (measured 2e-4 at 32768 keys), so no
+// more than the smallest half step of fp16, 2^-12, up to 32768 keys, and of bf16,
+// 2^-9, up to 262144.  fp32 outputs are formed otherwise (attn_tc_precise.cuh).
 #pragma once
 
 #include "multi_query_tc_kernel.cuh"
@@ -135,6 +137,16 @@ struct AttnSizes {
     [[maybe_unused]] constexpr uint32_t Q_BYTES = AttnSizes<D>::Q_BYTES;                      \
     [[maybe_unused]] constexpr uint32_t TILE_COLS = AttnSizes<D>::TILE_COLS;                  \
     [[maybe_unused]] constexpr uint32_t S_COL = AttnSizes<D>::S_COL;
+
+// 16-bit parts whose sum a softmax weight enters the second product as, for
+// 16-bit outputs.  Prefixes: two, the bits of every other decode of these caches
+// (a result does not depend on whether a prefix is attended once); one document
+// of 16384 tokens under 256 sequences 177 us, 165 with one part, sixteen groups
+// 195 and 194; error against 64 bits 1.66e-3 of the outputs' size, that of their
+// rounding, and 2.3e-3 with one part.  Prompts: one; two would take packed GQA
+// prompts from 183 to 265 us and two of 4096-8192 from 637 to 931, for 1.6e-3
+// instead of 2.0e-3.
+__host__ __device__ constexpr int attn_weight_parts(bool paged) { return paged ? 2 : 1; }
 
 // Row tiles per work item: fp32 outputs are made one at a time
 // (attn_tc_precise.cuh).
@@ -520,6 +532,7 @@ __device__ __forceinline__ void attn_guard(const AttnControl& ctl, const AttnPar
 template <int D, typename T, bool PAGED>
 __device__ __forceinline__ void attn_mma(const AttnControl& ctl, const AttnParams& p, int lane) {
     PKV_ATTN_SIZES(D)
+    constexpr int PARTS = attn_weight_parts(PAGED);
     const uint32_t id_s = tc_idesc<T>(kAtRows, kAtKeys, 0);
     const uint32_t id_o = tc_idesc<T>(kAtRows, D, 1);
     const uint64_t dq0 = tc_desc_sw128(smem_addr(ctl.sQ), 16, 1024);
@@ -625,10 +638,13 @@ __device__ __forceinline__ void attn_mma(const AttnControl& ctl, const AttnParam
                             const uint32_t o = ctl.tmem + t * TILE_COLS;
                             const uint64_t v = dv0 + (uint64_t)(vs * (KV_BYTES >> 4));
 #pragma unroll
-                            for (int i = half * 4; i < half * 4 + 4; ++i)
-                                at_mma_tmem_a(o, o + S_COL + i * 8,
-                                              v + (uint64_t)((i * 16 * 128) >> 4), id_o,
-                                              (j > 0 || i > 0) ? 1u : 0u, lead);
+                            for (int part = PARTS - 1; part >= 0; --part)
+#pragma unroll
+                                for (int i = half * 4; i < half * 4 + 4; ++i)
+                                    at_mma_tmem_a(o, o + S_COL + part * 64 + i * 8,
+                                                  v + (uint64_t)((i * 16 * 128) >> 4), id_o,
+                                                  (j > 0 || i > 0 || part < PARTS - 1) ? 1u : 0u,
+                                                  lead);
                             if (half && j + 1 == nt) at_commit(&ctl.o_full[t], lead);
                         }
                         __syncwarp();
@@ -712,6 +728,7 @@ template <int D, typename T, bool PAGED>
 __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnParams& p,
                                              const CUtensorMap& tm_o, int warp, int lane) {
     PKV_ATTN_SIZES(D)
+    constexpr int PARTS = attn_weight_parts(PAGED);
     const int G = p.group;
     const int QT = kAtRows / G;
     const int t = warp >> 2;
@@ -806,16 +823,23 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
                 const float2 mul = make_float2(a, a), add = make_float2(ref.add, ref.add);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    uint32_t w[32];
+                    uint32_t w[PARTS][32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         const int c = half * 64 + 2 * i;
                         const float2 e = __ffma2_rn(make_float2(y[c], y[c + 1]), mul, add);
                         const float2 pv = make_float2(exp2f(e.x), exp2f(e.y));
                         l4[i & 3] = __fadd2_rn(l4[i & 3], pv);
-                        w[i] = pack2<T>(pv.x, pv.y);
+                        w[0][i] = pack2<T>(pv.x, pv.y);
+                        if (PARTS > 1) {
+                            const float2 rest =
+                                __ffma2_rn(unpack2<T>(w[0][i]), make_float2(-1.f, -1.f), pv);
+                            w[PARTS - 1][i] = pack2<T>(rest.x, rest.y);
+                        }
                     }
-                    tc_st32(t_lane + S_COL + half * 32, w);
+#pragma unroll
+                    for (int k = 0; k < PARTS; ++k)
+                        tc_st32(t_lane + S_COL + k * 64 + half * 32, w[k]);
                     tc_wait_st();
                     tc_fence_before();
                     __syncwarp();
