@@ -525,7 +525,10 @@ PKV_API pkv_status kv_evict(void* k_pool, void* v_pool, pkv_dtype dtype,
  *                 table is read for them).  A member whose context is shorter than the prefix
  *                 is decoded alone.
  *   max_group, max_prefix  host-side bounds of a group's size (at most num_seqs)
- *                 and of prefix_lens (at most max_context_len)
+ *                 and of prefix_lens (at most max_context_len); prefixes are cut
+ *                 as if all were that long: one far longer than the others costs
+ *                 several times its own work (16384 tokens beside fifteen of 512,
+ *                 eight members each: 268 us; sixteen of the mean: 55)
  *   workspace     device, >= pkv_decode_shared_workspace_bytes(...) bytes,
  *                 256-byte aligned; contents on entry are ignored.  Calls that
  *                 may overlap on the GPU need a workspace each.
@@ -572,7 +575,11 @@ PKV_API pkv_status paged_attn_decode_shared(
  *                per token, so the three may be views of one fused tensor;
  *                strides multiples of 8 elements; out may not overlap them
  *   q_start      device int32 [num_seqs + 1], non-decreasing, within total_q
- *   max_len      host-side bound of a sequence's length
+ *   max_len      host-side bound of a sequence's length.  Work is laid out for
+ *                num_seqs sequences of max_len tokens: a batch in which one is
+ *                far longer than most costs several times its own work (8192
+ *                tokens beside 37 of 64: 5.6 ms, alone 0.17), so attend such a
+ *                one by a call of its own
  * out, q, k and v 16-byte aligned.  head_dim 64 or 128, G 1, 2, 4 or 8.
  * A sequence whose bounds lie outside the tokens or whose length exceeds
  * max_len is left out (its rows are not written) and flagged

@@ -160,10 +160,14 @@ PKV_API pkv_status pkv_attn_prompt(void* out, pkv_dtype out_dtype, const void* q
         p.n_items = per_seq * p.num_seqs;
         // Where there are more items than SMs, a CTA per item, and running CTAs
         // take over the waiting ones' items, so that the SMs finish together
-        // (GB300: packed prompts of 128-2048 tokens, grouped heads, 221 us dealt
-        // out in turn, 191 us taken over; prompts of 6.8K and 8K tokens 744 and
-        // 707 us).  Where lengths differ so much that most items of the longest
-        // sequence's count are empty, the CTAs skip those 32 at a time instead.
+        // (GB300, taken over and dealt out in turn: prompts of 6.8K and 8K tokens
+        // 576 and 721 us, one of 8192 with 4 kv heads 169 and 204; of 128-2048
+        // tokens, 8 kv heads, 179 and 171, 64 of 512 204 and 206, 300 of 100 180
+        // and 157).  Where most items of the longest sequence's count are empty --
+        // lengths that differ much, or a loose max_len -- the CTAs pass over those
+        // 32 at a time instead (the 128-2048 under a max_len of 32768: 171, taken
+        // over 301), and a long sequence's items may meet few of the CTAs (8192
+        // tokens beside 37 of 64: 5.6 ms, taken over 0.23-0.4).
         const long long real =
             (long long)n_kv_heads * ((long long)total_q / item_tokens + p.num_seqs);
         p.dynamic = p.n_items > dev->sm_count && p.n_items <= 2 * real;

@@ -28,13 +28,14 @@
 // overlap the last softmax and the output of the current one.
 //
 // What bounds it: the tensor core and the softmax in turn.  GB300: two prompts of
-// 4096-8192 tokens, 32 heads of 128: 580 us, 1.60 PFLOP/s (0.84 of the burst rate
-// measured for a library product; the tensor pipe is active 72 % of the time;
-// 610-655 us when calls follow one another for long, limited by power); sixteen
-// of 128-2048 tokens, 32 query and 8 kv heads: 175 us, 1.08 PFLOP/s (51 %: a
-// sixth of the products are hidden by the causal mask, and eight key tiles per
-// item leave its first and last steps in sight).  Pairs of SMs on one tile
-// (M = 256) took 1062 us for the first, two threads per softmax row 937.
+// 4096-8192 tokens, 32 heads of 128: 580 us for a call on a cool GPU, 1.60 PFLOP/s
+// (0.84 of the burst rate measured for a library product; the tensor pipe is
+// active 72 % of the time); 640-650 us when calls follow one another, limited by
+// power, 1.44 PFLOP/s (0.76 of that rate, 0.85 of the library's sustained one);
+// sixteen of 128-2048 tokens, 32 query and 8 kv heads: 178-185 us, 1.05 PFLOP/s
+// (50 %: a sixth of the products are hidden by the causal mask, and eight key
+// tiles per item leave its first and last steps in sight).  Pairs of SMs on one
+// tile (M = 256) took 1062 us for the first, two threads per softmax row 937.
 //
 // Precision: S, m, l and O are fp32.  A weight of a prompt is rounded once to the
 // 16-bit type of V before the second product (half an eps relative to each
@@ -76,7 +77,7 @@ struct AttnParams {
     int tiles;                 // items of row tiles of the longest sequence / largest group
     int band;                  // prompts: neighbouring items of a sequence and kv head
     long long n_items;
-    int dynamic;               // prompts: one CTA per item, running CTAs take over waiting ones
+    int dynamic;               // one CTA per item, running CTAs take over waiting ones
     // whole prompts
     const int* q_start;        // [num_seqs + 1]
     int total_q;
@@ -86,7 +87,6 @@ struct AttnParams {
     // shared prefixes
     const int* group_start;    // [num_groups + 1]
     const int* prefix_lens;    // [num_groups]
-    int num_groups;
     int max_group;
     int max_prefix;
     const int* block_tables;
@@ -112,7 +112,8 @@ struct AttnItem {
     int key0;        // prefix: first key of the split
     int n_keys;      // keys that exist
     int nt[2];       // key tiles per row tile
-    int split;       // prefix; -1: a page is missing, the partial states are empty
+    int split;       // prefix; negative: -1 - split of an item with a missing page, whose
+                     // partial states are empty
     int done;
 };
 

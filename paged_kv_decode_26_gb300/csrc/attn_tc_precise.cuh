@@ -17,8 +17,8 @@
 // per row, and write the output.  What bounds it: the softmax, 4000 cycles a key
 // tile of which 3000 (bf16; fp16 2260) form and store P's parts, one warp per
 // scheduler; the tensor core's 3 or 4 products of 128 x 128 x D take 1536 or
-// 2048.  GB300, sixteen prompts of 128-2048 tokens, 32/8 heads of 128: 473 us
-// (fp16 417); with O summed in tensor memory by the softmax warps, in turn with
+// 2048.  GB300, sixteen prompts of 128-2048 tokens, 32/8 heads of 128: 480 us
+// (fp16 418); with O summed in tensor memory by the softmax warps, in turn with
 // everything else, 672 (507).
 #pragma once
 

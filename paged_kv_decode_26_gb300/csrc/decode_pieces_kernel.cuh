@@ -16,7 +16,7 @@
 //
 // What bounds it: HBM.  Each K and V byte is read once; the products run on
 // mma.sync with the tokens as rows (decode_mma_kernel.cuh), far below the
-// tensor rate.  GB300, 64 contexts of 512-4096 tokens, 32 heads: 354 us of 371
+// tensor rate.  GB300, 64 contexts of 512-4096 tokens, 32 heads: 357 us of 371
 // (the rest: weights and merge), 6.9 TB/s of DRAM; 8 contexts of 8K-32K tokens,
 // 32/8 heads: 109 us of 123, 6.0 TB/s.
 //

@@ -6,10 +6,10 @@
 // A work item is a split of a prefix x a kv head x a pair of row tiles (256
 // rows: members x query heads).  The kernel is bound by the tensor cores where
 // a group has many rows, by HBM where it has few.  GB300, a document of 16384
-// tokens under 256 sequences, 32 query and 8 kv heads: 72 us by itself, on 128
-// of the SMs (a split per SM; twice as many half as long cost 9 us more), of
-// which 20 are its first and last steps; of the whole call's 166 us the own
-// tokens take 96 and the merge 8.
+// tokens under 256 sequences, 32 query and 8 kv heads: 87 us by itself (72 with
+// weights in one part, of which 20 were its first and last steps), the tensor
+// pipe active 48 % of it, on 128 of the SMs, a split per SM; of the whole call's
+// 177 us the own tokens take 96 and the merge 8.
 #pragma once
 
 #include "attn_tc_precise.cuh"

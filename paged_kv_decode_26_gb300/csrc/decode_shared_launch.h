@@ -20,7 +20,7 @@ struct SharedLaunch {
     cudaStream_t stream;
 };
 
-// Launch decode_pieces_kernel<D, T, false> and, as SMs get free of it,
+// Launch decode_pieces_kernel<D, T, false, false, precise> and, as SMs get free of it,
 // attn_prefix_kernel<D, T, precise>.
 cudaError_t launch_shared_bf16(int D, bool precise, const SharedLaunch& L);
 cudaError_t launch_shared_f16(int D, bool precise, const SharedLaunch& L);

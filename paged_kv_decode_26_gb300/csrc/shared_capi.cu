@@ -24,9 +24,9 @@ constexpr int kSplitCost = 4;
 // and the other members' reads of them, at most, come to 24 MB.  Below that every
 // member reads its whole context, which saves a launch.  GB300, GPU time of a
 // call (and with the launches from Python), each member alone against once per
-// group: 0.4 MB 10.7 (21) / 11.7 us (25); 16 MB 13.2 (20) / 13.5 (25); 31 MB 17.8
-// (21) / 12.7 (24), eight groups 18.6 / 21.0; 66 MB 21.1 / 16.4, of prefixes of 64
-// tokens 25.4 / 28.2; 251 MB 39.4 / 19.0, of 64 tokens 76.4 / 72.5.
+// group: 0.4 MB 11.3 (22) / 12.5 us (25); 16 MB 13.3 (22) / 14.9 (26); 31 MB 17.9
+// (22) / 14.2 (24), eight groups 18.7 / 20.6; 66 MB 21.3 / 17.8, of prefixes of 64
+// tokens 25.3 / 27.2; 251 MB 39.4 / 22.2, of 64 tokens 77.1 / 73.3.
 constexpr double kSharedLeast = 24e6;
 bool prefix_once(int num_seqs, int num_groups, int max_group, int max_prefix, int n_kv_heads,
                  int head_dim) {
@@ -188,7 +188,6 @@ PKV_API pkv_status paged_attn_decode_shared(
         a.tiles = (max_group + item_rows - 1) / item_rows;
         a.group_start = group_start;
         a.prefix_lens = prefix_lens;
-        a.num_groups = num_groups;
         a.max_group = max_group;
         a.max_prefix = max_prefix;
         a.block_tables = block_tables;
