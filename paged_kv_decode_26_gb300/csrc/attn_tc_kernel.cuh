@@ -792,7 +792,7 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
                                       fmaxf(m8[6], m8[7]));
                 const float x_max = __fmul_rn(mx, a);
                 if (__any_sync(0xffffffffu, ref.exceeded(x_max))) {
-                    if (!formed && __any_sync(0xffffffffu, ref.exceeded(x_max) &&
+                    if (!formed && __any_sync(0xffffffffu, real && ref.exceeded(x_max) &&
                                                                ref.beyond(x_max))) {
                         formed = true;
                         continue;                  // this tile once more (S is still there)

@@ -136,3 +136,20 @@ def test_shared_decode(dtype, out_dtype, size, D, once):
     finally:
         pkv.reset_tuning()
     assert pkv.device_errors(clear=True) == 0
+
+
+@pytest.mark.parametrize("out_dtype", [BF, F32])
+def test_prompts_do_not_change_with_their_neighbours(out_dtype):
+    """The rows behind a sequence's last ones in a tile are the next sequence's:
+    its size of scores is not this one's, bit for bit."""
+    g = torch.Generator().manual_seed(5)
+    q, k, v = (torch.randn(500, h, 128, generator=g).to(BF) for h in (4, 2, 2))
+    got = []
+    for big in (1.0, 2.0 ** 20, float("inf")):
+        q2 = q.clone()
+        q2[150:] *= big
+        out = torch.empty(500, 4, 128, dtype=out_dtype, device="cuda")
+        pkv.attn_prompt(out, q2.cuda(), k.cuda(), v.cuda(),
+                        torch.tensor([0, 150, 500], dtype=torch.int32, device="cuda"), 0.09, 350)
+        got.append(out[:150].clone())
+    assert torch.equal(got[1], got[0]) and torch.equal(got[2], got[0])
