@@ -138,18 +138,21 @@ def test_shared_decode(dtype, out_dtype, size, D, once):
     assert pkv.device_errors(clear=True) == 0
 
 
-@pytest.mark.parametrize("out_dtype", [BF, F32])
-def test_prompts_do_not_change_with_their_neighbours(out_dtype):
+@pytest.mark.parametrize("dtype,out_dtype", [(BF, FP), (FP, FP), (BF, F32)])
+def test_prompts_do_not_change_with_their_neighbours(dtype, out_dtype):
     """The rows behind a sequence's last ones in a tile are the next sequence's:
-    its size of scores is not this one's, bit for bit."""
+    its size of scores is not this one's, bit for bit (of some hundred thousand
+    elements, so that a difference of roundings would show)."""
+    n, S = 71, 80
     g = torch.Generator().manual_seed(5)
-    q, k, v = (torch.randn(500, h, 128, generator=g).to(BF) for h in (4, 2, 2))
+    q, k, v = (torch.randn(n * S, h, 128, generator=g).to(dtype) for h in (8, 2, 2))
+    odd = (torch.arange(n * S) // n % 2 == 1)[:, None, None]
+    starts = torch.arange(0, n * S + 1, n, dtype=torch.int32, device="cuda")
     got = []
-    for big in (1.0, 2.0 ** 20, float("inf")):
-        q2 = q.clone()
-        q2[150:] *= big
-        out = torch.empty(500, 4, 128, dtype=out_dtype, device="cuda")
-        pkv.attn_prompt(out, q2.cuda(), k.cuda(), v.cuda(),
-                        torch.tensor([0, 150, 500], dtype=torch.int32, device="cuda"), 0.09, 350)
-        got.append(out[:150].clone())
+    for big in (1.0, 2.0 ** 12, float("inf")):
+        q2 = torch.where(odd, q * big, q)
+        out = torch.empty(n * S, 8, 128, dtype=out_dtype, device="cuda")
+        pkv.attn_prompt(out, q2.cuda(), k.cuda(), v.cuda(), starts, 3.0, n)
+        got.append(out[~odd[:, 0, 0].cuda()].clone())
+    assert torch.isfinite(got[0]).all()
     assert torch.equal(got[1], got[0]) and torch.equal(got[2], got[0])
