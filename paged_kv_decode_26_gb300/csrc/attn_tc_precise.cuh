@@ -7,7 +7,7 @@
 //   sums      the tensor core drops the bits of a product below its
 //             accumulator's last one, always downwards: over 32768 keys O came
 //             out 2e-4 short.  So O of each key tile starts from zero, smallest
-//             parts first, and joins a sum in registers by fp32 additions (5e-7
+//             parts first, and joins a sum in registers by fp32 additions (7e-7
 //             at 32768 keys).
 //
 // Tensor memory then has room for one row tile: O of a key tile (D columns) and

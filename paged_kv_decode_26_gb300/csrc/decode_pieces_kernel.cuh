@@ -216,8 +216,8 @@ __device__ __forceinline__ void piece_chunk(MmaHeads<D>& st, uint32_t kbase, uin
     }
     const float mu0 = st.m[0] == -INFINITY ? 0.f : st.m[0];
     const float mu1 = st.m[1] == -INFINITY ? 0.f : st.m[1];
-    // (the difference first: see weight_range.cuh)
-    auto weight = [](float x, float mu) { return exp2f((x - mu) + Range::LIFT); };
+    // (the difference first: see weight_range.cuh; the factor behind, where it is exact)
+    auto weight = [](float x, float mu) { return exp2f(x - mu) * (1.f / Range::UNLIFT); };
     const float p0 = weight(x0, mu0), p1 = weight(x1, mu1);
     const float p2 = weight(x2, mu0), p3 = weight(x3, mu1);
     st.l[0] += p0 + p2;

@@ -11,8 +11,11 @@
 // set m.
 //   bf16  has fp32's exponents, and values up to the end of fp32's range, which
 //         their weighted sum O leaves before it is divided by l.  Lowered by
-//         2^16 O stays within it up to l = 2^16 of the largest weight; weights
-//         then vanish below 2^-110, and results below 2^-110.
+//         2^17 O stays within it up to l = 2^17 of the largest weight; weights
+//         then vanish below 2^-109, and results below 2^-109.  (17 and not 16:
+//         around -17 fp32's steps are as coarse as those of LIFT - m for m in
+//         -49 .. 15, so m + (LIFT - m) rounds to LIFT and a lone key's weight
+//         divides out to the last bit of an fp32 output.)
 //   fp16  is spaced by 2^-24 at best.  Without a lift weights below 2^-14 lose
 //         bits one by one and those below 2^-25 vanish -- thousands of keys of
 //         small weight beside one of large weight would not add up (1500 keys
@@ -29,8 +32,8 @@ template <typename T>
 struct WeightRange;
 template <>
 struct WeightRange<__nv_bfloat16> {
-    static constexpr float LIFT = -16.f, GROW = 8.f;
-    static constexpr float UNLIFT = 65536.f;              // 2^-LIFT
+    static constexpr float LIFT = -17.f, GROW = 8.f;
+    static constexpr float UNLIFT = 131072.f;             // 2^-LIFT
 };
 template <>
 struct WeightRange<__half> {
