@@ -578,8 +578,8 @@ PKV_API pkv_status paged_attn_decode_shared(
  *   max_len      host-side bound of a sequence's length.  Work is laid out for
  *                num_seqs sequences of max_len tokens: a batch in which one is
  *                far longer than most costs several times its own work (8192
- *                tokens beside 37 of 64: 5.6 ms, alone 0.17), so attend such a
- *                one by a call of its own
+ *                tokens beside 37 of 64, 16 query and 4 kv heads: 5.6 ms, alone
+ *                0.17), so attend such a one by a call of its own
  * out, q, k and v 16-byte aligned.  head_dim 64 or 128, G 1, 2, 4 or 8.
  * A sequence whose bounds lie outside the tokens or whose length exceeds
  * max_len is left out (its rows are not written) and flagged
