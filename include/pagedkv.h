@@ -74,6 +74,7 @@ typedef enum pkv_dtype { PKV_F16 = 0, PKV_BF16 = 1, PKV_F32 = 2 } pkv_dtype;
 #define PKV_DEVERR_PAIR 0x8u        /* copy: pair index beyond its pool */
 #define PKV_DEVERR_TIMEOUT 0x10u    /* a pipeline wait gave up (should never happen) */
 #define PKV_DEVERR_CONFIG 0x20u     /* inconsistent launch configuration (should never happen) */
+#define PKV_DEVERR_POSITION 0x40u /* append: position outside the rotation table */
 
 /* Human-readable name of a status code (static string). */
 PKV_API const char* pkv_status_string(pkv_status status);
@@ -617,6 +618,108 @@ PKV_API pkv_status kv_append(void* k_pool, void* v_pool, const void* k_new, cons
                              pkv_dtype dtype, const int64_t* slot_mapping, int num_seqs,
                              int n_kv_heads, int head_dim, int block_size, int num_blocks,
                              void* stream);
+
+/*
+ * pkv_rope_table -- cosines and sines for the appends that rotate:
+ *
+ *     table[t, i]                  = factor * cos(t * inv_freq[i])
+ *     table[t, rotary_dim / 2 + i] = factor * sin(t * inv_freq[i])
+ *
+ * for t < num_positions, i < rotary_dim / 2, formed in 64 bits and rounded
+ * once.  Scalings for long contexts are choices of inv_freq and factor.
+ *   table      device float [num_positions, rotary_dim], 16-byte aligned
+ *   inv_freq   host double [rotary_dim / 2], finite, read before the call returns
+ *   rotary_dim a multiple of 16, at most 128
+ */
+PKV_API pkv_status pkv_rope_table(float* table, int num_positions, int rotary_dim,
+                                  const double* inv_freq, float factor, void* stream);
+
+/*
+ * kv_append_rope -- kv_append straight from the projections' output, keys and
+ * queries rotated by their positions on the way ([SWAP] serving loop: the step
+ * between the projections and the attention).  For token i, with slot =
+ * slot_mapping[i] and the table's row t = positions[i]:
+ *
+ *     k_pool[slot / block_size, slot % block_size] = rotated k[i]
+ *     v_pool[...same...]                           = v[i], bit for bit
+ *     q_out[i] = rotated q[i],  k_out[i] = rotated k[i]   (where given)
+ *
+ * A pair (a, b) of a head's first rotary_dim elements becomes (a c - b s,
+ * a s + b c) in fp32, rounded once to dtype; pair j is (j, j + rotary_dim / 2),
+ * or with interleaved != 0 (2 j, 2 j + 1), and takes the table's columns j and
+ * rotary_dim / 2 + j.  Elements from rotary_dim on pass bit for bit.
+ *   k, v         device, token i at k + i * k_stride (elements of dtype, F16 or
+ *                BF16): [n_kv_heads, head_dim] contiguous per token, so q, k and v
+ *                may be views of one fused tensor; strides multiples of 8
+ *                elements, rows 16-byte aligned
+ *   k_pool, v_pool device [num_blocks, block_size, n_kv_heads, head_dim] of
+ *                dtype, 16-byte aligned; any block_size
+ *   slot_mapping device int64 [num_tokens]; a token with a negative slot (a
+ *                padded one) is left out altogether, q_out and k_out included; so
+ *                is one with a slot beyond the pool (flagged PKV_DEVERR_SLOT) or a
+ *                position outside the table (PKV_DEVERR_POSITION).  Slots are
+ *                distinct (of equal ones either may be written, or parts of both).
+ *   positions    device int32 [num_tokens]: where the token stands in its
+ *                sequence, whatever row its slot is (after kv_evict they differ)
+ *   rope_table   device float [table_positions, rotary_dim] (pkv_rope_table), or
+ *                NULL: no rotation; then positions is not read, and there are no q,
+ *                q_out and k_out
+ *   q, q_out     device, rows [n_heads, head_dim] as k; both or neither (NULL)
+ *   k_out        device, rows [n_kv_heads, head_dim], or NULL: the rotated keys for
+ *                pkv_attn_prompt
+ * q_out may be q itself and k_out k itself (same stride); otherwise outputs and
+ * pools overlap nothing else of the call.
+ * head_dim 64 or 128; rotary_dim a multiple of 16, at most head_dim; at most 4096
+ * heads.  One launch.
+ */
+PKV_API pkv_status kv_append_rope(void* k_pool, void* v_pool, const void* k, int64_t k_stride,
+                                  const void* v, int64_t v_stride, pkv_dtype dtype,
+                                  const int64_t* slot_mapping, const int32_t* positions,
+                                  const float* rope_table, int table_positions, int rotary_dim,
+                                  int interleaved, const void* q, int64_t q_stride, void* q_out,
+                                  int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                                  int num_tokens, int n_heads, int n_kv_heads, int head_dim,
+                                  int block_size, int num_blocks, void* stream);
+
+/*
+ * kv_append_rope_q8 -- kv_append_rope into a cache of 8 bits: elements are e4m3
+ * (4 exponent and 3 mantissa bits, largest number 448, no infinities), and stand
+ * for their value times the scale of their block and kv head:
+ *
+ *     K[t, h, :] = k_scale[block, h] * k_pool[block, row, h, :]     (same for V)
+ *
+ * The append sets a block's scale by what it holds: s(x), the least power of two
+ * (2^-117 at least) with x / s(x) <= 448 for the largest new value x of the block
+ * and head -- or the old scale, where earlier tokens are in the block and it is
+ * larger.  Where it grows the block's earlier rows are rounded to it anew; they
+ * change only where they come to lie below 2^-6 of the scale.  Values are rounded
+ * once, from fp32, to the nearest (ties to even); NaN stays NaN, infinities become
+ * +-448 and neither counts for the scale.
+ *   k_pool, v_pool device e4m3 bytes [num_blocks, block_size, n_kv_heads,
+ *                head_dim], 16-byte aligned; block_size 16 or 32
+ *   k_scale, v_scale device float [num_blocks, n_kv_heads]; read only of blocks
+ *                that hold earlier tokens, where they may be any positive numbers
+ *   slot_mapping as kv_append_rope, and: the tokens of one block follow one another
+ *                in the call, to rising rows (appended tokens in order do).  Rows of
+ *                the block ahead of the first hold tokens; the rows behind hold none
+ *                and are left as they were.  A token behind one of its block that
+ *                does not go to a later row, and those of the block that follow it,
+ *                are not appended (flagged PKV_DEVERR_SLOT; q_out is written).  If
+ *                the tokens of one block stand apart in the call, that block's
+ *                contents are undefined.  The block is the call's alone while it
+ *                runs (shared ones are copied on write).
+ *   other arguments as kv_append_rope: k, v, q, q_out and k_out are 16-bit.
+ * One launch.
+ */
+PKV_API pkv_status kv_append_rope_q8(void* k_pool, void* v_pool, float* k_scale, float* v_scale,
+                                     const void* k, int64_t k_stride, const void* v,
+                                     int64_t v_stride, pkv_dtype dtype,
+                                     const int64_t* slot_mapping, const int32_t* positions,
+                                     const float* rope_table, int table_positions, int rotary_dim,
+                                     int interleaved, const void* q, int64_t q_stride, void* q_out,
+                                     int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                                     int num_tokens, int n_heads, int n_kv_heads, int head_dim,
+                                     int block_size, int num_blocks, void* stream);
 
 /*
  * swap_blocks -- batched block copy ([SWAP] swap_blocks; [OPT] "Swap Blocks

@@ -21,6 +21,7 @@ DEVERR_CONTEXT = 0x2
 DEVERR_SLOT = 0x4
 DEVERR_PAIR = 0x8
 DEVERR_TIMEOUT = 0x10
+DEVERR_POSITION = 0x40
 
 # Launch-shape override knobs (pkv_tune_knob), by lower-case name.
 TUNE_AUTO = -2147483648
@@ -68,6 +69,11 @@ SIGNATURES = {
     "pkv_attn_prompt": (_i, [_p, _i, _p, _i64, _p, _i64, _p, _i64, _i, _p, _i, _i, _i, _i, _i, _i,
                          _f, _p]),
     "kv_append": (_i, [_p, _p, _p, _p, _i, _p, _i, _i, _i, _i, _i, _p]),
+    "pkv_rope_table": (_i, [_p, _i, _i, _p, _f, _p]),
+    "kv_append_rope": (_i, [_p, _p, _p, _i64, _p, _i64, _i, _p, _p, _p, _i, _i, _i, _p, _i64, _p,
+                            _i64, _p, _i64, _i, _i, _i, _i, _i, _i, _p]),
+    "kv_append_rope_q8": (_i, [_p, _p, _p, _p, _p, _i64, _p, _i64, _i, _p, _p, _p, _i, _i, _i, _p,
+                               _i64, _p, _i64, _p, _i64, _i, _i, _i, _i, _i, _i, _p]),
     "swap_blocks": (_i, [_p, _p, _sz, _p, _i, _i64, _i64, _p]),
     "swap_blocks_kv": (_i, [_p, _p, _p, _p, _sz, _p, _i, _i64, _i64, _p]),
     "pkv_block_manager_create": (_p, [_i, _i]),

@@ -6,6 +6,7 @@ CUDA kernels; torch provides device memory and streams.
 from __future__ import annotations
 
 import ctypes as C
+import math
 from typing import Optional
 
 import torch
@@ -636,6 +637,165 @@ def kv_append(k_pool: torch.Tensor, v_pool: torch.Tensor, k_new: torch.Tensor,
     st = lib().kv_append(_ptr(k_pool), _ptr(v_pool), _ptr(k_new), _ptr(v_new), _DT[k_pool.dtype],
                          _ptr(slot_mapping), S, Hk, D, B, nb, _stream_ptr(stream))
     check(st, "kv_append")
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[str] = None,
+                     factor: float = 1.0, original_positions: int = 0,
+                     beta_fast: float = 32.0, beta_slow: float = 1.0) -> tuple:
+    """Angles per position of the rotary_dim / 2 pairs (CPU float64) and the
+    factor of cosines and sines, for rope_table.  base^(-2 i / rotary_dim), and
+    for contexts `factor` times as long as the model was trained on:
+      "linear"  positions divided by factor
+      "ntk"     the base raised so that the slowest pair turns factor times slower
+      "yarn"    by parts (arXiv:2309.00071): pairs that turn more than beta_fast
+                times within original_positions as they are, fewer than beta_slow
+                times divided by factor, a ramp between; cosines and sines times
+                0.1 ln(factor) + 1"""
+    if rotary_dim <= 0 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be positive and even")
+    if not (math.isfinite(base) and base > 0 and math.isfinite(factor) and factor > 0):
+        raise ValueError("base and factor must be positive numbers")
+    pair = torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim
+    if scaling is None:
+        return base ** -pair, 1.0
+    if scaling == "linear":
+        return base ** -pair / factor, 1.0
+    if scaling == "ntk":
+        if rotary_dim < 4:
+            raise ValueError("ntk needs two pairs at least")
+        return (base * factor ** (rotary_dim / (rotary_dim - 2))) ** -pair, 1.0
+    if scaling != "yarn":
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if original_positions <= 0 or not 0 < beta_slow < beta_fast:
+        raise ValueError("yarn needs original_positions and 0 < beta_slow < beta_fast")
+    freq = base ** -pair
+
+    def pair_turning(times):
+        return rotary_dim * math.log(original_positions / (times * 2 * math.pi)) / \
+            (2 * math.log(base))
+
+    low = max(math.floor(pair_turning(beta_fast)), 0)
+    high = min(math.ceil(pair_turning(beta_slow)), rotary_dim - 1)
+    ramp = ((torch.arange(rotary_dim // 2, dtype=torch.float64) - low) /
+            max(high - low, 1e-3)).clamp(0, 1)
+    return freq * (1 - ramp) + freq / factor * ramp, \
+        0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+
+
+def rope_table(table: torch.Tensor, inv_freq, factor: float = 1.0,
+               stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Fills table (fp32 [positions, rotary_dim]) with factor * cos(t *
+    inv_freq[i]) and, behind them, the sines; angles in 64 bits.  inv_freq: the
+    rotary_dim / 2 angles per position (a CPU tensor or numbers), e.g. of
+    rope_frequencies."""
+    _need_here(("table",), (table,))
+    if table.dtype is not torch.float32 or table.dim() != 2:
+        raise ValueError("table must be float32 [positions, rotary_dim]")
+    freq = torch.as_tensor(inv_freq, dtype=torch.float64, device="cpu").contiguous()
+    if freq.shape != (table.shape[1] // 2,):
+        raise ValueError("inv_freq must have rotary_dim / 2 entries")
+    check(lib().pkv_rope_table(table.data_ptr(), table.shape[0], table.shape[1], freq.data_ptr(),
+                               float(factor), _stream_handle(stream)), "rope_table")
+    return table
+
+
+def _rope_append_args(k_pool, v_pool, pool_dtype, k, v, slot_mapping, positions, rope, q, q_out,
+                      k_out, interleaved) -> tuple:
+    """The checked C arguments of the rotating appends behind the pools."""
+    _need_here(("k_pool", "v_pool", "slot_mapping"), (k_pool, v_pool, slot_mapping))
+    dev = k_pool.get_device()
+    if k_pool.dim() != 4 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("pools are [num_blocks, B, Hk, D], k and v [tokens, Hk, D]")
+    nb, B, Hk, D = k_pool.shape
+    T = k.shape[0]
+    if (v_pool.shape != k_pool.shape or k.shape != (T, Hk, D) or v.shape != k.shape
+            or v.dtype != k.dtype or k_pool.dtype is not pool_dtype
+            or v_pool.dtype is not pool_dtype or slot_mapping.shape != (T,)):
+        raise ValueError("inconsistent shapes or dtypes")
+    if slot_mapping.dtype is not torch.int64:
+        raise ValueError("slot_mapping must be int64")
+    if k.dtype not in _DT:
+        raise ValueError("k and v must be float16 or bfloat16")
+    rows = [("k", k), ("v", v)]
+    if rope is not None:
+        _need_here(("rope", "positions"), (rope, positions))
+        if rope.get_device() != dev:
+            raise ValueError("tensors must be on the current CUDA device")
+        if rope.dtype is not torch.float32 or rope.dim() != 2:
+            raise ValueError("rope must be float32 [positions, rotary_dim]")
+        if positions.dtype is not torch.int32 or positions.shape != (T,):
+            raise ValueError("positions must be int32 [tokens]")
+    H = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out: both or neither")
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or q_out.shape != q.shape:
+            raise ValueError("q and q_out must be [tokens, H, D]")
+        H = q.shape[1]
+        rows += [("q", q), ("q_out", q_out)]
+    if k_out is not None:
+        if k_out.shape != k.shape:
+            raise ValueError("k_out must be shaped like k")
+        rows.append(("k_out", k_out))
+    stride = {}
+    for name, t in rows:
+        if t.get_device() != dev or t.dtype is not k.dtype:
+            raise ValueError(f"{name} must be of k's dtype, on the current CUDA device")
+        stride[name] = _token_stride(name, t)
+    return (k.data_ptr(), stride["k"], v.data_ptr(), stride["v"], _DT[k.dtype],
+            slot_mapping.data_ptr(), positions.data_ptr() if rope is not None else 0,
+            _address(rope), rope.shape[0] if rope is not None else 0,
+            rope.shape[1] if rope is not None else 0, 1 if interleaved else 0,
+            _address(q), stride.get("q", 0), _address(q_out), stride.get("q_out", 0),
+            _address(k_out), stride.get("k_out", 0), T, H, Hk, D, B, nb)
+
+
+def _address(t: Optional[torch.Tensor]) -> int:
+    return t.data_ptr() if t is not None else 0
+
+
+def kv_append_rope(k_pool: torch.Tensor, v_pool: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                   slot_mapping: torch.Tensor, positions: Optional[torch.Tensor] = None,
+                   rope: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                   q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                   interleaved: bool = False,
+                   stream: Optional[torch.cuda.Stream] = None) -> None:
+    """kv_append of k and v [T, Hk, D] (each token contiguous: views of one
+    fused projection will do), k rotated by positions (int32 [T], rows of the
+    table `rope`, see rope_table) on the way, and q [T, H, D] into q_out; k_out
+    takes the rotated keys too.  q_out may be q and k_out k.  Tokens of slot -1
+    are left out."""
+    args = _rope_append_args(k_pool, v_pool, k.dtype, k, v, slot_mapping, positions, rope, q,
+                             q_out, k_out, interleaved)
+    check(lib().kv_append_rope(k_pool.data_ptr(), v_pool.data_ptr(), *args,
+                               _stream_handle(stream)), "kv_append_rope")
+
+
+def _need_scales(k_pool, k_scale, v_scale) -> None:
+    _need_here(("k_pool", "k_scale", "v_scale"), (k_pool, k_scale, v_scale))
+    want = (k_pool.shape[0], k_pool.shape[2])
+    for t in (k_scale, v_scale):
+        if t.dtype is not torch.float32 or t.shape != want:
+            raise ValueError("k_scale and v_scale must be float32 [num_blocks, Hk]")
+
+
+def kv_append_rope_q8(k_pool: torch.Tensor, v_pool: torch.Tensor, k_scale: torch.Tensor,
+                      v_scale: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                      slot_mapping: torch.Tensor, positions: Optional[torch.Tensor] = None,
+                      rope: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                      q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                      interleaved: bool = False,
+                      stream: Optional[torch.cuda.Stream] = None) -> None:
+    """kv_append_rope into float8_e4m3fn pools with a scale (fp32 [num_blocks,
+    Hk]) for each block and kv head: the least power of two that holds the
+    block's rows; where it grows, the block's earlier rows are rounded anew.  The
+    tokens of one block follow one another in the call, in order."""
+    args = _rope_append_args(k_pool, v_pool, torch.float8_e4m3fn, k, v, slot_mapping, positions,
+                             rope, q, q_out, k_out, interleaved)
+    _need_scales(k_pool, k_scale, v_scale)
+    check(lib().kv_append_rope_q8(k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(),
+                                  v_scale.data_ptr(), *args, _stream_handle(stream)),
+          "kv_append_rope_q8")
 
 
 def swap_blocks(dst_pool: torch.Tensor, src_pool: torch.Tensor, pairs: torch.Tensor,
