@@ -722,6 +722,38 @@ PKV_API pkv_status kv_append_rope_q8(void* k_pool, void* v_pool, float* k_scale,
                                      int block_size, int num_blocks, void* stream);
 
 /*
+ * paged_attn_decode_q8 -- paged_attn_decode over a cache of 8 bits
+ * (kv_append_rope_q8 writes it): with codes k_t, v_t (e4m3) and the scales a_t, b_t
+ * of token t's block and kv head,
+ *
+ *     out[s,h,:] = sum_t softmax_t(scale * a_t (q[s,h,:] . k_t)) b_t v_t
+ *
+ *   q             device, [num_seqs, n_heads, head_dim] of q_dtype (F16 or BF16)
+ *   k_pool, v_pool device e4m3 bytes [num_blocks, block_size, n_kv_heads,
+ *                 head_dim], 16-byte aligned
+ *   k_scale, v_scale device float [num_blocks, n_kv_heads]: any positive numbers
+ *                 (powers of two from the append, or others, e.g. calibrated ones)
+ *   workspace     device, >= pkv_decode_q8_workspace_bytes(...) bytes, 256-byte
+ *                 aligned; contents on entry are ignored.  Calls that may overlap
+ *                 on the GPU need a workspace each.
+ *   other arguments as paged_attn_decode (the split is automatic).
+ * Scores, sums and outputs as in paged_attn_decode: products of the codes are exact,
+ * scales stay in fp32, weights enter the second product as two F16 parts.
+ * Supported shapes as paged_attn_decode; at most 65535 sequences, 4096 query
+ * heads.  16 tokens in a block outside the pool are left out and flagged
+ * PKV_DEVERR_BLOCK_ID.  Two launches.
+ */
+PKV_API size_t pkv_decode_q8_workspace_bytes(int num_seqs, int n_heads, int n_kv_heads,
+                                             int head_dim, int block_size, int max_context_len);
+
+PKV_API pkv_status paged_attn_decode_q8(
+    void* out, pkv_dtype out_dtype, const void* q, pkv_dtype q_dtype, const void* k_pool,
+    const void* v_pool, const float* k_scale, const float* v_scale, const int32_t* block_tables,
+    int max_blocks_per_seq, const int32_t* context_lens, int num_seqs, int n_heads,
+    int n_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
+    int max_context_len, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * swap_blocks -- batched block copy ([SWAP] swap_blocks; [OPT] "Swap Blocks
  * 机制", one call per cache: Key, then Value):
  *

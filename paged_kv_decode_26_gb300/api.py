@@ -798,6 +798,46 @@ def kv_append_rope_q8(k_pool: torch.Tensor, v_pool: torch.Tensor, k_scale: torch
           "kv_append_rope_q8")
 
 
+def decode_q8_workspace_bytes(num_seqs: int, n_heads: int, n_kv_heads: int, head_dim: int,
+                              block_size: int, max_context_len: int) -> int:
+    return int(lib().pkv_decode_q8_workspace_bytes(num_seqs, n_heads, n_kv_heads, head_dim,
+                                                   block_size, max_context_len))
+
+
+def paged_attn_decode_q8(out: torch.Tensor, q: torch.Tensor, k_pool: torch.Tensor,
+                         v_pool: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                         block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
+                         max_context_len: int, workspace: Optional[torch.Tensor] = None,
+                         stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """paged_attn_decode over float8_e4m3fn pools [num_blocks, B, Hk, D] with
+    scales fp32 [num_blocks, Hk] for each block and kv head; q is 16-bit."""
+    _need_here(_DECODE_NAMES + ("k_scale", "v_scale"),
+               (out, q, k_pool, v_pool, block_tables, context_lens, k_scale, v_scale))
+    _need_ints(("block_tables", "context_lens"), (block_tables, context_lens))
+    S, H, D = q.shape
+    nb, B, Hk, D2 = k_pool.shape
+    if (D2 != D or v_pool.shape != k_pool.shape or out.shape != q.shape
+            or k_pool.dtype is not torch.float8_e4m3fn or v_pool.dtype is not torch.float8_e4m3fn
+            or k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32
+            or k_scale.shape != (nb, Hk) or v_scale.shape != (nb, Hk)
+            or block_tables.dim() != 2 or block_tables.shape[0] != S
+            or context_lens.shape != (S,)):
+        raise ValueError("inconsistent shapes or dtypes")
+    max_context_len = int(max_context_len)
+    if workspace is None:
+        workspace = _stream_buffer(
+            lib().pkv_decode_q8_workspace_bytes(S, H, Hk, D, B, max_context_len), q.device, stream)
+    else:
+        _need_here(("workspace",), (workspace,))
+    st = lib().paged_attn_decode_q8(
+        out.data_ptr(), _DT[out.dtype], q.data_ptr(), _DT[q.dtype], k_pool.data_ptr(),
+        v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(),
+        block_tables.shape[1], context_lens.data_ptr(), S, H, Hk, D, B, nb, float(scale),
+        max_context_len, workspace.data_ptr(), workspace.nbytes, _stream_handle(stream))
+    check(st, "paged_attn_decode_q8")
+    return out
+
+
 def swap_blocks(dst_pool: torch.Tensor, src_pool: torch.Tensor, pairs: torch.Tensor,
                 stream: Optional[torch.cuda.Stream] = None) -> None:
     """dst_pool[j] = src_pool[i] for each (i, j) row of `pairs` (int64 [n, 2]).

@@ -36,10 +36,10 @@ int pieces_stream_heads(int n_kv_heads) {
 }
 
 PiecesGrid pieces_grid(int num_seqs, int n_kv_heads, int max_context_len, int sm_count,
-                       bool short_runs) {
+                       bool short_runs, int chunk_tokens) {
     const int hw = pieces_stream_heads(n_kv_heads), per_cta = kPieceWarps / hw;
     const long long chunks = (long long)num_seqs * (n_kv_heads / hw) *
-                             (((long long)max_context_len + kPieceTokens - 1) / kPieceTokens);
+                             (((long long)max_context_len + chunk_tokens - 1) / chunk_tokens);
     const long long streams = (chunks + kPieceMinRun - 1) / kPieceMinRun;
     const long long ctas = (streams + per_cta - 1) / per_cta;
     PiecesGrid g;
@@ -134,6 +134,17 @@ pkv_status fill_pieces(PieceParams* pp, CUtensorMap* tm_k, CUtensorMap* tm_v,
         (e = encode_chunk_map(tm_v, num_blocks > 0 ? v_pool : q, kv_dtype, map_blocks, block_size,
                               n_kv_heads, head_dim)))
         return cuda_fail(e);
+    fill_piece_problem(pp, grid, out, out_dtype, q, block_tables, max_blocks_per_seq, context_lens,
+                       num_seqs, n_heads, n_kv_heads, block_size, num_blocks, scale,
+                       max_context_len, w, workspace, dev);
+    return PKV_OK;
+}
+
+void fill_piece_problem(PieceParams* pp, const PiecesGrid& grid, void* out, pkv_dtype out_dtype,
+                        const void* q, const int32_t* block_tables, int max_blocks_per_seq,
+                        const int32_t* context_lens, int num_seqs, int n_heads, int n_kv_heads,
+                        int block_size, int num_blocks, float scale, int max_context_len,
+                        const PiecesWorkspace& w, void* workspace, const DeviceInfo& dev) {
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     PieceParams& p = *pp;
     p.out = out;
@@ -159,7 +170,6 @@ pkv_status fill_pieces(PieceParams* pp, CUtensorMap* tm_k, CUtensorMap* tm_v,
     p.seg_first = reinterpret_cast<int*>(ws + w.seg_first);
     p.seg_last = reinterpret_cast<int*>(ws + w.seg_last);
     p.errors = dev.errors;
-    return PKV_OK;
 }
 
 pkv_status check_workspace(const void* workspace, size_t bytes, size_t need) {

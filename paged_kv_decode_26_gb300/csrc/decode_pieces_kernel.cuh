@@ -334,14 +334,15 @@ __device__ __forceinline__ PieceShared piece_shared(unsigned char* ring, unsigne
     return sh;
 }
 
-// First chunk, context length and number of chunks of sequence i.
-template <bool WEIGHTS>
+// First chunk, context length and number of chunks (of TOKENS tokens) of
+// sequence i.
+template <bool WEIGHTS, int TOKENS = kPieceTokens>
 __device__ __forceinline__ int piece_span(const PieceParams& p, const int* gs, int i, int& first,
                                           int& n) {
     n = piece_length(p, i);
     const int start = WEIGHTS ? 0 : piece_start(p, gs, i, n);
-    first = start / kPieceTokens;
-    return (n + kPieceTokens - 1) / kPieceTokens - first;
+    first = start / TOKENS;
+    return (n + TOKENS - 1) / TOKENS - first;
 }
 
 // The barrier of the piece decode's 256 threads.
@@ -352,7 +353,7 @@ __device__ __forceinline__ void piece_sync() {
 // By threads 0 .. 255: barriers, group starts, and the chunks before each
 // block of 256 sequences, bad lengths and groups flagged, p.start written.  Returns the
 // chunks of all sequences.
-template <bool WEIGHTS>
+template <bool WEIGHTS, int TOKENS = kPieceTokens>
 __device__ __forceinline__ int piece_plan(const PieceParams& p, PieceShared& sh) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = p.num_seqs;
@@ -378,12 +379,12 @@ __device__ __forceinline__ int piece_plan(const PieceParams& p, PieceShared& sh)
         int c = 0;
         if (i < S) {
             int first, n;
-            c = piece_span<WEIGHTS>(p, sh.gs, i, first, n);
+            c = piece_span<WEIGHTS, TOKENS>(p, sh.gs, i, first, n);
             // (any CTA may be taken over before it starts, so all do this,
             // with the same values)
             const int raw_n = p.context_lens[i];
             if (raw_n < 0 || raw_n > p.cap_tokens) raise_error(p.errors, PKV_DEVERR_CONTEXT);
-            if (!WEIGHTS) p.start[i] = first * kPieceTokens;
+            if (!WEIGHTS) p.start[i] = first * TOKENS;
         }
 #pragma unroll
         for (int off = 16; off; off >>= 1) c += __shfl_xor_sync(0xffffffffu, c, off);
@@ -463,7 +464,7 @@ struct PieceCursor {
 };
 
 // The start of stream v's run, by a whole warp.
-template <bool WEIGHTS>
+template <bool WEIGHTS, int TOKENS = kPieceTokens>
 __device__ __forceinline__ PieceCursor piece_locate(const PieceParams& p, const PieceShared& sh,
                                                     const PieceRuns& r, int v, int lane) {
     const long long u0 = r.begin(v);
@@ -478,7 +479,7 @@ __device__ __forceinline__ PieceCursor piece_locate(const PieceParams& p, const 
     for (int base = b * 256;; base += 32) {
         const int i = base + lane;
         int f = 0, len = 0;
-        const int c = i < S ? piece_span<WEIGHTS>(p, sh.gs, i, f, len) : 0;
+        const int c = i < S ? piece_span<WEIGHTS, TOKENS>(p, sh.gs, i, f, len) : 0;
         int inc = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -504,7 +505,7 @@ __device__ __forceinline__ PieceCursor piece_locate(const PieceParams& p, const 
 }
 
 // The next unit of the run.
-template <bool WEIGHTS>
+template <bool WEIGHTS, int TOKENS = kPieceTokens>
 __device__ __forceinline__ void piece_advance(const PieceParams& p, const PieceShared& sh,
                                               PieceCursor& k) {
     --k.left;
@@ -514,7 +515,7 @@ __device__ __forceinline__ void piece_advance(const PieceParams& p, const PieceS
         if (k.left > 0) {
             int count;
             while (++k.s < p.num_seqs &&
-                   (count = piece_span<WEIGHTS>(p, sh.gs, k.s, k.first, k.n)) == 0) {
+                   (count = piece_span<WEIGHTS, TOKENS>(p, sh.gs, k.s, k.first, k.n)) == 0) {
             }
             k.end = k.first + count;
         }

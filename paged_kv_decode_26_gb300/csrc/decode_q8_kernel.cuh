@@ -1,0 +1,607 @@
+// decode_q8_kernel.cuh -- paged decode over 8-bit pages (e4m3 with a scale per
+// block and kv head) as equal pieces per warp (sm_103a): paged_attn_decode_q8.
+//
+// Mathematics: with codes k_t, v_t and the scales a_t, b_t of token t's block,
+// scores x_t = scale log2(e) a_t (q . k_t), the sum L of p_t = 2^(x_t - m) and
+// O = sum p_t b_t v_t; the result is O / L.  Codes are exact in fp16, so they
+// enter mma.sync as they are and the scales stay in fp32: a_t on the score, b_t on
+// the weight.
+//
+// What bounds it: HBM, at half the bytes of 16-bit pages for the same products, so
+// twice the work a byte.  A 32-token chunk of one kv head (8 KB) is 16 + 32
+// products m16n8k16, 128 conversions of two codes and 16 ldmatrix.
+//
+// Layout: the tokens are the rows of the score product and the inner dimension of
+// the second one.  An ldmatrix of 16-bit units hands a lane bytes 4 t .. 4 t + 3
+// of a token's 16 dims, which two conversions turn into two registers of the A
+// operand; the inner dimension's order is the queries' to choose (MMA columns
+// 2 t, 2 t + 1 stand for dims 4 t, 4 t + 1, columns 2 t + 8, + 9 for 4 t + 2, + 3).
+// Transposed, it hands a lane dims 2 g, 2 g + 1 of tokens 2 t, 2 t + 1; one byte
+// permutation puts each dim's tokens side by side, and rows g, g + 8 of the output
+// stand for dims 2 g, 2 g + 1.
+//
+// Precision: a bf16 query head is scaled by a power of two into fp16's range
+// (exact but for elements 2^-38 below its largest).  Weights enter the second
+// product as p b / b_ref in two fp16 parts, lifted as in weight_range.cuh; the
+// reference (m, b_ref) is the score and scale of the key with the largest p b when
+// it was set, m a score itself (weight_range.cuh says why).
+//
+// Runs, rings and merge as in decode_pieces_kernel.cuh, with chunks of 32 tokens.
+#pragma once
+
+#include "decode_pieces_kernel.cuh"
+
+namespace pkv {
+
+constexpr int kQ8Tokens = 32;                  // tokens per chunk: two halves of 16
+constexpr float kQ8LeastScale = 0x1p-100f;     // of a reference (blocks of zeros)
+
+struct Q8Params : PieceParams {
+    const float* k_scale;      // [num_blocks, n_kv_heads]
+    const float* v_scale;
+};
+
+// Two codes each of the low and the high half of w, as packed fp16 (exact).
+__device__ __forceinline__ void q8_widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
+// The 8x8 matrix of 16-bit elements that a warp holds (lane 4 r + c: row r,
+// columns 2 c, 2 c + 1), transposed.
+__device__ __forceinline__ uint32_t q8_transpose(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// Byte offset of 16-byte unit c of token row t in a box of [16 x D] bytes, swizzled
+// over D bytes.
+template <int D>
+__device__ __forceinline__ uint32_t q8_at(int t, int c) {
+    return D == 128 ? (uint32_t)(t * 128 + ((c ^ (t & 7)) << 4))
+                    : (uint32_t)(t * 64 + ((c ^ ((t >> 1) & 3)) << 4));
+}
+
+// One kv head's query heads in one warp, lane = 4 gid + tig: queries as B operands
+// of head gid; sums of heads 2 tig and 2 tig + 1 (o[j][0], o[j][2]: dims 16 j + 2
+// gid, + 1 of the first; o[j][1], o[j][3]: of the second).
+template <int D>
+struct Q8Heads {
+    uint32_t qb[D / 16][2];
+    float o[D / 16][4];
+    float qf[2];       // score of a unit product at scale 1
+    float m[2];        // the reference: a score,
+    float lv[2];       // the logarithm of its value scale,
+    float rv[2];       // and 1 over that
+    float l[2];        // this lane's part of the sum
+};
+
+template <int D, typename T>
+__device__ __forceinline__ void q8_heads_start(Q8Heads<D>& st, const T* qrow0, int G,
+                                               float scale_log2, int lane) {
+    const int gid = lane >> 2, tig = lane & 3;
+    const bool real = gid < G;
+    const T* row = qrow0 + (size_t)(real ? gid : 0) * D;
+    uint2 w[D / 16];
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c)
+        w[c] = *reinterpret_cast<const uint2*>(row + 16 * c + 4 * tig);
+    float back = 1.f;
+    if (std::is_same<T, __half>::value) {
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+            st.qb[c][0] = real ? w[c].x : 0u;
+            st.qb[c][1] = real ? w[c].y : 0u;
+        }
+    } else {
+        float top = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+            const float2 a = unpack2<T>(w[c].x), b = unpack2<T>(w[c].y);
+            auto take = [&](float x) { top = fabsf(x) < INFINITY ? fmaxf(top, fabsf(x)) : top; };
+            take(a.x), take(a.y), take(b.x), take(b.y);
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // the largest to 2^14 .. 2^15
+        const int e = min(max((int)(__float_as_uint(top) >> 23), 24), 254);
+        const float to = __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23);
+        back = __uint_as_float((uint32_t)(e - 14) << 23);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+            const float2 a = unpack2<T>(w[c].x), b = unpack2<T>(w[c].y);
+            st.qb[c][0] = real ? pack2<__half>(a.x * to, a.y * to) : 0u;
+            st.qb[c][1] = real ? pack2<__half>(b.x * to, b.y * to) : 0u;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        st.qf[e] = scale_log2 * __shfl_sync(0xffffffffu, back, 4 * (2 * tig + e));
+        st.m[e] = -INFINITY;
+        st.lv[e] = 0.f;
+        st.rv[e] = 1.f;
+        st.l[e] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) st.o[j][0] = st.o[j][1] = st.o[j][2] = st.o[j][3] = 0.f;
+}
+
+// The scales of a chunk's halves.
+struct Q8Scales {
+    float k[2], v[2];
+};
+
+// One chunk: halves of 16 tokens at kbase / vbase (+ 16 D bytes), `valid[h]` of a
+// half's tokens inside the context (0: nothing was loaded, or its block is
+// missing).  PRECISE: see piece_chunk.
+template <int D, bool PRECISE>
+__device__ __forceinline__ void q8_chunk(Q8Heads<D>& st, uint32_t kbase, uint32_t vbase,
+                                         const int (&valid)[2], const Q8Scales& sc, int lane) {
+    using Range = WeightRange<__half>;
+    constexpr uint32_t HALF = 16 * D;
+    const int gid = lane >> 2, tig = lane & 3;
+    const int mat = lane >> 3, mrow = lane & 7;
+    // ldmatrix matrices: (tokens 0-7, unit c), (8-15, c), (0-7, c+1), (8-15, c+1)
+    const int tok = (mat & 1) * 8 + mrow, unit = mat >> 1;
+
+    // ---- scores: rows = tokens, columns = query heads
+    float x[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < D / 16; c += 2) {
+            uint32_t r0, r1, r2, r3;
+            ldsm_x4(kbase + h * HALF + q8_at<D>(tok, c + unit), r0, r1, r2, r3);
+            uint32_t a[4];
+            q8_widen(r0, a[0], a[2]);
+            q8_widen(r1, a[1], a[3]);
+            mma16816<__half>(s0, a, st.qb[c][0], st.qb[c][1]);
+            q8_widen(r2, a[0], a[2]);
+            q8_widen(r3, a[1], a[3]);
+            mma16816<__half>(s1, a, st.qb[c + 1][0], st.qb[c + 1][1]);
+        }
+        // this lane: tokens gid (x0, x1) and gid + 8 (x2, x3) of heads 2 tig, + 1
+        const float f0 = st.qf[0] * sc.k[h], f1 = st.qf[1] * sc.k[h];
+        const bool in0 = gid < valid[h], in1 = gid + 8 < valid[h];
+        x[h][0] = in0 ? __fmul_rn(s0[0] + s1[0], f0) : -INFINITY;
+        x[h][1] = in0 ? __fmul_rn(s0[1] + s1[1], f1) : -INFINITY;
+        x[h][2] = in1 ? __fmul_rn(s0[2] + s1[2], f0) : -INFINITY;
+        x[h][3] = in1 ? __fmul_rn(s0[3] + s1[3], f1) : -INFINITY;
+    }
+    // ---- the reference, where a weight would leave its range
+    float lv[2], bv[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        bv[h] = fmaxf(sc.v[h], kQ8LeastScale);
+        lv[h] = __log2f(bv[h]);
+    }
+    float top[2][2];
+    bool beyond = false;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            top[h][e] = fmaxf(x[h][e], x[h][2 + e]);
+            beyond |= (top[h][e] - st.m[e]) + (lv[h] - st.lv[e]) > Range::GROW;
+        }
+    if (__any_sync(0xffffffffu, beyond)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float m = st.m[e], l = st.lv[e], b = 1.f;
+            bool moved = false;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float t = top[h][e];
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1)
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
+                if (t > -INFINITY && (m == -INFINITY || (t - m) + (lv[h] - l) > 0.f)) {
+                    m = t;
+                    l = lv[h];
+                    b = bv[h];
+                    moved = true;
+                }
+            }
+            if (moved) {
+                const float al = st.m[e] == -INFINITY ? 1.f : exp2f(st.m[e] - m);
+                const float ao = st.m[e] == -INFINITY ? 1.f : exp2f((st.m[e] - m) + (st.lv[e] - l));
+                st.m[e] = m;
+                st.lv[e] = l;
+                st.rv[e] = __frcp_rn(b);
+                st.l[e] *= al;
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) {
+                    st.o[j][e] *= ao;
+                    st.o[j][2 + e] *= ao;
+                }
+            }
+        }
+    }
+    // ---- weights, in two parts, as the B operand (rows = tokens, columns = heads)
+    uint32_t hi[2][2], lo[2][2];
+    const float mu0 = st.m[0] == -INFINITY ? 0.f : st.m[0];
+    const float mu1 = st.m[1] == -INFINITY ? 0.f : st.m[1];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float f0 = sc.v[h] * st.rv[0] * (1.f / Range::UNLIFT);
+        const float f1 = sc.v[h] * st.rv[1] * (1.f / Range::UNLIFT);
+        const float p0 = exp2f(x[h][0] - mu0), p1 = exp2f(x[h][1] - mu1);
+        const float p2 = exp2f(x[h][2] - mu0), p3 = exp2f(x[h][3] - mu1);
+        st.l[0] += p0 + p2;
+        st.l[1] += p1 + p3;
+        // (a half with nothing in it may have any scale)
+        const bool any = valid[h] > 0;
+        const float w0 = any ? p0 * f0 : 0.f, w1 = any ? p1 * f1 : 0.f;
+        const float w2 = any ? p2 * f0 : 0.f, w3 = any ? p3 * f1 : 0.f;
+        const uint32_t a = pack2<__half>(w0, w1), b = pack2<__half>(w2, w3);
+        const float2 fa = unpack2<__half>(a), fb = unpack2<__half>(b);
+        hi[h][0] = q8_transpose(a);
+        hi[h][1] = q8_transpose(b);
+        lo[h][0] = q8_transpose(pack2<__half>(w0 - fa.x, w1 - fa.y));
+        lo[h][1] = q8_transpose(pack2<__half>(w2 - fb.x, w3 - fb.y));
+    }
+    // ---- O^T += V^T P^T; rows behind the context may hold NaN: cleared
+    // (a byte permutation's result: tokens 2 tig, 2 tig + 1 of one dim, then of the next)
+    uint32_t vm[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            vm[h][k] = (8 * k + 2 * tig < valid[h] ? 0x00ff00ffu : 0u) |
+                       (8 * k + 2 * tig + 1 < valid[h] ? 0xff00ff00u : 0u);
+#pragma unroll
+    for (int c = 0; c < D / 16; c += 2) {
+        float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t r[4];
+            ldsm_x4_trans(vbase + h * HALF + q8_at<D>(tok, c + unit), r[0], r[1], r[2], r[3]);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                uint32_t a[4];
+                q8_widen(__byte_perm(r[2 * u], 0u, 0x3120) & vm[h][0], a[0], a[1]);
+                q8_widen(__byte_perm(r[2 * u + 1], 0u, 0x3120) & vm[h][1], a[2], a[3]);
+                float(&d)[4] = PRECISE ? acc[u] : st.o[c + u];
+                mma16816<__half>(d, a, lo[h][0], lo[h][1]);
+                mma16816<__half>(d, a, hi[h][0], hi[h][1]);
+            }
+        }
+        if (PRECISE)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) st.o[c + u][e] += acc[u][e];
+    }
+}
+
+// A piece's result: normalised rows to the output (WHOLE) or, with (m, L), to the
+// workspace's rows row0 + head.
+template <int D, bool WHOLE>
+__device__ __forceinline__ void q8_store(const Q8Heads<D>& st, const Q8Params& p, size_t row0,
+                                         int lane) {
+    const int gid = lane >> 2, tig = lane & 3;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        float l = st.l[e];
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+        const int hh = 2 * tig + e;
+        if (hh >= p.group) continue;
+        // (1 / rv in two factors: either alone may leave fp32's range)
+        const float inv = l != 0.f ? __fdiv_rn(WeightRange<__half>::UNLIFT, l) : 0.f;
+        const float b = __frcp_rn(st.rv[e]);
+        const size_t row = row0 + hh;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+            const float v0 = st.o[j][e] * inv * b, v1 = st.o[j][2 + e] * inv * b;
+            const size_t at = row * D + 16 * j + 2 * gid;
+            if (!WHOLE)
+                *reinterpret_cast<float2*>(p.ws_o + at) = make_float2(v0, v1);
+            else if (p.out_dtype == PKV_F32)
+                *reinterpret_cast<float2*>(reinterpret_cast<float*>(p.out) + at) =
+                    make_float2(v0, v1);
+            else
+                *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.out) + at) =
+                    pack_out(v0, v1, p.out_dtype);
+        }
+        if (!WHOLE && gid == 0)
+            *reinterpret_cast<float2*>(p.ws_ml + row * 2) = make_float2(st.m[e], l);
+    }
+}
+
+// A half chunk's K and V rows (a box of [16 x D] bytes each).
+__device__ __forceinline__ void q8_load(uint32_t k, const CUtensorMap* tm_k, uint32_t v,
+                                        const CUtensorMap* tm_v, uint32_t bar, int row, int head,
+                                        int block, uint64_t policy, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %9, 0;\n\t"
+        "@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%10, %5, %6, %7}], [%4], %8;\n\t"
+        "@q cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%2], [%3, {%10, %5, %6, %7}], [%4], %8;\n\t}" ::"r"(k),
+        "l"(reinterpret_cast<uint64_t>(tm_k)), "r"(v), "l"(reinterpret_cast<uint64_t>(tm_v)),
+        "r"(bar), "r"(row), "r"(head), "r"(block), "l"(policy), "r"(lead), "r"(0)
+        : "memory");
+}
+
+// Bytes of the control area beside piece_shared's: the block of each half of the
+// chunks in the rings.
+constexpr size_t kQ8BlockBytes = (size_t)kPieceWarps * kPieceStages * 2 * sizeof(int);
+
+// One warp's work on the CTA's runs (piece_worker's, on 8-bit pages).
+template <int D, typename T, bool TAKES, bool PRECISE>
+__device__ __forceinline__ void q8_worker(const Q8Params& p, const CUtensorMap& tm_k,
+                                          const CUtensorMap& tm_v, const PieceShared& sh,
+                                          int* blocks, const PieceRuns& runs,
+                                          const PieceNext& next) {
+    constexpr uint32_t HALF = 16 * D;                 // half a chunk of K (or V)
+    constexpr uint32_t SLOT = 4 * HALF;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int HW = p.stream_heads, hw = warp % HW;
+    unsigned char* ring = sh.ring + (size_t)warp * kPieceStages * SLOT;
+    uint64_t* full = sh.bars + warp * kPieceStages;
+    int* slot_block = blocks + warp * kPieceStages * 2;
+    const int pages = kQ8Tokens / p.block_size;       // of a chunk: 2 or 1
+    const uint64_t policy = l2_policy_evict_first();
+    const uint32_t lead = lane == 0 ? 1u : 0u;
+    if (lane == 0) {
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
+    }
+
+    PieceCursor ld;              // the next chunk to load
+    PieceCursor at;              // the chunk to work on
+    bool ahead_run = false;      // the loads are in a run that `at` has not reached
+    PieceCursor ahead_start;     // its start
+    bool more = true;            // there may be a run after ld's (TAKES)
+    int win = -1, bid = -1;      // block ids of the pair's pages win .. win + 31
+    int cta = blockIdx.x, taken = 0;
+    ld.left = 0;
+
+    auto next_run = [&](bool own) {
+        while (more) {
+            if (!TAKES && !own) more = false;
+            if (!more) return;
+            if (!own) {
+                const int slot = (taken + 1) & 1;
+                const bool w = mbar_wait(&next.full[slot], (taken >> 1) & 1, p.errors);
+                cta = __all_sync(0xffffffffu, w) ? next.cta[slot] : -1;
+                __syncwarp();
+                ++taken;
+                if (cta < 0) {
+                    more = false;
+                    return;
+                }
+            }
+            own = false;
+            const int v = piece_stream(p, runs, cta, warp);
+            if (v >= 0) {
+                ld = piece_locate<true, kQ8Tokens>(p, sh, runs, v, lane);
+                win = -1;
+                if (TAKES && ld.left <= kPieceSoon && lane == 0) mbar_arrive(next.soon);
+                return;
+            }
+            if (TAKES && lane == 0) mbar_arrive(next.soon);
+        }
+    };
+    auto known = [&]() -> bool {
+        return __all_sync(0xffffffffu, mbar_test(&next.full[(taken + 1) & 1], (taken >> 1) & 1));
+    };
+    auto issue = [&](int st) {
+        const int page0 = ld.c * pages;
+        const int kvh = ld.hg * HW + hw;
+        if (win < 0 || page0 < win || page0 + pages > win + 32) {
+            win = page0;
+            const int page = win + lane;
+            const bool want = page * p.block_size < ld.n && page < p.max_blocks_per_seq;
+            bid = want ? p.block_tables[(size_t)ld.s * p.max_blocks_per_seq + page] : -1;
+            if (want && (bid < 0 || bid >= p.num_blocks)) {
+                raise_error(p.errors, PKV_DEVERR_BLOCK_ID);
+                bid = -1;
+            }
+            // the scales come to L2 with their pages
+            if (bid >= 0) {
+                const size_t i = (size_t)bid * p.n_kv_heads + kvh;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(p.k_scale + i));
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(p.v_scale + i));
+            }
+        }
+        int b[2];
+        b[0] = __shfl_sync(0xffffffffu, bid, page0 - win);
+        b[1] = __shfl_sync(0xffffffffu, bid, page0 + pages - 1 - win);
+        if (ld.c * kQ8Tokens + 16 >= ld.n) b[1] = -1;      // nothing in the second half
+        const int loads = (b[0] >= 0) + (b[1] >= 0);
+        const uint32_t dst = smem_addr(ring) + st * SLOT, bar = smem_addr(&full[st]);
+        if (lane == 0) {
+            slot_block[2 * st] = b[0];
+            slot_block[2 * st + 1] = b[1];
+            if (loads)
+                mbar_arrive_expect_tx(&full[st], loads * 2 * HALF);
+            else
+                mbar_arrive(&full[st]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (b[h] >= 0)
+                q8_load(dst + h * HALF, &tm_k, dst + (2 + h) * HALF, &tm_v, bar,
+                        pages == 1 ? 16 * h : 0, kvh, b[h], policy, lead);
+        const int s = ld.s, hg = ld.hg;
+        piece_advance<true, kQ8Tokens>(p, sh, ld);
+        if (ld.s != s || ld.hg != hg) win = -1;
+        if (TAKES && ld.left == kPieceSoon && lane == 0) mbar_arrive(next.soon);
+    };
+
+    next_run(true);
+    if (ld.left == 0) return;
+    if (!TAKES) more = false;
+    at = ld;
+    Q8Heads<D> state;
+    bool fresh = true;                 // the next chunk starts a piece
+    bool from_start = false;           // the piece holds the pair's first chunk
+    int st = 0, put = 0, in_flight = 0;
+    uint32_t phase = 0;
+    for (;;) {
+        // ---- keep the ring full
+        while (in_flight < kPieceStages) {
+            if (ld.left == 0) {
+                if (!TAKES || !more || ahead_run || (in_flight > 0 && !known())) break;
+                next_run(false);
+                if (!more) break;
+                if (at.left == 0) {
+                    at = ld;
+                } else {
+                    ahead_run = true;
+                    ahead_start = ld;
+                }
+            }
+            issue(put);
+            if (++put == kPieceStages) put = 0;
+            ++in_flight;
+        }
+        if (in_flight == 0) break;
+        // ---- one chunk
+        const int kvh = at.hg * HW + hw, qh0 = kvh * p.group;
+        Q8Scales sc;
+        int valid[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int b = slot_block[2 * st + h];
+            const size_t i = (size_t)max(b, 0) * p.n_kv_heads + kvh;
+            valid[h] = b >= 0 ? min(16, at.n - at.c * kQ8Tokens - 16 * h) : 0;
+            sc.k[h] = b >= 0 ? __ldg(p.k_scale + i) : 0.f;
+            sc.v[h] = b >= 0 ? __ldg(p.v_scale + i) : 0.f;
+        }
+        if (fresh) {
+            q8_heads_start<D, T>(state,
+                                 reinterpret_cast<const T*>(p.q) +
+                                     ((size_t)at.s * p.n_heads + qh0) * D,
+                                 p.group, p.scale_log2, lane);
+            from_start = at.c == at.first;
+            fresh = false;
+        }
+        const bool w = mbar_wait(&full[st], phase, p.errors);
+        if (!__all_sync(0xffffffffu, w)) {
+            // the loads still in flight land before the CTA may exit
+            for (; in_flight > 0; --in_flight) {
+                mbar_wait(&full[st], phase, p.errors);
+                if (++st == kPieceStages) {
+                    st = 0;
+                    phase ^= 1u;
+                }
+            }
+            break;
+        }
+        const uint32_t kbase = smem_addr(ring) + st * SLOT;
+        if (valid[0] > 0 || valid[1] > 0)
+            q8_chunk<D, PRECISE>(state, kbase, kbase + 2 * HALF, valid, sc, lane);
+        __syncwarp();
+        --in_flight;
+        if (++st == kPieceStages) {
+            st = 0;
+            phase ^= 1u;
+        }
+        // ---- the piece ends with the pair or with the run
+        const bool pair_end = at.c + 1 == at.end;
+        if (pair_end || at.left == 1) {
+            const size_t pair = (size_t)at.s * p.n_kv_heads + kvh;
+            const size_t own = (size_t)at.s * p.n_heads + qh0;
+            if (from_start && pair_end)
+                q8_store<D, true>(state, p, own, lane);
+            else
+                q8_store<D, false>(state, p,
+                                   from_start ? own
+                                              : (size_t)p.num_seqs * p.n_heads +
+                                                    ((size_t)at.v * HW + hw) * p.group,
+                                   lane);
+            if (lane == 0) {
+                if (from_start) p.seg_first[pair] = at.v;
+                if (pair_end) p.seg_last[pair] = at.v;
+            }
+            fresh = true;
+        }
+        if (at.left == 1) {
+            if (ahead_run) {
+                at = ahead_start;
+                ahead_run = false;
+            } else {
+                at.left = 0;
+            }
+        } else {
+            piece_advance<true, kQ8Tokens>(p, sh, at);
+        }
+    }
+}
+
+inline size_t decode_q8_smem_bytes(int D) {
+    return decode_pieces_smem_bytes(D) + kQ8BlockBytes;
+}
+
+// CTAs, runs and the ninth warp as in decode_pieces_kernel.
+template <int D, typename T, bool TAKES, bool PRECISE>
+__global__ void __launch_bounds__(kPieceThreads + (TAKES ? 32 : 0), 1)
+    decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v,
+                     const __grid_constant__ Q8Params p) {
+    launch_dependents();
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    unsigned char* sm = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    unsigned char* control = sm + decode_pieces_ring_bytes(D);
+    uint4* steal = reinterpret_cast<uint4*>(control);
+    uint64_t* steal_bar = reinterpret_cast<uint64_t*>(control + 16);
+    PieceNext next;
+    next.soon = steal_bar + 1;
+    next.full = next.soon + 1;
+    next.cta = reinterpret_cast<int*>(next.full + 2);
+    int* blocks = reinterpret_cast<int*>(control + 64);
+    PieceShared sh = piece_shared(sm, control + 64 + kQ8BlockBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (TAKES && threadIdx.x == kPieceThreads) {
+        mbar_init(steal_bar, 1);
+        mbar_init(next.soon, kPieceWarps);
+        mbar_init(&next.full[0], 1);
+        mbar_init(&next.full[1], 1);
+        fence_barrier_init();
+    }
+    int chunks = 0;
+    if (warp < kPieceWarps) chunks = piece_plan<true, kQ8Tokens>(p, sh);
+    if (TAKES) __syncthreads();
+    if (warp < kPieceWarps) {
+        q8_worker<D, T, TAKES, PRECISE>(p, tm_k, tm_v, sh, blocks, piece_runs(p, chunks), next);
+    } else {
+        for (int k = 0;; ++k) {
+            int cta = -1;
+            bool ok = __all_sync(0xffffffffu, mbar_wait(next.soon, k & 1, p.errors));
+            if (ok) {
+                if (lane == 0) steal_cta(steal, steal_bar);
+                ok = __all_sync(0xffffffffu, mbar_wait(steal_bar, k & 1, p.errors));
+                if (ok) cta = stolen_cta(steal);
+                __syncwarp();
+            }
+            if (lane == 0) {
+                next.cta[(k + 1) & 1] = cta;
+                mbar_arrive(&next.full[(k + 1) & 1]);
+            }
+            if (cta < 0) break;
+        }
+    }
+}
+
+// Rows cut into pieces, merged; rows of no token, zero.  Grid x: rows of a
+// sequence, kFinishWarps / W per CTA; y: sequences.
+template <int D, int W>
+__global__ void __launch_bounds__(kFinishThreads)
+    decode_q8_finish_kernel(const __grid_constant__ PieceParams p) {
+    __shared__ __align__(16) float s_o[kFinishWarps * D];
+    dependency_wait();
+    const int s = blockIdx.y, h = blockIdx.x * (kFinishWarps / W) + (threadIdx.x >> 5) / W;
+    const PieceSet c = piece_set(p, s, min(h, p.n_heads - 1), piece_length(p, s), 0);
+    merge_rows<D, W>(p, c, h < p.n_heads && (c.extra || !c.first), s, h, s_o);
+}
+
+}  // namespace pkv

@@ -31,7 +31,7 @@ struct PiecesGrid {
     int ctas, extra;
 };
 PiecesGrid pieces_grid(int num_seqs, int n_kv_heads, int max_context_len, int sm_count,
-                       bool short_runs);
+                       bool short_runs, int chunk_tokens = kPieceTokens);
 
 PiecesWorkspace pieces_workspace(int num_seqs, int n_heads, int n_kv_heads, int head_dim,
                                  const PiecesGrid& grid);
@@ -45,6 +45,13 @@ pkv_status check_paged_decode(const void* out, pkv_dtype out_dtype, const void* 
                               float scale, int max_context_len);
 
 pkv_status check_workspace(const void* workspace, size_t bytes, size_t need);
+
+// Fills p.
+void fill_piece_problem(PieceParams* p, const PiecesGrid& grid, void* out, pkv_dtype out_dtype,
+                        const void* q, const int32_t* block_tables, int max_blocks_per_seq,
+                        const int32_t* context_lens, int num_seqs, int n_heads, int n_kv_heads,
+                        int block_size, int num_blocks, float scale, int max_context_len,
+                        const PiecesWorkspace& w, void* workspace, const DeviceInfo& dev);
 
 // Fills p and the chunk maps.
 pkv_status fill_pieces(PieceParams* p, CUtensorMap* tm_k, CUtensorMap* tm_v,

@@ -1,0 +1,117 @@
+// q8_capi.cu -- the C ABI's attention over 8-bit pages (paged_attn_decode_q8):
+// validation, workspace layout and launches.  Declarations and contracts:
+// pagedkv.h.
+#include <cudaTypedefs.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "capi_host.h"
+#include "decode_launch.h"
+#include "decode_q8_launch.h"
+#include "pieces_host.h"
+
+using namespace pkv::host;
+
+namespace {
+
+// The pool [num_blocks, B, Hk, D] of bytes as a 4-D tensor: dims (D, B, Hk,
+// blocks), box (D, 16, 1, 1), swizzled over D bytes: one load brings 16 tokens of
+// one kv head as [16][D].
+cudaError_t encode_q8_map(CUtensorMap* map, const void* pool, int num_blocks, int block_size,
+                          int n_kv_heads, int head_dim) {
+    auto encode = tensor_map_encoder();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint64_t D = (cuuint64_t)head_dim, row = D * n_kv_heads;
+    cuuint64_t dims[4] = {D, (cuuint64_t)block_size, (cuuint64_t)n_kv_heads,
+                          (cuuint64_t)num_blocks};
+    cuuint64_t strides[3] = {row, D, (cuuint64_t)block_size * row};
+    cuuint32_t box[4] = {(cuuint32_t)head_dim, 16, 1, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(pool), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+PiecesGrid q8_grid(int num_seqs, int n_kv_heads, int max_context_len, int sm_count) {
+    return pieces_grid(num_seqs, n_kv_heads, max_context_len, sm_count, true, pkv::kQ8Tokens);
+}
+
+pkv_status check_scales(const float* k_scale, const float* v_scale, int num_blocks) {
+    if (num_blocks > 0 && (!k_scale || !v_scale)) return invalid("k_scale or v_scale is NULL");
+    if (!aligned4(k_scale) || !aligned4(v_scale)) return invalid("scales must be 4-byte aligned");
+    return PKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+PKV_API size_t pkv_decode_q8_workspace_bytes(int num_seqs, int n_heads, int n_kv_heads,
+                                             int head_dim, int block_size, int max_context_len) {
+    if (!supported_shape(n_heads, n_kv_heads, head_dim, block_size) || num_seqs <= 0 ||
+        max_context_len < 0)
+        return 0;
+    DeviceInfo* dev = nullptr;
+    const int sms = device_info(&dev) == cudaSuccess ? dev->sm_count : kDefaultSms;
+    return pieces_workspace(num_seqs, n_heads, n_kv_heads, head_dim,
+                            q8_grid(num_seqs, n_kv_heads, max_context_len, sms))
+        .end;
+}
+
+PKV_API pkv_status paged_attn_decode_q8(
+    void* out, pkv_dtype out_dtype, const void* q, pkv_dtype q_dtype, const void* k_pool,
+    const void* v_pool, const float* k_scale, const float* v_scale, const int32_t* block_tables,
+    int max_blocks_per_seq, const int32_t* context_lens, int num_seqs, int n_heads,
+    int n_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
+    int max_context_len, void* workspace, size_t workspace_bytes, void* stream) {
+    pkv_status st = check_paged_decode(out, out_dtype, q, k_pool, v_pool, q_dtype, block_tables,
+                                       max_blocks_per_seq, context_lens, num_seqs, n_heads,
+                                       n_kv_heads, head_dim, block_size, num_blocks, scale,
+                                       max_context_len);
+    if (st != PKV_OK || num_seqs == 0) return st;
+    if ((st = check_scales(k_scale, v_scale, num_blocks)) != PKV_OK) return st;
+    DeviceInfo* dev = nullptr;
+    cudaError_t e = device_info(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    const PiecesGrid pieces = q8_grid(num_seqs, n_kv_heads, max_context_len, dev->sm_count);
+    const PiecesWorkspace w =
+        pieces_workspace(num_seqs, n_heads, n_kv_heads, head_dim, pieces);
+    if ((st = check_workspace(workspace, workspace_bytes, w.end)) != PKV_OK) return st;
+    pkv::Q8Launch L;
+    std::memset(&L, 0, sizeof(L));
+    L.stream = static_cast<cudaStream_t>(stream);
+    // (without blocks nothing is loaded; the maps need some valid tensor)
+    const int map_blocks = num_blocks > 0 ? num_blocks : 1;
+    if ((e = encode_q8_map(&L.tm_k, num_blocks > 0 ? k_pool : q, map_blocks, block_size,
+                           n_kv_heads, head_dim)) ||
+        (e = encode_q8_map(&L.tm_v, num_blocks > 0 ? v_pool : q, map_blocks, block_size,
+                           n_kv_heads, head_dim)))
+        return cuda_fail(e);
+    pkv::Q8Params& p = L.p;
+    fill_piece_problem(&p, pieces, out, out_dtype, q, block_tables, max_blocks_per_seq,
+                       context_lens, num_seqs, n_heads, n_kv_heads, block_size, num_blocks, scale,
+                       max_context_len, w, workspace, *dev);
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    e = q_dtype == PKV_BF16 ? pkv::launch_decode_q8_bf16(head_dim, L)
+                            : pkv::launch_decode_q8_f16(head_dim, L);
+    if (e != cudaSuccess) return cuda_fail(e);
+    // (pieces of a row to expect, and warps that merge them: as the shared decode)
+    const long long streams =
+        (long long)(p.ctas + p.extra_ctas) * (pkv::kPieceWarps / p.stream_heads);
+    const long long pairs = (long long)num_seqs * (n_kv_heads / p.stream_heads);
+    const bool few = 2 + streams / pairs <= 12;
+    const int rows = few ? pkv::kFinishWarps : 1;
+    const dim3 grid((unsigned)((n_heads + rows - 1) / rows), (unsigned)num_seqs);
+    auto merge = head_dim == 128
+                     ? (few ? pkv::decode_q8_finish_kernel<128, 1> : pkv::decode_q8_finish_kernel<128, 4>)
+                     : (few ? pkv::decode_q8_finish_kernel<64, 1> : pkv::decode_q8_finish_kernel<64, 4>);
+    e = launch_dependent(merge, grid, pkv::kFinishThreads, 0, L.stream,
+                         static_cast<const pkv::PieceParams&>(p));
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e);
+}
+
+}  // extern "C"

@@ -109,3 +109,65 @@ def append_q8(pool, scale, x, err, slots):
                 2 * torch.maximum(new[:, h].abs() * 2.0 ** -4, torch.tensor(s * 2.0 ** -10)).double()
                 + err[run][:, h], torch.zeros_like(err[run][:, h]))
     return pool, scale, bound, doubt
+
+
+def paged(lens, B, Hk, D, seed, scales="plain", extra_blocks=3):
+    """An 8-bit paged cache, poisoned: rows that no context covers are NaN, and so
+    are the scales of unused blocks.  scales: "plain" (near 1/200), "wide" (2^-16 ..
+    2^8, drawn per block and head), "powers".  Returns dict(k, v: per sequence the
+    float64 values [n, Hk, D]; kp, vp, ks, vs, tables, lens on the GPU)."""
+    g = torch.Generator().manual_seed(seed)
+    pages = [(n + B - 1) // B for n in lens]
+    blocks = sum(pages) + extra_blocks
+    perm = torch.randperm(blocks, generator=g).tolist()
+    tables = torch.full((len(lens), max(pages + [1])), -1, dtype=torch.int32)
+    out = {}
+    for name in ("k", "v"):
+        codes = round_e4m3(torch.randn(blocks, B, Hk, D, generator=g).double() * 100)
+        if scales == "plain":
+            scale = (torch.rand(blocks, Hk, generator=g) + 0.5) / 100
+        elif scales == "wide":
+            scale = (torch.rand(blocks, Hk, generator=g) * 24 - 16).exp2()
+            if name == "k":
+                scale = scale.clamp(max=2.0 ** -6)
+        else:
+            scale = torch.randint(-9, -5, (blocks, Hk), generator=g).float().exp2()
+        out[name] = (codes, scale)
+    vals = {"k": [], "v": []}
+    held = torch.zeros(blocks, B, dtype=torch.bool)
+    at = 0
+    for s, n in enumerate(lens):
+        ids = perm[at:at + pages[s]]
+        at += pages[s]
+        tables[s, :pages[s]] = torch.tensor(ids, dtype=torch.int32)
+        t = torch.arange(n)
+        b = torch.tensor(ids + [0])[t // B] if n else torch.zeros(0, dtype=torch.long)
+        held[b, t % B] = True
+        for name in ("k", "v"):
+            codes, scale = out[name]
+            vals[name].append(codes[b, t % B] * scale[b].double()[..., None])
+    for name in ("k", "v"):
+        codes, scale = out[name]
+        codes[~held] = math.nan
+        scale[~held.any(1)] = math.nan
+    return dict(k=vals["k"], v=vals["v"], kp=out["k"][0].to(torch.float8_e4m3fn).cuda(),
+                vp=out["v"][0].to(torch.float8_e4m3fn).cuda(), ks=out["k"][1].cuda(),
+                vs=out["v"][1].cuda(), tables=tables.cuda(),
+                lens=torch.tensor(lens, dtype=torch.int32).cuda())
+
+
+def attend_bound(q, k, v, scale, out_dtype, hidden=None, once=False):
+    """64-bit attention of q [R, D] over values k, v [n, D], and the largest error of
+    an output element (cache_ref's, with fp16 weights of p b / b_ref: two roundings
+    more, and steps of 2^-36 of the largest p b, times codes up to 448; `once`: one
+    fp16 part, half an eps of each weight)."""
+    from tests import cache_ref as ref
+    o, p, A, d = ref.attend(q, k, v, scale, hidden)
+    if k.shape[0] == 0:
+        return o, torch.zeros_like(o)
+    bound = ref.out_bound(o, A, d + 2.0 ** -23, torch.float16, out_dtype, once)
+    # (a code is up to 448 times its block's scale; p v covers p b |code|, so the
+    # largest p b is at most the largest p |v| / 2^-9 -- bounded here by the rows')
+    top = (p[:, :, None] * v.abs().amax(-1)[None, :, None]).amax(1)
+    step = k.shape[0] * 2.0 ** -36 * 448 * (2.0 ** 12 if once else 1)
+    return o, bound + step * top
