@@ -754,6 +754,37 @@ PKV_API pkv_status paged_attn_decode_q8(
     int max_context_len, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * paged_attn_multi_query_q8 -- paged_attn_multi_query over a cache of 8 bits (codes
+ * and scales as paged_attn_decode_q8): row i of sequence s sits at position p =
+ * context_lens[s] - q_len + i and sees the tokens t <= p, its own among them, already
+ * in the pool (kv_append_rope_q8).
+ *
+ *   out, q       device [total_q, n_heads, head_dim]; q of q_dtype (F16 or BF16), out
+ *                of out_dtype (F16, BF16, F32); 16-byte aligned; rows of no sequence
+ *                are not written
+ *   q_start      device int32 [num_seqs + 1], non-decreasing, q_start[0] >= 0,
+ *                q_start[num_seqs] <= total_q
+ *   max_q_len, max_context_len  host-side bounds of q_len and context_lens
+ *   other arguments as paged_attn_decode_q8.
+ * A sequence whose q_len is negative, above its context, above max_q_len or whose
+ * context exceeds max_context_len (rounded up to whole blocks) or the table is left
+ * out (its rows are not written) and flagged PKV_DEVERR_CONTEXT.  Tokens in a block
+ * outside the pool are left out and flagged PKV_DEVERR_BLOCK_ID; a row that sees no
+ * other gets zeros.  NaN in V reaches only the rows that see it.
+ * Softmax weights enter the second product rounded once to F16 (F32 outputs: two
+ * parts).  Sums over very long contexts come out short by up to 2^-23 per 16 keys.
+ * Supported shapes as paged_attn_decode; at most 65535 sequences, 4096 query heads.
+ * On tcgen05, 256 rows (tokens x query heads of a kv head) at a time.  One launch, no
+ * workspace.
+ */
+PKV_API pkv_status paged_attn_multi_query_q8(
+    void* out, pkv_dtype out_dtype, const void* q, pkv_dtype q_dtype, const int32_t* q_start,
+    int total_q, int max_q_len, const void* k_pool, const void* v_pool, const float* k_scale,
+    const float* v_scale, const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* context_lens, int num_seqs, int n_heads, int n_kv_heads, int head_dim,
+    int block_size, int num_blocks, float scale, int max_context_len, void* stream);
+
+/*
  * swap_blocks -- batched block copy ([SWAP] swap_blocks; [OPT] "Swap Blocks
  * 机制", one call per cache: Key, then Value):
  *

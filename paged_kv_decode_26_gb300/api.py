@@ -838,6 +838,37 @@ def paged_attn_decode_q8(out: torch.Tensor, q: torch.Tensor, k_pool: torch.Tenso
     return out
 
 
+def paged_attn_multi_query_q8(out: torch.Tensor, q: torch.Tensor, q_start: torch.Tensor,
+                              k_pool: torch.Tensor, v_pool: torch.Tensor, k_scale: torch.Tensor,
+                              v_scale: torch.Tensor, block_tables: torch.Tensor,
+                              context_lens: torch.Tensor, scale: float, max_q_len: int,
+                              max_context_len: int,
+                              stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """paged_attn_multi_query over float8_e4m3fn pools with scales fp32
+    [num_blocks, Hk] for each block and kv head; q is 16-bit."""
+    _need_here(_DECODE_NAMES + ("q_start", "k_scale", "v_scale"),
+               (out, q, k_pool, v_pool, block_tables, context_lens, q_start, k_scale, v_scale))
+    _need_ints(("q_start", "block_tables", "context_lens"), (q_start, block_tables, context_lens))
+    T, H, D = q.shape
+    nb, B, Hk, D2 = k_pool.shape
+    S = context_lens.shape[0]
+    if (D2 != D or v_pool.shape != k_pool.shape or out.shape != q.shape
+            or k_pool.dtype is not torch.float8_e4m3fn or v_pool.dtype is not torch.float8_e4m3fn
+            or k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32
+            or k_scale.shape != (nb, Hk) or v_scale.shape != (nb, Hk)
+            or block_tables.dim() != 2 or block_tables.shape[0] != S
+            or context_lens.dim() != 1 or q_start.shape != (S + 1,)):
+        raise ValueError("inconsistent shapes or dtypes")
+    st = lib().paged_attn_multi_query_q8(
+        out.data_ptr(), _DT[out.dtype], q.data_ptr(), _DT[q.dtype], q_start.data_ptr(), T,
+        int(max_q_len), k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(),
+        v_scale.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
+        context_lens.data_ptr(), S, H, Hk, D, B, nb, float(scale), int(max_context_len),
+        _stream_handle(stream))
+    check(st, "paged_attn_multi_query_q8")
+    return out
+
+
 def swap_blocks(dst_pool: torch.Tensor, src_pool: torch.Tensor, pairs: torch.Tensor,
                 stream: Optional[torch.cuda.Stream] = None) -> None:
     """dst_pool[j] = src_pool[i] for each (i, j) row of `pairs` (int64 [n, 2]).

@@ -1,0 +1,597 @@
+// multi_query_q8_kernel.cuh -- causal attention of several new tokens per
+// sequence over 8-bit pages (e4m3 with a scale per block and kv head) on tcgen05
+// (sm_103a): paged_attn_multi_query_q8.
+//
+// Mathematics: with codes k_t, v_t and the scales a_t, b_t of token t's block,
+// scores x_t = scale log2(e) a_t (q . k_t), weights w_t = 2^(x_t - M) b_t, O = sum
+// w_t v_t and L = sum w_t / b_t; the result is O / L.
+//
+// Tiles: 128 rows are 128 / G query tokens x the G query heads of a kv head; a CTA
+// has two row tiles (256 rows) that share every key tile of 128 keys: while the
+// softmax of one runs, the tensor core multiplies for the other.
+// Codes are exact in fp16, so both products are fp16 ones: warps 9-15 widen the
+// codes of K and V on their way from global to shared memory, 16 keys at a time in
+// turn, the next ones already in registers (no copy of the codes in shared memory:
+// the products' operands take most of its bandwidth).  Queries become fp16 too, each row
+// scaled by a power of two (exact but for elements 2^-38 below the row's largest).
+// A block's scales are one number per 16 keys: a_t multiplies the exponent's
+// factor, log2 b_t joins its addend, so they cost nothing per element; the sum L
+// takes the weights of 16 keys times 1 / b_t.
+//
+// Roles: warps 0-3 and 4-7 the softmax of tile 0 and 1, a thread per row; warp 8
+// issues every MMA; 9-15 load and widen K and V.
+//
+// Precision: S, M, L and O are fp32.  A weight is rounded once to fp16 before the
+// second product (fp32 outputs: two parts), lifted and bounded as in
+// weight_range.cuh; M = (m, log2 b_ref) with m the score and b_ref the scale of
+// the key with the largest weight when it was set.  O accumulates in the tensor
+// core, which drops what lies below its last bit: up to 2^-23 of O per 16 keys.
+#pragma once
+
+#include "attn_tc_kernel.cuh"
+#include "decode_q8_kernel.cuh"
+
+namespace pkv {
+
+constexpr int kMq8Keys = 128;
+constexpr int kMq8Rows = 128;
+constexpr int kMq8Threads = 512;      // 8 softmax warps, 1 MMA, 7 that widen
+constexpr int kMq8Widen = 7;
+constexpr int kMq8Ahead = 2;          // groups of 16 keys that a widening warp has under way
+// Registers per thread: 512 x 128 at launch
+constexpr int kMq8SoftmaxRegs = 184, kMq8OtherRegs = 72;
+static_assert(256 * kMq8SoftmaxRegs + 256 * kMq8OtherRegs <= kMq8Threads * 128, "registers");
+// Key tiles whose scales are kept: K of tile j + STAGES / 2 is widened as soon as
+// S_j is formed, while its softmax still reads the scales of tile j.
+constexpr int kMq8Scales = 8;
+
+struct Mq8Params : MultiQueryParams {
+    const void* k_pool;
+    const void* v_pool;
+    const float* k_scale;
+    const float* v_scale;
+    int q_bf16;
+};
+
+// Of a key tile's groups of 16 keys: a, log2 b and 1 / b, and whether there is a page.
+struct __align__(16) Mq8Scale {
+    float a[8], lb[8], ib[8];
+    unsigned char page[16];            // 8 of them: 1 or 0
+};
+
+template <int D>
+struct Mq8Sizes {
+    static constexpr int HALVES = D / 64;
+    static constexpr uint32_t KV_HALF = kMq8Keys * 128;
+    static constexpr uint32_t KV_BYTES = HALVES * KV_HALF;     // a widened K or V tile
+    static constexpr uint32_t Q_HALF = kMq8Rows * 128;
+    static constexpr uint32_t Q_BYTES = HALVES * Q_HALF;
+    static constexpr int STAGES = D == 128 ? 4 : 8;
+    static constexpr uint32_t TILE_COLS = 256;                 // per row tile: O, then S / P
+    static constexpr uint32_t S_COL = D;
+    static_assert(STAGES / 2 < kMq8Scales, "scales");
+    static constexpr size_t SMEM = 1024 + 2 * Q_BYTES + STAGES * KV_BYTES +
+                                   kMq8Scales * sizeof(Mq8Scale) + (2 * STAGES + 12) * 8 + 16;
+};
+
+// 16 codes to two chunks of 8 fp16.
+__device__ __forceinline__ void mq8_widen(const uint4& w, uint4& a, uint4& b) {
+    q8_widen(w.x, a.x, a.y);
+    q8_widen(w.y, a.z, a.w);
+    q8_widen(w.z, b.x, b.y);
+    q8_widen(w.w, b.z, b.w);
+}
+
+// Byte mask of the NaN codes (0x7f, 0xff) of a word.
+__device__ __forceinline__ uint32_t mq8_nans(uint32_t w) {
+    return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+}
+
+// The softmax's reference of a row.
+struct Mq8Reference {
+    float m = -INFINITY;      // a score
+    float lb = 0.f;           // log2 of a scale
+};
+
+template <int D, int BS, int PARTS>
+__global__ void __launch_bounds__(kMq8Threads, 1)
+    multi_query_q8_kernel(const __grid_constant__ Mq8Params p) {
+    using Z = Mq8Sizes<D>;
+    using Range = WeightRange<__half>;
+    constexpr int STAGES = Z::STAGES;
+    constexpr int UNITS = D / 16;                  // 16-code units of a row
+    constexpr int kParts = 16 * UNITS / 32;        // a lane's units of 16 rows
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    unsigned char* sm = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    unsigned char* sQ = sm;
+    unsigned char* sKV = sQ + 2 * Z::Q_BYTES;
+    Mq8Scale* s_scale = reinterpret_cast<Mq8Scale*>(sKV + STAGES * Z::KV_BYTES);
+    uint64_t* kv_full = reinterpret_cast<uint64_t*>(s_scale + kMq8Scales);
+    uint64_t* kv_free = kv_full + STAGES;
+    uint64_t* q_full = kv_free + STAGES;          // [tile]
+    uint64_t* s_full = q_full + 2;
+    uint64_t* p_full = s_full + 2;                // [tile][half of the keys]
+    uint64_t* o_full = p_full + 4;
+    uint64_t* fin = o_full + 2;
+    int* s_tmem = reinterpret_cast<int*>(fin + 2);
+    int* s_poison = s_tmem + 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    int tile = blockIdx.x, kvh = blockIdx.y, s = blockIdx.z;
+    if (p.lpt_seqs > 0) {
+        longest_first(p, reinterpret_cast<int*>(sKV), tile, kvh, s);   // (sKV: not yet in use)
+        __syncthreads();
+    }
+    const int G = p.group, QT = kMq8Rows / G;
+    const int qs0 = p.q_start[s], qs1 = p.q_start[s + 1];
+    const int n = p.context_lens[s];
+    const int q_len = qs1 - qs0;
+    if (q_len < 0 || q_len > n || qs0 < 0 || qs1 > p.total_q || q_len > p.max_q_len ||
+        n > (long long)p.max_pages * BS || n > (long long)p.max_blocks_per_seq * BS) {
+        if (tile == 0 && kvh == 0 && threadIdx.x == 0) raise_error(p.errors, PKV_DEVERR_CONTEXT);
+        return;
+    }
+    const int tok_lo = tile * 2 * QT;
+    if (tok_lo >= q_len) return;
+    const int pos0 = n - q_len + tok_lo;             // position of row tile 0's first token
+    const int rows = min(q_len - tok_lo, 2 * QT);    // tokens of this CTA
+    const int n_keys = pos0 + rows;                  // keys that some row sees
+    const int nt0 = (pos0 + min(rows, QT) + kMq8Keys - 1) / kMq8Keys;
+    const int nt1 = rows > QT ? (n_keys + kMq8Keys - 1) / kMq8Keys : 0;
+    const int n_tiles = max(nt0, nt1);
+
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_addr(s_tmem)),
+                     "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(&kv_full[i], 8);
+            mbar_init(&kv_free[i], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&q_full[t], 4);
+            mbar_init(&s_full[t], 1);
+            mbar_init(&p_full[2 * t], 4);
+            mbar_init(&p_full[2 * t + 1], 4);
+            mbar_init(&o_full[t], 1);
+            mbar_init(&fin[t], 1);
+        }
+        *s_poison = 0;
+        fence_barrier_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = (uint32_t)*s_tmem;
+
+    // (every warp of a warpgroup by the same instruction)
+    if (warp >= 8)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMq8OtherRegs));
+    else
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMq8SoftmaxRegs));
+    if (warp == 8) {
+        // ================= every MMA =================
+        const uint32_t id_s = tc_idesc<__half>(kMq8Rows, kMq8Keys, 0);
+        const uint32_t id_o = tc_idesc<__half>(kMq8Rows, D, 1);
+        const uint64_t dq0 = tc_desc_sw128(smem_addr(sQ), 16, 1024);
+        const uint64_t dk0 = tc_desc_sw128(smem_addr(sKV), 16, 1024);
+        const uint64_t dv0 = tc_desc_sw128(smem_addr(sKV), Z::KV_HALF, 1024);
+        const uint32_t lead = elect_one() ? 1u : 0u;
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u, p.errors));
+        };
+        // operand i of the ring (K_0, V_0, K_1, V_1, ...)
+        auto slot = [&](int i) { return i % STAGES; };
+        auto round = [&](int i) { return (uint32_t)(i / STAGES); };
+        auto issue_s = [&](int t, int j) {
+            if (j == 0) wait(&q_full[t], 0);
+            wait(&kv_full[slot(2 * j)], round(2 * j));
+            if (!ok) return;
+            tc_fence_after();
+            const uint64_t q = dq0 + (uint64_t)((t * Z::Q_BYTES) >> 4);
+            const uint64_t k = dk0 + (uint64_t)(slot(2 * j) * (Z::KV_BYTES >> 4));
+            const uint32_t d = tmem + t * Z::TILE_COLS + Z::S_COL;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+                at_mma(d, q + (((i / 4) * Z::Q_HALF + (i % 4) * 32) >> 4),
+                       k + (((i / 4) * Z::KV_HALF + (i % 4) * 32) >> 4), id_s, i > 0 ? 1u : 0u,
+                       lead);
+            at_commit(&s_full[t], lead);
+            __syncwarp();
+        };
+        for (int t = 0; t < 2; ++t)
+            if (ok && (t ? nt1 : nt0) > 0) issue_s(t, 0);
+        if (ok) at_commit(&kv_free[slot(0)], lead);
+        __syncwarp();
+        for (int j = 0; ok && j < n_tiles; ++j) {
+            const int vs = slot(2 * j + 1);
+            wait(&kv_full[vs], round(2 * j + 1));
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int nt = t ? nt1 : nt0;
+                if (!ok || j >= nt) continue;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    wait(&p_full[2 * t + half], (uint32_t)j);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t o = tmem + t * Z::TILE_COLS;
+                    const uint64_t v = dv0 + (uint64_t)(vs * (Z::KV_BYTES >> 4));
+#pragma unroll
+                    for (int part = PARTS - 1; part >= 0; --part)
+#pragma unroll
+                        for (int i = half * 4; i < half * 4 + 4; ++i)
+                            at_mma_tmem_a(o, o + Z::S_COL + part * 64 + i * 8,
+                                          v + (uint64_t)((i * 16 * 128) >> 4), id_o,
+                                          (j > 0 || i > 0 || part < PARTS - 1) ? 1u : 0u, lead);
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (j + 1 == nt)
+                    at_commit(&o_full[t], lead);
+                else
+                    issue_s(t, j + 1);
+            }
+            if (!ok) break;
+            at_commit(&kv_free[vs], lead);
+            if (j + 1 < n_tiles) at_commit(&kv_free[slot(2 * j + 2)], lead);
+            __syncwarp();
+        }
+        // every MMA complete before the tensor memory is released
+        at_commit(&fin[0], lead);
+        __syncwarp();
+        mbar_wait(&fin[0], 0, p.errors);
+        __syncwarp();
+    } else if (warp > 8) {
+        // ================= K and V, widened =================
+        // task k: keys 16 (k % 8) .. + 15 of operand k / 8 (K_0, V_0, K_1, ...)
+        const int n_tasks = 16 * n_tiles;
+        const int* table = p.block_tables + (size_t)s * p.max_blocks_per_seq;
+        const int guard_from = (pos0 + 1) / kMq8Keys;      // first tile that not every row sees all of
+        const size_t row_bytes = (size_t)p.n_kv_heads * D;
+        const int r0 = lane / UNITS, u = lane % UNITS;     // row and unit of this lane's part 0
+        auto first_key = [&](int k) { return (k / 16) * kMq8Keys + (k % 8) * 16; };
+        // block of a task's keys, -1: none
+        auto block_of = [&](int k) -> int {
+            const int key = first_key(k);
+            if (k >= n_tasks || key >= n_keys) return -1;
+            const int b = __ldg(table + key / BS);
+            if (b >= 0 && b < p.num_blocks) return b;
+            raise_error(p.errors, PKV_DEVERR_BLOCK_ID);
+            return -1;
+        };
+        struct Task {
+            uint4 codes[kParts];
+            float scale;                 // lane 0: of the keys, lane 1: of the values
+            int block;
+        };
+        auto fetch = [&](Task& t, int k, int block) {
+            const int key0 = first_key(k), op = (k / 8) & 1;
+            t.block = block;
+            t.scale = 0.f;
+            if (block >= 0 && op == 0 && lane < 2)
+                t.scale = __ldg((lane ? p.v_scale : p.k_scale) + (size_t)block * p.n_kv_heads + kvh);
+            const unsigned char* from =
+                static_cast<const unsigned char*>(op ? p.v_pool : p.k_pool) +
+                ((size_t)max(block, 0) * BS + key0 % BS + r0) * row_bytes + (size_t)kvh * D + u * 16;
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) {
+                const int row = r0 + i * (32 / UNITS);
+                t.codes[i] = block >= 0 && key0 + row < n_keys
+                                 ? __ldg(reinterpret_cast<const uint4*>(
+                                       from + (size_t)i * (32 / UNITS) * row_bytes))
+                                 : make_uint4(0u, 0u, 0u, 0u);
+            }
+        };
+        Task task[kMq8Ahead];
+        int k = warp - 9;
+#pragma unroll
+        for (int i = 0; i < kMq8Ahead; ++i) fetch(task[i], k + i * kMq8Widen, block_of(k + i * kMq8Widen));
+        int block = block_of(k + kMq8Ahead * kMq8Widen);
+        bool ok = true;
+        while (ok && k < n_tasks) {
+#pragma unroll
+            for (int i = 0; i < kMq8Ahead; ++i) {
+                if (!ok || k >= n_tasks) break;
+                Task& now = task[i];
+                const int i_op = k / 8, st = i_op % STAGES, g = k % 8, j = k / 16;
+                if (i_op >= STAGES)
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait(&kv_free[st], (uint32_t)(i_op / STAGES - 1) & 1u,
+                                              p.errors));
+                if (!ok) break;
+                if ((i_op & 1) == 0) {
+                    Mq8Scale& e = s_scale[j % kMq8Scales];
+                    if (lane == 0) {
+                        e.a[g] = now.scale;
+                        e.page[g] = now.block >= 0;
+                    } else if (lane == 1) {
+                        // (NaN stays)
+                        const float b = now.scale < kQ8LeastScale ? kQ8LeastScale : now.scale;
+                        e.lb[g] = __log2f(b);
+                        e.ib[g] = __frcp_rn(b);
+                    }
+                }
+                unsigned char* dst = sKV + (size_t)st * Z::KV_BYTES;
+                const bool guard = (i_op & 1) && j >= guard_from;
+#pragma unroll
+                for (int n = 0; n < kParts; ++n) {
+                    const int row = g * 16 + r0 + n * (32 / UNITS);
+                    uint4 w = now.codes[n];
+                    if (guard) {
+                        const uint4 bad = make_uint4(mq8_nans(w.x), mq8_nans(w.y), mq8_nans(w.z),
+                                                     mq8_nans(w.w));
+                        if (bad.x | bad.y | bad.z | bad.w) *s_poison = 1;
+                        w = make_uint4(w.x & ~bad.x, w.y & ~bad.y, w.z & ~bad.z, w.w & ~bad.w);
+                    }
+                    uint4 a, b;
+                    mq8_widen(w, a, b);
+                    // chunks 2 u, 2 u + 1 of the row; where eight lanes share a row those
+                    // of the upper dims take theirs in the other order, so that they
+                    // write to eight bank groups
+                    const int h = u / 4, c0 = (u % 4) * 2, sw = row & 7;
+                    unsigned char* at_row = dst + h * Z::KV_HALF + row * 128;
+                    const bool swap = D == 128 && h == 1;
+                    *reinterpret_cast<uint4*>(at_row + (((c0 + swap) ^ sw) << 4)) = swap ? b : a;
+                    *reinterpret_cast<uint4*>(at_row + (((c0 + !swap) ^ sw) << 4)) = swap ? a : b;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&kv_full[st]);
+                const int next = k + kMq8Ahead * kMq8Widen;
+                fetch(now, next, block);
+                block = block_of(next + kMq8Widen);
+                k += kMq8Widen;
+            }
+        }
+    } else {
+        // ================= softmax: thread r of group t owns row r of tile t =================
+        const int t = warp >> 2;
+        const int r = (warp & 3) * 32 + lane;
+        const int nt = t ? nt1 : nt0;
+        if (nt > 0) {
+            const int tok = t * QT + r / G;
+            const bool real = tok < rows;
+            const int pos = real ? pos0 + tok : -1;        // last key of this row
+            const int warp_pos = pos0 + t * QT + ((warp & 3) * 32) / G;
+            const size_t row = (size_t)(qs0 + tok_lo + (real ? tok : 0)) * p.n_heads + kvh * G + r % G;
+            // ---- the query row, as fp16
+            float qf = p.scale_log2;
+            {
+                const uint4* q4 = reinterpret_cast<const uint4*>(p.q) + row * (D / 8);
+                uint4 w[D / 8];
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) w[i] = real ? __ldg(q4 + i) : make_uint4(0u, 0u, 0u, 0u);
+                if (p.q_bf16) {
+                    float top = 0.f;
+                    uint32_t* x = reinterpret_cast<uint32_t*>(w);
+#pragma unroll
+                    for (int i = 0; i < D / 2; ++i) {
+                        const float2 f = unpack2<__nv_bfloat16>(x[i]);
+                        top = fabsf(f.x) < INFINITY ? fmaxf(top, fabsf(f.x)) : top;
+                        top = fabsf(f.y) < INFINITY ? fmaxf(top, fabsf(f.y)) : top;
+                    }
+                    const int e = min(max((int)(__float_as_uint(top) >> 23), 24), 254);
+                    const float to = __uint_as_float((uint32_t)(127 + 14 + 127 - e) << 23);
+                    qf *= __uint_as_float((uint32_t)(e - 14) << 23);
+#pragma unroll
+                    for (int i = 0; i < D / 2; ++i) {
+                        const float2 f = unpack2<__nv_bfloat16>(x[i]);
+                        x[i] = pack2<__half>(f.x * to, f.y * to);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+                    *reinterpret_cast<uint4*>(sQ + t * Z::Q_BYTES + (i / 8) * Z::Q_HALF + r * 128 +
+                                              (((i % 8) ^ (r & 7)) << 4)) = w[i];
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_full[t]);
+            }
+            const uint32_t t_lane = tmem + t * Z::TILE_COLS + ((uint32_t)((warp & 3) * 32) << 16);
+            Mq8Reference ref;
+            // scores formed ahead of the maximum: where their factor is not positive,
+            // or a row's are so large that y a + add would lose what matters
+            bool formed = !(p.scale_log2 > 0.f);
+            float l = 0.f;
+            bool ok = true;
+            for (int j = 0; j < nt;) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], (uint32_t)j & 1u, p.errors));
+                if (!ok) break;
+                tc_fence_after();
+                float y[kMq8Keys];
+                uint32_t* yr = reinterpret_cast<uint32_t*>(y);
+                tc_ld32(t_lane + Z::S_COL, yr);
+                tc_ld32(t_lane + Z::S_COL + 32, yr + 32);
+                tc_ld32(t_lane + Z::S_COL + 64, yr + 64);
+                tc_ld32(t_lane + Z::S_COL + 96, yr + 96);
+                tc_wait_ld();
+                const Mq8Scale& sc = s_scale[j % kMq8Scales];
+                const int key0 = j * kMq8Keys;
+                const uint2 pages = *reinterpret_cast<const uint2*>(sc.page);
+                const bool whole = key0 + kMq8Keys - 1 <= warp_pos &&
+                                   (pages.x & pages.y) == 0x01010101u;
+                // factors of the groups (never 0: hidden keys are -inf below)
+                float a[8];
+                unsigned seen = 0xffu;            // groups that this row sees keys of
+                if (!whole) {
+                    seen = 0u;
+#pragma unroll
+                    for (int g = 0; g < 8; ++g)
+                        if (key0 + 16 * g <= pos && sc.page[g]) seen |= 1u << g;
+                }
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    const float f = sc.a[g] * qf;
+                    a[g] = fabsf(f) < 1.2e-38f ? 1.2e-38f : f;
+                    if (!((seen >> g) & 1u)) a[g] = 1.f;
+                }
+                if (formed) {
+#pragma unroll
+                    for (int c = 0; c < kMq8Keys; ++c) y[c] *= a[c / 16];
+#pragma unroll
+                    for (int g = 0; g < 8; ++g) a[g] = 1.f;
+                }
+                if (!whole) {
+                    const int lim = pos - key0;
+#pragma unroll
+                    for (int c = 0; c < kMq8Keys; ++c)
+                        y[c] = c <= lim && ((seen >> (c / 16)) & 1u) ? y[c] : -INFINITY;
+                }
+                // ---- the reference
+                bool beyond = false;
+                float top = -INFINITY, top_lb = 0.f;
+#pragma unroll
+                for (int g = 0; g < 8; ++g) {
+                    const float* v = y + 16 * g;
+                    float m = max3(max3(v[0], v[1], v[2]), max3(v[3], v[4], v[5]),
+                                   max3(v[6], v[7], v[8]));
+                    m = max3(m, max3(v[9], v[10], v[11]), max3(v[12], v[13], fmaxf(v[14], v[15])));
+                    const float x = __fmul_rn(m, a[g]), lb = ((seen >> g) & 1u) ? sc.lb[g] : 0.f;
+                    beyond |= (x - ref.m) + (lb - ref.lb) > Range::GROW;
+                    if (top == -INFINITY || (x - top) + (lb - top_lb) > 0.f) {
+                        top = x;
+                        top_lb = lb;
+                    }
+                }
+                if (__any_sync(0xffffffffu, beyond)) {
+                    if (!formed && __any_sync(0xffffffffu, real && beyond && fabsf(top) > 32768.f)) {
+                        formed = true;
+                        continue;                  // this tile once more (S is still there)
+                    }
+                    float alpha = 1.f;
+                    if (beyond) {
+                        if (ref.m != -INFINITY) alpha = exp2f((ref.m - top) + (ref.lb - top_lb));
+                        ref.m = top;
+                        ref.lb = top_lb;
+                    }
+                    if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                        // O is at rest: the products up to key tile j - 1
+                        // completed before S_j did
+                        const float2 a2 = make_float2(alpha, alpha);
+#pragma unroll 1
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            uint32_t ov[32];
+                            tc_ld32(t_lane + c0, ov);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 32; c += 2) {
+                                const float2 v = __fmul2_rn(
+                                    make_float2(__uint_as_float(ov[c]), __uint_as_float(ov[c + 1])),
+                                    a2);
+                                ov[c] = __float_as_uint(v.x);
+                                ov[c + 1] = __float_as_uint(v.y);
+                            }
+                            tc_st32(t_lane + c0, ov);
+                        }
+                        l *= alpha;
+                    }
+                }
+                const float mu = ref.m == -INFINITY ? 0.f : ref.m;
+                float base = Range::LIFT - ref.lb;
+                if (formed) {
+#pragma unroll
+                    for (int c = 0; c < kMq8Keys; ++c) y[c] -= mu;      // exact first
+                } else {
+                    base -= mu;
+                }
+                // ---- weights
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t w[PARTS][32];
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const int gg = half * 4 + g;
+                        const bool in = (seen >> gg) & 1u;
+                        const float add1 = in ? base + sc.lb[gg] : 0.f;
+                        const float2 mul = make_float2(a[gg], a[gg]), add = make_float2(add1, add1);
+                        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int k = gg * 16 + 2 * i;
+                            const float2 e = __ffma2_rn(make_float2(y[k], y[k + 1]), mul, add);
+                            const float2 pv = make_float2(exp2f(e.x), exp2f(e.y));
+                            sum = __fadd2_rn(sum, pv);
+                            w[0][g * 8 + i] = pack2<__half>(pv.x, pv.y);
+                            if (PARTS > 1) {
+                                const float2 rest = __ffma2_rn(unpack2<__half>(w[0][g * 8 + i]),
+                                                               make_float2(-1.f, -1.f), pv);
+                                w[PARTS - 1][g * 8 + i] = pack2<__half>(rest.x, rest.y);
+                            }
+                        }
+                        if (in) l = fmaf(sum.x + sum.y, sc.ib[gg], l);
+                    }
+#pragma unroll
+                    for (int k = 0; k < PARTS; ++k)
+                        tc_st32(t_lane + Z::S_COL + k * 64 + half * 32, w[k]);
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
+                }
+                ++j;
+            }
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&o_full[t], 0, p.errors));
+            if (ok) {
+                tc_fence_after();
+                const float inv = l != 0.f ? __frcp_rn(l) : 0.f;
+                const bool poison = *reinterpret_cast<volatile int*>(s_poison) != 0;
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    float o[32];
+                    tc_ld32(t_lane + c0, reinterpret_cast<uint32_t*>(o));
+                    tc_wait_ld();
+                    if (!real) continue;
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) o[c] *= inv;
+                    if (poison) {
+                        // NaN that was taken out of V, from the rows that see it
+#pragma unroll 1
+                        for (int key = pos0 / kMq8Keys * kMq8Keys; key <= pos; ++key) {
+                            const int b = p.block_tables[(size_t)s * p.max_blocks_per_seq + key / BS];
+                            if (b < 0 || b >= p.num_blocks) continue;
+                            const unsigned char* v =
+                                static_cast<const unsigned char*>(p.v_pool) +
+                                (((size_t)b * BS + key % BS) * p.n_kv_heads + kvh) * D + c0;
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if ((v[c] & 0x7f) == 0x7f) o[c] = NAN;
+                        }
+                    }
+                    const size_t at = row * D + c0;
+                    if (p.out_dtype == PKV_F32) {
+                        float4* o4 = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at);
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4)
+                            o4[c / 4] = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                    } else {
+                        uint4* o4 = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + at);
+#pragma unroll
+                        for (int c = 0; c < 32; c += 8)
+                            o4[c / 8] = make_uint4(pack_out(o[c], o[c + 1], p.out_dtype),
+                                                   pack_out(o[c + 2], o[c + 3], p.out_dtype),
+                                                   pack_out(o[c + 4], o[c + 5], p.out_dtype),
+                                                   pack_out(o[c + 6], o[c + 7], p.out_dtype));
+                    }
+                }
+            }
+        }
+    }
+
+    // ---- tensor memory is released after every thread is done with it
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(512u)
+                     : "memory");
+}
+
+}  // namespace pkv

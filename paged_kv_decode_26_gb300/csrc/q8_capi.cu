@@ -1,6 +1,6 @@
-// q8_capi.cu -- the C ABI's attention over 8-bit pages (paged_attn_decode_q8):
-// validation, workspace layout and launches.  Declarations and contracts:
-// pagedkv.h.
+// q8_capi.cu -- the C ABI's attention over 8-bit pages (paged_attn_decode_q8,
+// paged_attn_multi_query_q8): validation, workspace layout and launches.
+// Declarations and contracts: pagedkv.h.
 #include <cudaTypedefs.h>
 
 #include <cmath>
@@ -9,6 +9,7 @@
 #include "capi_host.h"
 #include "decode_launch.h"
 #include "decode_q8_launch.h"
+#include "multi_query_q8_launch.h"
 #include "pieces_host.h"
 
 using namespace pkv::host;
@@ -44,6 +45,10 @@ pkv_status check_scales(const float* k_scale, const float* v_scale, int num_bloc
     if (!aligned4(k_scale) || !aligned4(v_scale)) return invalid("scales must be 4-byte aligned");
     return PKV_OK;
 }
+
+// Longest context first (longest_first), as paged_attn_multi_query.
+constexpr int kLptMaxSeqs = 256;
+constexpr int kLptMinContext = 8192;
 
 }  // namespace
 
@@ -111,6 +116,62 @@ PKV_API pkv_status paged_attn_decode_q8(
                      : (few ? pkv::decode_q8_finish_kernel<64, 1> : pkv::decode_q8_finish_kernel<64, 4>);
     e = launch_dependent(merge, grid, pkv::kFinishThreads, 0, L.stream,
                          static_cast<const pkv::PieceParams&>(p));
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e);
+}
+
+PKV_API pkv_status paged_attn_multi_query_q8(
+    void* out, pkv_dtype out_dtype, const void* q, pkv_dtype q_dtype, const int32_t* q_start,
+    int total_q, int max_q_len, const void* k_pool, const void* v_pool, const float* k_scale,
+    const float* v_scale, const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* context_lens, int num_seqs, int n_heads, int n_kv_heads, int head_dim,
+    int block_size, int num_blocks, float scale, int max_context_len, void* stream) {
+    if (total_q < 0 || max_q_len < 0) return invalid("sizes");
+    const bool none = num_seqs == 0 || total_q == 0 || max_q_len == 0;
+    pkv_status st = check_paged_decode(out, out_dtype, q, k_pool, v_pool, q_dtype, block_tables,
+                                       max_blocks_per_seq, context_lens, none ? 0 : num_seqs,
+                                       n_heads, n_kv_heads, head_dim, block_size, num_blocks,
+                                       scale, max_context_len);
+    if (st != PKV_OK) return st;
+    if (num_seqs < 0) return invalid("sizes");
+    if (none) return PKV_OK;
+    if (!q_start) return invalid("q_start is NULL");
+    if (!aligned4(q_start)) return invalid("q_start must be 4-byte aligned");
+    if ((st = check_scales(k_scale, v_scale, num_blocks)) != PKV_OK) return st;
+    DeviceInfo* dev = nullptr;
+    cudaError_t e = device_info(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    const int G = n_heads / n_kv_heads;
+    pkv::Mq8Launch L;
+    std::memset(&L, 0, sizeof(L));
+    pkv::Mq8Params& p = L.p;
+    p.out = out;
+    p.out_dtype = out_dtype;
+    p.q = q;
+    p.q_bf16 = q_dtype == PKV_BF16;
+    p.q_start = q_start;
+    p.total_q = total_q;
+    p.max_q_len = max_q_len;
+    p.k_pool = k_pool;
+    p.v_pool = v_pool;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.block_tables = block_tables;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.context_lens = context_lens;
+    p.num_seqs = num_seqs;
+    p.n_heads = n_heads;
+    p.n_kv_heads = n_kv_heads;
+    p.group = G;
+    p.num_blocks = num_blocks;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.max_pages = (int)(((long long)max_context_len + block_size - 1) / block_size);
+    p.errors = dev->errors;
+    p.lpt_seqs = max_context_len >= kLptMinContext && num_seqs <= kLptMaxSeqs ? num_seqs : 0;
+    const int cta_tokens = 2 * pkv::kMq8Rows / G;
+    L.grid = dim3((unsigned)((max_q_len + cta_tokens - 1) / cta_tokens), (unsigned)n_kv_heads,
+                  (unsigned)num_seqs);
+    L.stream = static_cast<cudaStream_t>(stream);
+    e = pkv::launch_multi_query_q8(head_dim, block_size, L);
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
 }
 

@@ -156,18 +156,20 @@ def paged(lens, B, Hk, D, seed, scales="plain", extra_blocks=3):
                 lens=torch.tensor(lens, dtype=torch.int32).cuda())
 
 
-def attend_bound(q, k, v, scale, out_dtype, hidden=None, once=False):
+def attend_bound(q, k, v, scale, out_dtype, hidden=None, once=False, chained=False):
     """64-bit attention of q [R, D] over values k, v [n, D], and the largest error of
     an output element (cache_ref's, with fp16 weights of p b / b_ref: two roundings
     more, and steps of 2^-36 of the largest p b, times codes up to 448; `once`: one
-    fp16 part, half an eps of each weight)."""
+    fp16 part, half an eps of each weight; `chained`: O stays in the tensor core,
+    2^-23 of sum p |v| lost per 16 keys)."""
     from tests import cache_ref as ref
     o, p, A, d = ref.attend(q, k, v, scale, hidden)
     if k.shape[0] == 0:
         return o, torch.zeros_like(o)
     bound = ref.out_bound(o, A, d + 2.0 ** -23, torch.float16, out_dtype, once)
-    # (a code is up to 448 times its block's scale; p v covers p b |code|, so the
-    # largest p b is at most the largest p |v| / 2^-9 -- bounded here by the rows')
-    top = (p[:, :, None] * v.abs().amax(-1)[None, :, None]).amax(1)
-    step = k.shape[0] * 2.0 ** -36 * 448 * (2.0 ** 12 if once else 1)
-    return o, bound + step * top
+    # (paged()'s rows hold codes of 64 and more, so the largest p b is at most 1 / 64
+    # of the largest p |v|)
+    top = (p * v.abs().amax(-1)).amax(-1)[:, None]
+    if chained:
+        bound = bound + A * (k.shape[0] / 16 + 1) * 2.0 ** -23
+    return o, bound + k.shape[0] * 2.0 ** -36 * E4M3_MAX / 64 * top

@@ -56,3 +56,33 @@ def test_decode_workspace_bytes(L):
     # at least a partial row per (sequence, head)
     assert f(2, 8, 8, 128, 16, 100) >= 2 * 8 * (128 + 2) * 4
     assert f(3, 8, 8, 128, 16, 100) > f(2, 8, 8, 128, 16, 100)
+
+
+def _chunk(L, **kw):
+    a = dict(out=FAKE(1), od=1, q=FAKE(2), qd=1, qs=FAKE(10), T=8, maxq=4, k=FAKE(3), v=FAKE(4),
+             ks=FAKE(5), vs=FAKE(6), bt=FAKE(7), mb=4, cl=FAKE(8), S=2, H=8, Hk=8, D=128, B=16,
+             nb=10, scale=0.1, maxc=64)
+    a.update(kw)
+    return L.paged_attn_multi_query_q8(a["out"], a["od"], a["q"], a["qd"], a["qs"], a["T"],
+                                       a["maxq"], a["k"], a["v"], a["ks"], a["vs"], a["bt"],
+                                       a["mb"], a["cl"], a["S"], a["H"], a["Hk"], a["D"], a["B"],
+                                       a["nb"], a["scale"], a["maxc"], NULL)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(S=-1), 1), (dict(S=65536), 2), (dict(T=-1), 1), (dict(maxq=-1), 1), (dict(maxc=-1), 1),
+    (dict(H=6, Hk=4), 1), (dict(D=96), 2), (dict(B=8), 2), (dict(H=48, Hk=4), 2), (dict(qd=2), 2),
+    (dict(od=7), 1), (dict(nb=-1), 1), (dict(k=NULL), 1), (dict(mb=0), 1),
+    (dict(scale=float("inf")), 1), (dict(q=NULL), 1), (dict(qs=NULL), 1),
+    (dict(qs=C.c_void_p(4098)), 1), (dict(cl=NULL), 1), (dict(ks=NULL), 1), (dict(vs=NULL), 1),
+    (dict(vs=C.c_void_p(4098)), 1), (dict(out=C.c_void_p(4104)), 1), (dict(v=C.c_void_p(4104)), 1),
+    (dict(mb=1 << 27, B=32), 2),
+])
+def test_chunk_refusals(L, kw, code):
+    assert _chunk(L, **kw) == code
+    assert L.pkv_last_error_detail()
+
+
+@pytest.mark.parametrize("kw", [dict(S=0), dict(T=0), dict(maxq=0)])
+def test_chunk_of_nothing_is_a_no_op(L, kw):
+    assert _chunk(L, q=NULL, ks=NULL, **kw) == 0
