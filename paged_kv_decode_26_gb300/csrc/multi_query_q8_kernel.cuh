@@ -82,16 +82,25 @@ __device__ __forceinline__ void mq8_widen(const uint4& w, uint4& a, uint4& b) {
     q8_widen(w.w, b.z, b.w);
 }
 
+// 16 bytes that nothing on this SM reads again.
+__device__ __forceinline__ uint4 mq8_load(const void* p) {
+    uint4 v;
+    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+        : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ void mq8_store(uint32_t at, const uint4& v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y),
+                 "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
 // Byte mask of the NaN codes (0x7f, 0xff) of a word.
 __device__ __forceinline__ uint32_t mq8_nans(uint32_t w) {
     return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
 }
-
-// The softmax's reference of a row.
-struct Mq8Reference {
-    float m = -INFINITY;      // a score
-    float lb = 0.f;           // log2 of a scale
-};
 
 template <int D, int BS, int PARTS>
 __global__ void __launch_bounds__(kMq8Threads, 1)
@@ -169,12 +178,9 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
     tc_fence_after();
     const uint32_t tmem = (uint32_t)*s_tmem;
 
-    // (every warp of a warpgroup by the same instruction)
-    if (warp >= 8)
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMq8OtherRegs));
-    else
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMq8SoftmaxRegs));
-    if (warp == 8) {
+    if (warp >= 8) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMq8OtherRegs));
+      if (warp == 8) {
         // ================= every MMA =================
         const uint32_t id_s = tc_idesc<__half>(kMq8Rows, kMq8Keys, 0);
         const uint32_t id_o = tc_idesc<__half>(kMq8Rows, D, 1);
@@ -248,110 +254,131 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
         __syncwarp();
         mbar_wait(&fin[0], 0, p.errors);
         __syncwarp();
-    } else if (warp > 8) {
+      } else {
         // ================= K and V, widened =================
         // task k: keys 16 (k % 8) .. + 15 of operand k / 8 (K_0, V_0, K_1, ...)
-        const int n_tasks = 16 * n_tiles;
+        const unsigned n_tasks = 16u * n_tiles;
         const int* table = p.block_tables + (size_t)s * p.max_blocks_per_seq;
-        const int guard_from = (pos0 + 1) / kMq8Keys;      // first tile that not every row sees all of
-        const size_t row_bytes = (size_t)p.n_kv_heads * D;
+        const unsigned guard_from = (unsigned)(pos0 + 1) / kMq8Keys;   // first tile that not
+                                                                       // every row sees all of
         const int r0 = lane / UNITS, u = lane % UNITS;     // row and unit of this lane's part 0
-        auto first_key = [&](int k) { return (k / 16) * kMq8Keys + (k % 8) * 16; };
-        // block of a task's keys, -1: none
-        auto block_of = [&](int k) -> int {
+        constexpr int ROWS = 32 / UNITS;                   // rows of a part
+        const size_t row_bytes = (size_t)p.n_kv_heads * D;
+        const size_t part_bytes = ROWS * row_bytes, page_bytes = BS * row_bytes;
+        const size_t mine = r0 * row_bytes + (size_t)kvh * D + u * 16;
+        const unsigned char* const k_mine = static_cast<const unsigned char*>(p.k_pool) + mine;
+        const unsigned char* const v_mine = static_cast<const unsigned char*>(p.v_pool) + mine;
+        auto first_key = [&](unsigned k) -> int { return (int)((k / 16) * kMq8Keys + (k % 8) * 16); };
+        // table entry of a task's keys (looked at a task later, when it is there)
+        auto entry_of = [&](unsigned k) -> int {
             const int key = first_key(k);
-            if (k >= n_tasks || key >= n_keys) return -1;
-            const int b = __ldg(table + key / BS);
-            if (b >= 0 && b < p.num_blocks) return b;
-            raise_error(p.errors, PKV_DEVERR_BLOCK_ID);
-            return -1;
+            return k < n_tasks && key < n_keys ? __ldg(table + key / BS) : 0;
         };
         struct Task {
             uint4 codes[kParts];
             float scale;                 // lane 0: of the keys, lane 1: of the values
-            int block;
+            bool page;
         };
-        auto fetch = [&](Task& t, int k, int block) {
-            const int key0 = first_key(k), op = (k / 8) & 1;
-            t.block = block;
+        auto fetch = [&](Task& t, unsigned k, int entry) {
+            const int key0 = first_key(k), left = k < n_tasks ? n_keys - key0 : 0;
+            const bool keys = ((k / 8) & 1) == 0;
+            t.page = left > 0 && entry >= 0 && entry < p.num_blocks;
             t.scale = 0.f;
-            if (block >= 0 && op == 0 && lane < 2)
-                t.scale = __ldg((lane ? p.v_scale : p.k_scale) + (size_t)block * p.n_kv_heads + kvh);
-            const unsigned char* from =
-                static_cast<const unsigned char*>(op ? p.v_pool : p.k_pool) +
-                ((size_t)max(block, 0) * BS + key0 % BS + r0) * row_bytes + (size_t)kvh * D + u * 16;
 #pragma unroll
-            for (int i = 0; i < kParts; ++i) {
-                const int row = r0 + i * (32 / UNITS);
-                t.codes[i] = block >= 0 && key0 + row < n_keys
-                                 ? __ldg(reinterpret_cast<const uint4*>(
-                                       from + (size_t)i * (32 / UNITS) * row_bytes))
-                                 : make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < kParts; ++i) t.codes[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (!t.page) {
+                if (left > 0) raise_error(p.errors, PKV_DEVERR_BLOCK_ID);
+                return;
+            }
+            if (keys && lane < 2)
+                t.scale = __ldg((lane ? p.v_scale : p.k_scale) + (size_t)entry * p.n_kv_heads + kvh);
+            const unsigned char* from = (keys ? k_mine : v_mine) + entry * page_bytes +
+                                        (BS > 16 ? (key0 % BS) * row_bytes : 0);
+            if (left >= 16) {
+#pragma unroll
+                for (int i = 0; i < kParts; ++i) t.codes[i] = mq8_load(from + i * part_bytes);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kParts; ++i)
+                    if (r0 + i * ROWS < left) t.codes[i] = mq8_load(from + i * part_bytes);
             }
         };
-        Task task[kMq8Ahead];
-        int k = warp - 9;
+        // this lane's chunks of a part: 2 u, 2 u + 1 of the row; where eight lanes share
+        // a row those of the upper dims store theirs in the other order, so that they
+        // write to eight bank groups
+        const bool swap = D == 128 && u >= 4;
+        auto chunk_at = [&](int row, int c) -> uint32_t {
+            return (u / 4) * Z::KV_HALF + row * 128 + ((((u % 4) * 2 + c) ^ (row & 7)) << 4);
+        };
+        // (rows r0 + ROWS i: the swizzle repeats every 8 rows)
+        uint32_t first_at[8 / ROWS > 0 ? 8 / ROWS : 1], second_at[8 / ROWS > 0 ? 8 / ROWS : 1];
 #pragma unroll
-        for (int i = 0; i < kMq8Ahead; ++i) fetch(task[i], k + i * kMq8Widen, block_of(k + i * kMq8Widen));
-        int block = block_of(k + kMq8Ahead * kMq8Widen);
+        for (int i = 0; i < 8 / ROWS; ++i) {
+            first_at[i] = smem_addr(sKV) + chunk_at(r0 + i * ROWS, swap);
+            second_at[i] = smem_addr(sKV) + chunk_at(r0 + i * ROWS, !swap);
+        }
+        Task task[kMq8Ahead];
+        unsigned k = warp - 9;
+#pragma unroll
+        for (int i = 0; i < kMq8Ahead; ++i)
+            fetch(task[i], k + i * kMq8Widen, entry_of(k + i * kMq8Widen));
+        int entry = entry_of(k + kMq8Ahead * kMq8Widen);
         bool ok = true;
         while (ok && k < n_tasks) {
 #pragma unroll
             for (int i = 0; i < kMq8Ahead; ++i) {
                 if (!ok || k >= n_tasks) break;
                 Task& now = task[i];
-                const int i_op = k / 8, st = i_op % STAGES, g = k % 8, j = k / 16;
+                const unsigned i_op = k / 8, st = i_op % STAGES, g = k % 8, j = k / 16;
                 if (i_op >= STAGES)
-                    ok = __all_sync(0xffffffffu,
-                                    mbar_wait(&kv_free[st], (uint32_t)(i_op / STAGES - 1) & 1u,
-                                              p.errors));
+                    ok = __all_sync(0xffffffffu, mbar_wait(&kv_free[st], (i_op / STAGES - 1) & 1u,
+                                                           p.errors));
                 if (!ok) break;
                 if ((i_op & 1) == 0) {
                     Mq8Scale& e = s_scale[j % kMq8Scales];
                     if (lane == 0) {
                         e.a[g] = now.scale;
-                        e.page[g] = now.block >= 0;
+                        e.page[g] = now.page;
                     } else if (lane == 1) {
                         // (NaN stays)
                         const float b = now.scale < kQ8LeastScale ? kQ8LeastScale : now.scale;
                         e.lb[g] = __log2f(b);
                         e.ib[g] = __frcp_rn(b);
                     }
-                }
-                unsigned char* dst = sKV + (size_t)st * Z::KV_BYTES;
-                const bool guard = (i_op & 1) && j >= guard_from;
+                } else if (j >= guard_from) {
+                    bool any = false;
 #pragma unroll
-                for (int n = 0; n < kParts; ++n) {
-                    const int row = g * 16 + r0 + n * (32 / UNITS);
-                    uint4 w = now.codes[n];
-                    if (guard) {
+                    for (int n = 0; n < kParts; ++n) {
+                        uint4& w = now.codes[n];
                         const uint4 bad = make_uint4(mq8_nans(w.x), mq8_nans(w.y), mq8_nans(w.z),
                                                      mq8_nans(w.w));
-                        if (bad.x | bad.y | bad.z | bad.w) *s_poison = 1;
+                        any |= (bad.x | bad.y | bad.z | bad.w) != 0u;
                         w = make_uint4(w.x & ~bad.x, w.y & ~bad.y, w.z & ~bad.z, w.w & ~bad.w);
                     }
+                    if (any) *s_poison = 1;
+                }
+                const uint32_t dst = st * Z::KV_BYTES + g * 2048;
+#pragma unroll
+                for (int n = 0; n < kParts; ++n) {
                     uint4 a, b;
-                    mq8_widen(w, a, b);
-                    // chunks 2 u, 2 u + 1 of the row; where eight lanes share a row those
-                    // of the upper dims take theirs in the other order, so that they
-                    // write to eight bank groups
-                    const int h = u / 4, c0 = (u % 4) * 2, sw = row & 7;
-                    unsigned char* at_row = dst + h * Z::KV_HALF + row * 128;
-                    const bool swap = D == 128 && h == 1;
-                    *reinterpret_cast<uint4*>(at_row + (((c0 + swap) ^ sw) << 4)) = swap ? b : a;
-                    *reinterpret_cast<uint4*>(at_row + (((c0 + !swap) ^ sw) << 4)) = swap ? a : b;
+                    mq8_widen(now.codes[n], a, b);
+                    const int r = n % (8 / ROWS), more = n / (8 / ROWS) * 1024;
+                    mq8_store(first_at[r] + dst + more, swap ? b : a);
+                    mq8_store(second_at[r] + dst + more, swap ? a : b);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&kv_full[st]);
-                const int next = k + kMq8Ahead * kMq8Widen;
-                fetch(now, next, block);
-                block = block_of(next + kMq8Widen);
+                const unsigned next = k + kMq8Ahead * kMq8Widen;
+                fetch(now, next, entry);
+                entry = entry_of(next + kMq8Widen);
                 k += kMq8Widen;
             }
         }
+      }
     } else {
         // ================= softmax: thread r of group t owns row r of tile t =================
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMq8SoftmaxRegs));
         const int t = warp >> 2;
         const int r = (warp & 3) * 32 + lane;
         const int nt = t ? nt1 : nt0;
@@ -395,145 +422,206 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
                 if (lane == 0) mbar_arrive(&q_full[t]);
             }
             const uint32_t t_lane = tmem + t * Z::TILE_COLS + ((uint32_t)((warp & 3) * 32) << 16);
-            Mq8Reference ref;
+            float m = -INFINITY, lb = 0.f;        // the reference: a score and log2 of a scale
             // scores formed ahead of the maximum: where their factor is not positive,
             // or a row's are so large that y a + add would lose what matters
             bool formed = !(p.scale_log2 > 0.f);
             float l = 0.f;
+            auto group_max = [](const float* v) -> float {
+                const float a = max3(max3(v[0], v[1], v[2]), v[3], v[4]);
+                const float b = max3(max3(v[5], v[6], v[7]), v[8], v[9]);
+                const float c = max3(max3(v[10], v[11], v[12]), v[13], v[14]);
+                return max3(max3(a, b, c), v[15], v[15]);
+            };
+            // The reference to (to, to_lb) where `moved`; what is summed up with it.
+            auto move = [&](int j, bool moved, float to, float to_lb) {
+                float alpha = 1.f;
+                if (moved) {
+                    if (m != -INFINITY) alpha = exp2f((m - to) + (lb - to_lb));
+                    m = to;
+                    lb = to_lb;
+                }
+                if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    // O is at rest: the products up to key tile j - 1 completed before
+                    // S_j did
+                    const float2 a2 = make_float2(alpha, alpha);
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t ov[32];
+                        tc_ld32(t_lane + c0, ov);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) {
+                            const float2 v = __fmul2_rn(
+                                make_float2(__uint_as_float(ov[c]), __uint_as_float(ov[c + 1])), a2);
+                            ov[c] = __float_as_uint(v.x);
+                            ov[c + 1] = __float_as_uint(v.y);
+                        }
+                        tc_st32(t_lane + c0, ov);
+                    }
+                    l *= alpha;
+                }
+            };
+            // 2^(y mul1 + add1) of 16 keys as 16-bit pairs from w[..][at] on; their sum.
+            auto weights = [](const float* y, float mul1, float add1, uint32_t (&w)[PARTS][16],
+                              int at) -> float {
+                const float2 mul = make_float2(mul1, mul1), add = make_float2(add1, add1);
+                float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 e = __ffma2_rn(make_float2(y[2 * i], y[2 * i + 1]), mul, add);
+                    const float2 pv = make_float2(exp2f(e.x), exp2f(e.y));
+                    sum = __fadd2_rn(sum, pv);
+                    w[0][at + i] = pack2<__half>(pv.x, pv.y);
+                    if (PARTS > 1) {
+                        const float2 rest = __ffma2_rn(unpack2<__half>(w[0][at + i]),
+                                                       make_float2(-1.f, -1.f), pv);
+                        w[PARTS - 1][at + i] = pack2<__half>(rest.x, rest.y);
+                    }
+                }
+                return sum.x + sum.y;
+            };
+            auto stored = [&](int half) {
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
+            };
+            // 32 keys' weights over the scores just read.
+            auto store = [&](uint32_t (&w)[PARTS][16], int part) {
+#pragma unroll
+                for (int i = 0; i < PARTS; ++i)
+                    tc_st16(t_lane + Z::S_COL + i * 64 + part * 16, w[i]);
+                if (part & 1) stored(part / 2);
+            };
             bool ok = true;
             for (int j = 0; j < nt;) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], (uint32_t)j & 1u, p.errors));
                 if (!ok) break;
                 tc_fence_after();
-                float y[kMq8Keys];
-                uint32_t* yr = reinterpret_cast<uint32_t*>(y);
-                tc_ld32(t_lane + Z::S_COL, yr);
-                tc_ld32(t_lane + Z::S_COL + 32, yr + 32);
-                tc_ld32(t_lane + Z::S_COL + 64, yr + 64);
-                tc_ld32(t_lane + Z::S_COL + 96, yr + 96);
-                tc_wait_ld();
                 const Mq8Scale& sc = s_scale[j % kMq8Scales];
                 const int key0 = j * kMq8Keys;
                 const uint2 pages = *reinterpret_cast<const uint2*>(sc.page);
                 const bool whole = key0 + kMq8Keys - 1 <= warp_pos &&
                                    (pages.x & pages.y) == 0x01010101u;
-                // factors of the groups (never 0: hidden keys are -inf below)
-                float a[8];
-                unsigned seen = 0xffu;            // groups that this row sees keys of
-                if (!whole) {
-                    seen = 0u;
+                if (whole && !formed) {
+                    // ---- the usual tile: this warp's rows see all of it
+                    float y[kMq8Keys];
+                    uint32_t* yr = reinterpret_cast<uint32_t*>(y);
+                    tc_ld32(t_lane + Z::S_COL, yr);
+                    tc_ld32(t_lane + Z::S_COL + 32, yr + 32);
+                    tc_ld32(t_lane + Z::S_COL + 64, yr + 64);
+                    tc_ld32(t_lane + Z::S_COL + 96, yr + 96);
+                    tc_wait_ld();
+                    float z = -INFINITY;                  // largest exponent
 #pragma unroll
                     for (int g = 0; g < 8; ++g)
-                        if (key0 + 16 * g <= pos && sc.page[g]) seen |= 1u << g;
-                }
-#pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    const float f = sc.a[g] * qf;
-                    a[g] = fabsf(f) < 1.2e-38f ? 1.2e-38f : f;
-                    if (!((seen >> g) & 1u)) a[g] = 1.f;
-                }
-                if (formed) {
-#pragma unroll
-                    for (int c = 0; c < kMq8Keys; ++c) y[c] *= a[c / 16];
-#pragma unroll
-                    for (int g = 0; g < 8; ++g) a[g] = 1.f;
-                }
-                if (!whole) {
-                    const int lim = pos - key0;
-#pragma unroll
-                    for (int c = 0; c < kMq8Keys; ++c)
-                        y[c] = c <= lim && ((seen >> (c / 16)) & 1u) ? y[c] : -INFINITY;
-                }
-                // ---- the reference
-                bool beyond = false;
-                float top = -INFINITY, top_lb = 0.f;
-#pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    const float* v = y + 16 * g;
-                    float m = max3(max3(v[0], v[1], v[2]), max3(v[3], v[4], v[5]),
-                                   max3(v[6], v[7], v[8]));
-                    m = max3(m, max3(v[9], v[10], v[11]), max3(v[12], v[13], fmaxf(v[14], v[15])));
-                    const float x = __fmul_rn(m, a[g]), lb = ((seen >> g) & 1u) ? sc.lb[g] : 0.f;
-                    beyond |= (x - ref.m) + (lb - ref.lb) > Range::GROW;
-                    if (top == -INFINITY || (x - top) + (lb - top_lb) > 0.f) {
-                        top = x;
-                        top_lb = lb;
-                    }
-                }
-                if (__any_sync(0xffffffffu, beyond)) {
-                    if (!formed && __any_sync(0xffffffffu, real && beyond && fabsf(top) > 32768.f)) {
-                        formed = true;
-                        continue;                  // this tile once more (S is still there)
-                    }
-                    float alpha = 1.f;
-                    if (beyond) {
-                        if (ref.m != -INFINITY) alpha = exp2f((ref.m - top) + (ref.lb - top_lb));
-                        ref.m = top;
-                        ref.lb = top_lb;
-                    }
-                    if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                        // O is at rest: the products up to key tile j - 1
-                        // completed before S_j did
-                        const float2 a2 = make_float2(alpha, alpha);
-#pragma unroll 1
-                        for (int c0 = 0; c0 < D; c0 += 32) {
-                            uint32_t ov[32];
-                            tc_ld32(t_lane + c0, ov);
-                            tc_wait_ld();
-#pragma unroll
-                            for (int c = 0; c < 32; c += 2) {
-                                const float2 v = __fmul2_rn(
-                                    make_float2(__uint_as_float(ov[c]), __uint_as_float(ov[c + 1])),
-                                    a2);
-                                ov[c] = __float_as_uint(v.x);
-                                ov[c + 1] = __float_as_uint(v.y);
-                            }
-                            tc_st32(t_lane + c0, ov);
+                        z = fmaxf(z, fmaf(group_max(y + 16 * g), sc.a[g] * qf, sc.lb[g]));
+                    const bool beyond = z - (m + lb) > Range::GROW;
+                    if (__any_sync(0xffffffffu, beyond)) {
+                        if (__any_sync(0xffffffffu, real && beyond && fabsf(z) > 32768.f)) {
+                            formed = true;
+                            continue;              // this tile once more (S is still there)
                         }
-                        l *= alpha;
+                        move(j, beyond, z, 0.f);
                     }
-                }
-                const float mu = ref.m == -INFINITY ? 0.f : ref.m;
-                float base = Range::LIFT - ref.lb;
-                if (formed) {
+                    const float base = Range::LIFT - (m == -INFINITY ? 0.f : m + lb);
 #pragma unroll
-                    for (int c = 0; c < kMq8Keys; ++c) y[c] -= mu;      // exact first
+                    for (int part = 0; part < 4; ++part) {
+                        uint32_t w[PARTS][16];
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            const int gg = part * 2 + g;
+                            l = fmaf(weights(y + 16 * gg, sc.a[gg] * qf, base + sc.lb[gg], w, g * 8),
+                                     sc.ib[gg], l);
+                        }
+                        store(w, part);
+                    }
                 } else {
-                    base -= mu;
-                }
-                // ---- weights
+                    // ---- tiles with hidden keys or missing pages, rows with large scores:
+                    // 32 keys at a time, once for the maximum and once for the weights
+                    const int lim = pos - key0;
+                    // group g as this row sees it: the score of a unit of y (never 0,
+                    // hidden keys are -inf), 0 for a group with nothing to see
+                    auto unit = [&](int g) -> float {
+                        const float f = sc.a[g] * qf;
+                        return 16 * g <= lim && sc.page[g] ? (fabsf(f) < 1.2e-38f ? 1.2e-38f : f)
+                                                           : 0.f;
+                    };
+                    // 32 keys' scores (formed) or products
+                    auto scores = [&](float (&y)[32], int part) {
+                        tc_ld32(t_lane + Z::S_COL + part * 32, reinterpret_cast<uint32_t*>(y));
+                        tc_wait_ld();
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t w[PARTS][32];
+                        for (int g = 0; g < 2; ++g) {
+                            const float f = unit(part * 2 + g);
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const int gg = half * 4 + g;
-                        const bool in = (seen >> gg) & 1u;
-                        const float add1 = in ? base + sc.lb[gg] : 0.f;
-                        const float2 mul = make_float2(a[gg], a[gg]), add = make_float2(add1, add1);
-                        float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int k = gg * 16 + 2 * i;
-                            const float2 e = __ffma2_rn(make_float2(y[k], y[k + 1]), mul, add);
-                            const float2 pv = make_float2(exp2f(e.x), exp2f(e.y));
-                            sum = __fadd2_rn(sum, pv);
-                            w[0][g * 8 + i] = pack2<__half>(pv.x, pv.y);
-                            if (PARTS > 1) {
-                                const float2 rest = __ffma2_rn(unpack2<__half>(w[0][g * 8 + i]),
-                                                               make_float2(-1.f, -1.f), pv);
-                                w[PARTS - 1][g * 8 + i] = pack2<__half>(rest.x, rest.y);
+                            for (int c = 16 * g; c < 16 * g + 16; ++c) {
+                                const float x = formed ? y[c] * f : y[c];
+                                y[c] = part * 32 + c <= lim && f != 0.f ? x : -INFINITY;
                             }
                         }
-                        if (in) l = fmaf(sum.x + sum.y, sc.ib[gg], l);
-                    }
+                    };
+                    bool beyond = false;
+                    float top = -INFINITY, top_lb = 0.f;
+#pragma unroll 1
+                    for (int part = 0; part < 4; ++part) {
+                        float y[32];
+                        scores(y, part);
 #pragma unroll
-                    for (int k = 0; k < PARTS; ++k)
-                        tc_st32(t_lane + Z::S_COL + k * 64 + half * 32, w[k]);
-                    tc_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
+                        for (int g = 0; g < 2; ++g) {
+                            const float f = unit(part * 2 + g);
+                            const float x = __fmul_rn(group_max(y + 16 * g),
+                                                      formed || f == 0.f ? 1.f : f);
+                            const float b = f == 0.f ? 0.f : sc.lb[part * 2 + g];
+                            beyond |= (x - m) + (b - lb) > Range::GROW;
+                            if (top == -INFINITY || (x - top) + (b - top_lb) > 0.f) {
+                                top = x;
+                                top_lb = b;
+                            }
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, beyond)) {
+                        if (!formed &&
+                            __any_sync(0xffffffffu, real && beyond && fabsf(top) > 32768.f)) {
+                            formed = true;
+                            continue;              // this tile once more (S is still there)
+                        }
+                        move(j, beyond, top, top_lb);
+                    }
+                    const float mu = m == -INFINITY ? 0.f : m;
+                    const float base = formed ? Range::LIFT - lb : Range::LIFT - (mu + lb);
+                    // (the first parts lie where scores were already read, the second
+                    // ones wait for the end)
+                    uint32_t rest[4][16];
+#pragma unroll
+                    for (int part = 0; part < 4; ++part) {
+                        float y[32];
+                        uint32_t w[PARTS][16];
+                        scores(y, part);
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            const float f = unit(part * 2 + g);
+                            if (formed) {
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) y[16 * g + c] -= mu;   // exact first
+                            }
+                            const float sum = weights(y + 16 * g, formed || f == 0.f ? 1.f : f,
+                                                      f == 0.f ? 0.f : base + sc.lb[part * 2 + g],
+                                                      w, g * 8);
+                            if (f != 0.f) l = fmaf(sum, sc.ib[part * 2 + g], l);
+                        }
+                        tc_st16(t_lane + Z::S_COL + part * 16, w[0]);
+                        if (PARTS > 1)
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) rest[part][c] = w[PARTS - 1][c];
+                    }
+                    if (PARTS > 1)
+#pragma unroll
+                        for (int part = 0; part < 4; ++part)
+                            tc_st16(t_lane + Z::S_COL + 64 + part * 16, rest[part]);
+                    stored(0);
+                    stored(1);
                 }
                 ++j;
             }
