@@ -37,7 +37,7 @@ constexpr int kMq8Keys = 128;
 constexpr int kMq8Rows = 128;
 constexpr int kMq8Threads = 512;      // 8 softmax warps, 1 MMA, 7 that widen
 constexpr int kMq8Widen = 7;
-constexpr int kMq8Ahead = 2;          // groups of 16 keys that a widening warp has under way
+constexpr int kMq8Ahead = 1;          // groups of 16 keys that a widening warp has under way
 // Registers per thread: 512 x 128 at launch
 constexpr int kMq8SoftmaxRegs = 184, kMq8OtherRegs = 72;
 static_assert(256 * kMq8SoftmaxRegs + 256 * kMq8OtherRegs <= kMq8Threads * 128, "registers");
@@ -108,8 +108,7 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
     using Z = Mq8Sizes<D>;
     using Range = WeightRange<__half>;
     constexpr int STAGES = Z::STAGES;
-    constexpr int UNITS = D / 16;                  // 16-code units of a row
-    constexpr int kParts = 16 * UNITS / 32;        // a lane's units of 16 rows
+    constexpr int kParts = 2 * Z::HALVES;          // 16-byte parts of 16 keys' codes per lane
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     unsigned char* sm = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
@@ -261,10 +260,11 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
         const int* table = p.block_tables + (size_t)s * p.max_blocks_per_seq;
         const unsigned guard_from = (unsigned)(pos0 + 1) / kMq8Keys;   // first tile that not
                                                                        // every row sees all of
-        const int r0 = lane / UNITS, u = lane % UNITS;     // row and unit of this lane's part 0
-        constexpr int ROWS = 32 / UNITS;                   // rows of a part
+        // Part i of a task: rows 8 (i / HALVES) + lane / 4, 16 codes from 64 (i %
+        // HALVES) + 16 (lane % 4) on.  So eight lanes store to eight bank groups.
+        const int r0 = lane / 4, u = lane % 4;
         const size_t row_bytes = (size_t)p.n_kv_heads * D;
-        const size_t part_bytes = ROWS * row_bytes, page_bytes = BS * row_bytes;
+        const size_t page_bytes = BS * row_bytes;
         const size_t mine = r0 * row_bytes + (size_t)kvh * D + u * 16;
         const unsigned char* const k_mine = static_cast<const unsigned char*>(p.k_pool) + mine;
         const unsigned char* const v_mine = static_cast<const unsigned char*>(p.v_pool) + mine;
@@ -284,39 +284,26 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
             const bool keys = ((k / 8) & 1) == 0;
             t.page = left > 0 && entry >= 0 && entry < p.num_blocks;
             t.scale = 0.f;
-#pragma unroll
-            for (int i = 0; i < kParts; ++i) t.codes[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (!t.page) {
-                if (left > 0) raise_error(p.errors, PKV_DEVERR_BLOCK_ID);
-                return;
-            }
-            if (keys && lane < 2)
-                t.scale = __ldg((lane ? p.v_scale : p.k_scale) + (size_t)entry * p.n_kv_heads + kvh);
-            const unsigned char* from = (keys ? k_mine : v_mine) + entry * page_bytes +
+            const unsigned char* from = (keys ? k_mine : v_mine) + (size_t)(t.page ? entry : 0) * page_bytes +
                                         (BS > 16 ? (key0 % BS) * row_bytes : 0);
-            if (left >= 16) {
-#pragma unroll
-                for (int i = 0; i < kParts; ++i) t.codes[i] = mq8_load(from + i * part_bytes);
-            } else {
+            if (t.page && keys && lane < 2)
+                t.scale = __ldg((lane ? p.v_scale : p.k_scale) + (size_t)entry * p.n_kv_heads + kvh);
+            if (t.page && left >= 16) {
 #pragma unroll
                 for (int i = 0; i < kParts; ++i)
-                    if (r0 + i * ROWS < left) t.codes[i] = mq8_load(from + i * part_bytes);
+                    t.codes[i] = mq8_load(from + i / Z::HALVES * 8 * row_bytes + i % Z::HALVES * 64);
+            } else {
+                if (!t.page && left > 0) raise_error(p.errors, PKV_DEVERR_BLOCK_ID);
+#pragma unroll
+                for (int i = 0; i < kParts; ++i)
+                    t.codes[i] = t.page && r0 + i / Z::HALVES * 8 < left
+                                     ? mq8_load(from + i / Z::HALVES * 8 * row_bytes + i % Z::HALVES * 64)
+                                     : make_uint4(0u, 0u, 0u, 0u);
             }
         };
-        // this lane's chunks of a part: 2 u, 2 u + 1 of the row; where eight lanes share
-        // a row those of the upper dims store theirs in the other order, so that they
-        // write to eight bank groups
-        const bool swap = D == 128 && u >= 4;
-        auto chunk_at = [&](int row, int c) -> uint32_t {
-            return (u / 4) * Z::KV_HALF + row * 128 + ((((u % 4) * 2 + c) ^ (row & 7)) << 4);
-        };
-        // (rows r0 + ROWS i: the swizzle repeats every 8 rows)
-        uint32_t first_at[8 / ROWS > 0 ? 8 / ROWS : 1], second_at[8 / ROWS > 0 ? 8 / ROWS : 1];
-#pragma unroll
-        for (int i = 0; i < 8 / ROWS; ++i) {
-            first_at[i] = smem_addr(sKV) + chunk_at(r0 + i * ROWS, swap);
-            second_at[i] = smem_addr(sKV) + chunk_at(r0 + i * ROWS, !swap);
-        }
+        // where a part's two chunks of 8 go in part 0
+        const uint32_t first_at = smem_addr(sKV) + r0 * 128 + (((2 * u) ^ r0) << 4);
+        const uint32_t second_at = smem_addr(sKV) + r0 * 128 + (((2 * u + 1) ^ r0) << 4);
         Task task[kMq8Ahead];
         unsigned k = warp - 9;
 #pragma unroll
@@ -362,9 +349,9 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
                 for (int n = 0; n < kParts; ++n) {
                     uint4 a, b;
                     mq8_widen(now.codes[n], a, b);
-                    const int r = n % (8 / ROWS), more = n / (8 / ROWS) * 1024;
-                    mq8_store(first_at[r] + dst + more, swap ? b : a);
-                    mq8_store(second_at[r] + dst + more, swap ? a : b);
+                    const uint32_t to = dst + n / Z::HALVES * 1024 + n % Z::HALVES * Z::KV_HALF;
+                    mq8_store(first_at + to, a);
+                    mq8_store(second_at + to, b);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
