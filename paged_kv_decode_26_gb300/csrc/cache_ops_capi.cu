@@ -29,20 +29,22 @@ namespace host {
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-int pieces_stream_heads(int n_kv_heads) {
-    int hw = kPieceWarps;
+int pieces_stream_heads(int n_kv_heads, int most) {
+    int hw = most;
     while (n_kv_heads % hw) hw /= 2;
     return hw;
 }
 
 PiecesGrid pieces_grid(int num_seqs, int n_kv_heads, int max_context_len, int sm_count,
-                       bool short_runs, int chunk_tokens) {
-    const int hw = pieces_stream_heads(n_kv_heads), per_cta = kPieceWarps / hw;
+                       bool short_runs, const PiecesKind& kind) {
+    const int hw = pieces_stream_heads(n_kv_heads, kind.heads), per_cta = kind.warps / hw;
     const long long chunks = (long long)num_seqs * (n_kv_heads / hw) *
-                             (((long long)max_context_len + chunk_tokens - 1) / chunk_tokens);
+                             (((long long)max_context_len + kind.tokens - 1) / kind.tokens);
     const long long streams = (chunks + kPieceMinRun - 1) / kPieceMinRun;
     const long long ctas = (streams + per_cta - 1) / per_cta;
     PiecesGrid g;
+    g.stream_heads = hw;
+    g.warps = kind.warps;
     g.ctas = (int)(ctas < 1 ? 1 : (ctas < sm_count ? ctas : sm_count));
     g.extra = short_runs && chunks >= (long long)g.ctas * per_cta * kPieceDealt
                   ? kPieceExtra * g.ctas
@@ -54,7 +56,7 @@ PiecesWorkspace pieces_workspace(int num_seqs, int n_heads, int n_kv_heads, int 
                                  const PiecesGrid& grid) {
     PiecesWorkspace w;
     const size_t rows = (size_t)num_seqs * n_heads + (size_t)(grid.ctas + grid.extra) *
-                                                         kPieceWarps * (n_heads / n_kv_heads);
+                                                         grid.warps * (n_heads / n_kv_heads);
     const size_t pairs = (size_t)num_seqs * n_kv_heads;
     w.o = 0;
     w.ml = align256(w.o + rows * head_dim * sizeof(float));
@@ -162,7 +164,7 @@ void fill_piece_problem(PieceParams* pp, const PiecesGrid& grid, void* out, pkv_
     const long long table = (long long)max_blocks_per_seq * block_size;
     p.cap_tokens = (int)(table < max_context_len ? table : max_context_len);
     p.scale_log2 = scale * 1.4426950408889634f;
-    p.stream_heads = pieces_stream_heads(n_kv_heads);
+    p.stream_heads = grid.stream_heads;
     p.ctas = grid.ctas;
     p.extra_ctas = grid.extra;
     p.ws_o = reinterpret_cast<float*>(ws + w.o);

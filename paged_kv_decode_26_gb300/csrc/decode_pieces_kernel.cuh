@@ -430,9 +430,10 @@ struct PieceRuns {
     }
 };
 
-__device__ __forceinline__ PieceRuns piece_runs(const PieceParams& p, int chunks) {
+__device__ __forceinline__ PieceRuns piece_runs(const PieceParams& p, int chunks,
+                                                int warps = kPieceWarps) {
     PieceRuns r;
-    const int per_cta = kPieceWarps / p.stream_heads;
+    const int per_cta = warps / p.stream_heads;
     r.total = (long long)chunks * (p.n_kv_heads / p.stream_heads);
     r.first = (int)min((long long)p.ctas * per_cta, (r.total + kPieceMinRun - 1) / kPieceMinRun);
     r.share = r.total;
@@ -446,8 +447,8 @@ __device__ __forceinline__ PieceRuns piece_runs(const PieceParams& p, int chunks
 
 // Stream of a CTA's warp, -1 where it has no work.
 __device__ __forceinline__ int piece_stream(const PieceParams& p, const PieceRuns& r, int cta,
-                                            int warp) {
-    const int per_cta = kPieceWarps / p.stream_heads;
+                                            int warp, int warps = kPieceWarps) {
+    const int per_cta = warps / p.stream_heads;
     const long long k = (long long)(cta < p.ctas ? cta : cta - p.ctas) * per_cta +
                         warp / p.stream_heads;
     if (cta < p.ctas) return k < r.first ? (int)k : -1;

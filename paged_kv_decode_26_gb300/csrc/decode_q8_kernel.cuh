@@ -26,7 +26,8 @@
 // reference (m, b_ref) is the score and scale of the key with the largest p b when
 // it was set, m a score itself (weight_range.cuh says why).
 //
-// Runs, rings and merge as in decode_pieces_kernel.cuh, with chunks of 32 tokens.
+// Runs, rings and merge as in decode_pieces_kernel.cuh, with chunks of 32 tokens and
+// no runs to take over.
 #pragma once
 
 #include "decode_pieces_kernel.cuh"
@@ -34,6 +35,14 @@
 namespace pkv {
 
 constexpr int kQ8Tokens = 32;                  // tokens per chunk: two halves of 16
+// Twelve warps with two chunks each under way.  (With eight and three the issue slots
+// were 42 % used, each warp waiting for its own products: 16 MHA contexts of 8K-32K
+// 553 us instead of 444, 128 GQA ones of up to 8192 217 instead of 181.)
+constexpr int kQ8Warps = 12;
+constexpr int kQ8Stages = 2;
+constexpr int kQ8StreamHeads = 4;              // kv heads (warps) per stream at most
+constexpr int kQ8Threads = 32 * kQ8Warps;
+static_assert(kQ8Warps * kQ8Stages == kPieceWarps * kPieceStages, "piece_shared's barriers");
 constexpr float kQ8LeastScale = 0x1p-100f;     // of a reference (blocks of zeros)
 
 struct Q8Params : PieceParams {
@@ -278,11 +287,11 @@ __device__ __forceinline__ void q8_chunk(Q8Heads<D>& st, uint32_t kbase, uint32_
     }
 }
 
-// A piece's result: normalised rows to the output (WHOLE) or, with (m, L), to the
-// workspace's rows row0 + head.
+// A piece's result: normalised rows row0 + head to the output (WHOLE) or, with (m,
+// L), to o and ml (of the workspace or shared memory).
 template <int D, bool WHOLE>
 __device__ __forceinline__ void q8_store(const Q8Heads<D>& st, const Q8Params& p, size_t row0,
-                                         int lane) {
+                                         float* o, float* ml, int lane) {
     const int gid = lane >> 2, tig = lane & 3;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -300,7 +309,7 @@ __device__ __forceinline__ void q8_store(const Q8Heads<D>& st, const Q8Params& p
             const float v0 = st.o[j][e] * inv * b, v1 = st.o[j][2 + e] * inv * b;
             const size_t at = row * D + 16 * j + 2 * gid;
             if (!WHOLE)
-                *reinterpret_cast<float2*>(p.ws_o + at) = make_float2(v0, v1);
+                *reinterpret_cast<float2*>(o + at) = make_float2(v0, v1);
             else if (p.out_dtype == PKV_F32)
                 *reinterpret_cast<float2*>(reinterpret_cast<float*>(p.out) + at) =
                     make_float2(v0, v1);
@@ -309,7 +318,7 @@ __device__ __forceinline__ void q8_store(const Q8Heads<D>& st, const Q8Params& p
                     pack_out(v0, v1, p.out_dtype);
         }
         if (!WHOLE && gid == 0)
-            *reinterpret_cast<float2*>(p.ws_ml + row * 2) = make_float2(st.m[e], l);
+            *reinterpret_cast<float2*>(ml + row * 2) = make_float2(st.m[e], l);
     }
 }
 
@@ -330,21 +339,20 @@ __device__ __forceinline__ void q8_load(uint32_t k, const CUtensorMap* tm_k, uin
 
 // Bytes of the control area beside piece_shared's: the block of each half of the
 // chunks in the rings.
-constexpr size_t kQ8BlockBytes = (size_t)kPieceWarps * kPieceStages * 2 * sizeof(int);
+constexpr size_t kQ8BlockBytes = (size_t)kQ8Warps * kQ8Stages * 2 * sizeof(int);
 
 // One warp's work on the CTA's runs (piece_worker's, on 8-bit pages).
-template <int D, typename T, bool TAKES, bool PRECISE>
+template <int D, typename T, bool PRECISE>
 __device__ __forceinline__ void q8_worker(const Q8Params& p, const CUtensorMap& tm_k,
                                           const CUtensorMap& tm_v, const PieceShared& sh,
-                                          int* blocks, const PieceRuns& runs,
-                                          const PieceNext& next) {
+                                          int* blocks, const PieceRuns& runs) {
     constexpr uint32_t HALF = 16 * D;                 // half a chunk of K (or V)
     constexpr uint32_t SLOT = 4 * HALF;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int HW = p.stream_heads, hw = warp % HW;
-    unsigned char* ring = sh.ring + (size_t)warp * kPieceStages * SLOT;
-    uint64_t* full = sh.bars + warp * kPieceStages;
-    int* slot_block = blocks + warp * kPieceStages * 2;
+    unsigned char* ring = sh.ring + (size_t)warp * kQ8Stages * SLOT;
+    uint64_t* full = sh.bars + warp * kQ8Stages;
+    int* slot_block = blocks + warp * kQ8Stages * 2;
     const int pages = kQ8Tokens / p.block_size;       // of a chunk: 2 or 1
     const uint64_t policy = l2_policy_evict_first();
     const uint32_t lead = lane == 0 ? 1u : 0u;
@@ -353,44 +361,12 @@ __device__ __forceinline__ void q8_worker(const Q8Params& p, const CUtensorMap& 
         prefetch_tensormap(&tm_v);
     }
 
-    PieceCursor ld;              // the next chunk to load
-    PieceCursor at;              // the chunk to work on
-    bool ahead_run = false;      // the loads are in a run that `at` has not reached
-    PieceCursor ahead_start;     // its start
-    bool more = true;            // there may be a run after ld's (TAKES)
+    const int v = piece_stream(p, runs, blockIdx.x, warp, kQ8Warps);
+    if (v < 0) return;
+    PieceCursor ld = piece_locate<true, kQ8Tokens>(p, sh, runs, v, lane);   // the next to load
+    PieceCursor at = ld;                                                    // and to work on
     int win = -1, bid = -1;      // block ids of the pair's pages win .. win + 31
-    int cta = blockIdx.x, taken = 0;
-    ld.left = 0;
 
-    auto next_run = [&](bool own) {
-        while (more) {
-            if (!TAKES && !own) more = false;
-            if (!more) return;
-            if (!own) {
-                const int slot = (taken + 1) & 1;
-                const bool w = mbar_wait(&next.full[slot], (taken >> 1) & 1, p.errors);
-                cta = __all_sync(0xffffffffu, w) ? next.cta[slot] : -1;
-                __syncwarp();
-                ++taken;
-                if (cta < 0) {
-                    more = false;
-                    return;
-                }
-            }
-            own = false;
-            const int v = piece_stream(p, runs, cta, warp);
-            if (v >= 0) {
-                ld = piece_locate<true, kQ8Tokens>(p, sh, runs, v, lane);
-                win = -1;
-                if (TAKES && ld.left <= kPieceSoon && lane == 0) mbar_arrive(next.soon);
-                return;
-            }
-            if (TAKES && lane == 0) mbar_arrive(next.soon);
-        }
-    };
-    auto known = [&]() -> bool {
-        return __all_sync(0xffffffffu, mbar_test(&next.full[(taken + 1) & 1], (taken >> 1) & 1));
-    };
     auto issue = [&](int st) {
         const int page0 = ld.c * pages;
         const int kvh = ld.hg * HW + hw;
@@ -433,13 +409,8 @@ __device__ __forceinline__ void q8_worker(const Q8Params& p, const CUtensorMap& 
         const int s = ld.s, hg = ld.hg;
         piece_advance<true, kQ8Tokens>(p, sh, ld);
         if (ld.s != s || ld.hg != hg) win = -1;
-        if (TAKES && ld.left == kPieceSoon && lane == 0) mbar_arrive(next.soon);
     };
 
-    next_run(true);
-    if (ld.left == 0) return;
-    if (!TAKES) more = false;
-    at = ld;
     Q8Heads<D> state;
     bool fresh = true;                 // the next chunk starts a piece
     bool from_start = false;           // the piece holds the pair's first chunk
@@ -447,20 +418,9 @@ __device__ __forceinline__ void q8_worker(const Q8Params& p, const CUtensorMap& 
     uint32_t phase = 0;
     for (;;) {
         // ---- keep the ring full
-        while (in_flight < kPieceStages) {
-            if (ld.left == 0) {
-                if (!TAKES || !more || ahead_run || (in_flight > 0 && !known())) break;
-                next_run(false);
-                if (!more) break;
-                if (at.left == 0) {
-                    at = ld;
-                } else {
-                    ahead_run = true;
-                    ahead_start = ld;
-                }
-            }
+        while (in_flight < kQ8Stages && ld.left > 0) {
             issue(put);
-            if (++put == kPieceStages) put = 0;
+            if (++put == kQ8Stages) put = 0;
             ++in_flight;
         }
         if (in_flight == 0) break;
@@ -489,7 +449,7 @@ __device__ __forceinline__ void q8_worker(const Q8Params& p, const CUtensorMap& 
             // the loads still in flight land before the CTA may exit
             for (; in_flight > 0; --in_flight) {
                 mbar_wait(&full[st], phase, p.errors);
-                if (++st == kPieceStages) {
+                if (++st == kQ8Stages) {
                     st = 0;
                     phase ^= 1u;
                 }
@@ -501,7 +461,7 @@ __device__ __forceinline__ void q8_worker(const Q8Params& p, const CUtensorMap& 
             q8_chunk<D, PRECISE>(state, kbase, kbase + 2 * HALF, valid, sc, lane);
         __syncwarp();
         --in_flight;
-        if (++st == kPieceStages) {
+        if (++st == kQ8Stages) {
             st = 0;
             phase ^= 1u;
         }
@@ -511,29 +471,20 @@ __device__ __forceinline__ void q8_worker(const Q8Params& p, const CUtensorMap& 
             const size_t pair = (size_t)at.s * p.n_kv_heads + kvh;
             const size_t own = (size_t)at.s * p.n_heads + qh0;
             if (from_start && pair_end)
-                q8_store<D, true>(state, p, own, lane);
+                q8_store<D, true>(state, p, own, nullptr, nullptr, lane);
             else
                 q8_store<D, false>(state, p,
                                    from_start ? own
                                               : (size_t)p.num_seqs * p.n_heads +
                                                     ((size_t)at.v * HW + hw) * p.group,
-                                   lane);
+                                   p.ws_o, p.ws_ml, lane);
             if (lane == 0) {
                 if (from_start) p.seg_first[pair] = at.v;
                 if (pair_end) p.seg_last[pair] = at.v;
             }
             fresh = true;
         }
-        if (at.left == 1) {
-            if (ahead_run) {
-                at = ahead_start;
-                ahead_run = false;
-            } else {
-                at.left = 0;
-            }
-        } else {
-            piece_advance<true, kQ8Tokens>(p, sh, at);
-        }
+        piece_advance<true, kQ8Tokens>(p, sh, at);
     }
 }
 
@@ -541,9 +492,11 @@ inline size_t decode_q8_smem_bytes(int D) {
     return decode_pieces_smem_bytes(D) + kQ8BlockBytes;
 }
 
-// CTAs, runs and the ninth warp as in decode_pieces_kernel.
-template <int D, typename T, bool TAKES, bool PRECISE>
-__global__ void __launch_bounds__(kPieceThreads + (TAKES ? 32 : 0), 1)
+// A run of equal length for each stream (short runs that CTAs take over, as in
+// decode_pieces_kernel, need one warp more, whose registers the twelve cannot spare:
+// 128 a thread spill, 662 us instead of 444 for 16 contexts of 8K-32K tokens).
+template <int D, typename T, bool PRECISE>
+__global__ void __launch_bounds__(kQ8Threads, 1)
     decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ Q8Params p) {
@@ -552,43 +505,150 @@ __global__ void __launch_bounds__(kPieceThreads + (TAKES ? 32 : 0), 1)
     const uint32_t raw = smem_addr(smem_raw);
     unsigned char* sm = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     unsigned char* control = sm + decode_pieces_ring_bytes(D);
-    uint4* steal = reinterpret_cast<uint4*>(control);
-    uint64_t* steal_bar = reinterpret_cast<uint64_t*>(control + 16);
-    PieceNext next;
-    next.soon = steal_bar + 1;
-    next.full = next.soon + 1;
-    next.cta = reinterpret_cast<int*>(next.full + 2);
     int* blocks = reinterpret_cast<int*>(control + 64);
     PieceShared sh = piece_shared(sm, control + 64 + kQ8BlockBytes);
+    if (threadIdx.x < kPieceThreads) piece_plan<true, kQ8Tokens>(p, sh);
+    __syncthreads();
+    const int chunks = sh.cum[(p.num_seqs + 255) / 256];
+    q8_worker<D, T, PRECISE>(p, tm_k, tm_v, sh, blocks, piece_runs(p, chunks, kQ8Warps));
+}
+
+// Short contexts: a CTA per (sequence, kv head), its warps taking the chunks in
+// turn, their states merged in shared memory: one launch, and no line of units to
+// lay out first.
+constexpr int kQ8ShortWarps = 4;
+constexpr int kQ8ShortThreads = 32 * kQ8ShortWarps;
+
+inline size_t decode_q8_short_smem_bytes(int D) {
+    return 1024 + (size_t)kQ8ShortWarps * kQ8Stages * 4 * 16 * D;
+}
+
+template <int D, typename T, bool PRECISE>
+__global__ void __launch_bounds__(kQ8ShortThreads)
+    decode_q8_short_kernel(const __grid_constant__ CUtensorMap tm_k,
+                           const __grid_constant__ CUtensorMap tm_v,
+                           const __grid_constant__ Q8Params p) {
+    constexpr uint32_t HALF = 16 * D, SLOT = 4 * HALF;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    __shared__ uint64_t s_bar[kQ8ShortWarps * kQ8Stages];
+    __shared__ float s_ml[kQ8ShortWarps * 8 * 2];
+    const uint32_t raw = smem_addr(smem_raw);
+    unsigned char* sm = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (TAKES && threadIdx.x == kPieceThreads) {
-        mbar_init(steal_bar, 1);
-        mbar_init(next.soon, kPieceWarps);
-        mbar_init(&next.full[0], 1);
-        mbar_init(&next.full[1], 1);
+    const int kvh = blockIdx.x, s = blockIdx.y, qh0 = kvh * p.group;
+    unsigned char* ring = sm + (size_t)warp * kQ8Stages * SLOT;
+    uint64_t* full = s_bar + warp * kQ8Stages;
+    const int raw_n = p.context_lens[s], n = piece_length(p, s);
+    if (threadIdx.x == 0 && kvh == 0 && raw_n != n) raise_error(p.errors, PKV_DEVERR_CONTEXT);
+    const int chunks = (n + kQ8Tokens - 1) / kQ8Tokens;
+    if (lane == 0) {
+        for (int i = 0; i < kQ8Stages; ++i) mbar_init(&full[i], 1);
         fence_barrier_init();
     }
-    int chunks = 0;
-    if (warp < kPieceWarps) chunks = piece_plan<true, kQ8Tokens>(p, sh);
-    if (TAKES) __syncthreads();
-    if (warp < kPieceWarps) {
-        q8_worker<D, T, TAKES, PRECISE>(p, tm_k, tm_v, sh, blocks, piece_runs(p, chunks), next);
-    } else {
-        for (int k = 0;; ++k) {
-            int cta = -1;
-            bool ok = __all_sync(0xffffffffu, mbar_wait(next.soon, k & 1, p.errors));
-            if (ok) {
-                if (lane == 0) steal_cta(steal, steal_bar);
-                ok = __all_sync(0xffffffffu, mbar_wait(steal_bar, k & 1, p.errors));
-                if (ok) cta = stolen_cta(steal);
-                __syncwarp();
+    __syncwarp();
+    const uint64_t policy = l2_policy_evict_first();
+    const uint32_t lead = lane == 0 ? 1u : 0u;
+    // halves of chunk c: their blocks (-1: none), their loads started
+    struct Blocks {
+        int b[2];
+        Q8Scales sc;
+    };
+    auto issue = [&](int c, int st) -> Blocks {
+        Blocks r;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int t = c * kQ8Tokens + 16 * h;
+            r.b[h] = -1;
+            r.sc.k[h] = r.sc.v[h] = 0.f;
+            if (t >= n) continue;
+            const int b = __ldg(p.block_tables + (size_t)s * p.max_blocks_per_seq + t / p.block_size);
+            if (b < 0 || b >= p.num_blocks) {
+                raise_error(p.errors, PKV_DEVERR_BLOCK_ID);
+                continue;
             }
-            if (lane == 0) {
-                next.cta[(k + 1) & 1] = cta;
-                mbar_arrive(&next.full[(k + 1) & 1]);
-            }
-            if (cta < 0) break;
+            r.b[h] = b;
+            const size_t i = (size_t)b * p.n_kv_heads + kvh;
+            r.sc.k[h] = __ldg(p.k_scale + i);
+            r.sc.v[h] = __ldg(p.v_scale + i);
         }
+        const int loads = (r.b[0] >= 0) + (r.b[1] >= 0);
+        if (lane == 0) {
+            if (loads)
+                mbar_arrive_expect_tx(&full[st], loads * 2 * HALF);
+            else
+                mbar_arrive(&full[st]);
+        }
+        __syncwarp();
+        const uint32_t dst = smem_addr(ring) + st * SLOT;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (r.b[h] >= 0)
+                q8_load(dst + h * HALF, &tm_k, dst + (2 + h) * HALF, &tm_v, smem_addr(&full[st]),
+                        (c * kQ8Tokens + 16 * h) % p.block_size, kvh, r.b[h], policy, lead);
+        return r;
+    };
+    Q8Heads<D> state;
+    if (warp < chunks) {
+        Blocks now = issue(warp, 0);
+        q8_heads_start<D, T>(state,
+                             reinterpret_cast<const T*>(p.q) + ((size_t)s * p.n_heads + qh0) * D,
+                             p.group, p.scale_log2, lane);
+        int st = 0;
+        uint32_t phase = 0;
+        for (int c = warp; c < chunks; c += kQ8ShortWarps) {
+            Blocks next = now;
+            const bool more = c + kQ8ShortWarps < chunks;
+            if (more) next = issue(c + kQ8ShortWarps, st ^ 1);
+            const bool w = mbar_wait(&full[st], phase, p.errors);
+            if (!__all_sync(0xffffffffu, w)) {
+                // the loads still in flight land before the CTA may exit
+                mbar_wait(&full[st], phase, p.errors);
+                if (more) mbar_wait(&full[st ^ 1], st ? phase ^ 1u : phase, p.errors);
+                break;
+            }
+            int valid[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                valid[h] = now.b[h] >= 0 ? min(16, n - c * kQ8Tokens - 16 * h) : 0;
+            const uint32_t kbase = smem_addr(ring) + st * SLOT;
+            if (valid[0] > 0 || valid[1] > 0)
+                q8_chunk<D, PRECISE>(state, kbase, kbase + 2 * HALF, valid, now.sc, lane);
+            __syncwarp();
+            now = next;
+            if (st) phase ^= 1u;
+            st ^= 1;
+        }
+    }
+    // ---- the warps' states (each over its own ring)
+    const int active = min(chunks, kQ8ShortWarps);
+    if (active == 1) {
+        if (warp == 0) q8_store<D, true>(state, p, (size_t)s * p.n_heads + qh0, nullptr, nullptr, lane);
+        return;
+    }
+    if (warp < active)
+        q8_store<D, false>(state, p, 0, reinterpret_cast<float*>(ring), s_ml + warp * 16, lane);
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.group * (D / 2); e += kQ8ShortThreads) {
+        const int h = e / (D / 2), d = e % (D / 2) * 2;
+        float2 ml = make_float2(-INFINITY, 0.f);
+        for (int w = 0; w < active; ++w)
+            ml = join_ml(ml, *reinterpret_cast<const float2*>(s_ml + w * 16 + 2 * h));
+        const float inv = ml.y != 0.f ? 1.f / ml.y : 0.f;
+        float2 o = make_float2(0.f, 0.f);
+        for (int w = 0; w < active; ++w) {
+            const float2 a = *reinterpret_cast<const float2*>(s_ml + w * 16 + 2 * h);
+            const float f = a.y != 0.f ? a.y * exp2f(a.x - ml.x) * inv : 0.f;
+            const float2 x = *reinterpret_cast<const float2*>(
+                sm + (size_t)w * kQ8Stages * SLOT + (h * D + d) * sizeof(float));
+            o.x += f * x.x;
+            o.y += f * x.y;
+        }
+        const size_t at = ((size_t)s * p.n_heads + qh0 + h) * D + d;
+        if (p.out_dtype == PKV_F32)
+            *reinterpret_cast<float2*>(reinterpret_cast<float*>(p.out) + at) = o;
+        else
+            *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.out) + at) =
+                pack_out(o.x, o.y, p.out_dtype);
     }
 }
 

@@ -10,10 +10,11 @@ struct Q8Launch {
     CUtensorMap tm_k;     // boxes of 16 tokens of one kv head
     CUtensorMap tm_v;
     Q8Params p;
+    bool whole;           // contexts by decode_q8_short_kernel, whole
     cudaStream_t stream;
 };
 
-// Launch decode_q8_kernel<D, T>.
+// Launch decode_q8_kernel<D, T> or decode_q8_short_kernel<D, T>.
 cudaError_t launch_decode_q8_bf16(int D, const Q8Launch& L);
 cudaError_t launch_decode_q8_f16(int D, const Q8Launch& L);
 

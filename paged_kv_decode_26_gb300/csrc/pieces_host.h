@@ -21,17 +21,24 @@ size_t align256(size_t n);
 
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// kv heads per stream: the largest of 8, 4, 2, 1 that divides n_kv_heads.
-int pieces_stream_heads(int n_kv_heads);
+// kv heads per stream: the largest of `most`, most / 2, .. 1 that divides n_kv_heads
+// (most a power of two).
+int pieces_stream_heads(int n_kv_heads, int most = kPieceWarps);
 
 // CTAs of the piece decode: one per SM, fewer where the longest contexts
 // allowed could not give every stream its least run; and, with short_runs, CTAs
 // of short runs, none where the longest contexts allowed are too short for them.
 struct PiecesGrid {
     int ctas, extra;
+    int stream_heads;
+    int warps;                // of a CTA that have streams
 };
+struct PiecesKind {           // of a kernel: tokens per chunk, warps, kv heads per stream at most
+    int tokens, warps, heads;
+};
+constexpr PiecesKind kPieces16 = {kPieceTokens, kPieceWarps, kPieceWarps};
 PiecesGrid pieces_grid(int num_seqs, int n_kv_heads, int max_context_len, int sm_count,
-                       bool short_runs, int chunk_tokens = kPieceTokens);
+                       bool short_runs, const PiecesKind& kind = kPieces16);
 
 PiecesWorkspace pieces_workspace(int num_seqs, int n_heads, int n_kv_heads, int head_dim,
                                  const PiecesGrid& grid);

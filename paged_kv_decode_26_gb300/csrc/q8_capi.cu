@@ -36,8 +36,19 @@ cudaError_t encode_q8_map(CUtensorMap* map, const void* pool, int num_blocks, in
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Contexts up to kShortContext tokens are decoded whole, by a CTA per kv head
+// (decode_q8_short_kernel), where there are at most kShortPairs of them per SM.
+// GB300, whole / in pieces, us: 64 pairs of 64 tokens 5.1 / 16.1, of 512 10.5 / 16.2,
+// of 1024 16.6 / 17.4, of 2048 29 / 18; 1024 pairs of up to 256 17 / 23, of up to
+// 1024 38 / 40, of up to 2048 69 / 58; 2048 pairs of up to 64 22.8 / 22.4, of up to
+// 512 46 / 40.
+constexpr int kShortContext = 1024;
+constexpr int kShortPairs = 7;
+
+constexpr PiecesKind kPiecesQ8 = {pkv::kQ8Tokens, pkv::kQ8Warps, pkv::kQ8StreamHeads};
+
 PiecesGrid q8_grid(int num_seqs, int n_kv_heads, int max_context_len, int sm_count) {
-    return pieces_grid(num_seqs, n_kv_heads, max_context_len, sm_count, true, pkv::kQ8Tokens);
+    return pieces_grid(num_seqs, n_kv_heads, max_context_len, sm_count, false, kPiecesQ8);
 }
 
 pkv_status check_scales(const float* k_scale, const float* v_scale, int num_blocks) {
@@ -101,12 +112,15 @@ PKV_API pkv_status paged_attn_decode_q8(
                        max_context_len, w, workspace, *dev);
     p.k_scale = k_scale;
     p.v_scale = v_scale;
+    L.whole = max_context_len <= kShortContext &&
+              (long long)num_seqs * n_kv_heads <= (long long)kShortPairs * dev->sm_count;
     e = q_dtype == PKV_BF16 ? pkv::launch_decode_q8_bf16(head_dim, L)
                             : pkv::launch_decode_q8_f16(head_dim, L);
     if (e != cudaSuccess) return cuda_fail(e);
+    if (L.whole) return PKV_OK;
     // (pieces of a row to expect, and warps that merge them: as the shared decode)
     const long long streams =
-        (long long)(p.ctas + p.extra_ctas) * (pkv::kPieceWarps / p.stream_heads);
+        (long long)p.ctas * (pkv::kQ8Warps / p.stream_heads);
     const long long pairs = (long long)num_seqs * (n_kv_heads / p.stream_heads);
     const bool few = 2 + streams / pairs <= 12;
     const int rows = few ? pkv::kFinishWarps : 1;

@@ -67,11 +67,14 @@ def test_decode_q8(lens, H, Hk, D, B, dtype, out_dtype):
     c = ref.paged(lens, B, Hk, D, 1)
     q = _q(len(lens), H, D, dtype)
     scale = 1.0 / math.sqrt(D)
-    out = _run(c, q, scale, out_dtype, max(lens) + 3)
-    assert _clean() == 0
-    check(out, *_want(c, q, scale, out_dtype), "decode")
-    again = _run(c, q, scale, out_dtype, max(lens) + 3)
-    assert torch.equal(out, again), "not the same bits twice"
+    want = _want(c, q, scale, out_dtype)
+    # (a bound far above the lengths: in pieces, even where contexts are short)
+    for max_len in (max(lens) + 3, 20000):
+        out = _run(c, q, scale, out_dtype, max_len)
+        assert _clean() == 0
+        check(out, *want, f"decode, bound {max_len}")
+        again = _run(c, q, scale, out_dtype, max_len)
+        assert torch.equal(out, again), "not the same bits twice"
 
 
 @pytest.mark.parametrize("out_dtype", [BF, F32])
@@ -81,9 +84,10 @@ def test_scales_of_all_sizes(D, B, out_dtype):
     lens = [700, 40, 16, 1]
     c = ref.paged(lens, B, 2, D, 3, scales="wide")
     q = _q(4, 4, D, BF, gain=0.5)
-    out = _run(c, q, 0.1, out_dtype, 700)
-    assert _clean() == 0
-    check(out, *_want(c, q, 0.1, out_dtype), "wide scales")
+    for max_len in (700, 7000):
+        out = _run(c, q, 0.1, out_dtype, max_len)
+        assert _clean() == 0
+        check(out, *_want(c, q, 0.1, out_dtype), f"wide scales, bound {max_len}")
 
 
 @pytest.mark.parametrize("dtype", [BF, FP])
@@ -120,11 +124,14 @@ def test_blocks_outside_the_pool_are_left_out():
         c["tables"][0, 1], c["tables"][1, 0], c["tables"][2, 0] = -1, n_blocks, 1 << 30
         out = _run(c, q, 0.125, F32, 100)
         assert _clean() == _lib.DEVERR_BLOCK_ID
+        pieces = _run(c, q, 0.125, F32, 3000)
+        assert _clean() == _lib.DEVERR_BLOCK_ID
         gone = {0: range(B, 2 * B), 1: range(0, B), 2: range(0, min(B, 20))}
         for s, rows in gone.items():
             keep = [t for t in range(lens[s]) if t not in rows]
             c["k"][s], c["v"][s] = c["k"][s][keep], c["v"][s][keep]
         check(out, *_want(c, q, 0.125, F32), "missing blocks")
+        check(pieces, *_want(c, q, 0.125, F32), "missing blocks, in pieces")
 
 
 def test_lengths_out_of_bounds():
@@ -133,7 +140,7 @@ def test_lengths_out_of_bounds():
     q = _q(3, 2, 64, BF)
     c["lens"][1], c["lens"][2] = -3, 1000
     out = _run(c, q, 0.1, F32, 64)
-    assert _clean() & _lib.DEVERR_CONTEXT
+    assert _clean() == _lib.DEVERR_CONTEXT
     c["k"][1], c["v"][1] = c["k"][1][:0], c["v"][1][:0]
     c["k"][2], c["v"][2] = c["k"][2][:64], c["v"][2][:64]
     check(out, *_want(c, q, 0.1, F32), "clamped")
@@ -144,12 +151,12 @@ def test_nan_in_the_cache_reaches_its_own_sequence_and_head():
     q = _q(2, 4, 64, BF)
     b = int(c["tables"][0, 1])
     c["vp"].view(torch.uint8)[b, 3, 1, 5] = 0x7f
-    out = _run(c, q, 0.1, F32, 40)
-    assert _clean() == 0
-    bad = out.isnan().cpu()
-    want = torch.zeros_like(bad)
+    want = torch.zeros(2, 4, 64, dtype=torch.bool)
     want[0, 2:, 5] = True
-    assert torch.equal(bad, want)
+    for max_len in (40, 4000):
+        out = _run(c, q, 0.1, F32, max_len)
+        assert _clean() == 0
+        assert torch.equal(out.isnan().cpu(), want)
 
 
 def test_empty_pool_and_empty_contexts():
@@ -196,12 +203,13 @@ def test_taken_over_runs_and_pools_beyond_4_gb():
             check(out[s, h:h + 1], o, bound, f"sequence {s} head {h}")
 
 
-def test_streams_graphs_and_workspaces():
+@pytest.mark.parametrize("bound", [512, 5000])
+def test_streams_graphs_and_workspaces(bound):
     lens = [500, 20, 0, 333]
     c = ref.paged(lens, 16, 2, 128, 10)
     q = _q(4, 8, 128, BF).cuda()
-    want = _run(c, q.cpu(), 0.1, BF, 512)
-    n = pkv.decode_q8_workspace_bytes(4, 8, 2, 128, 16, 512)
+    want = _run(c, q.cpu(), 0.1, BF, bound)
+    n = pkv.decode_q8_workspace_bytes(4, 8, 2, 128, 16, bound)
     outs, graphs = [], []
     for i in range(2):
         out = torch.zeros_like(want)
@@ -209,7 +217,7 @@ def test_streams_graphs_and_workspaces():
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             pkv.paged_attn_decode_q8(out, q, c["kp"], c["vp"], c["ks"], c["vs"], c["tables"],
-                                     c["lens"], 0.1, 512, workspace=ws)
+                                     c["lens"], 0.1, bound, workspace=ws)
         outs.append((out, ws))
         graphs.append(g)
     streams = [torch.cuda.Stream() for _ in range(2)]
@@ -221,7 +229,7 @@ def test_streams_graphs_and_workspaces():
                 g.replay()
     for s in streams:
         s.synchronize()
-    third = _run(c, q.cpu(), 0.1, BF, 512, stream=streams[0])
+    third = _run(c, q.cpu(), 0.1, BF, bound, stream=streams[0])
     streams[0].synchronize()
     assert _clean() == 0
     for out in (outs[0][0], outs[1][0], third):
