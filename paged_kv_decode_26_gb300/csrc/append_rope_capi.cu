@@ -153,20 +153,25 @@ void launch_append(const pkv::AppendRopeParams& p, cudaStream_t stream) {
 }
 
 // Tokens from which a CTA takes a window of block_size tokens instead of one.
-constexpr int kQ8WindowFrom = 1024;
+constexpr int kQ8WindowFrom = 192;
 
-template <int D, typename T>
-void launch_append_q8(const pkv::AppendRopeParams& p, cudaStream_t stream) {
-    constexpr int J = D / 16;
-    const int window = p.num_tokens >= kQ8WindowFrom ? p.block_size : 1;
-    const int cta_heads = pkv::q8_cta_heads(D, p.block_size);
-    const int parts = (2 * p.n_kv_heads + cta_heads - 1) / cta_heads;
-    int q_heads = pkv::kRopeThreads * pkv::kQ8Items / (window * J);
+template <int D, int B, typename T>
+void launch_append_q8_of(const pkv::AppendRopeParams& p, cudaStream_t stream) {
+    constexpr int J = D / 16, heads = pkv::q8_cta_heads(D, B);
+    const int window = p.num_tokens >= kQ8WindowFrom ? B : 1;
+    const int parts = (2 * p.n_kv_heads + heads - 1) / heads;
+    int q_heads = pkv::kAppendThreads * pkv::kAppendItems / (window * J);
     q_heads = q_heads < 1 ? 1 : (q_heads > p.n_heads ? p.n_heads : q_heads);
     const int q_parts = p.n_heads > 0 ? (p.n_heads + q_heads - 1) / q_heads : 0;
     const dim3 grid((unsigned)((p.num_tokens + window - 1) / window), (unsigned)(parts + q_parts));
-    pkv::append_rope_q8_kernel<D, T>
-        <<<grid, pkv::kRopeThreads, 0, stream>>>(p, window, parts, cta_heads, q_heads);
+    pkv::append_rope_q8_kernel<D, B, T>
+        <<<grid, pkv::kAppendThreads, 0, stream>>>(p, window, parts, q_heads);
+}
+
+template <int D, typename T>
+void launch_append_q8(const pkv::AppendRopeParams& p, cudaStream_t stream) {
+    p.block_size == 16 ? launch_append_q8_of<D, 16, T>(p, stream)
+                       : launch_append_q8_of<D, 32, T>(p, stream);
 }
 
 }  // namespace

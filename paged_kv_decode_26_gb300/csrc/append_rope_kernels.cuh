@@ -236,19 +236,23 @@ __global__ void __launch_bounds__(kRopeThreads)
 // numbers are spaced relative to their size), and makes the quotients exact and
 // most kept numbers survive a new scale unchanged.
 //
-// CTA x: a window of `window` tokens, whose runs (those that start in it) it
-// takes in turn, as many at a time as fit block_size rows; y: a part of the key
-// and value heads, then parts of the query heads.
+// CTA x: a window of `window` tokens, whose runs (those that start in it) it takes;
+// y: a part of the key and value heads, then parts of the query heads.  A window is
+// one token, or block_size of them: then the rows of its runs are block_size at most
+// but for the last run, which goes by itself if it does not fit beside the others.
+// A thread holds its items from the one pass over them to the next (the largest
+// value, then the codes).
 
 constexpr float kE4m3Max = 448.f;
 constexpr int kLeastExponent = -117;           // of a scale (a block of zeros)
-constexpr int kQ8Items = 4;                    // items that a thread holds
-constexpr int kQ8Window = 32;                  // most tokens of a window
-constexpr int kQ8MaxBlock = 32;
+constexpr int kAppendThreads = 128;
+constexpr int kAppendItems = 4;                    // items that a thread holds
+constexpr int kQ8MaxBlock = 32;                // tokens of a block, and of a window
 
-// Heads that a CTA takes: block_size rows of them are kQ8Items a thread.
+// Heads that a CTA takes (a power of two): block_size rows of them are kAppendItems a
+// thread.
 __host__ __device__ constexpr int q8_cta_heads(int D, int block_size) {
-    return kRopeThreads * kQ8Items / (block_size * (D / 16));
+    return kAppendThreads * kAppendItems / (block_size * (D / 16));
 }
 
 // s(x) of a largest value x >= 0 (finite).
@@ -284,206 +288,254 @@ __device__ __forceinline__ float2 unpack_e4m3(uint16_t w) {
 
 struct Q8Row {
     int token;          // of the call
-    int run;            // index of the row's run in the batch
-    int64_t slot;
+    int run;
+    int slot_in_block;
     int position;
 };
 
+// Queries of a window of tokens: heads h0 .. h0 + heads - 1.
 template <int D, typename T>
-__global__ void __launch_bounds__(kRopeThreads)
+__device__ __forceinline__ void append_q8_queries(const AppendRopeParams& p, int w0, int w1, int h0,
+                                                  int heads) {
+    constexpr int J = D / 16, V = D / 8, kBatch = 4, kStep = kAppendThreads / J;
+    const int j = threadIdx.x % J;
+    const ItemChunks at = item_chunks(p, j);
+    // (token, head) of this thread's next item
+    int t = w0 + (int)threadIdx.x / J / heads, h = (int)threadIdx.x / J % heads;
+    ItemTurn turn;
+    int turn_of = -1;                             // position of `turn`
+    while (t < w1) {
+        uint4 a[kBatch], b[kBatch];
+        int64_t slot[kBatch];
+        int position[kBatch], token[kBatch], head[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            token[i] = t;
+            head[i] = h0 + h;
+            if (t < w1) {
+                const uint4* row = static_cast<const uint4*>(p.q.p) +
+                                   (size_t)t * (p.q.stride / 8) + head[i] * V;
+                a[i] = __ldcs(row + at.a);
+                b[i] = __ldcs(row + at.b);
+                slot[i] = p.slots[t];
+                position[i] = p.table ? p.positions[t] : 0;
+            }
+            for (h += kStep; h >= heads; h -= heads) ++t;
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (token[i] >= w1 || !token_lives(p, slot[i], position[i], false)) continue;
+            if (at.turn) {
+                if (position[i] != turn_of) {
+                    load_turn(p, position[i], j, turn);
+                    turn_of = position[i];
+                }
+                float x[16];
+                item_values<T>(a[i], b[i], x);
+                turn_item(x, turn, p.interleaved);
+                pack_item<T>(x, a[i], b[i]);
+            }
+            uint4* to = static_cast<uint4*>(p.q_out) + (size_t)token[i] * (p.q_out_stride / 8) +
+                        head[i] * V;
+            to[at.a] = a[i];
+            to[at.b] = b[i];
+        }
+    }
+}
+
+// The largest finite |x|.
+__device__ __forceinline__ float largest(const float (&x)[16]) {
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));     // (passes NaN over)
+    if (top < INFINITY) return top;
+    top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = fabsf(x[i]) < INFINITY ? fmaxf(top, fabsf(x[i])) : top;
+    return top;
+}
+
+template <int D, int B, typename T>
+__global__ void __launch_bounds__(kAppendThreads)
     append_rope_q8_kernel(const __grid_constant__ AppendRopeParams p, int window, int kv_parts,
-                          int cta_heads, int q_heads) {
+                          int q_heads) {
     constexpr int J = D / 16;
     constexpr int V = D / 8;
-    constexpr int kSpan = kQ8MaxBlock + kQ8Window + kQ8MaxBlock;
+    constexpr int HC = q8_cta_heads(D, B);
+    constexpr int kSpan = 3 * kQ8MaxBlock;
+    constexpr int kPairs = kAppendThreads * kAppendItems / J;   // rows x heads of a CTA
+    static_assert(kSpan <= kAppendThreads, "a thread per token around the window");
     __shared__ int s_blk[kSpan];              // block and row of a token's slot, -1: none
     __shared__ int s_in[kSpan];
-    __shared__ int s_pos[kSpan];
-    __shared__ int s_head[kSpan];             // distance to the run's first token, -1: in none
-    __shared__ Q8Row s_row[kQ8MaxBlock];
-    __shared__ int s_first_row[kQ8MaxBlock];  // of a run: its first row in the block
-    __shared__ int s_block[kQ8MaxBlock];
-    // of a run and head: the largest value's bits, then the scale
-    __shared__ uint32_t s_top[kRopeThreads * kQ8Items / 4];
-    __shared__ float s_old[kRopeThreads * kQ8Items / 4];
-    __shared__ int s_rows, s_runs, s_next;
+    __shared__ int s_count[2][kAppendThreads / 32];
+    __shared__ Q8Row s_row[2 * kQ8MaxBlock];
+    __shared__ int s_first_row[kQ8MaxBlock + 1];  // of a run: its first row in the block
+    __shared__ int s_block[kQ8MaxBlock + 1];
+    __shared__ int s_last_row;                // of the window's rows: the last run's first
+    // of a run and head: the largest value's bits, then the scale; the old scale
+    __shared__ uint32_t s_top[kPairs];
+    __shared__ float s_old[kPairs];
 
-    const int tid = threadIdx.x, B = p.block_size;
+    const int tid = threadIdx.x, lane = tid & 31;
     const int j = tid % J;
     const ItemChunks at = item_chunks(p, j);
     const int w0 = blockIdx.x * window, w1 = min(w0 + window, p.num_tokens);
-
     if ((int)blockIdx.y >= kv_parts) {
-        // ---- queries
         const int h0 = ((int)blockIdx.y - kv_parts) * q_heads;
-        const int heads = min(q_heads, p.n_heads - h0);
-        const int items = (w1 - w0) * heads * J;
-        for (int e = tid; e < items; e += kRopeThreads) {
-            const int h = h0 + e / J % heads, t = w0 + e / J / heads;
-            const uint4* row = static_cast<const uint4*>(p.q.p) + (size_t)t * (p.q.stride / 8) +
-                               h * V;
-            uint4 a = __ldcs(row + at.a), b = __ldcs(row + at.b);
-            const int64_t slot = p.slots[t];
-            const int position = p.table ? p.positions[t] : 0;
-            if (!token_lives(p, slot, position, false)) continue;
-            if (at.turn) {
-                float x[16];
-                item_values<T>(a, b, x);
-                ItemTurn turn;
-                load_turn(p, position, j, turn);
-                turn_item(x, turn, p.interleaved);
-                pack_item<T>(x, a, b);
-            }
-            uint4* to = static_cast<uint4*>(p.q_out) + (size_t)t * (p.q_out_stride / 8) + h * V;
-            to[at.a] = a;
-            to[at.b] = b;
-        }
+        append_q8_queries<D, T>(p, w0, w1, h0, min(q_heads, p.n_heads - h0));
         return;
     }
 
-    // ---- the tokens around the window: index i is token w0 - B + i
-    const int span = min(w1 + B - 1, p.num_tokens) - (w0 - B), shift = B == 16 ? 4 : 5;
-    for (int i = tid; i < span; i += kRopeThreads) {
-        const int t = w0 - B + i;
-        const int64_t slot = t >= 0 ? p.slots[t] : -1;
-        const int position = t >= 0 && p.table ? p.positions[t] : 0;
-        const bool here = blockIdx.y == 0 && t >= w0 && t < w1;
-        if (here) token_lives(p, slot, position, true);      // (says what is wrong)
-        const bool in_pool = slot >= 0 && slot < (int64_t)p.num_blocks * B;
-        s_blk[i] = in_pool ? (int)(slot >> shift) : -1;
-        s_in[i] = (int)(slot & (B - 1));
-        s_pos[i] = position;
-    }
-    __syncthreads();
-    for (int i = tid; i < span; i += kRopeThreads) {
-        const int block = s_blk[i];
-        int back = block < 0 ? -1 : 0;
-        if (block >= 0) {
-            // (rising rows of one block: at most B - 1 steps)
-            while (i > back && s_blk[i - back - 1] == block && s_in[i - back] > s_in[i - back - 1])
-                ++back;
-            // a token that follows one of its block but not to a later row ends
-            // the run, and what follows it there is in none
-            if (i > back && s_blk[i - back - 1] == block) {
-                back = -1;
-                const int t = w0 - B + i;
-                if (blockIdx.y == 0 && t >= w0 && t < w1) raise_error(p.errors, PKV_DEVERR_SLOT);
-            }
+    // ---- the tokens around the window: thread i looks at token w0 - B + i
+    const int span = min(w1 + B - 1, p.num_tokens) - (w0 - B);
+    const int t = w0 - B + tid;
+    const bool here = t >= w0 && t < w1;
+    int block = -1, in_block = 0, position = 0;
+    if (tid < span && t >= 0) {
+        const int64_t slot = p.slots[t];
+        position = p.table ? p.positions[t] : 0;
+        if (here && blockIdx.y == 0) token_lives(p, slot, position, true);  // (says what is wrong)
+        if (slot >= 0 && slot < (int64_t)p.num_blocks * B) {
+            block = (int)(slot / B);
+            in_block = (int)(slot % B);
         }
-        s_head[i] = back;
+    }
+    if (tid < kSpan) {
+        s_blk[tid] = block;
+        s_in[tid] = in_block;
+    }
+    for (int e = tid; e < kPairs; e += kAppendThreads) s_top[e] = 0u;
+    __syncthreads();
+    // distance to the run's first token, -1: in no run
+    int back = -1;
+    if (block >= 0) {
+        // (rising rows of one block: at most B - 1 steps)
+        int above = in_block;
+        for (back = 0; tid > back && s_blk[tid - back - 1] == block; ++back) {
+            const int below = s_in[tid - back - 1];
+            if (below >= above) break;
+            above = below;
+        }
+        // a token that follows one of its block but not to a later row ends the run,
+        // and what follows it there is in none
+        if (tid > back && s_blk[tid - back - 1] == block) {
+            back = -1;
+            if (here && blockIdx.y == 0) raise_error(p.errors, PKV_DEVERR_SLOT);
+        }
+    }
+    // ---- rows and runs of the window, in order
+    const int first = tid - back;                // index of the run's first token
+    const bool mine = back >= 0 && first >= B && first < B + (w1 - w0);
+    const unsigned rows_here = __ballot_sync(0xffffffffu, mine);
+    const unsigned runs_here = __ballot_sync(0xffffffffu, mine && back == 0);
+    if (lane == 0) {
+        s_count[0][tid / 32] = __popc(rows_here);
+        s_count[1][tid / 32] = __popc(runs_here);
     }
     __syncthreads();
+    int n_rows = 0, n_runs = 0, row0 = 0, run0 = 0;
+#pragma unroll
+    for (int w = 0; w < kAppendThreads / 32; ++w) {
+        if (w == tid / 32) {
+            row0 = n_rows;
+            run0 = n_runs;
+        }
+        n_rows += s_count[0][w];
+        n_runs += s_count[1][w];
+    }
+    if (mine) {
+        const unsigned upto = 0xffffffffu >> (31 - lane);      // lanes 0 .. lane
+        const int r = row0 + __popc(rows_here & upto) - 1, run = run0 + __popc(runs_here & upto) - 1;
+        s_row[r] = {t, run, in_block, position};
+        if (back == 0) {
+            s_first_row[run] = in_block;
+            s_block[run] = block;
+            if (run == n_runs - 1) s_last_row = r;
+        }
+    }
+    __syncthreads();
+    if (n_rows == 0) return;
 
-    const int hs0 = (int)blockIdx.y * cta_heads;             // head slots: keys, then values
-    const int heads = min(cta_heads, 2 * p.n_kv_heads - hs0);
-    int next = B;                                            // token index to go on at
-    while (next < B + (w1 - w0)) {
-        // ---- whole runs, up to B rows
-        if (tid == 0) {
-            int rows = 0, runs = 0, i = next;
-            for (; i < span; ++i) {
-                const int back = s_head[i];
-                if (back < 0) {
-                    if (i >= B + (w1 - w0)) break;
-                    continue;
-                }
-                if (back == 0) {
-                    if (i >= B + (w1 - w0)) break;           // another window's
-                    int n = 1;
-                    while (i + n < span && s_head[i + n] == n) ++n;
-                    if (rows + n > B) break;
-                    s_first_row[runs] = s_in[i];
-                    s_block[runs] = s_blk[i];
-                    ++runs;
-                } else if (i - back < next) {
-                    continue;                                // an earlier window's run
-                }
-                s_row[rows].token = w0 - B + i;
-                s_row[rows].run = runs - 1;
-                s_row[rows].slot = ((int64_t)s_blk[i] << shift) + s_in[i];
-                s_row[rows].position = s_pos[i];
-                ++rows;
-            }
-            s_rows = rows;
-            s_runs = runs;
-            s_next = i;
-        }
-        __syncthreads();
-        const int rows = s_rows, runs = s_runs;
-        next = s_next;
-        const int pairs = runs * heads;
-        for (int e = tid; e < pairs; e += kRopeThreads) {
-            const int hs = hs0 + e % heads;
-            const float* scale = hs < p.n_kv_heads ? p.k_scale + hs : p.v_scale + (hs - p.n_kv_heads);
-            s_top[e] = 0u;
-            s_old[e] = s_first_row[e / heads] > 0
-                           ? scale[(size_t)s_block[e / heads] * p.n_kv_heads]
-                           : 0.f;
-        }
-        __syncthreads();
+    const int hs0 = (int)blockIdx.y * HC;                    // head slots: keys, then values
+    const int n_slots = 2 * p.n_kv_heads;
+    const bool split = n_rows > B;                           // the last run by itself
+    for (int batch = 0; batch < (split ? 2 : 1); ++batch) {
+        const int row_lo = batch ? s_last_row : 0, row_hi = split && !batch ? s_last_row : n_rows;
+        const int run_lo = batch ? n_runs - 1 : 0, run_hi = split && !batch ? n_runs - 1 : n_runs;
+        const int pairs = (run_hi - run_lo) * HC;
+        // item n of this thread: head slot hs0 + h of row row_lo + r0 + n * kRowStep
+        constexpr int kRowStep = kAppendThreads / (J * HC);
+        static_assert(kRowStep >= 1 && kRowStep * kAppendItems == B, "items");
+        const int h = tid / J % HC, hs = hs0 + h, r0 = row_lo + tid / (J * HC);
+        const bool key = hs < p.n_kv_heads, real = hs < n_slots;
+        const int kvh = key ? hs : hs - p.n_kv_heads;
+        const uint4* const from = static_cast<const uint4*>(key ? p.k.p : p.v.p) + kvh * V;
+        const size_t stride = (size_t)(key ? p.k.stride : p.v.stride) / 8;
         // ---- values, rotated, and the largest of every run and head
-        float x[kQ8Items][16];
-        const int items = rows * heads * J;
+        float x[kAppendItems][16];
+        uint4 a[kAppendItems], b[kAppendItems];
 #pragma unroll
-        for (int n = 0; n < kQ8Items; ++n) {
-            const int e = tid + n * kRopeThreads;
-            if (e >= items) continue;
-            const int h = e / J % heads, hs = hs0 + h;
-            const Q8Row& r = s_row[e / J / heads];
-            const bool key = hs < p.n_kv_heads;
-            const RopeSource& src = key ? p.k : p.v;
-            const uint4* row = static_cast<const uint4*>(src.p) +
-                               (size_t)r.token * (src.stride / 8) +
-                               (key ? hs : hs - p.n_kv_heads) * V;
-            uint4 a = __ldcs(row + at.a), b = __ldcs(row + at.b);
-            item_values<T>(a, b, x[n]);
-            const bool lives = !p.table || (r.position >= 0 && r.position < p.table_rows);
-            float top = 0.f;
-            if (lives) {
-                if (key && at.turn) {
-                    ItemTurn turn;
-                    load_turn(p, r.position, j, turn);
-                    turn_item(x[n], turn, p.interleaved);
-                }
-                if (key && p.k_out) {
-                    if (at.turn) pack_item<T>(x[n], a, b);
-                    uint4* to = static_cast<uint4*>(p.k_out) +
-                                (size_t)r.token * (p.k_out_stride / 8) + hs * V;
-                    to[at.a] = a;
-                    to[at.b] = b;
-                }
+        for (int n = 0; n < kAppendItems; ++n) {
+            const int r = r0 + n * kRowStep;
+            if (!real || r >= row_hi) continue;
+            const uint4* row = from + s_row[r].token * stride;
+            a[n] = __ldcs(row + at.a);
+            b[n] = __ldcs(row + at.b);
+        }
+        // (the old scales come meanwhile)
+        for (int e = tid; e < pairs; e += kAppendThreads) {
+            const int es = hs0 + e % HC, run = run_lo + e / HC;
+            if (es >= n_slots) continue;
+            const float* scale = es < p.n_kv_heads ? p.k_scale + es : p.v_scale + (es - p.n_kv_heads);
+            s_old[e] = s_first_row[run] > 0 ? scale[(size_t)s_block[run] * p.n_kv_heads] : 0.f;
+        }
+        unsigned lives = 0u;                  // items that are written
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float y = fabsf(x[n][i]);
-                    top = fmaxf(top, y <= 3.4028234e38f ? y : 0.f);   // (of finite ones)
-                }
+        for (int n = 0; n < kAppendItems; ++n) {
+            const int r = r0 + n * kRowStep;
+            if (!real || r >= row_hi) continue;
+            const int position = s_row[r].position;
+            if (p.table && (position < 0 || position >= p.table_rows)) continue;
+            lives |= 1u << n;
+            item_values<T>(a[n], b[n], x[n]);
+            if (key && at.turn) {
+                ItemTurn turn;
+                load_turn(p, position, j, turn);
+                turn_item(x[n], turn, p.interleaved);
+            }
+            if (key && p.k_out) {
+                if (at.turn) pack_item<T>(x[n], a[n], b[n]);
+                uint4* to = static_cast<uint4*>(p.k_out) +
+                            (size_t)s_row[r].token * (p.k_out_stride / 8) + kvh * V;
+                to[at.a] = a[n];
+                to[at.b] = b[n];
             }
             // (a head's items are on J neighbouring lanes)
-            const unsigned group = (unsigned)((1u << J) - 1u) << (tid % 32 / J * J);
-            const uint32_t bits = __reduce_max_sync(group, __float_as_uint(top));
-            if (j == 0) atomicMax(&s_top[r.run * heads + h], bits);
+            const unsigned group = (unsigned)((1u << J) - 1u) << (lane / J * J);
+            const uint32_t bits = __reduce_max_sync(group, __float_as_uint(largest(x[n])));
+            if (j == 0) atomicMax(&s_top[(s_row[r].run - run_lo) * HC + h], bits);
         }
         __syncthreads();
         // ---- scales
-        for (int e = tid; e < pairs; e += kRopeThreads) {
-            const int run = e / heads, hs = hs0 + e % heads;
+        for (int e = tid; e < pairs; e += kAppendThreads) {
+            const int run = run_lo + e / HC, es = hs0 + e % HC;
+            if (es >= n_slots) continue;
             const float old = s_old[e];
             const float scale = fmaxf(scale_for(__uint_as_float(s_top[e])), old);
-            float* to = hs < p.n_kv_heads ? p.k_scale + hs : p.v_scale + (hs - p.n_kv_heads);
+            float* to = es < p.n_kv_heads ? p.k_scale + es : p.v_scale + (es - p.n_kv_heads);
             if (s_first_row[run] == 0 || scale != old)
                 to[(size_t)s_block[run] * p.n_kv_heads] = scale;
             s_top[e] = __float_as_uint(scale);
         }
         __syncthreads();
         // ---- new rows
+        unsigned char* const page0 = static_cast<unsigned char*>(key ? p.k_pool : p.v_pool) +
+                                     (size_t)kvh * D;
 #pragma unroll
-        for (int n = 0; n < kQ8Items; ++n) {
-            const int e = tid + n * kRopeThreads;
-            if (e >= items) continue;
-            const int h = e / J % heads, hs = hs0 + h;
-            const Q8Row& r = s_row[e / J / heads];
-            if (p.table && (r.position < 0 || r.position >= p.table_rows)) continue;
-            const float scale = __uint_as_float(s_top[r.run * heads + h]);
+        for (int n = 0; n < kAppendItems; ++n) {
+            if (!((lives >> n) & 1u)) continue;
+            const Q8Row r = s_row[r0 + n * kRowStep];
+            const float scale = __uint_as_float(s_top[(r.run - run_lo) * HC + h]);
             const float inv = exact_inverse(scale);
             if (inv > 0.f) {
 #pragma unroll
@@ -492,10 +544,8 @@ __global__ void __launch_bounds__(kRopeThreads)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) x[n][i] = __fdiv_rn(x[n][i], scale);
             }
-            const bool key = hs < p.n_kv_heads;
-            unsigned char* row = static_cast<unsigned char*>(key ? p.k_pool : p.v_pool) +
-                                 ((size_t)r.slot * p.n_kv_heads +
-                                  (key ? hs : hs - p.n_kv_heads)) * D;
+            unsigned char* row = page0 + ((size_t)s_block[r.run] * B + r.slot_in_block) *
+                                             p.n_kv_heads * D;
             *reinterpret_cast<uint2*>(row + at.a * 8) =
                 make_uint2(pack_e4m3(x[n][0], x[n][1], x[n][2], x[n][3]),
                            pack_e4m3(x[n][4], x[n][5], x[n][6], x[n][7]));
@@ -504,17 +554,17 @@ __global__ void __launch_bounds__(kRopeThreads)
                            pack_e4m3(x[n][12], x[n][13], x[n][14], x[n][15]));
         }
         // ---- kept rows of a scale that grew, a warp per run and head
-        for (int e = tid / 32; e < pairs; e += kRopeThreads / 32) {
-            const int run = e / heads, hs = hs0 + e % heads;
+        for (int e = tid / 32; e < pairs; e += kAppendThreads / 32) {
+            const int run = run_lo + e / HC, es = hs0 + e % HC;
             const float scale = __uint_as_float(s_top[e]), old = s_old[e];
             const int kept = s_first_row[run];
-            if (kept == 0 || scale == old) continue;
+            if (es >= n_slots || kept == 0 || scale == old) continue;
             const float ratio = __fdiv_rn(old, scale);
-            const bool key = hs < p.n_kv_heads;
-            unsigned char* page = static_cast<unsigned char*>(key ? p.k_pool : p.v_pool) +
+            const bool of_keys = es < p.n_kv_heads;
+            unsigned char* page = static_cast<unsigned char*>(of_keys ? p.k_pool : p.v_pool) +
                                   ((size_t)s_block[run] * B * p.n_kv_heads +
-                                   (key ? hs : hs - p.n_kv_heads)) * D;
-            for (int c = tid % 32; c < kept * (D / 16); c += 32) {
+                                   (of_keys ? es : es - p.n_kv_heads)) * D;
+            for (int c = lane; c < kept * (D / 16); c += 32) {
                 uint4* at16 = reinterpret_cast<uint4*>(page + (size_t)(c / (D / 16)) *
                                                                   p.n_kv_heads * D) +
                               c % (D / 16);
@@ -530,7 +580,11 @@ __global__ void __launch_bounds__(kRopeThreads)
                 *at16 = make_uint4(now[0], now[1], now[2], now[3]);
             }
         }
-        __syncthreads();
+        if (split && batch == 0) {
+            __syncthreads();
+            for (int e = tid; e < kPairs; e += kAppendThreads) s_top[e] = 0u;
+            __syncthreads();
+        }
     }
 }
 
