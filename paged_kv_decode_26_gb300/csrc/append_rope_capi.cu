@@ -154,24 +154,31 @@ void launch_append(const pkv::AppendRopeParams& p, cudaStream_t stream) {
 
 // Tokens from which a CTA takes a window of block_size tokens instead of one.
 constexpr int kQ8WindowFrom = 192;
+// CTAs per SM from which one takes several parts of the heads.
+constexpr int kQ8CtasPerSm = 6;
 
 template <int D, int B, typename T>
-void launch_append_q8_of(const pkv::AppendRopeParams& p, cudaStream_t stream) {
+void launch_append_q8_of(const pkv::AppendRopeParams& p, int sm_count, cudaStream_t stream) {
     constexpr int J = D / 16, heads = pkv::q8_cta_heads(D, B);
     const int window = p.num_tokens >= kQ8WindowFrom ? B : 1;
+    const int windows = (p.num_tokens + window - 1) / window;
     const int parts = (2 * p.n_kv_heads + heads - 1) / heads;
+    // parts one after the other in a CTA, as long as there are enough CTAs
+    int cta_parts = (int)((long long)windows * parts / (kQ8CtasPerSm * sm_count));
+    cta_parts = cta_parts < 1 ? 1 : (cta_parts > parts ? parts : cta_parts);
+    const int kv_ctas = (parts + cta_parts - 1) / cta_parts;
     int q_heads = pkv::kAppendThreads * pkv::kAppendItems / (window * J);
     q_heads = q_heads < 1 ? 1 : (q_heads > p.n_heads ? p.n_heads : q_heads);
     const int q_parts = p.n_heads > 0 ? (p.n_heads + q_heads - 1) / q_heads : 0;
-    const dim3 grid((unsigned)((p.num_tokens + window - 1) / window), (unsigned)(parts + q_parts));
+    const dim3 grid((unsigned)windows, (unsigned)(kv_ctas + q_parts));
     pkv::append_rope_q8_kernel<D, B, T>
-        <<<grid, pkv::kAppendThreads, 0, stream>>>(p, window, parts, q_heads);
+        <<<grid, pkv::kAppendThreads, 0, stream>>>(p, window, kv_ctas, cta_parts, q_heads);
 }
 
 template <int D, typename T>
-void launch_append_q8(const pkv::AppendRopeParams& p, cudaStream_t stream) {
-    p.block_size == 16 ? launch_append_q8_of<D, 16, T>(p, stream)
-                       : launch_append_q8_of<D, 32, T>(p, stream);
+void launch_append_q8(const pkv::AppendRopeParams& p, int sm_count, cudaStream_t stream) {
+    p.block_size == 16 ? launch_append_q8_of<D, 16, T>(p, sm_count, stream)
+                       : launch_append_q8_of<D, 32, T>(p, sm_count, stream);
 }
 
 }  // namespace
@@ -267,11 +274,11 @@ PKV_API pkv_status kv_append_rope_q8(void* k_pool, void* v_pool, float* k_scale,
     p.errors = dev->errors;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (head_dim == 128)
-        dtype == PKV_BF16 ? launch_append_q8<128, __nv_bfloat16>(p, s)
-                          : launch_append_q8<128, __half>(p, s);
+        dtype == PKV_BF16 ? launch_append_q8<128, __nv_bfloat16>(p, dev->sm_count, s)
+                          : launch_append_q8<128, __half>(p, dev->sm_count, s);
     else
-        dtype == PKV_BF16 ? launch_append_q8<64, __nv_bfloat16>(p, s)
-                          : launch_append_q8<64, __half>(p, s);
+        dtype == PKV_BF16 ? launch_append_q8<64, __nv_bfloat16>(p, dev->sm_count, s)
+                          : launch_append_q8<64, __half>(p, dev->sm_count, s);
     e = cudaGetLastError();
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
 }

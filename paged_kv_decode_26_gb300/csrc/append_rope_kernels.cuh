@@ -93,21 +93,27 @@ __device__ __forceinline__ void item_values(const uint4& a, const uint4& b, floa
     }
 }
 
-// (one product rounded, the other within the sum, written out so that a value
-// does not depend on what the compiler contracts where)
-__device__ __forceinline__ void turn_pair(float& a, float& b, float c, float s) {
-    const float x = __fmaf_rn(a, c, -__fmul_rn(b, s)), y = __fmaf_rn(a, s, __fmul_rn(b, c));
-    a = x;
-    b = y;
+// Pairs (a0, b0) and (a1, b1): one product rounded, the other within the sum, written
+// out so that a value does not depend on what the compiler contracts where.
+__device__ __forceinline__ void turn_pairs(float& a0, float& b0, float& a1, float& b1, float2 c,
+                                           float2 s) {
+    const float2 a = make_float2(a0, a1), b = make_float2(b0, b1);
+    const float2 x = __ffma2_rn(b, make_float2(-s.x, -s.y), __fmul2_rn(a, c));
+    const float2 y = __ffma2_rn(b, c, __fmul2_rn(a, s));
+    a0 = x.x;
+    a1 = x.y;
+    b0 = y.x;
+    b1 = y.y;
 }
 
 __device__ __forceinline__ void turn_item(float (&x)[16], const ItemTurn& t, int interleaved) {
-    if (interleaved) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) turn_pair(x[2 * i], x[2 * i + 1], t.c[i], t.s[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) turn_pair(x[i], x[i + 8], t.c[i], t.s[i]);
+    for (int i = 0; i < 8; i += 2) {
+        const float2 c = make_float2(t.c[i], t.c[i + 1]), s = make_float2(t.s[i], t.s[i + 1]);
+        if (interleaved)
+            turn_pairs(x[2 * i], x[2 * i + 1], x[2 * i + 2], x[2 * i + 3], c, s);
+        else
+            turn_pairs(x[i], x[i + 8], x[i + 1], x[i + 9], c, s);
     }
 }
 
@@ -152,7 +158,7 @@ __device__ __forceinline__ bool token_lives(const AppendRopeParams& p, int64_t s
 //
 // CTA x: a token; its query, key and value heads are kRopeBatch items a thread
 // at a time, all loads ahead of the first store.
-constexpr int kRopeBatch = 2;
+constexpr int kRopeBatch = 3;
 
 template <int D, typename T>
 __global__ void __launch_bounds__(kRopeThreads)
@@ -237,16 +243,16 @@ __global__ void __launch_bounds__(kRopeThreads)
 // most kept numbers survive a new scale unchanged.
 //
 // CTA x: a window of `window` tokens, whose runs (those that start in it) it takes;
-// y: a part of the key and value heads, then parts of the query heads.  A window is
-// one token, or block_size of them: then the rows of its runs are block_size at most
-// but for the last run, which goes by itself if it does not fit beside the others.
+// y: parts of the key and value heads, or of the query heads.  A window is one token,
+// or block_size of them: then the rows of its runs are block_size at most but for the
+// last run, which goes by itself if it does not fit beside the others.
 // A thread holds its items from the one pass over them to the next (the largest
-// value, then the codes).
+// value, then the codes), while the next part's rows and scales are on their way.
 
 constexpr float kE4m3Max = 448.f;
 constexpr int kLeastExponent = -117;           // of a scale (a block of zeros)
 constexpr int kAppendThreads = 128;
-constexpr int kAppendItems = 4;                    // items that a thread holds
+constexpr int kAppendItems = 2;                    // items that a thread holds
 constexpr int kQ8MaxBlock = 32;                // tokens of a block, and of a window
 
 // Heads that a CTA takes (a power of two): block_size rows of them are kAppendItems a
@@ -276,7 +282,9 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
     uint16_t lo, hi;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-    return (uint32_t)lo | (uint32_t)hi << 16;
+    uint32_t w;
+    asm("mov.b32 %0, {%1, %2};" : "=r"(w) : "h"(lo), "h"(hi));
+    return w;
 }
 
 // Two e4m3 to fp32 (exact).
@@ -347,7 +355,8 @@ __device__ __forceinline__ void append_q8_queries(const AppendRopeParams& p, int
 __device__ __forceinline__ float largest(const float (&x)[16]) {
     float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));     // (passes NaN over)
+    for (int i = 0; i < 16; i += 2)                                  // (passes NaN over)
+        asm("max.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(fabsf(x[i])), "f"(fabsf(x[i + 1])));
     if (top < INFINITY) return top;
     top = 0.f;
 #pragma unroll
@@ -357,8 +366,8 @@ __device__ __forceinline__ float largest(const float (&x)[16]) {
 
 template <int D, int B, typename T>
 __global__ void __launch_bounds__(kAppendThreads)
-    append_rope_q8_kernel(const __grid_constant__ AppendRopeParams p, int window, int kv_parts,
-                          int q_heads) {
+    append_rope_q8_kernel(const __grid_constant__ AppendRopeParams p, int window, int kv_ctas,
+                          int cta_parts, int q_heads) {
     constexpr int J = D / 16;
     constexpr int V = D / 8;
     constexpr int HC = q8_cta_heads(D, B);
@@ -372,16 +381,17 @@ __global__ void __launch_bounds__(kAppendThreads)
     __shared__ int s_first_row[kQ8MaxBlock + 1];  // of a run: its first row in the block
     __shared__ int s_block[kQ8MaxBlock + 1];
     __shared__ int s_last_row;                // of the window's rows: the last run's first
-    // of a run and head: the largest value's bits, then the scale; the old scale
-    __shared__ uint32_t s_top[kPairs];
-    __shared__ float s_old[kPairs];
+    // of a run and head (in turn): the largest value's bits, then the scale; the old one
+    __shared__ uint32_t s_top[2][kPairs];
+    __shared__ float s_old[2][kPairs];
+    static_assert(kPairs <= kAppendThreads, "a thread per run and head");
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int j = tid % J;
     const ItemChunks at = item_chunks(p, j);
     const int w0 = blockIdx.x * window, w1 = min(w0 + window, p.num_tokens);
-    if ((int)blockIdx.y >= kv_parts) {
-        const int h0 = ((int)blockIdx.y - kv_parts) * q_heads;
+    if ((int)blockIdx.y >= kv_ctas) {
+        const int h0 = ((int)blockIdx.y - kv_ctas) * q_heads;
         append_q8_queries<D, T>(p, w0, w1, h0, min(q_heads, p.n_heads - h0));
         return;
     }
@@ -404,7 +414,7 @@ __global__ void __launch_bounds__(kAppendThreads)
         s_blk[tid] = block;
         s_in[tid] = in_block;
     }
-    for (int e = tid; e < kPairs; e += kAppendThreads) s_top[e] = 0u;
+    if (tid < kPairs) s_top[0][tid] = 0u;
     __syncthreads();
     // distance to the run's first token, -1: in no run
     int back = -1;
@@ -456,44 +466,68 @@ __global__ void __launch_bounds__(kAppendThreads)
     __syncthreads();
     if (n_rows == 0) return;
 
-    const int hs0 = (int)blockIdx.y * HC;                    // head slots: keys, then values
-    const int n_slots = 2 * p.n_kv_heads;
-    const bool split = n_rows > B;                           // the last run by itself
-    for (int batch = 0; batch < (split ? 2 : 1); ++batch) {
-        const int row_lo = batch ? s_last_row : 0, row_hi = split && !batch ? s_last_row : n_rows;
-        const int run_lo = batch ? n_runs - 1 : 0, run_hi = split && !batch ? n_runs - 1 : n_runs;
-        const int pairs = (run_hi - run_lo) * HC;
-        // item n of this thread: head slot hs0 + h of row row_lo + r0 + n * kRowStep
-        constexpr int kRowStep = kAppendThreads / (J * HC);
-        static_assert(kRowStep >= 1 && kRowStep * kAppendItems == B, "items");
-        const int h = tid / J % HC, hs = hs0 + h, r0 = row_lo + tid / (J * HC);
-        const bool key = hs < p.n_kv_heads, real = hs < n_slots;
-        const int kvh = key ? hs : hs - p.n_kv_heads;
-        const uint4* const from = static_cast<const uint4*>(key ? p.k.p : p.v.p) + kvh * V;
+    // ---- parts of HC heads, each in one batch, or two with the last run by itself
+    const int n_slots = 2 * p.n_kv_heads;                    // head slots: keys, then values
+    const bool split = n_rows > B;
+    const int batches = split ? 2 : 1;
+    const int n_parts = min(cta_parts, (n_slots + HC - 1) / HC - (int)blockIdx.y * cta_parts);
+    const int n_steps = n_parts * batches;
+    // item n of this thread: row r0 + n * kRowStep of the batch, head h of the part
+    constexpr int kRowStep = kAppendThreads / (J * HC);
+    static_assert(kRowStep >= 1 && kRowStep * kAppendItems == B, "items");
+    const int h = tid / J % HC, r0 = tid / (J * HC);
+    // (a head's items are on J neighbouring lanes)
+    const unsigned group = (unsigned)((1u << J) - 1u) << (lane / J * J);
+    struct Step {
+        int hs0;                    // first head slot
+        int row_lo, row_hi, run_lo, run_hi;
+    };
+    auto step_at = [&](int i) -> Step {
+        const int batch = i % batches;
+        Step s;
+        s.hs0 = ((int)blockIdx.y * cta_parts + i / batches) * HC;
+        s.row_lo = batch ? s_last_row : 0;
+        s.row_hi = split && !batch ? s_last_row : n_rows;
+        s.run_lo = batch ? n_runs - 1 : 0;
+        s.run_hi = split && !batch ? n_runs - 1 : n_runs;
+        return s;
+    };
+    uint4 a[kAppendItems], b[kAppendItems];
+    float old = 0.f;                // thread e: old scale of run e / HC, head e % HC
+    auto fetch = [&](const Step& s) {
+        const int hs = s.hs0 + h;
+        const bool key = hs < p.n_kv_heads;
+        const uint4* const from = static_cast<const uint4*>(key ? p.k.p : p.v.p) +
+                                  (key ? hs : hs - p.n_kv_heads) * V;
         const size_t stride = (size_t)(key ? p.k.stride : p.v.stride) / 8;
-        // ---- values, rotated, and the largest of every run and head
-        float x[kAppendItems][16];
-        uint4 a[kAppendItems], b[kAppendItems];
 #pragma unroll
         for (int n = 0; n < kAppendItems; ++n) {
-            const int r = r0 + n * kRowStep;
-            if (!real || r >= row_hi) continue;
+            const int r = s.row_lo + r0 + n * kRowStep;
+            if (hs >= n_slots || r >= s.row_hi) continue;
             const uint4* row = from + s_row[r].token * stride;
             a[n] = __ldcs(row + at.a);
             b[n] = __ldcs(row + at.b);
         }
-        // (the old scales come meanwhile)
-        for (int e = tid; e < pairs; e += kAppendThreads) {
-            const int es = hs0 + e % HC, run = run_lo + e / HC;
-            if (es >= n_slots) continue;
-            const float* scale = es < p.n_kv_heads ? p.k_scale + es : p.v_scale + (es - p.n_kv_heads);
-            s_old[e] = s_first_row[run] > 0 ? scale[(size_t)s_block[run] * p.n_kv_heads] : 0.f;
-        }
+        const int run = s.run_lo + tid / HC, es = s.hs0 + tid % HC;
+        old = 0.f;
+        if (run < s.run_hi && es < n_slots && s_first_row[run] > 0)
+            old = (es < p.n_kv_heads ? p.k_scale + es : p.v_scale + (es - p.n_kv_heads))
+                [(size_t)s_block[run] * p.n_kv_heads];
+    };
+    Step now = step_at(0);
+    fetch(now);
+    for (int i = 0; i < n_steps; ++i) {
+        uint32_t* const top = s_top[i & 1];
+        const int hs = now.hs0 + h;
+        const bool key = hs < p.n_kv_heads, real = hs < n_slots;
+        const int kvh = key ? hs : hs - p.n_kv_heads;
+        // ---- values, rotated, and the largest of every run and head
+        float x[kAppendItems][16];
         unsigned lives = 0u;                  // items that are written
 #pragma unroll
         for (int n = 0; n < kAppendItems; ++n) {
-            const int r = r0 + n * kRowStep;
-            if (!real || r >= row_hi) continue;
+            const int r = now.row_lo + r0 + n * kRowStep;
+            if (!real || r >= now.row_hi) continue;
             const int position = s_row[r].position;
             if (p.table && (position < 0 || position >= p.table_rows)) continue;
             lives |= 1u << n;
@@ -510,23 +544,25 @@ __global__ void __launch_bounds__(kAppendThreads)
                 to[at.a] = a[n];
                 to[at.b] = b[n];
             }
-            // (a head's items are on J neighbouring lanes)
-            const unsigned group = (unsigned)((1u << J) - 1u) << (lane / J * J);
             const uint32_t bits = __reduce_max_sync(group, __float_as_uint(largest(x[n])));
-            if (j == 0) atomicMax(&s_top[(s_row[r].run - run_lo) * HC + h], bits);
+            if (j == 0) atomicMax(&top[(s_row[r].run - now.run_lo) * HC + h], bits);
         }
+        const float was = old;
+        const Step next = step_at(min(i + 1, n_steps - 1));
+        if (i + 1 < n_steps) fetch(next);
         __syncthreads();
         // ---- scales
-        for (int e = tid; e < pairs; e += kAppendThreads) {
-            const int run = run_lo + e / HC, es = hs0 + e % HC;
-            if (es >= n_slots) continue;
-            const float old = s_old[e];
-            const float scale = fmaxf(scale_for(__uint_as_float(s_top[e])), old);
+        const int pairs = (now.run_hi - now.run_lo) * HC;
+        if (tid < pairs && now.hs0 + tid % HC < n_slots) {
+            const int run = now.run_lo + tid / HC, es = now.hs0 + tid % HC;
+            const float scale = fmaxf(scale_for(__uint_as_float(top[tid])), was);
             float* to = es < p.n_kv_heads ? p.k_scale + es : p.v_scale + (es - p.n_kv_heads);
-            if (s_first_row[run] == 0 || scale != old)
+            if (s_first_row[run] == 0 || scale != was)
                 to[(size_t)s_block[run] * p.n_kv_heads] = scale;
-            s_top[e] = __float_as_uint(scale);
+            top[tid] = __float_as_uint(scale);
+            s_old[i & 1][tid] = was;
         }
+        if (tid < kPairs) s_top[(i + 1) & 1][tid] = 0u;
         __syncthreads();
         // ---- new rows
         unsigned char* const page0 = static_cast<unsigned char*>(key ? p.k_pool : p.v_pool) +
@@ -534,15 +570,20 @@ __global__ void __launch_bounds__(kAppendThreads)
 #pragma unroll
         for (int n = 0; n < kAppendItems; ++n) {
             if (!((lives >> n) & 1u)) continue;
-            const Q8Row r = s_row[r0 + n * kRowStep];
-            const float scale = __uint_as_float(s_top[(r.run - run_lo) * HC + h]);
+            const Q8Row r = s_row[now.row_lo + r0 + n * kRowStep];
+            const float scale = __uint_as_float(top[(r.run - now.run_lo) * HC + h]);
             const float inv = exact_inverse(scale);
             if (inv > 0.f) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[n][i] *= inv;
+                for (int c = 0; c < 16; c += 2) {
+                    const float2 y = __fmul2_rn(make_float2(x[n][c], x[n][c + 1]),
+                                                make_float2(inv, inv));
+                    x[n][c] = y.x;
+                    x[n][c + 1] = y.y;
+                }
             } else {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[n][i] = __fdiv_rn(x[n][i], scale);
+                for (int c = 0; c < 16; ++c) x[n][c] = __fdiv_rn(x[n][c], scale);
             }
             unsigned char* row = page0 + ((size_t)s_block[r.run] * B + r.slot_in_block) *
                                              p.n_kv_heads * D;
@@ -555,11 +596,12 @@ __global__ void __launch_bounds__(kAppendThreads)
         }
         // ---- kept rows of a scale that grew, a warp per run and head
         for (int e = tid / 32; e < pairs; e += kAppendThreads / 32) {
-            const int run = run_lo + e / HC, es = hs0 + e % HC;
-            const float scale = __uint_as_float(s_top[e]), old = s_old[e];
+            const int run = now.run_lo + e / HC, es = now.hs0 + e % HC;
             const int kept = s_first_row[run];
-            if (es >= n_slots || kept == 0 || scale == old) continue;
-            const float ratio = __fdiv_rn(old, scale);
+            if (es >= n_slots || kept == 0) continue;
+            const float scale = __uint_as_float(top[e]), from = s_old[i & 1][e];
+            if (scale == from) continue;
+            const float ratio = __fdiv_rn(from, scale);
             const bool of_keys = es < p.n_kv_heads;
             unsigned char* page = static_cast<unsigned char*>(of_keys ? p.k_pool : p.v_pool) +
                                   ((size_t)s_block[run] * B * p.n_kv_heads +
@@ -568,23 +610,19 @@ __global__ void __launch_bounds__(kAppendThreads)
                 uint4* at16 = reinterpret_cast<uint4*>(page + (size_t)(c / (D / 16)) *
                                                                   p.n_kv_heads * D) +
                               c % (D / 16);
-                const uint4 was = *at16;
-                const uint32_t w[4] = {was.x, was.y, was.z, was.w};
-                uint32_t now[4];
+                const uint4 codes = *at16;
+                const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+                uint32_t anew[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 lo = unpack_e4m3((uint16_t)w[i]);
-                    const float2 hi = unpack_e4m3((uint16_t)(w[i] >> 16));
-                    now[i] = pack_e4m3(lo.x * ratio, lo.y * ratio, hi.x * ratio, hi.y * ratio);
+                for (int k = 0; k < 4; ++k) {
+                    const float2 lo = unpack_e4m3((uint16_t)w[k]);
+                    const float2 hi = unpack_e4m3((uint16_t)(w[k] >> 16));
+                    anew[k] = pack_e4m3(lo.x * ratio, lo.y * ratio, hi.x * ratio, hi.y * ratio);
                 }
-                *at16 = make_uint4(now[0], now[1], now[2], now[3]);
+                *at16 = make_uint4(anew[0], anew[1], anew[2], anew[3]);
             }
         }
-        if (split && batch == 0) {
-            __syncthreads();
-            for (int e = tid; e < kPairs; e += kAppendThreads) s_top[e] = 0u;
-            __syncthreads();
-        }
+        now = next;
     }
 }
 
