@@ -734,14 +734,15 @@ PKV_API pkv_status kv_append_rope_q8(void* k_pool, void* v_pool, float* k_scale,
  *   k_scale, v_scale device float [num_blocks, n_kv_heads]: any positive numbers
  *                 (powers of two from the append, or others, e.g. calibrated ones)
  *   workspace     device, >= pkv_decode_q8_workspace_bytes(...) bytes, 256-byte
- *                 aligned; contents on entry are ignored.  Calls that may overlap
- *                 on the GPU need a workspace each.
+ *                 aligned; contents on entry are ignored; may be NULL when that size
+ *                 is 0 (few short contexts).  Calls that may overlap on the GPU need
+ *                 a workspace each.
  *   other arguments as paged_attn_decode (the split is automatic).
  * Scores, sums and outputs as in paged_attn_decode: products of the codes are exact,
  * scales stay in fp32, weights enter the second product as two F16 parts.
  * Supported shapes as paged_attn_decode; at most 65535 sequences, 4096 query
  * heads.  16 tokens in a block outside the pool are left out and flagged
- * PKV_DEVERR_BLOCK_ID.  Two launches.
+ * PKV_DEVERR_BLOCK_ID.  One launch where the workspace's size is 0, else two.
  */
 PKV_API size_t pkv_decode_q8_workspace_bytes(int num_seqs, int n_heads, int n_kv_heads,
                                              int head_dim, int block_size, int max_context_len);

@@ -59,6 +59,13 @@ def _stream_handle(stream: Optional[torch.cuda.Stream]) -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+def _stream_on(dev: int, stream: Optional[torch.cuda.Stream]) -> int:
+    """_stream_handle where the current device is known to be `dev`."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream_handle(stream)
+
+
 def _addr(t: Optional[torch.Tensor]) -> int:
     """_ptr as a plain integer."""
     return t.data_ptr() if t is not None and t.numel() else 0
@@ -699,59 +706,72 @@ def rope_table(table: torch.Tensor, inv_freq, factor: float = 1.0,
     return table
 
 
+def _row_stride(name: str, t: torch.Tensor, T: int, heads: int, D: int) -> int:
+    """_token_stride of rows [T, heads, D] whose shape is checked already (the
+    appends sit on a serving loop's critical path)."""
+    row, head, one = t.stride()
+    if one == 1 and head == D and T > 1:
+        return row
+    return _token_stride(name, t)
+
+
 def _rope_append_args(k_pool, v_pool, pool_dtype, k, v, slot_mapping, positions, rope, q, q_out,
                       k_out, interleaved) -> tuple:
     """The checked C arguments of the rotating appends behind the pools."""
-    _need_here(("k_pool", "v_pool", "slot_mapping"), (k_pool, v_pool, slot_mapping))
     dev = k_pool.get_device()
+    if dev < 0 or dev != _current_device() or not (
+            v_pool.get_device() == slot_mapping.get_device() == k.get_device()
+            == v.get_device() == dev):
+        raise ValueError("tensors must be on the current CUDA device")
     if k_pool.dim() != 4 or k.dim() != 3 or v.dim() != 3:
         raise ValueError("pools are [num_blocks, B, Hk, D], k and v [tokens, Hk, D]")
-    nb, B, Hk, D = k_pool.shape
-    T = k.shape[0]
-    if (v_pool.shape != k_pool.shape or k.shape != (T, Hk, D) or v.shape != k.shape
-            or v.dtype != k.dtype or k_pool.dtype is not pool_dtype
+    pool_shape, shape, dtype = k_pool.shape, k.shape, k.dtype
+    nb, B, Hk, D = pool_shape
+    T = shape[0]
+    if (v_pool.shape != pool_shape or shape[1] != Hk or shape[2] != D or v.shape != shape
+            or v.dtype is not dtype or k_pool.dtype is not pool_dtype
             or v_pool.dtype is not pool_dtype or slot_mapping.shape != (T,)):
         raise ValueError("inconsistent shapes or dtypes")
+    if dtype is not torch.float16 and dtype is not torch.bfloat16:
+        raise ValueError("k and v must be float16 or bfloat16")
     if slot_mapping.dtype is not torch.int64:
         raise ValueError("slot_mapping must be int64")
-    if k.dtype not in _DT:
-        raise ValueError("k and v must be float16 or bfloat16")
-    rows = [("k", k), ("v", v)]
+    if not (k_pool.is_contiguous() and v_pool.is_contiguous() and slot_mapping.is_contiguous()):
+        raise ValueError("k_pool, v_pool and slot_mapping must be contiguous")
+    pos = table = rows = rot = 0
     if rope is not None:
-        _need_here(("rope", "positions"), (rope, positions))
-        if rope.get_device() != dev:
-            raise ValueError("tensors must be on the current CUDA device")
-        if rope.dtype is not torch.float32 or rope.dim() != 2:
-            raise ValueError("rope must be float32 [positions, rotary_dim]")
-        if positions.dtype is not torch.int32 or positions.shape != (T,):
-            raise ValueError("positions must be int32 [tokens]")
-    H = 0
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out: both or neither")
-    if q is not None:
-        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or q_out.shape != q.shape:
+        if positions is None or not rope.get_device() == positions.get_device() == dev:
+            raise ValueError("rope and positions must be on the current CUDA device")
+        if rope.dtype is not torch.float32 or rope.dim() != 2 or not rope.is_contiguous():
+            raise ValueError("rope must be contiguous float32 [positions, rotary_dim]")
+        if (positions.dtype is not torch.int32 or positions.shape != (T,)
+                or not positions.is_contiguous()):
+            raise ValueError("positions must be contiguous int32 [tokens]")
+        rows, rot = rope.shape
+        pos, table = positions.data_ptr(), rope.data_ptr()
+    H = q_at = q_row = qo_at = qo_row = ko_at = ko_row = 0
+    if q is not None or q_out is not None:
+        if q is None or q_out is None:
+            raise ValueError("q and q_out: both or neither")
+        q_shape = q.shape
+        if q.dim() != 3 or q_shape[0] != T or q_shape[2] != D or q_out.shape != q_shape:
             raise ValueError("q and q_out must be [tokens, H, D]")
-        H = q.shape[1]
-        rows += [("q", q), ("q_out", q_out)]
+        if (not q.get_device() == q_out.get_device() == dev or q.dtype is not dtype
+                or q_out.dtype is not dtype):
+            raise ValueError("q and q_out must be of k's dtype, on the current CUDA device")
+        H = q_shape[1]
+        q_at, q_row = q.data_ptr(), _row_stride("q", q, T, H, D)
+        qo_at, qo_row = q_out.data_ptr(), _row_stride("q_out", q_out, T, H, D)
     if k_out is not None:
-        if k_out.shape != k.shape:
+        if k_out.shape != shape:
             raise ValueError("k_out must be shaped like k")
-        rows.append(("k_out", k_out))
-    stride = {}
-    for name, t in rows:
-        if t.get_device() != dev or t.dtype is not k.dtype:
-            raise ValueError(f"{name} must be of k's dtype, on the current CUDA device")
-        stride[name] = _token_stride(name, t)
-    return (k.data_ptr(), stride["k"], v.data_ptr(), stride["v"], _DT[k.dtype],
-            slot_mapping.data_ptr(), positions.data_ptr() if rope is not None else 0,
-            _address(rope), rope.shape[0] if rope is not None else 0,
-            rope.shape[1] if rope is not None else 0, 1 if interleaved else 0,
-            _address(q), stride.get("q", 0), _address(q_out), stride.get("q_out", 0),
-            _address(k_out), stride.get("k_out", 0), T, H, Hk, D, B, nb)
-
-
-def _address(t: Optional[torch.Tensor]) -> int:
-    return t.data_ptr() if t is not None else 0
+        if k_out.get_device() != dev or k_out.dtype is not dtype:
+            raise ValueError("k_out must be of k's dtype, on the current CUDA device")
+        ko_at, ko_row = k_out.data_ptr(), _row_stride("k_out", k_out, T, Hk, D)
+    return (k.data_ptr(), _row_stride("k", k, T, Hk, D), v.data_ptr(),
+            _row_stride("v", v, T, Hk, D), _DT[dtype], slot_mapping.data_ptr(), pos, table, rows,
+            rot, 1 if interleaved else 0, q_at, q_row, qo_at, qo_row, ko_at, ko_row, T, H, Hk, D,
+            B, nb)
 
 
 def kv_append_rope(k_pool: torch.Tensor, v_pool: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -767,16 +787,18 @@ def kv_append_rope(k_pool: torch.Tensor, v_pool: torch.Tensor, k: torch.Tensor, 
     are left out."""
     args = _rope_append_args(k_pool, v_pool, k.dtype, k, v, slot_mapping, positions, rope, q,
                              q_out, k_out, interleaved)
-    check(lib().kv_append_rope(k_pool.data_ptr(), v_pool.data_ptr(), *args,
-                               _stream_handle(stream)), "kv_append_rope")
+    st = lib().kv_append_rope(k_pool.data_ptr(), v_pool.data_ptr(), *args,
+                              _stream_on(k_pool.get_device(), stream))
+    if st:
+        check(st, "kv_append_rope")
 
 
-def _need_scales(k_pool, k_scale, v_scale) -> None:
-    _need_here(("k_pool", "k_scale", "v_scale"), (k_pool, k_scale, v_scale))
-    want = (k_pool.shape[0], k_pool.shape[2])
+def _need_scales(dev: int, nb: int, Hk: int, k_scale: torch.Tensor, v_scale: torch.Tensor) -> None:
     for t in (k_scale, v_scale):
-        if t.dtype is not torch.float32 or t.shape != want:
+        if t.dtype is not torch.float32 or t.shape != (nb, Hk):
             raise ValueError("k_scale and v_scale must be float32 [num_blocks, Hk]")
+        if t.get_device() != dev or not t.is_contiguous():
+            raise ValueError("k_scale and v_scale must be contiguous, on the current CUDA device")
 
 
 def kv_append_rope_q8(k_pool: torch.Tensor, v_pool: torch.Tensor, k_scale: torch.Tensor,
@@ -792,16 +814,43 @@ def kv_append_rope_q8(k_pool: torch.Tensor, v_pool: torch.Tensor, k_scale: torch
     tokens of one block follow one another in the call, in order."""
     args = _rope_append_args(k_pool, v_pool, torch.float8_e4m3fn, k, v, slot_mapping, positions,
                              rope, q, q_out, k_out, interleaved)
-    _need_scales(k_pool, k_scale, v_scale)
-    check(lib().kv_append_rope_q8(k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(),
-                                  v_scale.data_ptr(), *args, _stream_handle(stream)),
-          "kv_append_rope_q8")
+    dev = k_pool.get_device()
+    _need_scales(dev, args[-1], args[-4], k_scale, v_scale)
+    st = lib().kv_append_rope_q8(k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(),
+                                 v_scale.data_ptr(), *args, _stream_on(dev, stream))
+    if st:
+        check(st, "kv_append_rope_q8")
 
 
 def decode_q8_workspace_bytes(num_seqs: int, n_heads: int, n_kv_heads: int, head_dim: int,
                               block_size: int, max_context_len: int) -> int:
     return int(lib().pkv_decode_q8_workspace_bytes(num_seqs, n_heads, n_kv_heads, head_dim,
                                                    block_size, max_context_len))
+
+
+def _q8_args(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens) -> tuple:
+    """Checks what the 8-bit attention calls share; (heads of q, pool shape)."""
+    dev = out.get_device()
+    if dev < 0 or dev != _current_device():
+        raise ValueError("tensors must be on the current CUDA device")
+    for t in (out, q, k_pool, v_pool, block_tables, context_lens):
+        if t.get_device() != dev or not t.is_contiguous():
+            raise ValueError("tensors must be contiguous, on the current CUDA device")
+    if q.dim() != 3 or k_pool.dim() != 4:
+        raise ValueError("q is [rows, H, D], pools are [num_blocks, B, Hk, D]")
+    q_shape, pool_shape = q.shape, k_pool.shape
+    nb, B, Hk, D = pool_shape
+    if (q_shape[2] != D or v_pool.shape != pool_shape or out.shape != q_shape
+            or k_pool.dtype is not torch.float8_e4m3fn or v_pool.dtype is not torch.float8_e4m3fn
+            or block_tables.dim() != 2 or context_lens.dim() != 1
+            or block_tables.shape[0] != context_lens.shape[0]):
+        raise ValueError("inconsistent shapes or dtypes")
+    if q.dtype not in _DT or out.dtype not in _DT:
+        raise ValueError("q must be 16-bit, out 16-bit or float32")
+    if block_tables.dtype is not torch.int32 or context_lens.dtype is not torch.int32:
+        raise ValueError("block_tables and context_lens must be int32")
+    _need_scales(dev, nb, Hk, k_scale, v_scale)
+    return q_shape[1], nb, B, Hk, D
 
 
 def paged_attn_decode_q8(out: torch.Tensor, q: torch.Tensor, k_pool: torch.Tensor,
@@ -811,30 +860,28 @@ def paged_attn_decode_q8(out: torch.Tensor, q: torch.Tensor, k_pool: torch.Tenso
                          stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """paged_attn_decode over float8_e4m3fn pools [num_blocks, B, Hk, D] with
     scales fp32 [num_blocks, Hk] for each block and kv head; q is 16-bit."""
-    _need_here(_DECODE_NAMES + ("k_scale", "v_scale"),
-               (out, q, k_pool, v_pool, block_tables, context_lens, k_scale, v_scale))
-    _need_ints(("block_tables", "context_lens"), (block_tables, context_lens))
-    S, H, D = q.shape
-    nb, B, Hk, D2 = k_pool.shape
-    if (D2 != D or v_pool.shape != k_pool.shape or out.shape != q.shape
-            or k_pool.dtype is not torch.float8_e4m3fn or v_pool.dtype is not torch.float8_e4m3fn
-            or k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32
-            or k_scale.shape != (nb, Hk) or v_scale.shape != (nb, Hk)
-            or block_tables.dim() != 2 or block_tables.shape[0] != S
-            or context_lens.shape != (S,)):
+    H, nb, B, Hk, D = _q8_args(out, q, k_pool, v_pool, k_scale, v_scale, block_tables,
+                               context_lens)
+    S = context_lens.shape[0]
+    if q.shape[0] != S:
         raise ValueError("inconsistent shapes or dtypes")
     max_context_len = int(max_context_len)
+    ws_at = ws_bytes = 0
     if workspace is None:
-        workspace = _stream_buffer(
-            lib().pkv_decode_q8_workspace_bytes(S, H, Hk, D, B, max_context_len), q.device, stream)
+        ws_bytes = lib().pkv_decode_q8_workspace_bytes(S, H, Hk, D, B, max_context_len)
+        if ws_bytes:
+            workspace = _stream_buffer(ws_bytes, q.device, stream)
+            ws_at = workspace.data_ptr()
     else:
         _need_here(("workspace",), (workspace,))
+        ws_at, ws_bytes = workspace.data_ptr(), workspace.nbytes
     st = lib().paged_attn_decode_q8(
         out.data_ptr(), _DT[out.dtype], q.data_ptr(), _DT[q.dtype], k_pool.data_ptr(),
         v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(),
         block_tables.shape[1], context_lens.data_ptr(), S, H, Hk, D, B, nb, float(scale),
-        max_context_len, workspace.data_ptr(), workspace.nbytes, _stream_handle(stream))
-    check(st, "paged_attn_decode_q8")
+        max_context_len, ws_at, ws_bytes, _stream_on(q.get_device(), stream))
+    if st:
+        check(st, "paged_attn_decode_q8")
     return out
 
 
@@ -846,26 +893,21 @@ def paged_attn_multi_query_q8(out: torch.Tensor, q: torch.Tensor, q_start: torch
                               stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """paged_attn_multi_query over float8_e4m3fn pools with scales fp32
     [num_blocks, Hk] for each block and kv head; q is 16-bit."""
-    _need_here(_DECODE_NAMES + ("q_start", "k_scale", "v_scale"),
-               (out, q, k_pool, v_pool, block_tables, context_lens, q_start, k_scale, v_scale))
-    _need_ints(("q_start", "block_tables", "context_lens"), (q_start, block_tables, context_lens))
-    T, H, D = q.shape
-    nb, B, Hk, D2 = k_pool.shape
-    S = context_lens.shape[0]
-    if (D2 != D or v_pool.shape != k_pool.shape or out.shape != q.shape
-            or k_pool.dtype is not torch.float8_e4m3fn or v_pool.dtype is not torch.float8_e4m3fn
-            or k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32
-            or k_scale.shape != (nb, Hk) or v_scale.shape != (nb, Hk)
-            or block_tables.dim() != 2 or block_tables.shape[0] != S
-            or context_lens.dim() != 1 or q_start.shape != (S + 1,)):
-        raise ValueError("inconsistent shapes or dtypes")
+    H, nb, B, Hk, D = _q8_args(out, q, k_pool, v_pool, k_scale, v_scale, block_tables,
+                               context_lens)
+    T, S = q.shape[0], context_lens.shape[0]
+    if q_start.get_device() != q.get_device() or not q_start.is_contiguous():
+        raise ValueError("q_start must be contiguous, on the current CUDA device")
+    if q_start.dtype is not torch.int32 or q_start.shape != (S + 1,):
+        raise ValueError("q_start must be int32 [S + 1]")
     st = lib().paged_attn_multi_query_q8(
         out.data_ptr(), _DT[out.dtype], q.data_ptr(), _DT[q.dtype], q_start.data_ptr(), T,
         int(max_q_len), k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(),
         v_scale.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
         context_lens.data_ptr(), S, H, Hk, D, B, nb, float(scale), int(max_context_len),
-        _stream_handle(stream))
-    check(st, "paged_attn_multi_query_q8")
+        _stream_on(q.get_device(), stream))
+    if st:
+        check(st, "paged_attn_multi_query_q8")
     return out
 
 

@@ -44,6 +44,10 @@ cudaError_t encode_q8_map(CUtensorMap* map, const void* pool, int num_blocks, in
 // 512 46 / 40.
 constexpr int kShortContext = 1024;
 constexpr int kShortPairs = 7;
+bool whole_contexts(int num_seqs, int n_kv_heads, int max_context_len, int sm_count) {
+    return max_context_len <= kShortContext &&
+           (long long)num_seqs * n_kv_heads <= (long long)kShortPairs * sm_count;
+}
 
 constexpr PiecesKind kPiecesQ8 = {pkv::kQ8Tokens, pkv::kQ8Warps, pkv::kQ8StreamHeads};
 
@@ -72,6 +76,7 @@ PKV_API size_t pkv_decode_q8_workspace_bytes(int num_seqs, int n_heads, int n_kv
         return 0;
     DeviceInfo* dev = nullptr;
     const int sms = device_info(&dev) == cudaSuccess ? dev->sm_count : kDefaultSms;
+    if (whole_contexts(num_seqs, n_kv_heads, max_context_len, sms)) return 0;
     return pieces_workspace(num_seqs, n_heads, n_kv_heads, head_dim,
                             q8_grid(num_seqs, n_kv_heads, max_context_len, sms))
         .end;
@@ -95,9 +100,10 @@ PKV_API pkv_status paged_attn_decode_q8(
     const PiecesGrid pieces = q8_grid(num_seqs, n_kv_heads, max_context_len, dev->sm_count);
     const PiecesWorkspace w =
         pieces_workspace(num_seqs, n_heads, n_kv_heads, head_dim, pieces);
-    if ((st = check_workspace(workspace, workspace_bytes, w.end)) != PKV_OK) return st;
     pkv::Q8Launch L;
     std::memset(&L, 0, sizeof(L));
+    L.whole = whole_contexts(num_seqs, n_kv_heads, max_context_len, dev->sm_count);
+    if (!L.whole && (st = check_workspace(workspace, workspace_bytes, w.end)) != PKV_OK) return st;
     L.stream = static_cast<cudaStream_t>(stream);
     // (without blocks nothing is loaded; the maps need some valid tensor)
     const int map_blocks = num_blocks > 0 ? num_blocks : 1;
@@ -112,8 +118,6 @@ PKV_API pkv_status paged_attn_decode_q8(
                        max_context_len, w, workspace, *dev);
     p.k_scale = k_scale;
     p.v_scale = v_scale;
-    L.whole = max_context_len <= kShortContext &&
-              (long long)num_seqs * n_kv_heads <= (long long)kShortPairs * dev->sm_count;
     e = q_dtype == PKV_BF16 ? pkv::launch_decode_q8_bf16(head_dim, L)
                             : pkv::launch_decode_q8_f16(head_dim, L);
     if (e != cudaSuccess) return cuda_fail(e);

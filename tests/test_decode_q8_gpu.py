@@ -213,7 +213,7 @@ def test_streams_graphs_and_workspaces(bound):
     outs, graphs = [], []
     for i in range(2):
         out = torch.zeros_like(want)
-        ws = torch.full((n,), 0xff, dtype=torch.uint8, device="cuda")
+        ws = torch.full((max(n, 256),), 0xff, dtype=torch.uint8, device="cuda")
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             pkv.paged_attn_decode_q8(out, q, c["kp"], c["vp"], c["ks"], c["vs"], c["tables"],
@@ -276,6 +276,7 @@ def test_binding_refusals():
         args[i] = bad
         with pytest.raises(ValueError):
             pkv.paged_attn_decode_q8(*args)
+    ok[-1] = 5000
     with pytest.raises(pkv.PagedKVError):
         pkv.paged_attn_decode_q8(*ok, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     assert _clean() == 0
