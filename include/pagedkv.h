@@ -775,15 +775,24 @@ PKV_API pkv_status paged_attn_decode_q8(
  * Softmax weights enter the second product rounded once to F16 (F32 outputs: two
  * parts).  Sums over very long contexts come out short by up to 2^-23 per 16 keys.
  * Supported shapes as paged_attn_decode; at most 65535 sequences, 4096 query heads.
- * On tcgen05, 256 rows (tokens x query heads of a kv head) at a time.  One launch, no
- * workspace.
+ *   workspace    device, >= pkv_multi_query_q8_workspace_bytes(...) bytes, 256-byte
+ *                aligned; contents on entry are ignored; may be NULL when that size is
+ *                0 (chunks that fill the SMs).  Calls that may overlap on the GPU need
+ *                a workspace each.
+ * On tcgen05, 256 rows (tokens x query heads of a kv head) at a time; where those are
+ * few their keys are cut into parts, merged by a second launch.
  */
+PKV_API size_t pkv_multi_query_q8_workspace_bytes(int num_seqs, int max_q_len, int n_heads,
+                                                  int n_kv_heads, int head_dim, int block_size,
+                                                  int max_context_len);
+
 PKV_API pkv_status paged_attn_multi_query_q8(
     void* out, pkv_dtype out_dtype, const void* q, pkv_dtype q_dtype, const int32_t* q_start,
     int total_q, int max_q_len, const void* k_pool, const void* v_pool, const float* k_scale,
     const float* v_scale, const int32_t* block_tables, int max_blocks_per_seq,
     const int32_t* context_lens, int num_seqs, int n_heads, int n_kv_heads, int head_dim,
-    int block_size, int num_blocks, float scale, int max_context_len, void* stream);
+    int block_size, int num_blocks, float scale, int max_context_len, void* workspace,
+    size_t workspace_bytes, void* stream);
 
 /*
  * swap_blocks -- batched block copy ([SWAP] swap_blocks; [OPT] "Swap Blocks

@@ -78,7 +78,8 @@ SIGNATURES = {
     "paged_attn_decode_q8": (_i, [_p, _i, _p, _i, _p, _p, _p, _p, _p, _i, _p, _i, _i, _i, _i, _i,
                                   _i, _f, _i, _p, _sz, _p]),
     "paged_attn_multi_query_q8": (_i, [_p, _i, _p, _i, _p, _i, _i, _p, _p, _p, _p, _p, _i, _p, _i,
-                                       _i, _i, _i, _i, _i, _f, _i, _p]),
+                                       _i, _i, _i, _i, _i, _f, _i, _p, _sz, _p]),
+    "pkv_multi_query_q8_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
     "swap_blocks": (_i, [_p, _p, _sz, _p, _i, _i64, _i64, _p]),
     "swap_blocks_kv": (_i, [_p, _p, _p, _p, _sz, _p, _i, _i64, _i64, _p]),
     "pkv_block_manager_create": (_p, [_i, _i]),

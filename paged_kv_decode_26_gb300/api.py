@@ -885,11 +885,17 @@ def paged_attn_decode_q8(out: torch.Tensor, q: torch.Tensor, k_pool: torch.Tenso
     return out
 
 
+def multi_query_q8_workspace_bytes(num_seqs: int, max_q_len: int, n_heads: int, n_kv_heads: int,
+                                   head_dim: int, block_size: int, max_context_len: int) -> int:
+    return int(lib().pkv_multi_query_q8_workspace_bytes(num_seqs, max_q_len, n_heads, n_kv_heads,
+                                                        head_dim, block_size, max_context_len))
+
+
 def paged_attn_multi_query_q8(out: torch.Tensor, q: torch.Tensor, q_start: torch.Tensor,
                               k_pool: torch.Tensor, v_pool: torch.Tensor, k_scale: torch.Tensor,
                               v_scale: torch.Tensor, block_tables: torch.Tensor,
                               context_lens: torch.Tensor, scale: float, max_q_len: int,
-                              max_context_len: int,
+                              max_context_len: int, workspace: Optional[torch.Tensor] = None,
                               stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """paged_attn_multi_query over float8_e4m3fn pools with scales fp32
     [num_blocks, Hk] for each block and kv head; q is 16-bit."""
@@ -900,12 +906,23 @@ def paged_attn_multi_query_q8(out: torch.Tensor, q: torch.Tensor, q_start: torch
         raise ValueError("q_start must be contiguous, on the current CUDA device")
     if q_start.dtype is not torch.int32 or q_start.shape != (S + 1,):
         raise ValueError("q_start must be int32 [S + 1]")
+    max_q_len, max_context_len = int(max_q_len), int(max_context_len)
+    ws_at = ws_bytes = 0
+    if workspace is None:
+        ws_bytes = lib().pkv_multi_query_q8_workspace_bytes(S, max_q_len, H, Hk, D, B,
+                                                            max_context_len)
+        if ws_bytes:
+            workspace = _stream_buffer(ws_bytes, q.device, stream)
+            ws_at = workspace.data_ptr()
+    else:
+        _need_here(("workspace",), (workspace,))
+        ws_at, ws_bytes = workspace.data_ptr(), workspace.nbytes
     st = lib().paged_attn_multi_query_q8(
         out.data_ptr(), _DT[out.dtype], q.data_ptr(), _DT[q.dtype], q_start.data_ptr(), T,
-        int(max_q_len), k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(),
+        max_q_len, k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(),
         v_scale.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
-        context_lens.data_ptr(), S, H, Hk, D, B, nb, float(scale), int(max_context_len),
-        _stream_on(q.get_device(), stream))
+        context_lens.data_ptr(), S, H, Hk, D, B, nb, float(scale), max_context_len, ws_at,
+        ws_bytes, _stream_on(q.get_device(), stream))
     if st:
         check(st, "paged_attn_multi_query_q8")
     return out

@@ -51,6 +51,12 @@ struct Mq8Params : MultiQueryParams {
     const float* k_scale;
     const float* v_scale;
     int q_bf16;
+    // the keys of a pair of row tiles in `splits` parts, a CTA each; partial states at
+    // unit ((s * max_q_len + token) * n_heads + head) * splits + part
+    int splits;
+    int block_size;
+    float* part_o;             // [units, D], normalised
+    float* part_ml;            // [units, 2]
 };
 
 // Of a key tile's groups of 16 keys: a, log2 b and 1 / b, and whether there is a page.
@@ -102,6 +108,59 @@ __device__ __forceinline__ uint32_t mq8_nans(uint32_t w) {
     return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
 }
 
+// Rows of key parts, merged: a warp per row (token, head) of sequence blockIdx.y.
+constexpr int kMq8MergeThreads = 128;
+template <int D>
+__global__ void __launch_bounds__(kMq8MergeThreads)
+    multi_query_q8_merge_kernel(const __grid_constant__ Mq8Params p) {
+    constexpr int V = D / 32;
+    dependency_wait();
+    const int s = blockIdx.y, lane = threadIdx.x & 31;
+    const int i = (int)(blockIdx.x * (kMq8MergeThreads / 32) + (threadIdx.x >> 5));
+    const int tok = i / p.n_heads;
+    const int qs0 = p.q_start[s], qs1 = p.q_start[s + 1], q_len = qs1 - qs0;
+    const int n = p.context_lens[s];
+    // (what the kernel ahead left out has no partial states)
+    if (q_len < 0 || q_len > n || qs0 < 0 || qs1 > p.total_q || q_len > p.max_q_len ||
+        n > (long long)p.max_pages * p.block_size ||
+        n > (long long)p.max_blocks_per_seq * p.block_size || tok >= q_len)
+        return;
+    const size_t unit = ((size_t)s * p.max_q_len * p.n_heads + i) * p.splits;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    for (int k = lane; k < p.splits; k += 32)
+        ml = join_ml(ml, *reinterpret_cast<const float2*>(p.part_ml + 2 * (unit + k)));
+#pragma unroll
+    for (int off = 16; off; off /= 2)
+        ml = join_ml(ml, make_float2(__shfl_xor_sync(0xffffffffu, ml.x, off),
+                                     __shfl_xor_sync(0xffffffffu, ml.y, off)));
+    const float inv = ml.y != 0.f ? 1.f / ml.y : 0.f;
+    float o[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[e] = 0.f;
+    for (int k = 0; k < p.splits; ++k) {
+        const float2 a = *reinterpret_cast<const float2*>(p.part_ml + 2 * (unit + k));
+        if (a.y == 0.f) continue;                  // (nothing was written for it)
+        const float f = a.y * exp2f(a.x - ml.x) * inv;
+        const float* row = p.part_o + (unit + k) * D + lane * V;
+#pragma unroll
+        for (int e = 0; e < V; e += 2) {
+            const float2 x = *reinterpret_cast<const float2*>(row + e);
+            o[e] += f * x.x;
+            o[e + 1] += f * x.y;
+        }
+    }
+    const size_t at = ((size_t)qs0 * p.n_heads + i) * D + lane * V;
+#pragma unroll
+    for (int e = 0; e < V; e += 2) {
+        if (p.out_dtype == PKV_F32)
+            *reinterpret_cast<float2*>(reinterpret_cast<float*>(p.out) + at + e) =
+                make_float2(o[e], o[e + 1]);
+        else
+            *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(p.out) + at + e) =
+                pack_out(o[e], o[e + 1], p.out_dtype);
+    }
+}
+
 template <int D, int BS, int PARTS>
 __global__ void __launch_bounds__(kMq8Threads, 1)
     multi_query_q8_kernel(const __grid_constant__ Mq8Params p) {
@@ -109,6 +168,7 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
     using Range = WeightRange<__half>;
     constexpr int STAGES = Z::STAGES;
     constexpr int kParts = 2 * Z::HALVES;          // 16-byte parts of 16 keys' codes per lane
+    launch_dependents();
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     unsigned char* sm = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
@@ -131,13 +191,16 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
         longest_first(p, reinterpret_cast<int*>(sKV), tile, kvh, s);   // (sKV: not yet in use)
         __syncthreads();
     }
+    const int part = tile % p.splits;
+    tile /= p.splits;
     const int G = p.group, QT = kMq8Rows / G;
     const int qs0 = p.q_start[s], qs1 = p.q_start[s + 1];
     const int n = p.context_lens[s];
     const int q_len = qs1 - qs0;
     if (q_len < 0 || q_len > n || qs0 < 0 || qs1 > p.total_q || q_len > p.max_q_len ||
         n > (long long)p.max_pages * BS || n > (long long)p.max_blocks_per_seq * BS) {
-        if (tile == 0 && kvh == 0 && threadIdx.x == 0) raise_error(p.errors, PKV_DEVERR_CONTEXT);
+        if (tile == 0 && part == 0 && kvh == 0 && threadIdx.x == 0)
+            raise_error(p.errors, PKV_DEVERR_CONTEXT);
         return;
     }
     const int tok_lo = tile * 2 * QT;
@@ -145,9 +208,25 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
     const int pos0 = n - q_len + tok_lo;             // position of row tile 0's first token
     const int rows = min(q_len - tok_lo, 2 * QT);    // tokens of this CTA
     const int n_keys = pos0 + rows;                  // keys that some row sees
-    const int nt0 = (pos0 + min(rows, QT) + kMq8Keys - 1) / kMq8Keys;
-    const int nt1 = rows > QT ? (n_keys + kMq8Keys - 1) / kMq8Keys : 0;
+    // key tiles that the row tiles see, and of them those of this part: j0 + 0, 1, ..
+    const int see0 = (pos0 + min(rows, QT) + kMq8Keys - 1) / kMq8Keys;
+    const int see1 = rows > QT ? (n_keys + kMq8Keys - 1) / kMq8Keys : 0;
+    const int part_tiles = (max(see0, see1) + p.splits - 1) / p.splits;
+    const int j0 = part * part_tiles;
+    const int nt0 = min(max(see0 - j0, 0), part_tiles), nt1 = min(max(see1 - j0, 0), part_tiles);
     const int n_tiles = max(nt0, nt1);
+    // partial state of row r of row tile t (token t * QT + r / G of the CTA)
+    auto unit_of = [&](int t, int r) -> size_t {
+        return (((size_t)s * p.max_q_len + tok_lo + t * QT + r / G) * p.n_heads + kvh * G + r % G) *
+                   p.splits + part;
+    };
+    if (n_tiles == 0) {
+        for (int i = threadIdx.x; i < 2 * kMq8Rows; i += kMq8Threads)
+            if (i / kMq8Rows * QT + i % kMq8Rows / G < rows)
+                *reinterpret_cast<float2*>(p.part_ml + 2 * unit_of(i / kMq8Rows, i % kMq8Rows)) =
+                    make_float2(-INFINITY, 0.f);
+        return;
+    }
 
     if (warp == 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -258,8 +337,8 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
         // task k: keys 16 (k % 8) .. + 15 of operand k / 8 (K_0, V_0, K_1, ...)
         const unsigned n_tasks = 16u * n_tiles;
         const int* table = p.block_tables + (size_t)s * p.max_blocks_per_seq;
-        const unsigned guard_from = (unsigned)(pos0 + 1) / kMq8Keys;   // first tile that not
-                                                                       // every row sees all of
+        // first tile that not every row sees all of
+        const unsigned guard_from = (unsigned)max((pos0 + 1) / kMq8Keys - j0, 0);
         // Part i of a task: rows 8 (i / HALVES) + lane / 4, 16 codes from 64 (i %
         // HALVES) + 16 (lane % 4) on.  So eight lanes store to eight bank groups.
         const int r0 = lane / 4, u = lane % 4;
@@ -268,7 +347,9 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
         const size_t mine = r0 * row_bytes + (size_t)kvh * D + u * 16;
         const unsigned char* const k_mine = static_cast<const unsigned char*>(p.k_pool) + mine;
         const unsigned char* const v_mine = static_cast<const unsigned char*>(p.v_pool) + mine;
-        auto first_key = [&](unsigned k) -> int { return (int)((k / 16) * kMq8Keys + (k % 8) * 16); };
+        auto first_key = [&](unsigned k) -> int {
+            return (j0 + (int)(k / 16)) * kMq8Keys + (int)(k % 8) * 16;
+        };
         // table entry of a task's keys (looked at a task later, when it is there)
         auto entry_of = [&](unsigned k) -> int {
             const int key = first_key(k);
@@ -369,6 +450,8 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
         const int t = warp >> 2;
         const int r = (warp & 3) * 32 + lane;
         const int nt = t ? nt1 : nt0;
+        if (nt == 0 && p.splits > 1 && t * QT + r / G < rows)
+            *reinterpret_cast<float2*>(p.part_ml + 2 * unit_of(t, r)) = make_float2(-INFINITY, 0.f);
         if (nt > 0) {
             const int tok = t * QT + r / G;
             const bool real = tok < rows;
@@ -487,7 +570,7 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const Mq8Scale& sc = s_scale[j % kMq8Scales];
-                const int key0 = j * kMq8Keys;
+                const int key0 = (j0 + j) * kMq8Keys;
                 const uint2 pages = *reinterpret_cast<const uint2*>(sc.page);
                 const bool whole = key0 + kMq8Keys - 1 <= warp_pos &&
                                    (pages.x & pages.y) == 0x01010101u;
@@ -616,6 +699,9 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
             if (ok) {
                 tc_fence_after();
                 const float inv = l != 0.f ? __frcp_rn(l) : 0.f;
+                if (p.splits > 1 && real)
+                    *reinterpret_cast<float2*>(p.part_ml + 2 * unit_of(t, r)) =
+                        make_float2(m, l * exp2f(lb - Range::LIFT));
                 const bool poison = *reinterpret_cast<volatile int*>(s_poison) != 0;
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
@@ -628,7 +714,8 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
                     if (poison) {
                         // NaN that was taken out of V, from the rows that see it
 #pragma unroll 1
-                        for (int key = pos0 / kMq8Keys * kMq8Keys; key <= pos; ++key) {
+                        for (int key = max(pos0 / kMq8Keys, j0) * kMq8Keys;
+                             key <= min(pos, (j0 + part_tiles) * kMq8Keys - 1); ++key) {
                             const int b = p.block_tables[(size_t)s * p.max_blocks_per_seq + key / BS];
                             if (b < 0 || b >= p.num_blocks) continue;
                             const unsigned char* v =
@@ -639,8 +726,13 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
                                 if ((v[c] & 0x7f) == 0x7f) o[c] = NAN;
                         }
                     }
-                    const size_t at = row * D + c0;
-                    if (p.out_dtype == PKV_F32) {
+                    const size_t at = (p.splits > 1 ? unit_of(t, r) : row) * D + c0;
+                    if (p.splits > 1) {
+                        float4* o4 = reinterpret_cast<float4*>(p.part_o + at);
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4)
+                            o4[c / 4] = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                    } else if (p.out_dtype == PKV_F32) {
                         float4* o4 = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at);
 #pragma unroll
                         for (int c = 0; c < 32; c += 4)

@@ -61,6 +61,35 @@ pkv_status check_scales(const float* k_scale, const float* v_scale, int num_bloc
     return PKV_OK;
 }
 
+// Parts that the keys of a chunk's row tiles are cut into: where the pairs of row
+// tiles leave most SMs idle, as many as fill them, each of kPartTiles key tiles at
+// least (a part costs its merge and a launch; GB300, 1 chunk of 512 tokens, 32 query and 8
+// kv heads, context 600: 23.1 us whole, 27.8 in parts of two key tiles; of 100 tokens at
+// context 8192: 120 us whole, 39 in parts; 2 chunks of 2 tokens, 4 heads, 16000: 229 / 27).
+constexpr int kPartTiles = 4;
+struct ChunkShape {
+    int tiles;            // pairs of row tiles of the longest chunk allowed
+    int splits;
+    size_t o, ml, end;    // workspace
+};
+ChunkShape chunk_shape(int num_seqs, int max_q_len, int n_heads, int n_kv_heads, int head_dim,
+                       int max_context_len, int sm_count) {
+    ChunkShape c;
+    const int G = n_heads / n_kv_heads, cta_tokens = 2 * pkv::kMq8Rows / G;
+    c.tiles = (int)(((long long)max_q_len + cta_tokens - 1) / cta_tokens);
+    const long long ctas = (long long)c.tiles * n_kv_heads * num_seqs;
+    const long long key_tiles = ((long long)max_context_len + pkv::kMq8Keys - 1) / pkv::kMq8Keys;
+    long long splits = sm_count / (ctas < 1 ? 1 : ctas);
+    if (splits > key_tiles / kPartTiles) splits = key_tiles / kPartTiles;
+    c.splits = splits < 2 ? 1 : (int)splits;
+    const size_t units =
+        c.splits > 1 ? (size_t)num_seqs * max_q_len * n_heads * c.splits : 0;
+    c.o = 0;
+    c.ml = align256(units * head_dim * sizeof(float));
+    c.end = align256(c.ml + units * 2 * sizeof(float));
+    return c;
+}
+
 // Longest context first (longest_first), as paged_attn_multi_query.
 constexpr int kLptMaxSeqs = 256;
 constexpr int kLptMinContext = 8192;
@@ -137,12 +166,24 @@ PKV_API pkv_status paged_attn_decode_q8(
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
 }
 
+PKV_API size_t pkv_multi_query_q8_workspace_bytes(int num_seqs, int max_q_len, int n_heads,
+                                                  int n_kv_heads, int head_dim, int block_size,
+                                                  int max_context_len) {
+    if (!supported_shape(n_heads, n_kv_heads, head_dim, block_size) || num_seqs <= 0 ||
+        max_q_len <= 0 || max_context_len < 0)
+        return 0;
+    DeviceInfo* dev = nullptr;
+    const int sms = device_info(&dev) == cudaSuccess ? dev->sm_count : kDefaultSms;
+    return chunk_shape(num_seqs, max_q_len, n_heads, n_kv_heads, head_dim, max_context_len, sms).end;
+}
+
 PKV_API pkv_status paged_attn_multi_query_q8(
     void* out, pkv_dtype out_dtype, const void* q, pkv_dtype q_dtype, const int32_t* q_start,
     int total_q, int max_q_len, const void* k_pool, const void* v_pool, const float* k_scale,
     const float* v_scale, const int32_t* block_tables, int max_blocks_per_seq,
     const int32_t* context_lens, int num_seqs, int n_heads, int n_kv_heads, int head_dim,
-    int block_size, int num_blocks, float scale, int max_context_len, void* stream) {
+    int block_size, int num_blocks, float scale, int max_context_len, void* workspace,
+    size_t workspace_bytes, void* stream) {
     if (total_q < 0 || max_q_len < 0) return invalid("sizes");
     const bool none = num_seqs == 0 || total_q == 0 || max_q_len == 0;
     pkv_status st = check_paged_decode(out, out_dtype, q, k_pool, v_pool, q_dtype, block_tables,
@@ -158,7 +199,10 @@ PKV_API pkv_status paged_attn_multi_query_q8(
     DeviceInfo* dev = nullptr;
     cudaError_t e = device_info(&dev);
     if (e != cudaSuccess) return cuda_fail(e);
-    const int G = n_heads / n_kv_heads;
+    const ChunkShape c = chunk_shape(num_seqs, max_q_len, n_heads, n_kv_heads, head_dim,
+                                     max_context_len, dev->sm_count);
+    if (c.splits > 1 && (st = check_workspace(workspace, workspace_bytes, c.end)) != PKV_OK)
+        return st;
     pkv::Mq8Launch L;
     std::memset(&L, 0, sizeof(L));
     pkv::Mq8Params& p = L.p;
@@ -179,17 +223,29 @@ PKV_API pkv_status paged_attn_multi_query_q8(
     p.num_seqs = num_seqs;
     p.n_heads = n_heads;
     p.n_kv_heads = n_kv_heads;
-    p.group = G;
+    p.group = n_heads / n_kv_heads;
     p.num_blocks = num_blocks;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.max_pages = (int)(((long long)max_context_len + block_size - 1) / block_size);
     p.errors = dev->errors;
     p.lpt_seqs = max_context_len >= kLptMinContext && num_seqs <= kLptMaxSeqs ? num_seqs : 0;
-    const int cta_tokens = 2 * pkv::kMq8Rows / G;
-    L.grid = dim3((unsigned)((max_q_len + cta_tokens - 1) / cta_tokens), (unsigned)n_kv_heads,
-                  (unsigned)num_seqs);
+    p.splits = c.splits;
+    p.block_size = block_size;
+    if (c.splits > 1) {
+        p.part_o = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + c.o);
+        p.part_ml = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + c.ml);
+    }
+    L.grid = dim3((unsigned)(c.tiles * c.splits), (unsigned)n_kv_heads, (unsigned)num_seqs);
     L.stream = static_cast<cudaStream_t>(stream);
     e = pkv::launch_multi_query_q8(head_dim, block_size, L);
+    if (e == cudaSuccess && c.splits > 1) {
+        const long long rows = (long long)max_q_len * n_heads;
+        const int per_cta = pkv::kMq8MergeThreads / 32;
+        const dim3 grid((unsigned)((rows + per_cta - 1) / per_cta), (unsigned)num_seqs);
+        e = launch_dependent(head_dim == 128 ? pkv::multi_query_q8_merge_kernel<128>
+                                             : pkv::multi_query_q8_merge_kernel<64>,
+                             grid, pkv::kMq8MergeThreads, 0, L.stream, p);
+    }
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
 }
 

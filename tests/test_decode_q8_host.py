@@ -63,12 +63,12 @@ def test_decode_workspace_bytes(L):
 def _chunk(L, **kw):
     a = dict(out=FAKE(1), od=1, q=FAKE(2), qd=1, qs=FAKE(10), T=8, maxq=4, k=FAKE(3), v=FAKE(4),
              ks=FAKE(5), vs=FAKE(6), bt=FAKE(7), mb=4, cl=FAKE(8), S=2, H=8, Hk=8, D=128, B=16,
-             nb=10, scale=0.1, maxc=64)
+             nb=10, scale=0.1, maxc=64, ws=NULL, wsb=0)
     a.update(kw)
     return L.paged_attn_multi_query_q8(a["out"], a["od"], a["q"], a["qd"], a["qs"], a["T"],
                                        a["maxq"], a["k"], a["v"], a["ks"], a["vs"], a["bt"],
                                        a["mb"], a["cl"], a["S"], a["H"], a["Hk"], a["D"], a["B"],
-                                       a["nb"], a["scale"], a["maxc"], NULL)
+                                       a["nb"], a["scale"], a["maxc"], a["ws"], a["wsb"], NULL)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -88,3 +88,12 @@ def test_chunk_refusals(L, kw, code):
 @pytest.mark.parametrize("kw", [dict(S=0), dict(T=0), dict(maxq=0)])
 def test_chunk_of_nothing_is_a_no_op(L, kw):
     assert _chunk(L, q=NULL, ks=NULL, **kw) == 0
+
+
+def test_chunk_workspace_bytes(L):
+    f = L.pkv_multi_query_q8_workspace_bytes
+    assert f(2, 64, 8, 3, 128, 16, 5000) == 0 and f(0, 64, 8, 8, 128, 16, 5000) == 0
+    # many row tiles, or few keys: one part
+    assert f(64, 256, 32, 32, 128, 16, 5000) == 0 and f(1, 16, 8, 8, 128, 16, 200) == 0
+    # one pair of row tiles: parts of every row
+    assert f(1, 16, 1, 1, 128, 16, 5000) >= 16 * 2 * (128 + 2) * 4

@@ -36,7 +36,8 @@ def _problem(seqs, H, Hk, D, B, dtype, seed=1, scales="plain", gain=1.0):
 def _run(c, scale, out_dtype, max_q, max_len, stream=None):
     out = torch.full(c["q"].shape, 7.0, dtype=out_dtype, device="cuda")
     pkv.paged_attn_multi_query_q8(out, c["q"].cuda(), c["q_start"], c["kp"], c["vp"], c["ks"],
-                                  c["vs"], c["tables"], c["lens"], scale, max_q, max_len, stream)
+                                  c["vs"], c["tables"], c["lens"], scale, max_q, max_len,
+                                  stream=stream)
     return out
 
 
@@ -87,8 +88,13 @@ def test_multi_query_q8(seqs, H, Hk, D, B, dtype, out_dtype):
     max_q, max_len = max(m for m, _ in seqs), max(n for _, n in seqs)
     out = _run(c, scale, out_dtype, max_q, max_len)
     assert _clean() == 0
-    check(out, *_want(c, scale, out_dtype), "chunk")
-    assert torch.equal(out, _run(c, scale, out_dtype, max_q + 300, max_len + 2)), "bounds"
+    want = _want(c, scale, out_dtype)
+    check(out, *want, "chunk")
+    assert torch.equal(out, _run(c, scale, out_dtype, max_q, max_len)), "not the same bits twice"
+    # bounds far above the lengths: more key parts, some of them empty
+    for more_q, more_len in ((0, 20000), (300, 2)):
+        check(_run(c, scale, out_dtype, max_q + more_q, max_len + more_len), *want, "bounds")
+    assert _clean() == 0
 
 
 @pytest.mark.parametrize("out_dtype", [BF, F32])
@@ -118,10 +124,11 @@ def test_scale_not_positive(scale):
     check(out, *_want(c, scale, BF), "scale")
 
 
-def test_large_scores():
+@pytest.mark.parametrize("bound", [300, 3000])
+def test_large_scores(bound):
     """Scores of 2^20 and more: formed ahead of the maximum; the largest wins."""
     c = _problem([(30, 300)], 4, 2, 128, 16, BF, 6, gain=1.0)
-    out = _run(c, 2.0 ** 20, BF, 30, 300)
+    out = _run(c, 2.0 ** 20, BF, 30, bound)
     assert _clean() == 0
     q, k, v = c["q"].double(), c["k"][0], c["v"][0]
     for h in range(4):
@@ -175,10 +182,11 @@ def test_sequences_out_of_bounds_are_left_out():
 
 
 @pytest.mark.parametrize("D,Hk", [(64, 2), (128, 1)])
-def test_nan_reaches_the_rows_that_see_it(D, Hk):
+@pytest.mark.parametrize("bound", [190, 9000])
+def test_nan_reaches_the_rows_that_see_it(D, Hk, bound):
     seqs = [(60, 190), (140, 140)]
     c = _problem(seqs, 4, Hk, D, 16, BF, 10)
-    clean = _run(c, 0.1, BF, 140, 190)
+    clean = _run(c, 0.1, BF, 140, bound)
     hit = [(0, 3, 0, 1), (0, 150, Hk - 1, D - 1), (0, 189, 0, 40), (1, 0, 0, 9), (1, 130, 0, 33)]
     want = torch.zeros(c["q"].shape, dtype=torch.bool)
     G = 4 // Hk
@@ -187,7 +195,7 @@ def test_nan_reaches_the_rows_that_see_it(D, Hk):
         c["vp"].view(torch.uint8)[b, t % 16, h, d] = 0xff if t % 2 else 0x7f
         first = max(0, t - (seqs[s][1] - seqs[s][0]))
         want[c["starts"][s] + first:c["starts"][s + 1], h * G:(h + 1) * G, d] = True
-    out = _run(c, 0.1, BF, 140, 190)
+    out = _run(c, 0.1, BF, 140, bound)
     assert _clean() == 0
     assert torch.equal(out.isnan().cpu(), want)
     assert torch.equal(out[~want.cuda()], clean[~want.cuda()])
@@ -264,21 +272,39 @@ def test_longest_first_order_and_pools_beyond_4_gb():
             check(out[starts[s]:starts[s + 1], h], o, e, f"sequence {s} head {h}")
 
 
-def test_stream_and_graph():
+def test_streams_graphs_and_workspaces():
     c = _problem([(30, 200), (5, 600)], 8, 2, 128, 16, BF, 15)
     want = _run(c, 0.1, BF, 30, 600)
-    s = torch.cuda.Stream()
-    s.wait_stream(torch.cuda.current_stream())
-    out = _run(c, 0.1, BF, 30, 600, s)
-    s.synchronize()
-    q, got = c["q"].cuda(), torch.zeros_like(want)
-    graph = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(graph):
-        pkv.paged_attn_multi_query_q8(got, q, c["q_start"], c["kp"], c["vp"], c["ks"], c["vs"],
-                                      c["tables"], c["lens"], 0.1, 30, 600)
-    graph.replay()
+    n = pkv.multi_query_q8_workspace_bytes(2, 30, 8, 2, 128, 16, 600)
+    assert n > 0
+    q = c["q"].cuda()
+    outs, graphs = [], []
+    for i in range(2):
+        out = torch.zeros_like(want)
+        ws = torch.full((n,), 0xff, dtype=torch.uint8, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            pkv.paged_attn_multi_query_q8(out, q, c["q_start"], c["kp"], c["vp"], c["ks"], c["vs"],
+                                          c["tables"], c["lens"], 0.1, 30, 600, workspace=ws)
+        outs.append((out, ws))
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    for s in streams:
+        s.synchronize()
+    third = _run(c, 0.1, BF, 30, 600, streams[0])
+    streams[0].synchronize()
     assert _clean() == 0
-    assert torch.equal(out, want) and torch.equal(got, want)
+    for out in (outs[0][0], outs[1][0], third):
+        assert torch.equal(out, want)
+    with pytest.raises(pkv.PagedKVError):
+        pkv.paged_attn_multi_query_q8(out, q, c["q_start"], c["kp"], c["vp"], c["ks"], c["vs"],
+                                      c["tables"], c["lens"], 0.1, 30, 600, workspace=ws[:256])
 
 
 def test_one_token_is_the_decode():
