@@ -130,6 +130,28 @@ def lib():
     return _lib
 
 
+_calls = None
+
+
+def calls():
+    """The native part of the binding (csrc_py/tensor_calls.cpp), built beside
+    the library."""
+    global _calls
+    if _calls is None:
+        lib()
+        with _lock:
+            if _calls is None:
+                try:
+                    from . import _tensor_calls
+                except ImportError as e:
+                    raise RuntimeError(
+                        "_tensor_calls.so is missing or does not load: build it with "
+                        "`python -c 'import paged_kv_decode_26_gb300.build as b; b.build()'` "
+                        f"({e})") from e
+                _calls = _tensor_calls
+    return _calls
+
+
 def check(status: int, where: str) -> None:
     if status != PKV_OK:
         detail = lib().pkv_last_error_detail()

@@ -12,7 +12,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._lib import check, lib
+from ._lib import calls, check, lib
 
 _DT = {torch.float16: _lib.PKV_F16, torch.bfloat16: _lib.PKV_BF16, torch.float32: _lib.PKV_F32}
 
@@ -57,13 +57,6 @@ def _stream_handle(stream: Optional[torch.cuda.Stream]) -> int:
     if _raw_stream is not None:
         return _raw_stream(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
-
-
-def _stream_on(dev: int, stream: Optional[torch.cuda.Stream]) -> int:
-    """_stream_handle where the current device is known to be `dev`."""
-    if stream is None and _raw_stream is not None:
-        return _raw_stream(dev)
-    return _stream_handle(stream)
 
 
 def _addr(t: Optional[torch.Tensor]) -> int:
@@ -706,72 +699,8 @@ def rope_table(table: torch.Tensor, inv_freq, factor: float = 1.0,
     return table
 
 
-def _row_stride(name: str, t: torch.Tensor, T: int, heads: int, D: int) -> int:
-    """_token_stride of rows [T, heads, D] whose shape is checked already (the
-    appends sit on a serving loop's critical path)."""
-    row, head, one = t.stride()
-    if one == 1 and head == D and T > 1:
-        return row
-    return _token_stride(name, t)
-
-
-def _rope_append_args(k_pool, v_pool, pool_dtype, k, v, slot_mapping, positions, rope, q, q_out,
-                      k_out, interleaved) -> tuple:
-    """The checked C arguments of the rotating appends behind the pools."""
-    dev = k_pool.get_device()
-    if dev < 0 or dev != _current_device() or not (
-            v_pool.get_device() == slot_mapping.get_device() == k.get_device()
-            == v.get_device() == dev):
-        raise ValueError("tensors must be on the current CUDA device")
-    if k_pool.dim() != 4 or k.dim() != 3 or v.dim() != 3:
-        raise ValueError("pools are [num_blocks, B, Hk, D], k and v [tokens, Hk, D]")
-    pool_shape, shape, dtype = k_pool.shape, k.shape, k.dtype
-    nb, B, Hk, D = pool_shape
-    T = shape[0]
-    if (v_pool.shape != pool_shape or shape[1] != Hk or shape[2] != D or v.shape != shape
-            or v.dtype is not dtype or k_pool.dtype is not pool_dtype
-            or v_pool.dtype is not pool_dtype or slot_mapping.shape != (T,)):
-        raise ValueError("inconsistent shapes or dtypes")
-    if dtype is not torch.float16 and dtype is not torch.bfloat16:
-        raise ValueError("k and v must be float16 or bfloat16")
-    if slot_mapping.dtype is not torch.int64:
-        raise ValueError("slot_mapping must be int64")
-    if not (k_pool.is_contiguous() and v_pool.is_contiguous() and slot_mapping.is_contiguous()):
-        raise ValueError("k_pool, v_pool and slot_mapping must be contiguous")
-    pos = table = rows = rot = 0
-    if rope is not None:
-        if positions is None or not rope.get_device() == positions.get_device() == dev:
-            raise ValueError("rope and positions must be on the current CUDA device")
-        if rope.dtype is not torch.float32 or rope.dim() != 2 or not rope.is_contiguous():
-            raise ValueError("rope must be contiguous float32 [positions, rotary_dim]")
-        if (positions.dtype is not torch.int32 or positions.shape != (T,)
-                or not positions.is_contiguous()):
-            raise ValueError("positions must be contiguous int32 [tokens]")
-        rows, rot = rope.shape
-        pos, table = positions.data_ptr(), rope.data_ptr()
-    H = q_at = q_row = qo_at = qo_row = ko_at = ko_row = 0
-    if q is not None or q_out is not None:
-        if q is None or q_out is None:
-            raise ValueError("q and q_out: both or neither")
-        q_shape = q.shape
-        if q.dim() != 3 or q_shape[0] != T or q_shape[2] != D or q_out.shape != q_shape:
-            raise ValueError("q and q_out must be [tokens, H, D]")
-        if (not q.get_device() == q_out.get_device() == dev or q.dtype is not dtype
-                or q_out.dtype is not dtype):
-            raise ValueError("q and q_out must be of k's dtype, on the current CUDA device")
-        H = q_shape[1]
-        q_at, q_row = q.data_ptr(), _row_stride("q", q, T, H, D)
-        qo_at, qo_row = q_out.data_ptr(), _row_stride("q_out", q_out, T, H, D)
-    if k_out is not None:
-        if k_out.shape != shape:
-            raise ValueError("k_out must be shaped like k")
-        if k_out.get_device() != dev or k_out.dtype is not dtype:
-            raise ValueError("k_out must be of k's dtype, on the current CUDA device")
-        ko_at, ko_row = k_out.data_ptr(), _row_stride("k_out", k_out, T, Hk, D)
-    return (k.data_ptr(), _row_stride("k", k, T, Hk, D), v.data_ptr(),
-            _row_stride("v", v, T, Hk, D), _DT[dtype], slot_mapping.data_ptr(), pos, table, rows,
-            rot, 1 if interleaved else 0, q_at, q_row, qo_at, qo_row, ko_at, ko_row, T, H, Hk, D,
-            B, nb)
+def _handle(stream: Optional[torch.cuda.Stream]) -> Optional[int]:
+    return None if stream is None else stream.cuda_stream
 
 
 def kv_append_rope(k_pool: torch.Tensor, v_pool: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -785,20 +714,10 @@ def kv_append_rope(k_pool: torch.Tensor, v_pool: torch.Tensor, k: torch.Tensor, 
     table `rope`, see rope_table) on the way, and q [T, H, D] into q_out; k_out
     takes the rotated keys too.  q_out may be q and k_out k.  Tokens of slot -1
     are left out."""
-    args = _rope_append_args(k_pool, v_pool, k.dtype, k, v, slot_mapping, positions, rope, q,
-                             q_out, k_out, interleaved)
-    st = lib().kv_append_rope(k_pool.data_ptr(), v_pool.data_ptr(), *args,
-                              _stream_on(k_pool.get_device(), stream))
+    st = calls().kv_append_rope(k_pool, v_pool, k, v, slot_mapping, positions, rope, q, q_out,
+                                k_out, interleaved, _handle(stream))
     if st:
         check(st, "kv_append_rope")
-
-
-def _need_scales(dev: int, nb: int, Hk: int, k_scale: torch.Tensor, v_scale: torch.Tensor) -> None:
-    for t in (k_scale, v_scale):
-        if t.dtype is not torch.float32 or t.shape != (nb, Hk):
-            raise ValueError("k_scale and v_scale must be float32 [num_blocks, Hk]")
-        if t.get_device() != dev or not t.is_contiguous():
-            raise ValueError("k_scale and v_scale must be contiguous, on the current CUDA device")
 
 
 def kv_append_rope_q8(k_pool: torch.Tensor, v_pool: torch.Tensor, k_scale: torch.Tensor,
@@ -812,12 +731,8 @@ def kv_append_rope_q8(k_pool: torch.Tensor, v_pool: torch.Tensor, k_scale: torch
     Hk]) for each block and kv head: the least power of two that holds the
     block's rows; where it grows, the block's earlier rows are rounded anew.  The
     tokens of one block follow one another in the call, in order."""
-    args = _rope_append_args(k_pool, v_pool, torch.float8_e4m3fn, k, v, slot_mapping, positions,
-                             rope, q, q_out, k_out, interleaved)
-    dev = k_pool.get_device()
-    _need_scales(dev, args[-1], args[-4], k_scale, v_scale)
-    st = lib().kv_append_rope_q8(k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(),
-                                 v_scale.data_ptr(), *args, _stream_on(dev, stream))
+    st = calls().kv_append_rope_q8(k_pool, v_pool, k_scale, v_scale, k, v, slot_mapping, positions,
+                                   rope, q, q_out, k_out, interleaved, _handle(stream))
     if st:
         check(st, "kv_append_rope_q8")
 
@@ -828,31 +743,6 @@ def decode_q8_workspace_bytes(num_seqs: int, n_heads: int, n_kv_heads: int, head
                                                    block_size, max_context_len))
 
 
-def _q8_args(out, q, k_pool, v_pool, k_scale, v_scale, block_tables, context_lens) -> tuple:
-    """Checks what the 8-bit attention calls share; (heads of q, pool shape)."""
-    dev = out.get_device()
-    if dev < 0 or dev != _current_device():
-        raise ValueError("tensors must be on the current CUDA device")
-    for t in (out, q, k_pool, v_pool, block_tables, context_lens):
-        if t.get_device() != dev or not t.is_contiguous():
-            raise ValueError("tensors must be contiguous, on the current CUDA device")
-    if q.dim() != 3 or k_pool.dim() != 4:
-        raise ValueError("q is [rows, H, D], pools are [num_blocks, B, Hk, D]")
-    q_shape, pool_shape = q.shape, k_pool.shape
-    nb, B, Hk, D = pool_shape
-    if (q_shape[2] != D or v_pool.shape != pool_shape or out.shape != q_shape
-            or k_pool.dtype is not torch.float8_e4m3fn or v_pool.dtype is not torch.float8_e4m3fn
-            or block_tables.dim() != 2 or context_lens.dim() != 1
-            or block_tables.shape[0] != context_lens.shape[0]):
-        raise ValueError("inconsistent shapes or dtypes")
-    if q.dtype not in _DT or out.dtype not in _DT:
-        raise ValueError("q must be 16-bit, out 16-bit or float32")
-    if block_tables.dtype is not torch.int32 or context_lens.dtype is not torch.int32:
-        raise ValueError("block_tables and context_lens must be int32")
-    _need_scales(dev, nb, Hk, k_scale, v_scale)
-    return q_shape[1], nb, B, Hk, D
-
-
 def paged_attn_decode_q8(out: torch.Tensor, q: torch.Tensor, k_pool: torch.Tensor,
                          v_pool: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
                          block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float,
@@ -860,26 +750,13 @@ def paged_attn_decode_q8(out: torch.Tensor, q: torch.Tensor, k_pool: torch.Tenso
                          stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """paged_attn_decode over float8_e4m3fn pools [num_blocks, B, Hk, D] with
     scales fp32 [num_blocks, Hk] for each block and kv head; q is 16-bit."""
-    H, nb, B, Hk, D = _q8_args(out, q, k_pool, v_pool, k_scale, v_scale, block_tables,
-                               context_lens)
-    S = context_lens.shape[0]
-    if q.shape[0] != S:
-        raise ValueError("inconsistent shapes or dtypes")
-    max_context_len = int(max_context_len)
-    ws_at = ws_bytes = 0
-    if workspace is None:
-        ws_bytes = lib().pkv_decode_q8_workspace_bytes(S, H, Hk, D, B, max_context_len)
-        if ws_bytes:
-            workspace = _stream_buffer(ws_bytes, q.device, stream)
-            ws_at = workspace.data_ptr()
-    else:
-        _need_here(("workspace",), (workspace,))
-        ws_at, ws_bytes = workspace.data_ptr(), workspace.nbytes
-    st = lib().paged_attn_decode_q8(
-        out.data_ptr(), _DT[out.dtype], q.data_ptr(), _DT[q.dtype], k_pool.data_ptr(),
-        v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(),
-        block_tables.shape[1], context_lens.data_ptr(), S, H, Hk, D, B, nb, float(scale),
-        max_context_len, ws_at, ws_bytes, _stream_on(q.get_device(), stream))
+    handle = _handle(stream)
+    st = calls().paged_attn_decode_q8(out, q, k_pool, v_pool, k_scale, v_scale, block_tables,
+                                      context_lens, scale, max_context_len, workspace, handle)
+    if st < 0:                              # the bytes of the workspace
+        workspace = _stream_buffer(-st, q.device, stream)
+        st = calls().paged_attn_decode_q8(out, q, k_pool, v_pool, k_scale, v_scale, block_tables,
+                                          context_lens, scale, max_context_len, workspace, handle)
     if st:
         check(st, "paged_attn_decode_q8")
     return out
@@ -899,30 +776,15 @@ def paged_attn_multi_query_q8(out: torch.Tensor, q: torch.Tensor, q_start: torch
                               stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """paged_attn_multi_query over float8_e4m3fn pools with scales fp32
     [num_blocks, Hk] for each block and kv head; q is 16-bit."""
-    H, nb, B, Hk, D = _q8_args(out, q, k_pool, v_pool, k_scale, v_scale, block_tables,
-                               context_lens)
-    T, S = q.shape[0], context_lens.shape[0]
-    if q_start.get_device() != q.get_device() or not q_start.is_contiguous():
-        raise ValueError("q_start must be contiguous, on the current CUDA device")
-    if q_start.dtype is not torch.int32 or q_start.shape != (S + 1,):
-        raise ValueError("q_start must be int32 [S + 1]")
-    max_q_len, max_context_len = int(max_q_len), int(max_context_len)
-    ws_at = ws_bytes = 0
-    if workspace is None:
-        ws_bytes = lib().pkv_multi_query_q8_workspace_bytes(S, max_q_len, H, Hk, D, B,
-                                                            max_context_len)
-        if ws_bytes:
-            workspace = _stream_buffer(ws_bytes, q.device, stream)
-            ws_at = workspace.data_ptr()
-    else:
-        _need_here(("workspace",), (workspace,))
-        ws_at, ws_bytes = workspace.data_ptr(), workspace.nbytes
-    st = lib().paged_attn_multi_query_q8(
-        out.data_ptr(), _DT[out.dtype], q.data_ptr(), _DT[q.dtype], q_start.data_ptr(), T,
-        max_q_len, k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(),
-        v_scale.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
-        context_lens.data_ptr(), S, H, Hk, D, B, nb, float(scale), max_context_len, ws_at,
-        ws_bytes, _stream_on(q.get_device(), stream))
+    handle = _handle(stream)
+    st = calls().paged_attn_multi_query_q8(out, q, q_start, k_pool, v_pool, k_scale, v_scale,
+                                           block_tables, context_lens, scale, max_q_len,
+                                           max_context_len, workspace, handle)
+    if st < 0:                              # the bytes of the workspace
+        workspace = _stream_buffer(-st, q.device, stream)
+        st = calls().paged_attn_multi_query_q8(out, q, q_start, k_pool, v_pool, k_scale, v_scale,
+                                               block_tables, context_lens, scale, max_q_len,
+                                               max_context_len, workspace, handle)
     if st:
         check(st, "paged_attn_multi_query_q8")
     return out

@@ -272,11 +272,12 @@ def test_longest_first_order_and_pools_beyond_4_gb():
             check(out[starts[s]:starts[s + 1], h], o, e, f"sequence {s} head {h}")
 
 
-def test_streams_graphs_and_workspaces():
+@pytest.mark.parametrize("bound,parts", [(600, False), (3000, True)])
+def test_streams_graphs_and_workspaces(bound, parts):
     c = _problem([(30, 200), (5, 600)], 8, 2, 128, 16, BF, 15)
-    want = _run(c, 0.1, BF, 30, 600)
-    n = pkv.multi_query_q8_workspace_bytes(2, 30, 8, 2, 128, 16, 600)
-    assert n > 0
+    want = _run(c, 0.1, BF, 30, bound)
+    n = pkv.multi_query_q8_workspace_bytes(2, 30, 8, 2, 128, 16, bound)
+    assert (n > 0) == parts          # keys in parts meet in the workspace
     q = c["q"].cuda()
     outs, graphs = [], []
     for i in range(2):
@@ -285,7 +286,7 @@ def test_streams_graphs_and_workspaces():
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             pkv.paged_attn_multi_query_q8(out, q, c["q_start"], c["kp"], c["vp"], c["ks"], c["vs"],
-                                          c["tables"], c["lens"], 0.1, 30, 600, workspace=ws)
+                                          c["tables"], c["lens"], 0.1, 30, bound, workspace=ws)
         outs.append((out, ws))
         graphs.append(graph)
     streams = [torch.cuda.Stream() for _ in range(2)]
@@ -297,14 +298,16 @@ def test_streams_graphs_and_workspaces():
                 g.replay()
     for s in streams:
         s.synchronize()
-    third = _run(c, 0.1, BF, 30, 600, streams[0])
+    third = _run(c, 0.1, BF, 30, bound, streams[0])
     streams[0].synchronize()
     assert _clean() == 0
     for out in (outs[0][0], outs[1][0], third):
         assert torch.equal(out, want)
+    if not parts:
+        return
     with pytest.raises(pkv.PagedKVError):
         pkv.paged_attn_multi_query_q8(out, q, c["q_start"], c["kp"], c["vp"], c["ks"], c["vs"],
-                                      c["tables"], c["lens"], 0.1, 30, 600, workspace=ws[:256])
+                                      c["tables"], c["lens"], 0.1, 30, bound, workspace=ws[:256])
 
 
 def test_one_token_is_the_decode():
