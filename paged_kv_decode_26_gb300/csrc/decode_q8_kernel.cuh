@@ -48,6 +48,11 @@ constexpr float kQ8LeastScale = 0x1p-100f;     // of a reference (blocks of zero
 struct Q8Params : PieceParams {
     const float* k_scale;      // [num_blocks, n_kv_heads]
     const float* v_scale;
+    // decode_q8_short_kernel on chunks (else null): a CTA per token of sequence
+    // s, q rows q_start[s] .. q_start[s + 1] - 1, at most max_q_len
+    const int32_t* q_start;
+    int total_q;
+    int max_q_len;
 };
 
 // Two codes each of the low and the high half of w, as packed fp16 (exact).
@@ -515,16 +520,16 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
 
 // Short contexts: a CTA per (sequence, kv head), its warps taking the chunks in
 // turn, their states merged in shared memory: one launch, and no line of units to
-// lay out first.
-constexpr int kQ8ShortWarps = 4;
-constexpr int kQ8ShortThreads = 32 * kQ8ShortWarps;
+// lay out first.  Of chunks of a few tokens (blockIdx.z) each is a context of its own,
+// up to the token.
+constexpr int kQ8ShortWarps = 12;        // at most
 
-inline size_t decode_q8_short_smem_bytes(int D) {
-    return 1024 + (size_t)kQ8ShortWarps * kQ8Stages * 4 * 16 * D;
+inline size_t decode_q8_short_smem_bytes(int D, int warps) {
+    return 1024 + (size_t)warps * kQ8Stages * 4 * 16 * D;
 }
 
 template <int D, typename T, bool PRECISE>
-__global__ void __launch_bounds__(kQ8ShortThreads)
+__global__ void __launch_bounds__(32 * kQ8ShortWarps)
     decode_q8_short_kernel(const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v,
                            const __grid_constant__ Q8Params p) {
@@ -534,12 +539,25 @@ __global__ void __launch_bounds__(kQ8ShortThreads)
     __shared__ float s_ml[kQ8ShortWarps * 8 * 2];
     const uint32_t raw = smem_addr(smem_raw);
     unsigned char* sm = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const int kvh = blockIdx.x, s = blockIdx.y, qh0 = kvh * p.group;
     unsigned char* ring = sm + (size_t)warp * kQ8Stages * SLOT;
     uint64_t* full = s_bar + warp * kQ8Stages;
-    const int raw_n = p.context_lens[s], n = piece_length(p, s);
-    if (threadIdx.x == 0 && kvh == 0 && raw_n != n) raise_error(p.errors, PKV_DEVERR_CONTEXT);
+    const int raw_n = p.context_lens[s];
+    int n = piece_length(p, s);
+    size_t row0 = (size_t)s * p.n_heads + qh0;       // of the output
+    bool ok = raw_n == n;
+    int q_len = 1;
+    if (p.q_start) {
+        const int qs0 = p.q_start[s], qs1 = p.q_start[s + 1];
+        q_len = qs1 - qs0;
+        ok = ok && q_len >= 0 && q_len <= n && qs0 >= 0 && qs1 <= p.total_q && q_len <= p.max_q_len;
+        n -= q_len - 1 - (int)blockIdx.z;
+        row0 = (size_t)(qs0 + (int)blockIdx.z) * p.n_heads + qh0;
+    }
+    if (!ok && threadIdx.x == 0 && kvh == 0 && blockIdx.z == 0)
+        raise_error(p.errors, PKV_DEVERR_CONTEXT);
+    if (p.q_start && (!ok || (int)blockIdx.z >= q_len)) return;
     const int chunks = (n + kQ8Tokens - 1) / kQ8Tokens;
     if (lane == 0) {
         for (int i = 0; i < kQ8Stages; ++i) mbar_init(&full[i], 1);
@@ -590,15 +608,14 @@ __global__ void __launch_bounds__(kQ8ShortThreads)
     Q8Heads<D> state;
     if (warp < chunks) {
         Blocks now = issue(warp, 0);
-        q8_heads_start<D, T>(state,
-                             reinterpret_cast<const T*>(p.q) + ((size_t)s * p.n_heads + qh0) * D,
-                             p.group, p.scale_log2, lane);
+        q8_heads_start<D, T>(state, reinterpret_cast<const T*>(p.q) + row0 * D, p.group,
+                             p.scale_log2, lane);
         int st = 0;
         uint32_t phase = 0;
-        for (int c = warp; c < chunks; c += kQ8ShortWarps) {
+        for (int c = warp; c < chunks; c += warps) {
             Blocks next = now;
-            const bool more = c + kQ8ShortWarps < chunks;
-            if (more) next = issue(c + kQ8ShortWarps, st ^ 1);
+            const bool more = c + warps < chunks;
+            if (more) next = issue(c + warps, st ^ 1);
             const bool w = mbar_wait(&full[st], phase, p.errors);
             if (!__all_sync(0xffffffffu, w)) {
                 // the loads still in flight land before the CTA may exit
@@ -620,15 +637,15 @@ __global__ void __launch_bounds__(kQ8ShortThreads)
         }
     }
     // ---- the warps' states (each over its own ring)
-    const int active = min(chunks, kQ8ShortWarps);
+    const int active = min(chunks, warps);
     if (active == 1) {
-        if (warp == 0) q8_store<D, true>(state, p, (size_t)s * p.n_heads + qh0, nullptr, nullptr, lane);
+        if (warp == 0) q8_store<D, true>(state, p, row0, nullptr, nullptr, lane);
         return;
     }
     if (warp < active)
         q8_store<D, false>(state, p, 0, reinterpret_cast<float*>(ring), s_ml + warp * 16, lane);
     __syncthreads();
-    for (int e = threadIdx.x; e < p.group * (D / 2); e += kQ8ShortThreads) {
+    for (int e = threadIdx.x; e < p.group * (D / 2); e += blockDim.x) {
         const int h = e / (D / 2), d = e % (D / 2) * 2;
         float2 ml = make_float2(-INFINITY, 0.f);
         for (int w = 0; w < active; ++w)
@@ -643,7 +660,7 @@ __global__ void __launch_bounds__(kQ8ShortThreads)
             o.x += f * x.x;
             o.y += f * x.y;
         }
-        const size_t at = ((size_t)s * p.n_heads + qh0 + h) * D + d;
+        const size_t at = (row0 + h) * D + d;
         if (p.out_dtype == PKV_F32)
             *reinterpret_cast<float2*>(reinterpret_cast<float*>(p.out) + at) = o;
         else

@@ -10,7 +10,7 @@ struct Q8Launch {
     CUtensorMap tm_k;     // boxes of 16 tokens of one kv head
     CUtensorMap tm_v;
     Q8Params p;
-    bool whole;           // contexts by decode_q8_short_kernel, whole
+    int whole;            // warps per context of decode_q8_short_kernel; 0: decode_q8_kernel
     cudaStream_t stream;
 };
 

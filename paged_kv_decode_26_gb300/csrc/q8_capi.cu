@@ -36,17 +36,32 @@ cudaError_t encode_q8_map(CUtensorMap* map, const void* pool, int num_blocks, in
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Without blocks nothing is loaded; the maps need some valid tensor: q.
+cudaError_t encode_q8_maps(pkv::Q8Launch* L, const void* k_pool, const void* v_pool, const void* q,
+                           int num_blocks, int block_size, int n_kv_heads, int head_dim) {
+    const int n = num_blocks > 0 ? num_blocks : 1;
+    const cudaError_t e = encode_q8_map(&L->tm_k, num_blocks > 0 ? k_pool : q, n, block_size,
+                                        n_kv_heads, head_dim);
+    return e != cudaSuccess ? e
+                            : encode_q8_map(&L->tm_v, num_blocks > 0 ? v_pool : q, n, block_size,
+                                            n_kv_heads, head_dim);
+}
+
 // Contexts up to kShortContext tokens are decoded whole, by a CTA per kv head
 // (decode_q8_short_kernel), where there are at most kShortPairs of them per SM.
 // GB300, whole / in pieces, us: 64 pairs of 64 tokens 5.1 / 16.1, of 512 10.5 / 16.2,
 // of 1024 16.6 / 17.4, of 2048 29 / 18; 1024 pairs of up to 256 17 / 23, of up to
 // 1024 38 / 40, of up to 2048 69 / 58; 2048 pairs of up to 64 22.8 / 22.4, of up to
 // 512 46 / 40.
+// Warps of such a CTA: kQ8ShortWarps where every SM has one at most, else 4.  4 / 12
+// warps: 32 pairs of up to 200 tokens 5.8 / 4.6, 128 of 512 9.4 / 7.0, of 1024 15.8 /
+// 9.4; 1024 of up to 256 24 / 39.
 constexpr int kShortContext = 1024;
 constexpr int kShortPairs = 7;
-bool whole_contexts(int num_seqs, int n_kv_heads, int max_context_len, int sm_count) {
-    return max_context_len <= kShortContext &&
-           (long long)num_seqs * n_kv_heads <= (long long)kShortPairs * sm_count;
+// Warps per context, 0: not whole.
+int whole_contexts(long long pairs, int max_context_len, int sm_count) {
+    if (max_context_len > kShortContext || pairs > (long long)kShortPairs * sm_count) return 0;
+    return pairs <= sm_count ? pkv::kQ8ShortWarps : 4;
 }
 
 constexpr PiecesKind kPiecesQ8 = {pkv::kQ8Tokens, pkv::kQ8Warps, pkv::kQ8StreamHeads};
@@ -66,15 +81,25 @@ pkv_status check_scales(const float* k_scale, const float* v_scale, int num_bloc
 // least (a part costs its merge and a launch; GB300, 1 chunk of 512 tokens, 32 query and 8
 // kv heads, context 600: 23.1 us whole, 27.8 in parts of two key tiles; of 100 tokens at
 // context 8192: 120 us whole, 39 in parts; 2 chunks of 2 tokens, 4 heads, 16000: 229 / 27).
+// Where there is an SM for every token and kv head, and contexts are short, the decode
+// of whole contexts takes each token for itself (2 tokens, 4 heads, context 1000: 13.4
+// us in row tiles, 9.5 so; with more CTAs than SMs it loses: 512 of up to 1000 tokens
+// 18.2 / 24.5).
 constexpr int kPartTiles = 4;
 struct ChunkShape {
     int tiles;            // pairs of row tiles of the longest chunk allowed
     int splits;
     size_t o, ml, end;    // workspace
+    int by_token;         // warps of a CTA for each token's context, 0: row tiles
 };
 ChunkShape chunk_shape(int num_seqs, int max_q_len, int n_heads, int n_kv_heads, int head_dim,
                        int max_context_len, int sm_count) {
     ChunkShape c;
+    std::memset(&c, 0, sizeof(c));
+    const long long tokens = (long long)num_seqs * max_q_len;
+    if (tokens * n_kv_heads <= sm_count)
+        c.by_token = whole_contexts(tokens * n_kv_heads, max_context_len, sm_count);
+    if (c.by_token) return c;
     const int G = n_heads / n_kv_heads, cta_tokens = 2 * pkv::kMq8Rows / G;
     c.tiles = (int)(((long long)max_q_len + cta_tokens - 1) / cta_tokens);
     const long long ctas = (long long)c.tiles * n_kv_heads * num_seqs;
@@ -105,7 +130,7 @@ PKV_API size_t pkv_decode_q8_workspace_bytes(int num_seqs, int n_heads, int n_kv
         return 0;
     DeviceInfo* dev = nullptr;
     const int sms = device_info(&dev) == cudaSuccess ? dev->sm_count : kDefaultSms;
-    if (whole_contexts(num_seqs, n_kv_heads, max_context_len, sms)) return 0;
+    if (whole_contexts((long long)num_seqs * n_kv_heads, max_context_len, sms)) return 0;
     return pieces_workspace(num_seqs, n_heads, n_kv_heads, head_dim,
                             q8_grid(num_seqs, n_kv_heads, max_context_len, sms))
         .end;
@@ -131,15 +156,11 @@ PKV_API pkv_status paged_attn_decode_q8(
         pieces_workspace(num_seqs, n_heads, n_kv_heads, head_dim, pieces);
     pkv::Q8Launch L;
     std::memset(&L, 0, sizeof(L));
-    L.whole = whole_contexts(num_seqs, n_kv_heads, max_context_len, dev->sm_count);
+    L.whole = whole_contexts((long long)num_seqs * n_kv_heads, max_context_len, dev->sm_count);
     if (!L.whole && (st = check_workspace(workspace, workspace_bytes, w.end)) != PKV_OK) return st;
     L.stream = static_cast<cudaStream_t>(stream);
-    // (without blocks nothing is loaded; the maps need some valid tensor)
-    const int map_blocks = num_blocks > 0 ? num_blocks : 1;
-    if ((e = encode_q8_map(&L.tm_k, num_blocks > 0 ? k_pool : q, map_blocks, block_size,
-                           n_kv_heads, head_dim)) ||
-        (e = encode_q8_map(&L.tm_v, num_blocks > 0 ? v_pool : q, map_blocks, block_size,
-                           n_kv_heads, head_dim)))
+    if ((e = encode_q8_maps(&L, k_pool, v_pool, q, num_blocks, block_size, n_kv_heads,
+                            head_dim)) != cudaSuccess)
         return cuda_fail(e);
     pkv::Q8Params& p = L.p;
     fill_piece_problem(&p, pieces, out, out_dtype, q, block_tables, max_blocks_per_seq,
@@ -203,6 +224,31 @@ PKV_API pkv_status paged_attn_multi_query_q8(
                                      max_context_len, dev->sm_count);
     if (c.splits > 1 && (st = check_workspace(workspace, workspace_bytes, c.end)) != PKV_OK)
         return st;
+    if (c.by_token) {
+        pkv::Q8Launch L;
+        std::memset(&L, 0, sizeof(L));
+        L.whole = c.by_token;
+        L.stream = static_cast<cudaStream_t>(stream);
+        if ((e = encode_q8_maps(&L, k_pool, v_pool, q, num_blocks, block_size, n_kv_heads,
+                                head_dim)) != cudaSuccess)
+            return cuda_fail(e);
+        pkv::Q8Params& p = L.p;
+        PiecesWorkspace w;
+        std::memset(&w, 0, sizeof(w));
+        const int blocks = (max_context_len + block_size - 1) / block_size;
+        fill_piece_problem(&p, q8_grid(num_seqs, n_kv_heads, max_context_len, dev->sm_count), out,
+                           out_dtype, q, block_tables, max_blocks_per_seq, context_lens, num_seqs,
+                           n_heads, n_kv_heads, block_size, num_blocks, scale, blocks * block_size,
+                           w, nullptr, *dev);
+        p.k_scale = k_scale;
+        p.v_scale = v_scale;
+        p.q_start = q_start;
+        p.total_q = total_q;
+        p.max_q_len = max_q_len;
+        e = q_dtype == PKV_BF16 ? pkv::launch_decode_q8_bf16(head_dim, L)
+                                : pkv::launch_decode_q8_f16(head_dim, L);
+        return e == cudaSuccess ? PKV_OK : cuda_fail(e);
+    }
     pkv::Mq8Launch L;
     std::memset(&L, 0, sizeof(L));
     pkv::Mq8Params& p = L.p;
