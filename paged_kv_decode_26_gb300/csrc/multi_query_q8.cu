@@ -22,7 +22,7 @@ cudaError_t launch(const Mq8Launch& L) {
         split_fits = true;
     }
     if ((e = ensure_smem_limit(fn, &done_mask, smem)) != cudaSuccess) return e;
-    multi_query_q8_kernel<D, BS, PARTS><<<L.grid, kMq8Threads, smem, L.stream>>>(L.p);
+    multi_query_q8_kernel<D, BS, PARTS><<<L.ctas, kMq8Threads, smem, L.stream>>>(L.p);
     return cudaGetLastError();
 }
 

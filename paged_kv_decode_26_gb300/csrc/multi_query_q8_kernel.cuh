@@ -51,12 +51,17 @@ struct Mq8Params : MultiQueryParams {
     const float* k_scale;
     const float* v_scale;
     int q_bf16;
-    // the keys of a pair of row tiles in `splits` parts, a CTA each; partial states at
-    // unit ((s * max_q_len + token) * n_heads + head) * splits + part
+    // Items are pairs of row tiles of a kv head, `tiles` of them for every sequence and
+    // head: a CTA for each of the first `whole`, and for each of the others one for every
+    // of `splits` parts of its keys
+    int tiles;
+    int whole;
     int splits;
     int block_size;
-    float* part_o;             // [units, D], normalised
-    float* part_ml;            // [units, 2]
+    float* part_o;             // [others, splits, 256 rows, D], normalised
+    float* part_ml;            // [others, splits, 256 rows, 2]
+    int4* heads;               // [others]: sequence (-1: nothing to merge), kv head, pair of
+                               // row tiles, parts with keys
 };
 
 // Of a key tile's groups of 16 keys: a, log2 b and 1 / b, and whether there is a page.
@@ -108,27 +113,28 @@ __device__ __forceinline__ uint32_t mq8_nans(uint32_t w) {
     return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
 }
 
-// Rows of key parts, merged: a warp per row (token, head) of sequence blockIdx.y.
-constexpr int kMq8MergeThreads = 128;
+// Rows of items in pieces, merged: a warp per row of the x-th item of several parts.
+constexpr int kMq8MergeRows = 16;
+constexpr int kMq8MergeThreads = 32 * kMq8MergeRows;
 template <int D>
 __global__ void __launch_bounds__(kMq8MergeThreads)
     multi_query_q8_merge_kernel(const __grid_constant__ Mq8Params p) {
     constexpr int V = D / 32;
     dependency_wait();
-    const int s = blockIdx.y, lane = threadIdx.x & 31;
-    const int i = (int)(blockIdx.x * (kMq8MergeThreads / 32) + (threadIdx.x >> 5));
-    const int tok = i / p.n_heads;
-    const int qs0 = p.q_start[s], qs1 = p.q_start[s + 1], q_len = qs1 - qs0;
-    const int n = p.context_lens[s];
-    // (what the kernel ahead left out has no partial states)
-    if (q_len < 0 || q_len > n || qs0 < 0 || qs1 > p.total_q || q_len > p.max_q_len ||
-        n > (long long)p.max_pages * p.block_size ||
-        n > (long long)p.max_blocks_per_seq * p.block_size || tok >= q_len)
-        return;
-    const size_t unit = ((size_t)s * p.max_q_len * p.n_heads + i) * p.splits;
+    const int4 head = p.heads[blockIdx.x];
+    if (head.x < 0) return;
+    const int lane = threadIdx.x & 31, G = p.group, QT = kMq8Rows / G;
+    const int pieces = head.w;
+    const int qs0 = p.q_start[head.x] + head.z * 2 * QT;
+    const int rows = min(p.q_start[head.x + 1] - qs0, 2 * QT);
+    const int i = blockIdx.y * kMq8MergeRows + (threadIdx.x >> 5), tok = i / G;
+    if (tok >= rows) return;
+    auto row_of = [&](int piece) -> size_t {
+        return ((size_t)blockIdx.x * p.splits + piece) * 2 * kMq8Rows + i;
+    };
     float2 ml = make_float2(-INFINITY, 0.f);
-    for (int k = lane; k < p.splits; k += 32)
-        ml = join_ml(ml, *reinterpret_cast<const float2*>(p.part_ml + 2 * (unit + k)));
+    for (int w = lane; w < pieces; w += 32)
+        ml = join_ml(ml, *reinterpret_cast<const float2*>(p.part_ml + 2 * row_of(w)));
 #pragma unroll
     for (int off = 16; off; off /= 2)
         ml = join_ml(ml, make_float2(__shfl_xor_sync(0xffffffffu, ml.x, off),
@@ -137,11 +143,11 @@ __global__ void __launch_bounds__(kMq8MergeThreads)
     float o[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) o[e] = 0.f;
-    for (int k = 0; k < p.splits; ++k) {
-        const float2 a = *reinterpret_cast<const float2*>(p.part_ml + 2 * (unit + k));
+    for (int w = 0; w < pieces; ++w) {
+        const float2 a = *reinterpret_cast<const float2*>(p.part_ml + 2 * row_of(w));
         if (a.y == 0.f) continue;                  // (nothing was written for it)
         const float f = a.y * exp2f(a.x - ml.x) * inv;
-        const float* row = p.part_o + (unit + k) * D + lane * V;
+        const float* row = p.part_o + row_of(w) * D + lane * V;
 #pragma unroll
         for (int e = 0; e < V; e += 2) {
             const float2 x = *reinterpret_cast<const float2*>(row + e);
@@ -149,7 +155,8 @@ __global__ void __launch_bounds__(kMq8MergeThreads)
             o[e + 1] += f * x.y;
         }
     }
-    const size_t at = ((size_t)qs0 * p.n_heads + i) * D + lane * V;
+    const size_t at =
+        ((size_t)(qs0 + tok) * p.n_heads + head.y * G + i % G) * D + lane * V;
 #pragma unroll
     for (int e = 0; e < V; e += 2) {
         if (p.out_dtype == PKV_F32)
@@ -186,47 +193,49 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
     int* s_poison = s_tmem + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    int tile = blockIdx.x, kvh = blockIdx.y, s = blockIdx.z;
+    const int cta = blockIdx.x;
+    const bool cut = cta >= p.whole && p.splits > 1;
+    const int other = cut ? (cta - p.whole) / p.splits : 0;
+    const int part = cut ? (cta - p.whole) % p.splits : 0, parts = cut ? p.splits : 1;
+    const int item = cut ? p.whole + other : cta;
+    int tile = item % p.tiles, kvh = item / p.tiles % p.n_kv_heads,
+        s = item / (p.tiles * p.n_kv_heads);
     if (p.lpt_seqs > 0) {
-        longest_first(p, reinterpret_cast<int*>(sKV), tile, kvh, s);   // (sKV: not yet in use)
+        longest_first(p, reinterpret_cast<int*>(sKV), item, p.tiles, p.n_kv_heads, tile, kvh,
+                      s);                               // (sKV: not yet in use)
         __syncthreads();
     }
-    const int part = tile % p.splits;
-    tile /= p.splits;
     const int G = p.group, QT = kMq8Rows / G;
     const int qs0 = p.q_start[s], qs1 = p.q_start[s + 1];
     const int n = p.context_lens[s];
     const int q_len = qs1 - qs0;
-    if (q_len < 0 || q_len > n || qs0 < 0 || qs1 > p.total_q || q_len > p.max_q_len ||
-        n > (long long)p.max_pages * BS || n > (long long)p.max_blocks_per_seq * BS) {
-        if (tile == 0 && part == 0 && kvh == 0 && threadIdx.x == 0)
+    const int tok_lo = tile * 2 * QT;
+    const bool bad = q_len < 0 || q_len > n || qs0 < 0 || qs1 > p.total_q ||
+                     q_len > p.max_q_len || n > (long long)p.max_pages * BS ||
+                     n > (long long)p.max_blocks_per_seq * BS;
+    if (bad || tok_lo >= q_len) {
+        if (bad && tile == 0 && part == 0 && kvh == 0 && threadIdx.x == 0)
             raise_error(p.errors, PKV_DEVERR_CONTEXT);
+        if (cut && part == 0 && threadIdx.x == 0) p.heads[other] = make_int4(-1, 0, 0, 0);
         return;
     }
-    const int tok_lo = tile * 2 * QT;
-    if (tok_lo >= q_len) return;
     const int pos0 = n - q_len + tok_lo;             // position of row tile 0's first token
     const int rows = min(q_len - tok_lo, 2 * QT);    // tokens of this CTA
     const int n_keys = pos0 + rows;                  // keys that some row sees
     // key tiles that the row tiles see, and of them those of this part: j0 + 0, 1, ..
     const int see0 = (pos0 + min(rows, QT) + kMq8Keys - 1) / kMq8Keys;
     const int see1 = rows > QT ? (n_keys + kMq8Keys - 1) / kMq8Keys : 0;
-    const int part_tiles = (max(see0, see1) + p.splits - 1) / p.splits;
+    const int see = max(see0, see1), part_tiles = (see + parts - 1) / parts;
+    if (cut && part == 0 && threadIdx.x == 0)
+        p.heads[other] = make_int4(s, kvh, tile, (see + part_tiles - 1) / part_tiles);
     const int j0 = part * part_tiles;
     const int nt0 = min(max(see0 - j0, 0), part_tiles), nt1 = min(max(see1 - j0, 0), part_tiles);
     const int n_tiles = max(nt0, nt1);
-    // partial state of row r of row tile t (token t * QT + r / G of the CTA)
+    if (n_tiles == 0) return;
+    // row r of row tile t of this part
     auto unit_of = [&](int t, int r) -> size_t {
-        return (((size_t)s * p.max_q_len + tok_lo + t * QT + r / G) * p.n_heads + kvh * G + r % G) *
-                   p.splits + part;
+        return (((size_t)other * parts + part) * 2 + t) * kMq8Rows + r;
     };
-    if (n_tiles == 0) {
-        for (int i = threadIdx.x; i < 2 * kMq8Rows; i += kMq8Threads)
-            if (i / kMq8Rows * QT + i % kMq8Rows / G < rows)
-                *reinterpret_cast<float2*>(p.part_ml + 2 * unit_of(i / kMq8Rows, i % kMq8Rows)) =
-                    make_float2(-INFINITY, 0.f);
-        return;
-    }
 
     if (warp == 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -450,7 +459,7 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
         const int t = warp >> 2;
         const int r = (warp & 3) * 32 + lane;
         const int nt = t ? nt1 : nt0;
-        if (nt == 0 && p.splits > 1 && t * QT + r / G < rows)
+        if (nt == 0 && cut && t * QT + r / G < rows)
             *reinterpret_cast<float2*>(p.part_ml + 2 * unit_of(t, r)) = make_float2(-INFINITY, 0.f);
         if (nt > 0) {
             const int tok = t * QT + r / G;
@@ -699,7 +708,7 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
             if (ok) {
                 tc_fence_after();
                 const float inv = l != 0.f ? __frcp_rn(l) : 0.f;
-                if (p.splits > 1 && real)
+                if (cut && real)
                     *reinterpret_cast<float2*>(p.part_ml + 2 * unit_of(t, r)) =
                         make_float2(m, l * exp2f(lb - Range::LIFT));
                 const bool poison = *reinterpret_cast<volatile int*>(s_poison) != 0;
@@ -726,8 +735,8 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
                                 if ((v[c] & 0x7f) == 0x7f) o[c] = NAN;
                         }
                     }
-                    const size_t at = (p.splits > 1 ? unit_of(t, r) : row) * D + c0;
-                    if (p.splits > 1) {
+                    const size_t at = (cut ? unit_of(t, r) : row) * D + c0;
+                    if (cut) {
                         float4* o4 = reinterpret_cast<float4*>(p.part_o + at);
 #pragma unroll
                         for (int c = 0; c < 32; c += 4)

@@ -7,7 +7,7 @@ namespace pkv {
 
 struct Mq8Launch {
     Mq8Params p;
-    dim3 grid;            // pairs of row tiles, kv heads, sequences
+    unsigned ctas;
     cudaStream_t stream;
 };
 

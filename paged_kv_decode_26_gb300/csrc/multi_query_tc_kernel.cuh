@@ -172,17 +172,16 @@ inline size_t multi_query_tc_smem_bytes(int D, int stages, int max_pages, int lp
 // query tiles), the kv head fastest and the query tiles from the last (the
 // one that sees the most keys).  s_len: p.lpt_seqs + 1 ints of shared
 // memory that nothing else uses.
-__device__ __forceinline__ void longest_first(const MultiQueryParams& p, int* s_len, int& tile,
-                                              int& kvh, int& s) {
+// The u-th of `tiles` query tiles of `heads` kv heads of every sequence.
+__device__ __forceinline__ void longest_first(const MultiQueryParams& p, int* s_len, long long u,
+                                              int tiles, int heads, int& tile, int& kvh, int& s) {
     const int S = p.lpt_seqs;
     int* s_pick = s_len + S;
-    const long long u =
-        blockIdx.x + (long long)gridDim.x * (blockIdx.y + (long long)gridDim.y * blockIdx.z);
-    const int per_seq = (int)(gridDim.x * gridDim.y);
+    const int per_seq = tiles * heads;
     const int r = (int)(u / per_seq);
     const int rem = (int)(u % per_seq);
-    kvh = rem % (int)gridDim.y;
-    tile = (int)gridDim.x - 1 - rem / (int)gridDim.y;
+    kvh = rem % heads;
+    tile = tiles - 1 - rem / heads;
     for (int i = threadIdx.x; i < S; i += blockDim.x) s_len[i] = p.context_lens[i];
     __syncthreads();
     // the ranks are a permutation of 0 .. S-1: exactly one sequence has rank r
@@ -197,6 +196,12 @@ __device__ __forceinline__ void longest_first(const MultiQueryParams& p, int* s_
     }
     __syncthreads();
     s = *s_pick;
+}
+__device__ __forceinline__ void longest_first(const MultiQueryParams& p, int* s_len, int& tile,
+                                              int& kvh, int& s) {
+    longest_first(p, s_len,
+                  blockIdx.x + (long long)gridDim.x * (blockIdx.y + (long long)gridDim.y * blockIdx.z),
+                  (int)gridDim.x, (int)gridDim.y, tile, kvh, s);
 }
 
 template <int D, int BS, typename T>

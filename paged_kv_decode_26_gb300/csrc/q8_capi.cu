@@ -3,6 +3,8 @@
 // Declarations and contracts: pagedkv.h.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstring>
 
@@ -76,20 +78,28 @@ pkv_status check_scales(const float* k_scale, const float* v_scale, int num_bloc
     return PKV_OK;
 }
 
-// Parts that the keys of a chunk's row tiles are cut into: where the pairs of row
-// tiles leave most SMs idle, as many as fill them, each of kPartTiles key tiles at
-// least (a part costs its merge and a launch; GB300, 1 chunk of 512 tokens, 32 query and 8
-// kv heads, context 600: 23.1 us whole, 27.8 in parts of two key tiles; of 100 tokens at
-// context 8192: 120 us whole, 39 in parts; 2 chunks of 2 tokens, 4 heads, 16000: 229 / 27).
+// How a chunk's items (pairs of row tiles of a kv head) meet the SMs, one at a time on
+// each.  Items that do not fill the SMs once more (all of them, where there are fewer
+// than SMs) are cut into parts of their keys, kPartTiles key tiles at least, so that the
+// last round is short: as many as make it shortest, at kItemTiles key tiles for a
+// part's start and end and kMergeTiles for the launch that merges.  GB300, us, whole / in
+// parts: 2 chunks of 2048 tokens behind 12K-16K, 32 heads 904 / 840; of 1500 tokens at
+// 4000, 32 query and 8 kv heads, 117 / 103, of 100 at 8192 120 / 35; 2 chunks of 2 tokens, 4
+// heads, at 16000 229 / 27; 16 of up to 8 tokens at up to 1000, 16 query and 4 kv heads 16.6
+// / 16.1; of 512 tokens at 600 23.1 / 27.8, therefore whole.
 // Where there is an SM for every token and kv head, and contexts are short, the decode
 // of whole contexts takes each token for itself (2 tokens, 4 heads, context 1000: 13.4
 // us in row tiles, 9.5 so; with more CTAs than SMs it loses: 512 of up to 1000 tokens
 // 18.2 / 24.5).
 constexpr int kPartTiles = 4;
+constexpr int kItemTiles = 2;
+constexpr int kMergeTiles = 3;
 struct ChunkShape {
     int tiles;            // pairs of row tiles of the longest chunk allowed
-    int splits;
-    size_t o, ml, end;    // workspace
+    long long items;
+    long long whole;      // items that are not cut
+    int splits;           // parts of the others
+    size_t o, ml, heads, end;    // workspace
     int by_token;         // warps of a CTA for each token's context, 0: row tiles
 };
 ChunkShape chunk_shape(int num_seqs, int max_q_len, int n_heads, int n_kv_heads, int head_dim,
@@ -102,16 +112,28 @@ ChunkShape chunk_shape(int num_seqs, int max_q_len, int n_heads, int n_kv_heads,
     if (c.by_token) return c;
     const int G = n_heads / n_kv_heads, cta_tokens = 2 * pkv::kMq8Rows / G;
     c.tiles = (int)(((long long)max_q_len + cta_tokens - 1) / cta_tokens);
-    const long long ctas = (long long)c.tiles * n_kv_heads * num_seqs;
+    c.items = (long long)c.tiles * n_kv_heads * num_seqs;
+    c.whole = c.items / sm_count * sm_count;
+    c.splits = 1;
+    const long long others = c.items - c.whole;
     const long long key_tiles = ((long long)max_context_len + pkv::kMq8Keys - 1) / pkv::kMq8Keys;
-    long long splits = sm_count / (ctas < 1 ? 1 : ctas);
-    if (splits > key_tiles / kPartTiles) splits = key_tiles / kPartTiles;
-    c.splits = splits < 2 ? 1 : (int)splits;
-    const size_t units =
-        c.splits > 1 ? (size_t)num_seqs * max_q_len * n_heads * c.splits : 0;
-    c.o = 0;
-    c.ml = align256(units * head_dim * sizeof(float));
-    c.end = align256(c.ml + units * 2 * sizeof(float));
+    long long best = key_tiles + kItemTiles;
+    for (int k = 2; others > 0 && k <= sm_count && k * kPartTiles <= key_tiles; ++k) {
+        const long long rounds = (others * k + sm_count - 1) / sm_count;
+        const long long time = rounds * ((key_tiles + k - 1) / k + kItemTiles) + kMergeTiles;
+        if (time < best) {
+            best = time;
+            c.splits = k;
+        }
+    }
+    if (c.splits == 1) {
+        c.whole = c.items;
+        return c;
+    }
+    const size_t rows = (size_t)others * c.splits * 2 * pkv::kMq8Rows;
+    c.ml = align256(rows * head_dim * sizeof(float));
+    c.heads = align256(c.ml + rows * 2 * sizeof(float));
+    c.end = align256(c.heads + (size_t)others * sizeof(int4));
     return c;
 }
 
@@ -220,8 +242,14 @@ PKV_API pkv_status paged_attn_multi_query_q8(
     DeviceInfo* dev = nullptr;
     cudaError_t e = device_info(&dev);
     if (e != cudaSuccess) return cuda_fail(e);
-    const ChunkShape c = chunk_shape(num_seqs, max_q_len, n_heads, n_kv_heads, head_dim,
-                                     max_context_len, dev->sm_count);
+    ChunkShape c = chunk_shape(num_seqs, max_q_len, n_heads, n_kv_heads, head_dim,
+                               max_context_len, dev->sm_count);
+    // (shorter chunks than the longest: how many items there are is not known here)
+    if (c.whole > 0 && total_q != (long long)num_seqs * max_q_len) {
+        c.whole = c.items;
+        c.splits = 1;
+    }
+    if (!c.by_token && c.whole + (c.items - c.whole) * c.splits > INT_MAX) return invalid("sizes");
     if (c.splits > 1 && (st = check_workspace(workspace, workspace_bytes, c.end)) != PKV_OK)
         return st;
     if (c.by_token) {
@@ -275,19 +303,24 @@ PKV_API pkv_status paged_attn_multi_query_q8(
     p.max_pages = (int)(((long long)max_context_len + block_size - 1) / block_size);
     p.errors = dev->errors;
     p.lpt_seqs = max_context_len >= kLptMinContext && num_seqs <= kLptMaxSeqs ? num_seqs : 0;
+    p.tiles = c.tiles;
+    p.whole = (int)c.whole;
     p.splits = c.splits;
     p.block_size = block_size;
     if (c.splits > 1) {
-        p.part_o = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + c.o);
-        p.part_ml = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + c.ml);
+        unsigned char* ws = static_cast<unsigned char*>(workspace);
+        p.part_o = reinterpret_cast<float*>(ws + c.o);
+        p.part_ml = reinterpret_cast<float*>(ws + c.ml);
+        p.heads = reinterpret_cast<int4*>(ws + c.heads);
     }
-    L.grid = dim3((unsigned)(c.tiles * c.splits), (unsigned)n_kv_heads, (unsigned)num_seqs);
+    const long long others = c.items - c.whole;
+    L.ctas = (unsigned)(c.whole + others * c.splits);
     L.stream = static_cast<cudaStream_t>(stream);
     e = pkv::launch_multi_query_q8(head_dim, block_size, L);
     if (e == cudaSuccess && c.splits > 1) {
-        const long long rows = (long long)max_q_len * n_heads;
-        const int per_cta = pkv::kMq8MergeThreads / 32;
-        const dim3 grid((unsigned)((rows + per_cta - 1) / per_cta), (unsigned)num_seqs);
+        const long long rows = std::min(2LL * pkv::kMq8Rows, (long long)max_q_len * p.group);
+        const dim3 grid((unsigned)others,
+                        (unsigned)((rows + pkv::kMq8MergeRows - 1) / pkv::kMq8MergeRows));
         e = launch_dependent(head_dim == 128 ? pkv::multi_query_q8_merge_kernel<128>
                                              : pkv::multi_query_q8_merge_kernel<64>,
                              grid, pkv::kMq8MergeThreads, 0, L.stream, p);

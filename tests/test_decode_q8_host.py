@@ -93,7 +93,8 @@ def test_chunk_of_nothing_is_a_no_op(L, kw):
 def test_chunk_workspace_bytes(L):
     f = L.pkv_multi_query_q8_workspace_bytes
     assert f(2, 64, 8, 3, 128, 16, 5000) == 0 and f(0, 64, 8, 8, 128, 16, 5000) == 0
-    # many row tiles, or few keys: one part
-    assert f(64, 256, 32, 32, 128, 16, 5000) == 0 and f(1, 16, 8, 8, 128, 16, 200) == 0
-    # one pair of row tiles: parts of every row
-    assert f(1, 16, 1, 1, 128, 16, 5000) >= 16 * 2 * (128 + 2) * 4
+    # too few keys to cut
+    assert f(64, 256, 32, 32, 128, 16, 500) == 0 and f(1, 16, 8, 8, 128, 16, 200) == 0
+    # one pair of row tiles: parts of every row; many: only of what fills no round of its own
+    assert f(1, 16, 1, 1, 128, 16, 5000) >= 2 * 256 * (128 + 2) * 4
+    assert f(64, 2560, 32, 32, 128, 16, 50000) < 1 << 28

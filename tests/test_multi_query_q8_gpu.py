@@ -310,6 +310,104 @@ def test_streams_graphs_and_workspaces(bound, parts):
                                       c["tables"], c["lens"], 0.1, 30, bound, workspace=ws[:256])
 
 
+# more pairs of row tiles than a GPU has SMs; the first three: the rest of them in parts
+MANY = [
+    ([(300, n) for n in (1400, 300, 2500, 513, 2000)], 32, 32, 64, 16, BF, BF),
+    ([(130, n) for n in (3000, 130, 1111, 2900)], 64, 16, 128, 32, FP, F32),
+    ([(40, 2000 + 7 * i) for i in range(10)], 64, 16, 64, 16, BF, F32),
+    ([(300, 1400), (1, 1), (0, 5), (257, 2500), (130, 600)], 32, 32, 64, 16, BF, BF),
+    ([(3, 700 + 3 * i) for i in range(60)], 8, 4, 64, 16, FP, FP),
+    ([(1 + i % 3, 3 + i % 50) for i in range(600)], 2, 2, 64, 32, BF, BF),
+]
+
+
+@pytest.mark.parametrize("seqs,H,Hk,D,B,dtype,out_dtype", MANY)
+def test_many_row_tiles(seqs, H, Hk, D, B, dtype, out_dtype):
+    c = _problem(seqs, H, Hk, D, B, dtype, 20)
+    scale = 1.0 / math.sqrt(D)
+    max_q, max_len = max(m for m, _ in seqs), max(n for _, n in seqs)
+    out = _run(c, scale, out_dtype, max_q, max_len)
+    assert _clean() == 0
+    want = _want(c, scale, out_dtype)
+    check(out, *want, "many row tiles")
+    assert torch.equal(out, _run(c, scale, out_dtype, max_q, max_len)), "not the same bits twice"
+    check(_run(c, scale, out_dtype, max_q + 300, max_len + 9000), *want, "bounds")
+    check(_run(c, scale, out_dtype, max_q, 9000), *want, "longest first")
+    assert _clean() == 0
+
+
+EQUAL = [(257, n) for n in (1400, 600, 2500, 1000, 2400)]
+
+
+@pytest.mark.parametrize("gone", [1, 4])
+def test_what_is_left_of_many_row_tiles(gone):
+    """A sequence that does not fit its bounds, missing blocks and NaN beside parts."""
+    H, B = 32, 16
+    c = _problem(EQUAL, H, H, 64, B, BF, 21)
+    nb, starts = c["kp"].shape[0], c["starts"]
+    assert pkv.multi_query_q8_workspace_bytes(5, 257, H, H, 64, B, 2500) > 0
+    _clean()
+    c["lens"][gone] = 256
+    c["tables"][0, 40], c["tables"][2, 3] = -1, nb
+    missing = {0: range(40 * B, 41 * B), 2: range(3 * B, 4 * B)}
+    if gone != 4:
+        c["tables"][4, 100] = -1
+        missing[4] = range(100 * B, 101 * B)
+    out = _run(c, 0.125, BF, 257, 2500)
+    assert _clean() == _lib.DEVERR_CONTEXT | _lib.DEVERR_BLOCK_ID
+    own = slice(starts[gone], starts[gone + 1])
+    assert (out[own] == 7.0).all()
+    want, bound = _want(c, 0.125, BF, missing)
+    want[own], bound[own] = 7.0, 0.0
+    check(out, want, bound, "what is left")
+    nan = torch.zeros(out.shape, dtype=torch.bool)
+    for s, t, h, d in ((0, 1399, 5, 3), (0, 20, 31, 63), (2, 2499, 0, 0), (4, 2200, 17, 9),
+                       (4, 9, 31, 1)):
+        if s == gone:
+            continue
+        b = int(c["tables"][s, t // B])
+        c["vp"].view(torch.uint8)[b, t % B, h, d] = 0x7f
+        first = max(0, t - (EQUAL[s][1] - EQUAL[s][0]))
+        nan[starts[s] + first:starts[s + 1], h, d] = True
+    hit = _run(c, 0.125, BF, 257, 2500)
+    _clean()
+    assert torch.equal(hit.isnan().cpu(), nan)
+    assert torch.equal(hit[~nan.cuda()], out[~nan.cuda()])
+
+
+def test_streams_graphs_of_many_row_tiles():
+    c = _problem(EQUAL, 32, 32, 64, 16, BF, 22)
+    want = _run(c, 0.1, BF, 257, 2500)
+    n = pkv.multi_query_q8_workspace_bytes(5, 257, 32, 32, 64, 16, 2500)
+    assert n > 0
+    q = c["q"].cuda()
+    outs, graphs = [], []
+    for i in range(2):
+        out, ws = torch.zeros_like(want), torch.full((n,), 0xff, dtype=torch.uint8, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            pkv.paged_attn_multi_query_q8(out, q, c["q_start"], c["kp"], c["vp"], c["ks"], c["vs"],
+                                          c["tables"], c["lens"], 0.1, 257, 2500, workspace=ws)
+        outs.append((out, ws))
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert _clean() == 0
+    for out, _ in outs:
+        assert torch.equal(out, want)
+    # other lengths at the next replay
+    c["lens"].copy_(torch.tensor([700, 257, 300, 599, 1500], dtype=torch.int32))
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0][0], _run(c, 0.1, BF, 257, 2500))
+
+
 def test_one_token_is_the_decode():
     lens = [300, 17, 1]
     c = _problem([(1, n) for n in lens], 8, 2, 64, 16, FP, 16)
