@@ -478,8 +478,6 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
     constexpr int kRowStep = kAppendThreads / (J * HC);
     static_assert(kRowStep >= 1 && kRowStep * kAppendItems == B, "items");
     const int h = tid / J % HC, r0 = tid / (J * HC);
-    // (a head's items are on J neighbouring lanes)
-    const unsigned group = (unsigned)((1u << J) - 1u) << (lane / J * J);
     struct Step {
         int hs0;                    // first head slot
         int row_lo, row_hi, run_lo, run_hi;
@@ -524,7 +522,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
         const bool key = hs < p.n_kv_heads, real = hs < n_slots;
         const int kvh = key ? hs : hs - p.n_kv_heads;
         // ---- values, rotated, and the largest of every run and head
-        float x[kAppendItems][16];
+        float x[kAppendItems][16], most[kAppendItems] = {};
         unsigned lives = 0u;                  // items that are written
 #pragma unroll
         for (int n = 0; n < kAppendItems; ++n) {
@@ -546,8 +544,17 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
                 to[at.a] = a[n];
                 to[at.b] = b[n];
             }
-            const uint32_t bits = __reduce_max_sync(group, __float_as_uint(largest(x[n])));
-            if (j == 0) atomicMax(&top[(s_row[r].run - now.run_lo) * HC + h], bits);
+            most[n] = largest(x[n]);
+        }
+        // (a head's items are on J neighbouring lanes)
+#pragma unroll
+        for (int n = 0; n < kAppendItems; ++n) {
+#pragma unroll
+            for (int off = 1; off < J; off <<= 1)
+                most[n] = fmaxf(most[n], __shfl_xor_sync(0xffffffffu, most[n], off));
+            if (j == 0 && ((lives >> n) & 1u))
+                atomicMax(&top[(s_row[now.row_lo + r0 + n * kRowStep].run - now.run_lo) * HC + h],
+                          __float_as_uint(most[n]));
         }
         const float was = old;
         const Step next = step_at(min(i + 1, n_steps - 1));
