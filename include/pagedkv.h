@@ -707,7 +707,8 @@ PKV_API pkv_status kv_append_rope(void* k_pool, void* v_pool, const void* k, int
  *                are not appended (flagged PKV_DEVERR_SLOT; q_out is written).  If
  *                the tokens of one block stand apart in the call, that block's
  *                contents are undefined.  The block is the call's alone while it
- *                runs (shared ones are copied on write).
+ *                runs (shared ones are copied on write; a block's copy is its rows
+ *                of the pools and of the scales).
  *   other arguments as kv_append_rope: k, v, q, q_out and k_out are 16-bit.
  * One launch.
  */
@@ -777,10 +778,12 @@ PKV_API pkv_status paged_attn_decode_q8(
  * Supported shapes as paged_attn_decode; at most 65535 sequences, 4096 query heads.
  *   workspace    device, >= pkv_multi_query_q8_workspace_bytes(...) bytes, 256-byte
  *                aligned; contents on entry are ignored; may be NULL when that size is
- *                0 (chunks that fill the SMs).  Calls that may overlap on the GPU need
- *                a workspace each.
- * On tcgen05, 256 rows (tokens x query heads of a kv head) at a time; where those are
- * few their keys are cut into parts, merged by a second launch.
+ *                0.  Calls that may overlap on the GPU need a workspace each.
+ * On tcgen05, 256 rows (tokens x query heads of a kv head) at a time; the keys of rows
+ * that would leave SMs idle are cut into parts, merged by a second launch.  A few tokens
+ * with short contexts are decoded one by one, in one launch.  Which way is taken follows
+ * from the sizes and bounds of the call, never from the data; the same call gives the
+ * same bits, other bounds may give other last bits.
  */
 PKV_API size_t pkv_multi_query_q8_workspace_bytes(int num_seqs, int max_q_len, int n_heads,
                                                   int n_kv_heads, int head_dim, int block_size,

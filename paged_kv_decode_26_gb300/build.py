@@ -69,7 +69,7 @@ def _compile_calls() -> str:
     """The extension's object (its headers are torch's and Python's)."""
     import torch
     top = os.path.join(os.path.dirname(torch.__file__), "include")
-    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
     obj = os.path.join(BUILD, "tensor_calls.cpp.o")
     abi = int(getattr(torch._C, "_GLIBCXX_USE_CXX11_ABI", True))
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",

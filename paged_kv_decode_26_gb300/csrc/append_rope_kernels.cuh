@@ -157,7 +157,9 @@ __device__ __forceinline__ bool token_lives(const AppendRopeParams& p, int64_t s
 // ------------------------------------------------------------ 16-bit pages
 //
 // CTA x: a token; its query, key and value heads are kRopeBatch items a thread
-// at a time, all loads ahead of the first store.
+// at a time, all loads ahead of the first store (2 / 3 of them: 85 / 80 us
+// for 16 prompts of 128-2048 tokens, 32 query and 8 kv heads, 5.9 TB/s; 4 tokens of a
+// small model 2.2 us, 250 of 32 heads 4.1).
 constexpr int kRopeBatch = 3;
 
 template <int D, typename T>
@@ -248,6 +250,12 @@ __global__ void __launch_bounds__(kRopeThreads)
 // last run, which goes by itself if it does not fit beside the others.
 // A thread holds its items from the one pass over them to the next (the largest
 // value, then the codes), while the next part's rows and scales are on their way.
+//
+// Measured: 8 prompts of 300-2048 tokens, 32 heads of 128, 87 us (3.8 TB/s), 16 of 32
+// query and 8 kv heads 94 (4.4 TB/s), 4 tokens 3.2 us.  Not bound by HBM but by the steps:
+// 300 instructions an item, two barriers a step.  A warp per run and head, its rows in
+// shared memory and no barriers, took 95 us and 6.4 for the 4 tokens; one barrier a step
+// 121; the parts of a window side by side in the grid 132.
 
 constexpr int kLeastExponent = -117;           // of a scale (a block of zeros)
 constexpr int kAppendThreads = 128;
