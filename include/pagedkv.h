@@ -781,9 +781,9 @@ PKV_API pkv_status paged_attn_decode_q8(
  *                0.  Calls that may overlap on the GPU need a workspace each.
  * On tcgen05, 256 rows (tokens x query heads of a kv head) at a time; the keys of rows
  * that would leave SMs idle are cut into parts, merged by a second launch.  A few tokens
- * with short contexts are decoded one by one, in one launch.  Which way is taken follows
- * from the sizes and bounds of the call, never from the data; the same call gives the
- * same bits, other bounds may give other last bits.
+ * with short contexts take the kernel of paged_attn_decode_q8, in one launch.  Which way
+ * is taken follows from the sizes and bounds of the call, never from the data; the same
+ * call gives the same bits, other bounds may give other last bits.
  */
 PKV_API size_t pkv_multi_query_q8_workspace_bytes(int num_seqs, int max_q_len, int n_heads,
                                                   int n_kv_heads, int head_dim, int block_size,

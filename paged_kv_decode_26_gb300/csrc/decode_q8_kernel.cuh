@@ -50,11 +50,11 @@ constexpr float kQ8LeastScale = 0x1p-100f;     // of a reference (blocks of zero
 struct Q8Params : PieceParams {
     const float* k_scale;      // [num_blocks, n_kv_heads]
     const float* v_scale;
-    // decode_q8_short_kernel on chunks (else null): a CTA per token of sequence
-    // s, q rows q_start[s] .. q_start[s + 1] - 1, at most max_q_len
+    // decode_q8_short_kernel on chunks (q_start else null)
     const int32_t* q_start;
     int total_q;
     int max_q_len;
+    const unsigned char* v_codes;      // the value pool
 };
 
 // Two codes each of the low and the high half of w, as packed fp16 (exact).
@@ -73,12 +73,23 @@ __device__ __forceinline__ uint32_t q8_transpose(uint32_t x) {
     return y;
 }
 
+// Byte mask of the NaN codes (0x7f, 0xff) of a word.
+__device__ __forceinline__ uint32_t q8_nans(uint32_t w) {
+    return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+}
+
 // Byte offset of 16-byte unit c of token row t in a box of [16 x D] bytes, swizzled
 // over D bytes.
 template <int D>
 __device__ __forceinline__ uint32_t q8_at(int t, int c) {
     return D == 128 ? (uint32_t)(t * 128 + ((c ^ (t & 7)) << 4))
                     : (uint32_t)(t * 64 + ((c ^ ((t >> 1) & 3)) << 4));
+}
+
+// Where lane 4 gid + tig finds its head's query among `heads` rows from q on.
+template <int D, typename T>
+__device__ __forceinline__ const T* q8_head_row(const T* q, int heads, int lane) {
+    return q + (size_t)(lane >> 2 < heads ? lane >> 2 : 0) * D;
 }
 
 // One kv head's query heads in one warp, lane = 4 gid + tig: queries as B operands
@@ -96,11 +107,9 @@ struct Q8Heads {
 };
 
 template <int D, typename T>
-__device__ __forceinline__ void q8_heads_start(Q8Heads<D>& st, const T* qrow0, int G,
+__device__ __forceinline__ void q8_heads_start(Q8Heads<D>& st, const T* row, bool real,
                                                float scale_log2, int lane) {
-    const int gid = lane >> 2, tig = lane & 3;
-    const bool real = gid < G;
-    const T* row = qrow0 + (size_t)(real ? gid : 0) * D;
+    const int tig = lane & 3;
     uint2 w[D / 16];
 #pragma unroll
     for (int c = 0; c < D / 16; ++c)
@@ -152,10 +161,12 @@ struct Q8Scales {
 
 // One chunk: halves of 16 tokens at kbase / vbase (+ 16 D bytes), `valid[h]` of a
 // half's tokens inside the context (0: nothing was loaded, or its block is
-// missing).  PRECISE: see piece_chunk.
-template <int D, bool PRECISE>
+// missing).  PRECISE: see piece_chunk.  MASKED: of `left[h]` tokens from the half's
+// first one on (0 if its block is missing), this lane's heads do not see the last less[e].
+template <int D, bool PRECISE, bool MASKED = false>
 __device__ __forceinline__ void q8_chunk(Q8Heads<D>& st, uint32_t kbase, uint32_t vbase,
-                                         const int (&valid)[2], const Q8Scales& sc, int lane) {
+                                         const int (&valid)[2], const int (&left)[2],
+                                         const int (&less)[2], const Q8Scales& sc, int lane) {
     using Range = WeightRange<__half>;
     constexpr uint32_t HALF = 16 * D;
     const int gid = lane >> 2, tig = lane & 3;
@@ -182,11 +193,12 @@ __device__ __forceinline__ void q8_chunk(Q8Heads<D>& st, uint32_t kbase, uint32_
         }
         // this lane: tokens gid (x0, x1) and gid + 8 (x2, x3) of heads 2 tig, + 1
         const float f0 = st.qf[0] * sc.k[h], f1 = st.qf[1] * sc.k[h];
-        const bool in0 = gid < valid[h], in1 = gid + 8 < valid[h];
-        x[h][0] = in0 ? __fmul_rn(s0[0] + s1[0], f0) : -INFINITY;
-        x[h][1] = in0 ? __fmul_rn(s0[1] + s1[1], f1) : -INFINITY;
-        x[h][2] = in1 ? __fmul_rn(s0[2] + s1[2], f0) : -INFINITY;
-        x[h][3] = in1 ? __fmul_rn(s0[3] + s1[3], f1) : -INFINITY;
+        const int see0 = MASKED ? left[h] - less[0] : valid[h];
+        const int see1 = MASKED ? left[h] - less[1] : valid[h];
+        x[h][0] = gid < see0 ? __fmul_rn(s0[0] + s1[0], f0) : -INFINITY;
+        x[h][1] = gid < see1 ? __fmul_rn(s0[1] + s1[1], f1) : -INFINITY;
+        x[h][2] = gid + 8 < see0 ? __fmul_rn(s0[2] + s1[2], f0) : -INFINITY;
+        x[h][3] = gid + 8 < see1 ? __fmul_rn(s0[3] + s1[3], f1) : -INFINITY;
     }
     // ---- the reference, where a weight would leave its range
     float lv[2], bv[2];
@@ -250,9 +262,10 @@ __device__ __forceinline__ void q8_chunk(Q8Heads<D>& st, uint32_t kbase, uint32_
         st.l[0] += p0 + p2;
         st.l[1] += p1 + p3;
         // (a half with nothing in it may have any scale)
-        const bool any = valid[h] > 0;
-        const float w0 = any ? p0 * f0 : 0.f, w1 = any ? p1 * f1 : 0.f;
-        const float w2 = any ? p2 * f0 : 0.f, w3 = any ? p3 * f1 : 0.f;
+        const bool any0 = (MASKED ? left[h] - less[0] : valid[h]) > 0;
+        const bool any1 = (MASKED ? left[h] - less[1] : valid[h]) > 0;
+        const float w0 = any0 ? p0 * f0 : 0.f, w1 = any1 ? p1 * f1 : 0.f;
+        const float w2 = any0 ? p2 * f0 : 0.f, w3 = any1 ? p3 * f1 : 0.f;
         const uint32_t a = pack2<__half>(w0, w1), b = pack2<__half>(w2, w3);
         const float2 fa = unpack2<__half>(a), fb = unpack2<__half>(b);
         hi[h][0] = q8_transpose(a);
@@ -294,11 +307,11 @@ __device__ __forceinline__ void q8_chunk(Q8Heads<D>& st, uint32_t kbase, uint32_
     }
 }
 
-// A piece's result: normalised rows row0 + head to the output (WHOLE) or, with (m,
-// L), to o and ml (of the workspace or shared memory).
-template <int D, bool WHOLE>
-__device__ __forceinline__ void q8_store(const Q8Heads<D>& st, const Q8Params& p, size_t row0,
-                                         float* o, float* ml, int lane) {
+// A piece's result: the normalised rows row_of(head) of `heads` heads to the output
+// (WHOLE) or, with (m, L), to o and ml (of the workspace or shared memory).
+template <int D, bool WHOLE, class RowOf>
+__device__ __forceinline__ void q8_store(const Q8Heads<D>& st, const Q8Params& p, int heads,
+                                         RowOf row_of, float* o, float* ml, int lane) {
     const int gid = lane >> 2, tig = lane & 3;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -306,11 +319,11 @@ __device__ __forceinline__ void q8_store(const Q8Heads<D>& st, const Q8Params& p
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
         const int hh = 2 * tig + e;
-        if (hh >= p.group) continue;
+        if (hh >= heads) continue;
         // (1 / rv in two factors: either alone may leave fp32's range)
         const float inv = l != 0.f ? __fdiv_rn(WeightRange<__half>::UNLIFT, l) : 0.f;
         const float b = __frcp_rn(st.rv[e]);
-        const size_t row = row0 + hh;
+        const size_t row = row_of(hh);
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
             const float v0 = st.o[j][e] * inv * b, v1 = st.o[j][2 + e] * inv * b;
@@ -445,9 +458,10 @@ __device__ __forceinline__ void q8_worker(const Q8Params& p, const CUtensorMap& 
         }
         if (fresh) {
             q8_heads_start<D, T>(state,
-                                 reinterpret_cast<const T*>(p.q) +
-                                     ((size_t)at.s * p.n_heads + qh0) * D,
-                                 p.group, p.scale_log2, lane);
+                                 q8_head_row<D, T>(reinterpret_cast<const T*>(p.q) +
+                                                       ((size_t)at.s * p.n_heads + qh0) * D,
+                                                   p.group, lane),
+                                 lane >> 2 < p.group, p.scale_log2, lane);
             from_start = at.c == at.first;
             fresh = false;
         }
@@ -465,7 +479,7 @@ __device__ __forceinline__ void q8_worker(const Q8Params& p, const CUtensorMap& 
         }
         const uint32_t kbase = smem_addr(ring) + st * SLOT;
         if (valid[0] > 0 || valid[1] > 0)
-            q8_chunk<D, PRECISE>(state, kbase, kbase + 2 * HALF, valid, sc, lane);
+            q8_chunk<D, PRECISE>(state, kbase, kbase + 2 * HALF, valid, valid, valid, sc, lane);
         __syncwarp();
         --in_flight;
         if (++st == kQ8Stages) {
@@ -478,13 +492,15 @@ __device__ __forceinline__ void q8_worker(const Q8Params& p, const CUtensorMap& 
             const size_t pair = (size_t)at.s * p.n_kv_heads + kvh;
             const size_t own = (size_t)at.s * p.n_heads + qh0;
             if (from_start && pair_end)
-                q8_store<D, true>(state, p, own, nullptr, nullptr, lane);
-            else
-                q8_store<D, false>(state, p,
-                                   from_start ? own
-                                              : (size_t)p.num_seqs * p.n_heads +
-                                                    ((size_t)at.v * HW + hw) * p.group,
-                                   p.ws_o, p.ws_ml, lane);
+                q8_store<D, true>(
+                    state, p, p.group, [&](int h) { return own + h; }, nullptr, nullptr, lane);
+            else {
+                const size_t to = from_start ? own
+                                             : (size_t)p.num_seqs * p.n_heads +
+                                                   ((size_t)at.v * HW + hw) * p.group;
+                q8_store<D, false>(
+                    state, p, p.group, [&](int h) { return to + h; }, p.ws_o, p.ws_ml, lane);
+            }
             if (lane == 0) {
                 if (from_start) p.seg_first[pair] = at.v;
                 if (pair_end) p.seg_last[pair] = at.v;
@@ -522,15 +538,18 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
 
 // Short contexts: a CTA per (sequence, kv head), its warps taking the chunks in
 // turn, their states merged in shared memory: one launch, and no line of units to
-// lay out first.  Of chunks of a few tokens (blockIdx.z) each is a context of its own,
-// up to the token.
+// lay out first.
+// CHUNK: sequence s has the queries q_start[s] .. q_start[s + 1] - 1, and 8 / G tokens of
+// it (the blockIdx.z-th) with their G heads are the product's eight columns.  The last
+// tokens of the context that some of them do not see are masked in the scores; NaN in
+// their values is taken out in shared memory and put where it belongs at the end.
 constexpr int kQ8ShortWarps = 12;        // at most
 
 inline size_t decode_q8_short_smem_bytes(int D, int warps) {
     return 1024 + (size_t)warps * kQ8Stages * 4 * 16 * D;
 }
 
-template <int D, typename T, bool PRECISE>
+template <int D, typename T, bool PRECISE, bool CHUNK>
 __global__ void __launch_bounds__(32 * kQ8ShortWarps)
     decode_q8_short_kernel(const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v,
@@ -539,6 +558,7 @@ __global__ void __launch_bounds__(32 * kQ8ShortWarps)
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ uint64_t s_bar[kQ8ShortWarps * kQ8Stages];
     __shared__ float s_ml[kQ8ShortWarps * 8 * 2];
+    __shared__ int s_poison;
     const uint32_t raw = smem_addr(smem_raw);
     unsigned char* sm = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
@@ -547,19 +567,31 @@ __global__ void __launch_bounds__(32 * kQ8ShortWarps)
     uint64_t* full = s_bar + warp * kQ8Stages;
     const int raw_n = p.context_lens[s];
     int n = piece_length(p, s);
-    size_t row0 = (size_t)s * p.n_heads + qh0;       // of the output
+    size_t row0 = (size_t)s * p.n_heads + qh0;       // of the first column
+    int tokens = 1;                                  // whose heads are the columns
     bool ok = raw_n == n;
-    int q_len = 1;
-    if (p.q_start) {
-        const int qs0 = p.q_start[s], qs1 = p.q_start[s + 1];
-        q_len = qs1 - qs0;
+    if (CHUNK) {
+        const int qs0 = p.q_start[s], qs1 = p.q_start[s + 1], q_len = qs1 - qs0;
+        const int first = (int)blockIdx.z * (8 / p.group);
         ok = ok && q_len >= 0 && q_len <= n && qs0 >= 0 && qs1 <= p.total_q && q_len <= p.max_q_len;
-        n -= q_len - 1 - (int)blockIdx.z;
-        row0 = (size_t)(qs0 + (int)blockIdx.z) * p.n_heads + qh0;
+        tokens = min(8 / p.group, q_len - first);
+        n -= q_len - first - tokens;                 // the last one's context
+        row0 += (size_t)(qs0 + first - s) * p.n_heads;
     }
     if (!ok && threadIdx.x == 0 && kvh == 0 && blockIdx.z == 0)
         raise_error(p.errors, PKV_DEVERR_CONTEXT);
-    if (p.q_start && (!ok || (int)blockIdx.z >= q_len)) return;
+    if (CHUNK && (!ok || tokens <= 0)) return;
+    const int cols = tokens * p.group;
+    auto row_of = [&](int c) -> size_t {
+        return CHUNK ? row0 + (size_t)(c / p.group) * p.n_heads + c % p.group : row0 + c;
+    };
+    // tokens of the context that column c does not see, the last ones
+    auto hidden = [&](int c) { return CHUNK ? max(tokens - 1 - c / p.group, 0) : 0; };
+    const int less[2] = {hidden(2 * (lane & 3)), hidden(2 * (lane & 3) + 1)};
+    if (CHUNK) {
+        if (threadIdx.x == 0) s_poison = 0;
+        __syncthreads();
+    }
     const int chunks = (n + kQ8Tokens - 1) / kQ8Tokens;
     if (lane == 0) {
         for (int i = 0; i < kQ8Stages; ++i) mbar_init(&full[i], 1);
@@ -610,8 +642,10 @@ __global__ void __launch_bounds__(32 * kQ8ShortWarps)
     Q8Heads<D> state;
     if (warp < chunks) {
         Blocks now = issue(warp, 0);
-        q8_heads_start<D, T>(state, reinterpret_cast<const T*>(p.q) + row0 * D, p.group,
-                             p.scale_log2, lane);
+        const int own = lane >> 2;
+        q8_heads_start<D, T>(state,
+                             reinterpret_cast<const T*>(p.q) + row_of(own < cols ? own : 0) * D,
+                             own < cols, p.scale_log2, lane);
         int st = 0;
         uint32_t phase = 0;
         for (int c = warp; c < chunks; c += warps) {
@@ -625,13 +659,33 @@ __global__ void __launch_bounds__(32 * kQ8ShortWarps)
                 if (more) mbar_wait(&full[st ^ 1], st ? phase ^ 1u : phase, p.errors);
                 break;
             }
-            int valid[2];
+            int valid[2], left[2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                valid[h] = now.b[h] >= 0 ? min(16, n - c * kQ8Tokens - 16 * h) : 0;
+            for (int h = 0; h < 2; ++h) {
+                left[h] = now.b[h] >= 0 ? n - c * kQ8Tokens - 16 * h : 0;
+                valid[h] = min(16, left[h]);
+            }
             const uint32_t kbase = smem_addr(ring) + st * SLOT;
+            if (CHUNK) {
+                // (a lane has 16 bytes of a row; nothing is loaded over the context's last
+                // chunks again)
+                for (int k = max(n - tokens + 1, c * kQ8Tokens); k < min(n, (c + 1) * kQ8Tokens); ++k) {
+                    const int h = k / 16 % 2;
+                    if ((h ? now.b[1] : now.b[0]) < 0 || lane >= D / 16) continue;
+                    uint4* unit = reinterpret_cast<uint4*>(ring + st * SLOT + (2 + h) * HALF +
+                                                           q8_at<D>(k % 16, lane));
+                    const uint4 w = *unit;
+                    const uint4 bad = make_uint4(q8_nans(w.x), q8_nans(w.y), q8_nans(w.z),
+                                                 q8_nans(w.w));
+                    if ((bad.x | bad.y | bad.z | bad.w) == 0u) continue;
+                    *unit = make_uint4(w.x & ~bad.x, w.y & ~bad.y, w.z & ~bad.z, w.w & ~bad.w);
+                    s_poison = 1;
+                }
+                __syncwarp();
+            }
             if (valid[0] > 0 || valid[1] > 0)
-                q8_chunk<D, PRECISE>(state, kbase, kbase + 2 * HALF, valid, now.sc, lane);
+                q8_chunk<D, PRECISE, CHUNK>(state, kbase, kbase + 2 * HALF, valid, left, less, now.sc,
+                                            lane);
             __syncwarp();
             now = next;
             if (st) phase ^= 1u;
@@ -640,14 +694,16 @@ __global__ void __launch_bounds__(32 * kQ8ShortWarps)
     }
     // ---- the warps' states (each over its own ring)
     const int active = min(chunks, warps);
-    if (active == 1) {
-        if (warp == 0) q8_store<D, true>(state, p, row0, nullptr, nullptr, lane);
+    if (!CHUNK && active == 1) {
+        if (warp == 0) q8_store<D, true>(state, p, cols, row_of, nullptr, nullptr, lane);
         return;
     }
     if (warp < active)
-        q8_store<D, false>(state, p, 0, reinterpret_cast<float*>(ring), s_ml + warp * 16, lane);
+        q8_store<D, false>(
+            state, p, cols, [](int c) { return (size_t)c; }, reinterpret_cast<float*>(ring),
+            s_ml + warp * 16, lane);
     __syncthreads();
-    for (int e = threadIdx.x; e < p.group * (D / 2); e += blockDim.x) {
+    for (int e = threadIdx.x; e < cols * (D / 2); e += blockDim.x) {
         const int h = e / (D / 2), d = e % (D / 2) * 2;
         float2 ml = make_float2(-INFINITY, 0.f);
         for (int w = 0; w < active; ++w)
@@ -662,7 +718,18 @@ __global__ void __launch_bounds__(32 * kQ8ShortWarps)
             o.x += f * x.x;
             o.y += f * x.y;
         }
-        const size_t at = (row0 + h) * D + d;
+        if (CHUNK && s_poison) {
+            // NaN that was taken out, to the columns that see it
+            for (int k = n - tokens + 1; k < n - hidden(h); ++k) {
+                const int b = p.block_tables[(size_t)s * p.max_blocks_per_seq + k / p.block_size];
+                if (b < 0 || b >= p.num_blocks) continue;
+                const unsigned char* v =
+                    p.v_codes + (((size_t)b * p.block_size + k % p.block_size) * p.n_kv_heads + kvh) * D + d;
+                if ((v[0] & 0x7f) == 0x7f) o.x = NAN;
+                if ((v[1] & 0x7f) == 0x7f) o.y = NAN;
+            }
+        }
+        const size_t at = row_of(h) * D + d;
         if (p.out_dtype == PKV_F32)
             *reinterpret_cast<float2*>(reinterpret_cast<float*>(p.out) + at) = o;
         else

@@ -119,11 +119,6 @@ __device__ __forceinline__ void mq8_store(uint32_t at, const uint4& v) {
                  : "memory");
 }
 
-// Byte mask of the NaN codes (0x7f, 0xff) of a word.
-__device__ __forceinline__ uint32_t mq8_nans(uint32_t w) {
-    return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
-}
-
 // Rows of items in pieces, merged: a warp per row of the x-th item of several parts.
 constexpr int kMq8MergeRows = 16;
 constexpr int kMq8MergeThreads = 32 * kMq8MergeRows;
@@ -438,8 +433,8 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
 #pragma unroll
                     for (int n = 0; n < kParts; ++n) {
                         uint4& w = now.codes[n];
-                        const uint4 bad = make_uint4(mq8_nans(w.x), mq8_nans(w.y), mq8_nans(w.z),
-                                                     mq8_nans(w.w));
+                        const uint4 bad = make_uint4(q8_nans(w.x), q8_nans(w.y), q8_nans(w.z),
+                                                     q8_nans(w.w));
                         any |= (bad.x | bad.y | bad.z | bad.w) != 0u;
                         w = make_uint4(w.x & ~bad.x, w.y & ~bad.y, w.z & ~bad.z, w.w & ~bad.w);
                     }

@@ -87,10 +87,12 @@ pkv_status check_scales(const float* k_scale, const float* v_scale, int num_bloc
 // 4000, 32 query and 8 kv heads, 117 / 103, of 100 at 8192 120 / 35; 2 chunks of 2 tokens, 4
 // heads, at 16000 229 / 27; 16 of up to 8 tokens at up to 1000, 16 query and 4 kv heads 16.6
 // / 16.1; of 512 tokens at 600 23.1 / 27.8, therefore whole.
-// Where there is an SM for every token and kv head, and contexts are short, the decode
-// of whole contexts takes each token for itself (2 tokens, 4 heads, context 1000: 13.4
-// us in row tiles, 9.5 so; with more CTAs than SMs it loses: 512 of up to 1000 tokens
-// 18.2 / 24.5).
+// A few tokens with short contexts go to the decode of whole contexts, 8 / G tokens to a
+// CTA, where its CTAs are all on the SMs at once (their rings: two a SM at head_dim 64, one
+// at 128).  Row tiles / so, us, head_dim 64, 16 query and 4 kv heads: 16 sequences of 8
+// tokens at 900-1000 18.8 / 14.1, of up to 8 at up to 1000 16.1 / 11.2, 1 of 2 tokens 13.9
+// / 10.0, of 150 21.3 / 14.1; head_dim 128, 32 and 8 heads, 4 of up to 16 at 900 (256
+// CTAs) 17.7 / 23.9.
 constexpr int kPartTiles = 4;
 constexpr int kItemTiles = 2;
 constexpr int kMergeTiles = 3;
@@ -100,17 +102,18 @@ struct ChunkShape {
     long long whole;      // items that are not cut
     int splits;           // parts of the others
     size_t o, ml, heads, end;    // workspace
-    int by_token;         // warps of a CTA for each token's context, 0: row tiles
+    int by_token;         // warps of a CTA that decodes whole contexts, 0: row tiles
 };
 ChunkShape chunk_shape(int num_seqs, int max_q_len, int n_heads, int n_kv_heads, int head_dim,
                        int max_context_len, int sm_count) {
     ChunkShape c;
     std::memset(&c, 0, sizeof(c));
-    const long long tokens = (long long)num_seqs * max_q_len;
-    if (tokens * n_kv_heads <= sm_count)
-        c.by_token = whole_contexts(tokens * n_kv_heads, max_context_len, sm_count);
-    if (c.by_token) return c;
     const int G = n_heads / n_kv_heads, cta_tokens = 2 * pkv::kMq8Rows / G;
+    const long long pairs =
+        (long long)num_seqs * n_kv_heads * (((long long)max_q_len + 8 / G - 1) / (8 / G));
+    if (pairs <= (long long)sm_count * (128 / head_dim))
+        c.by_token = whole_contexts(pairs, max_context_len, sm_count) ? pkv::kQ8ShortWarps : 0;
+    if (c.by_token) return c;
     c.tiles = (int)(((long long)max_q_len + cta_tokens - 1) / cta_tokens);
     c.items = (long long)c.tiles * n_kv_heads * num_seqs;
     c.whole = c.items / sm_count * sm_count;
@@ -273,6 +276,7 @@ PKV_API pkv_status paged_attn_multi_query_q8(
         p.q_start = q_start;
         p.total_q = total_q;
         p.max_q_len = max_q_len;
+        p.v_codes = static_cast<const unsigned char*>(v_pool);
         e = q_dtype == PKV_BF16 ? pkv::launch_decode_q8_bf16(head_dim, L)
                                 : pkv::launch_decode_q8_f16(head_dim, L);
         return e == cudaSuccess ? PKV_OK : cuda_fail(e);

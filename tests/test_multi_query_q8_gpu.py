@@ -408,6 +408,53 @@ def test_streams_graphs_of_many_row_tiles():
     assert torch.equal(outs[0][0], _run(c, 0.1, BF, 257, 2500))
 
 
+FEW = [(1, 1), (7, 7), (8, 8), (9, 33), (2, 32), (3, 31), (8, 64), (5, 65), (0, 9), (6, 1000), (4, 35)]
+
+
+@pytest.mark.parametrize("out_dtype", [BF, F32])
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+@pytest.mark.parametrize("D,B", [(64, 16), (128, 32)])
+def test_few_tokens(D, B, G, out_dtype):
+    """Tokens of a sequence as columns of one product (the second bound: row tiles)."""
+    c = _problem(FEW, G, 1, D, B, BF, 23)
+    for bound in (5000, 1000):
+        out = _run(c, 0.1, out_dtype, 9, bound)
+        assert _clean() == 0
+        check(out, *_want(c, 0.1, out_dtype), f"few tokens, bound {bound}")
+    # NaN in values of the last tokens, and in the scale of a block that only they reach
+    nan = torch.zeros(c["q"].shape, dtype=torch.bool)
+    for s, t, d in ((0, 0, 3), (2, 7, 0), (3, 32, D - 1), (3, 30, 1), (7, 63, 5), (7, 64, 5),
+                    (9, 995, 2), (9, 10, 9), (10, 31, 40), (10, 32, 41), (10, 34, 42)):
+        b = int(c["tables"][s, t // B])
+        c["vp"].view(torch.uint8)[b, t % B, 0, d] = 0xff
+        m, n = FEW[s]
+        nan[c["starts"][s] + max(0, t - (n - m)):c["starts"][s + 1], :, d] = True
+    hit = _run(c, 0.1, out_dtype, 9, 1000)
+    assert torch.equal(hit.isnan().cpu(), nan)
+    assert torch.equal(hit[~nan.cuda()], out[~nan.cuda()])
+    last = int(c["tables"][3, 32 // B])              # holds token 32 alone
+    c["vs"][last, 0] = math.nan
+    again = _run(c, 0.1, out_dtype, 9, 1000)
+    assert _clean() == 0
+    own = slice(c["starts"][3] + 8, c["starts"][4])  # the one token that sees it
+    nan[own] = True
+    assert torch.equal(again.isnan().cpu(), nan)
+    assert torch.equal(again[~nan.cuda()], hit[~nan.cuda()])
+
+
+def test_few_tokens_of_missing_blocks():
+    c = _problem([(6, 40), (3, 20), (5, 70)], 4, 2, 64, 16, FP, 24)
+    nb = c["kp"].shape[0]
+    _clean()
+    c["tables"][0, 2], c["tables"][2, 1] = nb, -1    # the last block of the first
+    c["lens"][1] = 2                                 # below its new tokens
+    out = _run(c, 0.1, F32, 6, 70)
+    assert _clean() == _lib.DEVERR_BLOCK_ID | _lib.DEVERR_CONTEXT
+    want, bound = _want(c, 0.1, F32, {0: range(32, 40), 2: range(16, 32)})
+    want[6:9], bound[6:9] = 7.0, 0.0
+    check(out, want, bound, "missing blocks")
+
+
 def test_one_token_is_the_decode():
     lens = [300, 17, 1]
     c = _problem([(1, n) for n in lens], 8, 2, 64, 16, FP, 16)
