@@ -666,8 +666,8 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[s
         return (base * factor ** (rotary_dim / (rotary_dim - 2))) ** -pair, 1.0
     if scaling != "yarn":
         raise ValueError(f"unknown scaling {scaling!r}")
-    if original_positions <= 0 or not 0 < beta_slow < beta_fast:
-        raise ValueError("yarn needs original_positions and 0 < beta_slow < beta_fast")
+    if original_positions <= 0 or not 0 < beta_slow < beta_fast or base <= 1:
+        raise ValueError("yarn needs original_positions, 0 < beta_slow < beta_fast and base > 1")
     freq = base ** -pair
 
     def pair_turning(times):

@@ -26,6 +26,15 @@ Span rows_span(const void* p, int64_t stride, int tokens, int heads, int head_di
     return {a, a + 2 * ((uint64_t)(tokens - 1) * (uint64_t)stride + row)};
 }
 
+// Rows of one tensor side by side: a's `an` elements a token, then b's, or the other way.
+bool side_by_side(const void* a, int64_t a_stride, int64_t an, const void* b, int64_t b_stride,
+                  int64_t bn) {
+    if (a_stride != b_stride) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    const uint64_t xn = 2 * (uint64_t)an, yn = 2 * (uint64_t)bn, row = 2 * (uint64_t)a_stride;
+    return x < y ? y - x >= xn && y - x + yn <= row : x - y >= yn && x - y + xn <= row;
+}
+
 Span pool_span(const void* p, size_t bytes) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p);
     return {a, a + bytes};
@@ -93,26 +102,22 @@ pkv_status fill_append(pkv::AppendRopeParams* pp, int es, void* k_pool, void* v_
         if ((st = check_rows(o, stride, heads, head_dim, "")) != PKV_OK) return st;
         out[i] = rows_span(o, stride, num_tokens, heads, head_dim);
         const bool in_place = o == (i ? k : q) && stride == (i ? k_stride : q_stride);
-        for (const Span& s : in)
-            if (!in_place && out[i].meets(s))
+        const void* const from[3] = {k, v, q};
+        const int64_t strides[3] = {k_stride, v_stride, q_stride};
+        for (int n = 0; n < 3; ++n) {
+            if (!out[i].meets(in[n]) || (in_place && n == (i ? 0 : 2))) continue;
+            // (in place, beside the others in one tensor)
+            if (!in_place || !side_by_side(o, stride, (int64_t)heads * head_dim, from[n], strides[n],
+                                           (int64_t)(n == 2 ? n_heads : n_kv_heads) * head_dim))
                 return invalid("q_out and k_out: in place, or apart from q, k and v");
+        }
         for (const Span& s : pools)
             if (pool > 0 && out[i].meets(s)) return invalid("q_out and k_out overlap a pool");
     }
-    const bool both_in_place = q_out == q && k_out == k;
-    if (q_out && k_out && !both_in_place && out[0].meets(out[1])) {
-        // rows of one tensor side by side
-        const bool apart =
-            q_out_stride == k_out_stride &&
-            [&] {
-                const uint64_t a = reinterpret_cast<uintptr_t>(q_out),
-                               b = reinterpret_cast<uintptr_t>(k_out);
-                const uint64_t qn = 2ull * n_heads * head_dim, kn = 2ull * n_kv_heads * head_dim;
-                const uint64_t row = 2ull * (uint64_t)q_out_stride;
-                return a < b ? b - a >= qn && b - a + kn <= row : a - b >= kn && a - b + qn <= row;
-            }();
-        if (!apart) return invalid("q_out and k_out overlap");
-    }
+    if (q_out && k_out && out[0].meets(out[1]) &&
+        !side_by_side(q_out, q_out_stride, (int64_t)n_heads * head_dim, k_out, k_out_stride,
+                      (int64_t)n_kv_heads * head_dim))
+        return invalid("q_out and k_out overlap");
     for (const Span& s : in)
         for (const Span& w : pools)
             if (pool > 0 && s.from != s.to && s.meets(w)) return invalid("q, k or v overlaps a pool");
@@ -266,6 +271,11 @@ PKV_API pkv_status kv_append_rope_q8(void* k_pool, void* v_pool, float* k_scale,
     const size_t scales = (size_t)num_blocks * n_kv_heads * sizeof(float);
     if (num_blocks > 0 && pool_span(k_scale, scales).meets(pool_span(v_scale, scales)))
         return invalid("k_scale and v_scale overlap");
+    const size_t pool = (size_t)num_blocks * block_size * n_kv_heads * head_dim;
+    for (const Span& s : {pool_span(k_scale, scales), pool_span(v_scale, scales)})
+        if (num_blocks > 0 &&
+            (s.meets(pool_span(k_pool, pool)) || s.meets(pool_span(v_pool, pool))))
+            return invalid("the scales overlap a pool");
     DeviceInfo* dev = nullptr;
     cudaError_t e = device_info(&dev);
     if (e != cudaSuccess) return cuda_fail(e);

@@ -67,7 +67,11 @@ struct Here {
         if (!t.is_contiguous()) refuse("tensors must be contiguous (q, k, v and their outputs: each token)");
     }
     void* stream(PyObject* o) const {
-        if (o != Py_None) return reinterpret_cast<void*>((uintptr_t)PyLong_AsUnsignedLongLong(o));
+        if (o != Py_None) {
+            const unsigned long long v = PyLong_AsUnsignedLongLong(o);
+            if (v == (unsigned long long)-1 && PyErr_Occurred()) throw Refused();
+            return reinterpret_cast<void*>((uintptr_t)v);
+        }
         return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();
     }
 };

@@ -68,6 +68,24 @@ def test_scale_refusals(L, kw, code):
 
 
 @pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("kw", [
+    dict(ko=FAKE(5), v=FAKE(5)),                           # keys in place that are the values too
+    dict(qo=FAKE(10), q_s=2048, qo_s=2048, k=C.c_void_p(640 * MB + 1024), k_s=2048),
+    dict(qo=FAKE(10), q_s=2048, qo_s=2048, k=C.c_void_p(640 * MB + 2048), k_s=4096),
+    dict(qo=FAKE(10), ko=FAKE(10), k=FAKE(10)),            # both in place, in the same rows
+])
+def test_refusals_in_place(L, q8, kw):
+    """What is rotated in place lies beside the other inputs, not over them."""
+    assert _call(L, q8, **kw) == 1
+    assert L.pkv_last_error_detail()
+
+
+def test_scales_in_a_pool(L):
+    for kw in (dict(ksc=C.c_void_p(64 * MB + 64)), dict(vsc=C.c_void_p(128 * MB + 64))):
+        assert _call(L, True, **kw) == 1
+
+
+@pytest.mark.parametrize("q8", [False, True])
 def test_no_tokens_is_a_no_op(L, q8):
     assert _call(L, q8, T=0, k=NULL, slots=NULL, kp=NULL) == 0
 
@@ -105,6 +123,7 @@ def test_frequencies():
     for bad in (dict(rotary_dim=7), dict(rotary_dim=0), dict(rotary_dim=64, base=-1.0),
                 dict(rotary_dim=64, factor=0.0), dict(rotary_dim=64, scaling="other"),
                 dict(rotary_dim=2, scaling="ntk", factor=2.0),
-                dict(rotary_dim=64, scaling="yarn", factor=2.0)):
+                dict(rotary_dim=64, scaling="yarn", factor=2.0),
+                dict(rotary_dim=64, base=1.0, scaling="yarn", factor=2.0, original_positions=64)):
         with pytest.raises(ValueError):
             pkv.rope_frequencies(**bad)
