@@ -355,6 +355,45 @@ def test_on_a_stream_and_in_a_graph(T):
         assert torch.equal(a["q"], x["q"])
 
 
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("T", [40, 300])
+def test_offsets_beyond_32_bits(q8, T):
+    """Pools of more than 4 GB and rows 2^24 elements apart, as small ones."""
+    gen = torch.Generator().manual_seed(12)
+    H, Hk, D, B, stride = 4, 32, 128, 16, 1 << 24
+    blocks = -(-T // B) + 1
+    nb = (5 << 30) // (B * Hk * D * (1 if q8 else 2))
+    _, q, k, v = _inputs(T, H, Hk, D, BF, gen)
+    far = [torch.empty(T * stride, dtype=BF, device="cuda") for _ in range(2)]
+    kf, qf = (x.as_strided((T, h, D), (stride, D, 1)) for x, h in zip(far, (Hk, H)))
+    kf.copy_(k)
+    qf.copy_(q)
+    pos = torch.arange(3, T + 3, dtype=torch.int32, device="cuda")
+    table = ref.table64(T + 3, 128, dev="cuda")
+
+    def call(nb, k, q):
+        kind = E4 if q8 else BF
+        pools = [torch.empty(nb, B, Hk, D, dtype=kind, device="cuda") for _ in range(2)]
+        for p in pools:
+            p[-blocks:].view(torch.uint8).zero_()
+        sc = [torch.ones(nb, Hk, device="cuda") for _ in range(2)] if q8 else []
+        slots = (nb - blocks) * B + 3 + torch.arange(T, device="cuda")
+        (pkv.kv_append_rope_q8 if q8 else pkv.kv_append_rope)(*pools, *sc, k, v, slots, pos, table,
+                                                              q, q)
+        return [p[-blocks:].view(torch.uint8).clone() for p in pools] + [x[-blocks:].clone() for x in sc]
+
+    want = call(blocks, k, q.clone())
+    got = call(nb, kf, qf)
+    assert _clean() == 0 and want[0].any()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    turned = q.clone()
+    pkv.kv_append_rope(torch.empty(1, B, Hk, D, dtype=BF, device="cuda"),
+                       torch.empty(1, B, Hk, D, dtype=BF, device="cuda"), k[:B], v[:B],
+                       torch.arange(B, device="cuda"), pos[:B], table, turned[:B], turned[:B])
+    assert torch.equal(qf[:B], turned[:B])
+
+
 def test_nothing_to_append():
     k = torch.zeros(0, 2, 64, dtype=BF, device="cuda")
     pools = [torch.zeros(2, 16, 2, 64, dtype=BF, device="cuda") for _ in range(2)]
