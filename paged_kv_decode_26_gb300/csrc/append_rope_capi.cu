@@ -157,9 +157,12 @@ void launch_append(const pkv::AppendRopeParams& p, cudaStream_t stream) {
            stream>>>(p);
 }
 
-// Tokens from which a CTA takes a window of block_size tokens instead of one.
+// Tokens from which a CTA takes a window of block_size tokens instead of one (decode
+// tokens, one / block_size: 64 3.9 / 8.6 us, 256 8.9 / 8.9, 900 26.7 / 9.8; a prompt of
+// 300 24 / 9.4).
 constexpr int kQ8WindowFrom = 192;
-// CTAs per SM from which one takes several parts of the heads.
+// CTAs per SM from which one takes several parts of the heads (4 / 6 / 9 / 14: 8 MHA
+// prompts 97 / 85 / 87 / 91 us, 16 GQA prompts 94 / 94 / 98 / 98).
 constexpr int kQ8CtasPerSm = 6;
 
 template <int D, int B, typename T>

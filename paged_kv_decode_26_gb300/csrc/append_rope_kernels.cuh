@@ -251,11 +251,11 @@ __global__ void __launch_bounds__(kRopeThreads)
 // A thread holds its items from the one pass over them to the next (the largest
 // value, then the codes), while the next part's rows and scales are on their way.
 //
-// Measured: 8 prompts of 300-2048 tokens, 32 heads of 128, 87 us (3.8 TB/s), 16 of 32
+// Measured: 8 prompts of 300-2048 tokens, 32 heads of 128, 85 us (3.9 TB/s), 16 of 32
 // query and 8 kv heads 94 (4.4 TB/s), 4 tokens 3.2 us.  Not bound by HBM but by the steps:
 // 300 instructions an item, two barriers a step.  A warp per run and head, its rows in
 // shared memory and no barriers, took 95 us and 6.4 for the 4 tokens; one barrier a step
-// 121; the parts of a window side by side in the grid 132.
+// 121; the parts of a window side by side in the grid 132; 256 threads 101.
 
 constexpr int kLeastExponent = -117;           // of a scale (a block of zeros)
 constexpr int kAppendThreads = 128;
@@ -359,6 +359,12 @@ __device__ __forceinline__ void append_q8_queries(const AppendRopeParams& p, int
             to[at.b] = b[i];
         }
     }
+}
+
+// (out of line: its code would sit in the way of what nearly every block takes)
+__device__ __noinline__ float4 divide(float4 x, float by) {
+    return make_float4(__fdiv_rn(x.x, by), __fdiv_rn(x.y, by), __fdiv_rn(x.z, by),
+                       __fdiv_rn(x.w, by));
 }
 
 // The largest finite |x|.
@@ -600,7 +606,14 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
                 }
             } else {
 #pragma unroll
-                for (int c = 0; c < 16; ++c) x[n][c] = __fdiv_rn(x[n][c], scale);
+                for (int c = 0; c < 16; c += 4) {
+                    const float4 y = divide(
+                        make_float4(x[n][c], x[n][c + 1], x[n][c + 2], x[n][c + 3]), scale);
+                    x[n][c] = y.x;
+                    x[n][c + 1] = y.y;
+                    x[n][c + 2] = y.z;
+                    x[n][c + 3] = y.w;
+                }
             }
             unsigned char* row = page0 + ((size_t)s_block[r.run] * B + r.slot_in_block) *
                                              p.n_kv_heads * D;
