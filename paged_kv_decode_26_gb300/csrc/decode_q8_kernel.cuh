@@ -613,7 +613,8 @@ __global__ void __launch_bounds__(32 * kQ8ShortWarps)
             r.b[h] = -1;
             r.sc.k[h] = r.sc.v[h] = 0.f;
             if (t >= n) continue;
-            const int b = __ldg(p.block_tables + (size_t)s * p.max_blocks_per_seq + t / p.block_size);
+            const int b =
+                __ldg(p.block_tables + (size_t)s * p.max_blocks_per_seq + t / p.block_size);
             if (b < 0 || b >= p.num_blocks) {
                 raise_error(p.errors, PKV_DEVERR_BLOCK_ID);
                 continue;
@@ -669,7 +670,8 @@ __global__ void __launch_bounds__(32 * kQ8ShortWarps)
             if (CHUNK) {
                 // (a lane has 16 bytes of a row; nothing is loaded over the context's last
                 // chunks again)
-                for (int k = max(n - tokens + 1, c * kQ8Tokens); k < min(n, (c + 1) * kQ8Tokens); ++k) {
+                const int to = min(n, (c + 1) * kQ8Tokens);
+                for (int k = max(n - tokens + 1, c * kQ8Tokens); k < to; ++k) {
                     const int h = k / 16 % 2;
                     if ((h ? now.b[1] : now.b[0]) < 0 || lane >= D / 16) continue;
                     uint4* unit = reinterpret_cast<uint4*>(ring + st * SLOT + (2 + h) * HALF +
@@ -684,8 +686,8 @@ __global__ void __launch_bounds__(32 * kQ8ShortWarps)
                 __syncwarp();
             }
             if (valid[0] > 0 || valid[1] > 0)
-                q8_chunk<D, PRECISE, CHUNK>(state, kbase, kbase + 2 * HALF, valid, left, less, now.sc,
-                                            lane);
+                q8_chunk<D, PRECISE, CHUNK>(state, kbase, kbase + 2 * HALF, valid, left, less,
+                                            now.sc, lane);
             __syncwarp();
             now = next;
             if (st) phase ^= 1u;
@@ -723,8 +725,8 @@ __global__ void __launch_bounds__(32 * kQ8ShortWarps)
             for (int k = n - tokens + 1; k < n - hidden(h); ++k) {
                 const int b = p.block_tables[(size_t)s * p.max_blocks_per_seq + k / p.block_size];
                 if (b < 0 || b >= p.num_blocks) continue;
-                const unsigned char* v =
-                    p.v_codes + (((size_t)b * p.block_size + k % p.block_size) * p.n_kv_heads + kvh) * D + d;
+                const size_t row = (size_t)b * p.block_size + k % p.block_size;
+                const unsigned char* v = p.v_codes + (row * p.n_kv_heads + kvh) * D + d;
                 if ((v[0] & 0x7f) == 0x7f) o.x = NAN;
                 if ((v[1] & 0x7f) == 0x7f) o.y = NAN;
             }
