@@ -700,12 +700,13 @@ PKV_API pkv_status kv_append_rope(void* k_pool, void* v_pool, const void* k, int
  *   k_scale, v_scale device float [num_blocks, n_kv_heads]; read only of blocks
  *                that hold earlier tokens, where they may be any positive numbers
  *   slot_mapping as kv_append_rope, and: the tokens of one block follow one another
- *                in the call, to rising rows (appended tokens in order do).  Rows of
- *                the block ahead of the first hold tokens; the rows behind hold none
- *                and are left as they were.  A token behind one of its block that
+ *                in the call, to rising rows (appended tokens in order do); tokens that
+ *                are left out may stand between them, any number, and change nothing.
+ *                Rows of the block ahead of the first hold tokens; the rows behind hold
+ *                none and are left as they were.  A token behind one of its block that
  *                does not go to a later row, and those of the block that follow it,
  *                are not appended (flagged PKV_DEVERR_SLOT; q_out is written).  If
- *                the tokens of one block stand apart in the call, that block's
+ *                tokens of another block stand between those of one block, that block's
  *                contents are undefined.  The block is the call's alone while it
  *                runs (shared ones are copied on write; a block's copy is its rows
  *                of the pools and of the scales).

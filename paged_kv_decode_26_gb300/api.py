@@ -730,7 +730,8 @@ def kv_append_rope_q8(k_pool: torch.Tensor, v_pool: torch.Tensor, k_scale: torch
     """kv_append_rope into float8_e4m3fn pools with a scale (fp32 [num_blocks,
     Hk]) for each block and kv head: the least power of two that holds the
     block's rows; where it grows, the block's earlier rows are rounded anew.  The
-    tokens of one block follow one another in the call, in order."""
+    tokens of one block follow one another in the call, in order (left-out ones may
+    stand between them)."""
     st = calls().kv_append_rope_q8(k_pool, v_pool, k_scale, v_scale, k, v, slot_mapping, positions,
                                    rope, q, q_out, k_out, interleaved, _handle(stream))
     if st:

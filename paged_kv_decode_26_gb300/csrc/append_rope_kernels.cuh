@@ -235,9 +235,9 @@ __global__ void __launch_bounds__(kRopeThreads)
 // ------------------------------------------------------------- 8-bit pages
 //
 // A block's scale covers all its rows of a head, so what is written to a block
-// is one unit: a run, tokens that follow one another in the call and go to
-// rising rows of one block.  The rows ahead of its first one hold tokens and are
-// kept, those behind hold none.  With s(x) the least power of two that brings x
+// is one unit: a run, tokens that follow one another in the call (but for those left
+// out between them, however many) and go to rising rows of one block.  The rows ahead
+// of its first one hold tokens and are kept, those behind hold none.  With s(x) the least power of two that brings x
 // down to 448 (e4m3's largest), a run sets the scale to s(its largest value), or
 // to the old scale if rows are kept and that is larger; kept rows are rounded
 // anew where the scale grew.  A power of two costs e4m3 no precision (its
@@ -247,7 +247,11 @@ __global__ void __launch_bounds__(kRopeThreads)
 // CTA x: a window of `window` tokens, whose runs (those that start in it) it takes;
 // y: parts of the key and value heads, or of the query heads.  A window is one token,
 // or block_size of them: then the rows of its runs are block_size at most but for the
-// last run, which goes by itself if it does not fit beside the others.
+// last run, which goes by itself if it does not fit beside the others.  Runs are found by
+// what stands within the threads' view of the window; where left-out tokens lie
+// between two of one block there, or up to the view's end, the living ones are sought
+// beyond (regather: 250 tokens padded to 256 4.8 -> 5.7 us, 100 of 256 4.7 -> 6.2, a
+// prompt of 1100 in 2048 11.3 -> 11.7; 32 query and 8 kv heads of 128).
 // A thread holds its items from the one pass over them to the next (the largest
 // value, then the codes), while the next part's rows and scales are on their way.
 //
@@ -380,6 +384,128 @@ __device__ __forceinline__ float largest(const float (&x)[16]) {
     return top;
 }
 
+// The first set bit from `from` on, kAppendThreads if there is none.
+__device__ __forceinline__ int next_living(const unsigned* lives, int from) {
+#pragma unroll
+    for (int w = 0; w < kAppendThreads / 32; ++w) {
+        const int skip = from - 32 * w;
+        const unsigned rest = skip >= 32 ? 0u : lives[w] & (0xffffffffu << max(skip, 0));
+        if (rest) return 32 * w + __ffs(rest) - 1;
+    }
+    return kAppendThreads;
+}
+
+// Block of token t, -1: left out, or no token.
+template <int B>
+__device__ __forceinline__ int living_block(const AppendRopeParams& p, long long t) {
+    if (t < 0 || t >= p.num_tokens) return -1;
+    const int64_t slot = p.slots[t];
+    return token_lives(p, slot, p.table ? p.positions[t] : 0, false) ? (int)(slot / B) : -1;
+}
+
+// By the whole CTA: whether a token may live (its slot is in the pool) among the
+// kLook * kAppendThreads from `at` on, in the direction `way`.
+constexpr int kLook = 16;
+template <int B>
+__device__ __forceinline__ bool group_lives(const AppendRopeParams& p, long long at, int way) {
+    const int64_t slots = (int64_t)p.num_blocks * B;
+    int64_t slot[kLook];
+#pragma unroll
+    for (int i = 0; i < kLook; ++i) {
+        const long long t = at + way * (i * kAppendThreads + (int)threadIdx.x);
+        slot[i] = t >= 0 && t < p.num_tokens ? p.slots[t] : -1;
+    }
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < kLook; ++i) any |= slot[i] >= 0 && slot[i] < slots;
+    return __syncthreads_or(any);
+}
+
+// The same of all tokens from `at` on.
+template <int B>
+__device__ __forceinline__ bool rest_lives(const AppendRopeParams& p, long long at, int way) {
+    for (; at >= 0 && at < p.num_tokens; at += way * kLook * kAppendThreads)
+        if (group_lives<B>(p, at, way)) return true;
+    return false;
+}
+
+// By the whole CTA: of the tokens that are not left out, tokens[B ..] get the window's
+// (their number is returned), tokens[.. B - 1] those ahead of it, the last at B - 1, and
+// tokens[B + that number ..] those behind; -1 where there is none.  Ahead and behind they
+// are sought, over whatever stands between, until B (B - 1) are found or one of another
+// block than the window's first (last): no run goes on beyond.
+template <int B>
+__device__ __forceinline__ int gather_living(const AppendRopeParams& p, int w0, int w1, int* tokens) {
+    __shared__ int s_found;
+    __shared__ int s_done;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const unsigned below = (1u << lane) - 1u;
+    if (tid < 3 * B) tokens[tid] = -1;
+    const int own = lane < w1 - w0 ? living_block<B>(p, w0 + lane) : -1;   // (32 tokens at most)
+    const unsigned living = __ballot_sync(0xffffffffu, own >= 0);
+    const int count = __popc(living);
+    __syncthreads();
+    if (tid < 32 && own >= 0) tokens[B + __popc(living & below)] = w0 + lane;
+#pragma unroll 1
+    for (int way = -1; way <= 1; way += 2) {
+        const int most = way < 0 ? B : B - 1;
+        const int edge = __shfl_sync(0xffffffffu, own, way < 0 ? __ffs(living) - 1 : 31 - __clz(living));
+        if (tid == 0) s_found = s_done = 0;
+        __syncthreads();
+        for (long long at = way < 0 ? w0 - 1LL : w1; at >= 0 && at < p.num_tokens;
+             at += way * kLook * kAppendThreads) {
+            if (!group_lives<B>(p, at, way)) continue;
+            if (tid < 32) {                    // 32 at a time, in order
+                int found = s_found;
+                bool done = false;
+                for (int i = 0; !done && i < kLook * kAppendThreads; i += 32) {
+                    const long long t = at + way * (i + lane);
+                    const int b = living_block<B>(p, t);
+                    const unsigned here = __ballot_sync(0xffffffffu, b >= 0);
+                    const int rank = found + __popc(here & below);
+                    if (b >= 0 && rank < most)
+                        tokens[way < 0 ? B - 1 - rank : B + count + rank] = (int)t;
+                    found += __popc(here);
+                    done = found >= most || __any_sync(0xffffffffu, b >= 0 && b != edge);
+                }
+                if (lane == 0) {
+                    s_found = found;
+                    s_done = done;
+                }
+            }
+            __syncthreads();
+            if (s_done) break;
+        }
+        __syncthreads();
+    }
+    return count;
+}
+
+// By the whole CTA, where tokens around the window are left out: 0 where none is left in
+// it, the tokens gathered (their number) where it matters what stands between them, else
+// -1: they matter between two of one block, and where nothing in view tells whether
+// they stand there.  Out of line: batches without padding never come here.
+template <int B>
+__device__ __noinline__ int regather(const AppendRopeParams& p, int w0, int w1, int block,
+                                     int in_block, bool out, const int* s_blk,
+                                     const unsigned* s_lives, int* s_tok) {
+    const int tid = threadIdx.x;
+    const int next = next_living(s_lives, tid + 1), first = next_living(s_lives, B);
+    if (first >= B + (w1 - w0)) return 0;
+    bool between = false, behind = false, ahead = false;
+    if (block >= 0 && next < kAppendThreads)
+        between = next > tid + 1 && s_blk[next] == block;
+    else if (block >= 0)
+        behind = tid >= B && tid + 1 < kAppendThreads && in_block < B - 1;
+    else if (out && tid == 0)
+        ahead = s_blk[next] == s_blk[first];
+    bool gather = __syncthreads_or(between);
+    if (!gather && __syncthreads_or(behind))
+        gather = rest_lives<B>(p, w0 - B + kAppendThreads, 1);
+    if (!gather && __syncthreads_or(ahead)) gather = rest_lives<B>(p, w0 - B - 1LL, -1);
+    return gather ? gather_living<B>(p, w0, w1, s_tok) : -1;
+}
+
 template <int D, int B, typename T>
 __global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
     append_rope_q8_kernel(const __grid_constant__ AppendRopeParams p, int window, int kv_ctas,
@@ -387,11 +513,12 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
     constexpr int J = D / 16;
     constexpr int V = D / 8;
     constexpr int HC = q8_cta_heads(D, B);
-    constexpr int kSpan = 3 * kQ8MaxBlock;
     constexpr int kPairs = kAppendThreads * kAppendItems / J;   // rows x heads of a CTA
-    static_assert(kSpan <= kAppendThreads, "a thread per token around the window");
-    __shared__ int s_blk[kSpan];              // block and row of a token's slot, -1: none
-    __shared__ int s_in[kSpan];
+    static_assert(3 * B <= kAppendThreads, "a thread per token around the window");
+    __shared__ int s_blk[kAppendThreads];     // block and row of a token's slot, -1: none
+    __shared__ int s_in[kAppendThreads];
+    __shared__ unsigned s_lives[kAppendThreads / 32];   // those of a block, as bits
+    __shared__ int s_tok[3 * B];              // as gather_living lists them
     __shared__ int s_count[2][kAppendThreads / 32];
     __shared__ Q8Row s_row[2 * kQ8MaxBlock];
     __shared__ int s_first_row[kQ8MaxBlock + 1];  // of a run: its first row in the block
@@ -413,25 +540,43 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
     }
 
     // ---- the tokens around the window: thread i looks at token w0 - B + i
-    const int span = min(w1 + B - 1, p.num_tokens) - (w0 - B);
-    const int t = w0 - B + tid;
-    const bool here = t >= w0 && t < w1;
+    int t = w0 - B + tid, count = w1 - w0;     // tokens of the window
+    bool here = t >= w0 && t < w1;
     int block = -1, in_block = 0, position = 0;
-    if (tid < span && t >= 0) {
+    bool out = false;                          // a token that is left out
+    if (t >= 0 && t < p.num_tokens) {
         const int64_t slot = p.slots[t];
         position = p.table ? p.positions[t] : 0;
-        if (here && blockIdx.y == 0) token_lives(p, slot, position, true);  // (says what is wrong)
-        if (slot >= 0 && slot < (int64_t)p.num_blocks * B) {
+        out = !token_lives(p, slot, position, here && blockIdx.y == 0);  // (says what is wrong)
+        if (!out) {
             block = (int)(slot / B);
             in_block = (int)(slot % B);
         }
     }
-    if (tid < kSpan) {
-        s_blk[tid] = block;
-        s_in[tid] = in_block;
-    }
+    s_blk[tid] = block;
+    s_in[tid] = in_block;
+    const unsigned lives_here = __ballot_sync(0xffffffffu, block >= 0);
+    if (lane == 0) s_lives[tid / 32] = lives_here;
     if (tid < kPairs) s_top[0][tid] = 0u;
-    __syncthreads();
+    if (__syncthreads_or(out)) {
+        const int living = regather<B>(p, w0, w1, block, in_block, out, s_blk, s_lives, s_tok);
+        if (living == 0) return;
+        if (living > 0) {
+            count = living;
+            t = tid < 3 * B ? s_tok[tid] : -1;
+            here = t >= w0 && t < w1;
+            block = -1;
+            if (t >= 0) {
+                const int64_t slot = p.slots[t];
+                position = p.table ? p.positions[t] : 0;
+                block = (int)(slot / B);
+                in_block = (int)(slot % B);
+            }
+            s_blk[tid] = block;
+            s_in[tid] = in_block;
+            __syncthreads();
+        }
+    }
     // distance to the run's first token, -1: in no run
     int back = -1;
     if (block >= 0) {
@@ -451,7 +596,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
     }
     // ---- rows and runs of the window, in order
     const int first = tid - back;                // index of the run's first token
-    const bool mine = back >= 0 && first >= B && first < B + (w1 - w0);
+    const bool mine = back >= 0 && first >= B && first < B + count;
     const unsigned rows_here = __ballot_sync(0xffffffffu, mine);
     const unsigned runs_here = __ballot_sync(0xffffffffu, mine && back == 0);
     if (lane == 0) {
@@ -542,13 +687,11 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
         for (int n = 0; n < kAppendItems; ++n) {
             const int r = now.row_lo + r0 + n * kRowStep;
             if (!real || r >= now.row_hi) continue;
-            const int position = s_row[r].position;
-            if (p.table && (position < 0 || position >= p.table_rows)) continue;
             lives |= 1u << n;
             item_values<T>(a[n], b[n], x[n]);
             if (key && at.turn) {
                 ItemTurn turn;
-                load_turn(p, position, j, turn);
+                load_turn(p, s_row[r].position, j, turn);
                 turn_item(x[n], turn, p.interleaved);
             }
             if (key && p.k_out) {
