@@ -698,7 +698,8 @@ PKV_API pkv_status kv_append_rope(void* k_pool, void* v_pool, const void* k, int
  *   k_pool, v_pool device e4m3 bytes [num_blocks, block_size, n_kv_heads,
  *                head_dim], 16-byte aligned; block_size 16 or 32
  *   k_scale, v_scale device float [num_blocks, n_kv_heads]; read only of blocks
- *                that hold earlier tokens, where they may be any positive numbers
+ *                that hold earlier tokens, where they may be any numbers from 2^-126
+ *                to 2^125
  *   slot_mapping as kv_append_rope, and: the tokens of one block follow one another
  *                in the call, to rising rows (appended tokens in order do); tokens that
  *                are left out may stand between them, any number, and change nothing.
@@ -733,8 +734,9 @@ PKV_API pkv_status kv_append_rope_q8(void* k_pool, void* v_pool, float* k_scale,
  *   q             device, [num_seqs, n_heads, head_dim] of q_dtype (F16 or BF16)
  *   k_pool, v_pool device e4m3 bytes [num_blocks, block_size, n_kv_heads,
  *                 head_dim], 16-byte aligned
- *   k_scale, v_scale device float [num_blocks, n_kv_heads]: any positive numbers
- *                 (powers of two from the append, or others, e.g. calibrated ones)
+ *   k_scale, v_scale device float [num_blocks, n_kv_heads]: any numbers from 2^-126
+ *                 to 2^125 (powers of two from the append, or others, e.g.
+ *                 calibrated ones), also far apart from block to block
  *   workspace     device, >= pkv_decode_q8_workspace_bytes(...) bytes, 256-byte
  *                 aligned; contents on entry are ignored; may be NULL when that size
  *                 is 0 (few short contexts).  Calls that may overlap on the GPU need

@@ -45,7 +45,11 @@ constexpr int kQ8Stages = 2;
 constexpr int kQ8StreamHeads = 4;              // kv heads (warps) per stream at most
 constexpr int kQ8Threads = 32 * kQ8Warps;
 static_assert(kQ8Warps * kQ8Stages == kPieceWarps * kPieceStages, "piece_shared's barriers");
-constexpr float kQ8LeastScale = 0x1p-100f;     // of a reference (blocks of zeros)
+constexpr float kQ8LeastScale = 0x1p-126f;     // fp32's least normal number
+
+// Scores above a reference's m by more than this move it, whatever their values' scale:
+// L stays below 2^kQ8Above a token.
+constexpr float kQ8Above = 96.f;
 
 struct Q8Params : PieceParams {
     const float* k_scale;      // [num_blocks, n_kv_heads]
@@ -214,13 +218,13 @@ __device__ __forceinline__ void q8_chunk(Q8Heads<D>& st, uint32_t kbase, uint32_
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             top[h][e] = fmaxf(x[h][e], x[h][2 + e]);
-            beyond |= (top[h][e] - st.m[e]) + (lv[h] - st.lv[e]) > Range::GROW;
+            beyond |= (top[h][e] - st.m[e]) + (lv[h] - st.lv[e]) > Range::GROW ||
+                      top[h][e] - st.m[e] > kQ8Above;
         }
     if (__any_sync(0xffffffffu, beyond)) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            float m = st.m[e], l = st.lv[e], b = 1.f;
-            bool moved = false;
+            float m = st.m[e], l = st.lv[e], b = 0.f, high = m;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float t = top[h][e];
@@ -231,15 +235,20 @@ __device__ __forceinline__ void q8_chunk(Q8Heads<D>& st, uint32_t kbase, uint32_
                     m = t;
                     l = lv[h];
                     b = bv[h];
-                    moved = true;
                 }
+                high = fmaxf(high, t);
             }
-            if (moved) {
-                const float al = st.m[e] == -INFINITY ? 1.f : exp2f(st.m[e] - m);
-                const float ao = st.m[e] == -INFINITY ? 1.f : exp2f((st.m[e] - m) + (st.lv[e] - l));
-                st.m[e] = m;
+            if (b != 0.f || high - m > kQ8Above) {
+                // lower for a scale below 2^-60, but never below what it was, nor far
+                // below a score
+                const float to = fmaxf(fmaxf(m + fminf(l + 60.f, 0.f), high - (kQ8Above - 6.f)),
+                                       st.m[e]);
+                l += m - to;
+                const float al = st.m[e] == -INFINITY ? 1.f : exp2f(st.m[e] - to);
+                const float ao = st.m[e] == -INFINITY ? 1.f : exp2f((st.m[e] - to) + (st.lv[e] - l));
+                st.rv[e] = to == m && b != 0.f ? __frcp_rn(b) : exp2f(-l);
+                st.m[e] = to;
                 st.lv[e] = l;
-                st.rv[e] = __frcp_rn(b);
                 st.l[e] *= al;
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) {
@@ -255,8 +264,10 @@ __device__ __forceinline__ void q8_chunk(Q8Heads<D>& st, uint32_t kbase, uint32_
     const float mu1 = st.m[1] == -INFINITY ? 0.f : st.m[1];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const float f0 = sc.v[h] * st.rv[0] * (1.f / Range::UNLIFT);
-        const float f1 = sc.v[h] * st.rv[1] * (1.f / Range::UNLIFT);
+        // (bounded where p is next to nothing; NaN stays)
+        float f0 = sc.v[h] * st.rv[0], f1 = sc.v[h] * st.rv[1];
+        f0 = (f0 > 0x1p116f ? 0x1p116f : f0) * (1.f / Range::UNLIFT);
+        f1 = (f1 > 0x1p116f ? 0x1p116f : f1) * (1.f / Range::UNLIFT);
         const float p0 = exp2f(x[h][0] - mu0), p1 = exp2f(x[h][1] - mu1);
         const float p2 = exp2f(x[h][2] - mu0), p3 = exp2f(x[h][3] - mu1);
         st.l[0] += p0 + p2;

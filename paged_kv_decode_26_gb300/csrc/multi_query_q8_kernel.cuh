@@ -34,9 +34,13 @@
 //
 // Precision: S, M, L and O are fp32.  A weight is rounded once to fp16 before the
 // second product (fp32 outputs: two parts), lifted and bounded as in
-// weight_range.cuh; M = (m, log2 b_ref) with m the score and b_ref the scale of
-// the key with the largest weight when it was set.  O accumulates in the tensor
-// core, which drops what lies below its last bit: up to 2^-23 of O per 16 keys.
+// weight_range.cuh; M = m + lb with m the score and lb = log2 b_ref of the key with the
+// largest weight when it was set, or their sum and 0 (m has to be a score itself only
+// where scores are large), and L is kept relative to 2^m.  Value scales outside 2^-60
+// .. 2^16 (blocks of zeros have the least), or a reference of such, take a way of
+// their own, where L has its own exponentials: weights there may be far below or
+// above what they add to L.  O accumulates in the tensor core, which drops what lies
+// below its last bit: up to 2^-23 of O per 16 keys.
 #pragma once
 
 #include "attn_tc_kernel.cuh"
@@ -75,10 +79,16 @@ struct Mq8Params : MultiQueryParams {
                                // row tiles, parts with keys
 };
 
+// log2 of value scales for which w_t / b_t adds up to L as it is.
+constexpr float kMq8LeastLog = -60.f, kMq8MostLog = 16.f;
+__device__ __forceinline__ bool mq8_usual(float lb) { return lb >= kMq8LeastLog && lb <= kMq8MostLog; }
+// Scores above m by more than this move it, whatever their values' scale.
+constexpr float kMq8Above = 64.f;
+
 // Of a key tile's groups of 16 keys: a, log2 b and 1 / b, and whether there is a page.
 struct __align__(16) Mq8Scale {
     float a[8], lb[8], ib[8];
-    unsigned char page[16];            // 8 of them: 1 or 0
+    unsigned char page[16];            // 8 of them: 0: none, 1, or 2: b not mq8_usual
 };
 
 template <int D>
@@ -421,12 +431,13 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
                     Mq8Scale& e = s_scale[j % kMq8Scales];
                     if (lane == 0) {
                         e.a[g] = now.scale;
-                        e.page[g] = now.page;
                     } else if (lane == 1) {
                         // (NaN stays)
                         const float b = now.scale < kQ8LeastScale ? kQ8LeastScale : now.scale;
-                        e.lb[g] = __log2f(b);
+                        const float lb = __log2f(b);
+                        e.lb[g] = lb;
                         e.ib[g] = __frcp_rn(b);
+                        e.page[g] = now.page ? (mq8_usual(lb) ? 1 : 2) : 0;
                     }
                 } else if (j >= guard_from) {
                     bool any = false;
@@ -507,7 +518,8 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
                 if (lane == 0) mbar_arrive(&q_full[t]);
             }
             const uint32_t t_lane = tmem + t * Z::TILE_COLS + ((uint32_t)((warp & 3) * 32) << 16);
-            float m = -INFINITY, lb = 0.f;        // the reference: a score and log2 of a scale
+            float m = -INFINITY, lb = 0.f;        // the reference (usual ones: lb 0 unless formed)
+            bool odd = false;                     // a row of this warp has one that is not
             // scores formed ahead of the maximum: where their factor is not positive,
             // or a row's are so large that y a + add would lose what matters
             bool formed = !(p.scale_log2 > 0.f);
@@ -522,10 +534,14 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
             auto move = [&](int j, bool moved, float to, float to_lb) {
                 float alpha = 1.f;
                 if (moved) {
-                    if (m != -INFINITY) alpha = exp2f((m - to) + (lb - to_lb));
+                    if (m != -INFINITY) {
+                        alpha = exp2f((m - to) + (lb - to_lb));
+                        l *= exp2f(m - to);
+                    }
                     m = to;
                     lb = to_lb;
                 }
+                odd = __any_sync(0xffffffffu, !mq8_usual(lb));
                 if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                     // O is at rest: the products up to key tile j - 1 completed before
                     // S_j did
@@ -544,7 +560,6 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
                         }
                         tc_st32(t_lane + c0, ov);
                     }
-                    l *= alpha;
                 }
             };
             // 2^(y mul1 + add1) of 16 keys as 16-bit pairs from w[..][at] on; their sum.
@@ -589,8 +604,8 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
                 const uint2 pages = *reinterpret_cast<const uint2*>(sc.page);
                 const bool whole = key0 + kMq8Keys - 1 <= warp_pos &&
                                    (pages.x & pages.y) == 0x01010101u;
-                if (whole && !formed) {
-                    // ---- the usual tile: this warp's rows see all of it
+                if (whole && !formed && !odd) {
+                    // ---- the usual tile: this warp's rows see all of it (and lb is 0)
                     float y[kMq8Keys];
                     uint32_t* yr = reinterpret_cast<uint32_t*>(y);
                     tc_ld32(t_lane + Z::S_COL, yr);
@@ -602,7 +617,7 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
 #pragma unroll
                     for (int g = 0; g < 8; ++g)
                         z = fmaxf(z, fmaf(group_max(y + 16 * g), sc.a[g] * qf, sc.lb[g]));
-                    const bool beyond = z - (m + lb) > Range::GROW;
+                    const bool beyond = z - m > Range::GROW;
                     if (__any_sync(0xffffffffu, beyond)) {
                         if (__any_sync(0xffffffffu, real && beyond && fabsf(z) > 32768.f)) {
                             formed = true;
@@ -610,7 +625,7 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
                         }
                         move(j, beyond, z, 0.f);
                     }
-                    const float base = Range::LIFT - (m == -INFINITY ? 0.f : m + lb);
+                    const float base = Range::LIFT - (m == -INFINITY ? 0.f : m);
 #pragma unroll
                     for (int part = 0; part < 4; ++part) {
                         uint32_t w[PARTS][16];
@@ -666,16 +681,65 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
                             }
                         }
                     }
-                    if (__any_sync(0xffffffffu, beyond)) {
+                    // scales far apart: L by itself, and m never far below a score
+                    const bool apart = odd || ((pages.x | pages.y) & 0x02020202u) != 0u;
+                    float high = -INFINITY;
+                    if (apart) {
+#pragma unroll 1
+                        for (int part = 0; part < 4; ++part) {
+                            float y[32];
+                            scores(y, part);
+#pragma unroll
+                            for (int g = 0; g < 2; ++g) {
+                                const float f = unit(part * 2 + g);
+                                high = fmaxf(high, __fmul_rn(group_max(y + 16 * g),
+                                                             formed || f == 0.f ? 1.f : f));
+                            }
+                        }
+                    }
+                    const bool moves = beyond || high - m > kMq8Above;
+                    if (__any_sync(0xffffffffu, moves)) {
                         if (!formed &&
-                            __any_sync(0xffffffffu, real && beyond && fabsf(top) > 32768.f)) {
+                            __any_sync(0xffffffffu, real && moves &&
+                                                        (fabsf(top) > 32768.f || high > 32768.f))) {
                             formed = true;
                             continue;              // this tile once more (S is still there)
                         }
-                        move(j, beyond, top, top_lb);
+                        float to = beyond ? top : m, to_lb = beyond ? top_lb : lb;
+                        auto join = [&] {
+                            if (formed || !mq8_usual(to_lb)) return;
+                            to += to_lb;
+                            to_lb = 0.f;
+                        };
+                        join();
+                        if (apart) {
+                            if (l > 0.f) high = fmaxf(high, m + (__log2f(l) - Range::LIFT));
+                            if (high - to > kMq8Above) {
+                                to_lb += to - high;
+                                to = high;
+                                join();
+                            }
+                        }
+                        move(j, moves, to, to_lb);
                     }
                     const float mu = m == -INFINITY ? 0.f : m;
+                    if (apart) {
+#pragma unroll 1
+                        for (int part = 0; part < 4; ++part) {
+                            float y[32];
+                            scores(y, part);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) {
+                                const float f = formed ? 1.f : unit(part * 2 + c / 16);
+                                // (hidden ones: -inf, where f may be 0)
+                                const float x = y[c] == -INFINITY ? y[c] : formed ? y[c] - mu
+                                                                                  : fmaf(y[c], f, -mu);
+                                l += exp2f(x + Range::LIFT);
+                            }
+                        }
+                    }
                     const float base = formed ? Range::LIFT - lb : Range::LIFT - (mu + lb);
+                    const float ref = exp2f(lb);
                     // (the first parts lie where scores were already read, the second
                     // ones wait for the end)
                     uint32_t rest[4][16];
@@ -694,7 +758,7 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
                             const float sum = weights(y + 16 * g, formed || f == 0.f ? 1.f : f,
                                                       f == 0.f ? 0.f : base + sc.lb[part * 2 + g],
                                                       w, g * 8);
-                            if (f != 0.f) l = fmaf(sum, sc.ib[part * 2 + g], l);
+                            if (f != 0.f && !apart) l = fmaf(sum, sc.ib[part * 2 + g] * ref, l);
                         }
                         tc_st16(t_lane + Z::S_COL + part * 16, w[0]);
                         if (PARTS > 1)
@@ -713,10 +777,11 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
             ok = ok && __all_sync(0xffffffffu, mbar_wait(&o_full[t], 0, p.errors));
             if (ok) {
                 tc_fence_after();
-                const float inv = l != 0.f ? __frcp_rn(l) : 0.f;
+                // O 2^lb / l, in two factors: either alone may leave fp32's range
+                const float root = exp2f(0.5f * lb), inv = l != 0.f ? __frcp_rn(l) * root : 0.f;
                 if (cut && real)
                     *reinterpret_cast<float2*>(p.part_ml + 2 * unit_of(t, r)) =
-                        make_float2(m, l * exp2f(lb - Range::LIFT));
+                        make_float2(m, l * Range::UNLIFT);
                 const bool poison = *reinterpret_cast<volatile int*>(s_poison) != 0;
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
@@ -725,7 +790,7 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
                     tc_wait_ld();
                     if (!real) continue;
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) o[c] *= inv;
+                    for (int c = 0; c < 32; ++c) o[c] = o[c] * inv * root;
                     if (poison) {
                         // NaN that was taken out of V, from the rows that see it
 #pragma unroll 1
