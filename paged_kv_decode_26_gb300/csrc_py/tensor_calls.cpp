@@ -76,6 +76,18 @@ struct Here {
     }
 };
 
+// The pointers of a call are all taken ahead of Py_BEGIN_ALLOW_THREADS: data_ptr() throws
+// for a tensor without storage (one of vmap's, say), and an exception needs the
+// interpreter.
+template <class T>
+T* pointer(const at::Tensor& t) {
+    return static_cast<T*>(t.data_ptr());
+}
+template <class T>
+T* pointer(const at::Tensor* t) {
+    return t ? pointer<T>(*t) : nullptr;
+}
+
 bool same_shape(const at::Tensor& a, const at::Tensor& b) { return a.sizes() == b.sizes(); }
 
 bool is(const at::Tensor& t, at::ScalarType type) { return t.scalar_type() == type; }
@@ -118,6 +130,9 @@ PyObject* guarded(F f) {
         return nullptr;
     } catch (const std::exception& e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    } catch (...) {
+        PyErr_SetString(PyExc_RuntimeError, "unknown error");
         return nullptr;
     }
 }
@@ -180,27 +195,27 @@ long long append(PyObject* const* a, Py_ssize_t n, bool q8) {
     const int inter = PyObject_IsTrue(b[8]);
     if (inter < 0) throw Refused();
     void* stream = here.stream(b[9]);
-    const int64_t* slot = static_cast<const int64_t*>(slots.data_ptr());
-    const int32_t* pos = rope ? static_cast<const int32_t*>(positions->data_ptr()) : nullptr;
-    const float* table = rope ? static_cast<const float*>(rope->data_ptr()) : nullptr;
     const int rows = rope ? as_int(rope->size(0)) : 0, rot = rope ? as_int(rope->size(1)) : 0;
-    const void* q_at = q ? q->data_ptr() : nullptr;
-    void *q_to = q ? q_out->data_ptr() : nullptr, *k_to = k_out ? k_out->data_ptr() : nullptr;
     const int t = as_int(T), h = as_int(H), hk = as_int(Hk), d = as_int(D), bs = as_int(B),
               blocks = as_int(nb);
+    void *kp = pointer<void>(k_pool), *vp = pointer<void>(v_pool);
+    const void *k_at = pointer<void>(k), *v_at = pointer<void>(v), *q_at = pointer<void>(q);
+    void *q_to = q ? pointer<void>(q_out) : nullptr, *k_to = pointer<void>(k_out);
+    const int64_t* slot = pointer<int64_t>(slots);
+    const int32_t* pos = rope ? pointer<int32_t>(positions) : nullptr;
+    const float* table = pointer<float>(rope);
+    float* ks = q8 ? pointer<float>(tensor(a[2])) : nullptr;
+    float* vs = q8 ? pointer<float>(tensor(a[3])) : nullptr;
     pkv_status st;
     Py_BEGIN_ALLOW_THREADS
     if (q8)
-        st = kv_append_rope_q8(k_pool.data_ptr(), v_pool.data_ptr(),
-                               static_cast<float*>(THPVariable_Unpack(a[2]).data_ptr()),
-                               static_cast<float*>(THPVariable_Unpack(a[3]).data_ptr()), k.data_ptr(),
-                               k_row, v.data_ptr(), v_row, dt, slot, pos, table, rows, rot, inter,
-                               q_at, q_row, q_to, q_out_row, k_to, k_out_row, t, h, hk, d, bs, blocks,
-                               stream);
+        st = kv_append_rope_q8(kp, vp, ks, vs, k_at, k_row, v_at, v_row, dt, slot, pos, table, rows,
+                               rot, inter, q_at, q_row, q_to, q_out_row, k_to, k_out_row, t, h, hk, d,
+                               bs, blocks, stream);
     else
-        st = kv_append_rope(k_pool.data_ptr(), v_pool.data_ptr(), k.data_ptr(), k_row, v.data_ptr(),
-                            v_row, dt, slot, pos, table, rows, rot, inter, q_at, q_row, q_to,
-                            q_out_row, k_to, k_out_row, t, h, hk, d, bs, blocks, stream);
+        st = kv_append_rope(kp, vp, k_at, k_row, v_at, v_row, dt, slot, pos, table, rows, rot, inter,
+                            q_at, q_row, q_to, q_out_row, k_to, k_out_row, t, h, hk, d, bs, blocks,
+                            stream);
     Py_END_ALLOW_THREADS
     return st;
 }
@@ -210,6 +225,13 @@ struct Q8 {
     const at::Tensor &out, &q, &k_pool, &v_pool, &k_scale, &v_scale, &tables, &lens;
     const at::Tensor* workspace;
     int H, nb, B, Hk, D, S;
+    void* out_at = nullptr;
+    const void *q_at = nullptr, *kp = nullptr, *vp = nullptr;
+    const float *ks = nullptr, *vs = nullptr;
+    const int32_t *table = nullptr, *len = nullptr;
+    int width = 0;
+    void* ws = nullptr;
+    size_t ws_bytes = 0;
 
     Q8(Here& here, PyObject* out_, PyObject* q_, PyObject* const* pools, PyObject* workspace_)
         : out(tensor(out_)), q(tensor(q_)), k_pool(tensor(pools[0])), v_pool(tensor(pools[1])),
@@ -233,10 +255,17 @@ struct Q8 {
         S = as_int(lens.size(0));
         check_scales(here, k_scale, v_scale, nb, Hk);
         if (workspace) here.check_contiguous(*workspace);
-    }
-    const float* scale(const at::Tensor& t) const { return static_cast<const float*>(t.data_ptr()); }
-    const int32_t* ints(const at::Tensor& t) const {
-        return static_cast<const int32_t*>(t.data_ptr());
+        out_at = pointer<void>(out);
+        q_at = pointer<void>(q);
+        kp = pointer<void>(k_pool);
+        vp = pointer<void>(v_pool);
+        ks = pointer<float>(k_scale);
+        vs = pointer<float>(v_scale);
+        table = pointer<int32_t>(tables);
+        len = pointer<int32_t>(lens);
+        width = as_int(tables.size(1));
+        ws = pointer<void>(workspace);
+        ws_bytes = workspace ? workspace->nbytes() : 0;
     }
 };
 
@@ -251,8 +280,6 @@ long long decode(PyObject* const* a, Py_ssize_t n) {
     const int max_len = as_int(integer(a[9]));
     const pkv_dtype out_dt = dtype_out(c.out), q_dt = dtype16(c.q);
     void* stream = here.stream(a[11]);
-    void* ws = c.workspace ? c.workspace->data_ptr() : nullptr;
-    const size_t ws_bytes = c.workspace ? c.workspace->nbytes() : 0;
     if (!c.workspace) {
         const size_t need =
             pkv_decode_q8_workspace_bytes(c.S, c.H, c.Hk, c.D, c.B, max_len);
@@ -260,10 +287,9 @@ long long decode(PyObject* const* a, Py_ssize_t n) {
     }
     pkv_status st;
     Py_BEGIN_ALLOW_THREADS
-    st = paged_attn_decode_q8(c.out.data_ptr(), out_dt, c.q.data_ptr(), q_dt, c.k_pool.data_ptr(),
-                              c.v_pool.data_ptr(), c.scale(c.k_scale), c.scale(c.v_scale),
-                              c.ints(c.tables), (int)c.tables.size(1), c.ints(c.lens), c.S, c.H, c.Hk,
-                              c.D, c.B, c.nb, scale, max_len, ws, ws_bytes, stream);
+    st = paged_attn_decode_q8(c.out_at, out_dt, c.q_at, q_dt, c.kp, c.vp, c.ks, c.vs, c.table,
+                              c.width, c.len, c.S, c.H, c.Hk, c.D, c.B, c.nb, scale, max_len, c.ws,
+                              c.ws_bytes, stream);
     Py_END_ALLOW_THREADS
     return st;
 }
@@ -282,9 +308,8 @@ long long chunk(PyObject* const* a, Py_ssize_t n) {
     const int max_q = as_int(integer(a[10])), max_len = as_int(integer(a[11])),
               total = as_int(c.q.size(0));
     const pkv_dtype out_dt = dtype_out(c.out), q_dt = dtype16(c.q);
+    const int32_t* start = pointer<int32_t>(q_start);
     void* stream = here.stream(a[13]);
-    void* ws = c.workspace ? c.workspace->data_ptr() : nullptr;
-    const size_t ws_bytes = c.workspace ? c.workspace->nbytes() : 0;
     if (!c.workspace) {
         const size_t need =
             pkv_multi_query_q8_workspace_bytes(c.S, max_q, c.H, c.Hk, c.D, c.B, max_len);
@@ -292,11 +317,9 @@ long long chunk(PyObject* const* a, Py_ssize_t n) {
     }
     pkv_status st;
     Py_BEGIN_ALLOW_THREADS
-    st = paged_attn_multi_query_q8(c.out.data_ptr(), out_dt, c.q.data_ptr(), q_dt, c.ints(q_start),
-                                   total, max_q, c.k_pool.data_ptr(), c.v_pool.data_ptr(),
-                                   c.scale(c.k_scale), c.scale(c.v_scale), c.ints(c.tables),
-                                   (int)c.tables.size(1), c.ints(c.lens), c.S, c.H, c.Hk, c.D, c.B,
-                                   c.nb, scale, max_len, ws, ws_bytes, stream);
+    st = paged_attn_multi_query_q8(c.out_at, out_dt, c.q_at, q_dt, start, total, max_q, c.kp, c.vp,
+                                   c.ks, c.vs, c.table, c.width, c.len, c.S, c.H, c.Hk, c.D, c.B,
+                                   c.nb, scale, max_len, c.ws, c.ws_bytes, stream);
     Py_END_ALLOW_THREADS
     return st;
 }
