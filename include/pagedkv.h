@@ -710,7 +710,7 @@ PKV_API pkv_status kv_append_rope(void* k_pool, void* v_pool, const void* k, int
  *                tokens of another block stand between those of one block, that block's
  *                contents are undefined.  The block is the call's alone while it
  *                runs (shared ones are copied on write; a block's copy is its rows
- *                of the pools and of the scales).
+ *                of the pools, swap_blocks_kv, and of the scales, swap_block_scales).
  *   other arguments as kv_append_rope: k, v, q, q_out and k_out are 16-bit.
  * One launch.
  */
@@ -833,6 +833,22 @@ PKV_API pkv_status swap_blocks_kv(void* dst_k, void* dst_v, const void* src_k,
                                   const void* src_v, size_t block_bytes, const int64_t* pairs,
                                   int n_pairs, int64_t num_src_blocks, int64_t num_dst_blocks,
                                   void* stream);
+
+/*
+ * swap_block_scales -- swap_blocks on the scales of an 8-bit cache, whose blocks
+ * (n_kv_heads floats each) need not be multiples of 16 bytes: for each pair (i, j)
+ *
+ *     dst_k[j, :] = src_k[i, :],   dst_v[j, :] = src_v[i, :]
+ *
+ *   dst_k, dst_v device float [num_dst_blocks, n_kv_heads]; src_k, src_v float
+ *                [num_src_blocks, n_kv_heads], in device or device-addressable pinned
+ *                host memory; 4-byte aligned.  dst_v and src_v may both be NULL.
+ *   pairs        as swap_blocks
+ */
+PKV_API pkv_status swap_block_scales(float* dst_k, float* dst_v, const float* src_k,
+                                     const float* src_v, int n_kv_heads, const int64_t* pairs,
+                                     int n_pairs, int64_t num_src_blocks, int64_t num_dst_blocks,
+                                     void* stream);
 
 /*
  * Host-side physical block manager ([LAYOUT] section 三 KVBlockManager):

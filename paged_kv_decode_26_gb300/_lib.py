@@ -82,6 +82,7 @@ SIGNATURES = {
     "pkv_multi_query_q8_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
     "swap_blocks": (_i, [_p, _p, _sz, _p, _i, _i64, _i64, _p]),
     "swap_blocks_kv": (_i, [_p, _p, _p, _p, _sz, _p, _i, _i64, _i64, _p]),
+    "swap_block_scales": (_i, [_p, _p, _p, _p, _i, _p, _i, _i64, _i64, _p]),
     "pkv_block_manager_create": (_p, [_i, _i]),
     "pkv_block_manager_create_with_free": (_p, [_i, _i, _p, _i]),
     "pkv_block_manager_destroy": (None, [_p]),

@@ -791,10 +791,16 @@ def paged_attn_multi_query_q8(out: torch.Tensor, q: torch.Tensor, q_start: torch
     return out
 
 
+def _are_scales(block_bytes: int, *pools: torch.Tensor) -> bool:
+    """Blocks of floats that are no multiple of 16 bytes: an 8-bit cache's scales."""
+    return block_bytes % 16 != 0 and all(p.dtype is torch.float32 for p in pools)
+
+
 def swap_blocks(dst_pool: torch.Tensor, src_pool: torch.Tensor, pairs: torch.Tensor,
                 stream: Optional[torch.cuda.Stream] = None) -> None:
     """dst_pool[j] = src_pool[i] for each (i, j) row of `pairs` (int64 [n, 2]).
-    src_pool and pairs may live in pinned host memory."""
+    src_pool and pairs may live in pinned host memory.  Blocks are multiples of 16
+    bytes, or any number of float32 (the scales of an 8-bit cache)."""
     _need_cuda("dst_pool", dst_pool)
     for name, t in (("src_pool", src_pool), ("pairs", pairs)):
         if not t.is_contiguous():
@@ -806,6 +812,11 @@ def swap_blocks(dst_pool: torch.Tensor, src_pool: torch.Tensor, pairs: torch.Ten
     bb = dst_pool[0].numel() * dst_pool.element_size() if dst_pool.shape[0] else 0
     if src_pool.shape[0] and src_pool[0].numel() * src_pool.element_size() != bb:
         raise ValueError("source and destination blocks differ in size")
+    if _are_scales(bb, dst_pool, src_pool):
+        check(lib().swap_block_scales(_ptr(dst_pool), None, _ptr(src_pool), None, bb // 4,
+                                      _ptr(pairs), pairs.shape[0], src_pool.shape[0],
+                                      dst_pool.shape[0], _stream_ptr(stream)), "swap_blocks")
+        return
     st = lib().swap_blocks(_ptr(dst_pool), _ptr(src_pool), bb, _ptr(pairs), pairs.shape[0],
                            src_pool.shape[0], dst_pool.shape[0], _stream_ptr(stream))
     check(st, "swap_blocks")
@@ -814,7 +825,8 @@ def swap_blocks(dst_pool: torch.Tensor, src_pool: torch.Tensor, pairs: torch.Ten
 def swap_blocks_kv(dst_k: torch.Tensor, dst_v: torch.Tensor, src_k: torch.Tensor,
                    src_v: torch.Tensor, pairs: torch.Tensor,
                    stream: Optional[torch.cuda.Stream] = None) -> None:
-    """swap_blocks on the Key and the Value cache in one launch (same pairs)."""
+    """swap_blocks on the Key and the Value cache (or their scales) in one launch (same
+    pairs)."""
     for name, t in (("dst_k", dst_k), ("dst_v", dst_v)):
         _need_cuda(name, t)
     for name, t in (("src_k", src_k), ("src_v", src_v), ("pairs", pairs)):
@@ -829,6 +841,11 @@ def swap_blocks_kv(dst_k: torch.Tensor, dst_v: torch.Tensor, src_k: torch.Tensor
     bb = dst_k[0].numel() * dst_k.element_size() if dst_k.shape[0] else 0
     if src_k.shape[0] and src_k[0].numel() * src_k.element_size() != bb:
         raise ValueError("source and destination blocks differ in size")
+    if _are_scales(bb, dst_k, dst_v, src_k, src_v):
+        check(lib().swap_block_scales(_ptr(dst_k), _ptr(dst_v), _ptr(src_k), _ptr(src_v), bb // 4,
+                                      _ptr(pairs), pairs.shape[0], src_k.shape[0], dst_k.shape[0],
+                                      _stream_ptr(stream)), "swap_blocks_kv")
+        return
     st = lib().swap_blocks_kv(_ptr(dst_k), _ptr(dst_v), _ptr(src_k), _ptr(src_v), bb, _ptr(pairs),
                               pairs.shape[0], src_k.shape[0], dst_k.shape[0], _stream_ptr(stream))
     check(st, "swap_blocks_kv")

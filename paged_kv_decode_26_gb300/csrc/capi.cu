@@ -1314,4 +1314,30 @@ PKV_API pkv_status swap_blocks_kv(void* dst_k, void* dst_v, const void* src_k,
                        stream);
 }
 
+PKV_API pkv_status swap_block_scales(float* dst_k, float* dst_v, const float* src_k,
+                                     const float* src_v, int n_kv_heads, const int64_t* pairs,
+                                     int n_pairs, int64_t num_src_blocks, int64_t num_dst_blocks,
+                                     void* stream) {
+    if (n_kv_heads <= 0 || n_pairs < 0 || num_src_blocks < 0 || num_dst_blocks < 0)
+        return invalid("sizes");
+    if ((dst_v == nullptr) != (src_v == nullptr)) return invalid("dst_v and src_v: both or neither");
+    if (n_pairs == 0) return PKV_OK;
+    if (!pairs || !dst_k || !src_k) return invalid("NULL pointer");
+    for (const void* ptr : {(const void*)dst_k, (const void*)dst_v, (const void*)src_k,
+                            (const void*)src_v})
+        if (((uintptr_t)ptr & 3) != 0) return invalid("scales must be 4-byte aligned");
+    if (((uintptr_t)pairs & 7) != 0) return invalid("pairs must be 8-byte aligned");
+    DeviceInfo* dev = nullptr;
+    cudaError_t e = device_info(&dev);
+    if (e != cudaSuccess) return cuda_fail(e);
+    const pkv::ScalePools pools = {{dst_k, dst_v}, {src_k, src_v}};
+    const long long ctas =
+        ((long long)n_pairs * n_kv_heads + pkv::kSwapThreads - 1) / pkv::kSwapThreads;
+    const dim3 grid((unsigned)std::min(ctas, 8LL * dev->sm_count), dst_v ? 2u : 1u);
+    pkv::swap_scales_kernel<<<grid, pkv::kSwapThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+        pools, n_kv_heads, pairs, n_pairs, num_src_blocks, num_dst_blocks, dev->errors);
+    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e);
+    return PKV_OK;
+}
+
 }  // extern "C"

@@ -94,6 +94,32 @@ __global__ void __launch_bounds__(kSwapThreads)
     }
 }
 
+// swap_blocks on rows of `width` floats (the scales of an 8-bit cache, a few bytes a
+// block): a thread per float, blockIdx.y the cache.
+struct ScalePools {
+    float* dst[2];
+    const float* src[2];
+};
+__global__ void __launch_bounds__(kSwapThreads)
+    swap_scales_kernel(const ScalePools pools, int width, const int64_t* __restrict__ pairs,
+                       int n_pairs, int64_t num_src, int64_t num_dst, unsigned int* errors) {
+    float* dst = pools.dst[blockIdx.y];
+    const float* src = pools.src[blockIdx.y];
+    const int64_t total = (int64_t)n_pairs * width;
+    for (int64_t e = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; e < total;
+         e += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t k = e / width;
+        const int h = (int)(e - k * width);
+        const int64_t i = pairs[2 * k], j = pairs[2 * k + 1];
+        if (i < 0 || j < 0) continue;
+        if (i >= num_src || j >= num_dst) {
+            if (h == 0 && blockIdx.y == 0) raise_error(errors, PKV_DEVERR_PAIR);
+            continue;
+        }
+        dst[j * width + h] = src[i * width + h];
+    }
+}
+
 // ------------------------------------------------------- bulk block copy
 //
 // swap_blocks between two device pools through the copy engine of each SM
