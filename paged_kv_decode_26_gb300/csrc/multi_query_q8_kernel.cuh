@@ -650,6 +650,7 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
                     };
                     // 32 keys' scores (formed) or products
                     auto scores = [&](float (&y)[32], int part) {
+                        __syncwarp();
                         tc_ld32(t_lane + Z::S_COL + part * 32, reinterpret_cast<uint32_t*>(y));
                         tc_wait_ld();
 #pragma unroll
@@ -760,6 +761,7 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
                                                       w, g * 8);
                             if (f != 0.f && !apart) l = fmaf(sum, sc.ib[part * 2 + g] * ref, l);
                         }
+                        __syncwarp();
                         tc_st16(t_lane + Z::S_COL + part * 16, w[0]);
                         if (PARTS > 1)
 #pragma unroll
@@ -786,6 +788,7 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
                     float o[32];
+                    __syncwarp();                  // (rows part ways in what follows)
                     tc_ld32(t_lane + c0, reinterpret_cast<uint32_t*>(o));
                     tc_wait_ld();
                     if (!real) continue;
