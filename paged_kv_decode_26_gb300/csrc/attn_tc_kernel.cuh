@@ -877,6 +877,7 @@ __device__ __forceinline__ void attn_softmax(const AttnControl& ctl, const AttnP
 #pragma unroll 1
             for (int g = 0; g < D / COLS; ++g) {
                 uint32_t w[32];
+                __syncwarp();                          // (rows part ways in what follows)
                 if (bad) {
 #pragma unroll
                     for (int c = 0; c < 32; ++c) w[c] = 0u;

@@ -618,6 +618,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
                     uint32_t ov[32];
+                    __syncwarp();                      // (rows part ways in what follows)
                     tc_ld32(t_lane + c0, ov);
                     tc_wait_ld();
                     if (!real) continue;
