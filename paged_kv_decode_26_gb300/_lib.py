@@ -146,9 +146,9 @@ def calls():
                     from . import _tensor_calls
                 except ImportError as e:
                     raise RuntimeError(
-                        "_tensor_calls.so is missing or does not load: build it with "
-                        "`python -c 'import paged_kv_decode_26_gb300.build as b; b.build()'` "
-                        f"({e})") from e
+                        "_tensor_calls.so is missing or does not load: build it, with a CUDA build "
+                        "of torch, by `python -c 'import paged_kv_decode_26_gb300.build as b; "
+                        f"b.build()'` ({e})") from e
                 _calls = _tensor_calls
     return _calls
 

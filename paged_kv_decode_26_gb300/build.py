@@ -3,7 +3,10 @@ _tensor_calls.so (the part of the binding that is native) with g++.
 
 Each translation unit compiles in parallel to an object under _build/, then
 nvcc links the shared library next to this file, and g++ the extension against
-it.  Rebuilds only when a source or header is newer than the libraries.
+it.  Rebuilds the library only when a source or header is newer, and the extension
+only then or when torch or Python are others than it was built with.  The library needs
+nvcc alone: without a CUDA build of torch there is no extension, and the calls that go
+through it say so.
 """
 from __future__ import annotations
 
@@ -22,6 +25,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpagedkv.so")
 CALLS_SRC = os.path.join(HERE, "csrc_py", "tensor_calls.cpp")
 CALLS = os.path.join(HERE, "_tensor_calls.so")
+CALLS_STAMP = os.path.join(BUILD, "tensor_calls.built_with")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--use_fast_math", "-Xcompiler", "-fPIC",
@@ -42,14 +46,44 @@ def _sources():
 def _deps():
     return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) +
             glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.inc")) +
-            glob.glob(os.path.join(INCLUDE, "*.h")) + [CALLS_SRC, os.path.abspath(__file__)])
+            glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(CALLS)):
+    """Whether the library and, where torch has CUDA, the extension are."""
+    return _lib_up_to_date() and (_calls_stamp() is None or _calls_up_to_date())
+
+
+def _newer(path: str, deps) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(d) <= os.path.getmtime(path) for d in deps)
+
+
+def _lib_up_to_date() -> bool:
+    return _newer(LIB, _deps())
+
+
+def _calls_stamp() -> str | None:
+    """What the extension's binary depends on besides its source; None without a CUDA
+    build of torch."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    if torch.version.cuda is None:
+        return None
+    return "\n".join([torch.__version__, torch.version.cuda, os.path.dirname(torch.__file__),
+                      str(int(getattr(torch._C, "_GLIBCXX_USE_CXX11_ABI", True))),
+                      str(sysconfig.get_config_var("SOABI"))])
+
+
+def _calls_up_to_date() -> bool:
+    try:
+        with open(CALLS_STAMP) as f:
+            built = f.read()
+    except OSError:
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return built == _calls_stamp() and _newer(CALLS, [CALLS_SRC, os.path.join(INCLUDE, "pagedkv.h"),
+                                                      os.path.abspath(__file__)])
 
 
 def _compile(src: str, verbose_ptxas: bool) -> str:
@@ -93,24 +127,30 @@ def _link_calls(obj: str) -> None:
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, CALLS)
+    with open(CALLS_STAMP, "w") as f:
+        f.write(_calls_stamp())
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, jobs: int | None = None) -> str:
-    if not force and up_to_date():
+    lib = force or not _lib_up_to_date()
+    calls = _calls_stamp() is not None and (force or not _calls_up_to_date())
+    if not (lib or calls):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    srcs = _sources()
+    srcs = _sources() if lib else []
     jobs = jobs or min(len(srcs) + 1, os.cpu_count() or 4)
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
-        calls = ex.submit(_compile_calls)
+        calls_obj = ex.submit(_compile_calls) if calls else None
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
-    os.replace(tmp, LIB)
-    _link_calls(calls.result())
+    if lib:
+        tmp = LIB + f".tmp{os.getpid()}"
+        cmd = [_nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
+        os.replace(tmp, LIB)
+    if calls:
+        _link_calls(calls_obj.result())
     return LIB
 
 
