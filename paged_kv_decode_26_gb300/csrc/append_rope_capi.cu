@@ -157,28 +157,39 @@ void launch_append(const pkv::AppendRopeParams& p, cudaStream_t stream) {
            stream>>>(p);
 }
 
-// Tokens from which a CTA takes a window of block_size tokens instead of one (decode
-// tokens, one / block_size: 64 3.9 / 8.6 us, 256 8.9 / 8.9, 900 26.7 / 9.8; a prompt of
-// 300 24 / 9.4).
-constexpr int kQ8WindowFrom = 192;
-// CTAs per SM from which one takes several parts of the heads (4 / 6 / 9 / 14: 8 MHA
-// prompts 97 / 85 / 87 / 91 us, 16 GQA prompts 94 / 94 / 98 / 98).
+// CTAs per SM up to which a CTA takes one token, and from which windows of block_size
+// tokens, where one takes several parts of the heads.
+// Windows, one token a CTA / windows, us: decode tokens of 32 query and 8 kv heads of 128,
+// pages of 16 (9 CTAs a token), 64 3.7 / 4.5, 96 5.4 / 4.6, 512 14 / 5.5; 32 of 32 heads,
+// pages of 32 (65 a token), 8 3.4 / 3.3, 16 5.3 / 3.5, 160 26 / 5.3; 8 of 1 head of 64
+// (2 a token), 448 3.8 / 5.4, 1024 7.0 / 5.5.  Of 540 sizes the rule takes 0.5 % longer in
+// sum than the better of both each (at 5 a SM 1.5 %, at 7 and 8 0.4 and 0.5 %).
+// Several parts (4 / 6 / 9 / 14): 8 MHA prompts 97 / 85 / 87 / 91 us, 16 GQA prompts 94 /
+// 94 / 98 / 98.
 constexpr int kQ8CtasPerSm = 6;
 
 template <int D, int B, typename T>
 void launch_append_q8_of(const pkv::AppendRopeParams& p, int sm_count, cudaStream_t stream) {
     constexpr int J = D / 16, heads = pkv::q8_cta_heads(D, B);
-    const int window = p.num_tokens >= kQ8WindowFrom ? B : 1;
-    const int windows = (p.num_tokens + window - 1) / window;
     const int parts = (2 * p.n_kv_heads + heads - 1) / heads;
+    // query heads and parts of them, at `tokens` a CTA
+    auto heads_of = [&](int tokens) {
+        const int most = pkv::kAppendThreads * pkv::kAppendItems / (tokens * J);
+        return most < 1 ? 1 : (most > p.n_heads ? p.n_heads : most);
+    };
+    auto parts_of = [&](int tokens) {
+        const int n = heads_of(tokens);
+        return n > 0 ? (p.n_heads + n - 1) / n : 0;
+    };
+    const long long enough = (long long)kQ8CtasPerSm * sm_count;
+    const int window = (long long)p.num_tokens * (parts + parts_of(1)) > enough ? B : 1;
+    const int windows = (p.num_tokens + window - 1) / window;
     // parts one after the other in a CTA, as long as there are enough CTAs
-    int cta_parts = (int)((long long)windows * parts / (kQ8CtasPerSm * sm_count));
+    int cta_parts = (int)((long long)windows * parts / enough);
     cta_parts = cta_parts < 1 ? 1 : (cta_parts > parts ? parts : cta_parts);
     const int kv_ctas = (parts + cta_parts - 1) / cta_parts;
-    int q_heads = pkv::kAppendThreads * pkv::kAppendItems / (window * J);
-    q_heads = q_heads < 1 ? 1 : (q_heads > p.n_heads ? p.n_heads : q_heads);
-    const int q_parts = p.n_heads > 0 ? (p.n_heads + q_heads - 1) / q_heads : 0;
-    const dim3 grid((unsigned)windows, (unsigned)(kv_ctas + q_parts));
+    const int q_heads = heads_of(window);
+    const dim3 grid((unsigned)windows, (unsigned)(kv_ctas + parts_of(window)));
     pkv::append_rope_q8_kernel<D, B, T>
         <<<grid, pkv::kAppendThreads, 0, stream>>>(p, window, kv_ctas, cta_parts, q_heads);
 }
