@@ -140,9 +140,23 @@ ChunkShape chunk_shape(int num_seqs, int max_q_len, int n_heads, int n_kv_heads,
     return c;
 }
 
-// Longest context first (longest_first), as paged_attn_multi_query.
+// Longest context first (longest_first): the items that end last begin first, but every
+// CTA ranks the sequences, and neighbours no longer share a head's keys.  In order /
+// longest first, us, chunks of 8 to 8192 / S tokens, 32 query and 8 kv heads: 8 sequences
+// at 1000-8000 183 / 152, 1000-3000 95 / 92, 64-500 43 / 41; 32 at 500-3000 192 / 187,
+// 256-2500 156 / 162; 64 at 500-4000 260 / 233, 64-500 97 / 99; 128 at 1000-8000 580 / 544,
+// 256-2000 206 / 211; 256 at 1000-16000 1949 / 1920, 500-4000 602 / 628.  Prompts (chunks
+// that are most of their contexts), 4 of 500-8000 1090 / 1067, 16 of 100-4000 924 / 932, 64
+// of 20-3000 2200 / 2357.  2 equal chunks of 2048 at 12K-16K 739 / 709, 32 / 32 heads 693 /
+// 721.
 constexpr int kLptMaxSeqs = 256;
-constexpr int kLptMinContext = 8192;
+constexpr int kLptMinContext = 2560, kLptSeqContext = 32, kLptPromptContext = 8192;
+bool longest_first_pays(int num_seqs, int max_q_len, int max_context_len) {
+    const int from = max_q_len > max_context_len / 2
+                         ? kLptPromptContext
+                         : std::max(kLptMinContext, kLptSeqContext * num_seqs);
+    return num_seqs <= kLptMaxSeqs && max_context_len >= from;
+}
 
 }  // namespace
 
@@ -306,7 +320,7 @@ PKV_API pkv_status paged_attn_multi_query_q8(
     p.scale_log2 = scale * 1.4426950408889634f;
     p.max_pages = (int)(((long long)max_context_len + block_size - 1) / block_size);
     p.errors = dev->errors;
-    p.lpt_seqs = max_context_len >= kLptMinContext && num_seqs <= kLptMaxSeqs ? num_seqs : 0;
+    p.lpt_seqs = longest_first_pays(num_seqs, max_q_len, max_context_len) ? num_seqs : 0;
     p.tiles = c.tiles;
     p.whole = (int)c.whole;
     p.splits = c.splits;
