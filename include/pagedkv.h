@@ -645,9 +645,10 @@ PKV_API pkv_status pkv_rope_table(float* table, int num_positions, int rotary_di
  *     q_out[i] = rotated q[i],  k_out[i] = rotated k[i]   (where given)
  *
  * A pair (a, b) of a head's first rotary_dim elements becomes (a c - b s,
- * a s + b c) in fp32, rounded once to dtype; pair j is (j, j + rotary_dim / 2),
- * or with interleaved != 0 (2 j, 2 j + 1), and takes the table's columns j and
- * rotary_dim / 2 + j.  Elements from rotary_dim on pass bit for bit.
+ * a s + b c) in fp32 (where numbers below 2^-126 may count as 0), rounded once to
+ * dtype; pair j is (j, j + rotary_dim / 2), or with interleaved != 0 (2 j, 2 j + 1),
+ * and takes the table's columns j and rotary_dim / 2 + j.  Elements from rotary_dim
+ * on pass bit for bit.
  *   k, v         device, token i at k + i * k_stride (elements of dtype, F16 or
  *                BF16): [n_kv_heads, head_dim] contiguous per token, so q, k and v
  *                may be views of one fused tensor; strides multiples of 8
@@ -731,7 +732,8 @@ PKV_API pkv_status kv_append_rope_q8(void* k_pool, void* v_pool, float* k_scale,
  *
  *     out[s,h,:] = sum_t softmax_t(scale * a_t (q[s,h,:] . k_t)) b_t v_t
  *
- *   q             device, [num_seqs, n_heads, head_dim] of q_dtype (F16 or BF16)
+ *   q             device, [num_seqs, n_heads, head_dim] of q_dtype (F16 or BF16); out may
+ *                 be q itself where it has 16 bits, else it overlaps nothing of the call
  *   k_pool, v_pool device e4m3 bytes [num_blocks, block_size, n_kv_heads,
  *                 head_dim], 16-byte aligned
  *   k_scale, v_scale device float [num_blocks, n_kv_heads]: any numbers from 2^-126
@@ -766,7 +768,8 @@ PKV_API pkv_status paged_attn_decode_q8(
  *
  *   out, q       device [total_q, n_heads, head_dim]; q of q_dtype (F16 or BF16), out
  *                of out_dtype (F16, BF16, F32); 16-byte aligned; rows of no sequence
- *                are not written
+ *                are not written; out may be q itself where it has 16 bits, else it
+ *                overlaps nothing of the call
  *   q_start      device int32 [num_seqs + 1], non-decreasing, q_start[0] >= 0,
  *                q_start[num_seqs] <= total_q
  *   max_q_len, max_context_len  host-side bounds of q_len and context_lens

@@ -78,6 +78,23 @@ pkv_status check_scales(const float* k_scale, const float* v_scale, int num_bloc
     return PKV_OK;
 }
 
+// The output is the queries themselves (every row is read by those that write it, before
+// they do) or lies apart from all that is read.
+pkv_status check_apart(const void* out, pkv_dtype out_dtype, const void* q, size_t elements,
+                       const void* k_pool, const void* v_pool, size_t pool, const float* k_scale,
+                       const float* v_scale, size_t scales) {
+    auto meets = [&](const void* p, size_t bytes) {
+        const uintptr_t o = reinterpret_cast<uintptr_t>(out), a = reinterpret_cast<uintptr_t>(p);
+        return o < a + bytes && a < o + elements * (out_dtype == PKV_F32 ? 4 : 2);
+    };
+    if (meets(q, elements * 2) && (out != q || out_dtype == PKV_F32))
+        return invalid("out overlaps q (it may be q itself, in 16 bits)");
+    if (meets(k_pool, pool) || meets(v_pool, pool) || meets(k_scale, scales * sizeof(float)) ||
+        meets(v_scale, scales * sizeof(float)))
+        return invalid("out overlaps the cache");
+    return PKV_OK;
+}
+
 // How a chunk's items (pairs of row tiles of a kv head) meet the SMs, one at a time on
 // each.  Items that do not fill the SMs once more (all of them, where there are fewer
 // than SMs) are cut into parts of their keys, kPartTiles key tiles at least, so that the
@@ -187,6 +204,10 @@ PKV_API pkv_status paged_attn_decode_q8(
                                        max_context_len);
     if (st != PKV_OK || num_seqs == 0) return st;
     if ((st = check_scales(k_scale, v_scale, num_blocks)) != PKV_OK) return st;
+    const size_t scales = (size_t)num_blocks * n_kv_heads;
+    if ((st = check_apart(out, out_dtype, q, (size_t)num_seqs * n_heads * head_dim, k_pool, v_pool,
+                          scales * block_size * head_dim, k_scale, v_scale, scales)) != PKV_OK)
+        return st;
     DeviceInfo* dev = nullptr;
     cudaError_t e = device_info(&dev);
     if (e != cudaSuccess) return cuda_fail(e);
@@ -256,6 +277,10 @@ PKV_API pkv_status paged_attn_multi_query_q8(
     if (!q_start) return invalid("q_start is NULL");
     if (!aligned4(q_start)) return invalid("q_start must be 4-byte aligned");
     if ((st = check_scales(k_scale, v_scale, num_blocks)) != PKV_OK) return st;
+    const size_t scales = (size_t)num_blocks * n_kv_heads;
+    if ((st = check_apart(out, out_dtype, q, (size_t)total_q * n_heads * head_dim, k_pool, v_pool,
+                          scales * block_size * head_dim, k_scale, v_scale, scales)) != PKV_OK)
+        return st;
     DeviceInfo* dev = nullptr;
     cudaError_t e = device_info(&dev);
     if (e != cudaSuccess) return cuda_fail(e);
