@@ -22,11 +22,13 @@
 // permutation puts each dim's tokens side by side, and rows g, g + 8 of the output
 // stand for dims 2 g, 2 g + 1.
 //
-// Precision: a bf16 query head is scaled by a power of two into fp16's range
-// (exact but for elements 2^-38 below its largest).  Weights enter the second
-// product as p b / b_ref in two fp16 parts, lifted as in weight_range.cuh; the
-// reference (m, b_ref) is the score and scale of the key with the largest p b when
-// it was set, m a score itself (weight_range.cuh says why).
+// Precision: a bf16 query head is scaled by a power of two into fp16's range (exact
+// down to 2^-31 of its largest element, below that off by 2^-39 of it at most).
+// Weights enter the second product as p b / b_ref in two fp16 parts, lifted as in
+// weight_range.cuh; the reference (m, b_ref) is the score and scale of the key with
+// the largest p b when it was set, m a score itself (weight_range.cuh says why).  Any
+// pair with that sum of exponents would do, and where scales lie far apart (blocks of
+// zeros beside others) m is one that keeps p, its sum and b / b_ref in fp32's range.
 //
 // Runs, rings and merge as in decode_pieces_kernel.cuh, with chunks of 32 tokens and
 // no runs to take over.

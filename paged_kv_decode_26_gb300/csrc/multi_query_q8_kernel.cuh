@@ -13,7 +13,8 @@
 // codes of K and V on their way from global to shared memory, 16 keys at a time in
 // turn, the next ones already in registers (no copy of the codes in shared memory:
 // the products' operands take most of its bandwidth).  Queries become fp16 too, each row
-// scaled by a power of two (exact but for elements 2^-38 below the row's largest).
+// scaled by a power of two (exact down to 2^-31 of the row's largest element, below
+// that off by 2^-39 of it at most).
 // A block's scales are one number per 16 keys: a_t multiplies the exponent's
 // factor, log2 b_t joins its addend, so they cost nothing per element; the sum L
 // takes the weights of 16 keys times 1 / b_t.
@@ -52,7 +53,6 @@ constexpr int kMq8Keys = 128;
 constexpr int kMq8Rows = 128;
 constexpr int kMq8Threads = 512;      // 8 softmax warps, 1 MMA, 7 that widen
 constexpr int kMq8Widen = 7;
-constexpr int kMq8Ahead = 1;          // groups of 16 keys that a widening warp has under way
 // Registers per thread: 512 x 128 at launch
 constexpr int kMq8SoftmaxRegs = 184, kMq8OtherRegs = 72;
 static_assert(256 * kMq8SoftmaxRegs + 256 * kMq8OtherRegs <= kMq8Threads * 128, "registers");
@@ -410,64 +410,54 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
         // where a part's two chunks of 8 go in part 0
         const uint32_t first_at = smem_addr(sKV) + r0 * 128 + (((2 * u) ^ r0) << 4);
         const uint32_t second_at = smem_addr(sKV) + r0 * 128 + (((2 * u + 1) ^ r0) << 4);
-        Task task[kMq8Ahead];
+        Task now;
         unsigned k = warp - 9;
-#pragma unroll
-        for (int i = 0; i < kMq8Ahead; ++i)
-            fetch(task[i], k + i * kMq8Widen, entry_of(k + i * kMq8Widen));
-        int entry = entry_of(k + kMq8Ahead * kMq8Widen);
-        bool ok = true;
-        while (ok && k < n_tasks) {
-#pragma unroll
-            for (int i = 0; i < kMq8Ahead; ++i) {
-                if (!ok || k >= n_tasks) break;
-                Task& now = task[i];
-                const unsigned i_op = k / 8, st = i_op % STAGES, g = k % 8, j = k / 16;
-                if (i_op >= STAGES)
-                    ok = __all_sync(0xffffffffu, mbar_wait(&kv_free[st], (i_op / STAGES - 1) & 1u,
-                                                           p.errors));
-                if (!ok) break;
-                if ((i_op & 1) == 0) {
-                    Mq8Scale& e = s_scale[j % kMq8Scales];
-                    if (lane == 0) {
-                        e.a[g] = now.scale;
-                    } else if (lane == 1) {
-                        // (NaN stays)
-                        const float b = now.scale < kQ8LeastScale ? kQ8LeastScale : now.scale;
-                        const float lb = __log2f(b);
-                        e.lb[g] = lb;
-                        e.ib[g] = __frcp_rn(b);
-                        e.page[g] = now.page ? (mq8_usual(lb) ? 1 : 2) : 0;
-                    }
-                } else if (j >= guard_from) {
-                    bool any = false;
-#pragma unroll
-                    for (int n = 0; n < kParts; ++n) {
-                        uint4& w = now.codes[n];
-                        const uint4 bad = make_uint4(q8_nans(w.x), q8_nans(w.y), q8_nans(w.z),
-                                                     q8_nans(w.w));
-                        any |= (bad.x | bad.y | bad.z | bad.w) != 0u;
-                        w = make_uint4(w.x & ~bad.x, w.y & ~bad.y, w.z & ~bad.z, w.w & ~bad.w);
-                    }
-                    if (any) *s_poison = 1;
+        fetch(now, k, entry_of(k));
+        int entry = entry_of(k + kMq8Widen);
+        while (k < n_tasks) {
+            const unsigned i_op = k / 8, st = i_op % STAGES, g = k % 8, j = k / 16;
+            if (i_op >= STAGES &&
+                !__all_sync(0xffffffffu, mbar_wait(&kv_free[st], (i_op / STAGES - 1) & 1u, p.errors)))
+                break;
+            if ((i_op & 1) == 0) {
+                Mq8Scale& e = s_scale[j % kMq8Scales];
+                if (lane == 0) {
+                    e.a[g] = now.scale;
+                } else if (lane == 1) {
+                    // (NaN stays)
+                    const float b = now.scale < kQ8LeastScale ? kQ8LeastScale : now.scale;
+                    const float lb = __log2f(b);
+                    e.lb[g] = lb;
+                    e.ib[g] = __frcp_rn(b);
+                    e.page[g] = now.page ? (mq8_usual(lb) ? 1 : 2) : 0;
                 }
-                const uint32_t dst = st * Z::KV_BYTES + g * 2048;
+            } else if (j >= guard_from) {
+                bool any = false;
 #pragma unroll
                 for (int n = 0; n < kParts; ++n) {
-                    uint4 a, b;
-                    mq8_widen(now.codes[n], a, b);
-                    const uint32_t to = dst + n / Z::HALVES * 1024 + n % Z::HALVES * Z::KV_HALF;
-                    mq8_store(first_at + to, a);
-                    mq8_store(second_at + to, b);
+                    uint4& w = now.codes[n];
+                    const uint4 bad = make_uint4(q8_nans(w.x), q8_nans(w.y), q8_nans(w.z),
+                                                 q8_nans(w.w));
+                    any |= (bad.x | bad.y | bad.z | bad.w) != 0u;
+                    w = make_uint4(w.x & ~bad.x, w.y & ~bad.y, w.z & ~bad.z, w.w & ~bad.w);
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&kv_full[st]);
-                const unsigned next = k + kMq8Ahead * kMq8Widen;
-                fetch(now, next, entry);
-                entry = entry_of(next + kMq8Widen);
-                k += kMq8Widen;
+                if (any) *s_poison = 1;
             }
+            const uint32_t dst = st * Z::KV_BYTES + g * 2048;
+#pragma unroll
+            for (int n = 0; n < kParts; ++n) {
+                uint4 a, b;
+                mq8_widen(now.codes[n], a, b);
+                const uint32_t to = dst + n / Z::HALVES * 1024 + n % Z::HALVES * Z::KV_HALF;
+                mq8_store(first_at + to, a);
+                mq8_store(second_at + to, b);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&kv_full[st]);
+            k += kMq8Widen;
+            fetch(now, k, entry);
+            entry = entry_of(k + kMq8Widen);
         }
       }
     } else {
