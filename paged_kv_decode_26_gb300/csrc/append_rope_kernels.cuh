@@ -248,15 +248,15 @@ __global__ void __launch_bounds__(kRopeThreads)
 // y: parts of the key and value heads, or of the query heads.  A window is one token,
 // or block_size of them: then the rows of its runs are block_size at most but for the
 // last run, which goes by itself if it does not fit beside the others.  Runs are found by
-// what stands within the threads' view of the window; where left-out tokens lie
-// between two of one block there, or up to the view's end, the living ones are sought
-// beyond (regather: 250 tokens padded to 256 4.8 -> 5.7 us, 100 of 256 4.7 -> 6.2, a
-// prompt of 1100 in 2048 11.3 -> 11.7; 32 query and 8 kv heads of 128).
+// what stands within B tokens of the window; where left-out tokens lie between two of one
+// block there, or up to the view's end, the living ones are sought beyond (regather: 250
+// tokens padded to 256 4.9 -> 6.0 us, 100 of 256 4.7 -> 5.8, a prompt of 1100 in 2048 11.4
+// -> 11.9; 32 query and 8 kv heads of 128).
 // A thread holds its items from the one pass over them to the next (the largest
 // value, then the codes), while the next part's rows and scales are on their way.
 //
-// Measured: 8 prompts of 300-2048 tokens, 32 heads of 128, 85 us (3.9 TB/s), 16 of 32
-// query and 8 kv heads 94 (4.4 TB/s), 4 tokens 3.2 us.  Not bound by HBM but by the steps:
+// Measured: 8 prompts of 300-2048 tokens, 32 heads of 128, 87-88 us (3.8 TB/s), 16 of 32
+// query and 8 kv heads 94 (4.4 TB/s), 4 tokens 3.3 us.  Not bound by HBM but by the steps:
 // 300 instructions an item, two barriers a step.  A warp per run and head, its rows in
 // shared memory and no barriers, took 95 us and 6.4 for the 4 tokens; one barrier a step
 // 121; the parts of a window side by side in the grid 132; 256 threads 101.
@@ -481,29 +481,60 @@ __device__ __forceinline__ int gather_living(const AppendRopeParams& p, int w0, 
     return count;
 }
 
-// By the whole CTA, where tokens around the window are left out: 0 where none is left in
-// it, the tokens gathered (their number) where it matters what stands between them, else
-// -1: they matter between two of one block, and where nothing in view tells whether
-// they stand there.  Out of line: batches without padding never come here.
+// By the whole CTA, where tokens around the window are left out: the living tokens of the
+// window (their number), gathered with their neighbours where it matters what stands
+// between them, that is between two of one block and where nothing in view tells whether
+// they stand there.  Thread i looks at token w0 - B + i, at `span` of them; s_blk and s_in
+// get what is gathered.  Out of line: batches without padding never come here.
+struct Gathered {
+    int count;                 // 0: none in the window, -1: nothing is to be gathered
+    int token, block, in_block, position;      // this thread's
+};
 template <int B>
-__device__ __noinline__ int regather(const AppendRopeParams& p, int w0, int w1, int block,
-                                     int in_block, bool out, const int* s_blk,
-                                     const unsigned* s_lives, int* s_tok) {
-    const int tid = threadIdx.x;
+__device__ __noinline__ Gathered regather(const AppendRopeParams& p, int w0, int w1, int span,
+                                          int block, int in_block, bool out, int* s_blk, int* s_in) {
+    __shared__ unsigned s_lives[kAppendThreads / 32];
+    __shared__ int s_tok[3 * B];               // as gather_living lists them
+    const int tid = threadIdx.x, t = w0 - B + tid;
+    Gathered r = {-1, -1, -1, 0, 0};
+    if (out && blockIdx.y == 0 && t >= w0 && t < w1)        // (says what is wrong)
+        token_lives(p, p.slots[t], p.table ? p.positions[t] : 0, true);
+    const unsigned lives = __ballot_sync(0xffffffffu, block >= 0);
+    if ((tid & 31) == 0) s_lives[tid / 32] = lives;
+    __syncthreads();
     const int next = next_living(s_lives, tid + 1), first = next_living(s_lives, B);
-    if (first >= B + (w1 - w0)) return 0;
+    if (first >= B + (w1 - w0)) {
+        r.count = 0;
+        return r;
+    }
     bool between = false, behind = false, ahead = false;
     if (block >= 0 && next < kAppendThreads)
         between = next > tid + 1 && s_blk[next] == block;
-    else if (block >= 0)
-        behind = tid >= B && tid + 1 < kAppendThreads && in_block < B - 1;
-    else if (out && tid == 0)
+    else if (block >= 0 && tid >= B && tid + 1 < span && in_block < B - 1) {
+        int last = B + (w1 - w0) - 1;          // of the window
+        while (!((s_lives[last / 32] >> (last % 32)) & 1u)) --last;
+        behind = s_blk[last] == block;
+    } else if (out && tid == 0) {
         ahead = s_blk[next] == s_blk[first];
+    }
     bool gather = __syncthreads_or(between);
-    if (!gather && __syncthreads_or(behind))
-        gather = rest_lives<B>(p, w0 - B + kAppendThreads, 1);
+    if (!gather && __syncthreads_or(behind)) gather = rest_lives<B>(p, w0 - B + span, 1);
     if (!gather && __syncthreads_or(ahead)) gather = rest_lives<B>(p, w0 - B - 1LL, -1);
-    return gather ? gather_living<B>(p, w0, w1, s_tok) : -1;
+    if (!gather) return r;
+    r.count = gather_living<B>(p, w0, w1, s_tok);
+    r.token = tid < 3 * B ? s_tok[tid] : -1;
+    if (r.token >= 0) {
+        const int64_t slot = p.slots[r.token];
+        r.position = p.table ? p.positions[r.token] : 0;
+        r.block = (int)(slot / B);
+        r.in_block = (int)(slot % B);
+    }
+    if (tid < 3 * B) {
+        s_blk[tid] = r.block;
+        s_in[tid] = r.in_block;
+    }
+    __syncthreads();
+    return r;
 }
 
 template <int D, int B, typename T>
@@ -515,10 +546,8 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
     constexpr int HC = q8_cta_heads(D, B);
     constexpr int kPairs = kAppendThreads * kAppendItems / J;   // rows x heads of a CTA
     static_assert(3 * B <= kAppendThreads, "a thread per token around the window");
-    __shared__ int s_blk[kAppendThreads];     // block and row of a token's slot, -1: none
-    __shared__ int s_in[kAppendThreads];
-    __shared__ unsigned s_lives[kAppendThreads / 32];   // those of a block, as bits
-    __shared__ int s_tok[3 * B];              // as gather_living lists them
+    __shared__ int s_blk[3 * B];              // block and row of a token's slot, -1: none
+    __shared__ int s_in[3 * B];
     __shared__ int s_count[2][kAppendThreads / 32];
     __shared__ Q8Row s_row[2 * kQ8MaxBlock];
     __shared__ int s_first_row[kQ8MaxBlock + 1];  // of a run: its first row in the block
@@ -540,41 +569,35 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
     }
 
     // ---- the tokens around the window: thread i looks at token w0 - B + i
+    const int span = min(w1 + B - 1, p.num_tokens) - (w0 - B);
     int t = w0 - B + tid, count = w1 - w0;     // tokens of the window
     bool here = t >= w0 && t < w1;
     int block = -1, in_block = 0, position = 0;
     bool out = false;                          // a token that is left out
-    if (t >= 0 && t < p.num_tokens) {
+    if (tid < span && t >= 0) {
         const int64_t slot = p.slots[t];
         position = p.table ? p.positions[t] : 0;
-        out = !token_lives(p, slot, position, here && blockIdx.y == 0);  // (says what is wrong)
+        out = !token_lives(p, slot, position, false);
         if (!out) {
             block = (int)(slot / B);
             in_block = (int)(slot % B);
         }
     }
-    s_blk[tid] = block;
-    s_in[tid] = in_block;
-    const unsigned lives_here = __ballot_sync(0xffffffffu, block >= 0);
-    if (lane == 0) s_lives[tid / 32] = lives_here;
+    if (tid < 3 * B) {
+        s_blk[tid] = block;
+        s_in[tid] = in_block;
+    }
     if (tid < kPairs) s_top[0][tid] = 0u;
     if (__syncthreads_or(out)) {
-        const int living = regather<B>(p, w0, w1, block, in_block, out, s_blk, s_lives, s_tok);
-        if (living == 0) return;
-        if (living > 0) {
-            count = living;
-            t = tid < 3 * B ? s_tok[tid] : -1;
+        const Gathered g = regather<B>(p, w0, w1, span, block, in_block, out, s_blk, s_in);
+        if (g.count == 0) return;
+        if (g.count > 0) {
+            count = g.count;
+            t = g.token;
             here = t >= w0 && t < w1;
-            block = -1;
-            if (t >= 0) {
-                const int64_t slot = p.slots[t];
-                position = p.table ? p.positions[t] : 0;
-                block = (int)(slot / B);
-                in_block = (int)(slot % B);
-            }
-            s_blk[tid] = block;
-            s_in[tid] = in_block;
-            __syncthreads();
+            block = g.block;
+            in_block = g.in_block;
+            position = g.position;
         }
     }
     // distance to the run's first token, -1: in no run

@@ -108,7 +108,7 @@ struct Q8Heads {
     float qf[2];       // score of a unit product at scale 1
     float m[2];        // the reference: a score,
     float lv[2];       // the logarithm of its value scale,
-    float rv[2];       // and 1 over that
+    float rv[2];       // and the weights' lift over that
     float l[2];        // this lane's part of the sum
 };
 
@@ -165,12 +165,26 @@ struct Q8Scales {
     float k[2], v[2];
 };
 
+// Value scales between which p and b / b_ref stay within fp32's range as they are (0: of
+// a half that holds nothing).
+__device__ __forceinline__ bool q8_usual(float b) {
+    return (b >= 0x1p-60f && b <= 0x1p16f) || b == 0.f;
+}
+
+// min(x, 2^127); NaN stays.
+__device__ __forceinline__ float q8_bounded(float x) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(0x1p127f));
+    return y;
+}
+
 // One chunk: halves of 16 tokens at kbase / vbase (+ 16 D bytes), `valid[h]` of a
 // half's tokens inside the context (0: nothing was loaded, or its block is
 // missing).  PRECISE: see piece_chunk.  MASKED: of `left[h]` tokens from the half's
 // first one on (0 if its block is missing), this lane's heads do not see the last less[e].
-template <int D, bool PRECISE, bool MASKED = false>
-__device__ __forceinline__ void q8_chunk(Q8Heads<D>& st, uint32_t kbase, uint32_t vbase,
+// APART: value scales may be any, else those so far and here are q8_usual.
+template <int D, bool PRECISE, bool MASKED, bool APART>
+__device__ __forceinline__ void q8_chunk_of(Q8Heads<D>& st, uint32_t kbase, uint32_t vbase,
                                          const int (&valid)[2], const int (&left)[2],
                                          const int (&less)[2], const Q8Scales& sc, int lane) {
     using Range = WeightRange<__half>;
@@ -220,8 +234,10 @@ __device__ __forceinline__ void q8_chunk(Q8Heads<D>& st, uint32_t kbase, uint32_
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             top[h][e] = fmaxf(x[h][e], x[h][2 + e]);
-            beyond |= (top[h][e] - st.m[e]) + (lv[h] - st.lv[e]) > Range::GROW ||
-                      top[h][e] - st.m[e] > kQ8Above;
+            // (apart: the scales' part bounded, so that a score kQ8Above above m is beyond too)
+            const float of = lv[h] - st.lv[e];
+            beyond |= (top[h][e] - st.m[e]) + (APART ? fmaxf(of, Range::GROW - kQ8Above) : of) >
+                      Range::GROW;
         }
     if (__any_sync(0xffffffffu, beyond)) {
 #pragma unroll
@@ -240,15 +256,17 @@ __device__ __forceinline__ void q8_chunk(Q8Heads<D>& st, uint32_t kbase, uint32_
                 }
                 high = fmaxf(high, t);
             }
-            if (b != 0.f || high - m > kQ8Above) {
+            if (b != 0.f || (APART && high - m > kQ8Above)) {
                 // lower for a scale below 2^-60, but never below what it was, nor far
                 // below a score
-                const float to = fmaxf(fmaxf(m + fminf(l + 60.f, 0.f), high - (kQ8Above - 6.f)),
-                                       st.m[e]);
+                const float to = APART ? fmaxf(fmaxf(m + fminf(l + 60.f, 0.f),
+                                                     high - (kQ8Above - 6.f)), st.m[e])
+                                       : m;
                 l += m - to;
                 const float al = st.m[e] == -INFINITY ? 1.f : exp2f(st.m[e] - to);
                 const float ao = st.m[e] == -INFINITY ? 1.f : exp2f((st.m[e] - to) + (st.lv[e] - l));
-                st.rv[e] = to == m && b != 0.f ? __frcp_rn(b) : exp2f(-l);
+                st.rv[e] = (!APART || (to == m && b != 0.f) ? __frcp_rn(b) : exp2f(-l)) *
+                           (1.f / Range::UNLIFT);
                 st.m[e] = to;
                 st.lv[e] = l;
                 st.l[e] *= al;
@@ -266,10 +284,11 @@ __device__ __forceinline__ void q8_chunk(Q8Heads<D>& st, uint32_t kbase, uint32_
     const float mu1 = st.m[1] == -INFINITY ? 0.f : st.m[1];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        // (bounded where p is next to nothing; NaN stays)
         float f0 = sc.v[h] * st.rv[0], f1 = sc.v[h] * st.rv[1];
-        f0 = (f0 > 0x1p116f ? 0x1p116f : f0) * (1.f / Range::UNLIFT);
-        f1 = (f1 > 0x1p116f ? 0x1p116f : f1) * (1.f / Range::UNLIFT);
+        if (APART) {                       // (where p is next to nothing)
+            f0 = q8_bounded(f0);
+            f1 = q8_bounded(f1);
+        }
         const float p0 = exp2f(x[h][0] - mu0), p1 = exp2f(x[h][1] - mu1);
         const float p2 = exp2f(x[h][2] - mu0), p3 = exp2f(x[h][3] - mu1);
         st.l[0] += p0 + p2;
@@ -320,6 +339,20 @@ __device__ __forceinline__ void q8_chunk(Q8Heads<D>& st, uint32_t kbase, uint32_
     }
 }
 
+// With the usual scales nothing leaves fp32's range; `apart` says whether there have been
+// others among a piece's chunks so far (the same for all lanes).
+template <int D, bool PRECISE, bool MASKED = false>
+__device__ __forceinline__ void q8_chunk(Q8Heads<D>& st, uint32_t kbase, uint32_t vbase,
+                                         const int (&valid)[2], const int (&left)[2],
+                                         const int (&less)[2], const Q8Scales& sc, bool& apart,
+                                         int lane) {
+    apart |= !q8_usual(sc.v[0]) || !q8_usual(sc.v[1]);
+    if (apart)
+        q8_chunk_of<D, PRECISE, MASKED, true>(st, kbase, vbase, valid, left, less, sc, lane);
+    else
+        q8_chunk_of<D, PRECISE, MASKED, false>(st, kbase, vbase, valid, left, less, sc, lane);
+}
+
 // A piece's result: the normalised rows row_of(head) of `heads` heads to the output
 // (WHOLE) or, with (m, L), to o and ml (of the workspace or shared memory).
 template <int D, bool WHOLE, class RowOf>
@@ -333,8 +366,8 @@ __device__ __forceinline__ void q8_store(const Q8Heads<D>& st, const Q8Params& p
         for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
         const int hh = 2 * tig + e;
         if (hh >= heads) continue;
-        // (1 / rv in two factors: either alone may leave fp32's range)
-        const float inv = l != 0.f ? __fdiv_rn(WeightRange<__half>::UNLIFT, l) : 0.f;
+        // (in two factors: either alone may leave fp32's range)
+        const float inv = l != 0.f ? __frcp_rn(l) : 0.f;
         const float b = __frcp_rn(st.rv[e]);
         const size_t row = row_of(hh);
 #pragma unroll
@@ -447,6 +480,7 @@ __device__ __forceinline__ void q8_worker(const Q8Params& p, const CUtensorMap& 
     Q8Heads<D> state;
     bool fresh = true;                 // the next chunk starts a piece
     bool from_start = false;           // the piece holds the pair's first chunk
+    bool apart = false;                // its scales so far are not all q8_usual
     int st = 0, put = 0, in_flight = 0;
     uint32_t phase = 0;
     for (;;) {
@@ -477,6 +511,7 @@ __device__ __forceinline__ void q8_worker(const Q8Params& p, const CUtensorMap& 
                                  lane >> 2 < p.group, p.scale_log2, lane);
             from_start = at.c == at.first;
             fresh = false;
+            apart = false;
         }
         const bool w = mbar_wait(&full[st], phase, p.errors);
         if (!__all_sync(0xffffffffu, w)) {
@@ -492,7 +527,8 @@ __device__ __forceinline__ void q8_worker(const Q8Params& p, const CUtensorMap& 
         }
         const uint32_t kbase = smem_addr(ring) + st * SLOT;
         if (valid[0] > 0 || valid[1] > 0)
-            q8_chunk<D, PRECISE>(state, kbase, kbase + 2 * HALF, valid, valid, valid, sc, lane);
+            q8_chunk<D, PRECISE>(state, kbase, kbase + 2 * HALF, valid, valid, valid, sc, apart,
+                                 lane);
         __syncwarp();
         --in_flight;
         if (++st == kQ8Stages) {
@@ -662,6 +698,7 @@ __global__ void __launch_bounds__(32 * kQ8ShortWarps)
                              own < cols, p.scale_log2, lane);
         int st = 0;
         uint32_t phase = 0;
+        bool apart = false;
         for (int c = warp; c < chunks; c += warps) {
             Blocks next = now;
             const bool more = c + warps < chunks;
@@ -700,7 +737,7 @@ __global__ void __launch_bounds__(32 * kQ8ShortWarps)
             }
             if (valid[0] > 0 || valid[1] > 0)
                 q8_chunk<D, PRECISE, CHUNK>(state, kbase, kbase + 2 * HALF, valid, left, less,
-                                            now.sc, lane);
+                                            now.sc, apart, lane);
             __syncwarp();
             now = next;
             if (st) phase ^= 1u;

@@ -630,6 +630,8 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
                 } else {
                     // ---- tiles with hidden keys or missing pages, rows with large scores:
                     // 32 keys at a time, once for the maximum and once for the weights
+                    // (rows choose values here, not ways)
+                    __syncwarp();
                     const int lim = pos - key0;
                     // group g as this row sees it: the score of a unit of y (never 0,
                     // hidden keys are -inf), 0 for a group with nothing to see
@@ -640,7 +642,6 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
                     };
                     // 32 keys' scores (formed) or products
                     auto scores = [&](float (&y)[32], int part) {
-                        __syncwarp();
                         tc_ld32(t_lane + Z::S_COL + part * 32, reinterpret_cast<uint32_t*>(y));
                         tc_wait_ld();
 #pragma unroll
@@ -730,7 +731,7 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
                         }
                     }
                     const float base = formed ? Range::LIFT - lb : Range::LIFT - (mu + lb);
-                    const float ref = exp2f(lb);
+                    const float ref = apart ? 0.f : formed ? exp2f(lb) : 1.f;
                     // (the first parts lie where scores were already read, the second
                     // ones wait for the end)
                     uint32_t rest[4][16];
@@ -749,9 +750,8 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
                             const float sum = weights(y + 16 * g, formed || f == 0.f ? 1.f : f,
                                                       f == 0.f ? 0.f : base + sc.lb[part * 2 + g],
                                                       w, g * 8);
-                            if (f != 0.f && !apart) l = fmaf(sum, sc.ib[part * 2 + g] * ref, l);
+                            l = fmaf(sum, f != 0.f ? sc.ib[part * 2 + g] * ref : 0.f, l);
                         }
-                        __syncwarp();
                         tc_st16(t_lane + Z::S_COL + part * 16, w[0]);
                         if (PARTS > 1)
 #pragma unroll
