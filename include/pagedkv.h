@@ -737,8 +737,8 @@ PKV_API pkv_status kv_append_rope_q8(void* k_pool, void* v_pool, float* k_scale,
  *   k_pool, v_pool device e4m3 bytes [num_blocks, block_size, n_kv_heads,
  *                 head_dim], 16-byte aligned
  *   k_scale, v_scale device float [num_blocks, n_kv_heads]: any numbers from 2^-126
- *                 to 2^125 (powers of two from the append, or others, e.g.
- *                 calibrated ones), also far apart from block to block
+ *                 to 2^125, or 0 for a block of zeros (powers of two from the append,
+ *                 or others, e.g. calibrated ones), also far apart from block to block
  *   workspace     device, >= pkv_decode_q8_workspace_bytes(...) bytes, 256-byte
  *                 aligned; contents on entry are ignored; may be NULL when that size
  *                 is 0 (few short contexts).  Calls that may overlap on the GPU need

@@ -160,16 +160,13 @@ __device__ __forceinline__ void q8_heads_start(Q8Heads<D>& st, const T* row, boo
     for (int j = 0; j < D / 16; ++j) st.o[j][0] = st.o[j][1] = st.o[j][2] = st.o[j][3] = 0.f;
 }
 
-// The scales of a chunk's halves.
+// The scales of a chunk's halves (0 and 1 where there is none).
 struct Q8Scales {
     float k[2], v[2];
 };
 
-// Value scales between which p and b / b_ref stay within fp32's range as they are (0: of
-// a half that holds nothing).
-__device__ __forceinline__ bool q8_usual(float b) {
-    return (b >= 0x1p-60f && b <= 0x1p16f) || b == 0.f;
-}
+// Value scales between which p and b / b_ref stay within fp32's range as they are.
+__device__ __forceinline__ bool q8_usual(float b) { return b >= 0x1p-60f && b <= 0x1p16f; }
 
 // min(x, 2^127); NaN stays.
 __device__ __forceinline__ float q8_bounded(float x) {
@@ -501,7 +498,7 @@ __device__ __forceinline__ void q8_worker(const Q8Params& p, const CUtensorMap& 
             const size_t i = (size_t)max(b, 0) * p.n_kv_heads + kvh;
             valid[h] = b >= 0 ? min(16, at.n - at.c * kQ8Tokens - 16 * h) : 0;
             sc.k[h] = b >= 0 ? __ldg(p.k_scale + i) : 0.f;
-            sc.v[h] = b >= 0 ? __ldg(p.v_scale + i) : 0.f;
+            sc.v[h] = b >= 0 ? __ldg(p.v_scale + i) : 1.f;
         }
         if (fresh) {
             q8_heads_start<D, T>(state,
@@ -660,7 +657,8 @@ __global__ void __launch_bounds__(32 * kQ8ShortWarps)
         for (int h = 0; h < 2; ++h) {
             const int t = c * kQ8Tokens + 16 * h;
             r.b[h] = -1;
-            r.sc.k[h] = r.sc.v[h] = 0.f;
+            r.sc.k[h] = 0.f;
+            r.sc.v[h] = 1.f;
             if (t >= n) continue;
             const int b =
                 __ldg(p.block_tables + (size_t)s * p.max_blocks_per_seq + t / p.block_size);

@@ -162,3 +162,34 @@ def test_long_contexts_without_values(chunk):
         pkv.paged_attn_decode_q8(out, q, kp, vp, ks, vs, tables, lens, scale, n)
     assert _clean() == 0
     assert (out == 0).all()
+
+
+@pytest.mark.parametrize("where", [[0], [1], [0, 2], None])
+@pytest.mark.parametrize("D,B", [(64, 16), (128, 32)])
+@pytest.mark.parametrize("out_dtype", [BF, F32])
+def test_scales_of_zero(D, B, where, out_dtype):
+    """Blocks of zeros whose scales are 0 (every block: None), on all routes."""
+    _clean()
+    seqs = [(1, 1), (1, B), (1, 3 * B + 5), (1, 600)]
+    c = _problem(seqs, 8, 2, D, B, BF, [None], 34)
+    for s, (_, n) in enumerate(seqs):
+        for j in range(-(-n // B)) if where is None else where:
+            if j * B >= n:
+                continue
+            b, rows = int(c["tables"][s, j]), slice(j * B, min(n, j * B + B))
+            for x, pool, sc in (("k", "kp", "ks"), ("v", "vp", "vs")):
+                c[pool].view(torch.uint8)[b] = 0
+                c[sc][b] = 0.0
+                c[x][s][rows] = 0.0
+    scale = 1.0 / math.sqrt(D)
+    rest = (c["kp"], c["vp"], c["ks"], c["vs"], c["tables"], c["lens"], scale)
+    for bound in (600, 20000):
+        out = torch.full(c["q"].shape, math.nan, dtype=out_dtype, device="cuda")
+        pkv.paged_attn_decode_q8(out, c["q"].cuda(), *rest, bound)
+        assert _clean() == 0
+        check(out, *_want(c, scale, out_dtype, False), "decode")
+    for max_q, bound in ((1, 600), (1, 5000), (9000, 1100)):
+        out = torch.full(c["q"].shape, math.nan, dtype=out_dtype, device="cuda")
+        pkv.paged_attn_multi_query_q8(out, c["q"].cuda(), c["q_start"], *rest, max_q, bound)
+        assert _clean() == 0
+        check(out, *_want(c, scale, out_dtype, out_dtype is not F32), "chunks")
