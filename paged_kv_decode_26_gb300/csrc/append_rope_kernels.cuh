@@ -237,12 +237,12 @@ __global__ void __launch_bounds__(kRopeThreads)
 // A block's scale covers all its rows of a head, so what is written to a block
 // is one unit: a run, tokens that follow one another in the call (but for those left
 // out between them, however many) and go to rising rows of one block.  The rows ahead
-// of its first one hold tokens and are kept, those behind hold none.  With s(x) the least power of two that brings x
-// down to 448 (e4m3's largest), a run sets the scale to s(its largest value), or
-// to the old scale if rows are kept and that is larger; kept rows are rounded
-// anew where the scale grew.  A power of two costs e4m3 no precision (its
-// numbers are spaced relative to their size), and makes the quotients exact and
-// most kept numbers survive a new scale unchanged.
+// of its first one hold tokens and are kept, those behind hold none.  With s(x) the least
+// power of two that brings x down to 448 (e4m3's largest), a run sets the scale to s(its
+// largest value), or to the old scale if rows are kept and that is larger; kept rows are
+// rounded anew where the scale grew.  A power of two costs e4m3 no precision (its numbers
+// are spaced relative to their size), and makes the quotients exact and most kept numbers
+// survive a new scale unchanged.
 //
 // CTA x: a window of `window` tokens, whose runs (those that start in it) it takes;
 // y: parts of the key and value heads, or of the query heads.  A window is one token,
@@ -256,10 +256,11 @@ __global__ void __launch_bounds__(kRopeThreads)
 // value, then the codes), while the next part's rows and scales are on their way.
 //
 // Measured: 8 prompts of 300-2048 tokens, 32 heads of 128, 87-88 us (3.8 TB/s), 16 of 32
-// query and 8 kv heads 94 (4.4 TB/s), 4 tokens 3.3 us.  Not bound by HBM but by the steps:
-// 300 instructions an item, two barriers a step.  A warp per run and head, its rows in
-// shared memory and no barriers, took 95 us and 6.4 for the 4 tokens; one barrier a step
-// 121; the parts of a window side by side in the grid 132; 256 threads 101.
+// query and 8 kv heads 94 (4.4 TB/s), 4 tokens 3.3 us.  Neither HBM nor the issue slots (62 %
+// busy, 300 instructions an item, 20 warps an SM) are full: a step's loads, two barriers
+// and codes follow one another.  A warp per run and head, its rows in shared memory and no
+// barriers, took 95 us and 6.4 for the 4 tokens; one barrier a step 121; the parts of a
+// window side by side in the grid 132; 256 threads 101.
 
 constexpr int kLeastExponent = -117;           // of a scale (a block of zeros)
 constexpr int kAppendThreads = 128;
@@ -449,7 +450,8 @@ __device__ __forceinline__ int gather_living(const AppendRopeParams& p, int w0, 
 #pragma unroll 1
     for (int way = -1; way <= 1; way += 2) {
         const int most = way < 0 ? B : B - 1;
-        const int edge = __shfl_sync(0xffffffffu, own, way < 0 ? __ffs(living) - 1 : 31 - __clz(living));
+        const int edge = __shfl_sync(0xffffffffu, own,
+                                     way < 0 ? __ffs(living) - 1 : 31 - __clz(living));
         if (tid == 0) s_found = s_done = 0;
         __syncthreads();
         for (long long at = way < 0 ? w0 - 1LL : w1; at >= 0 && at < p.num_tokens;

@@ -10,8 +10,9 @@
 // What bounds it: HBM, at half the bytes of 16-bit pages for the same products, so
 // twice the work a byte.  A 32-token chunk of one kv head (8 KB) is 16 + 32
 // products m16n8k16, 128 conversions of two codes and 16 ldmatrix.  Measured: 16
-// contexts of 8K-32K, 32 heads of 128, 414-434 us (6.9 TB/s), 128 of 16-8192, 32 query
-// and 8 kv heads, 174 us (6.4 TB/s); 4 of up to 200 tokens 4.6 us.
+// contexts of 8K-32K, 32 heads of 128, 414-434 us (6.6-6.9 TB/s), 128 of 16-8192, 32 query
+// and 8 kv heads, 171-179 us (6.2-6.5 TB/s); 4 of up to 200 tokens 5.0 us.  fp32 outputs
+// take as long.
 //
 // Layout: the tokens are the rows of the score product and the inner dimension of
 // the second one.  An ldmatrix of 16-bit units hands a lane bytes 4 t .. 4 t + 3

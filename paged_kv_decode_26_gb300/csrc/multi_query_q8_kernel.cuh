@@ -22,9 +22,10 @@
 // Roles: warps 0-3 and 4-7 the softmax of tile 0 and 1, a thread per row; warp 8
 // issues every MMA; 9-15 load and widen K and V.
 //
-// Measured: 2 chunks of 2048 tokens behind 12K-16K, 32 heads of 128, 840 us (1.17
-// PFLOP/s, 0.61 of a library bf16 product's rate); 8 of 100-512 tokens at 1K-8K, 32 query
-// and 8 kv heads, 160 us.  A step of 128 keys takes 3500 cycles, of which the tensor core
+// Measured: 2 chunks of 2048 tokens behind 12K-16K, 32 heads of 128, 844 us (1.16
+// PFLOP/s, 0.61 of a library bf16 product's rate), fp32 outputs 980-1050; 8 of 100-512
+// tokens at 1K-8K, 32 query and 8 kv heads, 158-163 us, fp32 outputs 200.  (Value scales
+// far apart, handled where they occur, cost 0.5-0.8 % of this.)  A step of 128 keys takes 3500 cycles, of which the tensor core
 // needs 2050 and the operands' way through shared memory as many; the rest is the
 // softmax's chain (scores in, maximum, weights out), two row tiles being all that the
 // tensor memory holds.  Without the exponentials it would be 8 % faster, without loads
@@ -81,7 +82,9 @@ struct Mq8Params : MultiQueryParams {
 
 // log2 of value scales for which w_t / b_t adds up to L as it is.
 constexpr float kMq8LeastLog = -60.f, kMq8MostLog = 16.f;
-__device__ __forceinline__ bool mq8_usual(float lb) { return lb >= kMq8LeastLog && lb <= kMq8MostLog; }
+__device__ __forceinline__ bool mq8_usual(float lb) {
+    return lb >= kMq8LeastLog && lb <= kMq8MostLog;
+}
 // Scores above m by more than this move it, whatever their values' scale.
 constexpr float kMq8Above = 64.f;
 
@@ -416,8 +419,9 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
         int entry = entry_of(k + kMq8Widen);
         while (k < n_tasks) {
             const unsigned i_op = k / 8, st = i_op % STAGES, g = k % 8, j = k / 16;
-            if (i_op >= STAGES &&
-                !__all_sync(0xffffffffu, mbar_wait(&kv_free[st], (i_op / STAGES - 1) & 1u, p.errors)))
+            if (i_op >= STAGES && !__all_sync(0xffffffffu, mbar_wait(&kv_free[st],
+                                                                     (i_op / STAGES - 1) & 1u,
+                                                                     p.errors)))
                 break;
             if ((i_op & 1) == 0) {
                 Mq8Scale& e = s_scale[j % kMq8Scales];
@@ -724,8 +728,9 @@ __global__ void __launch_bounds__(kMq8Threads, 1)
                             for (int c = 0; c < 32; ++c) {
                                 const float f = formed ? 1.f : unit(part * 2 + c / 16);
                                 // (hidden ones: -inf, where f may be 0)
-                                const float x = y[c] == -INFINITY ? y[c] : formed ? y[c] - mu
-                                                                                  : fmaf(y[c], f, -mu);
+                                const float x = y[c] == -INFINITY ? y[c]
+                                                : formed          ? y[c] - mu
+                                                                  : fmaf(y[c], f, -mu);
                                 l += exp2f(x + Range::LIFT);
                             }
                         }
