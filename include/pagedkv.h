@@ -745,7 +745,9 @@ PKV_API pkv_status kv_append_rope_q8(void* k_pool, void* v_pool, float* k_scale,
  *                 a workspace each.
  *   other arguments as paged_attn_decode (the split is automatic).
  * Scores, sums and outputs as in paged_attn_decode: products of the codes are exact,
- * scales stay in fp32, weights enter the second product as two F16 parts.
+ * scales stay in fp32, weights enter the second product as two F16 parts.  BF16 queries
+ * become F16 times a power of two per row: exact down to 2^-31 of the row's largest
+ * element, smaller ones are off by 2^-39 of it at most.
  * Supported shapes as paged_attn_decode; at most 65535 sequences, 4096 query
  * heads.  16 tokens in a block outside the pool are left out and flagged
  * PKV_DEVERR_BLOCK_ID.  One launch where the workspace's size is 0, else two.
@@ -779,8 +781,9 @@ PKV_API pkv_status paged_attn_decode_q8(
  * out (its rows are not written) and flagged PKV_DEVERR_CONTEXT.  Tokens in a block
  * outside the pool are left out and flagged PKV_DEVERR_BLOCK_ID; a row that sees no
  * other gets zeros.  NaN in V reaches only the rows that see it.
- * Softmax weights enter the second product rounded once to F16 (F32 outputs: two
- * parts).  Sums over very long contexts come out short by up to 2^-23 per 16 keys.
+ * Queries as in paged_attn_decode_q8.  Softmax weights enter the second product rounded
+ * once to F16 (F32 outputs: two parts).  Sums over very long contexts come out short by
+ * up to 2^-23 per 16 keys.
  * Supported shapes as paged_attn_decode; at most 65535 sequences, 4096 query heads.
  *   workspace    device, >= pkv_multi_query_q8_workspace_bytes(...) bytes, 256-byte
  *                aligned; contents on entry are ignored; may be NULL when that size is
